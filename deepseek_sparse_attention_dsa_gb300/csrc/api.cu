@@ -763,6 +763,125 @@ dsa_status dsa_attend_shared(dsa_ctx_t *ctx, const dsa_plan_t *plan, const void 
                     out, stream);
 }
 
+static bool is_type(int32_t t) { return t == DSA_BF16 || t == DSA_FP32; }
+
+// Whether c1 x c2 runs of `inner` written elements at strides s1 and s2 keep
+// clear of one another: one stride steps over a run, the other over all the
+// runs of the first.
+static bool apart(int64_t inner, int64_t c1, int64_t s1, int64_t c2 = 1, int64_t s2 = 0) {
+  if (c1 == 1) return c2 == 1 || s2 >= inner;
+  if (c2 == 1) return s1 >= inner;
+  return s1 <= s2 ? s1 >= inner && s2 >= (c1 - 1) * s1 + inner : s2 >= inner && s1 >= (c2 - 1) * s2 + inner;
+}
+
+// The call's rows against an optional plan: *count and *per_row as the
+// launchers take them.
+static dsa_status check_rows(dsa_ctx_t *ctx, const dsa_plan_t *plan, int64_t rows, const int32_t **count,
+                             int32_t *per_row) {
+  if (is_host_only(ctx) || rows < 0 || (plan && plan->ctx != ctx)) return DSA_ERR_INVALID_ARG;
+  *count = nullptr;
+  *per_row = 1;
+  if (plan) {
+    if (plan->T == 0 ? rows != 0 : rows % plan->T != 0) return DSA_ERR_INVALID_ARG;
+    if (plan->T > 0 && rows / plan->T > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+    if (plan->capturable) {
+      *count = plan->counts;
+      *per_row = static_cast<int32_t>(rows / plan->T);
+    }
+  }
+  if (rows > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  return cudaSetDevice(ctx->device) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+dsa_status dsa_rmsnorm(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_norm_t *shape, const void *x,
+                       const void *weight, const void *residual, void *residual_out, void *out, void *codes,
+                       float *scales, dsa_stream_t stream) {
+  if (!shape) return DSA_ERR_INVALID_ARG;
+  const dsa_norm_t &n = *shape;
+  if (n.width < 1 || !is_type(n.x_type) || !is_type(n.weight_type) || !is_type(n.residual_type) ||
+      !is_type(n.out_type) || !(n.eps >= 0.f) || n.x_stride < 0 || n.residual_stride < 0 || n.residual_out_stride < 0 ||
+      n.out_stride < 0 || n.codes_stride < 0 || n.scales_stride < 0)
+    return DSA_ERR_INVALID_ARG;
+  if (n.width > DSA_NORM_MAX_WIDTH) return DSA_ERR_UNSUPPORTED;
+  const int32_t *count;
+  int32_t per_row;
+  dsa_status st = check_rows(ctx, plan, n.rows, &count, &per_row);
+  if (st != DSA_OK) return st;
+  ctx->last_launches = 0;
+  if (n.rows == 0) return DSA_OK;
+  if ((residual_out && !residual) || (codes == nullptr) != (scales == nullptr) || (!out && !codes))
+    return DSA_ERR_INVALID_ARG;
+  if ((residual_out && !apart(n.width, n.rows, n.residual_out_stride)) || (out && !apart(n.width, n.rows, n.out_stride)) ||
+      (codes && (!apart(n.width, n.rows, n.codes_stride) || !apart((n.width + 127) / 128, n.rows, n.scales_stride))))
+    return DSA_ERR_INVALID_ARG;
+  if (!x) return DSA_ERR_INVALID_ARG;
+  return cuda_status(ctx, launch_rmsnorm(n, x, weight, residual, residual_out, out, codes, scales, count, per_row,
+                                         reinterpret_cast<cudaStream_t>(stream), &ctx->last_launches));
+}
+
+dsa_status dsa_quantize_rows(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_rows_t *shape, const void *x,
+                             void *codes, float *scales, dsa_stream_t stream) {
+  if (!shape) return DSA_ERR_INVALID_ARG;
+  const dsa_rows_t &r = *shape;
+  if (r.width < 1 || !is_type(r.x_type) || r.x_stride < 0 || r.codes_stride < 0 || r.scales_stride < 0)
+    return DSA_ERR_INVALID_ARG;
+  const int32_t *count;
+  int32_t per_row;
+  dsa_status st = check_rows(ctx, plan, r.rows, &count, &per_row);
+  if (st != DSA_OK) return st;
+  ctx->last_launches = 0;
+  if (r.rows == 0) return DSA_OK;
+  if (!apart(r.width, r.rows, r.codes_stride) || !apart((static_cast<int64_t>(r.width) + 127) / 128, r.rows, r.scales_stride))
+    return DSA_ERR_INVALID_ARG;
+  if (!x || !codes || !scales) return DSA_ERR_INVALID_ARG;
+  if ((static_cast<int64_t>(r.width) / 1024 + 1) * r.rows > 8ll * INT32_MAX) return DSA_ERR_UNSUPPORTED;   // the grid
+  return cuda_status(ctx, launch_quantize_rows(r, x, codes, scales, count, per_row,
+                                               reinterpret_cast<cudaStream_t>(stream), &ctx->last_launches));
+}
+
+dsa_status dsa_quantize_weight(dsa_ctx_t *ctx, const dsa_weight_t *shape, const void *w, void *codes, float *scales,
+                               dsa_stream_t stream) {
+  if (is_host_only(ctx) || !shape) return DSA_ERR_INVALID_ARG;
+  const dsa_weight_t &g = *shape;
+  if (g.batch < 1 || g.n < 1 || g.k < 1 || !is_type(g.w_type) || g.w_stride < 0 || g.w_batch < 0 ||
+      g.codes_stride < 0 || g.codes_batch < 0 || g.scales_stride < 0 || g.scales_batch < 0 || !w || !codes || !scales)
+    return DSA_ERR_INVALID_ARG;
+  if (!apart(g.k, g.n, g.codes_stride, g.batch, g.codes_batch) ||
+      !apart((static_cast<int64_t>(g.k) + 127) / 128, (g.n + 127) / 128, g.scales_stride, g.batch, g.scales_batch))
+    return DSA_ERR_INVALID_ARG;
+  if (g.batch > 65535 || g.n > 128 * 65535) return DSA_ERR_UNSUPPORTED;
+  if (cudaSetDevice(ctx->device) != cudaSuccess) return DSA_ERR_CUDA;
+  ctx->last_launches = 0;
+  return cuda_status(ctx, launch_quantize_weight(g, w, codes, scales, reinterpret_cast<cudaStream_t>(stream),
+                                                 &ctx->last_launches));
+}
+
+dsa_status dsa_project_fp8(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_project_t *shape, const void *a,
+                           const float *a_scale, const void *w, const float *w_scale, void *out,
+                           dsa_stream_t stream) {
+  if (!shape) return DSA_ERR_INVALID_ARG;
+  const dsa_project_t &g = *shape;
+  if (g.batch < 1 || g.n < 1 || g.k < 1 || !is_type(g.out_type) || g.a_stride < 0 || g.a_batch < 0 ||
+      g.a_scale_stride < 0 || g.a_scale_batch < 0 || g.w_stride < 0 || g.w_batch < 0 || g.w_scale_stride < 0 ||
+      g.w_scale_batch < 0 || g.out_stride < 0 || g.out_batch < 0)
+    return DSA_ERR_INVALID_ARG;
+  if (g.batch > 65535 || g.n > 64 * 65535) return DSA_ERR_UNSUPPORTED;
+  const int32_t *count;
+  int32_t per_row;
+  dsa_status st = check_rows(ctx, plan, g.rows, &count, &per_row);
+  if (st != DSA_OK) return st;
+  ctx->last_launches = 0;
+  if (g.rows == 0) return DSA_OK;
+  if (!apart(g.n, g.rows, g.out_stride, g.batch, g.out_batch)) return DSA_ERR_INVALID_ARG;
+  if (!a || !a_scale || !w || !w_scale || !out) return DSA_ERR_INVALID_ARG;
+  return cuda_status(ctx, launch_project_fp8(ctx, g, a, a_scale, w, w_scale, out, count, per_row,
+                                             reinterpret_cast<cudaStream_t>(stream), &ctx->last_launches));
+}
+
+int dsa_project_on_tensor_cores(const dsa_project_t *shape, const void *a, const void *w) {
+  return shape && project_tc_supported(*shape, a, w) ? 1 : 0;
+}
+
 dsa_status dsa_get_error(dsa_ctx_t *ctx, dsa_stream_t stream) {
   if (!ctx || is_host_only(ctx)) return DSA_ERR_INVALID_ARG;
   if (cudaSetDevice(ctx->device) != cudaSuccess) return DSA_ERR_CUDA;

@@ -270,6 +270,20 @@ cudaError_t launch_attend(const dsa_ctx *ctx, const dsa_plan_t *plan, const int3
                           const void *q_pe, const void *latent, const float *sink, float sm_scale, void *out,
                           cudaStream_t s, int32_t *launches);
 
+// The 8-bit rows and projections.  count: device row count of a capturable
+// plan (NULL: every row is live), per_row: the call's rows for each of its.
+cudaError_t launch_rmsnorm(const dsa_norm_t &n, const void *x, const void *weight, const void *residual,
+                           void *residual_out, void *out, void *codes, float *scales, const int32_t *count,
+                           int32_t per_row, cudaStream_t s, int32_t *launches);
+cudaError_t launch_quantize_rows(const dsa_rows_t &r, const void *x, void *codes, float *scales, const int32_t *count,
+                                 int32_t per_row, cudaStream_t s, int32_t *launches);
+cudaError_t launch_quantize_weight(const dsa_weight_t &w, const void *src, void *codes, float *scales, cudaStream_t s,
+                                   int32_t *launches);
+cudaError_t launch_project_fp8(const dsa_ctx *ctx, const dsa_project_t &g, const void *a, const float *a_scale,
+                               const void *w, const float *w_scale, void *out, const int32_t *count, int32_t per_row,
+                               cudaStream_t s, int32_t *launches);
+bool project_tc_supported(const dsa_project_t &g, const void *a, const void *w);
+
 // Device address of the fixed score array behind dsa_index_topk_static on the
 // current device (loads the module that holds it, so the array is taken when
 // the context is created rather than at the first call).

@@ -1,0 +1,167 @@
+// quantize_rows.cu -- bf16 or fp32 values to e4m3 codes with fp32 scales in the
+// layouts of the 8-bit product (project.cu): rows with a scale per 128 columns
+// (activations), matrices with a scale per 128 x 128 block (weights).  The rule
+// is the one of quantize-on-store (fp8.cuh).  Bound by HBM: every value is read
+// once and stays in registers between its group's maximum and its code.
+#include <cuda_runtime.h>
+
+#include "dsa_internal.h"
+#include "fp8.cuh"
+
+namespace dsa {
+namespace {
+
+struct RowsParams {
+  const char *x;
+  uint8_t *codes;
+  float *scales;
+  const int32_t *count;
+  int64_t rows, width;                               // values
+  int64_t x_stride, codes_stride, scales_stride;     // bytes
+  int64_t segments;                                  // warps a row
+  int64_t per_row;
+  int x_type;
+  bool x_vec, codes_vec, dense;
+};
+
+// Pieces of eight columns a lane: a warp's segment of a row is kRowPieces * 256 columns.
+constexpr int kRowPieces = 4;
+
+// One warp a segment, 16 lanes a group.
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const RowsParams p) {
+  const int64_t task = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
+  const int64_t row = task / p.segments;
+  if (row >= p.rows) return;
+  int64_t width = p.width;
+  if (p.count) {   // a dense matrix comes as one row, whose width is what the padding cuts
+    const int64_t live = static_cast<int64_t>(*p.count) * p.per_row;
+    if (p.dense) width = live < width ? live : width;
+    else if (row >= live) return;
+  }
+  const int lane = threadIdx.x % 32;
+  const int64_t col0 = (task % p.segments) * (kRowPieces * 256) + lane * 8;
+  const char *x = p.x + row * p.x_stride;
+  float v[kRowPieces][8];
+#pragma unroll
+  for (int c = 0; c < kRowPieces; ++c) load8(v[c], x, p.x_type, col0 + c * 256, width, p.x_vec);
+#pragma unroll
+  for (int c = 0; c < kRowPieces; ++c) {
+    uint32_t m = amax_bits8(v[c]);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float scale = group_scale(m);
+    const int64_t col = col0 + c * 256;
+    store_codes8(p.codes + row * p.codes_stride, col, width, p.codes_vec, codes8(v[c], scale));
+    if ((lane & 15) == 0 && col < width)
+      reinterpret_cast<float *>(reinterpret_cast<char *>(p.scales) + row * p.scales_stride)[col / 128] = scale;
+  }
+}
+
+struct BlocksParams {
+  const char *w;
+  uint8_t *codes;
+  float *scales;
+  int64_t w_stride, w_batch, codes_stride, codes_batch, scales_stride, scales_batch;   // bytes
+  int32_t n, k;
+  int w_type;
+  bool w_vec, codes_vec;
+};
+
+// One CTA a block of 128 x 128: 16 threads a row of it, 8 rows a thread.
+__global__ void __launch_bounds__(256) quantize_blocks_kernel(const BlocksParams p) {
+  const int64_t b = blockIdx.z;
+  const int col = blockIdx.x * 128 + (threadIdx.x % 16) * 8;
+  const int row0 = blockIdx.y * 128 + threadIdx.x / 16;
+  const char *w = p.w + b * p.w_batch;
+  float v[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = row0 + 16 * i;
+    if (row < p.n) {
+      load8(v[i], w + row * p.w_stride, p.w_type, col, p.k, p.w_vec);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    }
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, amax_bits8(v[i]));
+  m = __reduce_max_sync(0xffffffffu, m);
+  __shared__ uint32_t part[8];
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, part[i]);
+  const float scale = group_scale(m);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = row0 + 16 * i;
+    if (row < p.n)
+      store_codes8(p.codes + b * p.codes_batch + row * p.codes_stride, col, p.k, p.codes_vec, codes8(v[i], scale));
+  }
+  if (threadIdx.x == 0)
+    *reinterpret_cast<float *>(reinterpret_cast<char *>(p.scales) + b * p.scales_batch + blockIdx.y * p.scales_stride +
+                               blockIdx.x * 4) = scale;
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows(const dsa_rows_t &r, const void *x, void *codes, float *scales, const int32_t *count,
+                                 int32_t per_row, cudaStream_t s, int32_t *launches) {
+  RowsParams p{};
+  const int size = r.x_type == DSA_BF16 ? 2 : 4;
+  p.x = static_cast<const char *>(x);
+  p.codes = static_cast<uint8_t *>(codes);
+  p.scales = scales;
+  p.count = count;
+  p.per_row = per_row;
+  p.rows = r.rows;
+  p.width = r.width;
+  p.x_stride = r.x_stride * size;
+  p.codes_stride = r.codes_stride;
+  p.scales_stride = r.scales_stride * 4;
+  p.x_type = r.x_type;
+  // a dense matrix of whole groups is one long row: no lane idles on narrow rows
+  if (r.width % 128 == 0 && r.x_stride == r.width && r.codes_stride == r.width && r.scales_stride == r.width / 128) {
+    p.width = r.rows * r.width;
+    p.rows = 1;
+    p.per_row = static_cast<int64_t>(per_row) * r.width;
+    p.dense = true;
+  }
+  const bool one = p.rows == 1;
+  p.x_vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (one || p.x_stride % 16 == 0);
+  p.codes_vec = reinterpret_cast<uintptr_t>(codes) % 8 == 0 && (one || p.codes_stride % 8 == 0);
+  p.segments = (p.width + kRowPieces * 256 - 1) / (kRowPieces * 256);
+  quantize_rows_kernel<<<static_cast<unsigned>((p.rows * p.segments + 7) / 8), 256, 0, s>>>(p);
+  *launches += 1;
+  return cudaGetLastError();
+}
+
+cudaError_t launch_quantize_weight(const dsa_weight_t &w, const void *src, void *codes, float *scales, cudaStream_t s,
+                                   int32_t *launches) {
+  BlocksParams p{};
+  const int size = w.w_type == DSA_BF16 ? 2 : 4;
+  p.w = static_cast<const char *>(src);
+  p.codes = static_cast<uint8_t *>(codes);
+  p.scales = scales;
+  p.w_stride = w.w_stride * size;
+  p.w_batch = w.w_batch * size;
+  p.codes_stride = w.codes_stride;
+  p.codes_batch = w.codes_batch;
+  p.scales_stride = w.scales_stride * 4;
+  p.scales_batch = w.scales_batch * 4;
+  p.n = w.n;
+  p.k = w.k;
+  p.w_type = w.w_type;
+  p.w_vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && (w.n == 1 || p.w_stride % 16 == 0) &&
+            (w.batch == 1 || p.w_batch % 16 == 0);
+  p.codes_vec = reinterpret_cast<uintptr_t>(codes) % 8 == 0 && (w.n == 1 || p.codes_stride % 8 == 0) &&
+                (w.batch == 1 || p.codes_batch % 8 == 0);
+  const dim3 grid((w.k + 127) / 128, (w.n + 127) / 128, w.batch);
+  quantize_blocks_kernel<<<grid, 256, 0, s>>>(p);
+  *launches += 1;
+  return cudaGetLastError();
+}
+
+}  // namespace dsa

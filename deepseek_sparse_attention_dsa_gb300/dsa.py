@@ -20,6 +20,17 @@ fp8 query for the indexer (fp8 index cache): quantize_q, index_scores_fp8q,
 index_topk_fp8q.  Quantize-on-store: quantize_store_keys / _latents.  SHARED
 layers: attend_shared.
 
+Around the attention, in 8 bits (e4m3 codes, fp32 scales per 128 columns of a
+row or per 128 x 128 block of a weight):
+
+    codes, scale, h = ctx.rmsnorm_quantize(x, weight, eps, residual=h)   # dsa_rmsnorm
+    w_codes, w_scale = ctx.quantize_weight(w)                            # dsa_quantize_weight, once
+    y = ctx.project_fp8(codes, scale, w_codes, w_scale)                  # dsa_project_fp8
+    codes, scale = ctx.quantize_rows(out)                                # dsa_quantize_rows
+
+These four take rows at any stride and need no plan (plan= marks the padding
+rows of a capturable plan).
+
 Tensors are torch tensors on the context's device, contiguous, in the dtypes
 the header states; the calls run on torch's current CUDA stream unless a
 stream is given.
@@ -46,7 +57,8 @@ EXPORTED = ["dsa_create", "dsa_destroy", "dsa_plan", "dsa_plan_destroy", "dsa_pl
             "dsa_quantize_store_keys", "dsa_quantize_store_latents", "dsa_attend_shared", "dsa_plan_capturable",
             "dsa_plan_update", "dsa_plan_read_counts", "dsa_quantize_q", "dsa_index_scores_fp8q",
             "dsa_index_topk_fp8q", "dsa_selftest_wait_timeout", "dsa_msa_select_blocks", "dsa_msa_index_select",
-            "dsa_msa_attend", "dsa_msa_attend_on_tensor_cores"]
+            "dsa_msa_attend", "dsa_msa_attend_on_tensor_cores", "dsa_rmsnorm", "dsa_quantize_rows",
+            "dsa_quantize_weight", "dsa_project_fp8", "dsa_project_on_tensor_cores"]
 
 # dsa_device_span_t: q_len, ctx_start, page_start, page_off, num_pages, reserved (int32 each)
 DEVICE_SPAN_FIELDS = 6
@@ -74,6 +86,38 @@ class _Span(ctypes.Structure):
 class _MsaShape(ctypes.Structure):
     _fields_ = [("block_size", ctypes.c_int32), ("topk_blocks", ctypes.c_int32), ("q_heads", ctypes.c_int32),
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+_BF16, _FP32 = 0, 1
+_TYPES = {torch.bfloat16: _BF16, torch.float32: _FP32}
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+class _Norm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int32), ("x_type", ctypes.c_int32),
+                ("weight_type", ctypes.c_int32), ("residual_type", ctypes.c_int32), ("out_type", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64),
+                ("residual_out_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+                ("codes_stride", ctypes.c_int64), ("scales_stride", ctypes.c_int64)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int32), ("x_type", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64), ("codes_stride", ctypes.c_int64), ("scales_stride", ctypes.c_int64)]
+
+
+class _Weight(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("w_type", ctypes.c_int32),
+                ("w_stride", ctypes.c_int64), ("w_batch", ctypes.c_int64), ("codes_stride", ctypes.c_int64),
+                ("codes_batch", ctypes.c_int64), ("scales_stride", ctypes.c_int64), ("scales_batch", ctypes.c_int64)]
+
+
+class _Project(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("batch", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("out_type", ctypes.c_int32), ("a_stride", ctypes.c_int64), ("a_batch", ctypes.c_int64),
+                ("a_scale_stride", ctypes.c_int64), ("a_scale_batch", ctypes.c_int64), ("w_stride", ctypes.c_int64),
+                ("w_batch", ctypes.c_int64), ("w_scale_stride", ctypes.c_int64), ("w_scale_batch", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("out_batch", ctypes.c_int64)]
 
 
 def _msa_shape(ms) -> _MsaShape:
@@ -128,6 +172,12 @@ def load() -> ctypes.CDLL:
     L.dsa_index_topk_fp8q.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp]
     L.dsa_get_error.argtypes = [vp, vp]
     L.dsa_selftest_wait_timeout.argtypes = [vp, ctypes.c_uint64, vp, vp]
+    L.dsa_rmsnorm.argtypes = [vp, vp, ctypes.POINTER(_Norm), vp, vp, vp, vp, vp, vp, vp, vp]
+    L.dsa_quantize_rows.argtypes = [vp, vp, ctypes.POINTER(_Rows), vp, vp, vp, vp]
+    L.dsa_quantize_weight.argtypes = [vp, ctypes.POINTER(_Weight), vp, vp, vp, vp]
+    L.dsa_project_fp8.argtypes = [vp, vp, ctypes.POINTER(_Project), vp, vp, vp, vp, vp, vp]
+    L.dsa_project_on_tensor_cores.argtypes = [ctypes.POINTER(_Project), vp, vp]
+    L.dsa_project_on_tensor_cores.restype = ctypes.c_int
     msp = ctypes.POINTER(_MsaShape)
     L.dsa_msa_select_blocks.argtypes = [vp, vp, msp, vp, vp, vp]
     L.dsa_msa_index_select.argtypes = [vp, vp, msp, vp, vp, vp, vp, vp]
@@ -144,7 +194,8 @@ def load() -> ctypes.CDLL:
                  "dsa_index_scores", "dsa_topk_from_scores", "dsa_attend", "dsa_get_error", "dsa_quantize_store_keys",
                  "dsa_quantize_store_latents", "dsa_attend_shared", "dsa_plan_capturable", "dsa_plan_update",
                  "dsa_plan_read_counts", "dsa_quantize_q", "dsa_index_scores_fp8q", "dsa_index_topk_fp8q",
-                 "dsa_selftest_wait_timeout", "dsa_msa_select_blocks", "dsa_msa_index_select", "dsa_msa_attend"):
+                 "dsa_selftest_wait_timeout", "dsa_msa_select_blocks", "dsa_msa_index_select", "dsa_msa_attend",
+                 "dsa_rmsnorm", "dsa_quantize_rows", "dsa_quantize_weight", "dsa_project_fp8"):
         getattr(L, name).restype = i32
     _lib = L
     return L
@@ -180,6 +231,19 @@ def _ptr(t: Optional[torch.Tensor], device: torch.device, dtypes, name: str):
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _row_ptr(t: torch.Tensor, device: torch.device, dtypes, shape, name: str) -> int:
+    """Address of a tensor of this shape whose last dimension is adjacent; the others may have any stride."""
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.dtype not in dtypes:
+        raise TypeError("%s has dtype %s, expected one of %s" % (name, t.dtype, dtypes))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError("%s must have adjacent values in its last dimension" % name)
+    return t.data_ptr()
 
 
 def _stream(stream) -> ctypes.c_void_p:
@@ -428,6 +492,151 @@ class Context:
                                           _ptr(selection, d, (torch.int32,), "selection"), _stream(stream)),
                "dsa_index_topk_fp8q", self.handle)
         return selection
+
+    # ---------------------------------------------- 8-bit rows and projections
+    def _stream_of(self, stream):
+        if self.device_index < 0:
+            return None   # a host-only context: the call is refused
+        return _stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+
+    def _norm(self, x, weight, eps, residual, residual_out, out, codes, scales, plan, stream):
+        d = self.device
+        if x.dim() != 2:
+            raise ValueError("x must be (rows, width)")
+        rows, width = x.shape
+        types = (torch.bfloat16, torch.float32)
+        n = _Norm(rows, width, _TYPES.get(x.dtype, -1), 0, 0, 0, eps, x.stride(0), 0, 0, 0, 0, 0)
+        px = _row_ptr(x, d, types, x.shape, "x")
+        pw = pr = pro = po = pc = ps = None
+        if weight is not None:
+            pw = _row_ptr(weight, d, types, (width,), "weight")
+            n.weight_type = _TYPES[weight.dtype]
+        if residual is not None:
+            pr = _row_ptr(residual, d, types, x.shape, "residual")
+            pro = _row_ptr(residual_out, d, (residual.dtype,), x.shape, "residual_out")
+            n.residual_type = _TYPES[residual.dtype]
+            n.residual_stride, n.residual_out_stride = residual.stride(0), residual_out.stride(0)
+        elif residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+        if out is not None:
+            po = _row_ptr(out, d, types, x.shape, "out")
+            n.out_type, n.out_stride = _TYPES[out.dtype], out.stride(0)
+        if codes is not None:
+            pc = _row_ptr(codes, d, _CODES, x.shape, "codes")
+            ps = _row_ptr(scales, d, (torch.float32,), (rows, (width + 127) // 128), "scales")
+            n.codes_stride, n.scales_stride = codes.stride(0), scales.stride(0)
+        _check(load().dsa_rmsnorm(self.handle, plan.handle if plan is not None else None, n, px, pw, pr, pro, po, pc, ps,
+                                  self._stream_of(stream)), "dsa_rmsnorm", self.handle)
+
+    def rmsnorm(self, x, weight, eps=1e-6, residual=None, residual_out=None, out=None, out_dtype=torch.bfloat16,
+                plan=None, stream=None):
+        """dsa_rmsnorm: x (rows, width) bf16 or fp32 -> the normed rows in
+        out_dtype; with a residual (added first) -> (out, residual_out)."""
+        if out is None:
+            out = torch.empty(x.shape, dtype=out_dtype, device=self.device)
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty(x.shape, dtype=residual.dtype, device=self.device)
+        self._norm(x, weight, eps, residual, residual_out, out, None, None, plan, stream)
+        return out if residual is None else (out, residual_out)
+
+    def rmsnorm_quantize(self, x, weight, eps=1e-6, residual=None, residual_out=None, out=None, codes=None, scales=None,
+                         plan=None, stream=None):
+        """dsa_rmsnorm with an 8-bit output: (codes (rows, width) uint8, scales
+        (rows, ceil(width / 128)) fp32), and residual_out after them where there
+        is a residual.  out, where given, takes the normed rows too."""
+        if codes is None:
+            codes = torch.empty(x.shape, dtype=torch.uint8, device=self.device)
+        if scales is None:
+            scales = torch.empty(x.shape[0], (x.shape[-1] + 127) // 128, dtype=torch.float32, device=self.device)
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty(x.shape, dtype=residual.dtype, device=self.device)
+        self._norm(x, weight, eps, residual, residual_out, out, codes, scales, plan, stream)
+        return (codes, scales) if residual is None else (codes, scales, residual_out)
+
+    def quantize_rows(self, x, codes=None, scales=None, plan=None, stream=None):
+        """dsa_quantize_rows: x (rows, width) bf16 or fp32 -> (codes uint8 of
+        the same shape, scales (rows, ceil(width / 128)) fp32)."""
+        d = self.device
+        if x.dim() != 2:
+            raise ValueError("x must be (rows, width)")
+        rows, width = x.shape
+        groups = (width + 127) // 128
+        if codes is None:
+            codes = torch.empty(rows, width, dtype=torch.uint8, device=d)
+        if scales is None:
+            scales = torch.empty(rows, groups, dtype=torch.float32, device=d)
+        px = _row_ptr(x, d, (torch.bfloat16, torch.float32), x.shape, "x")
+        pc = _row_ptr(codes, d, _CODES, x.shape, "codes")
+        ps = _row_ptr(scales, d, (torch.float32,), (rows, groups), "scales")
+        r = _Rows(rows, width, _TYPES[x.dtype], x.stride(0), codes.stride(0), scales.stride(0))
+        _check(load().dsa_quantize_rows(self.handle, plan.handle if plan is not None else None, r, px, pc, ps,
+                                        self._stream_of(stream)), "dsa_quantize_rows", self.handle)
+        return codes, scales
+
+    def quantize_weight(self, w, codes=None, scales=None, stream=None):
+        """dsa_quantize_weight: w (n, k) or (batch, n, k) bf16 or fp32 -> (codes
+        uint8 of the same shape, scales (..., ceil(n / 128), ceil(k / 128)) fp32)."""
+        d = self.device
+        if w.dim() not in (2, 3):
+            raise ValueError("w must be (n, k) or (batch, n, k)")
+        n, k = w.shape[-2:]
+        s_shape = tuple(w.shape[:-2]) + ((n + 127) // 128, (k + 127) // 128)
+        if codes is None:
+            codes = torch.empty(w.shape, dtype=torch.uint8, device=d)
+        if scales is None:
+            scales = torch.empty(s_shape, dtype=torch.float32, device=d)
+        pw = _row_ptr(w, d, (torch.bfloat16, torch.float32), w.shape, "w")
+        pc = _row_ptr(codes, d, _CODES, w.shape, "codes")
+        ps = _row_ptr(scales, d, (torch.float32,), s_shape, "scales")
+        many = w.dim() == 3
+        g = _Weight(w.shape[0] if many else 1, n, k, _TYPES[w.dtype], w.stride(-2), w.stride(0) if many else 0,
+                    codes.stride(-2), codes.stride(0) if many else 0, scales.stride(-2), scales.stride(0) if many else 0)
+        _check(load().dsa_quantize_weight(self.handle, g, pw, pc, ps, self._stream_of(stream)), "dsa_quantize_weight",
+               self.handle)
+        return codes, scales
+
+    def _project(self, a, a_scale, w, w_scale, out):
+        """The call's shape and addresses (a, a_scale, w, w_scale, out)."""
+        d = self.device
+        many = w.dim() == 3
+        if w.dim() not in (2, 3) or a.dim() != w.dim():
+            raise ValueError("a (rows, k) goes with w (n, k), a (rows, batch, k) with w (batch, n, k)")
+        n, k = w.shape[-2:]
+        rows = a.shape[0]
+        kb, nb = (k + 127) // 128, (n + 127) // 128
+        if many:
+            b = w.shape[0]
+            a_shape, as_shape, ws_shape, o_shape = (rows, b, k), (rows, b, kb), (b, nb, kb), (rows, b, n)
+        else:
+            b = 1
+            a_shape, as_shape, ws_shape, o_shape = (rows, k), (rows, kb), (nb, kb), (rows, n)
+        f32 = (torch.float32,)
+        ptrs = (_row_ptr(a, d, _CODES, a_shape, "a"), _row_ptr(a_scale, d, f32, as_shape, "a_scale"),
+                _row_ptr(w, d, _CODES, w.shape, "w"), _row_ptr(w_scale, d, f32, ws_shape, "w_scale"),
+                _row_ptr(out, d, (torch.bfloat16, torch.float32), o_shape, "out"))
+        if many:
+            g = _Project(rows, b, n, k, _TYPES[out.dtype], a.stride(0), a.stride(1), a_scale.stride(0), a_scale.stride(1),
+                         w.stride(1), w.stride(0), w_scale.stride(1), w_scale.stride(0), out.stride(0), out.stride(1))
+        else:
+            g = _Project(rows, 1, n, k, _TYPES[out.dtype], a.stride(0), 0, a_scale.stride(0), 0, w.stride(0), 0,
+                         w_scale.stride(0), 0, out.stride(0), 0)
+        return g, ptrs
+
+    def project_fp8(self, a, a_scale, w, w_scale, out=None, out_dtype=torch.bfloat16, plan=None, stream=None):
+        """dsa_project_fp8: codes a (rows, k) with scales (rows, ceil(k / 128))
+        times w (n, k) with scales per 128 x 128 block -> (rows, n) in
+        out_dtype; or for each b, a (rows, batch, k) times w (batch, n, k) ->
+        (rows, batch, n).  Codes are uint8 or float8_e4m3fn."""
+        if out is None:
+            out = torch.empty(a.shape[:-1] + w.shape[-2:-1], dtype=out_dtype, device=self.device)
+        g, (pa, pas, pw, pws, po) = self._project(a, a_scale, w, w_scale, out)
+        _check(load().dsa_project_fp8(self.handle, plan.handle if plan is not None else None, g, pa, pas, pw, pws, po,
+                                      self._stream_of(stream)), "dsa_project_fp8", self.handle)
+        return out
+
+    def project_on_tensor_cores(self, a, a_scale, w, w_scale, out) -> bool:
+        g, (pa, _, pw, _, _) = self._project(a, a_scale, w, w_scale, out)
+        return bool(load().dsa_project_on_tensor_cores(g, pa, pw))
 
     def index_scores(self, plan: Plan, q, w, index_cache, scores=None, stream=None) -> torch.Tensor:
         d = self.device

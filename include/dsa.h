@@ -386,6 +386,101 @@ dsa_status dsa_msa_attend(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_msa_
 /* 1 when dsa_msa_attend runs this shape on the tensor cores, else 0 (host-side query). */
 int dsa_msa_attend_on_tensor_cores(const dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_msa_shape_t *shape);
 
+/* ---- 8-bit rows and projections --------------------------------------------
+ * What a layer does around the calls above: the norm before its projections,
+ * the projections themselves (of e4m3 codes, DeepSeek-style scales: one for 128
+ * columns of an activation row, one for a block of 128 x 128 of a weight), and
+ * the quantisers that feed them.  A value is e4m3(code) * scale.  Quantisation
+ * is the rule of dsa_quantize_store_keys: scale = amax / 448 in fp32 (1 where
+ * that is zero), code = E4M3(x / scale), rounded to nearest even.  The last
+ * group of a row (or block of a matrix) may be cut short.  A group that holds a
+ * NaN or an infinity gets a scale that is NaN or infinite, so that none of its
+ * values comes back finite.
+ *
+ * The calls use a context for its device, error word and launch count only:
+ * its shape and formats are not read.  They need no workspace.  `plan` may be
+ * NULL; with a plan of this context, rows must be a multiple (m times) of the
+ * plan's num_rows, and with a capturable plan the rows at or after m times the
+ * current row count are padding: what they hold does not matter, and nothing is
+ * written to them or their scales.
+ *
+ * Strides are in elements (codes: bytes) from one row, or one matrix of a
+ * batch, to the next; a row's own values are adjacent.  Rows must not overlap
+ * in anything written.  Any stride and alignment is accepted (of the type's own
+ * size); 16-byte aligned rows run faster, and project_fp8 needs them for the
+ * tensor cores.  DSA_ERR_INVALID_ARG: null pointers, sizes below 1 (rows may be
+ * 0: nothing is launched), unknown types, negative strides, written rows
+ * that would overlap, or rows that do not match the plan; DSA_ERR_UNSUPPORTED: sizes beyond the limits given below. */
+enum { DSA_BF16 = 0, DSA_FP32 = 1 };
+
+/* Root-mean-square norm with the residual's addition:
+ *   h = x + residual (fp32),  residual_out = h,
+ *   y = h * weight / sqrt(mean(h^2) + eps) (fp32),
+ *   out = y and/or (codes, scales) = y quantised in groups of 128 columns;
+ * residual_out, out and codes are each rounded once from fp32.  residual may be
+ * NULL (h = x), and then residual_out must be; residual_out, weight (all ones)
+ * and either of out and codes may be NULL; codes and scales come together.
+ * residual_out may be the buffer of residual or x, and out that of x, with the
+ * same type and stride.  width is at most DSA_NORM_MAX_WIDTH. */
+#define DSA_NORM_MAX_WIDTH 32768
+typedef struct dsa_norm {
+  int64_t rows;
+  int32_t width;
+  int32_t x_type, weight_type, residual_type, out_type;   /* DSA_BF16 or DSA_FP32; residual_type is residual_out's too */
+  float eps;                                              /* >= 0 */
+  int64_t x_stride, residual_stride, residual_out_stride, out_stride, codes_stride, scales_stride;
+} dsa_norm_t;
+dsa_status dsa_rmsnorm(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_norm_t *shape, const void *x,
+                       const void *weight, const void *residual, void *residual_out, void *out, void *codes,
+                       float *scales, dsa_stream_t stream);
+
+/* Rows of width values (bf16 or fp32) -> codes (rows, width) and scales
+ * (rows, ceil(width / 128)). */
+typedef struct dsa_rows {
+  int64_t rows;
+  int32_t width;
+  int32_t x_type;
+  int64_t x_stride, codes_stride, scales_stride;
+} dsa_rows_t;
+dsa_status dsa_quantize_rows(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_rows_t *shape, const void *x,
+                             void *codes, float *scales, dsa_stream_t stream);
+
+/* batch matrices w (n, k) (bf16 or fp32) -> codes (n, k) and scales
+ * (ceil(n / 128), ceil(k / 128)), one for each block of 128 x 128.  n at most
+ * 128 * 65535, batch at most 65535. */
+typedef struct dsa_weight {
+  int32_t batch, n, k;
+  int32_t w_type;
+  int64_t w_stride, w_batch, codes_stride, codes_batch, scales_stride, scales_batch;
+} dsa_weight_t;
+dsa_status dsa_quantize_weight(dsa_ctx_t *ctx, const dsa_weight_t *shape, const void *w, void *codes, float *scales,
+                               dsa_stream_t stream);
+
+/* Projection of e4m3 codes:
+ *   out[m, b, j] = sum_kb a_scale[m, b, kb] * w_scale[b, j / 128, kb]
+ *                  * sum_{k in block kb} e4m3(a[m, b, k]) * e4m3(w[b, j, k])
+ * for rows m, matrices b = 0 .. batch-1 (an absorbed projection's heads; 1
+ * otherwise) and columns j = 0 .. n-1, over blocks kb of 128 of the k columns;
+ * products and sums in fp32, out rounded once to out_type.  a: codes (rows,
+ * batch, k), w: codes (batch, n, k), scales as dsa_quantize_rows and
+ * dsa_quantize_weight lay them out, out (rows, batch, n); *_batch is the
+ * distance between neighbouring b.  Sums are added in a fixed order: equal
+ * calls give equal bits.  The tensor cores need a and w on 16 bytes with
+ * strides that are multiples of 16 (dsa_project_on_tensor_cores); other
+ * layouts run a CUDA-core kernel.  n at most 64 * 65535, batch at most 65535. */
+typedef struct dsa_project {
+  int64_t rows;
+  int32_t batch, n, k;
+  int32_t out_type;
+  int64_t a_stride, a_batch, a_scale_stride, a_scale_batch;
+  int64_t w_stride, w_batch, w_scale_stride, w_scale_batch;
+  int64_t out_stride, out_batch;
+} dsa_project_t;
+dsa_status dsa_project_fp8(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_project_t *shape, const void *a,
+                           const float *a_scale, const void *w, const float *w_scale, void *out, dsa_stream_t stream);
+/* 1 when dsa_project_fp8 runs this call on the tensor cores, else 0 (host-side query). */
+int dsa_project_on_tensor_cores(const dsa_project_t *shape, const void *a, const void *w);
+
 /* Drive the pipeline's bounded wait to its limit, for testing the failure
  * path (mstar IndexKeyStore.history: a failure is reported to the caller, not
  * fatal).  One CTA takes tensor memory, waits on an mbarrier that nothing
