@@ -4,30 +4,351 @@
 //                  * sum_{k in block kb} a[m, b, k] * w[b, n, k]
 //
 // for b = 0 .. batch-1 (the heads of an absorbed projection; 1 otherwise).
+//
+// project_tc_kernel: tcgen05 kind::f8f6f4.  A tile is 128 weight rows (the MMA's
+// 128 lanes, and exactly one row of scale blocks) by NT tokens (its columns),
+// so that one kernel covers a single token (NT = 16) and a prefill chunk.  The
+// scales change with every 128 of k, so the tensor core sums one block of 128
+// at a time into a tensor-memory buffer (four K = 32 steps), and the epilogue
+// warps add the blocks up in registers: acc[col] += s[kb][col] * block[col] with
+// s = a_scale * w_scale, which two helper warps put into shared memory ahead of
+// them.  Buffers of tensor memory let the tensor core run ahead of that.
+//
+// Few tiles: a cluster of S CTAs shares a tile, each taking a run of its k
+// blocks; every CTA leaves its partial sums in its own shared memory, and after
+// a cluster barrier rank r adds the S partials of its share of the columns in
+// rank order, so results do not depend on timing.
+//
+// Warp roles: 0 TMA producer, 1 MMA issuer and tensor-memory owner, 2-3 scales,
+// 4.. epilogue.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "dsa_internal.h"
 #include "fp8.cuh"
+#include "ptx.cuh"
 
 namespace dsa {
 namespace {
 
 struct ProjectParams {
+  CUtensorMap tm_a;   // token codes as [rows][batch][k], box {128, 1, NT}, 128-byte swizzle
+  CUtensorMap tm_w;   // weight codes as [batch][n][k], box {128, 128, 1}, 128-byte swizzle
   const uint8_t *a, *w;
   const float *a_scale, *w_scale;
   void *out;
   const int32_t *count;
+  int *err;
   int64_t rows;
   int64_t a_stride, a_batch, w_stride, w_batch, as_stride, as_batch, ws_stride, ws_batch, out_stride, out_batch;
-  int32_t n, k, per_row, out_type;
+  int32_t n, k, batch, per_row, out_type, split;
 };
+
+__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int NT_>
+struct ProjectTraits {
+  static constexpr int NT = NT_;
+  static constexpr int EPI = NT >= 128 ? 8 : 4;             // epilogue warps: 4 per half of the columns
+  static constexpr int THREADS = 128 + 32 * EPI;
+  static constexpr int COLS = NT / (EPI / 4);               // columns of an epilogue thread
+  static constexpr int W_BYTES = 128 * 128, A_BYTES = NT * 128;
+  static constexpr int STAGE = W_BYTES + A_BYTES;
+  static constexpr int STAGES = NT == 256 ? 4 : NT == 128 ? 6 : NT == 64 ? 8 : 10;
+  static constexpr int AB = NT == 256 ? 2 : 4;              // tensor-memory buffers
+  static constexpr int TMEM_COLS = AB * NT;
+  static constexpr int GK = 4, SG = 3;                      // k blocks per scale slot, slots
+  static constexpr int S_SLOT = GK * NT * 4;
+  static constexpr uint32_t IDESC = mma_idesc(128, NT, 0u, false, false);   // kind::f8f6f4: format 0 = e4m3
+  static constexpr int OFF_S = STAGES * STAGE;
+  static constexpr int OFF_BAR = OFF_S + SG * S_SLOT;
+  static constexpr int NBAR = 2 * STAGES + 2 * AB + 2 * SG;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM = OFF_MISC + 16 + 1024;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(NT * 128 * 4 <= STAGES * STAGE, "partial sums reuse the stages");
+};
+
+struct ProjectTile {
+  int b, n0;
+  int64_t m0;
+};
+
+// Tiles in order: tokens fastest, so that neighbouring CTAs share weights.
+__device__ __forceinline__ ProjectTile tile_at(int64_t t, int64_t m_tiles, int n_tiles, int NT) {
+  const int64_t rest = t / m_tiles;
+  return {static_cast<int>(rest / n_tiles), static_cast<int>(rest % n_tiles) * 128, (t % m_tiles) * NT};
+}
+
+__device__ __forceinline__ void store_out(const ProjectParams &p, int64_t m, int b, int n, float v) {
+  const int64_t at = m * p.out_stride + b * p.out_batch + n;
+  if (p.out_type == DSA_BF16) static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(v);
+  else static_cast<float *>(p.out)[at] = v;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kernel(const __grid_constant__ ProjectParams p) {
+  using C = ProjectTraits<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::OFF_BAR;
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
+  auto afull = [&](int b) { return bar0 + 8u * (2 * C::STAGES + b); };
+  auto aempty = [&](int b) { return bar0 + 8u * (2 * C::STAGES + C::AB + b); };
+  auto sfull = [&](int g) { return bar0 + 8u * (2 * C::STAGES + 2 * C::AB + g); };
+  auto sempty = [&](int g) { return bar0 + 8u * (2 * C::STAGES + 2 * C::AB + C::SG + g); };
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+
+  const int warp = threadIdx.x / 32;
+  const int lane = lane_id();
+  const int rank = p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int64_t live = live_rows(p.rows, p.count, p.per_row);
+  const int64_t m_tiles = (live + NT - 1) / NT;
+  const int n_tiles = (p.n + 127) / 128;
+  const int64_t tiles = m_tiles * n_tiles * p.batch;
+  const int64_t t0 = blockIdx.x / p.split, t_step = gridDim.x / p.split;
+  const int kbs = (p.k + 127) / 128;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(kbs) * rank / p.split);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(kbs) * (rank + 1) / p.split);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int b = 0; b < C::AB; ++b) {
+      mbar_init(afull(b), 1);
+      mbar_init(aempty(b), C::EPI);
+    }
+    for (int g = 0; g < C::SG; ++g) {
+      mbar_init(sfull(g), 64);
+      mbar_init(sempty(g), C::EPI);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_a);
+    tma_prefetch_desc(&p.tm_w);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int st = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int64_t t = t0; t < tiles && ok; t += t_step) {
+        const ProjectTile tile = tile_at(t, m_tiles, n_tiles, NT);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!(ok = mbar_wait(empty(st), ph ^ 1, abort_flag, p.err))) break;
+          mbar_arrive_expect_tx(full(st), C::STAGE);
+          const uint32_t dst = sbase + st * C::STAGE;
+          tma_load_3d(dst, &p.tm_w, kb * 128, tile.n0, tile.b, full(st));
+          tma_load_3d(dst + C::W_BYTES, &p.tm_a, kb * 128, tile.b, static_cast<int32_t>(tile.m0), full(st));
+          if (++st == C::STAGES) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      int st = 0, ab = 0;
+      uint32_t ph = 0, aph = 0;
+      bool ok = true;
+      for (int64_t t = t0; t < tiles && ok; t += t_step) {
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!(ok = mbar_wait(full(st), ph, abort_flag, p.err))) break;
+          if (!(ok = mbar_wait(aempty(ab), aph ^ 1, abort_flag, p.err))) break;
+          tc_fence_after();
+          const uint32_t waddr = sbase + st * C::STAGE, aaddr = waddr + C::W_BYTES;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)   // K = 32 codes (32 bytes) per step
+            mma_f8_ss(tmem_base + ab * NT, smem_desc(waddr + k * 32, 16, 1024, kSwizzle128),
+                      smem_desc(aaddr + k * 32, 16, 1024, kSwizzle128), C::IDESC, k != 0 ? 1u : 0u);
+          mma_commit(empty(st));
+          mma_commit(afull(ab));
+          if (++st == C::STAGES) {
+            st = 0;
+            ph ^= 1;
+          }
+          if (++ab == C::AB) {
+            ab = 0;
+            aph ^= 1;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ scales
+    const int ht = threadIdx.x - 64;
+    int sg = 0;
+    uint32_t sph = 0;
+    bool ok = true;
+    for (int64_t t = t0; t < tiles && ok; t += t_step) {
+      const ProjectTile tile = tile_at(t, m_tiles, n_tiles, NT);
+      const float *ws = p.w_scale + tile.b * p.ws_batch + tile.n0 / 128 * p.ws_stride;
+      const float *as = p.a_scale + tile.b * p.as_batch;
+      for (int kb = kb0; kb < kb1; kb += C::GK) {
+        float sw[C::GK];
+#pragma unroll
+        for (int g = 0; g < C::GK; ++g) sw[g] = kb + g < kb1 ? __ldg(ws + kb + g) : 0.f;
+        if (!(ok = mbar_wait(sempty(sg), sph ^ 1, abort_flag, p.err))) break;
+        float *slot = reinterpret_cast<float *>(smem + C::OFF_S + sg * C::S_SLOT);
+        for (int c = ht; c < NT; c += 64) {
+          const int64_t m = tile.m0 + c;
+          float sa[C::GK];
+#pragma unroll
+          for (int g = 0; g < C::GK; ++g) sa[g] = m < live && kb + g < kb1 ? __ldg(as + m * p.as_stride + kb + g) : 0.f;
+#pragma unroll
+          for (int g = 0; g < C::GK; ++g) slot[g * NT + c] = sa[g] * sw[g];
+        }
+        mbar_arrive(sfull(sg));
+        if (++sg == C::SG) {
+          sg = 0;
+          sph ^= 1;
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quad = warp & 3;
+    const int col0 = (warp - 4) / 4 * C::COLS;
+    const int nl = quad * 32 + lane;   // weight row within the tile
+    int ab = 0, sg = 0;
+    uint32_t aph = 0, sph = 0;
+    bool ok = true;
+    for (int64_t t = t0; t < tiles && ok; t += t_step) {
+      const ProjectTile tile = tile_at(t, m_tiles, n_tiles, NT);
+      uint64_t acc[C::COLS / 2];   // pairs of columns
+#pragma unroll
+      for (int c = 0; c < C::COLS / 2; ++c) acc[c] = 0;
+      for (int kb = kb0; kb < kb1 && ok; kb += C::GK) {
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(sfull(sg), sph, abort_flag, p.err)))) break;
+        const float *slot = reinterpret_cast<const float *>(smem + C::OFF_S + sg * C::S_SLOT) + col0;
+        const int gn = min(C::GK, kb1 - kb);
+        for (int g = 0; g < gn; ++g) {
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(afull(ab), aph, abort_flag, p.err)))) break;
+          tc_fence_after();
+          const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + ab * NT + col0;
+#pragma unroll
+          for (int c = 0; c < C::COLS; c += 16) {
+            float v[16];
+            tmem_ld16(tb + c, v);
+            tmem_ld_wait();
+            if (c + 16 == C::COLS) {   // everything is read: the buffer goes back
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(aempty(ab));
+            }
+            const ulonglong2 *s2 = reinterpret_cast<const ulonglong2 *>(slot + g * NT + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const ulonglong2 s = s2[i];
+              acc[c / 2 + 2 * i] = f2_fma(f2_pack(v[4 * i], v[4 * i + 1]), s.x, acc[c / 2 + 2 * i]);
+              acc[c / 2 + 2 * i + 1] = f2_fma(f2_pack(v[4 * i + 2], v[4 * i + 3]), s.y, acc[c / 2 + 2 * i + 1]);
+            }
+          }
+          if (++ab == C::AB) {
+            ab = 0;
+            aph ^= 1;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sempty(sg));
+        if (++sg == C::SG) {
+          sg = 0;
+          sph ^= 1;
+        }
+      }
+      if (!ok) break;
+      const int n = tile.n0 + nl;
+      if (p.split == 1) {
+        if (n < p.n) {
+#pragma unroll
+          for (int c = 0; c < C::COLS; c += 2) {
+            float x, y;
+            f2_unpack(acc[c / 2], x, y);
+            const int64_t m = tile.m0 + col0 + c;
+            if (m < live) store_out(p, m, tile.b, n, x);
+            if (m + 1 < live) store_out(p, m + 1, tile.b, n, y);
+          }
+        }
+      } else {
+        // every MMA has completed (this thread has seen the last block), so
+        // the stages are free for the partial sums: [column][weight row]
+        float *part = reinterpret_cast<float *>(smem) + nl;
+#pragma unroll
+        for (int c = 0; c < C::COLS; c += 2) {
+          float x, y;
+          f2_unpack(acc[c / 2], x, y);
+          part[(col0 + c) * 128] = x;
+          part[(col0 + c + 1) * 128] = y;
+        }
+      }
+    }
+  }
+
+  if (p.split > 1) {
+    // one tile a cluster (t_step covers them all)
+    __syncwarp();
+    cluster_sync();
+    if (t0 < tiles && !*abort_flag) {
+      const ProjectTile tile = tile_at(t0, m_tiles, n_tiles, NT);
+      const int c0 = NT * rank / p.split, c1 = NT * (rank + 1) / p.split;
+      const int cols = static_cast<int>(min(static_cast<int64_t>(c1), live - tile.m0)) - c0;
+      for (int i = threadIdx.x; i < cols * 128; i += C::THREADS) {
+        const int c = c0 + i / 128, nl = i % 128;
+        const uint32_t at = sbase + static_cast<uint32_t>(c * 128 + nl) * 4;
+        float sum = 0.f;
+        for (int r = 0; r < p.split; ++r) sum += ld_cluster_f32(map_to_cta(at, r));
+        if (tile.n0 + nl < p.n) store_out(p, tile.m0 + c, tile.b, tile.n0 + nl, sum);
+      }
+    }
+    cluster_sync();   // no CTA leaves while another may read its shared memory
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, C::TMEM_COLS);
+}
 
 __device__ __forceinline__ float e4m3_value(uint8_t c) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
 }
 
-// CUDA-core form: 64 x 64 outputs a CTA, 4 x 4 a thread.
+// CUDA-core form, for codes that are not on 16 bytes: 64 x 64 outputs a CTA, 4 x 4 a thread.
 __global__ void __launch_bounds__(256) project_simt_kernel(const ProjectParams p) {
   __shared__ float as[32][65], ws[32][65];
   const int64_t live = live_rows(p.rows, p.count, p.per_row);
@@ -79,11 +400,70 @@ __global__ void __launch_bounds__(256) project_simt_kernel(const ProjectParams p
     }
 }
 
+template <int NT>
+cudaError_t run_tc(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &p, int split, cudaStream_t s) {
+  using C = ProjectTraits<NT>;
+  // a dimension of one element takes any stride
+  auto stride = [](int64_t st, int64_t count) { return static_cast<uint64_t>(count > 1 ? st : 16); };
+  {
+    const uint64_t dims[3] = {static_cast<uint64_t>(g.k), static_cast<uint64_t>(g.batch), static_cast<uint64_t>(g.rows)};
+    const uint64_t strides[2] = {stride(g.a_batch, g.batch), stride(g.a_stride, g.rows)};
+    const uint32_t box[3] = {128, 1, NT};
+    if (!encode_tiled_3d(&p.tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(p.a), dims, strides, box,
+                         CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
+  {
+    const uint64_t dims[3] = {static_cast<uint64_t>(g.k), static_cast<uint64_t>(g.n), static_cast<uint64_t>(g.batch)};
+    const uint64_t strides[2] = {stride(g.w_stride, g.n), stride(g.w_batch, g.batch)};
+    const uint32_t box[3] = {128, 128, 1};
+    if (!encode_tiled_3d(&p.tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(p.w), dims, strides, box,
+                         CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
+  p.split = split;
+  const int64_t tiles = (g.rows + NT - 1) / NT * ((g.n + 127) / 128) * g.batch;
+  auto kern = project_tc_kernel<NT>;
+  static std::atomic<uint64_t> smem_limit_set{0};
+  if (cudaError_t e = ensure_smem_limit(kern, C::SMEM, ctx->device, smem_limit_set); e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(split > 1 ? tiles * split : std::min<int64_t>(tiles, ctx->num_sms)));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = split;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<const ProjectParams &>(p));
+}
+
+// Tokens per tile and CTAs per tile.
+void choose(const dsa_ctx *ctx, const dsa_project_t &g, int *nt, int *split) {
+  const int64_t blocks = static_cast<int64_t>((g.n + 127) / 128) * g.batch;
+  auto tiles = [&](int t) { return (g.rows + t - 1) / t * blocks; };
+  *nt = g.rows <= 16 ? 16 : g.rows <= 32 ? 32 : g.rows <= 64 ? 64 : 128;
+  if (g.rows > 128 && tiles(256) >= ctx->num_sms) *nt = 256;
+  while (*nt > 64 && g.rows > 64 && tiles(*nt / 2) <= ctx->num_sms) *nt /= 2;
+  const int kbs = (g.k + 127) / 128;
+  *split = 1;
+  if (*nt < 256)
+    while (*split < 8 && tiles(*nt) * *split * 2 <= ctx->num_sms && kbs >= *split * 2 * 4) *split *= 2;
+}
+
 }  // namespace
 
-bool project_tc_supported(const dsa_project_t &, const void *, const void *) { return false; }
+bool project_tc_supported(const dsa_project_t &g, const void *a, const void *w) {
+  auto on16 = [](int64_t stride, int64_t count) {
+    return count <= 1 || (stride >= 16 && stride % 16 == 0 && stride < (int64_t(1) << 40));
+  };
+  return reinterpret_cast<uintptr_t>(a) % 16 == 0 && reinterpret_cast<uintptr_t>(w) % 16 == 0 &&
+         on16(g.a_stride, g.rows) && on16(g.a_batch, g.batch) && on16(g.w_stride, g.n) && on16(g.w_batch, g.batch);
+}
 
-cudaError_t launch_project_fp8(const dsa_ctx *, const dsa_project_t &g, const void *a, const float *a_scale,
+cudaError_t launch_project_fp8(const dsa_ctx *ctx, const dsa_project_t &g, const void *a, const float *a_scale,
                                const void *w, const float *w_scale, void *out, const int32_t *count, int32_t per_row,
                                cudaStream_t s, int32_t *launches) {
   ProjectParams p{};
@@ -101,7 +481,21 @@ cudaError_t launch_project_fp8(const dsa_ctx *, const dsa_project_t &g, const vo
   p.ws_stride = g.w_scale_stride, p.ws_batch = g.w_scale_batch;
   p.out_stride = g.out_stride, p.out_batch = g.out_batch;
   p.n = g.n, p.k = g.k;
+  p.batch = g.batch;
   p.out_type = g.out_type;
+  p.err = ctx->err;
+  if (project_tc_supported(g, a, w)) {
+    int nt, split;
+    choose(ctx, g, &nt, &split);
+    *launches += 1;
+    switch (nt) {
+      case 16: return run_tc<16>(ctx, g, p, split, s);
+      case 32: return run_tc<32>(ctx, g, p, split, s);
+      case 64: return run_tc<64>(ctx, g, p, split, s);
+      case 128: return run_tc<128>(ctx, g, p, split, s);
+      default: return run_tc<256>(ctx, g, p, split, s);
+    }
+  }
   const dim3 grid(static_cast<unsigned>((g.rows + 63) / 64), (g.n + 63) / 64, g.batch);
   project_simt_kernel<<<grid, 256, 0, s>>>(p);
   *launches += 1;

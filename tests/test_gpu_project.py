@@ -100,6 +100,7 @@ def test_strided_and_unaligned_layouts(ctx, pad, shift, fast):
     for dt in (BF16, F32):
         store = torch.full((batch, rows + 2, n + 5), 77.0, dtype=dt, device="cuda")
         out = store[:, 1:rows + 1, 3:n + 3].transpose(0, 1)
+        assert ctx.project_on_tensor_cores(a2, as2, w2, ws2, out) == fast
         ctx.project_fp8(a2, as2, w2, ws2, out=out)
         check(out, a, asc, w, wsc)
         out.fill_(77.0)
