@@ -36,6 +36,7 @@ namespace {
 struct ProjectParams {
   CUtensorMap tm_a;   // token codes as [rows][batch][k], box {128, 1, NT}, 128-byte swizzle
   CUtensorMap tm_w;   // weight codes as [batch][n][k], box {128, 128, 1}, 128-byte swizzle
+  CUtensorMap tm_out; // out as [rows][batch][n], box {128 bytes, 1, 32}, 128-byte swizzle (pair kernel, where out_tma)
   const uint8_t *a, *w;
   const float *a_scale, *w_scale;
   void *out;
@@ -44,17 +45,10 @@ struct ProjectParams {
   int64_t rows;
   int64_t a_stride, a_batch, w_stride, w_batch, as_stride, as_batch, ws_stride, ws_batch, out_stride, out_batch;
   int32_t n, k, batch, per_row, out_type, split;
+  bool out_vec;   // rows of out start on 16 bytes
+  bool out_tma;   // and every row is live: whole boxes are stored by TMA
 };
 
-__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -69,11 +63,14 @@ struct ProjectTraits {
   static constexpr int COLS = NT / (EPI / 4);               // columns of an epilogue thread
   static constexpr int W_BYTES = 128 * 128, A_BYTES = NT * 128;
   static constexpr int STAGE = W_BYTES + A_BYTES;
-  static constexpr int STAGES = NT == 256 ? 4 : NT == 128 ? 6 : NT == 64 ? 8 : 10;
-  static constexpr int AB = NT == 256 ? 2 : 4;              // tensor-memory buffers
+  static constexpr int STAGES = NT == 128 ? 6 : NT == 64 ? 8 : 10;
+  static constexpr int AB = 4;                              // tensor-memory buffers
   static constexpr int TMEM_COLS = AB * NT;
-  static constexpr int GK = 4, SG = 3;                      // k blocks per scale slot, slots
-  static constexpr int S_SLOT = GK * NT * 4;
+  static constexpr int GK = NT == 128 ? 8 : 16; // k blocks per scale slot
+  static constexpr int SG = 3;                              // slots
+  static constexpr int S_ROW = NT + 4;                      // floats of a k block's scales (+4: fewer bank conflicts)
+  static constexpr int S_SLOT = GK * S_ROW * 4;
+  static constexpr int S_VALS = NT * GK / 64;               // values a helper thread brings to a slot
   static constexpr uint32_t IDESC = mma_idesc(128, NT, 0u, false, false);   // kind::f8f6f4: format 0 = e4m3
   static constexpr int OFF_S = STAGES * STAGE;
   static constexpr int OFF_BAR = OFF_S + SG * S_SLOT;
@@ -116,6 +113,7 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
   auto sempty = [&](int g) { return bar0 + 8u * (2 * C::STAGES + 2 * C::AB + C::SG + g); };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+  const uint32_t aborted = sbase + C::OFF_MISC + 4;
 
   const int warp = threadIdx.x / 32;
   const int lane = lane_id();
@@ -158,85 +156,92 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int st = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int64_t t = t0; t < tiles && ok; t += t_step) {
-        const ProjectTile tile = tile_at(t, m_tiles, n_tiles, NT);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!(ok = mbar_wait(empty(st), ph ^ 1, abort_flag, p.err))) break;
+    int st = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int64_t t = t0; t < tiles && ok; t += t_step) {
+      const ProjectTile tile = tile_at(t, m_tiles, n_tiles, NT);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!(ok = mbar_wait_warp(empty(st), ph ^ 1, aborted, p.err))) break;
+        if (elect_one()) {
           mbar_arrive_expect_tx(full(st), C::STAGE);
           const uint32_t dst = sbase + st * C::STAGE;
           tma_load_3d(dst, &p.tm_w, kb * 128, tile.n0, tile.b, full(st));
           tma_load_3d(dst + C::W_BYTES, &p.tm_a, kb * 128, tile.b, static_cast<int32_t>(tile.m0), full(st));
-          if (++st == C::STAGES) {
-            st = 0;
-            ph ^= 1;
-          }
+        }
+        __syncwarp();
+        if (++st == C::STAGES) {
+          st = 0;
+          ph ^= 1;
         }
       }
     }
-    __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      int st = 0, ab = 0;
-      uint32_t ph = 0, aph = 0;
-      bool ok = true;
-      for (int64_t t = t0; t < tiles && ok; t += t_step) {
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!(ok = mbar_wait(full(st), ph, abort_flag, p.err))) break;
-          if (!(ok = mbar_wait(aempty(ab), aph ^ 1, abort_flag, p.err))) break;
-          tc_fence_after();
-          const uint32_t waddr = sbase + st * C::STAGE, aaddr = waddr + C::W_BYTES;
+    const uint64_t desc0 = smem_desc(sbase, 16, 1024, kSwizzle128);
+    int st = 0, ab = 0;
+    uint32_t ph = 0, aph = 0;
+    bool ok = true;
+    for (int64_t t = t0; t < tiles && ok; t += t_step) {
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!(ok = mbar_wait_warp(full(st), ph, aborted, p.err) &&
+                    mbar_wait_warp(aempty(ab), aph ^ 1, aborted, p.err)))
+          break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t wd = desc0 + st * (C::STAGE >> 4), ad = wd + (C::W_BYTES >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)   // K = 32 codes (32 bytes) per step
-            mma_f8_ss(tmem_base + ab * NT, smem_desc(waddr + k * 32, 16, 1024, kSwizzle128),
-                      smem_desc(aaddr + k * 32, 16, 1024, kSwizzle128), C::IDESC, k != 0 ? 1u : 0u);
+            mma_f8<false>(tmem_base + ab * NT, wd + 2 * k, ad + 2 * k, C::IDESC, k != 0 ? 1u : 0u);
           mma_commit(empty(st));
           mma_commit(afull(ab));
-          if (++st == C::STAGES) {
-            st = 0;
-            ph ^= 1;
-          }
-          if (++ab == C::AB) {
-            ab = 0;
-            aph ^= 1;
-          }
+        }
+        __syncwarp();
+        if (++st == C::STAGES) {
+          st = 0;
+          ph ^= 1;
+        }
+        if (++ab == C::AB) {
+          ab = 0;
+          aph ^= 1;
         }
       }
     }
-    __syncwarp();
   } else if (warp < 4) {
     // ------------------------------------------------------------ scales
+    // thread: k block g of a slot and every (64 / GK)th token; the loads of
+    // the next slot are in flight while this one waits for its turn
     const int ht = threadIdx.x - 64;
+    const int g = ht % C::GK, c0 = ht / C::GK;
+    float sa[C::S_VALS], sw = 0.f;
+    auto load = [&](const ProjectTile &tile, int kb) {
+      const bool in = kb + g < kb1;
+      sw = in ? __ldg(p.w_scale + tile.b * p.ws_batch + tile.n0 / 128 * p.ws_stride + kb + g) : 0.f;
+      const float *as = p.a_scale + tile.b * p.as_batch + kb + g;
+#pragma unroll
+      for (int j = 0; j < C::S_VALS; ++j) {
+        const int64_t m = tile.m0 + c0 + j * (64 / C::GK);
+        sa[j] = in && m < live ? __ldg(as + m * p.as_stride) : 0.f;
+      }
+    };
     int sg = 0;
     uint32_t sph = 0;
     bool ok = true;
+    if (t0 < tiles) load(tile_at(t0, m_tiles, n_tiles, NT), kb0);
     for (int64_t t = t0; t < tiles && ok; t += t_step) {
       const ProjectTile tile = tile_at(t, m_tiles, n_tiles, NT);
-      const float *ws = p.w_scale + tile.b * p.ws_batch + tile.n0 / 128 * p.ws_stride;
-      const float *as = p.a_scale + tile.b * p.as_batch;
       for (int kb = kb0; kb < kb1; kb += C::GK) {
-        float sw[C::GK];
+        if (!(ok = mbar_wait_warp(sempty(sg), sph ^ 1, aborted, p.err))) break;
+        float *slot = reinterpret_cast<float *>(smem + C::OFF_S + sg * C::S_SLOT) + g * C::S_ROW + c0;
 #pragma unroll
-        for (int g = 0; g < C::GK; ++g) sw[g] = kb + g < kb1 ? __ldg(ws + kb + g) : 0.f;
-        if (!(ok = mbar_wait(sempty(sg), sph ^ 1, abort_flag, p.err))) break;
-        float *slot = reinterpret_cast<float *>(smem + C::OFF_S + sg * C::S_SLOT);
-        for (int c = ht; c < NT; c += 64) {
-          const int64_t m = tile.m0 + c;
-          float sa[C::GK];
-#pragma unroll
-          for (int g = 0; g < C::GK; ++g) sa[g] = m < live && kb + g < kb1 ? __ldg(as + m * p.as_stride + kb + g) : 0.f;
-#pragma unroll
-          for (int g = 0; g < C::GK; ++g) slot[g * NT + c] = sa[g] * sw[g];
-        }
+        for (int j = 0; j < C::S_VALS; ++j) slot[j * (64 / C::GK)] = sa[j] * sw;
         mbar_arrive(sfull(sg));
         if (++sg == C::SG) {
           sg = 0;
           sph ^= 1;
         }
+        if (kb + C::GK < kb1) load(tile, kb + C::GK);
+        else if (t + t_step < tiles) load(tile_at(t + t_step, m_tiles, n_tiles, NT), kb0);
       }
     }
     __syncwarp();
@@ -250,34 +255,36 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
     bool ok = true;
     for (int64_t t = t0; t < tiles && ok; t += t_step) {
       const ProjectTile tile = tile_at(t, m_tiles, n_tiles, NT);
-      uint64_t acc[C::COLS / 2];   // pairs of columns
+      float acc[C::COLS];
 #pragma unroll
-      for (int c = 0; c < C::COLS / 2; ++c) acc[c] = 0;
+      for (int c = 0; c < C::COLS; ++c) acc[c] = 0.f;
       for (int kb = kb0; kb < kb1 && ok; kb += C::GK) {
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(sfull(sg), sph, abort_flag, p.err)))) break;
+        if (!(ok = mbar_wait_warp(sfull(sg), sph, aborted, p.err))) break;
         const float *slot = reinterpret_cast<const float *>(smem + C::OFF_S + sg * C::S_SLOT) + col0;
         const int gn = min(C::GK, kb1 - kb);
         for (int g = 0; g < gn; ++g) {
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(afull(ab), aph, abort_flag, p.err)))) break;
+          if (!(ok = mbar_wait_warp(afull(ab), aph, aborted, p.err))) break;
           tc_fence_after();
           const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + ab * NT + col0;
+          float v[C::COLS];
+          if (C::COLS >= 32) {
 #pragma unroll
-          for (int c = 0; c < C::COLS; c += 16) {
-            float v[16];
-            tmem_ld16(tb + c, v);
-            tmem_ld_wait();
-            if (c + 16 == C::COLS) {   // everything is read: the buffer goes back
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(aempty(ab));
-            }
-            const ulonglong2 *s2 = reinterpret_cast<const ulonglong2 *>(slot + g * NT + c);
+            for (int c = 0; c < C::COLS; c += 32) tmem_ld32(tb + c, *reinterpret_cast<float(*)[32]>(v + c));
+          } else {
+            tmem_ld16(tb, *reinterpret_cast<float(*)[16]>(v));
+          }
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_relaxed(aempty(ab));   // everything is read: the buffer goes back
+          const float4 *s4 = reinterpret_cast<const float4 *>(slot + g * C::S_ROW);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const ulonglong2 s = s2[i];
-              acc[c / 2 + 2 * i] = f2_fma(f2_pack(v[4 * i], v[4 * i + 1]), s.x, acc[c / 2 + 2 * i]);
-              acc[c / 2 + 2 * i + 1] = f2_fma(f2_pack(v[4 * i + 2], v[4 * i + 3]), s.y, acc[c / 2 + 2 * i + 1]);
-            }
+          for (int c = 0; c < C::COLS / 4; ++c) {
+            const float4 sc = s4[c];
+            acc[4 * c] = fmaf(v[4 * c], sc.x, acc[4 * c]);
+            acc[4 * c + 1] = fmaf(v[4 * c + 1], sc.y, acc[4 * c + 1]);
+            acc[4 * c + 2] = fmaf(v[4 * c + 2], sc.z, acc[4 * c + 2]);
+            acc[4 * c + 3] = fmaf(v[4 * c + 3], sc.w, acc[4 * c + 3]);
           }
           if (++ab == C::AB) {
             ab = 0;
@@ -296,25 +303,15 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
       if (p.split == 1) {
         if (n < p.n) {
 #pragma unroll
-          for (int c = 0; c < C::COLS; c += 2) {
-            float x, y;
-            f2_unpack(acc[c / 2], x, y);
-            const int64_t m = tile.m0 + col0 + c;
-            if (m < live) store_out(p, m, tile.b, n, x);
-            if (m + 1 < live) store_out(p, m + 1, tile.b, n, y);
-          }
+          for (int c = 0; c < C::COLS; ++c)
+            if (tile.m0 + col0 + c < live) store_out(p, tile.m0 + col0 + c, tile.b, n, acc[c]);
         }
       } else {
         // every MMA has completed (this thread has seen the last block), so
         // the stages are free for the partial sums: [column][weight row]
         float *part = reinterpret_cast<float *>(smem) + nl;
 #pragma unroll
-        for (int c = 0; c < C::COLS; c += 2) {
-          float x, y;
-          f2_unpack(acc[c / 2], x, y);
-          part[(col0 + c) * 128] = x;
-          part[(col0 + c + 1) * 128] = y;
-        }
+        for (int c = 0; c < C::COLS; ++c) part[(col0 + c) * 128] = acc[c];
       }
     }
   }
@@ -342,6 +339,342 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem_base, C::TMEM_COLS);
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: a pair of CTAs (cta_group::2) shares tiles of 256 tokens (the
+// MMA's rows, 128 lanes in each CTA) by 256 weight rows (its columns); each CTA
+// brings half of both, so a block of k costs a CTA 32 KB for 128 x 256 x 128
+// products.  Tokens are the lanes here: an epilogue thread has one token and,
+// its warp being on one half of the columns, one weight block, so s is one
+// number of shared memory per block.  Two
+// tensor-memory buffers of 256 columns fill its 512.
+struct PairTraits {
+  static constexpr int EPI = 8;                             // epilogue warps: 4 per half of the columns
+  static constexpr int THREADS = 128 + 32 * EPI;
+  static constexpr int A_BYTES = 128 * 128, W_BYTES = 128 * 128;
+  static constexpr int STAGE = A_BYTES + W_BYTES;
+  static constexpr int STAGES = 4;
+  static constexpr int AB = 2;
+  static constexpr int GK = 4, SG = 3;                      // k blocks per scale slot, slots
+  static constexpr int S_SLOT = 2 * GK * 128 * 4;           // [half of the columns][k block][token]
+  static constexpr int S_VALS = 128 * GK / 64;              // token scales a helper thread brings to a slot
+  static constexpr int TMEM_COLS = 512;
+  static constexpr uint32_t IDESC = mma_idesc(256, 256, 0u, false, false);
+  static constexpr int OUT_WARP = 8192;                     // output staging of an epilogue warp: two boxes of 32 rows of 128 bytes
+  static constexpr int OFF_OUT = STAGES * STAGE;
+  static constexpr int OFF_S = OFF_OUT + EPI * OUT_WARP;
+  static constexpr int OFF_BAR = OFF_S + SG * S_SLOT;
+  static constexpr int NBAR = 2 * STAGES + 2 * AB + 2 * SG;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM = OFF_MISC + 16 + 1024;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  // registers: 384 threads launch with 168 each (64,512); the split keeps that sum
+  static constexpr int REGS_HELP = 72, REGS_EPI = 216;
+  static_assert(128 * REGS_HELP + 32 * EPI * REGS_EPI <= 384 * 168, "registers");
+};
+
+__device__ __forceinline__ ProjectTile pair_tile_at(int t, int m_tiles, int n_tiles) {
+  // groups of 8 token tiles, weights next, tokens within the group fastest:
+  // the tiles that run together share both operands in L2
+  const int per_b = m_tiles * n_tiles;
+  const int in_b = t % per_b;
+  const int group = in_b / (8 * n_tiles);
+  const int size = min(m_tiles - group * 8, 8);
+  const int in_g = in_b - group * 8 * n_tiles;
+  return {t / per_b, in_g / size * 256, static_cast<int64_t>(group * 8 + in_g % size) * 256};
+}
+
+// 32 rows of 128 bytes of columns from a swizzled box of shared memory to out, by one warp.
+__device__ __noinline__ void write_box(const ProjectParams &p, const uint8_t *box, int lane, int es, int64_t m0,
+                                       int64_t live, int b, int n0) {
+  const int chunk = lane & 7, per = 16 / es;
+  const int n = n0 + chunk * per;
+  for (int row = lane / 8; row < 32 && m0 + row < live; row += 4) {
+    if (n >= p.n) break;
+    const uint4 u = *reinterpret_cast<const uint4 *>(box + sw128_offset(row, chunk));
+    const int64_t at = (m0 + row) * p.out_stride + b * p.out_batch + n;
+    if (p.out_vec && n + per <= p.n) {
+      *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + at * es) = u;
+    } else {
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      for (int i = 0; i < per && n + i < p.n; ++i) {
+        if (es == 2) static_cast<uint16_t *>(p.out)[at + i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+        else static_cast<uint32_t *>(p.out)[at + i] = w[i];
+      }
+    }
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS, 1)
+    project_pair_kernel(const __grid_constant__ ProjectParams p) {
+  using C = PairTraits;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::OFF_BAR;
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
+  auto afull = [&](int b) { return bar0 + 8u * (2 * C::STAGES + b); };
+  auto aempty = [&](int b) { return bar0 + 8u * (2 * C::STAGES + C::AB + b); };
+  auto sfull = [&](int g) { return bar0 + 8u * (2 * C::STAGES + 2 * C::AB + g); };
+  auto sempty = [&](int g) { return bar0 + 8u * (2 * C::STAGES + 2 * C::AB + C::SG + g); };
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+  const uint32_t aborted = sbase + C::OFF_MISC + 4;
+
+  const int warp = threadIdx.x / 32;
+  const int lane = lane_id();
+  const int rank = static_cast<int>(cluster_rank());
+  const int64_t live = live_rows(p.rows, p.count, p.per_row);
+  const int m_tiles = static_cast<int>((live + 255) / 256);
+  const int n_tiles = (p.n + 255) / 256;
+  const int tiles = m_tiles * n_tiles * p.batch;
+  const int t0 = blockIdx.x / 2, t_step = gridDim.x / 2;
+  const int kbs = (p.k + 127) / 128;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int b = 0; b < C::AB; ++b) {
+      mbar_init(afull(b), 1);
+      mbar_init(aempty(b), 2 * C::EPI);   // both CTAs' epilogue warps, on the first CTA's barrier
+    }
+    for (int g = 0; g < C::SG; ++g) {
+      mbar_init(sfull(g), 64);
+      mbar_init(sempty(g), C::EPI);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_a);
+    tma_prefetch_desc(&p.tm_w);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_HELP));
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer (both CTAs)
+      int st = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = t0; t < tiles && ok; t += t_step) {
+        const ProjectTile tile = pair_tile_at(t, m_tiles, n_tiles);
+        const int m = static_cast<int>(tile.m0) + rank * 128, n = tile.n0 + rank * 128;
+        for (int kb = 0; kb < kbs; ++kb) {
+          if (!(ok = mbar_wait_warp(empty(st), ph ^ 1, aborted, p.err))) break;
+          if (elect_one()) {
+            // the first CTA's barrier counts both CTAs' bytes
+            if (rank == 0) mbar_arrive_expect_tx(full(st), 2 * C::STAGE);
+            const uint32_t dst = sbase + st * C::STAGE, bar = map_to_cta(full(st), 0);
+            tma_load_3d_pair(dst, &p.tm_a, kb * 128, tile.b, m, bar);
+            tma_load_3d_pair(dst + C::A_BYTES, &p.tm_w, kb * 128, n, tile.b, bar);
+          }
+          __syncwarp();
+          if (++st == C::STAGES) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      // the last commits have arrived here before this CTA may leave
+      for (int i = 0; i < C::STAGES && ok; ++i) {
+        ok = mbar_wait_warp(empty(st), ph ^ 1, aborted, p.err);
+        if (++st == C::STAGES) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    } else if (warp == 1 && rank == 0) {
+      // ---------------------------------------------------------- MMA issuer (first CTA)
+      const uint64_t desc0 = smem_desc(sbase, 16, 1024, kSwizzle128);
+      int st = 0, ab = 0;
+      uint32_t ph = 0, aph = 0;
+      bool ok = true;
+      for (int t = t0; t < tiles && ok; t += t_step) {
+        for (int kb = 0; kb < kbs; ++kb) {
+          if (!(ok = mbar_wait_warp(full(st), ph, aborted, p.err) &&
+                      mbar_wait_warp(aempty(ab), aph ^ 1, aborted, p.err)))
+            break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t ad = desc0 + st * (C::STAGE >> 4), wd = ad + (C::A_BYTES >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f8<true>(tmem_base + ab * 256, ad + 2 * k, wd + 2 * k, C::IDESC, k != 0 ? 1u : 0u);
+            mma_commit_pair(empty(st), 3);
+            mma_commit_pair(afull(ab), 3);
+          }
+          __syncwarp();
+          if (++st == C::STAGES) {
+            st = 0;
+            ph ^= 1;
+          }
+          if (++ab == C::AB) {
+            ab = 0;
+            aph ^= 1;
+          }
+        }
+      }
+    } else if (warp >= 2) {
+      // ---------------------------------------------------------- scales (both CTAs)
+      // thread: k block g of a slot and every 16th token; the loads of the
+      // next slot are in flight while this one waits for its turn
+      const int ht = threadIdx.x - 64;
+      const int g = ht % C::GK, c0 = ht / C::GK;
+      float sa[C::S_VALS], sw[2] = {0.f, 0.f};
+      auto load = [&](const ProjectTile &tile, int kb) {
+        const bool in = kb + g < kbs;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int n = tile.n0 + h * 128;
+          sw[h] = in && n < p.n ? __ldg(p.w_scale + tile.b * p.ws_batch + n / 128 * p.ws_stride + kb + g) : 0.f;
+        }
+        const float *as = p.a_scale + tile.b * p.as_batch + kb + g;
+#pragma unroll
+        for (int j = 0; j < C::S_VALS; ++j) {
+          const int64_t m = tile.m0 + rank * 128 + c0 + j * (64 / C::GK);
+          sa[j] = in && m < live ? __ldg(as + m * p.as_stride) : 0.f;
+        }
+      };
+      int sg = 0;
+      uint32_t sph = 0;
+      bool ok = true;
+      if (t0 < tiles) load(pair_tile_at(t0, m_tiles, n_tiles), 0);
+      for (int t = t0; t < tiles && ok; t += t_step) {
+        const ProjectTile tile = pair_tile_at(t, m_tiles, n_tiles);
+        for (int kb = 0; kb < kbs; kb += C::GK) {
+          if (!(ok = mbar_wait_warp(sempty(sg), sph ^ 1, aborted, p.err))) break;
+          float *slot = reinterpret_cast<float *>(smem + C::OFF_S + sg * C::S_SLOT) + g * 128 + c0;
+#pragma unroll
+          for (int j = 0; j < C::S_VALS; ++j) {
+            slot[j * (64 / C::GK)] = sa[j] * sw[0];
+            slot[C::GK * 128 + j * (64 / C::GK)] = sa[j] * sw[1];
+          }
+          mbar_arrive(sfull(sg));
+          if (++sg == C::SG) {
+            sg = 0;
+            sph ^= 1;
+          }
+          if (kb + C::GK < kbs) load(tile, kb + C::GK);
+          else if (t + t_step < tiles) load(pair_tile_at(t + t_step, m_tiles, n_tiles), 0);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_EPI));
+    const int quad = warp & 3;
+    const int col0 = (warp - 4) / 4 * 128;   // the warp's first column of the tile
+    const uint32_t tb0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + col0;
+    const int es = p.out_type == DSA_BF16 ? 2 : 4;
+    uint8_t *stage_out = smem + C::OFF_OUT + (warp - 4) * C::OUT_WARP;
+    int ab = 0, sg = 0;
+    uint32_t aph = 0, sph = 0;
+    bool ok = true;
+    for (int t = t0; t < tiles && ok; t += t_step) {
+      float acc[128];
+#pragma unroll
+      for (int c = 0; c < 128; ++c) acc[c] = 0.f;
+      for (int kb = 0; kb < kbs && ok; kb += C::GK) {
+        if (!(ok = mbar_wait_warp(sfull(sg), sph, aborted, p.err))) break;
+        const float *slot = reinterpret_cast<const float *>(smem + C::OFF_S + sg * C::S_SLOT) +
+                            col0 / 128 * C::GK * 128 + quad * 32 + lane;
+        const int gn = min(C::GK, kbs - kb);
+#pragma unroll 1
+        for (int g = 0; g < gn; ++g) {
+          if (!(ok = mbar_wait_warp(afull(ab), aph, aborted, p.err))) break;
+          tc_fence_after();
+          const uint32_t tb = tb0 + ab * 256;
+          const float sc = slot[g * 128];
+          float v[2][32];
+          tmem_ld32(tb, v[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld_wait();
+            if (c < 3) {
+              tmem_ld32(tb + (c + 1) * 32, v[(c + 1) & 1]);
+            } else {   // everything is read: the buffer goes back
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_remote_relaxed(map_to_cta(aempty(ab), 0));
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(v[c & 1][i], sc, acc[c * 32 + i]);
+          }
+          if (++ab == C::AB) {
+            ab = 0;
+            aph ^= 1;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sempty(sg));
+        if (++sg == C::SG) {
+          sg = 0;
+          sph ^= 1;
+        }
+      }
+      if (!ok) break;
+      const ProjectTile tile = pair_tile_at(t, m_tiles, n_tiles);
+      const int64_t mw = tile.m0 + rank * 128 + quad * 32;   // the warp's first token
+      const int nw = tile.n0 + col0;                         // and first column
+      // out, through shared memory: boxes of 32 rows by 128 bytes of columns,
+      // two at a time (all 128 columns of bf16, half of fp32).  A TMA store
+      // takes them while the next tile is under way; rows that TMA cannot take
+      // are written here, four to an instruction.
+      const uint32_t stage_addr = sbase + C::OFF_OUT + (warp - 4) * C::OUT_WARP;
+#pragma unroll
+      for (int c0 = 0; c0 < 128; c0 += 32) {   // half a box of bf16, a box of fp32
+        const int box = es == 2 ? c0 / 64 : c0 / 32 % 2;
+        if (es == 2 ? c0 == 0 : box == 0) {    // the stores that read these boxes before are done with them
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+        }
+        uint8_t *dst = stage_out + box * 4096;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {          // four columns
+          const float *x = acc + c0 + 4 * q;
+          if (es == 2) {
+            const uint2 u = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+            *reinterpret_cast<uint2 *>(dst + sw128_offset(lane, c0 % 64 / 8 + q / 2) + (q & 1) * 8) = u;
+          } else {
+            *reinterpret_cast<float4 *>(dst + sw128_offset(lane, q)) = make_float4(x[0], x[1], x[2], x[3]);
+          }
+        }
+        if (es == 2 && c0 % 64 == 0) continue;
+        const int n = nw + (es == 2 ? c0 - 32 : c0);   // the box's first column
+        if (p.out_tma) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && n < p.n && mw < live) {
+            tma_store_3d(&p.tm_out, stage_addr + box * 4096, n, tile.b, static_cast<int32_t>(mw));
+            bulk_commit();
+          }
+        } else {
+          __syncwarp();
+          write_box(p, dst, lane, es, mw, live, tile.b, n);
+          __syncwarp();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_read_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // neither CTA leaves while the other may signal it or read its operands
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
 }
 
 __device__ __forceinline__ float e4m3_value(uint8_t c) {
@@ -400,27 +733,50 @@ __global__ void __launch_bounds__(256) project_simt_kernel(const ProjectParams p
     }
 }
 
+// Tensor maps of both operands; box_a tokens a box of a.
+bool encode_operands(const dsa_project_t &g, ProjectParams &p, uint32_t box_a) {
+  // a dimension of one element takes any stride
+  auto stride = [](int64_t st, int64_t count) { return static_cast<uint64_t>(count > 1 ? st : 16); };
+  const uint64_t a_dims[3] = {static_cast<uint64_t>(g.k), static_cast<uint64_t>(g.batch), static_cast<uint64_t>(g.rows)};
+  const uint64_t a_strides[2] = {stride(g.a_batch, g.batch), stride(g.a_stride, g.rows)};
+  const uint32_t a_box[3] = {128, 1, box_a};
+  const uint64_t w_dims[3] = {static_cast<uint64_t>(g.k), static_cast<uint64_t>(g.n), static_cast<uint64_t>(g.batch)};
+  const uint64_t w_strides[2] = {stride(g.w_stride, g.n), stride(g.w_batch, g.batch)};
+  const uint32_t w_box[3] = {128, 128, 1};
+  return encode_tiled_3d(&p.tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(p.a), a_dims, a_strides, a_box,
+                         CU_TENSOR_MAP_SWIZZLE_128B) &&
+         encode_tiled_3d(&p.tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(p.w), w_dims, w_strides, w_box,
+                         CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+int64_t pair_tiles(const dsa_project_t &g) { return (g.rows + 255) / 256 * ((g.n + 255) / 256) * g.batch; }
+
+cudaError_t run_pair(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &p, cudaStream_t s) {
+  using C = PairTraits;
+  if (!encode_operands(g, p, 128)) return cudaErrorInvalidValue;
+  if (p.out_vec && p.count == nullptr) {
+    const bool bf16 = g.out_type == DSA_BF16;
+    const int64_t es = bf16 ? 2 : 4;
+    const uint64_t dims[3] = {static_cast<uint64_t>(g.n), static_cast<uint64_t>(g.batch), static_cast<uint64_t>(g.rows)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(g.batch > 1 ? g.out_batch * es : 16),
+                                 static_cast<uint64_t>(g.rows > 1 ? g.out_stride * es : 16)};
+    const uint32_t box[3] = {static_cast<uint32_t>(128 / es), 1, 32};
+    p.out_tma = encode_tiled_3d(&p.tm_out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                                p.out, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  }
+  static std::atomic<uint64_t> smem_limit_set{0};
+  if (cudaError_t e = ensure_smem_limit(project_pair_kernel, C::SMEM, ctx->device, smem_limit_set); e != cudaSuccess)
+    return e;
+  const int64_t tiles = pair_tiles(g);
+  const unsigned grid = static_cast<unsigned>(2 * std::min<int64_t>(tiles, ctx->num_sms / 2));
+  project_pair_kernel<<<grid, C::THREADS, C::SMEM, s>>>(p);
+  return cudaGetLastError();
+}
+
 template <int NT>
 cudaError_t run_tc(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &p, int split, cudaStream_t s) {
   using C = ProjectTraits<NT>;
-  // a dimension of one element takes any stride
-  auto stride = [](int64_t st, int64_t count) { return static_cast<uint64_t>(count > 1 ? st : 16); };
-  {
-    const uint64_t dims[3] = {static_cast<uint64_t>(g.k), static_cast<uint64_t>(g.batch), static_cast<uint64_t>(g.rows)};
-    const uint64_t strides[2] = {stride(g.a_batch, g.batch), stride(g.a_stride, g.rows)};
-    const uint32_t box[3] = {128, 1, NT};
-    if (!encode_tiled_3d(&p.tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(p.a), dims, strides, box,
-                         CU_TENSOR_MAP_SWIZZLE_128B))
-      return cudaErrorInvalidValue;
-  }
-  {
-    const uint64_t dims[3] = {static_cast<uint64_t>(g.k), static_cast<uint64_t>(g.n), static_cast<uint64_t>(g.batch)};
-    const uint64_t strides[2] = {stride(g.w_stride, g.n), stride(g.w_batch, g.batch)};
-    const uint32_t box[3] = {128, 128, 1};
-    if (!encode_tiled_3d(&p.tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(p.w), dims, strides, box,
-                         CU_TENSOR_MAP_SWIZZLE_128B))
-      return cudaErrorInvalidValue;
-  }
+  if (!encode_operands(g, p, NT)) return cudaErrorInvalidValue;
   p.split = split;
   const int64_t tiles = (g.rows + NT - 1) / NT * ((g.n + 127) / 128) * g.batch;
   auto kern = project_tc_kernel<NT>;
@@ -440,13 +796,13 @@ cudaError_t run_tc(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &p,
   return cudaLaunchKernelEx(&cfg, kern, static_cast<const ProjectParams &>(p));
 }
 
-// Tokens per tile and CTAs per tile.
+// Tokens per tile (256: the pair kernel) and CTAs per tile.
 void choose(const dsa_ctx *ctx, const dsa_project_t &g, int *nt, int *split) {
   const int64_t blocks = static_cast<int64_t>((g.n + 127) / 128) * g.batch;
   auto tiles = [&](int t) { return (g.rows + t - 1) / t * blocks; };
   *nt = g.rows <= 16 ? 16 : g.rows <= 32 ? 32 : g.rows <= 64 ? 64 : 128;
-  if (g.rows > 128 && tiles(256) >= ctx->num_sms) *nt = 256;
-  while (*nt > 64 && g.rows > 64 && tiles(*nt / 2) <= ctx->num_sms) *nt /= 2;
+  if (g.rows > 128 && tiles(256) >= ctx->num_sms && g.n > 128 && pair_tiles(g) < INT32_MAX / 8) *nt = 256;
+  while (*nt > 64 && *nt < 256 && tiles(*nt / 2) <= ctx->num_sms) *nt /= 2;
   const int kbs = (g.k + 127) / 128;
   *split = 1;
   if (*nt < 256)
@@ -484,6 +840,9 @@ cudaError_t launch_project_fp8(const dsa_ctx *ctx, const dsa_project_t &g, const
   p.batch = g.batch;
   p.out_type = g.out_type;
   p.err = ctx->err;
+  const int64_t es = g.out_type == DSA_BF16 ? 2 : 4;
+  p.out_vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && (g.rows == 1 || g.out_stride * es % 16 == 0) &&
+              (g.batch == 1 || g.out_batch * es % 16 == 0);
   if (project_tc_supported(g, a, w)) {
     int nt, split;
     choose(ctx, g, &nt, &split);
@@ -493,7 +852,7 @@ cudaError_t launch_project_fp8(const dsa_ctx *ctx, const dsa_project_t &g, const
       case 32: return run_tc<32>(ctx, g, p, split, s);
       case 64: return run_tc<64>(ctx, g, p, split, s);
       case 128: return run_tc<128>(ctx, g, p, split, s);
-      default: return run_tc<256>(ctx, g, p, split, s);
+      default: return run_pair(ctx, g, p, s);
     }
   }
   const dim3 grid(static_cast<unsigned>((g.rows + 63) / 64), (g.n + 63) / 64, g.batch);

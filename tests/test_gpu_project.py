@@ -70,6 +70,22 @@ def test_odd_and_ragged_sizes(ctx, rows, n, k):
     ctx.get_error()
 
 
+@pytest.mark.parametrize("rows,n,k", [(256, 20000, 128), (300, 10000, 144), (1031, 8192, 576), (2600, 2000, 272), (600, 6503, 16), (700, 6500, 1100)])
+def test_many_rows(ctx, rows, n, k):
+    """Shapes with a tile of 256 x 256 for every two SMs and more: whole and ragged tiles, one tile after another."""
+    t = make(rows + n + k, rows, n, k)
+    for dt in (BF16, F32):
+        check(ctx.project_fp8(*t, out_dtype=dt), *t)
+    ctx.get_error()
+
+
+def test_many_rows_and_heads(ctx):
+    for rows, batch, n, k in ((300, 40, 520, 128), (260, 128, 192, 576)):
+        t = make(rows, rows, n, k, batch)
+        check(ctx.project_fp8(*t), *t)
+    ctx.get_error()
+
+
 @pytest.mark.parametrize("rows,batch,n,k", [(1, 16, 128, 512), (3, 5, 512, 128), (17, 3, 65, 192), (140, 2, 128, 512), (300, 3, 192, 576),
                                             (2, 130, 64, 64)])
 def test_heads(ctx, rows, batch, n, k):
@@ -118,7 +134,7 @@ def test_one_weight_for_every_head(ctx):
 def test_both_kernels_give_what_the_definition_gives_for_integers(ctx):
     """Small whole codes and scales of powers of two: every sum is exact, so the
     two kernels, every split and the definition agree to the bit."""
-    for rows, n, k in ((1, 256, 2048), (16, 384, 1024), (100, 256, 512), (300, 136, 1152)):
+    for rows, n, k in ((1, 256, 2048), (16, 384, 1024), (100, 256, 512), (300, 136, 1152), (300, 9992, 384)):
         g = torch.Generator().manual_seed(rows)
         a = torch.randint(-3, 4, (rows, k), generator=g).float().to(torch.float8_e4m3fn).view(U8)
         w = torch.randint(-3, 4, (n, k), generator=g).float().to(torch.float8_e4m3fn).view(U8)
@@ -154,10 +170,10 @@ def test_no_rows_launch_nothing(ctx):
     assert ctx.last_launch_count() == 1
 
 
-@pytest.mark.parametrize("m", [1, 40])
-def test_padding_rows_of_a_capturable_plan_are_left(ctx, m):
+@pytest.mark.parametrize("m,n", [(1, 264), (40, 264), (80, 9000)])
+def test_padding_rows_of_a_capturable_plan_are_left(ctx, m, n):
     rows = 8 * m
-    t = make(10, rows, 264, 320)
+    t = make(10, rows, n, 320)
     full = ctx.project_fp8(*t)
     plan = None
     for live in (8, 0, 5):
@@ -168,14 +184,14 @@ def test_padding_rows_of_a_capturable_plan_are_left(ctx, m):
         a, asc, w, wsc = (x.clone() for x in t)
         a[live * m:] = 0x7F
         asc[live * m:] = float("nan")
-        out = torch.full((rows, 264), 77.0, dtype=BF16, device="cuda")
+        out = torch.full((rows, n), 77.0, dtype=BF16, device="cuda")
         ctx.project_fp8(a, asc, w, wsc, out=out, plan=plan)
         assert torch.equal(out[:live * m], full[:live * m]) and (out[live * m:] == 77).all()
     ctx.get_error()
 
 
 def test_equal_calls_give_equal_bits_on_any_stream(ctx):
-    for rows, n, k in ((1, 1024, 4096), (24, 512, 2048), (520, 384, 512)):
+    for rows, n, k in ((1, 1024, 4096), (24, 512, 2048), (520, 384, 512), (520, 9000, 512)):
         t = make(11, rows, n, k)
         ref = ctx.project_fp8(*t, out_dtype=F32)
         torch.cuda.synchronize()
