@@ -356,9 +356,9 @@ struct PairTraits {
   static constexpr int STAGE = A_BYTES + W_BYTES;
   static constexpr int STAGES = 4;
   static constexpr int AB = 2;
-  static constexpr int GK = 4, SG = 3;                      // k blocks per scale slot, slots
-  static constexpr int S_SLOT = 2 * GK * 128 * 4;           // [half of the columns][k block][token]
-  static constexpr int S_VALS = 128 * GK / 64;              // token scales a helper thread brings to a slot
+  static constexpr int GK = 16, SG = 3;                     // k blocks per scale slot, slots
+  static constexpr int S_ROW = 136;                         // floats of a k block's scales: 128 tokens, 2 weight blocks
+  static constexpr int S_SLOT = GK * S_ROW * 4;
   static constexpr int TMEM_COLS = 512;
   static constexpr uint32_t IDESC = mma_idesc(256, 256, 0u, false, false);
   static constexpr int OUT_WARP = 8192;                     // output staging of an epilogue warp: two boxes of 32 rows of 128 bytes
@@ -370,7 +370,7 @@ struct PairTraits {
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   // registers: 384 threads launch with 168 each (64,512); the split keeps that sum
-  static constexpr int REGS_HELP = 72, REGS_EPI = 216;
+  static constexpr int REGS_HELP = 56, REGS_EPI = 224;
   static_assert(128 * REGS_HELP + 32 * EPI * REGS_EPI <= 384 * 168, "registers");
 };
 
@@ -528,46 +528,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS,
       }
     } else if (warp >= 2) {
       // ---------------------------------------------------------- scales (both CTAs)
-      // thread: k block g of a slot and every 16th token; the loads of the
-      // next slot are in flight while this one waits for its turn
+      // thread: k block g of a slot and every fourth token, copied without a
+      // register in between; the two weight blocks' scales go beside them
       const int ht = threadIdx.x - 64;
       const int g = ht % C::GK, c0 = ht / C::GK;
-      float sa[C::S_VALS], sw[2] = {0.f, 0.f};
-      auto load = [&](const ProjectTile &tile, int kb) {
-        const bool in = kb + g < kbs;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int n = tile.n0 + h * 128;
-          sw[h] = in && n < p.n ? __ldg(p.w_scale + tile.b * p.ws_batch + n / 128 * p.ws_stride + kb + g) : 0.f;
-        }
-        const float *as = p.a_scale + tile.b * p.as_batch + kb + g;
-#pragma unroll
-        for (int j = 0; j < C::S_VALS; ++j) {
-          const int64_t m = tile.m0 + rank * 128 + c0 + j * (64 / C::GK);
-          sa[j] = in && m < live ? __ldg(as + m * p.as_stride) : 0.f;
-        }
-      };
       int sg = 0;
       uint32_t sph = 0;
       bool ok = true;
-      if (t0 < tiles) load(pair_tile_at(t0, m_tiles, n_tiles), 0);
       for (int t = t0; t < tiles && ok; t += t_step) {
         const ProjectTile tile = pair_tile_at(t, m_tiles, n_tiles);
+        const int m0 = static_cast<int>(tile.m0) + rank * 128;
         for (int kb = 0; kb < kbs; kb += C::GK) {
           if (!(ok = mbar_wait_warp(sempty(sg), sph ^ 1, aborted, p.err))) break;
-          float *slot = reinterpret_cast<float *>(smem + C::OFF_S + sg * C::S_SLOT) + g * 128 + c0;
-#pragma unroll
-          for (int j = 0; j < C::S_VALS; ++j) {
-            slot[j * (64 / C::GK)] = sa[j] * sw[0];
-            slot[C::GK * 128 + j * (64 / C::GK)] = sa[j] * sw[1];
+          const uint32_t row = sbase + C::OFF_S + sg * C::S_SLOT + g * C::S_ROW * 4;
+          if (kb + g < kbs) {
+            const float *as = p.a_scale + tile.b * p.as_batch + kb + g;
+#pragma unroll 4
+            for (int c = c0; c < 128; c += 64 / C::GK)
+              cp_async_4_zfill(row + c * 4, m0 + c < live ? as + (m0 + c) * p.as_stride : as, m0 + c < live ? 4 : 0);
+            if (c0 < 2) {
+              const int n = tile.n0 + c0 * 128;
+              const float *ws = p.w_scale + tile.b * p.ws_batch + kb + g;
+              cp_async_4_zfill(row + (128 + c0) * 4, n < p.n ? ws + n / 128 * p.ws_stride : ws, n < p.n ? 4 : 0);
+            }
           }
-          mbar_arrive(sfull(sg));
+          cp_async_mbar_arrive(sfull(sg));
           if (++sg == C::SG) {
             sg = 0;
             sph ^= 1;
           }
-          if (kb + C::GK < kbs) load(tile, kb + C::GK);
-          else if (t + t_step < tiles) load(pair_tile_at(t + t_step, m_tiles, n_tiles), 0);
         }
       }
     }
@@ -588,15 +577,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS,
       for (int c = 0; c < 128; ++c) acc[c] = 0.f;
       for (int kb = 0; kb < kbs && ok; kb += C::GK) {
         if (!(ok = mbar_wait_warp(sfull(sg), sph, aborted, p.err))) break;
-        const float *slot = reinterpret_cast<const float *>(smem + C::OFF_S + sg * C::S_SLOT) +
-                            col0 / 128 * C::GK * 128 + quad * 32 + lane;
+        const float *slot = reinterpret_cast<const float *>(smem + C::OFF_S + sg * C::S_SLOT);
         const int gn = min(C::GK, kbs - kb);
 #pragma unroll 1
         for (int g = 0; g < gn; ++g) {
           if (!(ok = mbar_wait_warp(afull(ab), aph, aborted, p.err))) break;
           tc_fence_after();
           const uint32_t tb = tb0 + ab * 256;
-          const float sc = slot[g * 128];
+          const float sc = slot[g * C::S_ROW + quad * 32 + lane] * slot[g * C::S_ROW + 128 + col0 / 128];
           float v[2][32];
           tmem_ld32(tb, v[0]);
 #pragma unroll
@@ -633,14 +621,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS,
       // takes them while the next tile is under way; rows that TMA cannot take
       // are written here, four to an instruction.
       const uint32_t stage_addr = sbase + C::OFF_OUT + (warp - 4) * C::OUT_WARP;
+      if (lane == 0) bulk_wait_read_all();     // the last tile's stores have read the boxes
+      __syncwarp();
 #pragma unroll
       for (int c0 = 0; c0 < 128; c0 += 32) {   // half a box of bf16, a box of fp32
-        const int box = es == 2 ? c0 / 64 : c0 / 32 % 2;
-        if (es == 2 ? c0 == 0 : box == 0) {    // the stores that read these boxes before are done with them
-          if (lane == 0) bulk_wait_read_all();
-          __syncwarp();
-        }
-        uint8_t *dst = stage_out + box * 4096;
+        uint8_t *dst = stage_out + (es == 2 ? c0 / 64 : c0 / 32 % 2) * 4096;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {          // four columns
           const float *x = acc + c0 + 4 * q;
@@ -651,18 +636,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS,
             *reinterpret_cast<float4 *>(dst + sw128_offset(lane, q)) = make_float4(x[0], x[1], x[2], x[3]);
           }
         }
-        if (es == 2 && c0 % 64 == 0) continue;
-        const int n = nw + (es == 2 ? c0 - 32 : c0);   // the box's first column
+        if (c0 != 96 && (es == 2 || c0 != 32)) continue;
+        const int n = nw + (es == 2 || c0 == 32 ? 0 : 64), per = 128 / es;   // the first box's first column, a box's columns
         if (p.out_tma) {
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && n < p.n && mw < live) {
-            tma_store_3d(&p.tm_out, stage_addr + box * 4096, n, tile.b, static_cast<int32_t>(mw));
+          if (lane == 0 && mw < live) {
+            if (n < p.n) tma_store_3d(&p.tm_out, stage_addr, n, tile.b, static_cast<int32_t>(mw));
+            if (n + per < p.n) tma_store_3d(&p.tm_out, stage_addr + 4096, n + per, tile.b, static_cast<int32_t>(mw));
             bulk_commit();
+            if (c0 == 32) bulk_wait_read_all();
           }
+          __syncwarp();
         } else {
           __syncwarp();
-          write_box(p, dst, lane, es, mw, live, tile.b, n);
+          write_box(p, stage_out, lane, es, mw, live, tile.b, n);
+          write_box(p, stage_out + 4096, lane, es, mw, live, tile.b, n + per);
           __syncwarp();
         }
       }

@@ -104,16 +104,17 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
-// mbar_wait for a converged warp, the answer uniform, in few registers.  A
-// completed phase costs one try and one vote; the clock is first read after 256
-// failed tries (each try is bounded by the hardware's own limit).
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint32_t abort_flag, int *err) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+// mbar_wait for a converged warp, in few registers, the answer uniform.  The
+// clock is first read after 256 failed tries (each bounded by the hardware's own
+// limit).  Lanes whose first try failed beside others whose succeeded need only
+// try again: the phase is complete and cannot pass on without this warp.
+__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, uint32_t abort_flag, int *err) {
+  const uint32_t lanes = __activemask();
   uint32_t t0 = 0, now, stop = 0;
 #pragma unroll 1
   for (uint32_t i = 1;; ++i) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    if ((i & 255) == 0) {
+    if (__all_sync(lanes, mbar_try_wait(bar, parity))) return true;
+    if ((i & 255) == 0 && lanes == 0xffffffffu) {
       asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
       if (i == 256) t0 = now;
       asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(stop) : "r"(abort_flag) : "memory");
@@ -122,9 +123,15 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, ui
         asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort_flag), "r"(1) : "memory");
         atomicOr(err, kErrTimeout);
       }
-      if (__any_sync(0xffffffffu, stop)) return false;
+      if (__any_sync(lanes, stop)) return false;
     }
   }
+}
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint32_t abort_flag, int *err) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) ok = mbar_wait_slow(bar, parity, abort_flag, err);
+  __syncwarp();
+  return ok;
 }
 
 // ----------------------------------------------------------------- fences
@@ -269,6 +276,10 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
 // 16-byte copy that reads `src_bytes` (0 or 16) bytes and zero-fills the rest.
 __device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void *src, uint32_t src_bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+// 4-byte copy that reads `src_bytes` (0 or 4) bytes and zero-fills the rest.
+__device__ __forceinline__ void cp_async_4_zfill(uint32_t dst, const void *src, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 // Arrive on `bar` once every cp.async this thread issued so far has landed
 // (the arrival counts as this thread's arrival: init the barrier with the
