@@ -374,15 +374,21 @@ struct PairTraits {
   static_assert(128 * REGS_HELP + 32 * EPI * REGS_EPI <= 384 * 168, "registers");
 };
 
-__device__ __forceinline__ ProjectTile pair_tile_at(int t, int m_tiles, int n_tiles) {
+__device__ __forceinline__ ProjectTile pair_tile_at(int t, int m_tiles, int n_tiles, int batch) {
   // groups of 8 token tiles, weights next, tokens within the group fastest:
   // the tiles that run together share both operands in L2
-  const int per_b = m_tiles * n_tiles;
-  const int in_b = t % per_b;
-  const int group = in_b / (8 * n_tiles);
+  // (divisions cost more than anything else between two tiles: one, where
+  // there is one matrix and the group is whole)
+  int b = 0;
+  if (batch > 1) {
+    b = t / (m_tiles * n_tiles);
+    t -= b * (m_tiles * n_tiles);
+  }
+  const int group = t / (8 * n_tiles);
   const int size = min(m_tiles - group * 8, 8);
-  const int in_g = in_b - group * 8 * n_tiles;
-  return {t / per_b, in_g / size * 256, static_cast<int64_t>(group * 8 + in_g % size) * 256};
+  const int in_g = t - group * 8 * n_tiles;
+  const int j = size == 8 ? in_g >> 3 : in_g / size;
+  return {b, j * 256, static_cast<int64_t>(group * 8 + in_g - j * size) * 256};
 }
 
 // 32 rows of 128 bytes of columns from a swizzled box of shared memory to out, by one warp.
@@ -469,7 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS,
       uint32_t ph = 0;
       bool ok = true;
       for (int t = t0; t < tiles && ok; t += t_step) {
-        const ProjectTile tile = pair_tile_at(t, m_tiles, n_tiles);
+        const ProjectTile tile = pair_tile_at(t, m_tiles, n_tiles, p.batch);
         const int m = static_cast<int>(tile.m0) + rank * 128, n = tile.n0 + rank * 128;
         for (int kb = 0; kb < kbs; ++kb) {
           if (!(ok = mbar_wait_warp(empty(st), ph ^ 1, aborted, p.err))) break;
@@ -498,32 +504,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS,
     } else if (warp == 1 && rank == 0) {
       // ---------------------------------------------------------- MMA issuer (first CTA)
       const uint64_t desc0 = smem_desc(sbase, 16, 1024, kSwizzle128);
-      int st = 0, ab = 0;
-      uint32_t ph = 0, aph = 0;
-      bool ok = true;
-      for (int t = t0; t < tiles && ok; t += t_step) {
-        for (int kb = 0; kb < kbs; ++kb) {
-          if (!(ok = mbar_wait_warp(full(st), ph, aborted, p.err) &&
-                      mbar_wait_warp(aempty(ab), aph ^ 1, aborted, p.err)))
-            break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t ad = desc0 + st * (C::STAGE >> 4), wd = ad + (C::A_BYTES >> 4);
+      const uint32_t blocks = static_cast<uint32_t>(t0 < tiles ? (tiles - t0 + t_step - 1) / t_step : 0) * kbs;
+#pragma unroll 1
+      for (uint32_t i = 0; i < blocks; ++i) {   // the k blocks of all this pair's tiles
+        const uint32_t st = i % C::STAGES, ab = i % C::AB;
+        if (!mbar_wait_warp(full(st), i / C::STAGES & 1, aborted, p.err) ||
+            !mbar_wait_warp(aempty(ab), (i / C::AB & 1) ^ 1, aborted, p.err))
+          break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t ad = desc0 + st * (C::STAGE >> 4), wd = ad + (C::A_BYTES >> 4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f8<true>(tmem_base + ab * 256, ad + 2 * k, wd + 2 * k, C::IDESC, k != 0 ? 1u : 0u);
-            mma_commit_pair(empty(st), 3);
-            mma_commit_pair(afull(ab), 3);
-          }
-          __syncwarp();
-          if (++st == C::STAGES) {
-            st = 0;
-            ph ^= 1;
-          }
-          if (++ab == C::AB) {
-            ab = 0;
-            aph ^= 1;
-          }
+          for (int k = 0; k < 4; ++k)   // K = 32 codes (32 bytes) per step
+            mma_f8<true>(tmem_base + ab * 256, ad + 2 * k, wd + 2 * k, C::IDESC, k != 0 ? 1u : 0u);
+          mma_commit_pair(empty(st), 3);
+          mma_commit_pair(afull(ab), 3);
         }
       }
     } else if (warp >= 2) {
@@ -536,7 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS,
       uint32_t sph = 0;
       bool ok = true;
       for (int t = t0; t < tiles && ok; t += t_step) {
-        const ProjectTile tile = pair_tile_at(t, m_tiles, n_tiles);
+        const ProjectTile tile = pair_tile_at(t, m_tiles, n_tiles, p.batch);
         const int m0 = static_cast<int>(tile.m0) + rank * 128;
         for (int kb = 0; kb < kbs; kb += C::GK) {
           if (!(ok = mbar_wait_warp(sempty(sg), sph ^ 1, aborted, p.err))) break;
@@ -613,7 +608,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS,
         }
       }
       if (!ok) break;
-      const ProjectTile tile = pair_tile_at(t, m_tiles, n_tiles);
+      const ProjectTile tile = pair_tile_at(t, m_tiles, n_tiles, p.batch);
       const int64_t mw = tile.m0 + rank * 128 + quad * 32;   // the warp's first token
       const int nw = tile.n0 + col0;                         // and first column
       // out, through shared memory: boxes of 32 rows by 128 bytes of columns,
@@ -627,13 +622,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS,
       for (int c0 = 0; c0 < 128; c0 += 32) {   // half a box of bf16, a box of fp32
         uint8_t *dst = stage_out + (es == 2 ? c0 / 64 : c0 / 32 % 2) * 4096;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {          // four columns
+        for (int q = 0; q < 8; q += 2) {       // eight columns
           const float *x = acc + c0 + 4 * q;
           if (es == 2) {
-            const uint2 u = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-            *reinterpret_cast<uint2 *>(dst + sw128_offset(lane, c0 % 64 / 8 + q / 2) + (q & 1) * 8) = u;
+            *reinterpret_cast<uint4 *>(dst + sw128_offset(lane, c0 % 64 / 8 + q / 2)) =
+                make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
           } else {
             *reinterpret_cast<float4 *>(dst + sw128_offset(lane, q)) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4 *>(dst + sw128_offset(lane, q + 1)) = make_float4(x[4], x[5], x[6], x[7]);
           }
         }
         if (c0 != 96 && (es == 2 || c0 != 32)) continue;
