@@ -49,25 +49,32 @@ struct ProjectParams {
   bool out_tma;   // and every row is live: whole boxes are stored by TMA
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
 template <int NT_>
 struct ProjectTraits {
   static constexpr int NT = NT_;
-  static constexpr int EPI = NT >= 128 ? 8 : 4;             // epilogue warps: 4 per half of the columns
+  // A chunk is KC blocks of k: they arrive on one barrier, are multiplied into
+  // neighbouring tensor-memory columns and handed over together, because each
+  // hand-over costs the issuing warp some 400 cycles however small the block.
+  static constexpr int KC = NT == 16 ? 4 : 2;
+  static constexpr int EPI = NT == 64 ? 8 : 4;   // epilogue warps, a multiple of 4
   static constexpr int THREADS = 128 + 32 * EPI;
   static constexpr int COLS = NT / (EPI / 4);               // columns of an epilogue thread
   static constexpr int W_BYTES = 128 * 128, A_BYTES = NT * 128;
-  static constexpr int STAGE = W_BYTES + A_BYTES;
-  static constexpr int STAGES = NT == 128 ? 6 : NT == 64 ? 8 : 10;
-  static constexpr int AB = 4;                              // tensor-memory buffers
-  static constexpr int TMEM_COLS = AB * NT;
-  static constexpr int GK = NT == 128 ? 8 : 16; // k blocks per scale slot
-  static constexpr int SG = 3;                              // slots
+  static constexpr int BLOCK = W_BYTES + A_BYTES;           // one block of k of a stage: weights, tokens
+  static constexpr int STAGE = KC * BLOCK;
+  static constexpr int STAGES = NT == 64 ? 4 : NT == 32 ? 5 : 3;
+  static constexpr int AB = 4;                              // tensor-memory buffers, each a chunk
+  static constexpr int TMEM_COLS = AB * KC * NT;
+  static constexpr int GK = 16, SG = 3;     // k blocks per scale slot (whole chunks), slots
   static constexpr int S_ROW = NT + 4;                      // floats of a k block's scales (+4: fewer bank conflicts)
   static constexpr int S_SLOT = GK * S_ROW * 4;
   static constexpr int S_VALS = NT * GK / 64;               // values a helper thread brings to a slot
@@ -79,6 +86,7 @@ struct ProjectTraits {
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(NT * 128 * 4 <= STAGES * STAGE, "partial sums reuse the stages");
+  static_assert(GK % KC == 0 && (TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS <= 512, "chunks");
 };
 
 struct ProjectTile {
@@ -96,6 +104,22 @@ __device__ __forceinline__ void store_out(const ProjectParams &p, int64_t m, int
   const int64_t at = m * p.out_stride + b * p.out_batch + n;
   if (p.out_type == DSA_BF16) static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(v);
   else static_cast<float *>(p.out)[at] = v;
+}
+
+// Columns n .. n+3 of one row (n a multiple of 4).
+__device__ __forceinline__ void store4(const ProjectParams &p, int64_t m, int b, int n, float4 v) {
+  const int64_t at = m * p.out_stride + b * p.out_batch + n;
+  if (p.out_vec && n + 4 <= p.n) {
+    if (p.out_type == DSA_BF16)
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+    else
+      *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = v;
+    return;
+  }
+  const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < p.n) store_out(p, m, b, n + i, x[i]);
 }
 
 template <int NT>
@@ -161,15 +185,17 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
     bool ok = true;
     for (int64_t t = t0; t < tiles && ok; t += t_step) {
       const ProjectTile tile = tile_at(t, m_tiles, n_tiles, NT);
-      for (int kb = kb0; kb < kb1; ++kb) {
+      for (int kb = kb0; kb < kb1; kb += C::KC) {
         if (!(ok = mbar_wait_warp(empty(st), ph ^ 1, aborted, p.err))) break;
         if (elect_one()) {
-          mbar_arrive_expect_tx(full(st), C::STAGE);
-          const uint32_t dst = sbase + st * C::STAGE;
-          tma_load_3d(dst, &p.tm_w, kb * 128, tile.n0, tile.b, full(st));
-          tma_load_3d(dst + C::W_BYTES, &p.tm_a, kb * 128, tile.b, static_cast<int32_t>(tile.m0), full(st));
+          const int n = min(C::KC, kb1 - kb);
+          mbar_arrive_expect_tx(full(st), n * C::BLOCK);
+          uint32_t dst = sbase + st * C::STAGE;
+          for (int j = 0; j < n; ++j, dst += C::BLOCK) {
+            tma_load_3d(dst, &p.tm_w, (kb + j) * 128, tile.n0, tile.b, full(st));
+            tma_load_3d(dst + C::W_BYTES, &p.tm_a, (kb + j) * 128, tile.b, static_cast<int32_t>(tile.m0), full(st));
+          }
         }
-        __syncwarp();
         if (++st == C::STAGES) {
           st = 0;
           ph ^= 1;
@@ -179,31 +205,33 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     const uint64_t desc0 = smem_desc(sbase, 16, 1024, kSwizzle128);
-    int st = 0, ab = 0;
-    uint32_t ph = 0, aph = 0;
+    int st = 0;
+    uint32_t ph = 0, i = 0;   // i: chunks so far
     bool ok = true;
     for (int64_t t = t0; t < tiles && ok; t += t_step) {
-      for (int kb = kb0; kb < kb1; ++kb) {
+      for (int kb = kb0; kb < kb1; kb += C::KC, ++i) {
+        const uint32_t ab = i % C::AB;
         if (!(ok = mbar_wait_warp(full(st), ph, aborted, p.err) &&
-                    mbar_wait_warp(aempty(ab), aph ^ 1, aborted, p.err)))
+                   mbar_wait_warp(aempty(ab), (i / C::AB & 1) ^ 1, aborted, p.err)))
           break;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t wd = desc0 + st * (C::STAGE >> 4), ad = wd + (C::W_BYTES >> 4);
+          const uint64_t wd = desc0 + st * (C::STAGE >> 4);
+          const uint32_t d = tmem_base + ab * (C::KC * NT);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)   // K = 32 codes (32 bytes) per step
-            mma_f8<false>(tmem_base + ab * NT, wd + 2 * k, ad + 2 * k, C::IDESC, k != 0 ? 1u : 0u);
+          for (int j = 0; j < C::KC; ++j)
+            if (kb + j < kb1) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)   // K = 32 codes (32 bytes) per step
+                mma_f8<false>(d + j * NT, wd + j * (C::BLOCK >> 4) + 2 * k,
+                              wd + j * (C::BLOCK >> 4) + (C::W_BYTES >> 4) + 2 * k, C::IDESC, k != 0 ? 1u : 0u);
+            }
           mma_commit(empty(st));
           mma_commit(afull(ab));
         }
-        __syncwarp();
         if (++st == C::STAGES) {
           st = 0;
           ph ^= 1;
-        }
-        if (++ab == C::AB) {
-          ab = 0;
-          aph ^= 1;
         }
       }
     }
@@ -250,46 +278,48 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
     const int quad = warp & 3;
     const int col0 = (warp - 4) / 4 * C::COLS;
     const int nl = quad * 32 + lane;   // weight row within the tile
-    int ab = 0, sg = 0;
-    uint32_t aph = 0, sph = 0;
+    int sg = 0;
+    uint32_t sph = 0, i = 0;
     bool ok = true;
     for (int64_t t = t0; t < tiles && ok; t += t_step) {
       const ProjectTile tile = tile_at(t, m_tiles, n_tiles, NT);
       float acc[C::COLS];
 #pragma unroll
       for (int c = 0; c < C::COLS; ++c) acc[c] = 0.f;
+      auto add = [&](const float *v, const float *srow) {
+        const float4 *s4 = reinterpret_cast<const float4 *>(srow);
+#pragma unroll
+        for (int c = 0; c < C::COLS / 4; ++c) {
+          const float4 sc = s4[c];
+          acc[4 * c] = fmaf(v[4 * c], sc.x, acc[4 * c]);
+          acc[4 * c + 1] = fmaf(v[4 * c + 1], sc.y, acc[4 * c + 1]);
+          acc[4 * c + 2] = fmaf(v[4 * c + 2], sc.z, acc[4 * c + 2]);
+          acc[4 * c + 3] = fmaf(v[4 * c + 3], sc.w, acc[4 * c + 3]);
+        }
+      };
+      auto load = [&](uint32_t tb, float *v) {
+        if (C::COLS == 16) tmem_ld16(tb, *reinterpret_cast<float(*)[16]>(v));
+        else tmem_ld32(tb, *reinterpret_cast<float(*)[32]>(v));
+      };
       for (int kb = kb0; kb < kb1 && ok; kb += C::GK) {
         if (!(ok = mbar_wait_warp(sfull(sg), sph, aborted, p.err))) break;
         const float *slot = reinterpret_cast<const float *>(smem + C::OFF_S + sg * C::S_SLOT) + col0;
         const int gn = min(C::GK, kb1 - kb);
-        for (int g = 0; g < gn; ++g) {
-          if (!(ok = mbar_wait_warp(afull(ab), aph, aborted, p.err))) break;
+        for (int g = 0; g < gn; g += C::KC, ++i) {
+          const uint32_t ab = i % C::AB;
+          if (!(ok = mbar_wait_warp(afull(ab), i / C::AB & 1, aborted, p.err))) break;
           tc_fence_after();
-          const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + ab * NT + col0;
-          float v[C::COLS];
-          if (C::COLS >= 32) {
+          const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + ab * (C::KC * NT) + col0;
+          float v[C::KC][C::COLS];
 #pragma unroll
-            for (int c = 0; c < C::COLS; c += 32) tmem_ld32(tb + c, *reinterpret_cast<float(*)[32]>(v + c));
-          } else {
-            tmem_ld16(tb, *reinterpret_cast<float(*)[16]>(v));
-          }
+          for (int j = 0; j < C::KC; ++j) load(tb + j * NT, v[j]);   // (past gn: old sums, not used)
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_relaxed(aempty(ab));   // everything is read: the buffer goes back
-          const float4 *s4 = reinterpret_cast<const float4 *>(slot + g * C::S_ROW);
 #pragma unroll
-          for (int c = 0; c < C::COLS / 4; ++c) {
-            const float4 sc = s4[c];
-            acc[4 * c] = fmaf(v[4 * c], sc.x, acc[4 * c]);
-            acc[4 * c + 1] = fmaf(v[4 * c + 1], sc.y, acc[4 * c + 1]);
-            acc[4 * c + 2] = fmaf(v[4 * c + 2], sc.z, acc[4 * c + 2]);
-            acc[4 * c + 3] = fmaf(v[4 * c + 3], sc.w, acc[4 * c + 3]);
-          }
-          if (++ab == C::AB) {
-            ab = 0;
-            aph ^= 1;
-          }
+          for (int j = 0; j < C::KC; ++j)
+            if (g + j < gn) add(v[j], slot + (g + j) * C::S_ROW);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(sempty(sg));
@@ -324,12 +354,15 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
       const ProjectTile tile = tile_at(t0, m_tiles, n_tiles, NT);
       const int c0 = NT * rank / p.split, c1 = NT * (rank + 1) / p.split;
       const int cols = static_cast<int>(min(static_cast<int64_t>(c1), live - tile.m0)) - c0;
-      for (int i = threadIdx.x; i < cols * 128; i += C::THREADS) {
-        const int c = c0 + i / 128, nl = i % 128;
+      for (int i = threadIdx.x; i < cols * 32; i += C::THREADS) {   // a column, four weight rows
+        const int c = c0 + i / 32, nl = i % 32 * 4;
         const uint32_t at = sbase + static_cast<uint32_t>(c * 128 + nl) * 4;
-        float sum = 0.f;
-        for (int r = 0; r < p.split; ++r) sum += ld_cluster_f32(map_to_cta(at, r));
-        if (tile.n0 + nl < p.n) store_out(p, tile.m0 + c, tile.b, tile.n0 + nl, sum);
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r = 0; r < p.split; ++r) {
+          const float4 v = ld_cluster_v4(map_to_cta(at, r));
+          sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
+        store4(p, tile.m0 + c, tile.b, tile.n0 + nl, sum);
       }
     }
     cluster_sync();   // no CTA leaves while another may read its shared memory
@@ -342,25 +375,33 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: a pair of CTAs (cta_group::2) shares tiles of 256 tokens (the
-// MMA's rows, 128 lanes in each CTA) by 256 weight rows (its columns); each CTA
-// brings half of both, so a block of k costs a CTA 32 KB for 128 x 256 x 128
-// products.  Tokens are the lanes here: an epilogue thread has one token and,
-// its warp being on one half of the columns, one weight block, so s is one
-// number of shared memory per block.  Two
-// tensor-memory buffers of 256 columns fill its 512.
-struct PairTraits {
+// More rows: tokens are the MMA's rows and lanes, weight rows its columns.  An
+// epilogue thread then has one token and, its warp being on one weight block, s
+// is one number per block of k; with weights on the lanes every column's s comes
+// out of shared memory for every lane, which beyond 64 columns costs more of its
+// bandwidth than the operands do.
+//
+//   kPair: a pair of CTAs (cta_group::2) on 256 tokens, 128 lanes in each, by N
+//   weight rows; each CTA brings its tokens and half of the weights, so at N =
+//   256 a block of k costs a CTA 32 KB for 128 x 256 x 128 products.
+//   else: one CTA on 128 tokens by 128 weight rows, and the k split as above.
+template <bool kPair_, int N_>
+struct RowsTraits {
+  static constexpr bool kPair = kPair_;
+  static constexpr int N = N_, M = kPair ? 256 : 128;
   static constexpr int EPI = 8;                             // epilogue warps: 4 per half of the columns
   static constexpr int THREADS = 128 + 32 * EPI;
-  static constexpr int A_BYTES = 128 * 128, W_BYTES = 128 * 128;
+  static constexpr int COLS = N / 2;                        // columns of an epilogue thread
+  static constexpr int W_ROWS = kPair ? N / 2 : N;
+  static constexpr int A_BYTES = 128 * 128, W_BYTES = W_ROWS * 128;
   static constexpr int STAGE = A_BYTES + W_BYTES;
-  static constexpr int STAGES = 4;
-  static constexpr int AB = 2;
+  static constexpr int STAGES = 4;                          // (powers of two, as AB: positions come out of one count)
+  static constexpr int AB = 512 / N;                        // tensor-memory buffers, all its columns
   static constexpr int GK = 16, SG = 3;                     // k blocks per scale slot, slots
-  static constexpr int S_ROW = 136;                         // floats of a k block's scales: 128 tokens, 2 weight blocks
+  static constexpr int S_ROW = 136;                         // floats of a k block's scales: 128 tokens, N / 128 weight blocks
   static constexpr int S_SLOT = GK * S_ROW * 4;
   static constexpr int TMEM_COLS = 512;
-  static constexpr uint32_t IDESC = mma_idesc(256, 256, 0u, false, false);
+  static constexpr uint32_t IDESC = mma_idesc(M, N, 0u, false, false);
   static constexpr int OUT_WARP = 8192;                     // output staging of an epilogue warp: two boxes of 32 rows of 128 bytes
   static constexpr int OFF_OUT = STAGES * STAGE;
   static constexpr int OFF_S = OFF_OUT + EPI * OUT_WARP;
@@ -368,13 +409,14 @@ struct PairTraits {
   static constexpr int NBAR = 2 * STAGES + 2 * AB + 2 * SG;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
-  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static constexpr int PART_ROW = N + 4;                    // floats of a token's partial sums (split): they reuse the stages
+  static_assert(SMEM <= 227 * 1024 && (kPair || 128 * PART_ROW * 4 <= STAGES * STAGE), "shared memory");
   // registers: 384 threads launch with 168 each (64,512); the split keeps that sum
-  static constexpr int REGS_HELP = 56, REGS_EPI = 224;
+  static constexpr int REGS_HELP = N == 256 ? 56 : 64, REGS_EPI = N == 256 ? 224 : 216;
   static_assert(128 * REGS_HELP + 32 * EPI * REGS_EPI <= 384 * 168, "registers");
 };
 
-__device__ __forceinline__ ProjectTile pair_tile_at(int t, int m_tiles, int n_tiles, int batch) {
+__device__ __forceinline__ ProjectTile rows_tile_at(int t, int m_tiles, int n_tiles, int batch, int M, int N) {
   // groups of 8 token tiles, weights next, tokens within the group fastest:
   // the tiles that run together share both operands in L2
   // (divisions cost more than anything else between two tiles: one, where
@@ -388,7 +430,7 @@ __device__ __forceinline__ ProjectTile pair_tile_at(int t, int m_tiles, int n_ti
   const int size = min(m_tiles - group * 8, 8);
   const int in_g = t - group * 8 * n_tiles;
   const int j = size == 8 ? in_g >> 3 : in_g / size;
-  return {b, j * 256, static_cast<int64_t>(group * 8 + in_g - j * size) * 256};
+  return {b, j * N, static_cast<int64_t>(group * 8 + in_g - j * size) * M};
 }
 
 // 32 rows of 128 bytes of columns from a swizzled box of shared memory to out, by one warp.
@@ -412,9 +454,9 @@ __device__ __noinline__ void write_box(const ProjectParams &p, const uint8_t *bo
   }
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS, 1)
-    project_pair_kernel(const __grid_constant__ ProjectParams p) {
-  using C = PairTraits;
+template <bool kPair, int N>
+__global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_constant__ ProjectParams p) {
+  using C = RowsTraits<kPair, N>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -431,13 +473,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS,
 
   const int warp = threadIdx.x / 32;
   const int lane = lane_id();
-  const int rank = static_cast<int>(cluster_rank());
+  // the cluster: a pair, or the CTAs that split a tile's k
+  const int ctas = kPair ? 2 : p.split;
+  const int rank = ctas > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int half = kPair ? rank : 0;   // of the tile's tokens
   const int64_t live = live_rows(p.rows, p.count, p.per_row);
-  const int m_tiles = static_cast<int>((live + 255) / 256);
-  const int n_tiles = (p.n + 255) / 256;
+  const int m_tiles = static_cast<int>((live + C::M - 1) / C::M);
+  const int n_tiles = (p.n + N - 1) / N;
   const int tiles = m_tiles * n_tiles * p.batch;
-  const int t0 = blockIdx.x / 2, t_step = gridDim.x / 2;
+  const int t0 = blockIdx.x / ctas, t_step = gridDim.x / ctas;
   const int kbs = (p.k + 127) / 128;
+  const int kb0 = kPair ? 0 : static_cast<int>(static_cast<int64_t>(kbs) * rank / ctas);
+  const int kb1 = kPair ? kbs : static_cast<int>(static_cast<int64_t>(kbs) * (rank + 1) / ctas);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -446,7 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS,
     }
     for (int b = 0; b < C::AB; ++b) {
       mbar_init(afull(b), 1);
-      mbar_init(aempty(b), 2 * C::EPI);   // both CTAs' epilogue warps, on the first CTA's barrier
+      mbar_init(aempty(b), (kPair ? 2 : 1) * C::EPI);   // a pair's: both CTAs' epilogue warps, on the first CTA's barrier
     }
     for (int g = 0; g < C::SG; ++g) {
       mbar_init(sfull(g), 64);
@@ -458,33 +505,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS,
     tma_prefetch_desc(&p.tm_w);
   }
   if (warp == 1) {
-    tmem_alloc_pair(smem_u32(tmem_slot), C::TMEM_COLS);
-    tmem_relinquish_pair();
+    if (kPair) {
+      tmem_alloc_pair(smem_u32(tmem_slot), C::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
+  if (kPair) cluster_sync();   // the other CTA's barriers are ready
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_HELP));
     if (warp == 0) {
-      // ---------------------------------------------------------- producer (both CTAs)
+      // ---------------------------------------------------------- producer (each CTA)
       int st = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int t = t0; t < tiles && ok; t += t_step) {
-        const ProjectTile tile = pair_tile_at(t, m_tiles, n_tiles, p.batch);
-        const int m = static_cast<int>(tile.m0) + rank * 128, n = tile.n0 + rank * 128;
-        for (int kb = 0; kb < kbs; ++kb) {
+        const ProjectTile tile = rows_tile_at(t, m_tiles, n_tiles, p.batch, C::M, C::N);
+        const int m = static_cast<int>(tile.m0) + half * 128, n = tile.n0 + half * C::W_ROWS;
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!(ok = mbar_wait_warp(empty(st), ph ^ 1, aborted, p.err))) break;
           if (elect_one()) {
-            // the first CTA's barrier counts both CTAs' bytes
-            if (rank == 0) mbar_arrive_expect_tx(full(st), 2 * C::STAGE);
-            const uint32_t dst = sbase + st * C::STAGE, bar = map_to_cta(full(st), 0);
-            tma_load_3d_pair(dst, &p.tm_a, kb * 128, tile.b, m, bar);
-            tma_load_3d_pair(dst + C::A_BYTES, &p.tm_w, kb * 128, n, tile.b, bar);
+            const uint32_t dst = sbase + st * C::STAGE;
+            if (kPair) {   // the first CTA's barrier counts both CTAs' bytes
+              if (rank == 0) mbar_arrive_expect_tx(full(st), 2 * C::STAGE);
+              const uint32_t bar = map_to_cta(full(st), 0);
+              tma_load_3d_pair(dst, &p.tm_a, kb * 128, tile.b, m, bar);
+              tma_load_3d_pair(dst + C::A_BYTES, &p.tm_w, kb * 128, n, tile.b, bar);
+            } else {
+              mbar_arrive_expect_tx(full(st), C::STAGE);
+              tma_load_3d(dst, &p.tm_a, kb * 128, tile.b, m, full(st));
+              tma_load_3d(dst + C::A_BYTES, &p.tm_w, kb * 128, n, tile.b, full(st));
+            }
           }
           __syncwarp();
           if (++st == C::STAGES) {
@@ -494,19 +552,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS,
         }
       }
       // the last commits have arrived here before this CTA may leave
-      for (int i = 0; i < C::STAGES && ok; ++i) {
+      for (int i = 0; kPair && i < C::STAGES && ok; ++i) {
         ok = mbar_wait_warp(empty(st), ph ^ 1, aborted, p.err);
         if (++st == C::STAGES) {
           st = 0;
           ph ^= 1;
         }
       }
-    } else if (warp == 1 && rank == 0) {
-      // ---------------------------------------------------------- MMA issuer (first CTA)
+    } else if (warp == 1 && half == 0) {
+      // ---------------------------------------------------------- MMA issuer (a pair's first CTA)
       const uint64_t desc0 = smem_desc(sbase, 16, 1024, kSwizzle128);
-      const uint32_t blocks = static_cast<uint32_t>(t0 < tiles ? (tiles - t0 + t_step - 1) / t_step : 0) * kbs;
+      const uint32_t blocks = static_cast<uint32_t>(t0 < tiles ? (tiles - t0 + t_step - 1) / t_step : 0) * (kb1 - kb0);
 #pragma unroll 1
-      for (uint32_t i = 0; i < blocks; ++i) {   // the k blocks of all this pair's tiles
+      for (uint32_t i = 0; i < blocks; ++i) {   // the k blocks of all its tiles
         const uint32_t st = i % C::STAGES, ab = i % C::AB;
         if (!mbar_wait_warp(full(st), i / C::STAGES & 1, aborted, p.err) ||
             !mbar_wait_warp(aempty(ab), (i / C::AB & 1) ^ 1, aborted, p.err))
@@ -516,32 +574,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS,
           const uint64_t ad = desc0 + st * (C::STAGE >> 4), wd = ad + (C::A_BYTES >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)   // K = 32 codes (32 bytes) per step
-            mma_f8<true>(tmem_base + ab * 256, ad + 2 * k, wd + 2 * k, C::IDESC, k != 0 ? 1u : 0u);
-          mma_commit_pair(empty(st), 3);
-          mma_commit_pair(afull(ab), 3);
+            mma_f8<kPair>(tmem_base + ab * N, ad + 2 * k, wd + 2 * k, C::IDESC, k != 0 ? 1u : 0u);
+          if (kPair) {
+            mma_commit_pair(empty(st), 3);
+            mma_commit_pair(afull(ab), 3);
+          } else {
+            mma_commit(empty(st));
+            mma_commit(afull(ab));
+          }
         }
       }
     } else if (warp >= 2) {
-      // ---------------------------------------------------------- scales (both CTAs)
+      // ---------------------------------------------------------- scales (each CTA)
       // thread: k block g of a slot and every fourth token, copied without a
-      // register in between; the two weight blocks' scales go beside them
+      // register in between; the weight blocks' scales go beside them
       const int ht = threadIdx.x - 64;
       const int g = ht % C::GK, c0 = ht / C::GK;
       int sg = 0;
       uint32_t sph = 0;
       bool ok = true;
       for (int t = t0; t < tiles && ok; t += t_step) {
-        const ProjectTile tile = pair_tile_at(t, m_tiles, n_tiles, p.batch);
-        const int m0 = static_cast<int>(tile.m0) + rank * 128;
-        for (int kb = 0; kb < kbs; kb += C::GK) {
+        const ProjectTile tile = rows_tile_at(t, m_tiles, n_tiles, p.batch, C::M, C::N);
+        const int m0 = static_cast<int>(tile.m0) + half * 128;
+        for (int kb = kb0; kb < kb1; kb += C::GK) {
           if (!(ok = mbar_wait_warp(sempty(sg), sph ^ 1, aborted, p.err))) break;
           const uint32_t row = sbase + C::OFF_S + sg * C::S_SLOT + g * C::S_ROW * 4;
-          if (kb + g < kbs) {
+          if (kb + g < kb1) {
             const float *as = p.a_scale + tile.b * p.as_batch + kb + g;
 #pragma unroll 4
             for (int c = c0; c < 128; c += 64 / C::GK)
               cp_async_4_zfill(row + c * 4, m0 + c < live ? as + (m0 + c) * p.as_stride : as, m0 + c < live ? 4 : 0);
-            if (c0 < 2) {
+            if (c0 < N / 128) {
               const int n = tile.n0 + c0 * 128;
               const float *ws = p.w_scale + tile.b * p.ws_batch + kb + g;
               cp_async_4_zfill(row + (128 + c0) * 4, n < p.n ? ws + n / 128 * p.ws_stride : ws, n < p.n ? 4 : 0);
@@ -559,7 +622,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS,
     // ------------------------------------------------------------ epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_EPI));
     const int quad = warp & 3;
-    const int col0 = (warp - 4) / 4 * 128;   // the warp's first column of the tile
+    const int col0 = (warp - 4) / 4 * C::COLS;   // the warp's first column of the tile
     const uint32_t tb0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + col0;
     const int es = p.out_type == DSA_BF16 ? 2 : 4;
     uint8_t *stage_out = smem + C::OFF_OUT + (warp - 4) * C::OUT_WARP;
@@ -567,30 +630,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS,
     uint32_t aph = 0, sph = 0;
     bool ok = true;
     for (int t = t0; t < tiles && ok; t += t_step) {
-      float acc[128];
+      float acc[C::COLS];
 #pragma unroll
-      for (int c = 0; c < 128; ++c) acc[c] = 0.f;
-      for (int kb = 0; kb < kbs && ok; kb += C::GK) {
+      for (int c = 0; c < C::COLS; ++c) acc[c] = 0.f;
+      for (int kb = kb0; kb < kb1 && ok; kb += C::GK) {
         if (!(ok = mbar_wait_warp(sfull(sg), sph, aborted, p.err))) break;
         const float *slot = reinterpret_cast<const float *>(smem + C::OFF_S + sg * C::S_SLOT);
-        const int gn = min(C::GK, kbs - kb);
+        const int gn = min(C::GK, kb1 - kb);
 #pragma unroll 1
         for (int g = 0; g < gn; ++g) {
           if (!(ok = mbar_wait_warp(afull(ab), aph, aborted, p.err))) break;
           tc_fence_after();
-          const uint32_t tb = tb0 + ab * 256;
+          const uint32_t tb = tb0 + ab * N;
           const float sc = slot[g * C::S_ROW + quad * 32 + lane] * slot[g * C::S_ROW + 128 + col0 / 128];
           float v[2][32];
           tmem_ld32(tb, v[0]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < C::COLS / 32; ++c) {
             tmem_ld_wait();
-            if (c < 3) {
+            if (c + 1 < C::COLS / 32) {
               tmem_ld32(tb + (c + 1) * 32, v[(c + 1) & 1]);
             } else {   // everything is read: the buffer goes back
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive_remote_relaxed(map_to_cta(aempty(ab), 0));
+              if (lane == 0) {
+                if (kPair) mbar_arrive_remote_relaxed(map_to_cta(aempty(ab), 0));
+                else mbar_arrive_relaxed(aempty(ab));
+              }
             }
 #pragma unroll
             for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(v[c & 1][i], sc, acc[c * 32 + i]);
@@ -608,18 +674,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS,
         }
       }
       if (!ok) break;
-      const ProjectTile tile = pair_tile_at(t, m_tiles, n_tiles, p.batch);
-      const int64_t mw = tile.m0 + rank * 128 + quad * 32;   // the warp's first token
+      const ProjectTile tile = rows_tile_at(t, m_tiles, n_tiles, p.batch, C::M, C::N);
+      const int64_t mw = tile.m0 + half * 128 + quad * 32;   // the warp's first token
       const int nw = tile.n0 + col0;                         // and first column
+      if (!kPair && p.split > 1) {
+        // every MMA has completed (this thread has seen the last block), so
+        // the stages are free for the partial sums: [token][column]
+        float *part = reinterpret_cast<float *>(smem) + (quad * 32 + lane) * C::PART_ROW + col0;
+#pragma unroll
+        for (int c = 0; c < C::COLS; c += 4)
+          *reinterpret_cast<float4 *>(part + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+        break;   // one tile a cluster
+      }
       // out, through shared memory: boxes of 32 rows by 128 bytes of columns,
-      // two at a time (all 128 columns of bf16, half of fp32).  A TMA store
-      // takes them while the next tile is under way; rows that TMA cannot take
-      // are written here, four to an instruction.
+      // at most two at a time.  A TMA store takes them while the next tile is
+      // under way; rows that TMA cannot take are written here, four to an
+      // instruction.
       const uint32_t stage_addr = sbase + C::OFF_OUT + (warp - 4) * C::OUT_WARP;
       if (lane == 0) bulk_wait_read_all();     // the last tile's stores have read the boxes
       __syncwarp();
 #pragma unroll
-      for (int c0 = 0; c0 < 128; c0 += 32) {   // half a box of bf16, a box of fp32
+      for (int c0 = 0; c0 < C::COLS; c0 += 32) {   // half a box of bf16, a box of fp32
         uint8_t *dst = stage_out + (es == 2 ? c0 / 64 : c0 / 32 % 2) * 4096;
 #pragma unroll
         for (int q = 0; q < 8; q += 2) {       // eight columns
@@ -632,22 +707,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS,
             *reinterpret_cast<float4 *>(dst + sw128_offset(lane, q + 1)) = make_float4(x[4], x[5], x[6], x[7]);
           }
         }
-        if (c0 != 96 && (es == 2 || c0 != 32)) continue;
-        const int n = nw + (es == 2 || c0 == 32 ? 0 : 64), per = 128 / es;   // the first box's first column, a box's columns
+        if (es == 2 ? c0 + 32 < C::COLS : c0 % 64 == 0) continue;
+        const int n = es == 2 ? nw : nw + c0 - 32, per = 128 / es;   // the first box's first column, a box's columns
+        const bool two = es == 4 || C::COLS == 128;
         if (p.out_tma) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0 && mw < live) {
             if (n < p.n) tma_store_3d(&p.tm_out, stage_addr, n, tile.b, static_cast<int32_t>(mw));
-            if (n + per < p.n) tma_store_3d(&p.tm_out, stage_addr + 4096, n + per, tile.b, static_cast<int32_t>(mw));
+            if (two && n + per < p.n) tma_store_3d(&p.tm_out, stage_addr + 4096, n + per, tile.b, static_cast<int32_t>(mw));
             bulk_commit();
-            if (c0 == 32) bulk_wait_read_all();
+            if (c0 + 32 < C::COLS) bulk_wait_read_all();   // the boxes are filled once more
           }
           __syncwarp();
         } else {
           __syncwarp();
           write_box(p, stage_out, lane, es, mw, live, tile.b, n);
-          write_box(p, stage_out + 4096, lane, es, mw, live, tile.b, n + per);
+          if (two) write_box(p, stage_out + 4096, lane, es, mw, live, tile.b, n + per);
           __syncwarp();
         }
       }
@@ -655,11 +731,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTraits::THREADS,
     if (lane == 0) bulk_wait_read_all();
   }
 
+  if (ctas > 1) {
+    __syncwarp();
+    cluster_sync();   // no CTA of a pair leaves while the other may signal it or read its operands
+    if (!kPair) {
+      if (t0 < tiles && !*abort_flag) {
+        // rank r adds up every split-th token from r on: a warp a token, a lane four columns
+        const ProjectTile tile = rows_tile_at(t0, m_tiles, n_tiles, p.batch, C::M, C::N);
+        const int rows = static_cast<int>(min(live - tile.m0, static_cast<int64_t>(128)));
+        const int n = tile.n0 + lane * 4;
+        for (int m = rank + ctas * warp; m < rows; m += ctas * (C::THREADS / 32)) {
+          const uint32_t at = sbase + static_cast<uint32_t>(m * C::PART_ROW + lane * 4) * 4;
+          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int r = 0; r < ctas; ++r) {
+            const float4 v = ld_cluster_v4(map_to_cta(at, r));
+            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+          }
+          store4(p, tile.m0 + m, tile.b, n, sum);
+        }
+      }
+      cluster_sync();   // no CTA leaves while another may read its shared memory
+    }
+  }
+
   tc_fence_before();
   __syncthreads();
-  cluster_sync();   // neither CTA leaves while the other may signal it or read its operands
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+  if (warp == 1) {
+    if (kPair) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    else tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
 }
 
 __device__ __forceinline__ float e4m3_value(uint8_t c) {
@@ -718,8 +819,8 @@ __global__ void __launch_bounds__(256) project_simt_kernel(const ProjectParams p
     }
 }
 
-// Tensor maps of both operands; box_a tokens a box of a.
-bool encode_operands(const dsa_project_t &g, ProjectParams &p, uint32_t box_a) {
+// Tensor maps of both operands, box_a tokens and box_w weight rows a box.
+bool encode_operands(const dsa_project_t &g, ProjectParams &p, uint32_t box_a, uint32_t box_w) {
   // a dimension of one element takes any stride
   auto stride = [](int64_t st, int64_t count) { return static_cast<uint64_t>(count > 1 ? st : 16); };
   const uint64_t a_dims[3] = {static_cast<uint64_t>(g.k), static_cast<uint64_t>(g.batch), static_cast<uint64_t>(g.rows)};
@@ -727,19 +828,42 @@ bool encode_operands(const dsa_project_t &g, ProjectParams &p, uint32_t box_a) {
   const uint32_t a_box[3] = {128, 1, box_a};
   const uint64_t w_dims[3] = {static_cast<uint64_t>(g.k), static_cast<uint64_t>(g.n), static_cast<uint64_t>(g.batch)};
   const uint64_t w_strides[2] = {stride(g.w_stride, g.n), stride(g.w_batch, g.batch)};
-  const uint32_t w_box[3] = {128, 128, 1};
+  const uint32_t w_box[3] = {128, box_w, 1};
   return encode_tiled_3d(&p.tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(p.a), a_dims, a_strides, a_box,
                          CU_TENSOR_MAP_SWIZZLE_128B) &&
          encode_tiled_3d(&p.tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(p.w), w_dims, w_strides, w_box,
                          CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-int64_t pair_tiles(const dsa_project_t &g) { return (g.rows + 255) / 256 * ((g.n + 255) / 256) * g.batch; }
+template <typename Kernel>
+cudaError_t launch(const dsa_ctx *ctx, Kernel kern, int threads, int smem, int64_t grid, int cluster,
+                   std::atomic<uint64_t> &smem_limit_set, const ProjectParams &p, cudaStream_t s) {
+  if (cudaError_t e = ensure_smem_limit(kern, smem, ctx->device, smem_limit_set); e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
 
-cudaError_t run_pair(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &p, cudaStream_t s) {
-  using C = PairTraits;
-  if (!encode_operands(g, p, 128)) return cudaErrorInvalidValue;
-  if (p.out_vec && p.count == nullptr) {
+// Tiles of M tokens by N weight rows.
+int64_t tiles_of(const dsa_project_t &g, int M, int N) {
+  return (g.rows + M - 1) / M * ((static_cast<int64_t>(g.n) + N - 1) / N) * g.batch;
+}
+
+template <bool kPair, int N>
+cudaError_t run_rows(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &p, int split, cudaStream_t s) {
+  using C = RowsTraits<kPair, N>;
+  if (!encode_operands(g, p, 128, C::W_ROWS)) return cudaErrorInvalidValue;
+  p.split = split;
+  if (p.out_vec && p.count == nullptr && split == 1) {
     const bool bf16 = g.out_type == DSA_BF16;
     const int64_t es = bf16 ? 2 : 4;
     const uint64_t dims[3] = {static_cast<uint64_t>(g.n), static_cast<uint64_t>(g.batch), static_cast<uint64_t>(g.rows)};
@@ -749,49 +873,34 @@ cudaError_t run_pair(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &
     p.out_tma = encode_tiled_3d(&p.tm_out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
                                 p.out, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
   }
+  const int64_t tiles = tiles_of(g, C::M, N);
+  const int cluster = kPair ? 2 : split;
+  const int64_t grid = split > 1 ? tiles * split : cluster * std::min<int64_t>(tiles, ctx->num_sms / cluster);
   static std::atomic<uint64_t> smem_limit_set{0};
-  if (cudaError_t e = ensure_smem_limit(project_pair_kernel, C::SMEM, ctx->device, smem_limit_set); e != cudaSuccess)
-    return e;
-  const int64_t tiles = pair_tiles(g);
-  const unsigned grid = static_cast<unsigned>(2 * std::min<int64_t>(tiles, ctx->num_sms / 2));
-  project_pair_kernel<<<grid, C::THREADS, C::SMEM, s>>>(p);
-  return cudaGetLastError();
+  return launch(ctx, project_rows_kernel<kPair, N>, C::THREADS, C::SMEM, grid, cluster, smem_limit_set, p, s);
 }
 
 template <int NT>
 cudaError_t run_tc(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &p, int split, cudaStream_t s) {
   using C = ProjectTraits<NT>;
-  if (!encode_operands(g, p, NT)) return cudaErrorInvalidValue;
+  if (!encode_operands(g, p, NT, 128)) return cudaErrorInvalidValue;
   p.split = split;
-  const int64_t tiles = (g.rows + NT - 1) / NT * ((g.n + 127) / 128) * g.batch;
-  auto kern = project_tc_kernel<NT>;
+  const int64_t tiles = tiles_of(g, NT, 128);
+  const int64_t grid = split > 1 ? tiles * split : std::min<int64_t>(tiles, ctx->num_sms);
   static std::atomic<uint64_t> smem_limit_set{0};
-  if (cudaError_t e = ensure_smem_limit(kern, C::SMEM, ctx->device, smem_limit_set); e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(split > 1 ? tiles * split : std::min<int64_t>(tiles, ctx->num_sms)));
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = split;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<const ProjectParams &>(p));
+  return launch(ctx, project_tc_kernel<NT>, C::THREADS, C::SMEM, grid, split, smem_limit_set, p, s);
 }
 
-// Tokens per tile (256: the pair kernel) and CTAs per tile.
+// The kernel (tokens a tile: 16, 32, 64 with weights on the lanes; 128 on one
+// CTA and 256 on a pair with tokens on the lanes, 257 the pair with 256 columns)
+// and the CTAs that split a tile's k.
 void choose(const dsa_ctx *ctx, const dsa_project_t &g, int *nt, int *split) {
-  const int64_t blocks = static_cast<int64_t>((g.n + 127) / 128) * g.batch;
-  auto tiles = [&](int t) { return (g.rows + t - 1) / t * blocks; };
-  *nt = g.rows <= 16 ? 16 : g.rows <= 32 ? 32 : g.rows <= 64 ? 64 : 128;
-  if (g.rows > 128 && tiles(256) >= ctx->num_sms && g.n > 128 && pair_tiles(g) < INT32_MAX / 8) *nt = 256;
-  while (*nt > 64 && *nt < 256 && tiles(*nt / 2) <= ctx->num_sms) *nt /= 2;
   const int kbs = (g.k + 127) / 128;
+  *nt = g.rows <= 16 ? 16 : g.rows <= 32 ? 32 : g.rows <= 64 ? 64 : 128;
+  if (g.rows > 128 && tiles_of(g, 256, 256) * 2 >= 64) *nt = g.n <= 128 ? 256 : 257;
   *split = 1;
   if (*nt < 256)
-    while (*split < 8 && tiles(*nt) * *split * 2 <= ctx->num_sms && kbs >= *split * 2 * 4) *split *= 2;
+    while (*split < 8 && tiles_of(g, *nt, 128) * *split * 2 <= ctx->num_sms && kbs >= *split * 2 * 4) *split *= 2;
 }
 
 }  // namespace
@@ -836,8 +945,9 @@ cudaError_t launch_project_fp8(const dsa_ctx *ctx, const dsa_project_t &g, const
       case 16: return run_tc<16>(ctx, g, p, split, s);
       case 32: return run_tc<32>(ctx, g, p, split, s);
       case 64: return run_tc<64>(ctx, g, p, split, s);
-      case 128: return run_tc<128>(ctx, g, p, split, s);
-      default: return run_pair(ctx, g, p, s);
+      case 128: return run_rows<false, 128>(ctx, g, p, split, s);
+      case 256: return run_rows<true, 128>(ctx, g, p, 1, s);
+      default: return run_rows<true, 256>(ctx, g, p, 1, s);
     }
   }
   const dim3 grid(static_cast<unsigned>((g.rows + 63) / 64), (g.n + 63) / 64, g.batch);
