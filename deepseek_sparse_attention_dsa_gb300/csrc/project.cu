@@ -58,6 +58,20 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
   return v;
 }
 
+// Four floats at one place in each CTA's shared memory, added in rank order; all are asked for first.
+constexpr int kMaxSplit = 8;
+__device__ __forceinline__ float4 sum_cluster(uint32_t at, int ctas) {
+  float4 v[kMaxSplit];
+#pragma unroll
+  for (int r = 0; r < kMaxSplit; ++r)
+    if (r < ctas) v[r] = ld_cluster_v4(map_to_cta(at, r));
+  float4 sum = v[0];
+#pragma unroll
+  for (int r = 1; r < kMaxSplit; ++r)
+    if (r < ctas) sum.x += v[r].x, sum.y += v[r].y, sum.z += v[r].z, sum.w += v[r].w;
+  return sum;
+}
+
 template <int NT_>
 struct ProjectTraits {
   static constexpr int NT = NT_;
@@ -357,12 +371,7 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
       for (int i = threadIdx.x; i < cols * 32; i += C::THREADS) {   // a column, four weight rows
         const int c = c0 + i / 32, nl = i % 32 * 4;
         const uint32_t at = sbase + static_cast<uint32_t>(c * 128 + nl) * 4;
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int r = 0; r < p.split; ++r) {
-          const float4 v = ld_cluster_v4(map_to_cta(at, r));
-          sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-        }
-        store4(p, tile.m0 + c, tile.b, tile.n0 + nl, sum);
+        store4(p, tile.m0 + c, tile.b, tile.n0 + nl, sum_cluster(at, p.split));
       }
     }
     cluster_sync();   // no CTA leaves while another may read its shared memory
@@ -742,12 +751,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
         const int n = tile.n0 + lane * 4;
         for (int m = rank + ctas * warp; m < rows; m += ctas * (C::THREADS / 32)) {
           const uint32_t at = sbase + static_cast<uint32_t>(m * C::PART_ROW + lane * 4) * 4;
-          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int r = 0; r < ctas; ++r) {
-            const float4 v = ld_cluster_v4(map_to_cta(at, r));
-            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-          }
-          store4(p, tile.m0 + m, tile.b, n, sum);
+          store4(p, tile.m0 + m, tile.b, n, sum_cluster(at, ctas));
         }
       }
       cluster_sync();   // no CTA leaves while another may read its shared memory
