@@ -15,9 +15,10 @@
 // them.  Buffers of tensor memory let the tensor core run ahead of that.
 //
 // Few tiles: a cluster of S CTAs shares a tile, each taking a run of its k
-// blocks; every CTA leaves its partial sums in its own shared memory, and after
-// a cluster barrier rank r adds the S partials of its share of the columns in
-// rank order, so results do not depend on timing.
+// blocks.  The tile's tokens are dealt out to the ranks; every CTA sends its
+// partial sums of a token to the token's owner (st.async, counted on the owner's
+// mbarrier), which adds the S of them in rank order, so results do not depend on
+// timing, and no CTA waits for another to finish.
 //
 // Warp roles: 0 TMA producer, 1 MMA issuer and tensor-memory owner, 2-3 scales,
 // 4.. epilogue.
@@ -49,26 +50,21 @@ struct ProjectParams {
   bool out_tma;   // and every row is live: whole boxes are stored by TMA
 };
 
-__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
-// Four floats at one place in each CTA's shared memory, added in rank order; all are asked for first.
 constexpr int kMaxSplit = 8;
-__device__ __forceinline__ float4 sum_cluster(uint32_t at, int ctas) {
+// S partial sums of four values, `stride` bytes apart in this CTA's shared memory, in rank order.
+__device__ __forceinline__ float4 sum_partials(uint32_t at, uint32_t stride, int split) {
   float4 v[kMaxSplit];
 #pragma unroll
   for (int r = 0; r < kMaxSplit; ++r)
-    if (r < ctas) v[r] = ld_cluster_v4(map_to_cta(at, r));
+    if (r < split)
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v[r].x), "=f"(v[r].y), "=f"(v[r].z), "=f"(v[r].w)
+                   : "r"(at + r * stride)
+                   : "memory");
   float4 sum = v[0];
 #pragma unroll
   for (int r = 1; r < kMaxSplit; ++r)
-    if (r < ctas) sum.x += v[r].x, sum.y += v[r].y, sum.z += v[r].z, sum.w += v[r].w;
+    if (r < split) sum.x += v[r].x, sum.y += v[r].y, sum.z += v[r].z, sum.w += v[r].w;
   return sum;
 }
 
@@ -78,14 +74,14 @@ struct ProjectTraits {
   // A chunk is KC blocks of k: they arrive on one barrier, are multiplied into
   // neighbouring tensor-memory columns and handed over together, because each
   // hand-over costs the issuing warp some 400 cycles however small the block.
-  static constexpr int KC = NT == 16 ? 4 : 2;
+  static constexpr int KC = 2;
   static constexpr int EPI = NT == 64 ? 8 : 4;   // epilogue warps, a multiple of 4
   static constexpr int THREADS = 128 + 32 * EPI;
   static constexpr int COLS = NT / (EPI / 4);               // columns of an epilogue thread
   static constexpr int W_BYTES = 128 * 128, A_BYTES = NT * 128;
   static constexpr int BLOCK = W_BYTES + A_BYTES;           // one block of k of a stage: weights, tokens
   static constexpr int STAGE = KC * BLOCK;
-  static constexpr int STAGES = NT == 64 ? 4 : NT == 32 ? 5 : 3;
+  static constexpr int STAGES = NT == 64 ? 3 : 5;
   static constexpr int AB = 4;                              // tensor-memory buffers, each a chunk
   static constexpr int TMEM_COLS = AB * KC * NT;
   static constexpr int GK = 16, SG = 3;     // k blocks per scale slot (whole chunks), slots
@@ -94,12 +90,12 @@ struct ProjectTraits {
   static constexpr int S_VALS = NT * GK / 64;               // values a helper thread brings to a slot
   static constexpr uint32_t IDESC = mma_idesc(128, NT, 0u, false, false);   // kind::f8f6f4: format 0 = e4m3
   static constexpr int OFF_S = STAGES * STAGE;
-  static constexpr int OFF_BAR = OFF_S + SG * S_SLOT;
-  static constexpr int NBAR = 2 * STAGES + 2 * AB + 2 * SG;
+  static constexpr int OFF_PART = OFF_S + SG * S_SLOT;      // partial sums (split): [rank][own token][weight row]
+  static constexpr int OFF_BAR = OFF_PART + NT * 128 * 4;
+  static constexpr int NBAR = 2 * STAGES + 2 * AB + 2 * SG + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
-  static_assert(NT * 128 * 4 <= STAGES * STAGE, "partial sums reuse the stages");
   static_assert(GK % KC == 0 && (TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS <= 512, "chunks");
 };
 
@@ -109,9 +105,10 @@ struct ProjectTile {
 };
 
 // Tiles in order: tokens fastest, so that neighbouring CTAs share weights.
-__device__ __forceinline__ ProjectTile tile_at(int64_t t, int64_t m_tiles, int n_tiles, int NT) {
-  const int64_t rest = t / m_tiles;
-  return {static_cast<int>(rest / n_tiles), static_cast<int>(rest % n_tiles) * 128, (t % m_tiles) * NT};
+__device__ __forceinline__ ProjectTile tile_at(uint32_t t, uint32_t m_tiles, uint32_t n_tiles, int NT) {
+  const uint32_t rest = m_tiles == 1 ? t : t / m_tiles, m = t - rest * m_tiles;
+  const uint32_t b = rest / n_tiles;
+  return {static_cast<int>(b), static_cast<int>(rest - b * n_tiles) * 128, static_cast<int64_t>(m) * NT};
 }
 
 __device__ __forceinline__ void store_out(const ProjectParams &p, int64_t m, int b, int n, float v) {
@@ -149,6 +146,7 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
   auto aempty = [&](int b) { return bar0 + 8u * (2 * C::STAGES + C::AB + b); };
   auto sfull = [&](int g) { return bar0 + 8u * (2 * C::STAGES + 2 * C::AB + g); };
   auto sempty = [&](int g) { return bar0 + 8u * (2 * C::STAGES + 2 * C::AB + C::SG + g); };
+  const uint32_t partfull = bar0 + 8u * (2 * C::STAGES + 2 * C::AB + 2 * C::SG);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
   const uint32_t aborted = sbase + C::OFF_MISC + 4;
@@ -157,15 +155,15 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
   const int lane = lane_id();
   const int rank = p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int64_t live = live_rows(p.rows, p.count, p.per_row);
-  const int64_t m_tiles = (live + NT - 1) / NT;
-  const int n_tiles = (p.n + 127) / 128;
-  const int64_t tiles = m_tiles * n_tiles * p.batch;
-  const int64_t t0 = blockIdx.x / p.split, t_step = gridDim.x / p.split;
+  const uint32_t m_tiles = static_cast<uint32_t>((live + NT - 1) / NT);
+  const uint32_t n_tiles = (p.n + 127) / 128;
+  const uint32_t tiles = m_tiles * n_tiles * p.batch;
+  const uint32_t t0 = blockIdx.x / p.split, t_step = gridDim.x / p.split;
   const int kbs = (p.k + 127) / 128;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(kbs) * rank / p.split);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(kbs) * (rank + 1) / p.split);
+  const int kb0 = kbs / p.split * rank + min(rank, kbs % p.split);   // the first kbs % split ranks have one more
+  const int kb1 = kb0 + kbs / p.split + (rank < kbs % p.split ? 1 : 0);
 
-  if (threadIdx.x == 0) {
+  if (warp == 0 && elect_one()) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
@@ -178,26 +176,33 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
       mbar_init(sfull(g), 64);
       mbar_init(sempty(g), C::EPI);
     }
+    mbar_init(partfull, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&p.tm_a);
-    tma_prefetch_desc(&p.tm_w);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  // the producer starts on the barriers that it has just made; the others wait
+  // for them and for the tensor memory
+  __syncwarp();
+  if (warp == 0) {
+    named_bar_arrive(1, C::THREADS);
+  } else {
+    tc_fence_before();
+    named_bar_sync(1, C::THREADS);
+    tc_fence_after();
+  }
+  if (p.split > 1) cluster_arrive();
+  const uint32_t tmem_base = warp == 0 ? 0 : *tmem_slot;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     int st = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int64_t t = t0; t < tiles && ok; t += t_step) {
+    for (uint32_t t = t0; t < tiles && ok; t += t_step) {
       const ProjectTile tile = tile_at(t, m_tiles, n_tiles, NT);
       for (int kb = kb0; kb < kb1; kb += C::KC) {
         if (!(ok = mbar_wait_warp(empty(st), ph ^ 1, aborted, p.err))) break;
@@ -222,7 +227,7 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
     int st = 0;
     uint32_t ph = 0, i = 0;   // i: chunks so far
     bool ok = true;
-    for (int64_t t = t0; t < tiles && ok; t += t_step) {
+    for (uint32_t t = t0; t < tiles && ok; t += t_step) {
       for (int kb = kb0; kb < kb1; kb += C::KC, ++i) {
         const uint32_t ab = i % C::AB;
         if (!(ok = mbar_wait_warp(full(st), ph, aborted, p.err) &&
@@ -270,7 +275,7 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
     uint32_t sph = 0;
     bool ok = true;
     if (t0 < tiles) load(tile_at(t0, m_tiles, n_tiles, NT), kb0);
-    for (int64_t t = t0; t < tiles && ok; t += t_step) {
+    for (uint32_t t = t0; t < tiles && ok; t += t_step) {
       const ProjectTile tile = tile_at(t, m_tiles, n_tiles, NT);
       for (int kb = kb0; kb < kb1; kb += C::GK) {
         if (!(ok = mbar_wait_warp(sempty(sg), sph ^ 1, aborted, p.err))) break;
@@ -295,7 +300,7 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
     int sg = 0;
     uint32_t sph = 0, i = 0;
     bool ok = true;
-    for (int64_t t = t0; t < tiles && ok; t += t_step) {
+    for (uint32_t t = t0; t < tiles && ok; t += t_step) {
       const ProjectTile tile = tile_at(t, m_tiles, n_tiles, NT);
       float acc[C::COLS];
 #pragma unroll
@@ -343,38 +348,42 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
         }
       }
       if (!ok) break;
-      const int n = tile.n0 + nl;
+      const int cols = static_cast<int>(min(live - tile.m0, static_cast<int64_t>(NT)));   // live tokens
       if (p.split == 1) {
+        const int n = tile.n0 + nl;
         if (n < p.n) {
 #pragma unroll
-          for (int c = 0; c < C::COLS; ++c)
-            if (tile.m0 + col0 + c < live) store_out(p, tile.m0 + col0 + c, tile.b, n, acc[c]);
+          for (int c = 0; c < C::COLS; ++c) {
+            if (col0 + c >= cols) break;
+            store_out(p, tile.m0 + col0 + c, tile.b, n, acc[c]);
+          }
         }
-      } else {
-        // every MMA has completed (this thread has seen the last block), so
-        // the stages are free for the partial sums: [column][weight row]
-        float *part = reinterpret_cast<float *>(smem) + nl;
+        continue;
+      }
+      // token m of the tile belongs to rank m % split, as its token m / split
+      const int split = p.split, sh = 31 - __clz(split), own = NT >> sh;   // (a power of two)
+      const int mine = (cols - rank + split - 1) >> sh;
+      if (warp == 4 && elect_one()) mbar_arrive_expect_tx(partfull, (split - 1) * max(mine, 0) * 512);
+      cluster_wait();   // the others are there
+      const uint32_t part = sbase + C::OFF_PART + (rank * own * 128 + nl) * 4;
 #pragma unroll
-        for (int c = 0; c < C::COLS; ++c) part[(col0 + c) * 128] = acc[c];
+      for (int c = 0; c < C::COLS; ++c) {
+        const int m = col0 + c;
+        if (m >= cols) break;
+        const uint32_t at = part + (m >> sh) * 512;
+        const int to = m & (split - 1);
+        if (to == rank) asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(acc[c]) : "memory");
+        else st_async(map_to_cta(at, to), acc[c], map_to_cta(partfull, to));
       }
-    }
-  }
-
-  if (p.split > 1) {
-    // one tile a cluster (t_step covers them all)
-    __syncwarp();
-    cluster_sync();
-    if (t0 < tiles && !*abort_flag) {
-      const ProjectTile tile = tile_at(t0, m_tiles, n_tiles, NT);
-      const int c0 = NT * rank / p.split, c1 = NT * (rank + 1) / p.split;
-      const int cols = static_cast<int>(min(static_cast<int64_t>(c1), live - tile.m0)) - c0;
-      for (int i = threadIdx.x; i < cols * 32; i += C::THREADS) {   // a column, four weight rows
-        const int c = c0 + i / 32, nl = i % 32 * 4;
-        const uint32_t at = sbase + static_cast<uint32_t>(c * 128 + nl) * 4;
-        store4(p, tile.m0 + c, tile.b, tile.n0 + nl, sum_cluster(at, p.split));
+      named_bar_sync(2, 32 * C::EPI);
+      if (!mbar_wait_warp(partfull, 0, aborted, p.err)) break;
+      for (int i = threadIdx.x - 128; i < mine * 32; i += 32 * C::EPI) {   // a token, four weight rows
+        const int m = i / 32, n4 = i % 32 * 4;
+        const float4 sum = sum_partials(sbase + C::OFF_PART + (m * 128 + n4) * 4, own * 512, split);
+        store4(p, tile.m0 + (m << sh) + rank, tile.b, tile.n0 + n4, sum);
       }
+      break;   // one tile a cluster
     }
-    cluster_sync();   // no CTA leaves while another may read its shared memory
   }
 
   tc_fence_before();
@@ -393,7 +402,7 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
 //   kPair: a pair of CTAs (cta_group::2) on 256 tokens, 128 lanes in each, by N
 //   weight rows; each CTA brings its tokens and half of the weights, so at N =
 //   256 a block of k costs a CTA 32 KB for 128 x 256 x 128 products.
-//   else: one CTA on 128 tokens by 128 weight rows, and the k split as above.
+//   else: one CTA on 128 tokens by 128 weight rows, or two on the halves of k.
 template <bool kPair_, int N_>
 struct RowsTraits {
   static constexpr bool kPair = kPair_;
@@ -415,11 +424,10 @@ struct RowsTraits {
   static constexpr int OFF_OUT = STAGES * STAGE;
   static constexpr int OFF_S = OFF_OUT + EPI * OUT_WARP;
   static constexpr int OFF_BAR = OFF_S + SG * S_SLOT;
-  static constexpr int NBAR = 2 * STAGES + 2 * AB + 2 * SG;
+  static constexpr int NBAR = 2 * STAGES + 2 * AB + 2 * SG + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
-  static constexpr int PART_ROW = N + 4;                    // floats of a token's partial sums (split): they reuse the stages
-  static_assert(SMEM <= 227 * 1024 && (kPair || 128 * PART_ROW * 4 <= STAGES * STAGE), "shared memory");
+  static_assert(SMEM <= 227 * 1024 && (kPair || 32 * COLS * 4 == OUT_WARP), "shared memory");
   // registers: 384 threads launch with 168 each (64,512); the split keeps that sum
   static constexpr int REGS_HELP = N == 256 ? 56 : 64, REGS_EPI = N == 256 ? 224 : 216;
   static_assert(128 * REGS_HELP + 32 * EPI * REGS_EPI <= 384 * 168, "registers");
@@ -476,6 +484,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
   auto aempty = [&](int b) { return bar0 + 8u * (2 * C::STAGES + C::AB + b); };
   auto sfull = [&](int g) { return bar0 + 8u * (2 * C::STAGES + 2 * C::AB + g); };
   auto sempty = [&](int g) { return bar0 + 8u * (2 * C::STAGES + 2 * C::AB + C::SG + g); };
+  const uint32_t partfull = bar0 + 8u * (2 * C::STAGES + 2 * C::AB + 2 * C::SG);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
   const uint32_t aborted = sbase + C::OFF_MISC + 4;
@@ -492,10 +501,10 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
   const int tiles = m_tiles * n_tiles * p.batch;
   const int t0 = blockIdx.x / ctas, t_step = gridDim.x / ctas;
   const int kbs = (p.k + 127) / 128;
-  const int kb0 = kPair ? 0 : static_cast<int>(static_cast<int64_t>(kbs) * rank / ctas);
-  const int kb1 = kPair ? kbs : static_cast<int>(static_cast<int64_t>(kbs) * (rank + 1) / ctas);
+  const int kb0 = kPair ? 0 : kbs / ctas * rank + min(rank, kbs % ctas);   // the first kbs % split ranks have one more
+  const int kb1 = kPair ? kbs : kb0 + kbs / ctas + (rank < kbs % ctas ? 1 : 0);
 
-  if (threadIdx.x == 0) {
+  if (warp == 0 && elect_one()) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
@@ -508,10 +517,10 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
       mbar_init(sfull(g), 64);
       mbar_init(sempty(g), C::EPI);
     }
+    mbar_init(partfull, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&p.tm_a);
-    tma_prefetch_desc(&p.tm_w);
+    if (!kPair && ctas == 2) mbar_arrive_expect_tx(partfull, C::EPI / 2 * C::OUT_WARP);
   }
   if (warp == 1) {
     if (kPair) {
@@ -522,11 +531,25 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
       tmem_relinquish();
     }
   }
-  tc_fence_before();
-  __syncthreads();
-  if (kPair) cluster_sync();   // the other CTA's barriers are ready
-  tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  __syncwarp();
+  if (kPair) {
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // the other CTA's barriers are ready
+    tc_fence_after();
+  } else {
+    // the producer starts on the barriers that it has just made; the others
+    // wait for them and for the tensor memory
+    if (warp == 0) {
+      named_bar_arrive(1, C::THREADS);
+    } else {
+      tc_fence_before();
+      named_bar_sync(1, C::THREADS);
+      tc_fence_after();
+    }
+    if (ctas > 1) cluster_arrive();
+  }
+  const uint32_t tmem_base = !kPair && warp == 0 ? 0 : *tmem_slot;
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_HELP));
@@ -686,20 +709,38 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
       const ProjectTile tile = rows_tile_at(t, m_tiles, n_tiles, p.batch, C::M, C::N);
       const int64_t mw = tile.m0 + half * 128 + quad * 32;   // the warp's first token
       const int nw = tile.n0 + col0;                         // and first column
-      if (!kPair && p.split > 1) {
-        // every MMA has completed (this thread has seen the last block), so
-        // the stages are free for the partial sums: [token][column]
-        float *part = reinterpret_cast<float *>(smem) + (quad * 32 + lane) * C::PART_ROW + col0;
+      const uint32_t stage_addr = sbase + C::OFF_OUT + (warp - 4) * C::OUT_WARP;
+      if (!kPair && ctas == 2) {
+        // two CTAs share the tile (one tile a cluster): rank r finishes tokens
+        // 64 r .. 64 r + 63.  A warp of the other tokens copies its sums into the
+        // same warp's staging in the other CTA, as the 16-byte pieces of each
+        // lane's row in an order that keeps the lanes apart.
+        cluster_wait();   // the other CTA is there
+        if (quad / 2 != rank) {
 #pragma unroll
-        for (int c = 0; c < C::COLS; c += 4)
-          *reinterpret_cast<float4 *>(part + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
-        break;   // one tile a cluster
+          for (int c = 0; c < C::COLS; c += 4)
+            *reinterpret_cast<float4 *>(stage_out + lane * (C::COLS * 4) + (((c / 4) ^ (lane & 7)) << 4)) =
+                make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            bulk_copy_to_cta(map_to_cta(stage_addr, rank ^ 1), stage_addr, C::OUT_WARP, map_to_cta(partfull, rank ^ 1));
+            bulk_commit();
+          }
+          break;
+        }
+        if (!mbar_wait_warp(partfull, 0, aborted, p.err)) break;
+#pragma unroll
+        for (int c = 0; c < C::COLS; c += 4) {
+          const float4 v = *reinterpret_cast<const float4 *>(stage_out + lane * (C::COLS * 4) + (((c / 4) ^ (lane & 7)) << 4));
+          acc[c] += v.x, acc[c + 1] += v.y, acc[c + 2] += v.z, acc[c + 3] += v.w;
+        }
+        __syncwarp();   // the staging is read before it is filled again
       }
       // out, through shared memory: boxes of 32 rows by 128 bytes of columns,
       // at most two at a time.  A TMA store takes them while the next tile is
       // under way; rows that TMA cannot take are written here, four to an
       // instruction.
-      const uint32_t stage_addr = sbase + C::OFF_OUT + (warp - 4) * C::OUT_WARP;
       if (lane == 0) bulk_wait_read_all();     // the last tile's stores have read the boxes
       __syncwarp();
 #pragma unroll
@@ -740,24 +781,10 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
     if (lane == 0) bulk_wait_read_all();
   }
 
-  if (ctas > 1) {
+  if (kPair) {
     __syncwarp();
-    cluster_sync();   // no CTA of a pair leaves while the other may signal it or read its operands
-    if (!kPair) {
-      if (t0 < tiles && !*abort_flag) {
-        // rank r adds up every split-th token from r on: a warp a token, a lane four columns
-        const ProjectTile tile = rows_tile_at(t0, m_tiles, n_tiles, p.batch, C::M, C::N);
-        const int rows = static_cast<int>(min(live - tile.m0, static_cast<int64_t>(128)));
-        const int n = tile.n0 + lane * 4;
-        for (int m = rank + ctas * warp; m < rows; m += ctas * (C::THREADS / 32)) {
-          const uint32_t at = sbase + static_cast<uint32_t>(m * C::PART_ROW + lane * 4) * 4;
-          store4(p, tile.m0 + m, tile.b, n, sum_cluster(at, ctas));
-        }
-      }
-      cluster_sync();   // no CTA leaves while another may read its shared memory
-    }
+    cluster_sync();   // neither CTA leaves while the other may signal it or read its operands
   }
-
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -867,7 +894,7 @@ cudaError_t run_rows(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &
   using C = RowsTraits<kPair, N>;
   if (!encode_operands(g, p, 128, C::W_ROWS)) return cudaErrorInvalidValue;
   p.split = split;
-  if (p.out_vec && p.count == nullptr && split == 1) {
+  if (p.out_vec && p.count == nullptr) {
     const bool bf16 = g.out_type == DSA_BF16;
     const int64_t es = bf16 ? 2 : 4;
     const uint64_t dims[3] = {static_cast<uint64_t>(g.n), static_cast<uint64_t>(g.batch), static_cast<uint64_t>(g.rows)};
@@ -897,14 +924,31 @@ cudaError_t run_tc(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &p,
 
 // The kernel (tokens a tile: 16, 32, 64 with weights on the lanes; 128 on one
 // CTA and 256 on a pair with tokens on the lanes, 257 the pair with 256 columns)
-// and the CTAs that split a tile's k.
+// and the CTAs that split a tile's k: the least of what the measured times of a
+// block of k on each (us, beside others on the card; the pairs' with a share of
+// the tile's end) make of the blocks that the busiest CTA gets.
 void choose(const dsa_ctx *ctx, const dsa_project_t &g, int *nt, int *split) {
+  struct Form {
+    int nt, m, n, ctas, max_split;
+    float block, tile;
+  };
+  static const Form forms[] = {{16, 16, 128, 1, 8, 0.19f, 0.2f},  {32, 32, 128, 1, 8, 0.21f, 0.4f},
+                               {64, 64, 128, 1, 8, 0.26f, 0.7f},  {128, 128, 128, 1, 2, 0.33f, 0.5f},
+                               {256, 256, 128, 2, 1, 0.29f, 0.5f}, {257, 256, 256, 2, 1, 0.40f, 0.9f}};
   const int kbs = (g.k + 127) / 128;
-  *nt = g.rows <= 16 ? 16 : g.rows <= 32 ? 32 : g.rows <= 64 ? 64 : 128;
-  if (g.rows > 128 && tiles_of(g, 256, 256) * 2 >= 64) *nt = g.n <= 128 ? 256 : 257;
-  *split = 1;
-  if (*nt < 256)
-    while (*split < 8 && tiles_of(g, *nt, 128) * *split * 2 <= ctx->num_sms && kbs >= *split * 2 * 4) *split *= 2;
+  float best = 0.f;
+  *nt = 0;
+  for (const Form &f : forms) {
+    if (f.m < 64 && g.rows > 4 * f.m) continue;
+    const int64_t tiles = tiles_of(g, f.m, f.n), cap = ctx->num_sms / f.ctas;
+    if (f.m >= 256 && tiles >= INT32_MAX / 8) continue;   // (32-bit tile counts)
+    for (int s = 1; s <= f.max_split; s *= 2) {
+      if (s > 1 && (tiles * s > cap || kbs < 2 * s)) break;
+      const int64_t per_cta = s > 1 ? 1 : (tiles + cap - 1) / cap;
+      const float t = static_cast<float>(per_cta) * (((kbs + s - 1) / s) * f.block + f.tile) + (s > 1 ? 0.4f : 0.f);
+      if (*nt == 0 || t < best) best = t, *nt = f.nt, *split = s;
+    }
+  }
 }
 
 }  // namespace
