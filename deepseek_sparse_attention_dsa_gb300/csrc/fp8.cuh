@@ -19,15 +19,25 @@ namespace dsa {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// Eight bf16 values of a 16-byte piece: as floats, and the bits of their
+// largest magnitude (as of a float), two at a time.
+__device__ __forceinline__ void unpack8(float (&v)[8], uint4 u) {
+  v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
+  v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
+}
+__device__ __forceinline__ uint32_t amax_bits8(uint4 u) {
+  const uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu),
+                              __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
+  return max(m << 16, m & 0xFFFF0000u);
+}
+
 // Values col .. col+7 of a row (zero at and after `width`).  `vec`: the row
 // starts on 16 bytes, so a whole piece is one or two 16-byte loads.
 __device__ __forceinline__ void load8(float (&v)[8], const void *row, int type, int64_t col, int64_t width, bool vec) {
   if (type == DSA_BF16) {
     const uint16_t *p = static_cast<const uint16_t *>(row) + col;
     if (vec && col + 8 <= width) {
-      const uint4 u = *reinterpret_cast<const uint4 *>(p);
-      v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
-      v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
+      unpack8(v, *reinterpret_cast<const uint4 *>(p));
       return;
     }
 #pragma unroll
@@ -95,11 +105,34 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
+// Values of one group to codes, by two products instead of a division each.
+// r = 1 / scale rounded is off by half a step, so the exact quotient lies
+// between value * lo and value * hi with lo, hi = r * (1 -+ 2^-22): each of
+// those products is at most 3 half steps off the quotient's (1 -+ 2^-22)-fold,
+// that is on its own side of the rounded quotient by a half step at least.
+// Rounding to e4m3 is monotone: where both products have one code it is the
+// quotient's, and where they differ (a quotient within 2^-22 of a border
+// between two codes) the quotient itself decides.
+struct GroupScale {
+  float scale, lo, hi;
+  __device__ __forceinline__ explicit GroupScale(uint32_t amax_bits) {
+    scale = group_scale(amax_bits);
+    const float r = 1.f / scale;
+    lo = r * (1.f - 0x1p-22f);
+    hi = r * (1.f + 0x1p-22f);
+    if (scale < 0x1p-100f) lo = 0.f, hi = __int_as_float(0x7F800000);   // r near fp32's end: always the quotient
+  }
+};
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float r) {
+  return e4m3x2(a * r, b * r) | e4m3x2(c * r, d * r) << 16;
+}
 // Eight values of one group to eight codes.
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float scale) {
-  uint2 c;
-  c.x = e4m3x2(v[0] / scale, v[1] / scale) | e4m3x2(v[2] / scale, v[3] / scale) << 16;
-  c.y = e4m3x2(v[4] / scale, v[5] / scale) | e4m3x2(v[6] / scale, v[7] / scale) << 16;
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], const GroupScale &g) {
+  uint2 c = make_uint2(codes4(v[0], v[1], v[2], v[3], g.lo), codes4(v[4], v[5], v[6], v[7], g.lo));
+  if (c.x != codes4(v[0], v[1], v[2], v[3], g.hi) || c.y != codes4(v[4], v[5], v[6], v[7], g.hi)) {
+    c.x = e4m3x2(v[0] / g.scale, v[1] / g.scale) | e4m3x2(v[2] / g.scale, v[3] / g.scale) << 16;
+    c.y = e4m3x2(v[4] / g.scale, v[5] / g.scale) | e4m3x2(v[6] / g.scale, v[7] / g.scale) << 16;
+  }
   return c;
 }
 

@@ -49,11 +49,49 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const RowsParams p) 
     uint32_t m = amax_bits8(v[c]);
 #pragma unroll
     for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float scale = group_scale(m);
+    const GroupScale g(m);
     const int64_t col = col0 + c * 256;
-    store_codes8(p.codes + row * p.codes_stride, col, width, p.codes_vec, codes8(v[c], scale));
+    store_codes8(p.codes + row * p.codes_stride, col, width, p.codes_vec, codes8(v[c], g));
     if ((lane & 15) == 0 && col < width)
-      reinterpret_cast<float *>(reinterpret_cast<char *>(p.scales) + row * p.scales_stride)[col / 128] = scale;
+      reinterpret_cast<float *>(reinterpret_cast<char *>(p.scales) + row * p.scales_stride)[col / 128] = g.scale;
+  }
+}
+
+// The same for bf16 rows of whole 16-byte pieces on 16 bytes, codes on 8: the
+// pieces wait in their packed form, half the registers.
+__global__ void __launch_bounds__(256) quantize_rows_bf16_kernel(const RowsParams p) {
+  const uint32_t task = blockIdx.x * 8u + threadIdx.x / 32;   // (fewer than 2^32: the grid)
+  const uint32_t segments = static_cast<uint32_t>(p.segments);
+  const uint32_t row = segments >= task + 1 ? 0 : task / segments;
+  if (row >= p.rows) return;
+  int64_t width = p.width;
+  if (p.count) {
+    const int64_t live = static_cast<int64_t>(*p.count) * p.per_row;
+    if (p.dense) width = live < width ? live : width;
+    else if (row >= live) return;
+  }
+  const int lane = threadIdx.x % 32;
+  const int64_t col0 = static_cast<int64_t>(task - row * segments) * (kRowPieces * 256) + lane * 8;
+  const uint4 *x = reinterpret_cast<const uint4 *>(p.x + row * p.x_stride + col0 * 2);
+  const int64_t left = width - col0;   // columns from this lane's first on
+  uint4 u[kRowPieces];
+#pragma unroll
+  for (int c = 0; c < kRowPieces; ++c) u[c] = c * 256 < left ? __ldcs(x + c * 32) : make_uint4(0, 0, 0, 0);
+  uint2 *codes = reinterpret_cast<uint2 *>(p.codes + row * p.codes_stride + col0);
+  float *scales = reinterpret_cast<float *>(reinterpret_cast<char *>(p.scales) + row * p.scales_stride) + col0 / 128;
+#pragma unroll
+  for (int c = 0; c < kRowPieces; ++c) {
+    uint32_t m = amax_bits8(u[c]);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const GroupScale g(m);
+    float v[8];
+    unpack8(v, u[c]);
+    const uint2 code = codes8(v, g);
+    if (c * 256 < left) {
+      codes[c * 32] = code;
+      if ((lane & 15) == 0) scales[c * 2] = g.scale;
+    }
   }
 }
 
@@ -93,16 +131,16 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const BlocksParams
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, part[i]);
-  const float scale = group_scale(m);
+  const GroupScale g(m);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int row = row0 + 16 * i;
     if (row < p.n)
-      store_codes8(p.codes + b * p.codes_batch + row * p.codes_stride, col, p.k, p.codes_vec, codes8(v[i], scale));
+      store_codes8(p.codes + b * p.codes_batch + row * p.codes_stride, col, p.k, p.codes_vec, codes8(v[i], g));
   }
   if (threadIdx.x == 0)
     *reinterpret_cast<float *>(reinterpret_cast<char *>(p.scales) + b * p.scales_batch + blockIdx.y * p.scales_stride +
-                               blockIdx.x * 4) = scale;
+                               blockIdx.x * 4) = g.scale;
 }
 
 }  // namespace
@@ -133,7 +171,11 @@ cudaError_t launch_quantize_rows(const dsa_rows_t &r, const void *x, void *codes
   p.x_vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (one || p.x_stride % 16 == 0);
   p.codes_vec = reinterpret_cast<uintptr_t>(codes) % 8 == 0 && (one || p.codes_stride % 8 == 0);
   p.segments = (p.width + kRowPieces * 256 - 1) / (kRowPieces * 256);
-  quantize_rows_kernel<<<static_cast<unsigned>((p.rows * p.segments + 7) / 8), 256, 0, s>>>(p);
+  const int64_t grid = (p.rows * p.segments + 7) / 8;
+  if (p.x_type == DSA_BF16 && p.x_vec && p.codes_vec && p.width % 8 == 0 && grid < (int64_t(1) << 29))
+    quantize_rows_bf16_kernel<<<static_cast<unsigned>(grid), 256, 0, s>>>(p);
+  else
+    quantize_rows_kernel<<<static_cast<unsigned>(grid), 256, 0, s>>>(p);
   *launches += 1;
   return cudaGetLastError();
 }

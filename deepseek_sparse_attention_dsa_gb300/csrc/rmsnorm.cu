@@ -95,9 +95,9 @@ __global__ void __launch_bounds__(TPR *ROWS) rmsnorm_kernel(const NormParams p) 
       uint32_t m = amax_bits8(h[c]);
 #pragma unroll
       for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));   // the group's 16 lanes
-      const float scale = group_scale(m);
-      store_codes8(row_at(p.codes, row, p.codes_stride), col, p.width, p.codes_vec, codes8(h[c], scale));
-      if ((t & 15) == 0 && col < p.width) row_at(p.scales, row, p.scales_stride)[col / 128] = scale;
+      const GroupScale g(m);
+      store_codes8(row_at(p.codes, row, p.codes_stride), col, p.width, p.codes_vec, codes8(h[c], g));
+      if ((t & 15) == 0 && col < p.width) row_at(p.scales, row, p.scales_stride)[col / 128] = g.scale;
     }
   }
 }
