@@ -815,7 +815,7 @@ dsa_status dsa_rmsnorm(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_norm_t 
       (codes && (!apart(n.width, n.rows, n.codes_stride) || !apart((n.width + 127) / 128, n.rows, n.scales_stride))))
     return DSA_ERR_INVALID_ARG;
   if (!x) return DSA_ERR_INVALID_ARG;
-  return cuda_status(ctx, launch_rmsnorm(n, x, weight, residual, residual_out, out, codes, scales, count, per_row,
+  return cuda_status(ctx, launch_rmsnorm(ctx->num_sms, n, x, weight, residual, residual_out, out, codes, scales, count, per_row,
                                          reinterpret_cast<cudaStream_t>(stream), &ctx->last_launches));
 }
 

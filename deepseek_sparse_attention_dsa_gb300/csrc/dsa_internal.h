@@ -272,7 +272,7 @@ cudaError_t launch_attend(const dsa_ctx *ctx, const dsa_plan_t *plan, const int3
 
 // The 8-bit rows and projections.  count: device row count of a capturable
 // plan (NULL: every row is live), per_row: the call's rows for each of its.
-cudaError_t launch_rmsnorm(const dsa_norm_t &n, const void *x, const void *weight, const void *residual,
+cudaError_t launch_rmsnorm(int num_sms, const dsa_norm_t &n, const void *x, const void *weight, const void *residual,
                            void *residual_out, void *out, void *codes, float *scales, const int32_t *count,
                            int32_t per_row, cudaStream_t s, int32_t *launches);
 cudaError_t launch_quantize_rows(const dsa_rows_t &r, const void *x, void *codes, float *scales, const int32_t *count,

@@ -4,7 +4,8 @@
 //
 // Quantisation, as everywhere in the library: a group's scale is amax / 448 in
 // fp32 (1 where that is zero: an all-zero group, or one below fp32's range), a
-// code is E4M3 of the fp32 quotient by it, rounded to nearest with ties to even.  The maximum is taken over the bit
+// code is E4M3 of the fp32 quotient by it, rounded to nearest with ties to even, NaN
+// being 0x7F and finite values saturating at 448.  The maximum is taken over the bit
 // patterns of the magnitudes, which order as the magnitudes do with NaN above
 // infinity, so a NaN or an infinity always reaches the scale: such a group has
 // the scale NaN or infinity and no finite value comes back out of it.
@@ -97,14 +98,6 @@ __device__ __forceinline__ float group_scale(uint32_t amax_bits) {
   return s == 0.f ? 1.f : s;
 }
 
-// Two quotients to two e4m3 codes (lo in bits 0-7): round to nearest even,
-// finite values saturate at 448, NaN is 0x7F.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // Values of one group to codes, by two products instead of a division each.
 // r = 1 / scale rounded is off by half a step, so the exact quotient lies
 // between value * lo and value * hi with lo, hi = r * (1 -+ 2^-22): each of
@@ -116,22 +109,36 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 struct GroupScale {
   float scale, lo, hi;
   __device__ __forceinline__ explicit GroupScale(uint32_t amax_bits) {
-    scale = group_scale(amax_bits);
-    const float r = 1.f / scale;
+    const float s = group_scale(amax_bits);
+    set(s, 1.f / s);
+  }
+  __device__ __forceinline__ GroupScale(float s, float r) { set(s, r); }   // r = 1 / s, rounded
+  __device__ __forceinline__ void set(float s, float r) {
+    scale = s;
     lo = r * (1.f - 0x1p-22f);
     hi = r * (1.f + 0x1p-22f);
     if (scale < 0x1p-100f) lo = 0.f, hi = __int_as_float(0x7F800000);   // r near fp32's end: always the quotient
   }
 };
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float r) {
-  return e4m3x2(a * r, b * r) | e4m3x2(c * r, d * r) << 16;
+// Four quotients to four codes, the first in bits 0-7.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
 }
 // Eight values of one group to eight codes.
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], const GroupScale &g) {
-  uint2 c = make_uint2(codes4(v[0], v[1], v[2], v[3], g.lo), codes4(v[4], v[5], v[6], v[7], g.lo));
-  if (c.x != codes4(v[0], v[1], v[2], v[3], g.hi) || c.y != codes4(v[4], v[5], v[6], v[7], g.hi)) {
-    c.x = e4m3x2(v[0] / g.scale, v[1] / g.scale) | e4m3x2(v[2] / g.scale, v[3] / g.scale) << 16;
-    c.y = e4m3x2(v[4] / g.scale, v[5] / g.scale) | e4m3x2(v[6] / g.scale, v[7] / g.scale) << 16;
+  uint2 c = make_uint2(e4m3x4(v[0] * g.lo, v[1] * g.lo, v[2] * g.lo, v[3] * g.lo),
+                       e4m3x4(v[4] * g.lo, v[5] * g.lo, v[6] * g.lo, v[7] * g.lo));
+  if (c.x != e4m3x4(v[0] * g.hi, v[1] * g.hi, v[2] * g.hi, v[3] * g.hi) ||
+      c.y != e4m3x4(v[4] * g.hi, v[5] * g.hi, v[6] * g.hi, v[7] * g.hi)) {
+    c.x = e4m3x4(v[0] / g.scale, v[1] / g.scale, v[2] / g.scale, v[3] / g.scale);
+    c.y = e4m3x4(v[4] / g.scale, v[5] / g.scale, v[6] / g.scale, v[7] / g.scale);
   }
   return c;
 }

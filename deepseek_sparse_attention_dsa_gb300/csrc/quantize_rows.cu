@@ -25,7 +25,7 @@ struct RowsParams {
 };
 
 // Pieces of eight columns a lane: a warp's segment of a row is kRowPieces * 256 columns.
-constexpr int kRowPieces = 4;
+constexpr int kRowPieces = 4;   // (four: the scales of a half warp's groups are shared out over four lanes)
 
 // One warp a segment, 16 lanes a group.
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const RowsParams p) {
@@ -79,12 +79,21 @@ __global__ void __launch_bounds__(256) quantize_rows_bf16_kernel(const RowsParam
   for (int c = 0; c < kRowPieces; ++c) u[c] = c * 256 < left ? __ldcs(x + c * 32) : make_uint4(0, 0, 0, 0);
   uint2 *codes = reinterpret_cast<uint2 *>(p.codes + row * p.codes_stride + col0);
   float *scales = reinterpret_cast<float *>(reinterpret_cast<char *>(p.scales) + row * p.scales_stride) + col0 / 128;
+  // A half warp's four groups: their maxima, then both divisions of a group in
+  // one lane of four (every lane would do them otherwise, half of the kernel's
+  // instructions), then the scales back to the lanes
+  uint32_t m[kRowPieces];
 #pragma unroll
   for (int c = 0; c < kRowPieces; ++c) {
-    uint32_t m = amax_bits8(u[c]);
+    m[c] = amax_bits8(u[c]);
 #pragma unroll
-    for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const GroupScale g(m);
+    for (int o = 8; o; o >>= 1) m[c] = max(m[c], __shfl_xor_sync(0xffffffffu, m[c], o));
+  }
+  const float scale = group_scale(lane & 2 ? (lane & 1 ? m[3] : m[2]) : (lane & 1 ? m[1] : m[0]));
+  const float r = 1.f / scale;
+#pragma unroll
+  for (int c = 0; c < kRowPieces; ++c) {
+    const GroupScale g(__shfl_sync(0xffffffffu, scale, c, 16), __shfl_sync(0xffffffffu, r, c, 16));
     float v[8];
     unpack8(v, u[c]);
     const uint2 code = codes8(v, g);
@@ -105,38 +114,48 @@ struct BlocksParams {
   bool w_vec, codes_vec;
 };
 
-// One CTA a block of 128 x 128: 16 threads a row of it, 8 rows a thread.
-__global__ void __launch_bounds__(256) quantize_blocks_kernel(const BlocksParams p) {
+// One CTA a block of 128 x 128: 16 threads a row of it, 4 rows a thread.
+// kPacked: bf16 in whole 16-byte pieces, which wait for the maximum in their
+// packed form; many small CTAs keep enough of them in flight.
+template <bool kPacked>
+__global__ void __launch_bounds__(512, kPacked ? 3 : 2) quantize_blocks_kernel(const BlocksParams p) {
   const int64_t b = blockIdx.z;
   const int col = blockIdx.x * 128 + (threadIdx.x % 16) * 8;
   const int row0 = blockIdx.y * 128 + threadIdx.x / 16;
   const char *w = p.w + b * p.w_batch;
-  float v[8][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = row0 + 16 * i;
-    if (row < p.n) {
-      load8(v[i], w + row * p.w_stride, p.w_type, col, p.k, p.w_vec);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    }
-  }
+  uint4 u[kPacked ? 4 : 1];
+  float v[kPacked ? 1 : 4][8];
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, amax_bits8(v[i]));
+  for (int i = 0; i < 4; ++i) {
+    const int row = row0 + 32 * i;
+    if (kPacked) {
+      u[kPacked ? i : 0] = row < p.n && col < p.k ? __ldcs(reinterpret_cast<const uint4 *>(w + row * p.w_stride + col * 2))
+                                                  : make_uint4(0, 0, 0, 0);
+    } else {
+      if (row < p.n) {
+        load8(v[kPacked ? 0 : i], w + row * p.w_stride, p.w_type, col, p.k, p.w_vec);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[kPacked ? 0 : i][j] = 0.f;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, kPacked ? amax_bits8(u[kPacked ? i : 0]) : amax_bits8(v[kPacked ? 0 : i]));
   m = __reduce_max_sync(0xffffffffu, m);
-  __shared__ uint32_t part[8];
+  __shared__ uint32_t part[16];
   if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = m;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, part[i]);
+  for (int i = 0; i < 16; ++i) m = max(m, part[i]);
   const GroupScale g(m);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = row0 + 16 * i;
-    if (row < p.n)
-      store_codes8(p.codes + b * p.codes_batch + row * p.codes_stride, col, p.k, p.codes_vec, codes8(v[i], g));
+  for (int i = 0; i < 4; ++i) {
+    const int row = row0 + 32 * i;
+    if (kPacked) unpack8(v[0], u[kPacked ? i : 0]);
+    const uint2 c = codes8(v[kPacked ? 0 : i], g);
+    if (row < p.n) store_codes8(p.codes + b * p.codes_batch + row * p.codes_stride, col, p.k, p.codes_vec, c);
   }
   if (threadIdx.x == 0)
     *reinterpret_cast<float *>(reinterpret_cast<char *>(p.scales) + b * p.scales_batch + blockIdx.y * p.scales_stride +
@@ -201,7 +220,8 @@ cudaError_t launch_quantize_weight(const dsa_weight_t &w, const void *src, void 
   p.codes_vec = reinterpret_cast<uintptr_t>(codes) % 8 == 0 && (w.n == 1 || p.codes_stride % 8 == 0) &&
                 (w.batch == 1 || p.codes_batch % 8 == 0);
   const dim3 grid((w.k + 127) / 128, (w.n + 127) / 128, w.batch);
-  quantize_blocks_kernel<<<grid, 256, 0, s>>>(p);
+  if (w.w_type == DSA_BF16 && p.w_vec && w.k % 8 == 0) quantize_blocks_kernel<true><<<grid, 512, 0, s>>>(p);
+  else quantize_blocks_kernel<false><<<grid, 512, 0, s>>>(p);
   *launches += 1;
   return cudaGetLastError();
 }

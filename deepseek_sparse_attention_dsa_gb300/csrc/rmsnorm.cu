@@ -102,6 +102,112 @@ __global__ void __launch_bounds__(TPR *ROWS) rmsnorm_kernel(const NormParams p) 
   }
 }
 
+// The usual types, bf16 throughout in whole 16-byte pieces: a CTA (or a warp, TPR
+// = 32) walks rows with the weights in its registers and the next row's pieces
+// in flight while it norms this one.  CTAs of 1024 threads an SM in all.
+template <int TPR, int CH>
+constexpr int norm_rows() { return TPR == 32 ? 8 : 1; }   // rows a CTA
+
+template <int TPR, int CH, bool kResidual>
+__global__ void __launch_bounds__(TPR *norm_rows<TPR, CH>(), 1024 / (TPR * norm_rows<TPR, CH>()))
+    rmsnorm_bf16_kernel(const NormParams p) {
+  constexpr int ROWS = norm_rows<TPR, CH>();
+  __shared__ float part[2][TPR / 32];
+  const int t = threadIdx.x % TPR;
+  const int64_t live = live_rows(p.rows, p.count, p.per_row);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / TPR;
+  if (row >= live) return;   // uniform over a row's threads
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  bool in[CH];
+  uint4 w[CH], x[CH], r[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) in[c] = (c * TPR + t) * 8 < p.width;
+  auto fetch = [&](int64_t at) {
+    const uint4 *xr = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.x) + at * p.x_stride) + t;
+    const uint4 *rr = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.residual) + at * p.residual_stride) + t;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) x[c] = in[c] ? xr[c * TPR] : zero;
+    if (kResidual)
+#pragma unroll
+      for (int c = 0; c < CH; ++c) r[c] = in[c] ? rr[c * TPR] : zero;
+  };
+  fetch(row);
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+    w[c] = p.weight == nullptr ? make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u)
+           : in[c]             ? static_cast<const uint4 *>(p.weight)[c * TPR + t]
+                               : zero;
+  for (int turn = 0;; turn ^= 1) {
+    float h[CH][8], sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      unpack8(h[c], x[c]);
+      if (kResidual) {
+        float v[8];
+        unpack8(v, r[c]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[c][i] += v[i];
+      }
+    }
+    const int64_t next = row + step;
+    if (next < live) fetch(next);
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fmaf(h[c][i], h[c][i], sum);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (TPR > 32) {
+      // (two buffers: a warp that runs ahead writes the other one, and cannot
+      // come back to this before every warp has passed the next barrier)
+      if (threadIdx.x % 32 == 0) part[turn][threadIdx.x / 32] = sum;
+      __syncthreads();
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < TPR / 32; ++i) sum += part[turn][i];
+    }
+    const float rstd = 1.f / sqrtf(sum / static_cast<float>(p.width) + p.eps);
+    if (kResidual && p.residual_out) {
+      void *ro = row_at(static_cast<char *>(p.residual_out), row, p.residual_out_stride);
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        if (in[c]) store8(ro, DSA_BF16, (c * TPR + t) * 8, p.width, true, h[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = (c * TPR + t) * 8;
+      float wf[8];
+      unpack8(wf, w[c]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[c][i] *= rstd * wf[i];
+      if (p.out && in[c]) store8(row_at(static_cast<char *>(p.out), row, p.out_stride), DSA_BF16, col, p.width, true, h[c]);
+      if (p.codes) {
+        uint32_t m = amax_bits8(h[c]);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));   // the group's 16 lanes
+        const GroupScale g(m);
+        const uint2 code = codes8(h[c], g);
+        if (in[c]) {
+          *reinterpret_cast<uint2 *>(row_at(p.codes, row, p.codes_stride) + col) = code;
+          if ((t & 15) == 0) row_at(p.scales, row, p.scales_stride)[col / 128] = g.scale;
+        }
+      }
+    }
+    if (next >= live) break;
+    row = next;
+  }
+}
+
+template <int TPR, int CH>
+void run_bf16(const NormParams &p, int num_sms, cudaStream_t s) {
+  constexpr int ROWS = norm_rows<TPR, CH>(), THREADS = TPR * ROWS;
+  const int64_t ctas = (p.rows + ROWS - 1) / ROWS, cap = static_cast<int64_t>(num_sms) * (1024 / THREADS);
+  const unsigned grid = static_cast<unsigned>(ctas < cap ? ctas : cap);
+  if (p.residual) rmsnorm_bf16_kernel<TPR, CH, true><<<grid, THREADS, 0, s>>>(p);
+  else rmsnorm_bf16_kernel<TPR, CH, false><<<grid, THREADS, 0, s>>>(p);
+}
+
 bool aligned(const void *p, int64_t stride_bytes, int64_t rows, int bytes) {
   return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (rows <= 1 || stride_bytes % bytes == 0);
 }
@@ -113,7 +219,7 @@ void run(const NormParams &p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_rmsnorm(const dsa_norm_t &n, const void *x, const void *weight, const void *residual,
+cudaError_t launch_rmsnorm(int num_sms, const dsa_norm_t &n, const void *x, const void *weight, const void *residual,
                            void *residual_out, void *out, void *codes, float *scales, const int32_t *count,
                            int32_t per_row, cudaStream_t s, int32_t *launches) {
   auto size = [](int type) { return type == DSA_BF16 ? 2 : 4; };
@@ -147,6 +253,19 @@ cudaError_t launch_rmsnorm(const dsa_norm_t &n, const void *x, const void *weigh
   p.out_vec = aligned(out, p.out_stride, n.rows, 16);
   p.codes_vec = aligned(codes, p.codes_stride, n.rows, 8);
   const int pieces = (n.width + 7) / 8;
+  if (n.width % 8 == 0 && pieces <= 2048 && n.x_type == DSA_BF16 && p.x_vec && (!weight || (n.weight_type == DSA_BF16 && p.weight_vec)) &&
+      (!residual || (n.residual_type == DSA_BF16 && p.residual_vec)) && (!residual_out || p.residual_out_vec) &&
+      (!out || (n.out_type == DSA_BF16 && p.out_vec)) && (!codes || p.codes_vec)) {
+    if (pieces <= 32) run_bf16<32, 1>(p, num_sms, s);
+    else if (pieces <= 64) run_bf16<32, 2>(p, num_sms, s);
+    else if (pieces <= 128) run_bf16<64, 2>(p, num_sms, s);
+    else if (pieces <= 256) run_bf16<128, 2>(p, num_sms, s);
+    else if (pieces <= 512) run_bf16<256, 2>(p, num_sms, s);
+    else if (pieces <= 1024) run_bf16<512, 2>(p, num_sms, s);
+    else run_bf16<1024, 2>(p, num_sms, s);
+    *launches += 1;
+    return cudaGetLastError();
+  }
   if (pieces <= 32) run<32, 8, 1>(p, s);
   else if (pieces <= 64) run<32, 8, 2>(p, s);
   else if (pieces <= 128) run<32, 8, 4>(p, s);
