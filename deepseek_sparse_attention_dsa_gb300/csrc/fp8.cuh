@@ -98,26 +98,21 @@ __device__ __forceinline__ float group_scale(uint32_t amax_bits) {
   return s == 0.f ? 1.f : s;
 }
 
-// Values of one group to codes, by two products instead of a division each.
-// r = 1 / scale rounded is off by half a step, so the exact quotient lies
-// between value * lo and value * hi with lo, hi = r * (1 -+ 2^-22): each of
-// those products is at most 3 half steps off the quotient's (1 -+ 2^-22)-fold,
-// that is on its own side of the rounded quotient by a half step at least.
-// Rounding to e4m3 is monotone: where both products have one code it is the
-// quotient's, and where they differ (a quotient within 2^-22 of a border
-// between two codes) the quotient itself decides.
+// A group's scale and its reciprocal, rounded.  Exact quotients by the scale then
+// take three instructions (Markstein, "Computation of elementary functions on
+// the IBM RISC System/6000 processor", 1990: with r the rounded reciprocal of s,
+// q the rounded product x r and e = x - q s, which a fused multiply-add has
+// exactly, q + e r rounds to the rounded quotient x / s).  They have to be exact:
+// bf16 values over bf16 maxima meet borders between two codes in one value of
+// some 600.  e is exact down to x = 2^-102, and below it the quotient by a scale
+// of 2^-80 or more is far inside code 0; smaller scales take the division.
 struct GroupScale {
-  float scale, lo, hi;
-  __device__ __forceinline__ explicit GroupScale(uint32_t amax_bits) {
-    const float s = group_scale(amax_bits);
-    set(s, 1.f / s);
-  }
-  __device__ __forceinline__ GroupScale(float s, float r) { set(s, r); }   // r = 1 / s, rounded
-  __device__ __forceinline__ void set(float s, float r) {
-    scale = s;
-    lo = r * (1.f - 0x1p-22f);
-    hi = r * (1.f + 0x1p-22f);
-    if (scale < 0x1p-100f) lo = 0.f, hi = __int_as_float(0x7F800000);   // r near fp32's end: always the quotient
+  float scale, r;
+  __device__ __forceinline__ explicit GroupScale(uint32_t amax_bits) : scale(group_scale(amax_bits)), r(1.f / scale) {}
+  __device__ __forceinline__ GroupScale(float s, float reciprocal) : scale(s), r(reciprocal) {}
+  __device__ __forceinline__ float quotient(float x) const {
+    const float q = x * r;
+    return fmaf(fmaf(-q, scale, x), r, q);
   }
 };
 // Four quotients to four codes, the first in bits 0-7.
@@ -133,14 +128,11 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 }
 // Eight values of one group to eight codes.
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], const GroupScale &g) {
-  uint2 c = make_uint2(e4m3x4(v[0] * g.lo, v[1] * g.lo, v[2] * g.lo, v[3] * g.lo),
-                       e4m3x4(v[4] * g.lo, v[5] * g.lo, v[6] * g.lo, v[7] * g.lo));
-  if (c.x != e4m3x4(v[0] * g.hi, v[1] * g.hi, v[2] * g.hi, v[3] * g.hi) ||
-      c.y != e4m3x4(v[4] * g.hi, v[5] * g.hi, v[6] * g.hi, v[7] * g.hi)) {
-    c.x = e4m3x4(v[0] / g.scale, v[1] / g.scale, v[2] / g.scale, v[3] / g.scale);
-    c.y = e4m3x4(v[4] / g.scale, v[5] / g.scale, v[6] / g.scale, v[7] / g.scale);
-  }
-  return c;
+  if (g.scale < 0x1p-80f)
+    return make_uint2(e4m3x4(v[0] / g.scale, v[1] / g.scale, v[2] / g.scale, v[3] / g.scale),
+                      e4m3x4(v[4] / g.scale, v[5] / g.scale, v[6] / g.scale, v[7] / g.scale));
+  return make_uint2(e4m3x4(g.quotient(v[0]), g.quotient(v[1]), g.quotient(v[2]), g.quotient(v[3])),
+                    e4m3x4(g.quotient(v[4]), g.quotient(v[5]), g.quotient(v[6]), g.quotient(v[7])));
 }
 
 // Codes col .. col+7 of a row.  `vec`: the row starts on 8 bytes.

@@ -153,9 +153,17 @@ def test_quantize_rows_boundaries(ctx):
     near = torch.cat([every, mid, mid * (1 + 2.0 ** -22), mid * (1 - 2.0 ** -22), -mid])
     near = torch.cat([near, torch.full((-len(near) % 127,), 0.5)]).view(-1, 127)
     v = torch.cat([torch.full((near.shape[0], 1), 448.0), near], 1)   # each group's maximum is 448: the scale is 1
-    for scale in (1.0, 3.0, 2.0 ** -60, 2.0 ** -126 / 448, 2.0 ** 119):
+    for scale in (1.0, 3.0, 1 + 2.0 ** -23, 2 - 2.0 ** -23, 2.0 ** -60, 1.7 * 2.0 ** -79, 1.3 * 2.0 ** -81, 2.0 ** -126 / 448,
+                  2.0 ** 118 * 1.9):
         x = (v * scale).cuda()
         _exact(*ctx.quantize_rows(x), R.quantize(x, 1))
+    # every bf16 mantissa under every bf16 maximum, where quotients on a border are common
+    m = torch.arange(128, 256).float()
+    v = torch.cat([(m / 256).expand(128, 128) * torch.cat([m.new_full((64,), -1.0), m.new_full((64,), 1.0)]), m[:, None].expand(128, 128) / 128], 1)
+    for shift in (0, 3, -20):
+        x = (v * torch.where(torch.arange(256) % 128 == 7, 1.0, 2.0 ** (shift % 5))).contiguous()
+        x[:, 5] = x[:, 128 + 5] = m / 16
+        _exact(*ctx.quantize_rows(x.to(BF16).cuda()), R.quantize(x.to(BF16), 1))
     # a maximum whose 448th part is below fp32's range: the group counts as zero
     x = torch.zeros(2, 128)
     x[0, 3], x[1, 7] = 2.0 ** -142, -(2.0 ** -149)
