@@ -38,6 +38,7 @@ stream is given.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional, Sequence
 
@@ -88,12 +89,6 @@ class _MsaShape(ctypes.Structure):
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
-_BF16, _FP32 = 0, 1
-_TYPES = {torch.bfloat16: _BF16, torch.float32: _FP32}
-_CODES = {torch.uint8: 0, torch.float8_e4m3fn: 0}
-_SCALES = {torch.float32: 0}
-
-
 class _Norm(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int32), ("x_type", ctypes.c_int32),
                 ("weight_type", ctypes.c_int32), ("residual_type", ctypes.c_int32), ("out_type", ctypes.c_int32),
@@ -133,6 +128,7 @@ class PlanInfo(ctypes.Structure):
 
 
 _lib = None
+_binding = None
 
 
 def library_path() -> str:
@@ -202,6 +198,23 @@ def load() -> ctypes.CDLL:
     return L
 
 
+def _load_binding():
+    """The extension module that passes tensors to the 8-bit calls (csrc/binding.cpp); raises if it has not been built."""
+    global _binding
+    if _binding is None:
+        load()
+        path = os.path.join(os.path.dirname(LIB_PATH), "_dsa_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError("_dsa_binding.so is not built (%s); run "
+                               "`python -m deepseek_sparse_attention_dsa_gb300.build`" % path)
+        spec = importlib.util.spec_from_file_location("_dsa_binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.set_check(lambda status, what, handle: _check(status, what, ctypes.c_void_p(handle)))
+        _binding = module
+    return _binding
+
+
 def _status_str(s: int) -> str:
     try:
         return load().dsa_status_str(int(s)).decode()
@@ -232,15 +245,6 @@ def _ptr(t: Optional[torch.Tensor], device: torch.device, dtypes, name: str):
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     return ctypes.c_void_p(t.data_ptr())
-
-
-def _raw_stream(device_index: int) -> int:
-    """Handle of torch's current stream on a device."""
-    return torch.cuda.current_stream(device_index).cuda_stream
-
-
-if hasattr(torch._C, "_cuda_getCurrentRawStream"):
-    _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _stream(stream) -> ctypes.c_void_p:
@@ -308,6 +312,7 @@ class Context:
         h = ctypes.c_void_p()
         _check(L.dsa_create(ctypes.byref(cfg), int(device), ctypes.byref(h)), "dsa_create")
         self.handle = h
+        self._rows = _load_binding()
         self.shape = shape
         self.device_index = int(device)
         self.device = torch.device("cuda", device) if device >= 0 else torch.device("cpu")
@@ -491,191 +496,56 @@ class Context:
         return selection
 
     # ---------------------------------------------- 8-bit rows and projections
-    # These calls are short enough for the host's part to count: a tensor is
-    # checked in few steps, new outputs not at all, and the stream is asked for
-    # without a Python object around it.
-    def _stream_of(self, stream):
-        if stream is not None:
-            return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        if self.device_index < 0:
-            return None   # a host-only context: the call is refused
-        return _raw_stream(self.device_index)
+    # (their tensors are read and made in csrc/binding.cpp: these calls are short
+    # enough for the host's part to count)
+    @staticmethod
+    def _plan_of(plan):
+        return None if plan is None else plan.handle.value
 
-    def _rows_of(self, t, shape, types, name):
-        """(address, type, stride of the rows) of t, of this shape with adjacent values in a row."""
-        kind = types.get(t.dtype)
-        if kind is None:
-            raise TypeError("%s has dtype %s, expected one of %s" % (name, t.dtype, tuple(types)))
-        if t.get_device() != self.device_index:
-            raise ValueError("%s is on %s, expected %s" % (name, t.device, self.device))
-        if t.shape != shape:
-            raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-        if t.is_contiguous():
-            return t.data_ptr(), kind, shape[-1]
-        st = t.stride()
-        if st[-1] != 1 and shape[-1] > 1:
-            raise ValueError("%s must have adjacent values in its last dimension" % name)
-        return t.data_ptr(), kind, st[0] if len(st) > 1 else 0
-
-    def _norm(self, x, weight, eps, residual, residual_out, out, out_type, codes, scales, plan, stream):
-        """out None: a new one of out_type (where that is not None); codes False: no codes, None: new ones."""
-        shape = x.shape
-        if len(shape) != 2:
-            raise ValueError("x must be (rows, width)")
-        rows, width = shape
-        dev = self.device
-        px, tx, sx = self._rows_of(x, shape, _TYPES, "x")
-        pw = pr = pro = po = pc = ps = None
-        tw = tr = to = sr = sro = so = sc = ss = 0
-        if weight is not None:
-            pw, tw, _ = self._rows_of(weight, (width,), _TYPES, "weight")
-        if residual is not None:
-            pr, tr, sr = self._rows_of(residual, shape, _TYPES, "residual")
-            if residual_out is None:
-                residual_out = torch.empty(shape, dtype=residual.dtype, device=dev)
-                pro, sro = residual_out.data_ptr(), width
-            elif residual_out is residual:
-                pro, sro = pr, sr
-            else:
-                if residual_out.dtype != residual.dtype:
-                    raise TypeError("residual_out has dtype %s, expected the residual's" % residual_out.dtype)
-                pro, _, sro = self._rows_of(residual_out, shape, _TYPES, "residual_out")
-        elif residual_out is not None:
-            raise ValueError("residual_out needs a residual")
-        if out is not None:
-            po, to, so = self._rows_of(out, shape, _TYPES, "out")
-        elif out_type is not None:
-            out = torch.empty(shape, dtype=out_type, device=dev)
-            po, to, so = out.data_ptr(), _TYPES[out_type], width
-        if codes is not False:
-            groups = (width + 127) // 128
-            if codes is None:
-                codes = torch.empty(shape, dtype=torch.uint8, device=dev)
-                pc, sc = codes.data_ptr(), width
-            else:
-                pc, _, sc = self._rows_of(codes, shape, _CODES, "codes")
-            if scales is None:
-                scales = torch.empty((rows, groups), dtype=torch.float32, device=dev)
-                ps, ss = scales.data_ptr(), groups
-            else:
-                ps, _, ss = self._rows_of(scales, (rows, groups), _SCALES, "scales")
-        st = load().dsa_rmsnorm(self.handle, plan.handle if plan is not None else None,
-                                _Norm(rows, width, tx, tw, tr, to, eps, sx, sr, sro, so, sc, ss), px, pw, pr, pro, po,
-                                pc, ps, self._stream_of(stream))
-        if st:
-            _check(st, "dsa_rmsnorm", self.handle)
-        return out, codes, scales, residual_out
+    @staticmethod
+    def _stream_of(stream):
+        return None if stream is None else _stream(stream).value or 0
 
     def rmsnorm(self, x, weight, eps=1e-6, residual=None, residual_out=None, out=None, out_dtype=torch.bfloat16,
                 plan=None, stream=None):
         """dsa_rmsnorm: x (rows, width) bf16 or fp32 -> the normed rows in
         out_dtype; with a residual (added first) -> (out, residual_out)."""
-        out, _, _, h = self._norm(x, weight, eps, residual, residual_out, out, out_dtype, False, None, plan, stream)
-        return out if residual is None else (out, h)
+        return self._rows.rmsnorm(self.handle.value, self.device_index, plan and self._plan_of(plan),
+                                  stream and self._stream_of(stream), x, weight, eps, residual, residual_out, out,
+                                  out_dtype, None, None, False)
 
     def rmsnorm_quantize(self, x, weight, eps=1e-6, residual=None, residual_out=None, out=None, codes=None, scales=None,
                          plan=None, stream=None):
         """dsa_rmsnorm with an 8-bit output: (codes (rows, width) uint8, scales
         (rows, ceil(width / 128)) fp32), and residual_out after them where there
         is a residual.  out, where given, takes the normed rows too."""
-        _, codes, scales, h = self._norm(x, weight, eps, residual, residual_out, out, None, codes, scales, plan, stream)
-        return (codes, scales) if residual is None else (codes, scales, h)
+        return self._rows.rmsnorm(self.handle.value, self.device_index, plan and self._plan_of(plan),
+                                  stream and self._stream_of(stream), x, weight, eps, residual, residual_out, out, None,
+                                  codes, scales, True)
 
     def quantize_rows(self, x, codes=None, scales=None, plan=None, stream=None):
         """dsa_quantize_rows: x (rows, width) bf16 or fp32 -> (codes uint8 of
         the same shape, scales (rows, ceil(width / 128)) fp32)."""
-        shape = x.shape
-        if len(shape) != 2:
-            raise ValueError("x must be (rows, width)")
-        rows, width = shape
-        groups = (width + 127) // 128
-        px, tx, sx = self._rows_of(x, shape, _TYPES, "x")
-        if codes is None:
-            codes = torch.empty(shape, dtype=torch.uint8, device=self.device)
-            pc, sc = codes.data_ptr(), width
-        else:
-            pc, _, sc = self._rows_of(codes, shape, _CODES, "codes")
-        if scales is None:
-            scales = torch.empty((rows, groups), dtype=torch.float32, device=self.device)
-            ps, ss = scales.data_ptr(), groups
-        else:
-            ps, _, ss = self._rows_of(scales, (rows, groups), _SCALES, "scales")
-        st = load().dsa_quantize_rows(self.handle, plan.handle if plan is not None else None,
-                                      _Rows(rows, width, tx, sx, sc, ss), px, pc, ps, self._stream_of(stream))
-        if st:
-            _check(st, "dsa_quantize_rows", self.handle)
-        return codes, scales
+        return self._rows.quantize_rows(self.handle.value, self.device_index, plan and self._plan_of(plan),
+                                        stream and self._stream_of(stream), x, codes, scales)
 
     def quantize_weight(self, w, codes=None, scales=None, stream=None):
         """dsa_quantize_weight: w (n, k) or (batch, n, k) bf16 or fp32 -> (codes
         uint8 of the same shape, scales (..., ceil(n / 128), ceil(k / 128)) fp32)."""
-        shape = tuple(w.shape)
-        if len(shape) not in (2, 3):
-            raise ValueError("w must be (n, k) or (batch, n, k)")
-        n, k = shape[-2:]
-        s_shape = shape[:-2] + ((n + 127) // 128, (k + 127) // 128)
-        if codes is None:
-            codes = torch.empty(shape, dtype=torch.uint8, device=self.device)
-        if scales is None:
-            scales = torch.empty(s_shape, dtype=torch.float32, device=self.device)
-        pw, tw, _ = self._rows_of(w, shape, _TYPES, "w")
-        pc, _, _ = self._rows_of(codes, shape, _CODES, "codes")
-        ps, _, _ = self._rows_of(scales, s_shape, _SCALES, "scales")
-        many = len(shape) == 3
-        g = _Weight(shape[0] if many else 1, n, k, tw, w.stride(-2), w.stride(0) if many else 0,
-                    codes.stride(-2), codes.stride(0) if many else 0, scales.stride(-2), scales.stride(0) if many else 0)
-        _check(load().dsa_quantize_weight(self.handle, g, pw, pc, ps, self._stream_of(stream)), "dsa_quantize_weight",
-               self.handle)
-        return codes, scales
-
-    def _project(self, a, a_scale, w, w_scale, out, out_type):
-        """The call's shape, its addresses (a, a_scale, w, w_scale, out), and out: a new one of out_type for None."""
-        ws, sh = w.shape, a.shape
-        if len(ws) == 2 and len(sh) == 2:
-            n, k = ws
-            rows = sh[0]
-            kb = (k + 127) // 128
-            pa, _, sa = self._rows_of(a, (rows, k), _CODES, "a")
-            pas, _, sas = self._rows_of(a_scale, (rows, kb), _SCALES, "a_scale")
-            pw, _, sw = self._rows_of(w, ws, _CODES, "w")
-            pws, _, sws = self._rows_of(w_scale, ((n + 127) // 128, kb), _SCALES, "w_scale")
-            if out is None:
-                out = torch.empty((rows, n), dtype=out_type, device=self.device)
-                po, to, so = out.data_ptr(), _TYPES[out_type], n
-            else:
-                po, to, so = self._rows_of(out, (rows, n), _TYPES, "out")
-            return _Project(rows, 1, n, k, to, sa, 0, sas, 0, sw, 0, sws, 0, so, 0), (pa, pas, pw, pws, po), out
-        if len(ws) != 3 or len(sh) != 3:
-            raise ValueError("a (rows, k) goes with w (n, k), a (rows, batch, k) with w (batch, n, k)")
-        b, n, k = ws
-        rows = sh[0]
-        kb = (k + 127) // 128
-        if out is None:
-            out = torch.empty((rows, b, n), dtype=out_type, device=self.device)
-        ptrs = (self._rows_of(a, (rows, b, k), _CODES, "a")[0],
-                self._rows_of(a_scale, (rows, b, kb), _SCALES, "a_scale")[0],
-                self._rows_of(w, ws, _CODES, "w")[0],
-                self._rows_of(w_scale, (b, (n + 127) // 128, kb), _SCALES, "w_scale")[0])
-        po, to, _ = self._rows_of(out, (rows, b, n), _TYPES, "out")
-        (a0, a1, _), (as0, as1, _), (w0, w1, _) = a.stride(), a_scale.stride(), w.stride()
-        (ws0, ws1, _), (o0, o1, _) = w_scale.stride(), out.stride()
-        return _Project(rows, b, n, k, to, a0, a1, as0, as1, w1, w0, ws1, ws0, o0, o1), ptrs + (po,), out
+        return self._rows.quantize_weight(self.handle.value, self.device_index, None, stream and self._stream_of(stream),
+                                          w, codes, scales)
 
     def project_fp8(self, a, a_scale, w, w_scale, out=None, out_dtype=torch.bfloat16, plan=None, stream=None):
         """dsa_project_fp8: codes a (rows, k) with scales (rows, ceil(k / 128))
         times w (n, k) with scales per 128 x 128 block -> (rows, n) in
         out_dtype; or for each b, a (rows, batch, k) times w (batch, n, k) ->
         (rows, batch, n).  Codes are uint8 or float8_e4m3fn."""
-        g, (pa, pas, pw, pws, po), out = self._project(a, a_scale, w, w_scale, out, out_dtype)
-        st = load().dsa_project_fp8(self.handle, plan.handle if plan is not None else None, g, pa, pas, pw, pws, po,
-                                    self._stream_of(stream))
-        if st:
-            _check(st, "dsa_project_fp8", self.handle)
-        return out
+        return self._rows.project_fp8(self.handle.value, self.device_index, plan and self._plan_of(plan),
+                                      stream and self._stream_of(stream), a, a_scale, w, w_scale, out, out_dtype, False)
 
     def project_on_tensor_cores(self, a, a_scale, w, w_scale, out) -> bool:
-        g, (pa, _, pw, _, _), _ = self._project(a, a_scale, w, w_scale, out, None)
-        return bool(load().dsa_project_on_tensor_cores(g, pa, pw))
+        """Whether project_fp8 runs this call on the tensor cores."""
+        return self._rows.project_fp8(self.handle.value, self.device_index, None, 0, a, a_scale, w, w_scale, out, None, True)
 
     def index_scores(self, plan: Plan, q, w, index_cache, scores=None, stream=None) -> torch.Tensor:
         d = self.device
