@@ -112,6 +112,27 @@ __host__ __device__ inline int64_t index_cta_of_tile(int64_t t, int64_t total, i
   return t * cap / total;
 }
 
+// Launches a kernel that begins with grid_dependency() (fp8.cuh): it may be set
+// up while the stream's previous kernel still runs.  cluster: CTAs a cluster.
+template <typename Params>
+cudaError_t launch_overlapped(void (*kern)(Params), dim3 grid, int threads, int smem, int cluster, cudaStream_t s,
+                              const Params &p) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
 // Order-preserving 32-bit key of a score (larger score, larger key; -0.0
 // ranks as +0.0).  Every score, -inf included, has a key above 0, so 0 can
 // stand for "no score".

@@ -17,6 +17,18 @@
 
 namespace dsa {
 
+// The kernels of these operators are short, so the next one's launch and set-up
+// weigh: each lets its successor be launched at once and waits, before it touches
+// global memory, until its predecessor is complete and its writes are visible.
+// Every CTA waits (also one without work: a kernel that ended before its
+// predecessor would let its successor run beside that).
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency() {
+  launch_dependents();
+  grid_dependency_wait();
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 

@@ -154,15 +154,11 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
   const int warp = threadIdx.x / 32;
   const int lane = lane_id();
   const int rank = p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int64_t live = live_rows(p.rows, p.count, p.per_row);
-  const uint32_t m_tiles = static_cast<uint32_t>((live + NT - 1) / NT);
-  const uint32_t n_tiles = (p.n + 127) / 128;
-  const uint32_t tiles = m_tiles * n_tiles * p.batch;
-  const uint32_t t0 = blockIdx.x / p.split, t_step = gridDim.x / p.split;
   const int kbs = (p.k + 127) / 128;
   const int kb0 = kbs / p.split * rank + min(rank, kbs % p.split);   // the first kbs % split ranks have one more
   const int kb1 = kb0 + kbs / p.split + (rank < kbs % p.split ? 1 : 0);
 
+  launch_dependents();
   if (warp == 0 && elect_one()) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(full(s), 1);
@@ -195,6 +191,12 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
     tc_fence_after();
   }
   if (p.split > 1) cluster_arrive();
+  grid_dependency_wait();
+  const int64_t live = live_rows(p.rows, p.count, p.per_row);
+  const uint32_t m_tiles = static_cast<uint32_t>((live + NT - 1) / NT);
+  const uint32_t n_tiles = (p.n + 127) / 128;
+  const uint32_t tiles = m_tiles * n_tiles * p.batch;
+  const uint32_t t0 = blockIdx.x / p.split, t_step = gridDim.x / p.split;
   const uint32_t tmem_base = warp == 0 ? 0 : *tmem_slot;
 
   if (warp == 0) {
@@ -495,15 +497,11 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
   const int ctas = kPair ? 2 : p.split;
   const int rank = ctas > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int half = kPair ? rank : 0;   // of the tile's tokens
-  const int64_t live = live_rows(p.rows, p.count, p.per_row);
-  const int m_tiles = static_cast<int>((live + C::M - 1) / C::M);
-  const int n_tiles = (p.n + N - 1) / N;
-  const int tiles = m_tiles * n_tiles * p.batch;
-  const int t0 = blockIdx.x / ctas, t_step = gridDim.x / ctas;
   const int kbs = (p.k + 127) / 128;
   const int kb0 = kPair ? 0 : kbs / ctas * rank + min(rank, kbs % ctas);   // the first kbs % split ranks have one more
   const int kb1 = kPair ? kbs : kb0 + kbs / ctas + (rank < kbs % ctas ? 1 : 0);
 
+  launch_dependents();
   if (warp == 0 && elect_one()) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(full(s), 1);
@@ -549,6 +547,12 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
     }
     if (ctas > 1) cluster_arrive();
   }
+  grid_dependency_wait();
+  const int64_t live = live_rows(p.rows, p.count, p.per_row);
+  const int m_tiles = static_cast<int>((live + C::M - 1) / C::M);
+  const int n_tiles = (p.n + N - 1) / N;
+  const int tiles = m_tiles * n_tiles * p.batch;
+  const int t0 = blockIdx.x / ctas, t_step = gridDim.x / ctas;
   const uint32_t tmem_base = !kPair && warp == 0 ? 0 : *tmem_slot;
 
   if (warp < 4) {
@@ -801,6 +805,7 @@ __device__ __forceinline__ float e4m3_value(uint8_t c) {
 // CUDA-core form, for codes that are not on 16 bytes: 64 x 64 outputs a CTA, 4 x 4 a thread.
 __global__ void __launch_bounds__(256) project_simt_kernel(const ProjectParams p) {
   __shared__ float as[32][65], ws[32][65];
+  grid_dependency();
   const int64_t live = live_rows(p.rows, p.count, p.per_row);
   const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 64;
   if (m0 >= live) return;
@@ -866,22 +871,10 @@ bool encode_operands(const dsa_project_t &g, ProjectParams &p, uint32_t box_a, u
                          CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <typename Kernel>
-cudaError_t launch(const dsa_ctx *ctx, Kernel kern, int threads, int smem, int64_t grid, int cluster,
+cudaError_t launch(const dsa_ctx *ctx, void (*kern)(ProjectParams), int threads, int smem, int64_t grid, int cluster,
                    std::atomic<uint64_t> &smem_limit_set, const ProjectParams &p, cudaStream_t s) {
   if (cudaError_t e = ensure_smem_limit(kern, smem, ctx->device, smem_limit_set); e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  return launch_overlapped(kern, dim3(static_cast<unsigned>(grid)), threads, smem, cluster, s, p);
 }
 
 // Tiles of M tokens by N weight rows.
@@ -999,9 +992,8 @@ cudaError_t launch_project_fp8(const dsa_ctx *ctx, const dsa_project_t &g, const
     }
   }
   const dim3 grid(static_cast<unsigned>((g.rows + 63) / 64), (g.n + 63) / 64, g.batch);
-  project_simt_kernel<<<grid, 256, 0, s>>>(p);
   *launches += 1;
-  return cudaGetLastError();
+  return launch_overlapped(project_simt_kernel, grid, 256, 0, 1, s, p);
 }
 
 }  // namespace dsa

@@ -29,6 +29,7 @@ constexpr int kRowPieces = 4;   // (four: the scales of a half warp's groups are
 
 // One warp a segment, 16 lanes a group.
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const RowsParams p) {
+  grid_dependency();
   const int64_t task = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
   const int64_t row = task / p.segments;
   if (row >= p.rows) return;
@@ -60,6 +61,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const RowsParams p) 
 // The same for bf16 rows of whole 16-byte pieces on 16 bytes, codes on 8: the
 // pieces wait in their packed form, half the registers.
 __global__ void __launch_bounds__(256) quantize_rows_bf16_kernel(const RowsParams p) {
+  grid_dependency();
   const uint32_t task = blockIdx.x * 8u + threadIdx.x / 32;   // (fewer than 2^32: the grid)
   const uint32_t segments = static_cast<uint32_t>(p.segments);
   const uint32_t row = segments >= task + 1 ? 0 : task / segments;
@@ -119,6 +121,7 @@ struct BlocksParams {
 // packed form; many small CTAs keep enough of them in flight.
 template <bool kPacked>
 __global__ void __launch_bounds__(512, kPacked ? 3 : 2) quantize_blocks_kernel(const BlocksParams p) {
+  grid_dependency();
   const int64_t b = blockIdx.z;
   const int col = blockIdx.x * 128 + (threadIdx.x % 16) * 8;
   const int row0 = blockIdx.y * 128 + threadIdx.x / 16;
@@ -191,12 +194,10 @@ cudaError_t launch_quantize_rows(const dsa_rows_t &r, const void *x, void *codes
   p.codes_vec = reinterpret_cast<uintptr_t>(codes) % 8 == 0 && (one || p.codes_stride % 8 == 0);
   p.segments = (p.width + kRowPieces * 256 - 1) / (kRowPieces * 256);
   const int64_t grid = (p.rows * p.segments + 7) / 8;
-  if (p.x_type == DSA_BF16 && p.x_vec && p.codes_vec && p.width % 8 == 0 && grid < (int64_t(1) << 29))
-    quantize_rows_bf16_kernel<<<static_cast<unsigned>(grid), 256, 0, s>>>(p);
-  else
-    quantize_rows_kernel<<<static_cast<unsigned>(grid), 256, 0, s>>>(p);
+  const bool packed = p.x_type == DSA_BF16 && p.x_vec && p.codes_vec && p.width % 8 == 0 && grid < (int64_t(1) << 29);
   *launches += 1;
-  return cudaGetLastError();
+  return launch_overlapped(packed ? quantize_rows_bf16_kernel : quantize_rows_kernel, dim3(static_cast<unsigned>(grid)), 256,
+                           0, 1, s, p);
 }
 
 cudaError_t launch_quantize_weight(const dsa_weight_t &w, const void *src, void *codes, float *scales, cudaStream_t s,
@@ -220,10 +221,9 @@ cudaError_t launch_quantize_weight(const dsa_weight_t &w, const void *src, void 
   p.codes_vec = reinterpret_cast<uintptr_t>(codes) % 8 == 0 && (w.n == 1 || p.codes_stride % 8 == 0) &&
                 (w.batch == 1 || p.codes_batch % 8 == 0);
   const dim3 grid((w.k + 127) / 128, (w.n + 127) / 128, w.batch);
-  if (w.w_type == DSA_BF16 && p.w_vec && w.k % 8 == 0) quantize_blocks_kernel<true><<<grid, 512, 0, s>>>(p);
-  else quantize_blocks_kernel<false><<<grid, 512, 0, s>>>(p);
+  const bool packed = w.w_type == DSA_BF16 && p.w_vec && w.k % 8 == 0;
   *launches += 1;
-  return cudaGetLastError();
+  return launch_overlapped(packed ? quantize_blocks_kernel<true> : quantize_blocks_kernel<false>, grid, 512, 0, 1, s, p);
 }
 
 }  // namespace dsa

@@ -40,6 +40,7 @@ __device__ __forceinline__ T *row_at(T *base, int64_t row, int64_t stride) {
 // TPR threads a row (32: a warp), ROWS rows a CTA.
 template <int TPR, int ROWS, int CH>
 __global__ void __launch_bounds__(TPR *ROWS) rmsnorm_kernel(const NormParams p) {
+  grid_dependency();
   const int t = threadIdx.x % TPR;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / TPR;
   if (row >= live_rows(p.rows, p.count, p.per_row)) return;   // uniform over a row's threads
@@ -113,6 +114,7 @@ __global__ void __launch_bounds__(TPR *norm_rows<TPR, CH>(), 1024 / (TPR * norm_
     rmsnorm_bf16_kernel(const NormParams p) {
   constexpr int ROWS = norm_rows<TPR, CH>();
   __shared__ float part[2][TPR / 32];
+  grid_dependency();
   const int t = threadIdx.x % TPR;
   const int64_t live = live_rows(p.rows, p.count, p.per_row);
   const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS;
@@ -200,12 +202,12 @@ __global__ void __launch_bounds__(TPR *norm_rows<TPR, CH>(), 1024 / (TPR * norm_
 }
 
 template <int TPR, int CH>
-void run_bf16(const NormParams &p, int num_sms, cudaStream_t s) {
+cudaError_t run_bf16(const NormParams &p, int num_sms, cudaStream_t s) {
   constexpr int ROWS = norm_rows<TPR, CH>(), THREADS = TPR * ROWS;
   const int64_t ctas = (p.rows + ROWS - 1) / ROWS, cap = static_cast<int64_t>(num_sms) * (1024 / THREADS);
   const unsigned grid = static_cast<unsigned>(ctas < cap ? ctas : cap);
-  if (p.residual) rmsnorm_bf16_kernel<TPR, CH, true><<<grid, THREADS, 0, s>>>(p);
-  else rmsnorm_bf16_kernel<TPR, CH, false><<<grid, THREADS, 0, s>>>(p);
+  return launch_overlapped(p.residual ? rmsnorm_bf16_kernel<TPR, CH, true> : rmsnorm_bf16_kernel<TPR, CH, false>, dim3(grid),
+                           THREADS, 0, 1, s, p);
 }
 
 bool aligned(const void *p, int64_t stride_bytes, int64_t rows, int bytes) {
@@ -213,8 +215,9 @@ bool aligned(const void *p, int64_t stride_bytes, int64_t rows, int bytes) {
 }
 
 template <int TPR, int ROWS, int CH>
-void run(const NormParams &p, cudaStream_t s) {
-  rmsnorm_kernel<TPR, ROWS, CH><<<static_cast<unsigned>((p.rows + ROWS - 1) / ROWS), TPR * ROWS, 0, s>>>(p);
+cudaError_t run(const NormParams &p, cudaStream_t s) {
+  return launch_overlapped(rmsnorm_kernel<TPR, ROWS, CH>, dim3(static_cast<unsigned>((p.rows + ROWS - 1) / ROWS)), TPR * ROWS,
+                           0, 1, s, p);
 }
 
 }  // namespace
@@ -256,26 +259,24 @@ cudaError_t launch_rmsnorm(int num_sms, const dsa_norm_t &n, const void *x, cons
   if (n.width % 8 == 0 && pieces <= 2048 && n.x_type == DSA_BF16 && p.x_vec && (!weight || (n.weight_type == DSA_BF16 && p.weight_vec)) &&
       (!residual || (n.residual_type == DSA_BF16 && p.residual_vec)) && (!residual_out || p.residual_out_vec) &&
       (!out || (n.out_type == DSA_BF16 && p.out_vec)) && (!codes || p.codes_vec)) {
-    if (pieces <= 32) run_bf16<32, 1>(p, num_sms, s);
-    else if (pieces <= 64) run_bf16<32, 2>(p, num_sms, s);
-    else if (pieces <= 128) run_bf16<64, 2>(p, num_sms, s);
-    else if (pieces <= 256) run_bf16<128, 2>(p, num_sms, s);
-    else if (pieces <= 512) run_bf16<256, 2>(p, num_sms, s);
-    else if (pieces <= 1024) run_bf16<512, 2>(p, num_sms, s);
-    else run_bf16<1024, 2>(p, num_sms, s);
     *launches += 1;
-    return cudaGetLastError();
+    return pieces <= 32     ? run_bf16<32, 1>(p, num_sms, s)
+           : pieces <= 64   ? run_bf16<32, 2>(p, num_sms, s)
+           : pieces <= 128  ? run_bf16<64, 2>(p, num_sms, s)
+           : pieces <= 256  ? run_bf16<128, 2>(p, num_sms, s)
+           : pieces <= 512  ? run_bf16<256, 2>(p, num_sms, s)
+           : pieces <= 1024 ? run_bf16<512, 2>(p, num_sms, s)
+                            : run_bf16<1024, 2>(p, num_sms, s);
   }
-  if (pieces <= 32) run<32, 8, 1>(p, s);
-  else if (pieces <= 64) run<32, 8, 2>(p, s);
-  else if (pieces <= 128) run<32, 8, 4>(p, s);
-  else if (pieces <= 256) run<128, 1, 2>(p, s);
-  else if (pieces <= 512) run<256, 1, 2>(p, s);
-  else if (pieces <= 1024) run<512, 1, 2>(p, s);
-  else if (pieces <= 2048) run<512, 1, 4>(p, s);
-  else run<1024, 1, 4>(p, s);   // up to kNormMaxWidth
   *launches += 1;
-  return cudaGetLastError();
+  return pieces <= 32     ? run<32, 8, 1>(p, s)
+         : pieces <= 64   ? run<32, 8, 2>(p, s)
+         : pieces <= 128  ? run<32, 8, 4>(p, s)
+         : pieces <= 256  ? run<128, 1, 2>(p, s)
+         : pieces <= 512  ? run<256, 1, 2>(p, s)
+         : pieces <= 1024 ? run<512, 1, 2>(p, s)
+         : pieces <= 2048 ? run<512, 1, 4>(p, s)
+                          : run<1024, 1, 4>(p, s);   // up to DSA_NORM_MAX_WIDTH
 }
 
 }  // namespace dsa
