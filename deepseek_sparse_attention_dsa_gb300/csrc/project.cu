@@ -232,9 +232,7 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
     for (uint32_t t = t0; t < tiles && ok; t += t_step) {
       for (int kb = kb0; kb < kb1; kb += C::KC, ++i) {
         const uint32_t ab = i % C::AB;
-        if (!(ok = mbar_wait_warp(full(st), ph, aborted, p.err) &&
-                   mbar_wait_warp(aempty(ab), (i / C::AB & 1) ^ 1, aborted, p.err)))
-          break;
+        if (!(ok = mbar_wait_warp_both(full(st), ph, aempty(ab), (i / C::AB & 1) ^ 1, aborted, p.err))) break;
         tc_fence_after();
         if (elect_one()) {
           const uint64_t wd = desc0 + st * (C::STAGE >> 4);
@@ -602,9 +600,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
 #pragma unroll 1
       for (uint32_t i = 0; i < blocks; ++i) {   // the k blocks of all its tiles
         const uint32_t st = i % C::STAGES, ab = i % C::AB;
-        if (!mbar_wait_warp(full(st), i / C::STAGES & 1, aborted, p.err) ||
-            !mbar_wait_warp(aempty(ab), (i / C::AB & 1) ^ 1, aborted, p.err))
-          break;
+        if (!mbar_wait_warp_both(full(st), i / C::STAGES & 1, aempty(ab), (i / C::AB & 1) ^ 1, aborted, p.err)) break;
         tc_fence_after();
         if (elect_one()) {
           const uint64_t ad = desc0 + st * (C::STAGE >> 4), wd = ad + (C::A_BYTES >> 4);
