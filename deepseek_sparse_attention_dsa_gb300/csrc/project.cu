@@ -390,6 +390,7 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem_base, C::TMEM_COLS);
+  if (p.split > 1) linger_if_aborted(aborted);
 }
 
 // ---------------------------------------------------------------------------
@@ -792,6 +793,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
     if (kPair) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
     else tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
+  if (!kPair && ctas > 1) linger_if_aborted(aborted);
 }
 
 __device__ __forceinline__ float e4m3_value(uint8_t c) {
@@ -930,7 +932,7 @@ void choose(const dsa_ctx *ctx, const dsa_project_t &g, int *nt, int *split) {
   for (const Form &f : forms) {
     if (f.m < 64 && g.rows > 4 * f.m) continue;
     const int64_t tiles = tiles_of(g, f.m, f.n), cap = ctx->num_sms / f.ctas;
-    if (f.m >= 256 && tiles >= INT32_MAX / 8) continue;   // (32-bit tile counts)
+    if (f.m >= 128 && tiles >= INT32_MAX / 8) continue;   // (32-bit tile counts)
     for (int s = 1; s <= f.max_split; s *= 2) {
       if (s > 1 && (tiles * s > cap || kbs < 2 * s)) break;
       const int64_t per_cta = s > 1 ? 1 : (tiles + cap - 1) / cap;

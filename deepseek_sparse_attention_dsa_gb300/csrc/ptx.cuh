@@ -134,6 +134,16 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, ui
   return ok;
 }
 
+// A CTA that gave up stays for as long as its cluster's others may still send to
+// its shared memory: each of their waits ends within the limit.
+__device__ __forceinline__ void linger_if_aborted(uint32_t abort_flag) {
+  uint32_t stop;
+  asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(stop) : "r"(abort_flag) : "memory");
+  if (!stop) return;
+  const uint64_t t0 = globaltimer();
+  while (globaltimer() - t0 < 3 * kWaitLimitNs) __nanosleep(1000);
+}
+
 // Both of two phases, tried together first so that one try's latency covers the other's.
 __device__ __forceinline__ bool mbar_wait_warp_both(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1,
                                                     uint32_t abort_flag, int *err) {

@@ -124,6 +124,19 @@ def test_strided_and_unaligned_layouts(ctx, pad, shift, fast):
     ctx.get_error()
 
 
+@pytest.mark.parametrize("rows,batch,n,k", [(20, 3, 136, 272), (300, 3, 136, 272), (300, 40, 520, 128)])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_heads_outermost_output(ctx, rows, batch, n, k, dt):
+    """out as [batch][rows][n] in a larger buffer, on 16 bytes: whole boxes are stored at permuted strides."""
+    t = make(21, rows, n, k, batch)
+    store = torch.full((batch, rows + 1, n + 8), 77.0, dtype=dt, device="cuda")
+    out = store[:, :rows, :n].transpose(0, 1)
+    ctx.project_fp8(*t, out=out)
+    check(out, *t)
+    out.fill_(77.0)
+    assert (store == 77).all()
+
+
 def test_one_weight_for_every_head(ctx):
     """w expanded over the batch (a stride of zero)."""
     a, asc, w, wsc = make(6, 20, 128, 256, 4)
