@@ -5,23 +5,35 @@
 //
 // for b = 0 .. batch-1 (the heads of an absorbed projection; 1 otherwise).
 //
-// project_tc_kernel: tcgen05 kind::f8f6f4.  A tile is 128 weight rows (the MMA's
-// 128 lanes, and exactly one row of scale blocks) by NT tokens (its columns),
-// so that one kernel covers a single token (NT = 16) and a prefill chunk.  The
-// scales change with every 128 of k, so the tensor core sums one block of 128
-// at a time into a tensor-memory buffer (four K = 32 steps), and the epilogue
-// warps add the blocks up in registers: acc[col] += s[kb][col] * block[col] with
-// s = a_scale * w_scale, which two helper warps put into shared memory ahead of
-// them.  Buffers of tensor memory let the tensor core run ahead of that.
+// The scales change with every 128 of k, so the tensor core (tcgen05
+// kind::f8f6f4) sums one block of 128 at a time into a tensor-memory buffer
+// (four K = 32 steps) and the epilogue warps add the blocks up in registers:
+// acc[col] += s * block[col], s = a_scale * w_scale.  Several buffers let the
+// tensor core run ahead of that.  A block of 128 of every weight row has one
+// scale for 128 rows, so a tile never needs more than one or two of them.
+//
+// project_tc_kernel, few rows: a tile is 128 weight rows (the MMA's 128 lanes) by
+// NT = 16, 32 or 64 tokens (its columns); two helper warps put s for the tile's
+// tokens into shared memory ahead of the epilogue.  Bound by the weights' bytes:
+// 16 x 8192 x 8192 takes 13.4 us on one GB300, 67 MB at 5.0 TB/s, of which some
+// 3 us are the first loads' latency and the last block's way out (1 x 8192 x
+// 2048: 4.3 us).
+//
+// project_rows_kernel, more rows: tokens are the lanes (see there).
 //
 // Few tiles: a cluster of S CTAs shares a tile, each taking a run of its k
 // blocks.  The tile's tokens are dealt out to the ranks; every CTA sends its
 // partial sums of a token to the token's owner (st.async, counted on the owner's
 // mbarrier), which adds the S of them in rank order, so results do not depend on
-// timing, and no CTA waits for another to finish.
+// timing, and no CTA waits for another to finish (with the partial sums fetched
+// from the other CTAs between two cluster barriers a call took 0.9 us longer).
 //
 // Warp roles: 0 TMA producer, 1 MMA issuer and tensor-memory owner, 2-3 scales,
-// 4.. epilogue.
+// 4.. epilogue.  What their hand-overs cost decides the small tiles: a wait on a
+// completed mbarrier is some 70 cycles, so the issuer tries both of its barriers
+// in one go; arrivals that order nothing but completed reads are relaxed (with
+// release semantics at cluster scope an arrival took 340 cycles, and over 1000
+// beside TMA traffic: 770 us instead of 530 for 8192 x 8192 x 4096 at the time).
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -398,12 +410,22 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
 // epilogue thread then has one token and, its warp being on one weight block, s
 // is one number per block of k; with weights on the lanes every column's s comes
 // out of shared memory for every lane, which beyond 64 columns costs more of its
-// bandwidth than the operands do.
+// bandwidth than the operands do (8192 x 8192 x 4096 on 128 x 128 tiles: 451 us
+// with weights on the lanes, 257 with tokens).
 //
 //   kPair: a pair of CTAs (cta_group::2) on 256 tokens, 128 lanes in each, by N
 //   weight rows; each CTA brings its tokens and half of the weights, so at N =
 //   256 a block of k costs a CTA 32 KB for 128 x 256 x 128 products.
 //   else: one CTA on 128 tokens by 128 weight rows, or two on the halves of k.
+//
+// Bounds, at 8192 x 8192 x 4096 (197 us, 2.79 PFLOP/s; 215 us when repeated, the
+// card then at its power limit and 1.75 GHz): a block's 512 cycles of MMA, its
+// way to the epilogue and back through two buffers, and 256 FMAs a scheduler;
+// without the FMAs it took 169 us, without the loads too 142.  Tried and slower:
+// packed FMAs (253 us), 16 epilogue warps (267 us: spills), the next block's
+// first load before a block's last FMAs (loop-carried registers are copied).
+// 128 x 128 tiles and N = 128 pairs are bound by operand reads from shared memory
+// (540 and 410 cycles a block with neither loads nor FMAs, 64 bytes a cycle).
 template <bool kPair_, int N_>
 struct RowsTraits {
   static constexpr bool kPair = kPair_;
@@ -916,8 +938,11 @@ cudaError_t run_tc(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &p,
 // The kernel (tokens a tile: 16, 32, 64 with weights on the lanes; 128 on one
 // CTA and 256 on a pair with tokens on the lanes, 257 the pair with 256 columns)
 // and the CTAs that split a tile's k: the least of what the measured times of a
-// block of k on each (us, beside others on the card; the pairs' with a share of
-// the tile's end) make of the blocks that the busiest CTA gets.
+// block of k and of a tile's end on each (us) make of the blocks that the busiest
+// CTA gets.  Measured on either side of its choices (us a call): 128 x 8192 x
+// 4096 12.0 with {128, 2 CTAs}, 12.9 with {64}, 15.1 with {128}; 256 x 8192 x
+// 4096 15.4 with {256}, 15.6 with {128}, 18.7 with {257}; 1024 x 4096 x 4096 19.7
+// with {257}, 24.8 with {256}; 16 x 8192 x 2048 5.9 with {16, 2}, 6.4 with {16}.
 void choose(const dsa_ctx *ctx, const dsa_project_t &g, int *nt, int *split) {
   struct Form {
     int nt, m, n, ctas, max_split;

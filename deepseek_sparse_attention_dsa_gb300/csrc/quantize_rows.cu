@@ -2,7 +2,10 @@
 // layouts of the 8-bit product (project.cu): rows with a scale per 128 columns
 // (activations), matrices with a scale per 128 x 128 block (weights).  The rule
 // is the one of quantize-on-store (fp8.cuh).  Bound by HBM: every value is read
-// once and stays in registers between its group's maximum and its code.
+// once and stays in registers between its group's maximum and its code (rows of
+// 2048 x 65536 bf16: 62.9 us, 6.47 TB/s, 95% of the measured copy; blocks of 8192
+// x 4096 bf16: 16.7 us, 6.0 TB/s).  With a division for each value the first took
+// 149 us, bound by its instructions.
 #include <cuda_runtime.h>
 
 #include "dsa_internal.h"

@@ -398,7 +398,11 @@ int dsa_msa_attend_on_tensor_cores(const dsa_ctx_t *ctx, const dsa_plan_t *plan,
  * values comes back finite.
  *
  * The calls use a context for its device, error word and launch count only:
- * its shape and formats are not read.  They need no workspace.  `plan` may be
+ * its shape and formats are not read.  They need no workspace, and calls on
+ * different streams or threads share nothing.  Their kernels are launched with
+ * programmatic stream serialization: set up while the stream's previous kernel
+ * still runs, they wait for its end before they read or write global memory, and
+ * a kernel that a caller launches after them in the same way does so too.  `plan` may be
  * NULL; with a plan of this context, rows must be a multiple (m times) of the
  * plan's num_rows, and with a capturable plan the rows at or after m times the
  * current row count are padding: what they hold does not matter, and nothing is
@@ -467,7 +471,7 @@ dsa_status dsa_quantize_weight(dsa_ctx_t *ctx, const dsa_weight_t *shape, const 
  * distance between neighbouring b.  Sums are added in a fixed order: equal
  * calls give equal bits.  The tensor cores need a and w on 16 bytes with
  * strides that are multiples of 16 (dsa_project_on_tensor_cores); other
- * layouts run a CUDA-core kernel.  n at most 64 * 65535, batch at most 65535. */
+ * layouts run a CUDA-core kernel.  out must not overlap the operands.  n at most 64 * 65535, batch at most 65535. */
 typedef struct dsa_project {
   int64_t rows;
   int32_t batch, n, k;
