@@ -11,6 +11,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include "dsa.h"
@@ -36,17 +37,24 @@ struct Call {
   dsa_plan_t *plan;
   int device;   // -1: a host-only context, whose tensors are the host's
   dsa_stream_t stream;
+  bool other;   // a stream was given: it may not be the current one
 
   // (handle, device, plan, stream): the first four arguments of every function
   bool take(PyObject *const *args) {
     ctx = static_cast<dsa_ctx_t *>(PyLong_AsVoidPtr(args[0]));
     device = static_cast<int>(PyLong_AsLong(args[1]));
     plan = args[2] == Py_None ? nullptr : static_cast<dsa_plan_t *>(PyLong_AsVoidPtr(args[2]));
-    if (args[3] != Py_None) stream = static_cast<dsa_stream_t>(PyLong_AsVoidPtr(args[3]));
+    other = args[3] != Py_None;
+    if (other) stream = static_cast<dsa_stream_t>(PyLong_AsVoidPtr(args[3]));
     else stream = device < 0 ? nullptr : reinterpret_cast<dsa_stream_t>(c10::cuda::getCurrentCUDAStream(device).stream());
     return !PyErr_Occurred();
   }
+  // A new tensor of the call's stream: memory that the current stream has freed
+  // but may still be working on is not written from another.
   at::Tensor make(at::IntArrayRef shape, at::ScalarType type) const {
+    c10::cuda::OptionalCUDAStreamGuard guard;
+    if (other && device >= 0)
+      guard.reset_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream), device));
     return at::empty(shape, at::TensorOptions().dtype(type).device(device < 0 ? at::Device(at::kCPU)
                                                                              : at::Device(at::kCUDA, device)));
   }

@@ -93,7 +93,7 @@ struct ProjectTraits {
   static constexpr int W_BYTES = 128 * 128, A_BYTES = NT * 128;
   static constexpr int BLOCK = W_BYTES + A_BYTES;           // one block of k of a stage: weights, tokens
   static constexpr int STAGE = KC * BLOCK;
-  static constexpr int STAGES = NT == 64 ? 3 : 5;
+  static constexpr int STAGES = NT == 64 ? 3 : 4;
   static constexpr int AB = 4;                              // tensor-memory buffers, each a chunk
   static constexpr int TMEM_COLS = AB * KC * NT;
   static constexpr int GK = 16, SG = 3;     // k blocks per scale slot (whole chunks), slots

@@ -262,6 +262,36 @@ def test_captured_and_replayed_on_new_data(ctx):
             assert torch.equal(a, b)
 
 
+def test_new_outputs_belong_to_the_stream_of_the_call(ctx):
+    """Memory that the current stream has given back but still has work on is not
+    handed to a call on another stream."""
+    x = placed(rand(22, 64, 4096), BF16)
+    want = [t.clone() for t in ctx.quantize_rows(x)]
+    a = torch.zeros(64, 4096, dtype=torch.uint8, device="cuda")
+    asc, w, wsc = torch.ones(64, 32, device="cuda"), torch.zeros(4096, 4096, dtype=torch.uint8, device="cuda"), torch.ones(32, 32, device="cuda")
+    side = torch.cuda.Stream()
+    for given in (side, side.cuda_stream):
+        for call, like in ((lambda: ctx.quantize_rows(x, stream=given)[0], torch.uint8),
+                           (lambda: ctx.project_fp8(a, asc, w, wsc, stream=given), BF16),
+                           (lambda: ctx.rmsnorm(x, None, stream=given), BF16)):
+            for _ in range(2):
+                torch.cuda.synchronize()
+                torch.cuda.empty_cache()
+                held = torch.empty(64, 4096, dtype=like, device="cuda")
+                at = held.data_ptr()
+                torch.cuda._sleep(20_000_000)      # some 10 ms on the current stream
+                held.fill_(7)
+                del held
+                out = call()
+                assert out.data_ptr() != at
+                side.synchronize()
+                kept = out.clone()
+                torch.cuda.synchronize()
+                assert torch.equal(out, kept)
+                if like == torch.uint8:
+                    assert torch.equal(out, want[0])
+
+
 def test_refused_calls_leave_the_context_usable(ctx):
     x = placed(rand(19, 4, 256), BF16)
     plan3 = ctx.plan([W.Span(0, 0, 3, 0, np.zeros(1, np.int32))], 1)
