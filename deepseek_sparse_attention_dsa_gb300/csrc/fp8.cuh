@@ -21,7 +21,8 @@ namespace dsa {
 // weigh: each lets its successor be launched at once and waits, before it touches
 // global memory, until its predecessor is complete and its writes are visible.
 // Every CTA waits (also one without work: a kernel that ended before its
-// predecessor would let its successor run beside that).
+// predecessor would let its successor run beside that).  Inputs may be written
+// after such a kernel has started, so it does not use read-only (nc) loads.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependency() {

@@ -269,18 +269,20 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
   } else if (warp < 4) {
     // ------------------------------------------------------------ scales
     // thread: k block g of a slot and every (64 / GK)th token; the loads of
-    // the next slot are in flight while this one waits for its turn
+    // the next slot are in flight while this one waits for its turn.  (From L2:
+    // the kernel may have been set up before its inputs were written, so none of
+    // them is read-only for its whole life.)
     const int ht = threadIdx.x - 64;
     const int g = ht % C::GK, c0 = ht / C::GK;
     float sa[C::S_VALS], sw = 0.f;
     auto load = [&](const ProjectTile &tile, int kb) {
       const bool in = kb + g < kb1;
-      sw = in ? __ldg(p.w_scale + tile.b * p.ws_batch + tile.n0 / 128 * p.ws_stride + kb + g) : 0.f;
+      sw = in ? __ldcg(p.w_scale + tile.b * p.ws_batch + tile.n0 / 128 * p.ws_stride + kb + g) : 0.f;
       const float *as = p.a_scale + tile.b * p.as_batch + kb + g;
 #pragma unroll
       for (int j = 0; j < C::S_VALS; ++j) {
         const int64_t m = tile.m0 + c0 + j * (64 / C::GK);
-        sa[j] = in && m < live ? __ldg(as + m * p.as_stride) : 0.f;
+        sa[j] = in && m < live ? __ldcg(as + m * p.as_stride) : 0.f;
       }
     };
     int sg = 0;

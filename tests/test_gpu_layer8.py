@@ -174,6 +174,55 @@ def test_steps_back_to_back_equal_steps_with_a_wait_between_the_calls(built):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("rows", [3, 40, 100, 300])
+def test_buffers_rewritten_call_after_call(built, rows):
+    """Codes, scales and rows written and read again and again in the same
+    buffers by launches that overlap, on few enough CTAs for three of them to be
+    on the card at once."""
+    ctx = dsa.Context(W.DSAShape(**W.DEEPSEEK), 0)
+    g = torch.Generator().manual_seed(rows)
+    w = ctx.quantize_weight((torch.randn(256, 1024, generator=g) / 32).to(BF16).cuda())
+    back = ctx.quantize_weight((torch.randn(1024, 256, generator=g) / 16).to(BF16).cuda())
+    xs = [(torch.randn(rows, 1024, generator=g) * (i + 1)).to(BF16).cuda() for i in range(8)]
+
+    codes, scales = torch.empty(rows, 1024, dtype=torch.uint8, device="cuda"), torch.empty(rows, 8, device="cuda")
+    yc, ys = torch.empty(rows, 256, dtype=torch.uint8, device="cuda"), torch.empty(rows, 2, device="cuda")
+    y, h = torch.empty(rows, 256, dtype=F32, device="cuda"), torch.empty(rows, 1024, dtype=BF16, device="cuda")
+    res = torch.empty(rows, 1024, dtype=BF16, device="cuda")
+    outs = [torch.empty(rows, 256, dtype=F32, device="cuda") for _ in range(64)]
+
+    def body(wait=False):
+        h.zero_()
+        res.zero_()
+        for i in range(64):
+            for call in (lambda: ctx.rmsnorm_quantize(xs[i % 8] if i % 3 else h, None, residual=res if i % 8 else xs[i % 8],
+                                                      residual_out=res, codes=codes, scales=scales),
+                         lambda: ctx.project_fp8(codes, scales, *w, out=y),
+                         lambda: ctx.quantize_rows(y, yc, ys),
+                         lambda: ctx.project_fp8(yc, ys, *back, out=h),
+                         lambda: ctx.project_fp8(codes, scales, *w, out=outs[i])):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+
+    def results():
+        torch.cuda.synchronize()
+        ctx.get_error()
+        return [t.clone() for t in outs + [res, h]]
+
+    body(wait=True)
+    want = results()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        body()
+    for go in [body] * 4 + [g.replay] * 4:
+        for t in outs:
+            t.fill_(-1)
+        go()
+        for i, (a, b) in enumerate(zip(results(), want)):
+            assert torch.equal(a, b), (go, i)
+
+
 def test_a_captured_layer_replays_over_rewritten_spans(built):
     """The whole step on a capturable plan in one graph: replays over two
     different steps (fewer rows, then more) equal the eager calls, and the rows
