@@ -937,14 +937,43 @@ cudaError_t run_tc(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &p,
   return launch(ctx, project_tc_kernel<NT>, C::THREADS, C::SMEM, grid, split, smem_limit_set, p, s);
 }
 
+// Clusters of `ctas` CTAs, one to an SM, that the device holds at once: less than
+// its SMs allow, as a cluster lies within a group of them (a GB300 with 152 SMs
+// holds 36 of four and 15 of eight; 48 x 2048 x 8192 on 16 clusters of eight took
+// 12.2 us, on as many of four 7.8).  Asked of the driver once a device.
+int clusters_at_once(const dsa_ctx *ctx, int ctas) {
+  if (ctas <= 2) return ctx->num_sms / ctas;
+  static std::atomic<int> known[64][2];
+  const int dev = ctx->device < 64 ? ctx->device : 63, slot = ctas == 4 ? 0 : 1;
+  int n = ctx->device < 64 ? known[dev][slot].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  using C = ProjectTraits<64>;
+  static std::atomic<uint64_t> smem_limit_set{0};
+  if (ensure_smem_limit(project_tc_kernel<64>, C::SMEM, ctx->device, smem_limit_set) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas * ctx->num_sms);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = ctas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, project_tc_kernel<64>, &cfg) != cudaSuccess) return 0;
+  if (ctx->device < 64) known[dev][slot].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 // The kernel (tokens a tile: 16, 32, 64 with weights on the lanes; 128 on one
 // CTA and 256 on a pair with tokens on the lanes, 257 the pair with 256 columns)
 // and the CTAs that split a tile's k: the least of what the measured times of a
 // block of k and of a tile's end on each (us) make of the blocks that the busiest
 // CTA gets.  Measured on either side of its choices (us a call): 128 x 8192 x
-// 4096 12.0 with {128, 2 CTAs}, 12.9 with {64}, 15.1 with {128}; 256 x 8192 x
-// 4096 15.4 with {256}, 15.6 with {128}, 18.7 with {257}; 1024 x 4096 x 4096 19.7
-// with {257}, 24.8 with {256}; 16 x 8192 x 2048 5.9 with {16, 2}, 6.4 with {16}.
+// 4096 10.6 with {128, 2 CTAs}, 11.8 with {64}, 13.3 with {128}; 256 x 8192 x
+// 4096 13.8 with {256}, 13.9 with {128}, 17.3 with {257}; 1024 x 4096 x 4096 18.6
+// with {257}, 22.7 with {256}; 16 x 8192 x 2048 4.7 with {16, 2}, 5.4 with {16}.
+// Of 35 sizes it misses the best by 5 to 8% in three, by 1% or less in the others.
 void choose(const dsa_ctx *ctx, const dsa_project_t &g, int *nt, int *split) {
   struct Form {
     int nt, m, n, ctas, max_split;
@@ -961,7 +990,7 @@ void choose(const dsa_ctx *ctx, const dsa_project_t &g, int *nt, int *split) {
     const int64_t tiles = tiles_of(g, f.m, f.n), cap = ctx->num_sms / f.ctas;
     if (f.m >= 128 && tiles >= INT32_MAX / 8) continue;   // (32-bit tile counts)
     for (int s = 1; s <= f.max_split; s *= 2) {
-      if (s > 1 && (tiles * s > cap || kbs < 2 * s)) break;
+      if (s > 1 && (kbs < 2 * s || tiles > clusters_at_once(ctx, s))) break;
       const int64_t per_cta = s > 1 ? 1 : (tiles + cap - 1) / cap;
       const float t = static_cast<float>(per_cta) * (((kbs + s - 1) / s) * f.block + f.tile) + (s > 1 ? 0.4f : 0.f);
       if (*nt == 0 || t < best) best = t, *nt = f.nt, *split = s;
