@@ -498,9 +498,14 @@ class Context:
     # ---------------------------------------------- 8-bit rows and projections
     # (their tensors are read and made in csrc/binding.cpp: these calls are short
     # enough for the host's part to count)
+    def _address(self):
+        return self.handle.value if self.handle else 0   # (closed: the call refuses it)
+
     @staticmethod
     def _plan_of(plan):
-        return None if plan is None else plan.handle.value
+        if not plan.handle:   # a closed plan is not the same as none
+            raise DSAError(1, "plan")
+        return plan.handle.value
 
     @staticmethod
     def _stream_of(stream):
@@ -510,7 +515,7 @@ class Context:
                 plan=None, stream=None):
         """dsa_rmsnorm: x (rows, width) bf16 or fp32 -> the normed rows in
         out_dtype; with a residual (added first) -> (out, residual_out)."""
-        return self._rows.rmsnorm(self.handle.value, self.device_index, plan and self._plan_of(plan),
+        return self._rows.rmsnorm(self._address(), self.device_index, plan and self._plan_of(plan),
                                   stream and self._stream_of(stream), x, weight, eps, residual, residual_out, out,
                                   out_dtype, None, None, False)
 
@@ -519,20 +524,20 @@ class Context:
         """dsa_rmsnorm with an 8-bit output: (codes (rows, width) uint8, scales
         (rows, ceil(width / 128)) fp32), and residual_out after them where there
         is a residual.  out, where given, takes the normed rows too."""
-        return self._rows.rmsnorm(self.handle.value, self.device_index, plan and self._plan_of(plan),
+        return self._rows.rmsnorm(self._address(), self.device_index, plan and self._plan_of(plan),
                                   stream and self._stream_of(stream), x, weight, eps, residual, residual_out, out, None,
                                   codes, scales, True)
 
     def quantize_rows(self, x, codes=None, scales=None, plan=None, stream=None):
         """dsa_quantize_rows: x (rows, width) bf16 or fp32 -> (codes uint8 of
         the same shape, scales (rows, ceil(width / 128)) fp32)."""
-        return self._rows.quantize_rows(self.handle.value, self.device_index, plan and self._plan_of(plan),
+        return self._rows.quantize_rows(self._address(), self.device_index, plan and self._plan_of(plan),
                                         stream and self._stream_of(stream), x, codes, scales)
 
     def quantize_weight(self, w, codes=None, scales=None, stream=None):
         """dsa_quantize_weight: w (n, k) or (batch, n, k) bf16 or fp32 -> (codes
         uint8 of the same shape, scales (..., ceil(n / 128), ceil(k / 128)) fp32)."""
-        return self._rows.quantize_weight(self.handle.value, self.device_index, None, stream and self._stream_of(stream),
+        return self._rows.quantize_weight(self._address(), self.device_index, None, stream and self._stream_of(stream),
                                           w, codes, scales)
 
     def project_fp8(self, a, a_scale, w, w_scale, out=None, out_dtype=torch.bfloat16, plan=None, stream=None):
@@ -540,12 +545,12 @@ class Context:
         times w (n, k) with scales per 128 x 128 block -> (rows, n) in
         out_dtype; or for each b, a (rows, batch, k) times w (batch, n, k) ->
         (rows, batch, n).  Codes are uint8 or float8_e4m3fn."""
-        return self._rows.project_fp8(self.handle.value, self.device_index, plan and self._plan_of(plan),
+        return self._rows.project_fp8(self._address(), self.device_index, plan and self._plan_of(plan),
                                       stream and self._stream_of(stream), a, a_scale, w, w_scale, out, out_dtype, False)
 
     def project_on_tensor_cores(self, a, a_scale, w, w_scale, out) -> bool:
         """Whether project_fp8 runs this call on the tensor cores."""
-        return self._rows.project_fp8(self.handle.value, self.device_index, None, 0, a, a_scale, w, w_scale, out, None, True)
+        return self._rows.project_fp8(self._address(), self.device_index, None, 0, a, a_scale, w, w_scale, out, None, True)
 
     def index_scores(self, plan: Plan, q, w, index_cache, scores=None, stream=None) -> torch.Tensor:
         d = self.device

@@ -410,9 +410,9 @@ int dsa_msa_attend_on_tensor_cores(const dsa_ctx_t *ctx, const dsa_plan_t *plan,
  *
  * Strides are in elements (codes: bytes) from one row, or one matrix of a
  * batch, to the next; a row's own values are adjacent.  Rows must not overlap
- * in anything written.  Any stride and alignment is accepted (of the type's own
- * size); 16-byte aligned rows run faster, and project_fp8 needs them for the
- * tensor cores.  DSA_ERR_INVALID_ARG: null pointers, sizes below 1 (rows may be
+ * in anything written (what is only read may overlap or repeat).  Any stride and
+ * alignment is accepted (of the type's own size); 16-byte aligned rows run
+ * faster, and project_fp8 needs them for the tensor cores.  DSA_ERR_INVALID_ARG: null pointers, sizes below 1 (rows may be
  * 0: nothing is launched), unknown types, negative strides, written rows
  * that would overlap, or rows that do not match the plan; DSA_ERR_UNSUPPORTED: sizes beyond the limits given below. */
 enum { DSA_BF16 = 0, DSA_FP32 = 1 };
@@ -425,7 +425,9 @@ enum { DSA_BF16 = 0, DSA_FP32 = 1 };
  * NULL (h = x), and then residual_out must be; residual_out, weight (all ones)
  * and either of out and codes may be NULL; codes and scales come together.
  * residual_out may be the buffer of residual or x, and out that of x, with the
- * same type and stride.  width is at most DSA_NORM_MAX_WIDTH. */
+ * same type and stride.  The sum of squares has fp32's range: a row of finite
+ * values whose sum is beyond it gives zeros, and an all-zero row gives NaN where
+ * eps is 0.  width is at most DSA_NORM_MAX_WIDTH. */
 #define DSA_NORM_MAX_WIDTH 32768
 typedef struct dsa_norm {
   int64_t rows;

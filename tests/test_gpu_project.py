@@ -255,3 +255,25 @@ def test_refused_calls_leave_the_context_usable(ctx):
     with pytest.raises(ValueError):
         ctx.project_fp8(a.cpu(), asc, w, wsc)
     ctx.get_error()
+
+
+@pytest.mark.parametrize("rows", [5, 70, 130, 700])
+def test_inputs_may_overlap_or_repeat(ctx, rows):
+    """Rows 16 codes apart (windows of one sequence) on the tensor cores; one row, or one matrix, for all (stride 0) off them."""
+    n, k = 1024, 272
+    a, asc, w, wsc = make(rows, rows, n, k)
+    windows = make(rows + 1, 1, 128, 16 * rows + k)[0].view(-1).as_strided((rows, k), (16, 1))
+    for x, ws, fast in ((windows, w, True), (a, make(3, 1, 128, 16 * n + k)[0].view(-1).as_strided((n, k), (16, 1)), True),
+                        (a[:1].expand(rows, k), w, False), (a, w[:1].expand(n, k), False)):
+        out = torch.empty(rows, n, dtype=F32, device="cuda")
+        assert ctx.project_on_tensor_cores(x, asc, ws, wsc, out) is fast
+        check(ctx.project_fp8(x, asc, ws, wsc, out=out), x, asc, ws, wsc)
+    ctx.get_error()
+
+
+def test_heads_share_a_matrix_or_their_rows(ctx):
+    rows, batch, n, k = 40, 6, 200, 272
+    a, asc, w, wsc = make(8, rows, n, k, batch)
+    for x, xs, m, ms in ((a, asc, w[:1].expand_as(w), wsc[:1].expand_as(wsc)), (a[:, :1].expand_as(a), asc[:, :1].expand_as(asc), w, wsc)):
+        check(ctx.project_fp8(x, xs, m, ms), x, xs, m, ms)
+    ctx.get_error()

@@ -314,3 +314,15 @@ def test_refused_calls_leave_the_context_usable(ctx):
     assert status(lambda: ctx.rmsnorm(x, None, out=torch.empty(256, dtype=BF16, device="cuda").expand(4, 256))) == 1
     _exact(*ctx.quantize_rows(x[:3], plan=plan3), R.quantize(x[:3], 1))
     ctx.get_error()
+
+
+def test_norm_at_the_ends_of_the_sum_of_squares(ctx):
+    """Beyond fp32's range the sum gives zeros; an all-zero row gives zeros with an eps and NaN without."""
+    x = torch.zeros(3, 640, dtype=BF16, device="cuda")
+    x[1] = 1e20
+    x[2] = 1.0
+    for dt in (BF16, F32):
+        out = ctx.rmsnorm(x.to(dt), None, eps=1e-6, out_dtype=F32)
+        assert (out[:2] == 0).all() and ((out[2] - 1).abs() < 1e-6).all()
+        out = ctx.rmsnorm(x.to(dt), None, eps=0.0, out_dtype=F32)
+        assert out[0].isnan().all() and (out[1] == 0).all() and (out[2] == 1).all()

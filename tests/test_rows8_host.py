@@ -85,6 +85,24 @@ def test_calls_refuse_a_host_only_context(ctx):
         assert e.value.status == 1
 
 
+def test_calls_refuse_closed_contexts_and_plans():
+    c = dsa.Context(W.DSAShape(**W.DEEPSEEK), device=-1)
+    plan = c.plan([], 1)
+    x = torch.zeros(4, 256, dtype=BF16)
+    calls = [lambda p: c.rmsnorm(x, None, plan=p), lambda p: c.rmsnorm_quantize(x, None, plan=p),
+             lambda p: c.quantize_rows(x, plan=p),
+             lambda p: c.project_fp8(x.to(U8), torch.zeros(4, 2), x.to(U8), torch.zeros(1, 2), plan=p)]
+    plan.close()
+    for call in calls:      # not taken for a call without a plan
+        with pytest.raises(dsa.DSAError, match="plan"):
+            call(plan)
+    c.close()
+    for call in calls + [lambda p: c.quantize_weight(x)]:
+        with pytest.raises(dsa.DSAError) as e:
+            call(None)
+        assert e.value.status == 1
+
+
 def _norm(**kw):
     base = dict(rows=4, width=256, eps=1e-6, x_stride=256, residual_stride=256, residual_out_stride=256, out_stride=256,
                 codes_stride=256, scales_stride=2)
