@@ -57,7 +57,8 @@ struct ProjectParams {
   int *err;
   int64_t rows;
   int64_t a_stride, a_batch, w_stride, w_batch, as_stride, as_batch, ws_stride, ws_batch, out_stride, out_batch;
-  int32_t n, k, batch, per_row, out_type, split;
+  int32_t n, batch, per_row, out_type;
+  int32_t k, kbs, split, split_log2;   // kbs: blocks of 128 of k; split: CTAs (pairs) of a cluster that share them
   bool out_vec;   // rows of out start on 16 bytes
   bool out_tma;   // and every row is live: whole boxes are stored by TMA
 };
@@ -119,7 +120,7 @@ struct ProjectTile {
 // Tiles in order: tokens fastest, so that neighbouring CTAs share weights.
 __device__ __forceinline__ ProjectTile tile_at(uint32_t t, uint32_t m_tiles, uint32_t n_tiles, int NT) {
   const uint32_t rest = m_tiles == 1 ? t : t / m_tiles, m = t - rest * m_tiles;
-  const uint32_t b = rest / n_tiles;
+  const uint32_t b = rest < n_tiles ? 0 : rest / n_tiles;
   return {static_cast<int>(b), static_cast<int>(rest - b * n_tiles) * 128, static_cast<int64_t>(m) * NT};
 }
 
@@ -145,6 +146,22 @@ __device__ __forceinline__ void store4(const ProjectParams &p, int64_t m, int b,
     if (n + i < p.n) store_out(p, m, b, n + i, x[i]);
 }
 
+// The first of a rank's k blocks: they are dealt out evenly, the first kbs % split
+// ranks having one more.  (A split is a power of two: a division at a kernel's
+// start is on its way to the first load, and costs 0.1 us.)
+__device__ __forceinline__ int first_block(const ProjectParams &p, int rank) {
+  const int each = p.kbs >> p.split_log2;
+  return each * rank + min(rank, p.kbs - (each << p.split_log2));
+}
+
+// Arrivals that barrier i takes, in the order of the kernels' barriers: one lane
+// sets up each.  ctas: the CTAs whose epilogue warps hand buffers back.
+template <typename C>
+__device__ __forceinline__ uint32_t barrier_arrivals(int i, int ctas) {
+  const int j = i - 2 * C::STAGES, k = j - 2 * C::AB;
+  return j < C::AB ? 1 : k < 0 ? ctas * C::EPI : k < C::SG ? 64 : k < 2 * C::SG ? C::EPI : 1;
+}
+
 template <int NT>
 __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kernel(const __grid_constant__ ProjectParams p) {
   using C = ProjectTraits<NT>;
@@ -166,26 +183,12 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
   const int warp = threadIdx.x / 32;
   const int lane = lane_id();
   const int rank = p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int kbs = (p.k + 127) / 128;
-  const int kb0 = kbs / p.split * rank + min(rank, kbs % p.split);   // the first kbs % split ranks have one more
-  const int kb1 = kb0 + kbs / p.split + (rank < kbs % p.split ? 1 : 0);
+  const int kb0 = first_block(p, rank), kb1 = first_block(p, rank + 1);
 
   launch_dependents();
-  if (warp == 0 && elect_one()) {
-    for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), 1);
-    }
-    for (int b = 0; b < C::AB; ++b) {
-      mbar_init(afull(b), 1);
-      mbar_init(aempty(b), C::EPI);
-    }
-    for (int g = 0; g < C::SG; ++g) {
-      mbar_init(sfull(g), 64);
-      mbar_init(sempty(g), C::EPI);
-    }
-    mbar_init(partfull, 1);
-    *abort_flag = 0;
+  if (warp == 0) {
+    if (lane < C::NBAR) mbar_init(bar0 + 8u * lane, barrier_arrivals<C>(lane, 1));
+    if (lane == 0) *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -202,13 +205,13 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
     named_bar_sync(1, C::THREADS);
     tc_fence_after();
   }
-  if (p.split > 1) cluster_arrive();
+  if (p.split > 1) cluster_arrive_relaxed();   // (the barriers are fenced; nothing else is handed over)
   grid_dependency_wait();
   const int64_t live = live_rows(p.rows, p.count, p.per_row);
   const uint32_t m_tiles = static_cast<uint32_t>((live + NT - 1) / NT);
   const uint32_t n_tiles = (p.n + 127) / 128;
   const uint32_t tiles = m_tiles * n_tiles * p.batch;
-  const uint32_t t0 = blockIdx.x / p.split, t_step = gridDim.x / p.split;
+  const uint32_t t0 = blockIdx.x >> p.split_log2, t_step = gridDim.x >> p.split_log2;
   const uint32_t tmem_base = warp == 0 ? 0 : *tmem_slot;
 
   if (warp == 0) {
@@ -311,6 +314,7 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
     const int quad = warp & 3;
     const int col0 = (warp - 4) / 4 * C::COLS;
     const int nl = quad * 32 + lane;   // weight row within the tile
+    if (p.split > 1) cluster_wait();   // the others are there (0.3 us, in the first loads' shade)
     int sg = 0;
     uint32_t sph = 0, i = 0;
     bool ok = true;
@@ -378,7 +382,6 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
       const int split = p.split, sh = 31 - __clz(split), own = NT >> sh;   // (a power of two)
       const int mine = (cols - rank + split - 1) >> sh;
       if (warp == 4 && elect_one()) mbar_arrive_expect_tx(partfull, (split - 1) * max(mine, 0) * 512);
-      cluster_wait();   // the others are there
       const uint32_t part = sbase + C::OFF_PART + (rank * own * 128 + nl) * 4;
 #pragma unroll
       for (int c = 0; c < C::COLS; ++c) {
@@ -458,17 +461,18 @@ struct RowsTraits {
   static_assert(128 * REGS_HELP + 32 * EPI * REGS_EPI <= 384 * 168, "registers");
 };
 
-__device__ __forceinline__ ProjectTile rows_tile_at(int t, int m_tiles, int n_tiles, int batch, int M, int N) {
+__device__ __forceinline__ ProjectTile rows_tile_at(int t, int m_tiles, int n_tiles, int M, int N) {
   // groups of 8 token tiles, weights next, tokens within the group fastest:
   // the tiles that run together share both operands in L2
   // (divisions cost more than anything else between two tiles: one, where
   // there is one matrix and the group is whole)
   int b = 0;
-  if (batch > 1) {
+  if (t >= m_tiles * n_tiles) {
     b = t / (m_tiles * n_tiles);
     t -= b * (m_tiles * n_tiles);
   }
-  const int group = t / (8 * n_tiles);
+  if (m_tiles == 1) return {b, t * N, 0};
+  const int group = m_tiles <= 8 ? 0 : t / (8 * n_tiles);
   const int size = min(m_tiles - group * 8, 8);
   const int in_g = t - group * 8 * n_tiles;
   const int j = size == 8 ? in_g >> 3 : in_g / size;
@@ -520,28 +524,15 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
   const int ctas = kPair ? 2 : p.split;
   const int rank = ctas > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int half = kPair ? rank : 0;   // of the tile's tokens
-  const int kbs = (p.k + 127) / 128;
-  const int kb0 = kPair ? 0 : kbs / ctas * rank + min(rank, kbs % ctas);   // the first kbs % split ranks have one more
-  const int kb1 = kPair ? kbs : kb0 + kbs / ctas + (rank < kbs % ctas ? 1 : 0);
+  const int kb0 = kPair ? 0 : first_block(p, rank), kb1 = kPair ? p.kbs : first_block(p, rank + 1);
 
   launch_dependents();
-  if (warp == 0 && elect_one()) {
-    for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), 1);
-    }
-    for (int b = 0; b < C::AB; ++b) {
-      mbar_init(afull(b), 1);
-      mbar_init(aempty(b), (kPair ? 2 : 1) * C::EPI);   // a pair's: both CTAs' epilogue warps, on the first CTA's barrier
-    }
-    for (int g = 0; g < C::SG; ++g) {
-      mbar_init(sfull(g), 64);
-      mbar_init(sempty(g), C::EPI);
-    }
-    mbar_init(partfull, 1);
-    *abort_flag = 0;
+  if (warp == 0) {
+    // (a pair's buffers: both CTAs' epilogue warps, on the first CTA's barrier)
+    if (lane < C::NBAR) mbar_init(bar0 + 8u * lane, barrier_arrivals<C>(lane, kPair ? 2 : 1));
+    if (lane == 0) *abort_flag = 0;
     fence_mbar_init();
-    if (!kPair && ctas == 2) mbar_arrive_expect_tx(partfull, C::EPI / 2 * C::OUT_WARP);
+    if (!kPair && ctas == 2 && lane == C::NBAR - 1) mbar_arrive_expect_tx(partfull, C::EPI / 2 * C::OUT_WARP);
   }
   if (warp == 1) {
     if (kPair) {
@@ -568,14 +559,15 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
       named_bar_sync(1, C::THREADS);
       tc_fence_after();
     }
-    if (ctas > 1) cluster_arrive();
+    if (ctas > 1) cluster_arrive_relaxed();
   }
   grid_dependency_wait();
   const int64_t live = live_rows(p.rows, p.count, p.per_row);
   const int m_tiles = static_cast<int>((live + C::M - 1) / C::M);
   const int n_tiles = (p.n + N - 1) / N;
   const int tiles = m_tiles * n_tiles * p.batch;
-  const int t0 = blockIdx.x / ctas, t_step = gridDim.x / ctas;
+  const int log2 = kPair ? 1 : p.split_log2;
+  const int t0 = blockIdx.x >> log2, t_step = gridDim.x >> log2;
   const uint32_t tmem_base = !kPair && warp == 0 ? 0 : *tmem_slot;
 
   if (warp < 4) {
@@ -586,7 +578,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
       uint32_t ph = 0;
       bool ok = true;
       for (int t = t0; t < tiles && ok; t += t_step) {
-        const ProjectTile tile = rows_tile_at(t, m_tiles, n_tiles, p.batch, C::M, C::N);
+        const ProjectTile tile = rows_tile_at(t, m_tiles, n_tiles, C::M, C::N);
         const int m = static_cast<int>(tile.m0) + half * 128, n = tile.n0 + half * C::W_ROWS;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!(ok = mbar_wait_warp(empty(st), ph ^ 1, aborted, p.err))) break;
@@ -651,7 +643,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
       uint32_t sph = 0;
       bool ok = true;
       for (int t = t0; t < tiles && ok; t += t_step) {
-        const ProjectTile tile = rows_tile_at(t, m_tiles, n_tiles, p.batch, C::M, C::N);
+        const ProjectTile tile = rows_tile_at(t, m_tiles, n_tiles, C::M, C::N);
         const int m0 = static_cast<int>(tile.m0) + half * 128;
         for (int kb = kb0; kb < kb1; kb += C::GK) {
           if (!(ok = mbar_wait_warp(sempty(sg), sph ^ 1, aborted, p.err))) break;
@@ -686,6 +678,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
     int ab = 0, sg = 0;
     uint32_t aph = 0, sph = 0;
     bool ok = true;
+    if (!kPair && ctas > 1) cluster_wait();   // the other CTA is there
     for (int t = t0; t < tiles && ok; t += t_step) {
       float acc[C::COLS];
 #pragma unroll
@@ -731,33 +724,24 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
         }
       }
       if (!ok) break;
-      const ProjectTile tile = rows_tile_at(t, m_tiles, n_tiles, p.batch, C::M, C::N);
+      const ProjectTile tile = rows_tile_at(t, m_tiles, n_tiles, C::M, C::N);
       const int64_t mw = tile.m0 + half * 128 + quad * 32;   // the warp's first token
       const int nw = tile.n0 + col0;                         // and first column
       const uint32_t stage_addr = sbase + C::OFF_OUT + (warp - 4) * C::OUT_WARP;
       if (!kPair && ctas == 2) {
         // two CTAs share the tile (one tile a cluster): rank r finishes tokens
-        // 64 r .. 64 r + 63.  A warp of the other tokens copies its sums into the
-        // same warp's staging in the other CTA, as the 16-byte pieces of each
-        // lane's row in an order that keeps the lanes apart.
-        cluster_wait();   // the other CTA is there
+        // 64 r .. 64 r + 63.  A warp of the other tokens sends its sums to the same
+        // warp's staging in the other CTA, four columns of its 32 rows at a time.
         if (quad / 2 != rank) {
+          const uint32_t to = map_to_cta(stage_addr + lane * 16, rank ^ 1), bar = map_to_cta(partfull, rank ^ 1);
 #pragma unroll
-          for (int c = 0; c < C::COLS; c += 4)
-            *reinterpret_cast<float4 *>(stage_out + lane * (C::COLS * 4) + (((c / 4) ^ (lane & 7)) << 4)) =
-                make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            bulk_copy_to_cta(map_to_cta(stage_addr, rank ^ 1), stage_addr, C::OUT_WARP, map_to_cta(partfull, rank ^ 1));
-            bulk_commit();
-          }
+          for (int c = 0; c < C::COLS; c += 4) st_async4(to + c * 128, acc + c, bar);
           break;
         }
         if (!mbar_wait_warp(partfull, 0, aborted, p.err)) break;
 #pragma unroll
         for (int c = 0; c < C::COLS; c += 4) {
-          const float4 v = *reinterpret_cast<const float4 *>(stage_out + lane * (C::COLS * 4) + (((c / 4) ^ (lane & 7)) << 4));
+          const float4 v = *reinterpret_cast<const float4 *>(stage_out + c * 128 + lane * 16);
           acc[c] += v.x, acc[c + 1] += v.y, acc[c + 2] += v.z, acc[c + 3] += v.w;
         }
         __syncwarp();   // the staging is read before it is filled again
@@ -836,9 +820,11 @@ __global__ void __launch_bounds__(256) project_simt_kernel(const ProjectParams p
   const float *as_ = p.a_scale + b * p.as_batch, *ws_ = p.w_scale + b * p.ws_batch;
   const int tm = threadIdx.x / 16, tn = threadIdx.x % 16;
   float acc[4][4] = {};
-  for (int kb = 0; kb * 128 < p.k; ++kb) {
+  for (int kb = 0; kb < p.kbs; ++kb) {
     float part[4][4] = {};
-    for (int k0 = kb * 128; k0 < min(p.k, kb * 128 + 128); k0 += 32) {
+    const int width = min(p.k - kb * 128, 128);
+    for (int j0 = 0; j0 < width; j0 += 32) {
+      const int k0 = kb * 128 + j0;
       __syncthreads();
       for (int i = threadIdx.x; i < 64 * 32; i += 256) {
         const int r = i / 32, c = i % 32;
@@ -908,7 +894,7 @@ template <bool kPair, int N>
 cudaError_t run_rows(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &p, int split, cudaStream_t s) {
   using C = RowsTraits<kPair, N>;
   if (!encode_operands(g, p, 128, C::W_ROWS)) return cudaErrorInvalidValue;
-  p.split = split;
+  p.split = split, p.split_log2 = split == 8 ? 3 : split / 2;
   if (p.out_vec && p.count == nullptr) {
     const bool bf16 = g.out_type == DSA_BF16;
     const int64_t es = bf16 ? 2 : 4;
@@ -930,7 +916,7 @@ template <int NT>
 cudaError_t run_tc(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &p, int split, cudaStream_t s) {
   using C = ProjectTraits<NT>;
   if (!encode_operands(g, p, NT, 128)) return cudaErrorInvalidValue;
-  p.split = split;
+  p.split = split, p.split_log2 = split == 8 ? 3 : split / 2;
   const int64_t tiles = tiles_of(g, NT, 128);
   const int64_t grid = split > 1 ? tiles * split : std::min<int64_t>(tiles, ctx->num_sms);
   static std::atomic<uint64_t> smem_limit_set{0};
@@ -982,7 +968,7 @@ void choose(const dsa_ctx *ctx, const dsa_project_t &g, int *nt, int *split) {
   static const Form forms[] = {{16, 16, 128, 1, 8, 0.19f, 0.2f},  {32, 32, 128, 1, 8, 0.21f, 0.4f},
                                {64, 64, 128, 1, 8, 0.26f, 0.7f},  {128, 128, 128, 1, 2, 0.33f, 0.5f},
                                {256, 256, 128, 2, 1, 0.29f, 0.5f}, {257, 256, 256, 2, 1, 0.40f, 0.9f}};
-  const int kbs = (g.k + 127) / 128;
+  const int kbs = (g.k - 1) / 128 + 1;
   float best = 0.f;
   *nt = 0;
   for (const Form &f : forms) {
@@ -1025,7 +1011,8 @@ cudaError_t launch_project_fp8(const dsa_ctx *ctx, const dsa_project_t &g, const
   p.as_stride = g.a_scale_stride, p.as_batch = g.a_scale_batch;
   p.ws_stride = g.w_scale_stride, p.ws_batch = g.w_scale_batch;
   p.out_stride = g.out_stride, p.out_batch = g.out_batch;
-  p.n = g.n, p.k = g.k;
+  p.n = g.n, p.k = g.k, p.kbs = (g.k - 1) / 128 + 1;
+  p.split = 1;
   p.batch = g.batch;
   p.out_type = g.out_type;
   p.err = ctx->err;

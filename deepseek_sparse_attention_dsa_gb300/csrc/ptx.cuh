@@ -347,13 +347,19 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // The cluster barrier in two halves, for warps that need not wait where they arrive.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // Store into another CTA's shared memory (dst and bar from mapa); the bytes
 // count on that CTA's mbarrier once they are there.
 __device__ __forceinline__ void st_async(uint32_t dst_cluster, float v, uint32_t bar_cluster) {
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(dst_cluster),
                "r"(__float_as_uint(v)), "r"(bar_cluster)
+               : "memory");
+}
+__device__ __forceinline__ void st_async4(uint32_t dst_cluster, const float *v, uint32_t bar_cluster) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst_cluster),
+               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+               "r"(__float_as_uint(v[3])), "r"(bar_cluster)
                : "memory");
 }
 __device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t nthreads) {

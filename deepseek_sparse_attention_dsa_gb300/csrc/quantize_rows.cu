@@ -223,7 +223,7 @@ cudaError_t launch_quantize_weight(const dsa_weight_t &w, const void *src, void 
             (w.batch == 1 || p.w_batch % 16 == 0);
   p.codes_vec = reinterpret_cast<uintptr_t>(codes) % 8 == 0 && (w.n == 1 || p.codes_stride % 8 == 0) &&
                 (w.batch == 1 || p.codes_batch % 8 == 0);
-  const dim3 grid((w.k + 127) / 128, (w.n + 127) / 128, w.batch);
+  const dim3 grid((w.k - 1) / 128 + 1, (w.n + 127) / 128, w.batch);
   const bool packed = w.w_type == DSA_BF16 && p.w_vec && w.k % 8 == 0;
   *launches += 1;
   return launch_overlapped(packed ? quantize_blocks_kernel<true> : quantize_blocks_kernel<false>, grid, 512, 0, 1, s, p);

@@ -277,3 +277,33 @@ def test_heads_share_a_matrix_or_their_rows(ctx):
     for x, xs, m, ms in ((a, asc, w[:1].expand_as(w), wsc[:1].expand_as(wsc)), (a[:, :1].expand_as(a), asc[:, :1].expand_as(asc), w, wsc)):
         check(ctx.project_fp8(x, xs, m, ms), x, xs, m, ms)
     ctx.get_error()
+
+
+def test_the_longest_rows(ctx):
+    """k up to the last block of 32 bits."""
+    k = 2 ** 31 - 16
+    a = torch.zeros(1, k, dtype=U8, device="cuda")
+    w = torch.zeros(1, k, dtype=U8, device="cuda")
+    at = torch.tensor([0, 127, 128, 2 ** 24 + 5, 2 ** 30, k - 129, k - 128, k - 1], device="cuda")
+    a[0, at] = 0x38            # 1.0
+    w[0, at] = 0x40            # 2.0
+    asc = torch.full((1, R.groups(k)), 0.5, device="cuda")
+    wsc = torch.full((1, R.groups(k)), 0.25, device="cuda")
+    wsc[0, at // 128] = 3.0
+    out = ctx.project_fp8(a, asc, w, wsc, out_dtype=F32)
+    assert ctx.project_on_tensor_cores(a, asc, w, wsc, out)
+    assert out.item() == 0.5 * 3.0 * 2.0 * 8
+    ctx.get_error()
+
+
+def test_the_longest_rows_quantised(ctx):
+    """One row: its groups of 128 columns are its blocks too."""
+    k = 2 ** 31 - 1
+    x = torch.zeros(1, k, dtype=BF16, device="cuda")
+    x[0, ::1000003] = 3.5
+    x[0, -5:] = -7.0
+    codes, scales = ctx.quantize_rows(x)
+    assert codes[0, -5:].tolist() == [0xFE] * 5 and scales[0, -1].item() == 7.0 / 448
+    w_codes, w_scales = ctx.quantize_weight(x)
+    assert torch.equal(codes, w_codes) and torch.equal(scales, w_scales)
+    assert int((codes != 0).sum()) == int((x != 0).sum())
