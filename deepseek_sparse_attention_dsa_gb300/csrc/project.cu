@@ -206,12 +206,17 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
     tc_fence_after();
   }
   if (p.split > 1) cluster_arrive_relaxed();   // (the barriers are fenced; nothing else is handed over)
-  grid_dependency_wait();
+  // (a row count in memory is an input; without one the first tile is known before the wait)
+  if (p.count) grid_dependency_wait();
   const int64_t live = live_rows(p.rows, p.count, p.per_row);
   const uint32_t m_tiles = static_cast<uint32_t>((live + NT - 1) / NT);
   const uint32_t n_tiles = (p.n + 127) / 128;
   const uint32_t tiles = m_tiles * n_tiles * p.batch;
   const uint32_t t0 = blockIdx.x >> p.split_log2, t_step = gridDim.x >> p.split_log2;
+  ProjectTile tile{};
+  if (t0 < tiles) tile = tile_at(t0, m_tiles, n_tiles, NT);
+  asm volatile("" ::"r"(tile.b), "r"(tile.n0), "l"(tile.m0));   // (not later)
+  if (!p.count) grid_dependency_wait();
   const uint32_t tmem_base = warp == 0 ? 0 : *tmem_slot;
 
   if (warp == 0) {
@@ -219,10 +224,11 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
     int st = 0;
     uint32_t ph = 0;
     bool ok = true;
+    bool fresh = true;   // stages that have not been filled are not waited for
     for (uint32_t t = t0; t < tiles && ok; t += t_step) {
-      const ProjectTile tile = tile_at(t, m_tiles, n_tiles, NT);
+      if (t != t0) tile = tile_at(t, m_tiles, n_tiles, NT);
       for (int kb = kb0; kb < kb1; kb += C::KC) {
-        if (!(ok = mbar_wait_warp(empty(st), ph ^ 1, aborted, p.err))) break;
+        if (!fresh && !(ok = mbar_wait_warp(empty(st), ph ^ 1, aborted, p.err))) break;
         if (elect_one()) {
           const int n = min(C::KC, kb1 - kb);
           mbar_arrive_expect_tx(full(st), n * C::BLOCK);
@@ -235,6 +241,7 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
         if (++st == C::STAGES) {
           st = 0;
           ph ^= 1;
+          fresh = false;
         }
       }
     }
@@ -291,9 +298,8 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
     int sg = 0;
     uint32_t sph = 0;
     bool ok = true;
-    if (t0 < tiles) load(tile_at(t0, m_tiles, n_tiles, NT), kb0);
+    if (t0 < tiles) load(tile, kb0);
     for (uint32_t t = t0; t < tiles && ok; t += t_step) {
-      const ProjectTile tile = tile_at(t, m_tiles, n_tiles, NT);
       for (int kb = kb0; kb < kb1; kb += C::GK) {
         if (!(ok = mbar_wait_warp(sempty(sg), sph ^ 1, aborted, p.err))) break;
         float *slot = reinterpret_cast<float *>(smem + C::OFF_S + sg * C::S_SLOT) + g * C::S_ROW + c0;
@@ -305,7 +311,7 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
           sph ^= 1;
         }
         if (kb + C::GK < kb1) load(tile, kb + C::GK);
-        else if (t + t_step < tiles) load(tile_at(t + t_step, m_tiles, n_tiles, NT), kb0);
+        else if (t + t_step < tiles) load(tile = tile_at(t + t_step, m_tiles, n_tiles, NT), kb0);
       }
     }
     __syncwarp();
@@ -319,7 +325,6 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
     uint32_t sph = 0, i = 0;
     bool ok = true;
     for (uint32_t t = t0; t < tiles && ok; t += t_step) {
-      const ProjectTile tile = tile_at(t, m_tiles, n_tiles, NT);
       float acc[C::COLS];
 #pragma unroll
       for (int c = 0; c < C::COLS; ++c) acc[c] = 0.f;
@@ -366,6 +371,7 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
         }
       }
       if (!ok) break;
+      if (t != t0) tile = tile_at(t, m_tiles, n_tiles, NT);
       const int cols = static_cast<int>(min(live - tile.m0, static_cast<int64_t>(NT)));   // live tokens
       if (p.split == 1) {
         const int n = tile.n0 + nl;
@@ -561,13 +567,20 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
     }
     if (ctas > 1) cluster_arrive_relaxed();
   }
-  grid_dependency_wait();
+  // (a row count in memory is an input; without one the first tile is known before the wait)
+  if (p.count) grid_dependency_wait();
   const int64_t live = live_rows(p.rows, p.count, p.per_row);
   const int m_tiles = static_cast<int>((live + C::M - 1) / C::M);
   const int n_tiles = (p.n + N - 1) / N;
   const int tiles = m_tiles * n_tiles * p.batch;
   const int log2 = kPair ? 1 : p.split_log2;
   const int t0 = blockIdx.x >> log2, t_step = gridDim.x >> log2;
+  ProjectTile tile{};
+  if (N == 128) {   // (at 256 columns there are no registers to keep it in)
+    if (t0 < tiles) tile = rows_tile_at(t0, m_tiles, n_tiles, C::M, C::N);
+    asm volatile("" ::"r"(tile.b), "r"(tile.n0), "l"(tile.m0));   // (not later)
+  }
+  if (!p.count) grid_dependency_wait();
   const uint32_t tmem_base = !kPair && warp == 0 ? 0 : *tmem_slot;
 
   if (warp < 4) {
@@ -577,11 +590,12 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
       int st = 0;
       uint32_t ph = 0;
       bool ok = true;
+      bool fresh = true;   // stages that have not been filled are not waited for
       for (int t = t0; t < tiles && ok; t += t_step) {
-        const ProjectTile tile = rows_tile_at(t, m_tiles, n_tiles, C::M, C::N);
+        if (N != 128 || t != t0) tile = rows_tile_at(t, m_tiles, n_tiles, C::M, C::N);
         const int m = static_cast<int>(tile.m0) + half * 128, n = tile.n0 + half * C::W_ROWS;
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!(ok = mbar_wait_warp(empty(st), ph ^ 1, aborted, p.err))) break;
+          if (!fresh && !(ok = mbar_wait_warp(empty(st), ph ^ 1, aborted, p.err))) break;
           if (elect_one()) {
             const uint32_t dst = sbase + st * C::STAGE;
             if (kPair) {   // the first CTA's barrier counts both CTAs' bytes
@@ -599,6 +613,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
           if (++st == C::STAGES) {
             st = 0;
             ph ^= 1;
+            fresh = false;
           }
         }
       }
@@ -643,7 +658,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
       uint32_t sph = 0;
       bool ok = true;
       for (int t = t0; t < tiles && ok; t += t_step) {
-        const ProjectTile tile = rows_tile_at(t, m_tiles, n_tiles, C::M, C::N);
+        if (N != 128 || t != t0) tile = rows_tile_at(t, m_tiles, n_tiles, C::M, C::N);
         const int m0 = static_cast<int>(tile.m0) + half * 128;
         for (int kb = kb0; kb < kb1; kb += C::GK) {
           if (!(ok = mbar_wait_warp(sempty(sg), sph ^ 1, aborted, p.err))) break;
@@ -724,7 +739,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
         }
       }
       if (!ok) break;
-      const ProjectTile tile = rows_tile_at(t, m_tiles, n_tiles, C::M, C::N);
+      tile = rows_tile_at(t, m_tiles, n_tiles, C::M, C::N);
       const int64_t mw = tile.m0 + half * 128 + quad * 32;   // the warp's first token
       const int nw = tile.n0 + col0;                         // and first column
       const uint32_t stage_addr = sbase + C::OFF_OUT + (warp - 4) * C::OUT_WARP;
