@@ -49,7 +49,7 @@ namespace {
 struct ProjectParams {
   CUtensorMap tm_a;   // token codes as [rows][batch][k], box {128, 1, NT}, 128-byte swizzle
   CUtensorMap tm_w;   // weight codes as [batch][n][k], box {128, 128, 1}, 128-byte swizzle
-  CUtensorMap tm_out; // out as [rows][batch][n], box {128 bytes, 1, 32}, 128-byte swizzle (pair kernel, where out_tma)
+  CUtensorMap tm_out; // out as [rows][batch][n], box {128 bytes, 1, 32}, 128-byte swizzle (where out_tma)
   const uint8_t *a, *w;
   const float *a_scale, *w_scale;
   void *out;
@@ -60,7 +60,7 @@ struct ProjectParams {
   int32_t n, batch, per_row, out_type;
   int32_t k, kbs, split, split_log2;   // kbs: blocks of 128 of k; split: CTAs (pairs) of a cluster that share them
   bool out_vec;   // rows of out start on 16 bytes
-  bool out_tma;   // and every row is live: whole boxes are stored by TMA
+  bool out_tma;   // TMA takes them: it stores whole boxes of live rows
 };
 
 constexpr int kMaxSplit = 8;
@@ -488,19 +488,30 @@ __device__ __forceinline__ ProjectTile rows_tile_at(int t, int m_tiles, int n_ti
 // 32 rows of 128 bytes of columns from a swizzled box of shared memory to out, by one warp.
 __device__ __noinline__ void write_box(const ProjectParams &p, const uint8_t *box, int lane, int es, int64_t m0,
                                        int64_t live, int b, int n0) {
-  const int chunk = lane & 7, per = 16 / es;
+  const int chunk = lane & 7, per = 16 / es, row0 = lane / 8;
   const int n = n0 + chunk * per;
-  for (int row = lane / 8; row < 32 && m0 + row < live; row += 4) {
-    if (n >= p.n) break;
-    const uint4 u = *reinterpret_cast<const uint4 *>(box + sw128_offset(row, chunk));
-    const int64_t at = (m0 + row) * p.out_stride + b * p.out_batch + n;
-    if (p.out_vec && n + per <= p.n) {
-      *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + at * es) = u;
-    } else {
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-      for (int i = 0; i < per && n + i < p.n; ++i) {
-        if (es == 2) static_cast<uint16_t *>(p.out)[at + i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
-        else static_cast<uint32_t *>(p.out)[at + i] = w[i];
+  if (n >= p.n) return;
+  uint4 u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = *reinterpret_cast<const uint4 *>(box + sw128_offset(row0 + 4 * i, chunk));
+  uint8_t *out = static_cast<uint8_t *>(p.out) + ((m0 + row0) * p.out_stride + b * p.out_batch + n) * es;
+  const int64_t step = 4 * p.out_stride * es;
+  const bool whole = p.out_vec && n + per <= p.n;
+#pragma unroll
+  for (int i = 0; i < 8; ++i, out += step) {
+    if (m0 + row0 + 4 * i >= live) return;
+    if (whole) {
+      *reinterpret_cast<uint4 *>(out) = u[i];
+      continue;
+    }
+    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (es == 4) {
+        if (n + e < p.n) reinterpret_cast<uint32_t *>(out)[e] = w[e];
+      } else {
+        if (n + 2 * e < p.n) reinterpret_cast<uint16_t *>(out)[2 * e] = static_cast<uint16_t>(w[e]);
+        if (n + 2 * e + 1 < p.n) reinterpret_cast<uint16_t *>(out)[2 * e + 1] = static_cast<uint16_t>(w[e] >> 16);
       }
     }
   }
@@ -605,8 +616,8 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
               tma_load_3d_pair(dst + C::A_BYTES, &p.tm_w, kb * 128, n, tile.b, bar);
             } else {
               mbar_arrive_expect_tx(full(st), C::STAGE);
-              tma_load_3d(dst, &p.tm_a, kb * 128, tile.b, m, full(st));
               tma_load_3d(dst + C::A_BYTES, &p.tm_w, kb * 128, n, tile.b, full(st));
+              tma_load_3d(dst, &p.tm_a, kb * 128, tile.b, m, full(st));
             }
           }
           __syncwarp();
@@ -784,7 +795,9 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
         if (es == 2 ? c0 + 32 < C::COLS : c0 % 64 == 0) continue;
         const int n = es == 2 ? nw : nw + c0 - 32, per = 128 / es;   // the first box's first column, a box's columns
         const bool two = es == 4 || C::COLS == 128;
-        if (p.out_tma) {
+        // (what is past p.rows TMA drops, what is past the live rows it would write;
+        // the vote makes the branch uniform for the compiler too)
+        if (__all_sync(0xffffffffu, p.out_tma && (p.count == nullptr || mw + 32 <= live))) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0 && mw < live) {
@@ -910,7 +923,7 @@ cudaError_t run_rows(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &
   using C = RowsTraits<kPair, N>;
   if (!encode_operands(g, p, 128, C::W_ROWS)) return cudaErrorInvalidValue;
   p.split = split, p.split_log2 = split == 8 ? 3 : split / 2;
-  if (p.out_vec && p.count == nullptr) {
+  if (p.out_vec) {
     const bool bf16 = g.out_type == DSA_BF16;
     const int64_t es = bf16 ? 2 : 4;
     const uint64_t dims[3] = {static_cast<uint64_t>(g.n), static_cast<uint64_t>(g.batch), static_cast<uint64_t>(g.rows)};

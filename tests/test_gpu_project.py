@@ -307,3 +307,22 @@ def test_the_longest_rows_quantised(ctx):
     w_codes, w_scales = ctx.quantize_weight(x)
     assert torch.equal(codes, w_codes) and torch.equal(scales, w_scales)
     assert int((codes != 0).sum()) == int((x != 0).sum())
+
+
+@pytest.mark.parametrize("n", [136, 700, 20000])
+def test_padding_begins_at_any_row(ctx, n):
+    """Inside, at the start and at the end of the 32 rows that are stored together, in whole and in cut columns."""
+    cap = 300
+    t = make(14, cap, n, 160)
+    plan = ctx.plan_capturable(cap, cap, cap, 1)
+    spans = torch.tensor([[1, 0, 0, 0, 1, 0]] * cap, dtype=torch.int32, device="cuda")   # one token each, all in page 0
+    pages = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for dt in (BF16, F32):
+        full = ctx.project_fp8(*t, out_dtype=dt)
+        for live in (1, 31, 32, 33, 100, 128, 160, 256, 289, 299, 300):
+            count = torch.tensor([live], dtype=torch.int32, device="cuda")
+            ctx.plan_update(plan, count, spans, pages)
+            out = torch.full((cap, n), 77.0, dtype=dt, device="cuda")
+            ctx.project_fp8(*t, out=out, plan=plan)
+            assert torch.equal(out[:live], full[:live]) and (out[live:] == 77).all()
+    ctx.get_error()
