@@ -984,18 +984,18 @@ int clusters_at_once(const dsa_ctx *ctx, int ctas) {
 // and the CTAs that split a tile's k: the least of what the measured times of a
 // block of k and of a tile's end on each (us) make of the blocks that the busiest
 // CTA gets.  Measured on either side of its choices (us a call): 128 x 8192 x
-// 4096 10.6 with {128, 2 CTAs}, 11.8 with {64}, 13.3 with {128}; 256 x 8192 x
-// 4096 13.8 with {256}, 13.9 with {128}, 17.3 with {257}; 1024 x 4096 x 4096 18.6
-// with {257}, 22.7 with {256}; 16 x 8192 x 2048 4.7 with {16, 2}, 5.4 with {16}.
-// Of 35 sizes it misses the best by 5 to 8% in three, by 1% or less in the others.
+// 4096 9.6 with {128, 2 CTAs}, 11.4 with {64}, 12.5 with {128}; 256 x 8192 x
+// 4096 13.1 with {128}, 13.3 with {256}, 16.9 with {257}; 1024 x 4096 x 4096 18.3
+// with {257}, 22.0 with {128}; 16 x 8192 x 2048 4.5 with {16, 2}, 5.0 with {16}.
+// Of 35 sizes it misses the best by 2 to 4% in three, by 1% or less in the others.
 void choose(const dsa_ctx *ctx, const dsa_project_t &g, int *nt, int *split) {
   struct Form {
     int nt, m, n, ctas, max_split;
     float block, tile;
   };
-  static const Form forms[] = {{16, 16, 128, 1, 8, 0.19f, 0.2f},  {32, 32, 128, 1, 8, 0.21f, 0.4f},
-                               {64, 64, 128, 1, 8, 0.26f, 0.7f},  {128, 128, 128, 1, 2, 0.33f, 0.5f},
-                               {256, 256, 128, 2, 1, 0.29f, 0.5f}, {257, 256, 256, 2, 1, 0.40f, 0.9f}};
+  static const Form forms[] = {{16, 16, 128, 1, 8, 0.18f, 0.23f},   {32, 32, 128, 1, 8, 0.18f, 0.52f},
+                               {64, 64, 128, 1, 8, 0.31f, 0.62f},   {128, 128, 128, 1, 2, 0.32f, 0.51f},
+                               {256, 256, 128, 2, 1, 0.32f, 0.60f}, {257, 256, 256, 2, 1, 0.42f, 0.70f}};
   const int kbs = (g.k - 1) / 128 + 1;
   float best = 0.f;
   *nt = 0;
