@@ -15,9 +15,9 @@
 // project_tc_kernel, few rows: a tile is 128 weight rows (the MMA's 128 lanes) by
 // NT = 16, 32 or 64 tokens (its columns); two helper warps put s for the tile's
 // tokens into shared memory ahead of the epilogue.  Bound by the weights' bytes:
-// 16 x 8192 x 8192 takes 13.4 us on one GB300, 67 MB at 5.0 TB/s, of which some
+// 16 x 8192 x 8192 takes 13.3 us on one GB300, 67 MB at 5.0 TB/s, of which some
 // 3 us are the first loads' latency and the last block's way out (1 x 8192 x
-// 2048: 4.3 us).
+// 2048: 4.0 us).
 //
 // project_rows_kernel, more rows: tokens are the lanes (see there).
 //
@@ -63,17 +63,19 @@ struct ProjectParams {
   bool out_tma;   // TMA takes them: it stores whole boxes of live rows
 };
 
+__device__ __forceinline__ float4 ld_shared4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
 constexpr int kMaxSplit = 8;
 // S partial sums of four values, `stride` bytes apart in this CTA's shared memory, in rank order.
 __device__ __forceinline__ float4 sum_partials(uint32_t at, uint32_t stride, int split) {
   float4 v[kMaxSplit];
 #pragma unroll
   for (int r = 0; r < kMaxSplit; ++r)
-    if (r < split)
-      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(v[r].x), "=f"(v[r].y), "=f"(v[r].z), "=f"(v[r].w)
-                   : "r"(at + r * stride)
-                   : "memory");
+    if (r < split) v[r] = ld_shared4(at + r * stride);
   float4 sum = v[0];
 #pragma unroll
   for (int r = 1; r < kMaxSplit; ++r)
@@ -427,7 +429,10 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
 //   kPair: a pair of CTAs (cta_group::2) on 256 tokens, 128 lanes in each, by N
 //   weight rows; each CTA brings its tokens and half of the weights, so at N =
 //   256 a block of k costs a CTA 32 KB for 128 x 256 x 128 products.
-//   else: one CTA on 128 tokens by 128 weight rows, or two on the halves of k.
+//   else: one CTA on 128 tokens by 128 weight rows.
+//   SPLIT 2: two CTAs, or two pairs at N = 128, on the halves of a tile's k.  (Pairs
+//   at N = 256 were slower split than whole: 512 x 4096 x 4096 14.4 us against 11.7
+//   on smaller tiles; the partial sums of a CTA are then 64 KB.)
 //
 // Bounds, at 8192 x 8192 x 4096 (197 us, 2.79 PFLOP/s; 215 us when repeated, the
 // card then at its power limit and 1.75 GHz): a block's 512 cycles of MMA, its
@@ -461,7 +466,7 @@ struct RowsTraits {
   static constexpr int NBAR = 2 * STAGES + 2 * AB + 2 * SG + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
-  static_assert(SMEM <= 227 * 1024 && (kPair || 32 * COLS * 4 == OUT_WARP), "shared memory");
+  static_assert(SMEM <= 227 * 1024 && (COLS == 128 || 32 * COLS * 4 == OUT_WARP), "shared memory");
   // registers: 384 threads launch with 168 each (64,512); the split keeps that sum
   static constexpr int REGS_HELP = N == 256 ? 56 : 64, REGS_EPI = N == 256 ? 224 : 216;
   static_assert(128 * REGS_HELP + 32 * EPI * REGS_EPI <= 384 * 168, "registers");
@@ -517,7 +522,7 @@ __device__ __noinline__ void write_box(const ProjectParams &p, const uint8_t *bo
   }
 }
 
-template <bool kPair, int N>
+template <bool kPair, int N, int SPLIT>
 __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_constant__ ProjectParams p) {
   using C = RowsTraits<kPair, N>;
   extern __shared__ uint8_t smem_raw[];
@@ -537,11 +542,13 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
 
   const int warp = threadIdx.x / 32;
   const int lane = lane_id();
-  // the cluster: a pair, or the CTAs that split a tile's k
-  const int ctas = kPair ? 2 : p.split;
-  const int rank = ctas > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int half = kPair ? rank : 0;   // of the tile's tokens
-  const int kb0 = kPair ? 0 : first_block(p, rank), kb1 = kPair ? p.kbs : first_block(p, rank + 1);
+  // the cluster: the CTAs, or pairs of neighbouring CTAs, that split a tile's k
+  constexpr int CTAS = (kPair ? 2 : 1) * SPLIT, LOG2 = CTAS / 2;   // (1, 2 or 4)
+  const int rank = CTAS > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int part = SPLIT > 1 ? (kPair ? rank / 2 : rank) : 0;      // of the k blocks
+  const int lead = kPair && SPLIT > 1 ? rank & 2 : 0;              // the pair's first CTA
+  const int half = kPair ? rank - lead : 0;                        // of the tile's tokens
+  const int kb0 = SPLIT > 1 ? first_block(p, part) : 0, kb1 = SPLIT > 1 ? first_block(p, part + 1) : p.kbs;
 
   launch_dependents();
   if (warp == 0) {
@@ -549,7 +556,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
     if (lane < C::NBAR) mbar_init(bar0 + 8u * lane, barrier_arrivals<C>(lane, kPair ? 2 : 1));
     if (lane == 0) *abort_flag = 0;
     fence_mbar_init();
-    if (!kPair && ctas == 2 && lane == C::NBAR - 1) mbar_arrive_expect_tx(partfull, C::EPI / 2 * C::OUT_WARP);
+    if (SPLIT > 1 && lane == C::NBAR - 1) mbar_arrive_expect_tx(partfull, C::EPI / 2 * C::OUT_WARP);
   }
   if (warp == 1) {
     if (kPair) {
@@ -576,7 +583,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
       named_bar_sync(1, C::THREADS);
       tc_fence_after();
     }
-    if (ctas > 1) cluster_arrive_relaxed();
+    if (SPLIT > 1) cluster_arrive_relaxed();
   }
   // (a row count in memory is an input; without one the first tile is known before the wait)
   if (p.count) grid_dependency_wait();
@@ -584,14 +591,16 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
   const int m_tiles = static_cast<int>((live + C::M - 1) / C::M);
   const int n_tiles = (p.n + N - 1) / N;
   const int tiles = m_tiles * n_tiles * p.batch;
-  const int log2 = kPair ? 1 : p.split_log2;
-  const int t0 = blockIdx.x >> log2, t_step = gridDim.x >> log2;
+  const int t0 = blockIdx.x >> LOG2;
+  // (a cluster that splits k has one tile.  Said so to the compiler, pairs take
+  // 9.4 us for 1031 x 704 x 5120, else 9.7; CTAs 10.2 and 9.9)
+  auto next = [&](int t) { return SPLIT > 1 && kPair ? tiles : t + static_cast<int>(gridDim.x >> LOG2); };
   ProjectTile tile{};
   if (N == 128) {   // (at 256 columns there are no registers to keep it in)
     if (t0 < tiles) tile = rows_tile_at(t0, m_tiles, n_tiles, C::M, C::N);
     asm volatile("" ::"r"(tile.b), "r"(tile.n0), "l"(tile.m0));   // (not later)
   }
-  if (kPair) cluster_wait();   // the other CTA's barriers and tensor memory are ready
+  if (kPair) cluster_wait();   // the others' barriers and tensor memory are ready
   if (!p.count) grid_dependency_wait();
   const uint32_t tmem_base = !kPair && warp == 0 ? 0 : *tmem_slot;
 
@@ -603,7 +612,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
       uint32_t ph = 0;
       bool ok = true;
       bool fresh = true;   // stages that have not been filled are not waited for
-      for (int t = t0; t < tiles && ok; t += t_step) {
+      for (int t = t0; t < tiles && ok; t = next(t)) {
         if (N != 128 || t != t0) tile = rows_tile_at(t, m_tiles, n_tiles, C::M, C::N);
         const int m = static_cast<int>(tile.m0) + half * 128, n = tile.n0 + half * C::W_ROWS;
         for (int kb = kb0; kb < kb1; ++kb) {
@@ -611,8 +620,8 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
           if (elect_one()) {
             const uint32_t dst = sbase + st * C::STAGE;
             if (kPair) {   // the first CTA's barrier counts both CTAs' bytes
-              if (rank == 0) mbar_arrive_expect_tx(full(st), 2 * C::STAGE);
-              const uint32_t bar = map_to_cta(full(st), 0);
+              if (half == 0) mbar_arrive_expect_tx(full(st), 2 * C::STAGE);
+              const uint32_t bar = map_to_cta(full(st), lead);
               tma_load_3d_pair(dst, &p.tm_a, kb * 128, tile.b, m, bar);
               tma_load_3d_pair(dst + C::A_BYTES, &p.tm_w, kb * 128, n, tile.b, bar);
             } else {
@@ -640,7 +649,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
     } else if (warp == 1 && half == 0) {
       // ---------------------------------------------------------- MMA issuer (a pair's first CTA)
       const uint64_t desc0 = smem_desc(sbase, 16, 1024, kSwizzle128);
-      const uint32_t blocks = static_cast<uint32_t>(t0 < tiles ? (tiles - t0 + t_step - 1) / t_step : 0) * (kb1 - kb0);
+      const uint32_t blocks = (t0 >= tiles ? 0u : 1u + (tiles - 1 - t0) / (gridDim.x >> LOG2)) * (kb1 - kb0);
 #pragma unroll 1
       for (uint32_t i = 0; i < blocks; ++i) {   // the k blocks of all its tiles
         const uint32_t st = i % C::STAGES, ab = i % C::AB;
@@ -652,8 +661,8 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
           for (int k = 0; k < 4; ++k)   // K = 32 codes (32 bytes) per step
             mma_f8<kPair>(tmem_base + ab * N, ad + 2 * k, wd + 2 * k, C::IDESC, k != 0 ? 1u : 0u);
           if (kPair) {
-            mma_commit_pair(empty(st), 3);
-            mma_commit_pair(afull(ab), 3);
+            mma_commit_pair(empty(st), 3 << lead);
+            mma_commit_pair(afull(ab), 3 << lead);
           } else {
             mma_commit(empty(st));
             mma_commit(afull(ab));
@@ -669,7 +678,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
       int sg = 0;
       uint32_t sph = 0;
       bool ok = true;
-      for (int t = t0; t < tiles && ok; t += t_step) {
+      for (int t = t0; t < tiles && ok; t = next(t)) {
         if (N != 128 || t != t0) tile = rows_tile_at(t, m_tiles, n_tiles, C::M, C::N);
         const int m0 = static_cast<int>(tile.m0) + half * 128;
         for (int kb = kb0; kb < kb1; kb += C::GK) {
@@ -705,8 +714,8 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
     int ab = 0, sg = 0;
     uint32_t aph = 0, sph = 0;
     bool ok = true;
-    if (!kPair && ctas > 1) cluster_wait();   // the other CTA is there
-    for (int t = t0; t < tiles && ok; t += t_step) {
+    if (!kPair && SPLIT > 1) cluster_wait();   // the other CTA is there
+    for (int t = t0; t < tiles && ok; t = next(t)) {
       float acc[C::COLS];
 #pragma unroll
       for (int c = 0; c < C::COLS; ++c) acc[c] = 0.f;
@@ -731,7 +740,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
               tc_fence_before();
               __syncwarp();
               if (lane == 0) {
-                if (kPair) mbar_arrive_remote_relaxed(map_to_cta(aempty(ab), 0));
+                if (kPair) mbar_arrive_remote_relaxed(map_to_cta(aempty(ab), lead));
                 else mbar_arrive_relaxed(aempty(ab));
               }
             }
@@ -755,12 +764,15 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
       const int64_t mw = tile.m0 + half * 128 + quad * 32;   // the warp's first token
       const int nw = tile.n0 + col0;                         // and first column
       const uint32_t stage_addr = sbase + C::OFF_OUT + (warp - 4) * C::OUT_WARP;
-      if (!kPair && ctas == 2) {
-        // two CTAs share the tile (one tile a cluster): rank r finishes tokens
-        // 64 r .. 64 r + 63.  A warp of the other tokens sends its sums to the same
-        // warp's staging in the other CTA, four columns of its 32 rows at a time.
-        if (quad / 2 != rank) {
-          const uint32_t to = map_to_cta(stage_addr + lane * 16, rank ^ 1), bar = map_to_cta(partfull, rank ^ 1);
+      if (SPLIT > 1) {
+        // two CTAs, or pairs, share the tile (one tile a cluster): part r finishes
+        // what its CTAs hold of lanes 64 r .. 64 r + 63.  A warp of the other lanes
+        // sends its sums into the staging of the same warp of the other part, four
+        // columns of its 32 rows at a time.
+        const uint32_t at = stage_addr + lane * 16;
+        if (quad / 2 != part) {
+          const int other = rank ^ (kPair ? 2 : 1);
+          const uint32_t to = map_to_cta(at, other), bar = map_to_cta(partfull, other);
 #pragma unroll
           for (int c = 0; c < C::COLS; c += 4) st_async4(to + c * 128, acc + c, bar);
           break;
@@ -768,7 +780,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
         if (!mbar_wait_warp(partfull, 0, aborted, p.err)) break;
 #pragma unroll
         for (int c = 0; c < C::COLS; c += 4) {
-          const float4 v = *reinterpret_cast<const float4 *>(stage_out + c * 128 + lane * 16);
+          const float4 v = ld_shared4(at + c * 128);
           acc[c] += v.x, acc[c + 1] += v.y, acc[c + 2] += v.z, acc[c + 3] += v.w;
         }
         __syncwarp();   // the staging is read before it is filled again
@@ -822,7 +834,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
   if (kPair) {
     __syncwarp();
     cluster_arrive_relaxed();
-    cluster_wait();   // neither CTA leaves while the other may signal it or read its operands
+    cluster_wait();   // no CTA leaves while another may signal it or read its operands
   }
   tc_fence_before();
   __syncthreads();
@@ -831,7 +843,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
     if (kPair) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
     else tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
-  if (!kPair && ctas > 1) linger_if_aborted(aborted);
+  if (SPLIT > 1) linger_if_aborted(aborted);
 }
 
 __device__ __forceinline__ float e4m3_value(uint8_t c) {
@@ -920,11 +932,11 @@ int64_t tiles_of(const dsa_project_t &g, int M, int N) {
   return (g.rows + M - 1) / M * ((static_cast<int64_t>(g.n) + N - 1) / N) * g.batch;
 }
 
-template <bool kPair, int N>
-cudaError_t run_rows(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &p, int split, cudaStream_t s) {
+template <bool kPair, int N, int SPLIT>
+cudaError_t run_rows(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &p, cudaStream_t s) {
   using C = RowsTraits<kPair, N>;
   if (!encode_operands(g, p, 128, C::W_ROWS)) return cudaErrorInvalidValue;
-  p.split = split, p.split_log2 = split == 8 ? 3 : split / 2;
+  p.split = SPLIT, p.split_log2 = SPLIT / 2;
   if (p.out_vec) {
     const bool bf16 = g.out_type == DSA_BF16;
     const int64_t es = bf16 ? 2 : 4;
@@ -936,10 +948,10 @@ cudaError_t run_rows(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &
                                 p.out, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
   }
   const int64_t tiles = tiles_of(g, C::M, N);
-  const int cluster = kPair ? 2 : split;
-  const int64_t grid = split > 1 ? tiles * split : cluster * std::min<int64_t>(tiles, ctx->num_sms / cluster);
+  const int cluster = (kPair ? 2 : 1) * SPLIT;
+  const int64_t grid = SPLIT > 1 ? tiles * cluster : cluster * std::min<int64_t>(tiles, ctx->num_sms / cluster);
   static std::atomic<uint64_t> smem_limit_set{0};
-  return launch(ctx, project_rows_kernel<kPair, N>, C::THREADS, C::SMEM, grid, cluster, smem_limit_set, p, s);
+  return launch(ctx, project_rows_kernel<kPair, N, SPLIT>, C::THREADS, C::SMEM, grid, cluster, smem_limit_set, p, s);
 }
 
 template <int NT>
@@ -956,7 +968,7 @@ cudaError_t run_tc(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &p,
 // Clusters of `ctas` CTAs, one to an SM, that the device holds at once: less than
 // its SMs allow, as a cluster lies within a group of them (a GB300 with 152 SMs
 // holds 36 of four and 15 of eight; 48 x 2048 x 8192 on 16 clusters of eight took
-// 12.2 us, on as many of four 7.8).  Asked of the driver once a device.
+// 11.1 us, on as many of four 7.4).  Asked of the driver once a device.
 int clusters_at_once(const dsa_ctx *ctx, int ctas) {
   if (ctas <= 2) return ctx->num_sms / ctas;
   static std::atomic<int> known[64][2];
@@ -983,21 +995,22 @@ int clusters_at_once(const dsa_ctx *ctx, int ctas) {
 
 // The kernel (tokens a tile: 16, 32, 64 with weights on the lanes; 128 on one
 // CTA and 256 on a pair with tokens on the lanes, 257 the pair with 256 columns)
-// and the CTAs that split a tile's k: the least of what the measured times of a
-// block of k and of a tile's end on each (us) make of the blocks that the busiest
-// CTA gets.  Measured on either side of its choices (us a call): 128 x 8192 x
-// 4096 9.6 with {128, 2 CTAs}, 11.4 with {64}, 12.5 with {128}; 256 x 8192 x
-// 4096 13.1 with {128}, 13.3 with {256}, 16.9 with {257}; 1024 x 4096 x 4096 18.3
-// with {257}, 22.0 with {128}; 16 x 8192 x 2048 4.5 with {16, 2}, 5.0 with {16}.
-// Of 35 sizes it comes within 1.5% of the best form in every one.
+// and the CTAs, or pairs, that split a tile's k: the least of what the measured
+// times of a block of k, of a tile's end, of a pair's start and of a split (us) make
+// of the blocks that the busiest CTA gets.  Measured on either side of its choices (us a
+// call): 128 x 8192 x 4096 9.5 with {128, 2 CTAs}, 11.4 with {64}, 12.5 with {128};
+// 200 x 4096 x 4096 8.2 with {256, 2 pairs}, 8.8 with {128, 2 CTAs}, 10.4 with {64};
+// 256 x 8192 x 4096 13.0 with {256}, 13.1 with {128}, 16.6 with {257}; 1024 x 4096 x
+// 4096 18.0 with {257}, 21.7 with {128}; 16 x 8192 x 2048 4.5 with {16, 2}, 5.0 with
+// {16}.  Of 35 sizes it comes within 1.5% of the best form in every one.
 void choose(const dsa_ctx *ctx, const dsa_project_t &g, int *nt, int *split) {
   struct Form {
     int nt, m, n, ctas, max_split;
-    float block, tile;
+    float block, tile, start;
   };
-  static const Form forms[] = {{16, 16, 128, 1, 8, 0.18f, 0.23f},   {32, 32, 128, 1, 8, 0.18f, 0.52f},
-                               {64, 64, 128, 1, 8, 0.31f, 0.62f},   {128, 128, 128, 1, 2, 0.32f, 0.51f},
-                               {256, 256, 128, 2, 1, 0.30f, 0.58f}, {257, 256, 256, 2, 1, 0.43f, 0.60f}};
+  static const Form forms[] = {{16, 16, 128, 1, 8, 0.17f, 0.18f, 0.f},    {32, 32, 128, 1, 8, 0.18f, 0.52f, 0.f},
+                               {64, 64, 128, 1, 8, 0.26f, 0.91f, 0.f},    {128, 128, 128, 1, 2, 0.31f, 0.52f, 0.f},
+                               {256, 256, 128, 2, 2, 0.27f, 0.52f, 0.16f}, {257, 256, 256, 2, 1, 0.46f, 0.50f, 0.15f}};
   const int kbs = (g.k - 1) / 128 + 1;
   float best = 0.f;
   *nt = 0;
@@ -1006,9 +1019,9 @@ void choose(const dsa_ctx *ctx, const dsa_project_t &g, int *nt, int *split) {
     const int64_t tiles = tiles_of(g, f.m, f.n), cap = ctx->num_sms / f.ctas;
     if (f.m >= 128 && tiles >= INT32_MAX / 8) continue;   // (32-bit tile counts)
     for (int s = 1; s <= f.max_split; s *= 2) {
-      if (s > 1 && (kbs < 2 * s || tiles > clusters_at_once(ctx, s))) break;
+      if (s > 1 && (kbs < 2 * s || tiles > clusters_at_once(ctx, s * f.ctas))) break;
       const int64_t per_cta = s > 1 ? 1 : (tiles + cap - 1) / cap;
-      const float t = static_cast<float>(per_cta) * (((kbs + s - 1) / s) * f.block + f.tile) + (s > 1 ? 0.4f : 0.f);
+      const float t = static_cast<float>(per_cta) * (((kbs + s - 1) / s) * f.block + f.tile) + f.start + (s > 1 ? 0.64f : 0.f);
       if (*nt == 0 || t < best) best = t, *nt = f.nt, *split = s;
     }
   }
@@ -1057,9 +1070,9 @@ cudaError_t launch_project_fp8(const dsa_ctx *ctx, const dsa_project_t &g, const
       case 16: return run_tc<16>(ctx, g, p, split, s);
       case 32: return run_tc<32>(ctx, g, p, split, s);
       case 64: return run_tc<64>(ctx, g, p, split, s);
-      case 128: return run_rows<false, 128>(ctx, g, p, split, s);
-      case 256: return run_rows<true, 128>(ctx, g, p, 1, s);
-      default: return run_rows<true, 256>(ctx, g, p, 1, s);
+      case 128: return split > 1 ? run_rows<false, 128, 2>(ctx, g, p, s) : run_rows<false, 128, 1>(ctx, g, p, s);
+      case 256: return split > 1 ? run_rows<true, 128, 2>(ctx, g, p, s) : run_rows<true, 128, 1>(ctx, g, p, s);
+      default: return run_rows<true, 256, 1>(ctx, g, p, s);
     }
   }
   const dim3 grid(static_cast<unsigned>((g.rows + 63) / 64), (g.n + 63) / 64, g.batch);

@@ -326,3 +326,14 @@ def test_padding_begins_at_any_row(ctx, n):
             ctx.project_fp8(*t, out=out, plan=plan)
             assert torch.equal(out[:live], full[:live]) and (out[live:] == 77).all()
     ctx.get_error()
+
+
+@pytest.mark.parametrize("rows,n,k", [(200, 4096, 4096), (1031, 704, 5120), (130, 200, 1040), (300, 520, 3000), (256, 2048, 1152)])
+def test_pairs_that_split_k(ctx, rows, n, k):
+    """Few tiles of many tokens: two pairs of CTAs share one, with even and odd numbers of blocks."""
+    t = make(rows + n, rows, n, k)
+    for dt in (BF16, F32):
+        out = ctx.project_fp8(*t, out_dtype=dt)
+        check(out, *t)
+        assert torch.equal(out, ctx.project_fp8(*t, out_dtype=dt))
+    ctx.get_error()
