@@ -337,3 +337,35 @@ def test_pairs_that_split_k(ctx, rows, n, k):
         check(out, *t)
         assert torch.equal(out, ctx.project_fp8(*t, out_dtype=dt))
     ctx.get_error()
+
+
+def test_threads_share_a_context(ctx):
+    """Calls from several threads at once, each on a stream of its own, from the first call of a size on."""
+    import threading
+    sizes = [(1, 1032, 2048), (48, 1032, 2064), (200, 1032, 2080), (600, 1032, 2096)]
+    ts = [make(30 + i, *s) for i, s in enumerate(sizes)]
+    x = torch.randn(70, 1032, device="cuda").to(BF16)
+    got, failed = {}, []
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for j in range(20):
+                    a = (i + j) % len(ts)
+                    got[i, j] = a, ctx.project_fp8(*ts[a], out_dtype=F32), ctx.rmsnorm(x, None), ctx.quantize_rows(x)
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    outs = [ctx.project_fp8(*t, out_dtype=F32) for t in ts]
+    y, (codes, scales) = ctx.rmsnorm(x, None), ctx.quantize_rows(x)
+    for a, out, yi, (ci, si) in got.values():
+        assert torch.equal(out, outs[a]) and torch.equal(yi, y) and torch.equal(ci, codes) and torch.equal(si, scales)
+    ctx.get_error()
