@@ -372,7 +372,10 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
           sph ^= 1;
         }
       }
-      if (!ok) break;
+      if (!ok) {
+        if (p.split > 1) named_bar_arrive(2, 32 * C::EPI);   // the others may be on their way there
+        break;
+      }
       if (t != t0) tile = tile_at(t, m_tiles, n_tiles, NT);
       const int cols = static_cast<int>(min(live - tile.m0, static_cast<int64_t>(NT)));   // live tokens
       if (p.split == 1) {
