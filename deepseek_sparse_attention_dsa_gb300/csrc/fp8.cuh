@@ -118,14 +118,18 @@ __device__ __forceinline__ float group_scale(uint32_t amax_bits) {
 // exactly, q + e r rounds to the rounded quotient x / s).  They have to be exact:
 // bf16 values over bf16 maxima meet borders between two codes in one value of
 // some 600.  e is exact down to x = 2^-102, and below it the quotient by a scale
-// of 2^-80 or more is far inside code 0; smaller scales take the division.
+// of 2^-80 or more is far inside code 0; smaller scales take the division.  The
+// negative of e is taken, q s - x, for the sign of a zero: an exact difference is
+// +0, so x = -0 gives -(+0) r + -0 = -0, and x = +0 gives -0 + +0 = +0 (with x - q s
+// it is +0 for both; x's sign put onto the result instead took 66.5 us for 2048 x
+// 65536 bf16 against 63.8).
 struct GroupScale {
   float scale, r;
   __device__ __forceinline__ explicit GroupScale(uint32_t amax_bits) : scale(group_scale(amax_bits)), r(1.f / scale) {}
   __device__ __forceinline__ GroupScale(float s, float reciprocal) : scale(s), r(reciprocal) {}
   __device__ __forceinline__ float quotient(float x) const {
     const float q = x * r;
-    return fmaf(fmaf(-q, scale, x), r, q);
+    return fmaf(-fmaf(q, scale, -x), r, q);
   }
 };
 // Four quotients to four codes, the first in bits 0-7.
