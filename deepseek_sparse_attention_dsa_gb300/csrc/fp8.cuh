@@ -122,14 +122,16 @@ __device__ __forceinline__ float group_scale(uint32_t amax_bits) {
 // negative of e is taken, q s - x, for the sign of a zero: an exact difference is
 // +0, so x = -0 gives -(+0) r + -0 = -0, and x = +0 gives -0 + +0 = +0 (with x - q s
 // it is +0 for both; x's sign put onto the result instead took 66.5 us for 2048 x
-// 65536 bf16 against 63.8).
+// 65536 bf16 against 63.8).  An infinite scale has r = 0 and q = +-0 for a finite x;
+// bounded, s keeps q s a zero, so that the quotient is x's zero as by a division
+// (and NaN for an infinite x, whose q is NaN); a NaN scale has r = NaN.
 struct GroupScale {
   float scale, r;
   __device__ __forceinline__ explicit GroupScale(uint32_t amax_bits) : scale(group_scale(amax_bits)), r(1.f / scale) {}
   __device__ __forceinline__ GroupScale(float s, float reciprocal) : scale(s), r(reciprocal) {}
   __device__ __forceinline__ float quotient(float x) const {
     const float q = x * r;
-    return fmaf(-fmaf(q, scale, -x), r, q);
+    return fmaf(-fmaf(q, fminf(scale, 0x1.fffffep127f), -x), r, q);
   }
 };
 // Four quotients to four codes, the first in bits 0-7.

@@ -1,6 +1,8 @@
 """GPU: the codes of the 8-bit rows byte for byte where a value says nothing
-about them: zeros of both signs.  The reference is the rule itself, scale = amax / 448 and code = E4M3(x / scale)
-with fp32 divisions, and for bf16 the oracle's and the quantise-on-store kernels'."""
+about them: zeros of both signs, values far below their group's scale, and
+groups that hold an infinity or a NaN.  The reference is the rule itself, scale
+= amax / 448 and code = E4M3(x / scale) with fp32 divisions, and for bf16 the
+oracle's and the quantise-on-store kernels'."""
 import numpy as np
 import pytest
 import torch
@@ -85,3 +87,63 @@ def test_the_quantisers_agree_byte_for_byte(ctx):
     assert torch.equal(codes.view(-1), q_codes.view(torch.uint8).view(-1)) and torch.equal(scales.view(-1), q_scales.view(-1))
     o_codes, o_scales = oracle.quantize_rows(x.cpu(), width)
     assert np.array_equal(codes.cpu().numpy().reshape(-1), o_codes) and np.array_equal(scales.cpu().numpy().reshape(-1), o_scales)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,width,stride,offset", LAYOUTS)
+def test_groups_that_are_not_finite_follow_the_rule(ctx, dtype, rows, width, stride, offset):
+    """Over an infinite scale a finite value is a zero of its sign and an infinity NaN (0x7F); over NaN all is NaN."""
+    v = with_zeros(rows, width)
+    v[2, 5], v[3, 130], v[3, 131] = float("inf"), float("-inf"), float("inf")
+    v[4, 200], v[5, 300] = float("nan"), -float("nan")
+    v[6, 10], v[6, 20] = float("inf"), float("nan")
+    x = placed(v, dtype, stride, offset)
+    codes, scales = (t.cpu() for t in ctx.quantize_rows(x))
+    x = x.cpu().float()
+    for j in range(scales.shape[1]):
+        at = slice(128 * j, 128 * j + 128)
+        group = x[:, at]
+        bad = ~group.isfinite().all(dim=1)
+        amax = group.abs().amax(dim=1)      # (NaN where there is one)
+        assert torch.equal(scales[bad, j].isnan(), amax[bad].isnan())
+        assert (scales[bad, j][~amax[bad].isnan()] == float("inf")).all()
+        q = group[bad] / scales[bad, j:j + 1]
+        want = torch.where(q.isnan(), 0x7F, torch.where(q.signbit(), 0x80, 0)).to(torch.uint8)
+        assert torch.equal(codes[bad, at], want), j
+        good, want = ~bad, R.quantize(group[~bad], 1)
+        assert torch.equal(codes[good, at], want[0]) and torch.equal(scales[good, j:j + 1], want[1])
+    # a matrix's block of 128 x 128 holds all rows: every one of these blocks is spoilt by its own values
+    w_codes, w_scales = (t.cpu() for t in ctx.quantize_weight(placed(v, dtype, stride, offset)))
+    for j in range(w_scales.shape[1]):
+        at = slice(128 * j, 128 * j + 128)
+        block, s = x[:, at], w_scales[0, j]
+        if block.isfinite().all():
+            continue
+        assert s.isnan() if block.isnan().any() else s == float("inf")
+        q = block / s
+        assert torch.equal(w_codes[:, at], torch.where(q.isnan(), 0x7F, torch.where(q.signbit(), 0x80, 0)).to(torch.uint8)), j
+
+
+def test_values_far_below_their_scale(ctx):
+    """Subnormal and tiny values beside large ones keep their signs as zeros."""
+    v = torch.zeros(4, 128)
+    v[:, 0] = torch.tensor([1.0, 448.0, 2.0 ** 127, 2.0 ** -60])
+    tiny = torch.tensor([2.0 ** -149, 2.0 ** -127, 2.0 ** -126, 2.0 ** -103, 2.0 ** -102, 2.0 ** -101, 3 * 2.0 ** -73, 2.0 ** -72])
+    v[:, 1:9], v[:, 9:17] = tiny, -tiny
+    same_bytes(ctx.quantize_rows(v.cuda()), R.quantize(v, 1))
+
+
+def test_an_infinite_norm_follows_the_rule(ctx):
+    """The norm's codes where y overflows: the value NaN, its group's others zeros of their signs."""
+    for width in (512, 515):
+        x = placed(rand(3, 3, width), BF16)
+        w = torch.ones(width)
+        w[5], w[300] = 3e38, -3e38
+        x[:, 5] = x[:, 300] = 16.0          # some 4 to 16 after the norm: beyond fp32 times these weights
+        codes, scales = (t.cpu() for t in ctx.rmsnorm_quantize(x, w.to(BF16).cuda(), 1e-6))
+        assert (scales[:, [0, 2]] == float("inf")).all() and scales[:, [1, 3]].isfinite().all()
+        for group in (0, 2):
+            at = slice(128 * group, 128 * group + 128)
+            want = torch.where(x.cpu()[:, at].signbit(), 0x80, 0).to(torch.uint8)
+            want[:, 5 if group == 0 else 300 - 256] = 0x7F
+            assert torch.equal(codes[:, at], want)
