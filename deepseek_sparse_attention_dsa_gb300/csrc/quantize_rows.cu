@@ -139,8 +139,9 @@ __global__ void __launch_bounds__(512, kPacked ? 3 : 2) quantize_blocks_kernel(c
   for (int i = 0; i < 4; ++i) {
     const int row = row0 + 32 * i;
     if (kPacked) {
-      u[kPacked ? i : 0] = row < p.n && col < p.k ? __ldcs(reinterpret_cast<const uint4 *>(w + row * p.w_stride + col * 2))
-                                                  : make_uint4(0, 0, 0, 0);
+      // (in bytes a column passes 32 bits)
+      const char *at = w + row * p.w_stride + static_cast<int64_t>(col) * 2;
+      u[kPacked ? i : 0] = row < p.n && col < p.k ? __ldcs(reinterpret_cast<const uint4 *>(at)) : make_uint4(0, 0, 0, 0);
     } else {
       if (row < p.n) {
         load8(v[kPacked ? 0 : i], w + row * p.w_stride, p.w_type, col, p.k, p.w_vec);

@@ -147,3 +147,20 @@ def test_an_infinite_norm_follows_the_rule(ctx):
             want = torch.where(x.cpu()[:, at].signbit(), 0x80, 0).to(torch.uint8)
             want[:, 5 if group == 0 else 300 - 256] = 0x7F
             assert torch.equal(codes[:, at], want)
+
+
+@pytest.mark.parametrize("k", [2 ** 31 - 8, 2 ** 30 + 1032])
+def test_long_rows_in_whole_pieces(ctx, k):
+    """bf16 rows of whole 16-byte pieces whose bytes, or columns, come up to 32 bits: the packed kernels' offsets."""
+    x = torch.zeros(1, k, dtype=BF16, device="cuda")
+    at = torch.tensor([0, 127, 128, 2 ** 30 - 1, 2 ** 30, 2 ** 30 + 129, k - 8, k - 1], device="cuda")
+    x[0, at] = torch.tensor([1.0, -2.0, 3.0, -4.0, 5.0, -6.0, 7.0, -3.5], dtype=BF16, device="cuda")
+    for codes, scales in (ctx.quantize_rows(x), ctx.quantize_weight(x)):
+        groups = torch.unique(at // 128)
+        assert int((codes != 0).sum()) == len(at) and int((scales != 1).sum()) == len(groups)
+        cols = (groups[:, None] * 128 + torch.arange(128, device="cuda")).clamp(max=k - 1)
+        want = R.quantize(torch.where(groups[:, None] * 128 + torch.arange(128, device="cuda") < k, x[0, cols], 0), 1)
+        assert torch.equal(scales[0, groups].cpu(), want[1][:, 0])
+        inside = groups[:, None].cpu() * 128 + torch.arange(128) < k
+        assert torch.equal(codes[0, cols].cpu()[inside], want[0][inside])
+        del codes, scales
