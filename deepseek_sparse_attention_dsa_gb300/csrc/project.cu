@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
         else st_async(map_to_cta(at, to), acc[c], map_to_cta(partfull, to));
       }
       named_bar_sync(2, 32 * C::EPI);
-      if (!mbar_wait_warp(partfull, 0, aborted, p.err)) break;
+      if (!mbar_wait_warp<true>(partfull, 0, aborted, p.err)) break;   // the others' sums are there, and visible
       for (int i = threadIdx.x - 128; i < mine * 32; i += 32 * C::EPI) {   // a token, four weight rows
         const int m = i / 32, n4 = i % 32 * 4;
         const float4 sum = sum_partials(sbase + C::OFF_PART + (m * 128 + n4) * 4, own * 512, split);
@@ -780,7 +780,7 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
           for (int c = 0; c < C::COLS; c += 4) st_async4(to + c * 128, acc + c, bar);
           break;
         }
-        if (!mbar_wait_warp(partfull, 0, aborted, p.err)) break;
+        if (!mbar_wait_warp<true>(partfull, 0, aborted, p.err)) break;
 #pragma unroll
         for (int c = 0; c < C::COLS; c += 4) {
           const float4 v = ld_shared4(at + c * 128);

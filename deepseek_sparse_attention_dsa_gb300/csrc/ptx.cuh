@@ -108,12 +108,16 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 // clock is first read after 256 failed tries (each bounded by the hardware's own
 // limit).  Lanes whose first try failed beside others whose succeeded need only
 // try again: the phase is complete and cannot pass on without this warp.
+// kCluster: the phase completes what other CTAs of the cluster have stored here
+// (st.async), which only an acquire at the cluster's scope orders before the
+// reads that follow.
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, uint32_t abort_flag, int *err) {
   const uint32_t lanes = __activemask();
   uint32_t t0 = 0, now, stop = 0;
 #pragma unroll 1
   for (uint32_t i = 1;; ++i) {
-    if (__all_sync(lanes, mbar_try_wait(bar, parity))) return true;
+    if (__all_sync(lanes, kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) return true;
     if ((i & 255) == 0 && lanes == 0xffffffffu) {
       asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
       if (i == 256) t0 = now;
@@ -127,9 +131,10 @@ __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, ui
     }
   }
 }
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint32_t abort_flag, int *err) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (!ok) ok = mbar_wait_slow(bar, parity, abort_flag, err);
+  bool ok = kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+  if (!ok) ok = mbar_wait_slow<kCluster>(bar, parity, abort_flag, err);
   __syncwarp();
   return ok;
 }

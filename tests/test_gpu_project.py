@@ -369,3 +369,28 @@ def test_threads_share_a_context(ctx):
     for a, out, yi, (ci, si) in got.values():
         assert torch.equal(out, outs[a]) and torch.equal(yi, y) and torch.equal(ci, codes) and torch.equal(si, scales)
     ctx.get_error()
+
+
+@pytest.mark.parametrize("rows,n,k", [(1, 1032, 8192), (16, 2048, 4096), (30, 1032, 8192), (60, 520, 8192), (128, 8192, 4096), (200, 4096, 4096),
+                                      (1031, 704, 5120)])
+def test_sums_that_cross_ctas_are_whole(ctx, rows, n, k):
+    """Every form that splits k, again and again on other numbers: whole codes and
+    scales of powers of two, so that a sum read before it is there, or read from
+    the call before, is off by more than a rounding."""
+    g = torch.Generator().manual_seed(rows)
+    w = torch.randint(-3, 4, (n, k), generator=g).float()
+    ts = []
+    for i in range(4):
+        a = torch.randint(-3, 4, (rows, k), generator=g).float()
+        asc = 2.0 ** torch.randint(-2, 3, (rows, R.groups(k)), generator=g).float()
+        ts.append((a.to(torch.float8_e4m3fn).cuda(), asc.cuda()))
+    wc, wsc = w.to(torch.float8_e4m3fn).cuda(), 2.0 ** torch.randint(-2, 3, (R.groups(n), R.groups(k)), generator=g).float().cuda()
+    col, row = torch.arange(k, device="cuda") // R.GROUP, torch.arange(n, device="cuda") // R.GROUP
+    wv = wc.float().double() * wsc.double()[row][:, col]
+    want = [((a.float().double() * s.double()[:, col]) @ wv.t()).float() for a, s in ts]
+    outs = []
+    for i in range(80):
+        outs.append(ctx.project_fp8(*ts[i % 4], wc, wsc, out_dtype=F32))
+    for i, out in enumerate(outs):
+        assert torch.equal(out, want[i % 4]), i
+    ctx.get_error()
