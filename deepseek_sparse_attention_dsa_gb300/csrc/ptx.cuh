@@ -104,39 +104,37 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
-// mbar_wait for a converged warp, in few registers, the answer uniform.  The
-// clock is first read after 256 failed tries (each bounded by the hardware's own
-// limit).  Lanes whose first try failed beside others whose succeeded need only
-// try again: the phase is complete and cannot pass on without this warp.
-// kCluster: the phase completes what other CTAs of the cluster have stored here
-// (st.async), which only an acquire at the cluster's scope orders before the
-// reads that follow.
+// mbar_wait for a converged warp, in few registers, the answer the same in every
+// lane (the warp goes on to collective instructions): the lanes vote on the first
+// try and on every later one.  It ends within limit_ns and 256 tries, each of
+// which the hardware holds for a bounded time.  kCluster: the phase completes what
+// other CTAs of the cluster have stored here (st.async), which only an acquire at
+// the cluster's scope orders before the reads that follow.
 template <bool kCluster = false>
-__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, uint32_t abort_flag, int *err) {
-  const uint32_t lanes = __activemask();
-  uint32_t t0 = 0, now, stop = 0;
+__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, uint32_t abort_flag, int *err,
+                                               uint32_t limit_ns) {
+  uint32_t t0, now, stop;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t0));
 #pragma unroll 1
   for (uint32_t i = 1;; ++i) {
-    if (__all_sync(lanes, kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) return true;
-    if ((i & 255) == 0 && lanes == 0xffffffffu) {
+    if (__all_sync(0xffffffffu, kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) return true;
+    if ((i & 255) == 0) {
       asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
-      if (i == 256) t0 = now;
       asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(stop) : "r"(abort_flag) : "memory");
-      if (now - t0 > static_cast<uint32_t>(kWaitLimitNs)) {
+      if (now - t0 > limit_ns) {
         stop = 1;
         asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort_flag), "r"(1) : "memory");
         atomicOr(err, kErrTimeout);
       }
-      if (__any_sync(lanes, stop)) return false;
+      if (__any_sync(0xffffffffu, stop)) return false;
     }
   }
 }
 template <bool kCluster = false>
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint32_t abort_flag, int *err) {
-  bool ok = kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
-  if (!ok) ok = mbar_wait_slow<kCluster>(bar, parity, abort_flag, err);
-  __syncwarp();
-  return ok;
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint32_t abort_flag, int *err,
+                                               uint32_t limit_ns = static_cast<uint32_t>(kWaitLimitNs)) {
+  if (__all_sync(0xffffffffu, kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) return true;
+  return mbar_wait_slow<kCluster>(bar, parity, abort_flag, err, limit_ns);
 }
 
 // A CTA that gave up stays for as long as its cluster's others may still send to
@@ -151,7 +149,8 @@ __device__ __forceinline__ void linger_if_aborted(uint32_t abort_flag) {
 
 // Both of two phases, tried together first so that one try's latency covers the other's.
 __device__ __forceinline__ bool mbar_wait_warp_both(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1,
-                                                    uint32_t abort_flag, int *err) {
+                                                    uint32_t abort_flag, int *err,
+                                                    uint32_t limit_ns = static_cast<uint32_t>(kWaitLimitNs)) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
@@ -162,9 +161,8 @@ __device__ __forceinline__ bool mbar_wait_warp_both(uint32_t bar0, uint32_t pari
       : "=r"(ok)
       : "r"(bar0), "r"(parity0), "r"(bar1), "r"(parity1)
       : "memory");
-  if (!ok) ok = mbar_wait_slow(bar0, parity0, abort_flag, err) && mbar_wait_slow(bar1, parity1, abort_flag, err);
-  __syncwarp();
-  return ok;
+  if (__all_sync(0xffffffffu, ok)) return true;
+  return mbar_wait_slow(bar0, parity0, abort_flag, err, limit_ns) && mbar_wait_slow(bar1, parity1, abort_flag, err, limit_ns);
 }
 
 // ----------------------------------------------------------------- fences

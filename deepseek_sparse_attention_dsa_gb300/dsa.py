@@ -57,7 +57,7 @@ EXPORTED = ["dsa_create", "dsa_destroy", "dsa_plan", "dsa_plan_destroy", "dsa_pl
             "dsa_last_launch_count", "dsa_status_str", "dsa_index_topk_static", "dsa_last_cuda_error",
             "dsa_quantize_store_keys", "dsa_quantize_store_latents", "dsa_attend_shared", "dsa_plan_capturable",
             "dsa_plan_update", "dsa_plan_read_counts", "dsa_quantize_q", "dsa_index_scores_fp8q",
-            "dsa_index_topk_fp8q", "dsa_selftest_wait_timeout", "dsa_msa_select_blocks", "dsa_msa_index_select",
+            "dsa_index_topk_fp8q", "dsa_selftest_wait_timeout", "dsa_selftest_warp_wait_timeout", "dsa_msa_select_blocks", "dsa_msa_index_select",
             "dsa_msa_attend", "dsa_msa_attend_on_tensor_cores", "dsa_rmsnorm", "dsa_quantize_rows",
             "dsa_quantize_weight", "dsa_project_fp8", "dsa_project_on_tensor_cores"]
 
@@ -169,6 +169,7 @@ def load() -> ctypes.CDLL:
     L.dsa_index_topk_fp8q.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp]
     L.dsa_get_error.argtypes = [vp, vp]
     L.dsa_selftest_wait_timeout.argtypes = [vp, ctypes.c_uint64, vp, vp]
+    L.dsa_selftest_warp_wait_timeout.argtypes = [vp, ctypes.c_uint64, vp, vp]
     L.dsa_rmsnorm.argtypes = [vp, vp, ctypes.POINTER(_Norm), vp, vp, vp, vp, vp, vp, vp, vp]
     L.dsa_quantize_rows.argtypes = [vp, vp, ctypes.POINTER(_Rows), vp, vp, vp, vp]
     L.dsa_quantize_weight.argtypes = [vp, ctypes.POINTER(_Weight), vp, vp, vp, vp]
@@ -191,7 +192,7 @@ def load() -> ctypes.CDLL:
                  "dsa_index_scores", "dsa_topk_from_scores", "dsa_attend", "dsa_get_error", "dsa_quantize_store_keys",
                  "dsa_quantize_store_latents", "dsa_attend_shared", "dsa_plan_capturable", "dsa_plan_update",
                  "dsa_plan_read_counts", "dsa_quantize_q", "dsa_index_scores_fp8q", "dsa_index_topk_fp8q",
-                 "dsa_selftest_wait_timeout", "dsa_msa_select_blocks", "dsa_msa_index_select", "dsa_msa_attend",
+                 "dsa_selftest_wait_timeout", "dsa_selftest_warp_wait_timeout", "dsa_msa_select_blocks", "dsa_msa_index_select", "dsa_msa_attend",
                  "dsa_rmsnorm", "dsa_quantize_rows", "dsa_quantize_weight", "dsa_project_fp8"):
         getattr(L, name).restype = i32
     _lib = L

@@ -68,3 +68,37 @@ def test_selftest_rejects_bad_arguments():
     assert _selftest(ctx, 2_000_000_000, result) == DSA_ERR_INVALID_ARG
     assert _selftest(ctx, 1000, None) == DSA_ERR_INVALID_ARG
     assert int(np.count_nonzero(result.cpu().numpy())) == 0   # nothing ran
+
+
+def test_warp_waits_time_out_in_every_lane(built):
+    """The waits that a warp makes together, each made to run out with a 20 ms
+    limit: no lane is told of success, the raised flag ends the next wait before
+    its own limit, complete phases are still seen, and the context goes on."""
+    ctx = dsa.Context(W.DSAShape(**W.DEEPSEEK), 0)
+    L = dsa.load()
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    limit_ns = 20_000_000
+
+    def run(limit, result):
+        ptr = ctypes.c_void_p(result.data_ptr()) if result is not None else None
+        return L.dsa_selftest_warp_wait_timeout(ctx.handle, ctypes.c_uint64(limit), ptr, stream)
+
+    for _ in range(2):
+        result = torch.full((23,), -1, dtype=torch.int64, device="cuda")
+        assert run(limit_ns, result) == dsa.DSA_OK
+        assert L.dsa_get_error(ctx.handle, stream) == DSA_ERR_TIMEOUT
+        assert L.dsa_get_error(ctx.handle, stream) == dsa.DSA_OK
+        got = result.cpu().tolist()
+        for form in range(4):
+            first, first_ns, second, second_ns, flag = got[5 * form:5 * form + 5]
+            assert first == 0 and second == 0 and flag == 1, form
+            assert limit_ns <= first_ns < limit_ns + 250_000_000, (form, first_ns)
+            assert second_ns < limit_ns, (form, second_ns)
+        assert got[20] == 0xFFFFFFFF and got[21] == 0xFFFFFFFF and got[22] == -1
+    assert run(0, result) == DSA_ERR_INVALID_ARG and run(1_000_000_001, result) == DSA_ERR_INVALID_ARG
+    assert run(1000, None) == DSA_ERR_INVALID_ARG
+    # the kernels that wait so still compute
+    a = torch.full((3, 256), 0x38, dtype=torch.uint8, device="cuda")
+    out = ctx.project_fp8(a, torch.ones(3, 2, device="cuda"), a, torch.ones(1, 2, device="cuda"), out_dtype=torch.float32)
+    assert (out == 256).all()
+    ctx.get_error()
