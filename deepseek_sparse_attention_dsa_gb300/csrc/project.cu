@@ -164,6 +164,12 @@ __device__ __forceinline__ uint32_t barrier_arrivals(int i, int ctas) {
   return j < C::AB ? 1 : k < 0 ? ctas * C::EPI : k < C::SG ? 64 : k < 2 * C::SG ? C::EPI : 1;
 }
 
+// How long a CTA that gave up stays.  The other CTAs that share its tile started
+// with it and have as many blocks of k, none of 1 us, and then send their sums or
+// give up themselves after one wait, a limit and its last tries.  (Pairs also
+// meet at the end.)
+__device__ __forceinline__ uint64_t stay_ns(int blocks) { return 2 * kWaitLimitNs + static_cast<uint64_t>(blocks) * 1000; }
+
 template <int NT>
 __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kernel(const __grid_constant__ ProjectParams p) {
   using C = ProjectTraits<NT>;
@@ -417,8 +423,8 @@ __global__ void __launch_bounds__(ProjectTraits<NT>::THREADS, 1) project_tc_kern
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  linger_if_aborted(aborted, stay_ns(kb1 - kb0));
   if (warp == 1) tmem_dealloc(tmem_base, C::TMEM_COLS);
-  if (p.split > 1) linger_if_aborted(aborted);
 }
 
 // ---------------------------------------------------------------------------
@@ -834,19 +840,18 @@ __global__ void __launch_bounds__(384, 1) project_rows_kernel(const __grid_const
     if (lane == 0) bulk_wait_read_all();
   }
 
-  if (kPair) {
-    __syncwarp();
-    cluster_arrive_relaxed();
-    cluster_wait();   // no CTA leaves while another may signal it or read its operands
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  linger_if_aborted(aborted, stay_ns(kb1 - kb0));
+  if (kPair) {
+    cluster_arrive_relaxed();
+    cluster_wait();   // no CTA leaves while another may signal it or read its operands
+  }
   if (warp == 1) {
     if (kPair) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
     else tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
-  if (SPLIT > 1) linger_if_aborted(aborted);
 }
 
 __device__ __forceinline__ float e4m3_value(uint8_t c) {

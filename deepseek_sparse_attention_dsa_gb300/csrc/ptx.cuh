@@ -137,14 +137,15 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, ui
   return mbar_wait_slow<kCluster>(bar, parity, abort_flag, err, limit_ns);
 }
 
-// A CTA that gave up stays for as long as its cluster's others may still send to
-// its shared memory: each of their waits ends within the limit.
-__device__ __forceinline__ void linger_if_aborted(uint32_t abort_flag) {
+// A CTA that gave up stays for another stay_ns before it frees its tensor memory
+// and leaves: its own copies and MMAs in flight end in microseconds, and the
+// other CTAs of its cluster may still send to its shared memory.
+__device__ __forceinline__ void linger_if_aborted(uint32_t abort_flag, uint64_t stay_ns) {
   uint32_t stop;
   asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(stop) : "r"(abort_flag) : "memory");
   if (!stop) return;
   const uint64_t t0 = globaltimer();
-  while (globaltimer() - t0 < 3 * kWaitLimitNs) __nanosleep(1000);
+  while (globaltimer() - t0 < stay_ns) __nanosleep(1000);
 }
 
 // Both of two phases, tried together first so that one try's latency covers the other's.

@@ -109,6 +109,17 @@ __global__ void __launch_bounds__(64, 1) warp_wait_timeout_kernel(int *err, uint
     const uint32_t one = __ballot_sync(0xffffffffu, mbar_wait_warp(d, 0, flag, err, limit_ns));
     const uint32_t both = __ballot_sync(0xffffffffu, mbar_wait_warp_both(d, 0, d, 0, flag, err, limit_ns));
     if (lane_id() == 0) result[20] = one, result[21] = both;
+    // what a CTA stays for once it gave up, and not otherwise (the last flag is down again)
+    __syncwarp();
+    if (lane_id() == 0) *reinterpret_cast<volatile int *>(&abort_flag[3]) = 0;
+    __syncwarp();
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t t0 = globaltimer();
+      linger_if_aborted(smem_u32(&abort_flag[3 * i]), limit_ns);
+      __syncwarp();
+      if (lane_id() == 0) result[22 + i] = static_cast<int64_t>(globaltimer() - t0);
+    }
   }
   tc_fence_before();
   __syncthreads();

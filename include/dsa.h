@@ -502,10 +502,12 @@ int dsa_project_on_tensor_cores(const dsa_project_t *shape, const void *a, const
 dsa_status dsa_selftest_wait_timeout(dsa_ctx_t *ctx, uint64_t limit_ns, int64_t *result, dsa_stream_t stream);
 /* The same for the waits that a whole warp makes together (the projections'):
  * on one phase, at the cluster's scope, and on both of two phases of which the
- * first or the second never completes.  result: DEVICE int64[22]: for each of
+ * first or the second never completes.  result: DEVICE int64[24]: for each of
  * the four the five values above, [0] and [2] with a bit for each lane that was
  * told of success (all or none); then the lanes told so of a phase that is
- * complete, after the flag was raised, and of two such phases (all of them). */
+ * complete, after the flag was raised, and of two such phases (all of them);
+ * then how long a CTA that gave up stays when told to for limit_ns, and one
+ * that did not (not at all), in ns. */
 dsa_status dsa_selftest_warp_wait_timeout(dsa_ctx_t *ctx, uint64_t limit_ns, int64_t *result, dsa_stream_t stream);
 
 /* Number of kernels the last compute call on this context launched (for

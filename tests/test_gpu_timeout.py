@@ -73,7 +73,8 @@ def test_selftest_rejects_bad_arguments():
 def test_warp_waits_time_out_in_every_lane(built):
     """The waits that a warp makes together, each made to run out with a 20 ms
     limit: no lane is told of success, the raised flag ends the next wait before
-    its own limit, complete phases are still seen, and the context goes on."""
+    its own limit, complete phases are still seen, a CTA that gave up stays as
+    long as it is told, and the context goes on."""
     ctx = dsa.Context(W.DSAShape(**W.DEEPSEEK), 0)
     L = dsa.load()
     stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
@@ -84,7 +85,7 @@ def test_warp_waits_time_out_in_every_lane(built):
         return L.dsa_selftest_warp_wait_timeout(ctx.handle, ctypes.c_uint64(limit), ptr, stream)
 
     for _ in range(2):
-        result = torch.full((23,), -1, dtype=torch.int64, device="cuda")
+        result = torch.full((25,), -1, dtype=torch.int64, device="cuda")
         assert run(limit_ns, result) == dsa.DSA_OK
         assert L.dsa_get_error(ctx.handle, stream) == DSA_ERR_TIMEOUT
         assert L.dsa_get_error(ctx.handle, stream) == dsa.DSA_OK
@@ -94,7 +95,8 @@ def test_warp_waits_time_out_in_every_lane(built):
             assert first == 0 and second == 0 and flag == 1, form
             assert limit_ns <= first_ns < limit_ns + 250_000_000, (form, first_ns)
             assert second_ns < limit_ns, (form, second_ns)
-        assert got[20] == 0xFFFFFFFF and got[21] == 0xFFFFFFFF and got[22] == -1
+        assert got[20] == 0xFFFFFFFF and got[21] == 0xFFFFFFFF and got[24] == -1
+        assert limit_ns <= got[22] < limit_ns + 250_000_000 and got[23] < limit_ns
     assert run(0, result) == DSA_ERR_INVALID_ARG and run(1_000_000_001, result) == DSA_ERR_INVALID_ARG
     assert run(1000, None) == DSA_ERR_INVALID_ARG
     # the kernels that wait so still compute
