@@ -64,13 +64,6 @@ struct Layout {
 
 bool is_host_only(const dsa_ctx *ctx) { return ctx == nullptr || ctx->device < 0; }
 
-// DSA_OK, or DSA_ERR_CUDA with the CUDA error recorded in the context.
-dsa_status cuda_status(dsa_ctx *ctx, cudaError_t e) {
-  if (e == cudaSuccess) return DSA_OK;
-  snprintf(ctx->last_cuda_error, sizeof(ctx->last_cuda_error), "%s: %s", cudaGetErrorName(e), cudaGetErrorString(e));
-  return DSA_ERR_CUDA;
-}
-
 dsa_status ensure_scratch(dsa_ctx *ctx, size_t scores, size_t slots) {
   if (scores > ctx->scores_cap) {
     size_t cap = std::max(scores, ctx->scores_cap * 3 / 2);
@@ -100,6 +93,22 @@ dsa_status ensure_scratch(dsa_ctx *ctx, size_t scores, size_t slots) {
 // tensor maps
 // ----------------------------------------------------------------------------
 namespace dsa {
+
+const char *cuda_error_text(cudaError_t e) {
+  constexpr int kCodes = 1024;
+  static std::atomic<const char *> texts[kCodes];
+  const int i = static_cast<int>(e);
+  if (i < 0 || i >= kCodes) return "unknown CUDA error";
+  const char *known = texts[i].load(std::memory_order_acquire);
+  if (known) return known;
+  constexpr size_t kBytes = 160;
+  char *text = new (std::nothrow) char[kBytes];
+  if (!text) return cudaGetErrorName(e);
+  snprintf(text, kBytes, "%s: %s", cudaGetErrorName(e), cudaGetErrorString(e));
+  if (texts[i].compare_exchange_strong(known, text, std::memory_order_acq_rel)) return text;
+  delete[] text;   // another thread was first
+  return known;
+}
 
 namespace {
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -612,11 +621,11 @@ dsa_status dsa_store_keys(dsa_ctx_t *ctx, const dsa_plan_t *plan, const void *ke
                           dsa_stream_t stream) {
   dsa_status st = check_call(ctx, plan);
   if (st != DSA_OK) return st;
-  ctx->last_launches = 0;
+  LaunchCount launched(ctx);
   if (plan->T == 0) return DSA_OK;
   if (!keys || !index_cache) return DSA_ERR_INVALID_ARG;
   cudaError_t e = launch_store_keys(ctx, plan, keys, index_cache, reinterpret_cast<cudaStream_t>(stream),
-                                    &ctx->last_launches);
+                                    &launched.n);
   return cuda_status(ctx, e);
 }
 
@@ -624,12 +633,12 @@ dsa_status dsa_quantize_store_keys(dsa_ctx_t *ctx, const dsa_plan_t *plan, const
                                    void *index_cache, dsa_stream_t stream) {
   dsa_status st = check_call(ctx, plan);
   if (st != DSA_OK) return st;
-  ctx->last_launches = 0;
+  LaunchCount launched(ctx);
   if (ctx->cfg.index_fmt != DSA_INDEX_FP8_132 || ctx->cfg.index_dim != 128) return DSA_ERR_UNSUPPORTED;
   if (plan->T == 0) return DSA_OK;
   if (!keys_bf16 || !index_cache) return DSA_ERR_INVALID_ARG;
   cudaError_t e = launch_quantize_keys(ctx, plan, keys_bf16, index_cache, reinterpret_cast<cudaStream_t>(stream),
-                                       &ctx->last_launches);
+                                       &launched.n);
   return cuda_status(ctx, e);
 }
 
@@ -637,13 +646,13 @@ dsa_status dsa_quantize_store_latents(dsa_ctx_t *ctx, const dsa_plan_t *plan, co
                                       void *latent_cache, dsa_stream_t stream) {
   dsa_status st = check_call(ctx, plan);
   if (st != DSA_OK) return st;
-  ctx->last_launches = 0;
+  LaunchCount launched(ctx);
   if (ctx->cfg.latent_fmt != DSA_LATENT_FP8_656 || ctx->cfg.kv_lora_rank != 512 || ctx->cfg.rope_dim != 64)
     return DSA_ERR_UNSUPPORTED;
   if (plan->T == 0) return DSA_OK;
   if (!latents_bf16 || !latent_cache) return DSA_ERR_INVALID_ARG;
   cudaError_t e = launch_quantize_latents(ctx, plan, latents_bf16, latent_cache,
-                                          reinterpret_cast<cudaStream_t>(stream), &ctx->last_launches);
+                                          reinterpret_cast<cudaStream_t>(stream), &launched.n);
   return cuda_status(ctx, e);
 }
 
@@ -651,11 +660,11 @@ dsa_status dsa_index_scores(dsa_ctx_t *ctx, const dsa_plan_t *plan, const void *
                             const void *index_cache, float *scores, dsa_stream_t stream) {
   dsa_status st = check_call(ctx, plan);
   if (st != DSA_OK) return st;
-  ctx->last_launches = 0;
+  LaunchCount launched(ctx);
   if (plan->T == 0) return DSA_OK;
   if (!q || !w || !index_cache || !scores) return DSA_ERR_INVALID_ARG;
   cudaError_t e = launch_index_scores(ctx, plan, q, w, index_cache, scores, reinterpret_cast<cudaStream_t>(stream),
-                                      &ctx->last_launches);
+                                      &launched.n);
   return cuda_status(ctx, e);
 }
 
@@ -663,11 +672,11 @@ dsa_status dsa_topk_from_scores(dsa_ctx_t *ctx, const dsa_plan_t *plan, const fl
                                 dsa_stream_t stream) {
   dsa_status st = check_call(ctx, plan);
   if (st != DSA_OK) return st;
-  ctx->last_launches = 0;
+  LaunchCount launched(ctx);
   if (plan->T == 0) return DSA_OK;
   if (!scores || !selection) return DSA_ERR_INVALID_ARG;
   cudaError_t e = launch_topk(ctx, plan, scores, selection, reinterpret_cast<cudaStream_t>(stream),
-                              &ctx->last_launches);
+                              &launched.n);
   if (e == cudaSuccess) plan->last_selection = selection;
   return cuda_status(ctx, e);
 }
@@ -676,7 +685,7 @@ dsa_status dsa_index_topk(dsa_ctx_t *ctx, const dsa_plan_t *plan, const void *q,
                           const void *index_cache, int32_t *selection, dsa_stream_t stream) {
   dsa_status st = check_call(ctx, plan);
   if (st != DSA_OK) return st;
-  ctx->last_launches = 0;
+  LaunchCount launched(ctx);
   if (plan->T == 0) return DSA_OK;
   if (!q || !w || !index_cache || !selection) return DSA_ERR_INVALID_ARG;
   if (!plan->own_scores && static_cast<size_t>(plan->num_scores) > ctx->scores_cap)
@@ -687,7 +696,7 @@ dsa_status dsa_index_topk(dsa_ctx_t *ctx, const dsa_plan_t *plan, const void *q,
   cudaError_t e = launch_index_scores(ctx, plan, q, w, index_cache, scores, s, &n);
   if (e == cudaSuccess) e = launch_topk(ctx, plan, scores, selection, s, &n);
   if (e == cudaSuccess) plan->last_selection = selection;
-  ctx->last_launches = n;
+  launched.n = n;
   return cuda_status(ctx, e);
 }
 
@@ -700,12 +709,12 @@ dsa_status dsa_quantize_q(dsa_ctx_t *ctx, const dsa_plan_t *plan, const void *q_
                           dsa_stream_t stream) {
   dsa_status st = check_call(ctx, plan);
   if (st != DSA_OK) return st;
-  ctx->last_launches = 0;
+  LaunchCount launched(ctx);
   if (ctx->cfg.index_heads != 64 || ctx->cfg.index_dim != 128) return DSA_ERR_UNSUPPORTED;
   if (plan->T == 0) return DSA_OK;
   if (!q_bf16 || !q_codes || !q_scale) return DSA_ERR_INVALID_ARG;
   cudaError_t e = launch_quantize_q(ctx, plan, q_bf16, q_codes, q_scale, reinterpret_cast<cudaStream_t>(stream),
-                                    &ctx->last_launches);
+                                    &launched.n);
   return cuda_status(ctx, e);
 }
 
@@ -713,12 +722,12 @@ dsa_status dsa_index_scores_fp8q(dsa_ctx_t *ctx, const dsa_plan_t *plan, const v
                                  const float *w, const void *index_cache, float *scores, dsa_stream_t stream) {
   dsa_status st = check_call(ctx, plan);
   if (st != DSA_OK) return st;
-  ctx->last_launches = 0;
+  LaunchCount launched(ctx);
   if (!f8q_ok(ctx, plan)) return DSA_ERR_UNSUPPORTED;
   if (plan->T == 0) return DSA_OK;
   if (!q_codes || !q_scale || !w || !index_cache || !scores) return DSA_ERR_INVALID_ARG;
   cudaError_t e = launch_index_scores_f8q(ctx, plan, q_codes, q_scale, w, index_cache, scores,
-                                          reinterpret_cast<cudaStream_t>(stream), &ctx->last_launches);
+                                          reinterpret_cast<cudaStream_t>(stream), &launched.n);
   return cuda_status(ctx, e);
 }
 
@@ -726,7 +735,7 @@ dsa_status dsa_index_topk_fp8q(dsa_ctx_t *ctx, const dsa_plan_t *plan, const voi
                                const float *w, const void *index_cache, int32_t *selection, dsa_stream_t stream) {
   dsa_status st = check_call(ctx, plan);
   if (st != DSA_OK) return st;
-  ctx->last_launches = 0;
+  LaunchCount launched(ctx);
   if (!f8q_ok(ctx, plan)) return DSA_ERR_UNSUPPORTED;
   if (plan->T == 0) return DSA_OK;
   if (!q_codes || !q_scale || !w || !index_cache || !selection) return DSA_ERR_INVALID_ARG;
@@ -737,7 +746,7 @@ dsa_status dsa_index_topk_fp8q(dsa_ctx_t *ctx, const dsa_plan_t *plan, const voi
   cudaError_t e = launch_index_scores_f8q(ctx, plan, q_codes, q_scale, w, index_cache, scores, s, &n);
   if (e == cudaSuccess) e = launch_topk(ctx, plan, scores, selection, s, &n);
   if (e == cudaSuccess) plan->last_selection = selection;
-  ctx->last_launches = n;
+  launched.n = n;
   return cuda_status(ctx, e);
 }
 
@@ -746,12 +755,12 @@ dsa_status dsa_attend(dsa_ctx_t *ctx, const dsa_plan_t *plan, const int32_t *sel
                       dsa_stream_t stream) {
   dsa_status st = check_call(ctx, plan);
   if (st != DSA_OK) return st;
-  ctx->last_launches = 0;
+  LaunchCount launched(ctx);
   if (plan->T == 0) return DSA_OK;
   if (!selection || !q_nope || !latent_cache || !out || (!q_pe && ctx->cfg.rope_dim > 0)) return DSA_ERR_INVALID_ARG;
   if (!plan->own_opart && static_cast<size_t>(plan->n_slots) > ctx->part_cap) return DSA_ERR_INVALID_ARG;
   cudaError_t e = launch_attend(ctx, plan, selection, q_nope, q_pe, latent_cache, sink, sm_scale, out,
-                                reinterpret_cast<cudaStream_t>(stream), &ctx->last_launches);
+                                reinterpret_cast<cudaStream_t>(stream), &launched.n);
   return cuda_status(ctx, e);
 }
 
@@ -807,7 +816,7 @@ dsa_status dsa_rmsnorm(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_norm_t 
   int32_t per_row;
   dsa_status st = check_rows(ctx, plan, n.rows, &count, &per_row);
   if (st != DSA_OK) return st;
-  ctx->last_launches = 0;
+  LaunchCount launched(ctx);
   if (n.rows == 0) return DSA_OK;
   if ((residual_out && !residual) || (codes == nullptr) != (scales == nullptr) || (!out && !codes))
     return DSA_ERR_INVALID_ARG;
@@ -816,7 +825,7 @@ dsa_status dsa_rmsnorm(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_norm_t 
     return DSA_ERR_INVALID_ARG;
   if (!x) return DSA_ERR_INVALID_ARG;
   return cuda_status(ctx, launch_rmsnorm(ctx->num_sms, n, x, weight, residual, residual_out, out, codes, scales, count, per_row,
-                                         reinterpret_cast<cudaStream_t>(stream), &ctx->last_launches));
+                                         reinterpret_cast<cudaStream_t>(stream), &launched.n));
 }
 
 dsa_status dsa_quantize_rows(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_rows_t *shape, const void *x,
@@ -829,14 +838,14 @@ dsa_status dsa_quantize_rows(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_r
   int32_t per_row;
   dsa_status st = check_rows(ctx, plan, r.rows, &count, &per_row);
   if (st != DSA_OK) return st;
-  ctx->last_launches = 0;
+  LaunchCount launched(ctx);
   if (r.rows == 0) return DSA_OK;
   if (!apart(r.width, r.rows, r.codes_stride) || !apart((static_cast<int64_t>(r.width) + 127) / 128, r.rows, r.scales_stride))
     return DSA_ERR_INVALID_ARG;
   if (!x || !codes || !scales) return DSA_ERR_INVALID_ARG;
   if ((static_cast<int64_t>(r.width) / 1024 + 1) * r.rows > 8ll * INT32_MAX) return DSA_ERR_UNSUPPORTED;   // the grid
   return cuda_status(ctx, launch_quantize_rows(r, x, codes, scales, count, per_row,
-                                               reinterpret_cast<cudaStream_t>(stream), &ctx->last_launches));
+                                               reinterpret_cast<cudaStream_t>(stream), &launched.n));
 }
 
 dsa_status dsa_quantize_weight(dsa_ctx_t *ctx, const dsa_weight_t *shape, const void *w, void *codes, float *scales,
@@ -851,9 +860,9 @@ dsa_status dsa_quantize_weight(dsa_ctx_t *ctx, const dsa_weight_t *shape, const 
     return DSA_ERR_INVALID_ARG;
   if (g.batch > 65535 || g.n > 128 * 65535) return DSA_ERR_UNSUPPORTED;
   if (cudaSetDevice(ctx->device) != cudaSuccess) return DSA_ERR_CUDA;
-  ctx->last_launches = 0;
+  LaunchCount launched(ctx);
   return cuda_status(ctx, launch_quantize_weight(g, w, codes, scales, reinterpret_cast<cudaStream_t>(stream),
-                                                 &ctx->last_launches));
+                                                 &launched.n));
 }
 
 dsa_status dsa_project_fp8(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_project_t *shape, const void *a,
@@ -870,12 +879,12 @@ dsa_status dsa_project_fp8(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_pro
   int32_t per_row;
   dsa_status st = check_rows(ctx, plan, g.rows, &count, &per_row);
   if (st != DSA_OK) return st;
-  ctx->last_launches = 0;
+  LaunchCount launched(ctx);
   if (g.rows == 0) return DSA_OK;
   if (!apart(g.n, g.rows, g.out_stride, g.batch, g.out_batch)) return DSA_ERR_INVALID_ARG;
   if (!a || !a_scale || !w || !w_scale || !out) return DSA_ERR_INVALID_ARG;
   return cuda_status(ctx, launch_project_fp8(ctx, g, a, a_scale, w, w_scale, out, count, per_row,
-                                             reinterpret_cast<cudaStream_t>(stream), &ctx->last_launches));
+                                             reinterpret_cast<cudaStream_t>(stream), &launched.n));
 }
 
 int dsa_project_on_tensor_cores(const dsa_project_t *shape, const void *a, const void *w) {
@@ -896,8 +905,8 @@ dsa_status dsa_get_error(dsa_ctx_t *ctx, dsa_stream_t stream) {
   return DSA_OK;
 }
 
-int32_t dsa_last_launch_count(const dsa_ctx_t *ctx) { return ctx ? ctx->last_launches : 0; }
+int32_t dsa_last_launch_count(const dsa_ctx_t *ctx) { return ctx ? ctx->last_launches.load(std::memory_order_relaxed) : 0; }
 
-const char *dsa_last_cuda_error(const dsa_ctx_t *ctx) { return ctx ? ctx->last_cuda_error : ""; }
+const char *dsa_last_cuda_error(const dsa_ctx_t *ctx) { return ctx ? ctx->last_cuda_error.load(std::memory_order_acquire) : ""; }
 
 }  // extern "C"

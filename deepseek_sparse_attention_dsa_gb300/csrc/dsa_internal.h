@@ -207,12 +207,38 @@ struct dsa_ctx {
   float *opart = nullptr;         // attention partial outputs [slots][H][L]
   float *mlpart = nullptr;        // attention partial (m, l) [slots][H][2]
   size_t part_cap = 0;            // slots
-  int32_t last_launches = 0;
-  char last_cuda_error[160] = {0};  // name and text of the last CUDA error a call returned DSA_ERR_CUDA for
+  // Written by every call, the 8-bit rows' and projections' from any thread: the
+  // last call to end decides.
+  std::atomic<int32_t> last_launches{0};
+  std::atomic<const char *> last_cuda_error{""};   // name and text of the last CUDA error a call returned DSA_ERR_CUDA for
   float *static_scores = nullptr; // device address of the library's fixed score array (dsa_index_topk_static)
   uint32_t *block_keys = nullptr; // MSA block maxima scratch (dsa_msa_index_select)
   size_t block_keys_cap = 0;      // words
 };
+
+namespace dsa {
+
+// Counts a call's launches and leaves the number in the context when the call ends.
+struct LaunchCount {
+  explicit LaunchCount(dsa_ctx *c) : ctx(c) {}
+  ~LaunchCount() { ctx->last_launches.store(n, std::memory_order_relaxed); }
+  LaunchCount(const LaunchCount &) = delete;
+  LaunchCount &operator=(const LaunchCount &) = delete;
+  dsa_ctx *const ctx;
+  int32_t n = 0;
+};
+
+// Name and text of a CUDA error: made once, valid as long as the library is loaded.
+const char *cuda_error_text(cudaError_t e);
+
+// DSA_OK, or DSA_ERR_CUDA with the CUDA error recorded in the context.
+inline dsa_status cuda_status(dsa_ctx *ctx, cudaError_t e) {
+  if (e == cudaSuccess) return DSA_OK;
+  ctx->last_cuda_error.store(cuda_error_text(e), std::memory_order_release);
+  return DSA_ERR_CUDA;
+}
+
+}  // namespace dsa
 
 struct dsa_plan {
   dsa_ctx *ctx = nullptr;

@@ -49,7 +49,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <cstdio>
 
 #include "dsa_internal.h"
 #include "ptx.cuh"
@@ -1264,12 +1263,6 @@ dsa_status msa_check(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_msa_shape
   return DSA_OK;
 }
 
-dsa_status msa_status(dsa_ctx_t *ctx, cudaError_t e) {
-  if (e == cudaSuccess) return DSA_OK;
-  snprintf(ctx->last_cuda_error, sizeof(ctx->last_cuda_error), "%s: %s", cudaGetErrorName(e), cudaGetErrorString(e));
-  return DSA_ERR_CUDA;
-}
-
 }  // namespace
 
 extern "C" {
@@ -1278,19 +1271,19 @@ dsa_status dsa_msa_select_blocks(dsa_ctx_t *ctx, const dsa_plan_t *plan, const d
                                  const float *scores, int32_t *block_sel, dsa_stream_t stream) {
   dsa_status st = msa_check(ctx, plan, shape);
   if (st != DSA_OK) return st;
-  ctx->last_launches = 0;
+  dsa::LaunchCount launched(ctx);
   if (!dsa::msa_select_supported(plan, *shape)) return DSA_ERR_UNSUPPORTED;
   if (plan->T == 0) return DSA_OK;
   if (!scores || !block_sel) return DSA_ERR_INVALID_ARG;
-  return msa_status(ctx, dsa::launch_msa_select(ctx, plan, *shape, scores, nullptr, block_sel,
-                                                reinterpret_cast<cudaStream_t>(stream), &ctx->last_launches));
+  return dsa::cuda_status(ctx, dsa::launch_msa_select(ctx, plan, *shape, scores, nullptr, block_sel,
+                                                reinterpret_cast<cudaStream_t>(stream), &launched.n));
 }
 
 dsa_status dsa_msa_index_select(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_msa_shape_t *shape, const void *q,
                                 const float *w, const void *index_cache, int32_t *block_sel, dsa_stream_t stream) {
   dsa_status st = msa_check(ctx, plan, shape);
   if (st != DSA_OK) return st;
-  ctx->last_launches = 0;
+  dsa::LaunchCount launched(ctx);
   if (!dsa::msa_select_supported(plan, *shape)) return DSA_ERR_UNSUPPORTED;
   if (plan->T == 0) return DSA_OK;
   if (!q || !w || !index_cache || !block_sel) return DSA_ERR_INVALID_ARG;
@@ -1316,8 +1309,8 @@ dsa_status dsa_msa_index_select(dsa_ctx_t *ctx, const dsa_plan_t *plan, const ds
     e = dsa::launch_index_scores(ctx, plan, q, w, index_cache, ctx->scores, s, &n);
     if (e == cudaSuccess) e = dsa::launch_msa_select(ctx, plan, *shape, ctx->scores, nullptr, block_sel, s, &n);
   }
-  ctx->last_launches = n;
-  return msa_status(ctx, e);
+  launched.n = n;
+  return dsa::cuda_status(ctx, e);
 }
 
 dsa_status dsa_msa_attend(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_msa_shape_t *shape,
@@ -1325,7 +1318,7 @@ dsa_status dsa_msa_attend(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_msa_
                           dsa_stream_t stream) {
   dsa_status st = msa_check(ctx, plan, shape);
   if (st != DSA_OK) return st;
-  ctx->last_launches = 0;
+  dsa::LaunchCount launched(ctx);
   if (plan->T == 0) return DSA_OK;
   if (!block_sel || !q || !kv_cache || !out) return DSA_ERR_INVALID_ARG;
   if (!dsa::msa_attend_tc_supported(ctx->cfg, *shape, plan->box_rows) &&
@@ -1333,8 +1326,8 @@ dsa_status dsa_msa_attend(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_msa_
               sizeof(float) >
           227 * 1024)
     return DSA_ERR_UNSUPPORTED;
-  return msa_status(ctx, dsa::launch_msa_attend(ctx, plan, *shape, block_sel, q, kv_cache, sm_scale, out,
-                                                reinterpret_cast<cudaStream_t>(stream), &ctx->last_launches));
+  return dsa::cuda_status(ctx, dsa::launch_msa_attend(ctx, plan, *shape, block_sel, q, kv_cache, sm_scale, out,
+                                                reinterpret_cast<cudaStream_t>(stream), &launched.n));
 }
 
 int dsa_msa_attend_on_tensor_cores(const dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_msa_shape_t *shape) {

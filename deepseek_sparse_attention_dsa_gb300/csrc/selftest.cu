@@ -13,8 +13,6 @@
 // memory and exits.  No fault, trap or unbounded wait is involved.
 #include <cuda_runtime.h>
 
-#include <cstdio>
-
 #include "dsa_internal.h"
 #include "ptx.cuh"
 
@@ -134,12 +132,7 @@ dsa_status run(void (*kern)(int *, Limit, int64_t *), dsa_ctx_t *ctx, uint64_t l
   if (cudaSetDevice(ctx->device) != cudaSuccess) return DSA_ERR_CUDA;
   kern<<<1, 64, 0, reinterpret_cast<cudaStream_t>(stream)>>>(ctx->err, static_cast<Limit>(limit_ns), result);
   ctx->last_launches = 1;
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) {
-    snprintf(ctx->last_cuda_error, sizeof(ctx->last_cuda_error), "%s: %s", cudaGetErrorName(e), cudaGetErrorString(e));
-    return DSA_ERR_CUDA;
-  }
-  return DSA_OK;
+  return cuda_status(ctx, cudaGetLastError());
 }
 
 }  // namespace

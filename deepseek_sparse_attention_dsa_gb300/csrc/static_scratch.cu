@@ -19,8 +19,6 @@
 // the array and must be serialised by the caller.
 #include <cuda_runtime.h>
 
-#include <cstdio>
-
 #include "dsa_internal.h"
 
 namespace {
@@ -55,17 +53,13 @@ extern "C" dsa_status dsa_index_topk_static(dsa_ctx_t *ctx, const dsa_plan_t *pl
   if (plan->num_scores > static_cast<int64_t>(DSA_STATIC_SCORES_MAX)) return DSA_ERR_SCRATCH_LIMIT;
   if (!ctx->static_scores) return DSA_ERR_INVALID_ARG;   // dsa_create records the address for every device context
   if (cudaSetDevice(ctx->device) != cudaSuccess) return DSA_ERR_CUDA;
-  ctx->last_launches = 0;
+  dsa::LaunchCount launched(ctx);
   if (plan->T == 0) return DSA_OK;
   if (!q || !w || !index_cache || !selection) return DSA_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int32_t n = 0;
   cudaError_t e = dsa::launch_index_scores(ctx, plan, q, w, index_cache, ctx->static_scores, s, &n);
   if (e == cudaSuccess) e = dsa::launch_topk(ctx, plan, ctx->static_scores, selection, s, &n);
-  ctx->last_launches = n;
-  if (e != cudaSuccess) {
-    snprintf(ctx->last_cuda_error, sizeof(ctx->last_cuda_error), "%s: %s", cudaGetErrorName(e), cudaGetErrorString(e));
-    return DSA_ERR_CUDA;
-  }
-  return DSA_OK;
+  launched.n = n;
+  return dsa::cuda_status(ctx, e);
 }

@@ -399,7 +399,8 @@ int dsa_msa_attend_on_tensor_cores(const dsa_ctx_t *ctx, const dsa_plan_t *plan,
  *
  * The calls use a context for its device, error word and launch count only:
  * its shape and formats are not read.  They need no workspace, and calls on
- * different streams or threads share nothing.  Their kernels are launched with
+ * different streams or threads share nothing but the context's launch count and
+ * error text, which are those of the last call to end.  Their kernels are launched with
  * programmatic stream serialization: set up while the stream's previous kernel
  * still runs, they wait for its end before they read or write global memory, and
  * a kernel that a caller launches after them in the same way does so too.  `plan` may be
@@ -511,13 +512,14 @@ dsa_status dsa_selftest_wait_timeout(dsa_ctx_t *ctx, uint64_t limit_ns, int64_t 
 dsa_status dsa_selftest_warp_wait_timeout(dsa_ctx_t *ctx, uint64_t limit_ns, int64_t *result, dsa_stream_t stream);
 
 /* Number of kernels the last compute call on this context launched (for
- * accounting; host-side counter, no synchronisation). */
+ * accounting; host-side counter, no synchronisation): of calls from several
+ * threads, one that ended last. */
 int32_t dsa_last_launch_count(const dsa_ctx_t *ctx);
 
 const char *dsa_status_str(dsa_status s);
 
 /* Name and text of the CUDA error behind the context's last DSA_ERR_CUDA
- * ("" when there was none); owned by the context. */
+ * ("" when there was none); owned by the library, and valid as long as it is loaded. */
 const char *dsa_last_cuda_error(const dsa_ctx_t *ctx);
 
 #ifdef __cplusplus

@@ -394,3 +394,35 @@ def test_sums_that_cross_ctas_are_whole(ctx, rows, n, k):
     for i, out in enumerate(outs):
         assert torch.equal(out, want[i % 4]), i
     ctx.get_error()
+
+
+def test_threads_leave_a_launch_count_of_one_call(ctx):
+    """One launch a call: the count that a call leaves is one, also where another
+    thread's calls begin and end while it waits for room in its stream."""
+    import threading
+    import time
+    x = torch.randn(3, 256, device="cuda").to(BF16)
+    codes, scales = ctx.quantize_rows(x)
+    full, free = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    seen, done = set(), threading.Event()
+
+    def fill():     # more calls than a stream takes while its first kernel runs: one of them waits
+        with torch.cuda.stream(full):
+            torch.cuda._sleep(600_000_000)      # some 0.3 s
+            for _ in range(3000):
+                ctx.quantize_rows(x, codes, scales)
+                seen.add(ctx.last_launch_count())
+        done.set()
+
+    filler = threading.Thread(target=fill)
+    filler.start()
+    while not done.is_set():
+        ctx.quantize_rows(x, stream=free)
+        seen.add(ctx.last_launch_count())
+        time.sleep(0.002)
+    filler.join()
+    torch.cuda.synchronize()
+    assert seen == {1}
+    assert dsa.load().dsa_last_cuda_error(ctx.handle) == b""
+    ctx.get_error()
