@@ -40,6 +40,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import threading
 from typing import Optional, Sequence
 
 import numpy as np
@@ -129,6 +130,7 @@ class PlanInfo(ctypes.Structure):
 
 _lib = None
 _binding = None
+_binding_lock = threading.Lock()
 
 
 def library_path() -> str:
@@ -199,21 +201,22 @@ def load() -> ctypes.CDLL:
     return L
 
 
-def _load_binding():
+def load_binding():
     """The extension module that passes tensors to the 8-bit calls (csrc/binding.cpp); raises if it has not been built."""
     global _binding
-    if _binding is None:
-        load()
-        path = os.path.join(os.path.dirname(LIB_PATH), "_dsa_binding.so")
-        if not os.path.exists(path):
-            raise RuntimeError("_dsa_binding.so is not built (%s); run "
-                               "`python -m deepseek_sparse_attention_dsa_gb300.build`" % path)
-        spec = importlib.util.spec_from_file_location("_dsa_binding", path)
-        module = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(module)
-        module.set_check(lambda status, what, handle: _check(status, what, ctypes.c_void_p(handle)))
-        _binding = module
-    return _binding
+    with _binding_lock:
+        if _binding is None:
+            load()
+            path = os.path.join(os.path.dirname(LIB_PATH), "_dsa_binding.so")
+            if not os.path.exists(path):
+                raise RuntimeError("_dsa_binding.so is not built (%s); run "
+                                   "`python -m deepseek_sparse_attention_dsa_gb300.build`" % path)
+            spec = importlib.util.spec_from_file_location("_dsa_binding", path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.set_check(lambda status, what, handle: _check(status, what, ctypes.c_void_p(handle)))
+            _binding = module
+        return _binding
 
 
 def _status_str(s: int) -> str:
@@ -313,7 +316,6 @@ class Context:
         h = ctypes.c_void_p()
         _check(L.dsa_create(ctypes.byref(cfg), int(device), ctypes.byref(h)), "dsa_create")
         self.handle = h
-        self._rows = _load_binding()
         self.shape = shape
         self.device_index = int(device)
         self.device = torch.device("cuda", device) if device >= 0 else torch.device("cpu")
@@ -499,6 +501,12 @@ class Context:
     # ---------------------------------------------- 8-bit rows and projections
     # (their tensors are read and made in csrc/binding.cpp: these calls are short
     # enough for the host's part to count)
+    def __getattr__(self, name):
+        if name != "_rows":
+            raise AttributeError(name)
+        self._rows = load_binding()   # at the first of these calls: the others do without
+        return self._rows
+
     def _address(self):
         return self.handle.value if self.handle else 0   # (closed: the call refuses it)
 
