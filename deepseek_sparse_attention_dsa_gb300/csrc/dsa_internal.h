@@ -231,9 +231,11 @@ struct LaunchCount {
 // Name and text of a CUDA error: made once, valid as long as the library is loaded.
 const char *cuda_error_text(cudaError_t e);
 
-// DSA_OK, or DSA_ERR_CUDA with the CUDA error recorded in the context.
+// DSA_OK, or DSA_ERR_CUDA with the CUDA error recorded in the context and taken
+// from the runtime, which would hand it to the next call that asks for its own.
 inline dsa_status cuda_status(dsa_ctx *ctx, cudaError_t e) {
   if (e == cudaSuccess) return DSA_OK;
+  cudaGetLastError();
   ctx->last_cuda_error.store(cuda_error_text(e), std::memory_order_release);
   return DSA_ERR_CUDA;
 }
