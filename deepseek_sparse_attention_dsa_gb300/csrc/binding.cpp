@@ -110,6 +110,10 @@ bool view(const Call &call, PyObject *o, const char *name, Kind kind, at::IntArr
     PyErr_Format(PyExc_ValueError, "%s must have adjacent values in its last dimension", name);
     return false;
   }
+  if (t.is_neg() || t._is_zerotensor()) {   // (their memory does not hold their values)
+    PyErr_Format(PyExc_ValueError, "%s is a view that negates its memory, or has none", name);
+    return false;
+  }
   for (size_t i = 0; i + 1 < shape.size(); ++i) v->stride[i] = strides[i];
   v->p = t.data_ptr();
   return true;

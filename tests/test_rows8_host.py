@@ -140,3 +140,17 @@ def test_sizes_beyond_the_limits_are_told_from_bad_ones(ctx, lib):
 def test_new_entry_points_are_exported(lib):
     for name in ("dsa_rmsnorm", "dsa_quantize_rows", "dsa_quantize_weight", "dsa_project_fp8", "dsa_project_on_tensor_cores"):
         assert name in dsa.EXPORTED and hasattr(lib, name)
+
+
+def test_views_that_negate_their_memory_are_refused(ctx):
+    """The imaginary part of a conjugate: its memory holds the other sign."""
+    c = torch.conj(torch.randn(4, 1, dtype=torch.complex64))
+    x = c.imag
+    assert x.is_neg() and x.dtype == F32
+    for call in (lambda: ctx.rmsnorm(x, None), lambda: ctx.quantize_rows(x), lambda: ctx.quantize_weight(x),
+                 lambda: ctx.rmsnorm(torch.zeros(4, 1), None, residual=x),
+                 lambda: ctx.project_fp8(torch.zeros(4, 1, dtype=U8), x, torch.zeros(1, 1, dtype=U8), torch.zeros(1, 1))):
+        with pytest.raises(ValueError, match="negates"):
+            call()
+    with pytest.raises(dsa.DSAError):       # written out it goes as far as the host-only context
+        ctx.quantize_rows(x.resolve_neg())
