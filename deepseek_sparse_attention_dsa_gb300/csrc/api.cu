@@ -774,6 +774,9 @@ dsa_status dsa_attend_shared(dsa_ctx_t *ctx, const dsa_plan_t *plan, const void 
 
 static bool is_type(int32_t t) { return t == DSA_BF16 || t == DSA_FP32; }
 
+// Whether p is aligned for values of its type (a null pointer is).
+static bool aligned(const void *p, int32_t type) { return reinterpret_cast<uintptr_t>(p) % (type == DSA_BF16 ? 2 : 4) == 0; }
+
 // Whether c1 x c2 runs of `inner` written elements at strides s1 and s2 keep
 // clear of one another: one stride steps over a run, the other over all the
 // runs of the first.
@@ -823,7 +826,9 @@ dsa_status dsa_rmsnorm(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_norm_t 
   if ((residual_out && !apart(n.width, n.rows, n.residual_out_stride)) || (out && !apart(n.width, n.rows, n.out_stride)) ||
       (codes && (!apart(n.width, n.rows, n.codes_stride) || !apart((n.width + 127) / 128, n.rows, n.scales_stride))))
     return DSA_ERR_INVALID_ARG;
-  if (!x) return DSA_ERR_INVALID_ARG;
+  if (!x || !aligned(x, n.x_type) || !aligned(weight, n.weight_type) || !aligned(residual, n.residual_type) ||
+      !aligned(residual_out, n.residual_type) || !aligned(out, n.out_type) || !aligned(scales, DSA_FP32))
+    return DSA_ERR_INVALID_ARG;
   return cuda_status(ctx, launch_rmsnorm(ctx->num_sms, n, x, weight, residual, residual_out, out, codes, scales, count, per_row,
                                          reinterpret_cast<cudaStream_t>(stream), &launched.n));
 }
@@ -842,7 +847,7 @@ dsa_status dsa_quantize_rows(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_r
   if (r.rows == 0) return DSA_OK;
   if (!apart(r.width, r.rows, r.codes_stride) || !apart((static_cast<int64_t>(r.width) + 127) / 128, r.rows, r.scales_stride))
     return DSA_ERR_INVALID_ARG;
-  if (!x || !codes || !scales) return DSA_ERR_INVALID_ARG;
+  if (!x || !codes || !scales || !aligned(x, r.x_type) || !aligned(scales, DSA_FP32)) return DSA_ERR_INVALID_ARG;
   if ((static_cast<int64_t>(r.width) / 1024 + 1) * r.rows > 8ll * INT32_MAX) return DSA_ERR_UNSUPPORTED;   // the grid
   return cuda_status(ctx, launch_quantize_rows(r, x, codes, scales, count, per_row,
                                                reinterpret_cast<cudaStream_t>(stream), &launched.n));
@@ -853,7 +858,8 @@ dsa_status dsa_quantize_weight(dsa_ctx_t *ctx, const dsa_weight_t *shape, const 
   if (is_host_only(ctx) || !shape) return DSA_ERR_INVALID_ARG;
   const dsa_weight_t &g = *shape;
   if (g.batch < 1 || g.n < 1 || g.k < 1 || !is_type(g.w_type) || g.w_stride < 0 || g.w_batch < 0 ||
-      g.codes_stride < 0 || g.codes_batch < 0 || g.scales_stride < 0 || g.scales_batch < 0 || !w || !codes || !scales)
+      g.codes_stride < 0 || g.codes_batch < 0 || g.scales_stride < 0 || g.scales_batch < 0 || !w || !codes || !scales ||
+      !aligned(w, g.w_type) || !aligned(scales, DSA_FP32))
     return DSA_ERR_INVALID_ARG;
   if (!apart(g.k, g.n, g.codes_stride, g.batch, g.codes_batch) ||
       !apart((static_cast<int64_t>(g.k) + 127) / 128, (g.n + 127) / 128, g.scales_stride, g.batch, g.scales_batch))
@@ -882,7 +888,9 @@ dsa_status dsa_project_fp8(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_pro
   LaunchCount launched(ctx);
   if (g.rows == 0) return DSA_OK;
   if (!apart(g.n, g.rows, g.out_stride, g.batch, g.out_batch)) return DSA_ERR_INVALID_ARG;
-  if (!a || !a_scale || !w || !w_scale || !out) return DSA_ERR_INVALID_ARG;
+  if (!a || !a_scale || !w || !w_scale || !out || !aligned(a_scale, DSA_FP32) || !aligned(w_scale, DSA_FP32) ||
+      !aligned(out, g.out_type))
+    return DSA_ERR_INVALID_ARG;
   return cuda_status(ctx, launch_project_fp8(ctx, g, a, a_scale, w, w_scale, out, count, per_row,
                                              reinterpret_cast<cudaStream_t>(stream), &launched.n));
 }

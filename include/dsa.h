@@ -413,7 +413,8 @@ int dsa_msa_attend_on_tensor_cores(const dsa_ctx_t *ctx, const dsa_plan_t *plan,
  * batch, to the next; a row's own values are adjacent.  Rows must not overlap
  * in anything written (what is only read may overlap or repeat).  Any stride and
  * alignment is accepted (of the type's own size); 16-byte aligned rows run
- * faster, and project_fp8 needs them for the tensor cores.  DSA_ERR_INVALID_ARG: null pointers, sizes below 1 (rows may be
+ * faster, and project_fp8 needs them for the tensor cores.  DSA_ERR_INVALID_ARG: null
+ * pointers, pointers off their type's own size, sizes below 1 (rows may be
  * 0: nothing is launched), unknown types, negative strides, written rows
  * that would overlap, or rows that do not match the plan; DSA_ERR_UNSUPPORTED: sizes beyond the limits given below. */
 enum { DSA_BF16 = 0, DSA_FP32 = 1 };

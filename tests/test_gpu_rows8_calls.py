@@ -49,3 +49,30 @@ def test_a_launch_that_is_refused_spoils_no_later_call(ctx):
     assert cudart.cudaStreamDestroy(own) == 0
     assert torch.equal(ctx.quantize_rows(x)[0], want)
     ctx.get_error()
+
+
+def test_pointers_off_their_type_are_refused(ctx):
+    """Through the C calls (a tensor is always on its type's size): each pointer in turn one byte, or half a float, off."""
+    L = dsa.load()
+    store = torch.zeros(16 * 4096, dtype=U8, device="cuda")
+    base = store.data_ptr()
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    norm = dsa._Norm(rows=2, width=128, x_type=0, weight_type=1, residual_type=1, out_type=0, eps=1e-6, x_stride=128, residual_stride=128,
+                     residual_out_stride=128, out_stride=128, codes_stride=128, scales_stride=1)
+    rows = dsa._Rows(rows=2, width=128, x_type=1, x_stride=128, codes_stride=128, scales_stride=1)
+    weight = dsa._Weight(batch=1, n=2, k=128, w_type=0, w_stride=128, codes_stride=128, scales_stride=1)
+    project = dsa._Project(rows=2, batch=1, n=2, k=128, out_type=0, a_stride=128, a_scale_stride=1, w_stride=128, w_scale_stride=1, out_stride=2)
+    # the call with its tensors in order, and the bytes that each has to be on
+    calls = ((lambda *p: L.dsa_rmsnorm(ctx.handle, None, ctypes.byref(norm), *p, stream), (2, 4, 4, 4, 2, 1, 4)),
+             (lambda *p: L.dsa_quantize_rows(ctx.handle, None, ctypes.byref(rows), *p, stream), (4, 1, 4)),
+             (lambda *p: L.dsa_quantize_weight(ctx.handle, ctypes.byref(weight), *p, stream), (2, 1, 4)),
+             (lambda *p: L.dsa_project_fp8(ctx.handle, None, ctypes.byref(project), *p, stream), (1, 4, 1, 4, 2)))
+    for call, on in calls:
+        at = [base + 4096 * i for i in range(len(on))]
+        assert call(*map(ctypes.c_void_p, at)) == dsa.DSA_OK
+        for i, size in enumerate(on):
+            for off in {1, size // 2, size - 1} - {0}:
+                moved = at[:i] + [at[i] + off] + at[i + 1:]
+                got = call(*map(ctypes.c_void_p, moved))
+                assert got == (1 if size > 1 else dsa.DSA_OK), (i, off)
+    ctx.get_error()
