@@ -76,3 +76,76 @@ def test_pointers_off_their_type_are_refused(ctx):
                 got = call(*map(ctypes.c_void_p, moved))
                 assert got == (1 if size > 1 else dsa.DSA_OK), (i, off)
     ctx.get_error()
+
+
+def test_a_captured_fork_and_join(ctx):
+    """Two streams in one graph whose launches overlap with each other's: the
+    norm's codes go into two projections on two streams, whose outputs are
+    quantised after the join; replayed over new inputs in the same buffers."""
+    g = torch.Generator().manual_seed(4)
+    ws = [ctx.quantize_weight((torch.randn(n, 1024, generator=g) / 32).to(BF16).cuda()) for n in (512, 2048)]
+    x, res = (torch.zeros(70, 1024, dtype=BF16, device="cuda") for _ in range(2))
+
+    def step(main, side):
+        codes, scales, h = ctx.rmsnorm_quantize(x, None, residual=res)
+        fork, join = torch.cuda.Event(), torch.cuda.Event()
+        fork.record(main)
+        side.wait_event(fork)
+        with torch.cuda.stream(side):
+            b = ctx.project_fp8(codes, scales, *ws[1])
+            bq = ctx.quantize_rows(b)
+            join.record(side)
+        a = ctx.project_fp8(codes, scales, *ws[0])
+        main.wait_event(join)
+        return [codes, scales, h, a, b, *bq, *ctx.quantize_rows(a), ctx.rmsnorm(b, None)]
+
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(main):
+        step(main, side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        got = step(main, side)
+    for seed in range(5, 9):
+        x.copy_(rand(seed, 70, 1024))
+        res.copy_(rand(seed + 50, 70, 1024))
+        torch.cuda.synchronize()
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in got]
+        with torch.cuda.stream(main):
+            want = step(main, side)
+        torch.cuda.synchronize()
+        for i, (p, q) in enumerate(zip(kept, want)):
+            assert torch.equal(p, q), (seed, i)
+    ctx.get_error()
+
+
+def test_the_same_tensor_as_both_operands(ctx):
+    """A product of codes with themselves: whole numbers, so exact."""
+    g = torch.Generator().manual_seed(5)
+    for rows in (1, 40, 200):
+        codes = torch.randint(-3, 4, (rows, 384), generator=g).float().to(torch.float8_e4m3fn).cuda()
+        ones = torch.ones(rows, 3, device="cuda")
+        out = ctx.project_fp8(codes, ones, codes, torch.ones(-(-rows // 128), 3, device="cuda"), out_dtype=F32)
+        v = codes.float()
+        assert torch.equal(out, v @ v.t()) or torch.equal(out.double(), v.double() @ v.double().t())
+    ctx.get_error()
+
+
+def test_no_rows_and_rows_that_are_all_padding(ctx):
+    """Nothing to do, with and without a plan: nothing is written, nothing is wrong."""
+    from tests.test_gpu_rows8 import capturable
+    plan = capturable(ctx, 0)
+    empty = ctx.plan([], 1)
+    w = torch.zeros(128, 256, dtype=U8, device="cuda"), torch.ones(1, 2, device="cuda")
+    for rows, p in ((0, None), (0, empty), (0, plan), (8, plan), (64, plan)):
+        x = torch.full((rows, 256), float("nan"), dtype=BF16, device="cuda")
+        out, codes = torch.full((rows, 256), 7.0, dtype=BF16, device="cuda"), torch.full((rows, 256), 9, dtype=U8, device="cuda")
+        scales, y = torch.full((rows, 2), 5.0, device="cuda"), torch.full((rows, 128), 3.0, dtype=BF16, device="cuda")
+        ctx.rmsnorm(x, None, out=out, plan=p)
+        ctx.quantize_rows(x, codes, scales, plan=p)
+        ctx.project_fp8(codes, scales, *w, out=y, plan=p)
+        assert (out == 7).all() and (codes == 9).all() and (scales == 5).all() and (y == 3).all()
+    ctx.get_error()
