@@ -15,9 +15,9 @@
 // project_tc_kernel, few rows: a tile is 128 weight rows (the MMA's 128 lanes) by
 // NT = 16, 32 or 64 tokens (its columns); two helper warps put s for the tile's
 // tokens into shared memory ahead of the epilogue.  Bound by the weights' bytes:
-// 16 x 8192 x 8192 takes 13.3 us on one GB300, 67 MB at 5.0 TB/s, of which some
-// 3 us are the first loads' latency and the last block's way out (1 x 8192 x
-// 2048: 4.0 us).
+// 16 x 8192 x 8192 takes 12.9 us on one GB300 with the weights in DRAM, 67 MB at
+// 5.2 TB/s, of which some 3 us are the first loads' latency and the last block's way
+// out (8.2 us where they are in L2; 1 x 8192 x 2048: 5.4 and 3.9 us).
 //
 // project_rows_kernel, more rows: tokens are the lanes (see there).
 //
@@ -858,7 +858,11 @@ __device__ __forceinline__ float e4m3_value(uint8_t c) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
 }
 
-// CUDA-core form, for codes that are not on 16 bytes: 64 x 64 outputs a CTA, 4 x 4 a thread.
+// CUDA-core form, for codes that are not on 16 bytes (or have a stride of 0): 64 x 64
+// outputs a CTA, 4 x 4 a thread.  Right, and slow: a byte of codes a load, products on
+// the FMA pipe, nothing of the next block in flight (8192 x 8192, k 4100: 22.2 ms where
+// k 4096 takes 0.2 and 32-bit products of a library 8.6; 128 x 8192, k 4100: 436 us
+// against 10; 1 x 8192, k 2052: 210 us against 5).
 __global__ void __launch_bounds__(256) project_simt_kernel(const ProjectParams p) {
   __shared__ float as[32][65], ws[32][65];
   grid_dependency();
@@ -976,7 +980,9 @@ cudaError_t run_tc(const dsa_ctx *ctx, const dsa_project_t &g, ProjectParams &p,
 // Clusters of `ctas` CTAs, one to an SM, that the device holds at once: less than
 // its SMs allow, as a cluster lies within a group of them (a GB300 with 152 SMs
 // holds 36 of four and 15 of eight; 48 x 2048 x 8192 on 16 clusters of eight took
-// 11.1 us, on as many of four 7.4).  Asked of the driver once a device.
+// 11.1 us, on as many of four 7.4).  Asked of the driver once a device, for
+// project_tc_kernel<64>, and used for every form: all of them take more than half of
+// an SM's shared memory, which makes it one CTA an SM whichever it is.
 int clusters_at_once(const dsa_ctx *ctx, int ctas) {
   if (ctas <= 2) return ctx->num_sms / ctas;
   static std::atomic<int> known[64][2];
@@ -1003,14 +1009,20 @@ int clusters_at_once(const dsa_ctx *ctx, int ctas) {
 
 // The kernel (tokens a tile: 16, 32, 64 with weights on the lanes; 128 on one
 // CTA and 256 on a pair with tokens on the lanes, 257 the pair with 256 columns)
-// and the CTAs, or pairs, that split a tile's k: the least of what the measured
-// times of a block of k, of a tile's end, of a pair's start and of a split (us) make
-// of the blocks that the busiest CTA gets.  Measured on either side of its choices (us a
-// call): 128 x 8192 x 4096 9.5 with {128, 2 CTAs}, 11.4 with {64}, 12.5 with {128};
+// and the CTAs, or pairs, that split a tile's k: the least of what a time for a block
+// of k, one for a tile's end, one for a pair's start and one for a split (us) make of
+// the blocks that the busiest CTA gets.  The times are a fit, by random search, to
+// what every form took at 35 sizes with the weights partly in L2; at those the choice
+// is within 1.5% of the best form.  At 30 sizes that had no part in it, drawn over
+// the logarithms of 1-4000 rows, 256-24576 columns and k of 256-16384, it was within 4%
+// at 28 and 19 and 21% slower at two, where more than two tiles of some forms fall to a
+// CTA (2643 x 1984 x 608: {257} 10.0 us, {256} 8.4; 1829 x 5864 x 6192: {256} 82 us, {257}
+// 68).  Measured on either side of its choices (us a call): 128 x 8192 x 4096 9.5 with
+// {128, 2 CTAs}, 11.4 with {64}, 12.5 with {128};
 // 200 x 4096 x 4096 8.2 with {256, 2 pairs}, 8.8 with {128, 2 CTAs}, 10.4 with {64};
 // 256 x 8192 x 4096 13.0 with {256}, 13.1 with {128}, 16.6 with {257}; 1024 x 4096 x
 // 4096 18.0 with {257}, 21.7 with {128}; 16 x 8192 x 2048 4.5 with {16, 2}, 5.0 with
-// {16}.  Of 35 sizes it comes within 1.5% of the best form in every one.
+// {16}.
 void choose(const dsa_ctx *ctx, const dsa_project_t &g, int *nt, int *split) {
   struct Form {
     int nt, m, n, ctas, max_split;

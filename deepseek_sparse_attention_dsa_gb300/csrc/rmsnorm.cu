@@ -9,8 +9,10 @@
 // them between the sum of squares and the output, so x, residual and weight
 // are each read once and every output written once.  Bound by HBM for many
 // rows (8192 x 4096 with residual to codes: 36.9 us, 6.39 TB/s, 94% of the
-// measured copy) and by one launch's latency for few (1 x 5120: 2.6 us).  A
-// thread holds CH pieces of eight
+// measured copy) and by one launch's latency for few (1 x 5120: 2.6 us).  fp32 or
+// mixed types, and rows off 16 bytes, take rmsnorm_kernel, a row at a time: the same
+// with x and residual in fp32 71.6 us (6.10 TB/s, 90%), bf16 with an fp32 residual 71.8
+// (5.16 TB/s), bf16 rows at an odd stride 58.9 (4.0 TB/s).  A thread holds CH pieces of eight
 // consecutive columns, piece c of thread t at column (c * THREADS + t) * 8, so
 // 16 neighbouring lanes hold a group of 128 and its maximum is four shuffles.
 #include <cuda_runtime.h>

@@ -553,7 +553,8 @@ class Context:
         """dsa_project_fp8: codes a (rows, k) with scales (rows, ceil(k / 128))
         times w (n, k) with scales per 128 x 128 block -> (rows, n) in
         out_dtype; or for each b, a (rows, batch, k) times w (batch, n, k) ->
-        (rows, batch, n).  Codes are uint8 or float8_e4m3fn."""
+        (rows, batch, n).  Codes are uint8 or float8_e4m3fn; off 16 bytes, or at a
+        stride of 0, they take a far slower kernel (project_on_tensor_cores tells)."""
         return self._rows.project_fp8(self._address(), self.device_index, plan and self._plan_of(plan),
                                       stream and self._stream_of(stream), a, a_scale, w, w_scale, out, out_dtype, False)
 

@@ -391,11 +391,14 @@ int dsa_msa_attend_on_tensor_cores(const dsa_ctx_t *ctx, const dsa_plan_t *plan,
  * the projections themselves (of e4m3 codes, DeepSeek-style scales: one for 128
  * columns of an activation row, one for a block of 128 x 128 of a weight), and
  * the quantisers that feed them.  A value is e4m3(code) * scale.  Quantisation
- * is the rule of dsa_quantize_store_keys: scale = amax / 448 in fp32 (1 where
- * that is zero), code = E4M3(x / scale), rounded to nearest even.  The last
- * group of a row (or block of a matrix) may be cut short.  A group that holds a
- * NaN or an infinity gets a scale that is NaN or infinite, so that none of its
- * values comes back finite.
+ * is the rule of dsa_quantize_store_keys, byte for byte: scale = amax / 448 in
+ * fp32 (1 where that is zero), code = E4M3(x / scale), the fp32 quotient rounded
+ * to nearest even, zeros keeping their sign.  The last group of a row (or block
+ * of a matrix) may be cut short.  A group that holds a NaN or an infinity gets a
+ * scale that is NaN or infinite, so that none of its values comes back finite;
+ * its codes follow the rule, a NaN quotient being 0x7F.  (dsa_quantize_store_*
+ * and dsa_quantize_q expect finite values: there a NaN does not reach the scale
+ * and a quotient that is NaN gets the code of 448.)
  *
  * The calls use a context for its device, error word and launch count only:
  * its shape and formats are not read.  They need no workspace, and calls on
@@ -473,9 +476,14 @@ dsa_status dsa_quantize_weight(dsa_ctx_t *ctx, const dsa_weight_t *shape, const 
  * batch, k), w: codes (batch, n, k), scales as dsa_quantize_rows and
  * dsa_quantize_weight lay them out, out (rows, batch, n); *_batch is the
  * distance between neighbouring b.  Sums are added in a fixed order: equal
- * calls give equal bits.  The tensor cores need a and w on 16 bytes with
- * strides that are multiples of 16 (dsa_project_on_tensor_cores); other
- * layouts run a CUDA-core kernel.  out must not overlap the operands.  n at most 64 * 65535, batch at most 65535. */
+ * calls give equal bits.  The product of two scales is taken first and has
+ * fp32's range.  The tensor cores need a and w on 16 bytes with strides that are
+ * multiples of 16 and not 0 (dsa_project_on_tensor_cores); other layouts, a k
+ * whose rows are packed off 16 bytes or one matrix expanded over the batch among
+ * them, run a CUDA-core kernel that is far slower (8192 x 8192, k 4100: 22 ms
+ * against 0.2 for k 4096, and slower than a plain 32-bit product): copy such
+ * operands, or give their rows a stride that is a multiple of 16.  out must not
+ * overlap the operands.  n at most 64 * 65535, batch at most 65535. */
 typedef struct dsa_project {
   int64_t rows;
   int32_t batch, n, k;
