@@ -66,11 +66,14 @@ def library_up_to_date() -> bool:
     return os.path.exists(LIB) and os.path.getmtime(LIB) >= _library_deps()
 
 
-def binding_up_to_date() -> bool:
-    if not os.path.exists(BINDING) or os.path.getmtime(BINDING) < _binding_deps():
-        return False
-    key = BINDING + ".key"
+def binding_matches(path: str) -> bool:
+    """Whether the module at this path was built for this interpreter and torch."""
+    key = path + ".key"
     return os.path.exists(key) and open(key).read() == _binding_key()
+
+
+def binding_up_to_date() -> bool:
+    return os.path.exists(BINDING) and os.path.getmtime(BINDING) >= _binding_deps() and binding_matches(BINDING)
 
 
 def up_to_date() -> bool:

@@ -46,6 +46,8 @@ from typing import Optional, Sequence
 import numpy as np
 import torch
 
+from . import build
+
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", "libdsa_gb300.so")
 
 DSA_OK = 0
@@ -210,6 +212,9 @@ def load_binding():
             path = os.path.join(os.path.dirname(LIB_PATH), "_dsa_binding.so")
             if not os.path.exists(path):
                 raise RuntimeError("_dsa_binding.so is not built (%s); run "
+                                   "`python -m deepseek_sparse_attention_dsa_gb300.build`" % path)
+            if not build.binding_matches(path):
+                raise RuntimeError("_dsa_binding.so is built for another torch or Python (%s); run "
                                    "`python -m deepseek_sparse_attention_dsa_gb300.build`" % path)
             spec = importlib.util.spec_from_file_location("_dsa_binding", path)
             module = importlib.util.module_from_spec(spec)

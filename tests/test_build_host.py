@@ -64,3 +64,14 @@ def test_contexts_do_without_the_module(tmp_path, monkeypatch):
     monkeypatch.undo()
     with pytest.raises(dsa.DSAError):       # there again: a host-only context is refused by the call itself
         ctx.quantize_rows(torch.zeros(1, 128, dtype=torch.bfloat16))
+
+
+def test_the_module_of_another_torch_is_not_loaded(monkeypatch):
+    dsa.load_binding()
+    key = dsa_build._binding_key()
+    monkeypatch.setattr(dsa, "_binding", None)
+    monkeypatch.setattr(dsa_build, "_binding_key", lambda: key + "0.0")
+    with pytest.raises(RuntimeError, match="another torch"):
+        dsa.load_binding()
+    monkeypatch.undo()
+    dsa.load_binding()
