@@ -11,6 +11,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -383,6 +384,7 @@ dsa_status dsa_plan(dsa_ctx_t *ctx, const dsa_span_t *spans, int32_t num_spans, 
   const size_t bytes = std::max<size_t>(lay.bytes, 256);
   try {
     plan->host.assign(bytes, 0);
+    plan->spans.resize(num_spans);
   } catch (...) {
     delete plan;
     return DSA_ERR_OOM;
@@ -395,11 +397,13 @@ dsa_status dsa_plan(dsa_ctx_t *ctx, const dsa_span_t *spans, int32_t num_spans, 
     auto *ps = reinterpret_cast<int32_t *>(h + o_ps);
     auto *soff = reinterpret_cast<int64_t *>(h + o_soff);
     auto *pg = reinterpret_cast<int32_t *>(h + o_pages);
+    plan->host_pages = pg;
     int32_t row = 0, poff_acc = 0;
     int64_t sacc = 0;
     for (int32_t i = 0; i < num_spans; ++i) {
       const dsa_span_t &s = spans[i];
       if (s.num_pages) std::memcpy(pg + poff_acc, s.pages, sizeof(int32_t) * s.num_pages);
+      plan->spans[i] = PlanSpan{s.q_start, s.q_len, s.ctx_start, s.page_start, poff_acc, s.num_pages};
       for (int32_t r = 0; r < s.q_len; ++r, ++row) {
         pos[row] = s.ctx_start + r;
         poff[row] = poff_acc;
@@ -897,6 +901,172 @@ dsa_status dsa_project_fp8(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_pro
 
 int dsa_project_on_tensor_cores(const dsa_project_t *shape, const void *a, const void *w) {
   return shape && project_tc_supported(*shape, a, w) ? 1 : 0;
+}
+
+// ---------------------------------------------------------------------------
+// rotary positions and appends
+// ---------------------------------------------------------------------------
+// Frequencies in radians a position; false where the configuration has none.
+static bool rotary_frequencies(const dsa_rotary_config_t &c, double *f) {
+  const int n = c.rot_dim / 2;
+  if (c.form == DSA_ROTARY_GIVEN) {
+    for (int i = 0; i < n; ++i) f[i] = c.frequencies[i];
+  } else {
+    if (!(c.base > 1.0) || !std::isfinite(c.base)) return false;
+    for (int i = 0; i < n; ++i) f[i] = std::pow(c.base, -2.0 * i / c.rot_dim);
+  }
+  if (c.form == DSA_ROTARY_LINEAR || c.form == DSA_ROTARY_YARN) {
+    if (!(c.factor > 0.0) || !std::isfinite(c.factor)) return false;
+    double low = 0.0, span = 0.0;
+    if (c.form == DSA_ROTARY_YARN) {
+      if (!(c.original_context > 0.0) || !(c.beta_slow > 0.0) || !(c.beta_fast >= c.beta_slow) ||
+          !std::isfinite(c.original_context) || !std::isfinite(c.beta_fast))
+        return false;
+      constexpr double kTwoPi = 6.283185307179586476925286766559;
+      auto pair = [&](double turns) { return c.rot_dim * std::log(c.original_context / (kTwoPi * turns)) / (2.0 * std::log(c.base)); };
+      low = std::max(std::floor(pair(c.beta_fast)), 0.0);
+      span = std::max(std::min(std::ceil(pair(c.beta_slow)), c.rot_dim - 1.0) - low, 0.001);
+    }
+    for (int i = 0; i < n; ++i) {
+      const double r = c.form == DSA_ROTARY_LINEAR ? 1.0 : std::min(std::max((i - low) / span, 0.0), 1.0);
+      f[i] = f[i] * (1.0 - r) + f[i] / c.factor * r;
+    }
+  }
+  for (int i = 0; i < n; ++i)
+    if (!std::isfinite(f[i])) return false;
+  return true;
+}
+
+dsa_status dsa_rotary_create(dsa_ctx_t *ctx, const dsa_rotary_config_t *cfg, dsa_rotary_t **out) {
+  if (!out) return DSA_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!ctx || !cfg || cfg->rot_dim < 2 || cfg->rot_dim > 1024 || cfg->rot_dim % 2 || cfg->form < DSA_ROTARY_PLAIN ||
+      cfg->form > DSA_ROTARY_GIVEN || !std::isfinite(cfg->amplitude) || (cfg->form == DSA_ROTARY_GIVEN && !cfg->frequencies))
+    return DSA_ERR_INVALID_ARG;
+  double f[512];
+  if (!rotary_frequencies(*cfg, f)) return DSA_ERR_INVALID_ARG;
+  uint64_t turns[512];
+  const int n = cfg->rot_dim / 2;
+  for (int i = 0; i < n; ++i) {
+    // whole turns a position change nothing: the fraction alone, 2^64 of them a turn
+    double t = f[i] / 6.283185307179586476925286766559;
+    t -= std::floor(t);
+    turns[i] = t < 1.0 ? static_cast<uint64_t>(std::ldexp(t, 64)) : 0;
+  }
+  dsa_rotary_t *table = new (std::nothrow) dsa_rotary_t();
+  if (!table) return DSA_ERR_OOM;
+  table->device = ctx->device, table->rot = cfg->rot_dim, table->amplitude = static_cast<float>(cfg->amplitude);
+  if (!is_host_only(ctx)) {
+    cudaError_t e = cudaSetDevice(ctx->device);
+    if (e == cudaSuccess && cudaMalloc(reinterpret_cast<void **>(&table->turns), n * sizeof(uint64_t)) != cudaSuccess) {
+      cudaGetLastError();
+      delete table;
+      return DSA_ERR_OOM;
+    }
+    if (e == cudaSuccess) e = cudaMemcpy(table->turns, turns, n * sizeof(uint64_t), cudaMemcpyHostToDevice);
+    if (e != cudaSuccess) {
+      cudaFree(table->turns);
+      delete table;
+      return cuda_status(ctx, e);
+    }
+  }
+  *out = table;
+  return DSA_OK;
+}
+
+void dsa_rotary_destroy(dsa_rotary_t *table) {
+  if (!table) return;
+  if (table->turns) {
+    cudaSetDevice(table->device);
+    cudaFree(table->turns);
+  }
+  delete table;
+}
+
+static bool is_layout(int32_t l) { return l == DSA_ROTARY_INTERLEAVED || l == DSA_ROTARY_HALF; }
+
+dsa_status dsa_rotate(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_rotary_t *table, const dsa_rotate_t *shape,
+                      const void *x, const int32_t *positions, void *out, dsa_stream_t stream) {
+  if (!ctx || !table || table->device != ctx->device || !shape) return DSA_ERR_INVALID_ARG;
+  const dsa_rotate_t &g = *shape;
+  if (g.heads < 1 || g.width < 1 || g.offset < 0 || static_cast<int64_t>(g.offset) + table->rot > g.width ||
+      !is_layout(g.layout) || (g.inverse != 0 && g.inverse != 1) || !is_type(g.type) || g.x_stride < 0 || g.x_head < 0 ||
+      g.out_stride < 0 || g.out_head < 0 || (plan && positions) || (!plan && !positions && g.rows > 0) ||
+      (plan && g.rows != plan->T))
+    return DSA_ERR_INVALID_ARG;
+  const int32_t *count;
+  int32_t per_row;
+  dsa_status st = check_rows(ctx, plan, g.rows, &count, &per_row);
+  if (st != DSA_OK) return st;
+  LaunchCount launched(ctx);
+  if (g.rows == 0) return DSA_OK;
+  if (!x || !out || !aligned(x, g.type) || !aligned(out, g.type) || !aligned(positions, DSA_FP32) ||
+      !apart(g.width, g.rows, g.out_stride, g.heads, g.out_head) ||
+      (x == out && (g.x_stride != g.out_stride || g.x_head != g.out_head)))
+    return DSA_ERR_INVALID_ARG;
+  if (rotary_ctas(table, g, x == out) > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  return cuda_status(ctx, launch_rotary(table, g, x, plan ? plan->row_pos : positions, plan != nullptr, out,
+                                        reinterpret_cast<cudaStream_t>(stream), &launched.n));
+}
+
+// What both appends ask of their plan, table and index keys.
+static dsa_status check_append(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_rotary_t *table, const dsa_append_t &a,
+                               const void *keys, const void *index_cache) {
+  if ((table && table->device != ctx->device) || !is_layout(a.layout) || !is_layout(a.key_layout) ||
+      !is_type(a.c_type) || !is_type(a.k_pe_type) || !is_type(a.key_type) || !is_type(a.kv_type) || a.c_stride < 0 ||
+      a.k_pe_stride < 0 || a.keys_stride < 0 || a.k_stride < 0 || a.k_head < 0 || a.v_stride < 0 || a.v_head < 0 ||
+      a.kv_offset < 0 || a.key_offset < 0)
+    return DSA_ERR_INVALID_ARG;
+  if (plan && plan->T == 0) return DSA_OK;   // (an empty step's tensors may be null)
+  if ((keys == nullptr) != (index_cache == nullptr)) return DSA_ERR_INVALID_ARG;
+  if (keys) {
+    const dsa_config_t &c = ctx->cfg;
+    if (!aligned(keys, a.key_type) || !aligned(index_cache, c.index_fmt == DSA_INDEX_BF16 ? DSA_BF16 : DSA_FP32) ||
+        (table && static_cast<int64_t>(a.key_offset) + table->rot > c.index_dim))
+      return DSA_ERR_INVALID_ARG;
+  }
+  return DSA_OK;
+}
+
+dsa_status dsa_append_latents(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_rotary_t *table, const dsa_append_t *shape,
+                              const void *c, const void *k_pe, void *latent_cache, const void *keys, void *index_cache,
+                              dsa_stream_t stream) {
+  if (!ctx || !shape) return DSA_ERR_INVALID_ARG;
+  const dsa_append_t &a = *shape;
+  const dsa_config_t &g = ctx->cfg;
+  dsa_status st = check_append(ctx, plan, table, a, keys, index_cache);
+  if (st != DSA_OK) return st;
+  const bool latents = (c || k_pe || latent_cache) && !(plan && plan->T == 0);
+  if (latents) {
+    if (!c || !latent_cache || (!k_pe && g.rope_dim > 0) || (table && g.rope_dim > 0 && table->rot != g.rope_dim) ||
+        !aligned(c, a.c_type) || !aligned(k_pe, a.k_pe_type) ||
+        !aligned(latent_cache, g.latent_fmt == DSA_LATENT_BF16 ? DSA_BF16 : DSA_FP32))
+      return DSA_ERR_INVALID_ARG;
+  }
+  if ((st = check_call(ctx, plan)) != DSA_OK) return st;
+  LaunchCount launched(ctx);
+  if (plan->T == 0) return DSA_OK;
+  if (!latents && !keys) return DSA_ERR_INVALID_ARG;
+  return cuda_status(ctx, launch_append_latents(ctx, plan, table, a, c, k_pe, latent_cache, keys, index_cache,
+                                                reinterpret_cast<cudaStream_t>(stream), &launched.n));
+}
+
+dsa_status dsa_append_kv(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_rotary_t *table, const dsa_msa_shape_t *msa,
+                         const dsa_append_t *shape, const void *k, const void *v, void *kv_cache, const void *keys,
+                         void *index_cache, dsa_stream_t stream) {
+  if (!ctx || !shape || !msa || msa->kv_heads < 1 || msa->head_dim < 1 || msa->reserved != 0) return DSA_ERR_INVALID_ARG;
+  const dsa_append_t &a = *shape;
+  dsa_status st = check_append(ctx, plan, table, a, keys, index_cache);
+  if (st != DSA_OK) return st;
+  if (table && static_cast<int64_t>(a.kv_offset) + table->rot > msa->head_dim) return DSA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(msa->kv_heads) * msa->head_dim > (1 << 24)) return DSA_ERR_UNSUPPORTED;
+  if ((st = check_call(ctx, plan)) != DSA_OK) return st;
+  LaunchCount launched(ctx);
+  if (plan->T == 0) return DSA_OK;
+  if (!k || !v || !kv_cache || !aligned(k, a.kv_type) || !aligned(v, a.kv_type) || !aligned(kv_cache, DSA_BF16))
+    return DSA_ERR_INVALID_ARG;
+  return cuda_status(ctx, launch_append_kv(ctx, plan, table, a, msa->kv_heads, msa->head_dim, k, v, kv_cache, keys, index_cache,
+                                           reinterpret_cast<cudaStream_t>(stream), &launched.n));
 }
 
 dsa_status dsa_get_error(dsa_ctx_t *ctx, dsa_stream_t stream) {

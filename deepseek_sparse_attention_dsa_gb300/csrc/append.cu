@@ -1,0 +1,222 @@
+// append.cu -- a step's rows into the paged caches, rotated by their positions
+// on the way: latent rows [c | rotated k_pe] and index keys (bf16, or quantised
+// to the 656- and 132-byte rows), or the keys and values of a GQA cache.
+//
+// Each value is read and written once.  A warp takes one part of one row (its
+// latent, its index key, its keys, its values), since a row is one to four
+// kilobytes and a decode step has few of them.  Values to be quantised stay in
+// fp32 between rotation and code, so that they are rounded once.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "dsa_internal.h"
+#include "ptx.cuh"
+#include "rotary.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kAppendWarps = 8;
+
+enum Part { kPartLatent, kPartKey, kPartK, kPartV };
+
+struct AppendParams {
+  const int32_t *row_pos, *row_page_off, *row_npages, *row_page_start, *pages;
+  const uint64_t *turns;
+  int *err;
+  int32_t T, P, num_pages, rot, parts, part[3];
+  float amplitude;
+  // latents
+  const char *c, *k_pe;
+  char *latent;
+  int64_t c_stride, k_pe_stride;   // bytes
+  int32_t L, R, c_type, k_pe_type, layout, latent_row, rope_at;   // bytes of a cached row, and of its rope's start
+  bool latent_fp8, c_vec, k_pe_vec, latent_vec, rope_vec;
+  // index keys
+  const char *keys;
+  char *index;
+  int64_t keys_stride;
+  int32_t D, key_type, key_layout, key_offset;
+  bool index_fp8, keys_vec, index_vec;
+  // keys and values
+  const char *k, *v;
+  char *kv;
+  int64_t k_stride, k_head, v_stride, v_head;
+  int32_t heads, dim, kv_type, kv_layout, kv_offset;
+  bool k_vec, v_vec, kv_vec;
+};
+
+// Eight columns from `col` on of a row of `width`, rounded to bf16.
+__device__ __forceinline__ void copy8(const char *src, int type, bool src_vec, char *dst, bool dst_vec, int col, int width) {
+  float v[8];
+  load8(v, src, type, col, width, src_vec);
+  store8(dst, DSA_BF16, col, width, dst_vec, v);
+}
+
+__global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendParams p) {
+  extern __shared__ float shared[];   // a warp: [rotary_pairs(rot)] angles, then [D] values of a key to be quantised
+  grid_dependency();
+  const int warp = threadIdx.x / 32, lane = lane_id();
+  const int64_t task = static_cast<int64_t>(blockIdx.x) * kAppendWarps + warp;
+  const int64_t row = task / p.parts;
+  if (row >= p.T) return;
+  const int part = p.part[task - row * p.parts];
+  const int32_t pos = p.row_pos[row];
+  if (pos < 0) return;   // padding of a capturable plan
+  const int64_t slot = static_cast<int64_t>(p.row_page_start[row]) + pos, pi = slot / p.P;
+  int page = -1;
+  if (pi < p.row_npages[row]) page = p.pages[p.row_page_off[row] + pi];
+  if (page < 0 || page >= p.num_pages) {
+    if (lane == 0) atomicOr(p.err, kErrBounds);
+    return;
+  }
+  const int in_page = static_cast<int>(slot - pi * p.P);
+  const int64_t at = static_cast<int64_t>(page) * p.P + in_page;
+
+  const int pitch = p.rot ? rotary_pairs(p.rot) : 0;
+  float2 *cs = reinterpret_cast<float2 *>(shared) + warp * pitch;
+  if (p.rot && part != kPartV) {
+    for (int i = lane; i < p.rot / 2; i += 32) cs[i] = rotary_angle(pos, p.turns[i], p.amplitude);
+    __syncwarp();
+  }
+
+  if (part == kPartLatent) {
+    const char *c = p.c + row * p.c_stride, *k_pe = p.k_pe + row * p.k_pe_stride;
+    char *out = p.latent + at * p.latent_row;
+    if (p.latent_fp8) {
+      for (int c0 = 0; c0 < p.L; c0 += 256) {   // (the whole warp: a group's maximum is over 16 lanes)
+        const int col = c0 + lane * 8;
+        float v[8];
+        load8(v, c, p.c_type, col, p.L, p.c_vec);
+        uint32_t m = amax_bits8(v);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const GroupScale g(m);
+        store_codes8(reinterpret_cast<uint8_t *>(out), col, p.L, p.latent_vec, codes8(v, g));
+        if ((lane & 15) == 0 && col < p.L) reinterpret_cast<float *>(out + p.L)[col / 128] = g.scale;
+      }
+    } else {
+      for (int col = lane * 8; col < p.L; col += 256) copy8(c, p.c_type, p.c_vec, out, p.latent_vec, col, p.L);
+    }
+    char *rope = out + p.rope_at;
+    const int n = p.rot ? rotary_units(p.rot, p.layout) : (p.R + 7) / 8;   // (rot is R, or 0: all copies)
+    for (int u = lane; u < n; u += 32)
+      rotary_unit(u, p.rot, p.layout, 0, p.R, cs, k_pe, p.k_pe_type, p.k_pe_vec, rope, DSA_BF16, p.rope_vec);
+  } else if (part == kPartKey) {
+    const char *key = p.keys + row * p.keys_stride;
+    const int n = (p.rot ? rotary_units(p.rot, p.key_layout) : 0) + rotary_copies(p.D, p.key_offset, p.rot);
+    if (p.index_fp8) {
+      float *v = shared + kAppendWarps * pitch * 2 + warp * p.D;
+      for (int u = lane; u < n; u += 32)
+        rotary_unit(u, p.rot, p.key_layout, p.key_offset, p.D, cs, key, p.key_type, p.keys_vec, v, DSA_FP32, false);
+      __syncwarp();
+      // D is 128: one group, four columns a lane
+      float x[4];
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(x[i] = v[lane * 4 + i]) & 0x7FFFFFFFu);
+      const GroupScale g(__reduce_max_sync(0xffffffffu, m));
+      char *base = p.index + static_cast<int64_t>(page) * p.P * (128 + 4);
+      const uint32_t codes = g.scale < 0x1p-80f
+                                 ? e4m3x4(x[0] / g.scale, x[1] / g.scale, x[2] / g.scale, x[3] / g.scale)
+                                 : e4m3x4(g.quotient(x[0]), g.quotient(x[1]), g.quotient(x[2]), g.quotient(x[3]));
+      reinterpret_cast<uint32_t *>(base + in_page * 128)[lane] = codes;
+      if (lane == 0) *reinterpret_cast<float *>(base + static_cast<int64_t>(p.P) * 128 + in_page * 4) = g.scale;
+    } else {
+      char *out = p.index + at * p.D * 2;
+      for (int u = lane; u < n; u += 32)
+        rotary_unit(u, p.rot, p.key_layout, p.key_offset, p.D, cs, key, p.key_type, p.keys_vec, out, DSA_BF16, p.index_vec);
+    }
+  } else {
+    const bool is_k = part == kPartK;
+    char *out = p.kv + at * (4ll * p.heads * p.dim) + (is_k ? 0 : 2ll * p.heads * p.dim);
+    const int rot = is_k ? p.rot : 0;
+    const int n = (rot ? rotary_units(rot, p.kv_layout) : 0) + rotary_copies(p.dim, rot ? p.kv_offset : 0, rot);
+    for (int i = lane; i < n * p.heads; i += 32) {
+      const int h = i / n, u = i - h * n;
+      const char *src = is_k ? p.k + row * p.k_stride + h * p.k_head : p.v + row * p.v_stride + h * p.v_head;
+      rotary_unit(u, rot, p.kv_layout, rot ? p.kv_offset : 0, p.dim, cs, src, p.kv_type, is_k ? p.k_vec : p.v_vec,
+                  out + 2ll * h * p.dim, DSA_BF16, p.kv_vec);
+    }
+  }
+}
+
+int bytes_of(int type) { return type == DSA_BF16 ? 2 : 4; }
+
+bool on16(const void *p, int64_t stride_bytes, int64_t head_bytes = 0) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride_bytes % 16 == 0 && head_bytes % 16 == 0;
+}
+
+AppendParams append_base(const dsa_ctx *ctx, const dsa_plan_t *plan, const dsa_rotary *table) {
+  AppendParams p{};
+  p.row_pos = plan->row_pos, p.row_page_off = plan->row_page_off, p.row_npages = plan->row_npages;
+  p.row_page_start = plan->row_page_start, p.pages = plan->pages, p.err = ctx->err;
+  p.T = plan->T, p.P = ctx->cfg.page_size, p.num_pages = plan->cache_pages;
+  if (table) p.turns = table->turns, p.rot = table->rot, p.amplitude = table->amplitude;
+  return p;
+}
+
+void append_keys(const dsa_ctx *ctx, AppendParams &p, const dsa_append_t &a, const void *keys, void *index_cache) {
+  const dsa_config_t &c = ctx->cfg;
+  p.part[p.parts++] = kPartKey;
+  p.keys = static_cast<const char *>(keys), p.index = static_cast<char *>(index_cache);
+  p.key_type = a.key_type, p.keys_stride = a.keys_stride * bytes_of(a.key_type);
+  p.D = c.index_dim, p.key_layout = a.key_layout, p.key_offset = p.rot ? a.key_offset : 0;
+  p.index_fp8 = c.index_fmt == DSA_INDEX_FP8_132;
+  const bool whole = rotary_whole(p.key_offset, p.rot, a.key_layout);
+  p.keys_vec = whole && on16(keys, p.keys_stride);
+  p.index_vec = whole && on16(index_cache, p.D * 2);
+}
+
+cudaError_t launch_append(const AppendParams &p, cudaStream_t s, int32_t *launches) {
+  int floats = p.rot ? rotary_pairs(p.rot) * 2 : 0;
+  if (p.keys && p.index_fp8) floats += p.D;
+  const int64_t tasks = static_cast<int64_t>(p.T) * p.parts;
+  *launches += 1;
+  return launch_overlapped(append_kernel, dim3(static_cast<unsigned>((tasks + kAppendWarps - 1) / kAppendWarps)),
+                           kAppendWarps * 32, floats * kAppendWarps * 4, 1, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_append_latents(const dsa_ctx *ctx, const dsa_plan_t *plan, const dsa_rotary *table, const dsa_append_t &a,
+                                  const void *c, const void *k_pe, void *latent_cache, const void *keys, void *index_cache,
+                                  cudaStream_t s, int32_t *launches) {
+  AppendParams p = append_base(ctx, plan, table);
+  if (c) {
+    const dsa_config_t &g = ctx->cfg;
+    p.part[p.parts++] = kPartLatent;
+    p.c = static_cast<const char *>(c), p.k_pe = static_cast<const char *>(k_pe), p.latent = static_cast<char *>(latent_cache);
+    p.L = g.kv_lora_rank, p.R = g.rope_dim, p.c_type = a.c_type, p.k_pe_type = a.k_pe_type, p.layout = a.layout;
+    p.c_stride = a.c_stride * bytes_of(a.c_type), p.k_pe_stride = a.k_pe_stride * bytes_of(a.k_pe_type);
+    p.latent_fp8 = g.latent_fmt == DSA_LATENT_FP8_656;
+    p.rope_at = p.latent_fp8 ? p.L + 4 * (p.L / 128) : 2 * p.L;
+    p.latent_row = p.rope_at + 2 * p.R;
+    const bool whole = rotary_whole(0, p.rot, a.layout);
+    p.c_vec = on16(c, p.c_stride), p.k_pe_vec = whole && on16(k_pe, p.k_pe_stride);
+    p.latent_vec = on16(latent_cache, p.latent_row);
+    p.rope_vec = whole && p.latent_vec && p.rope_at % 16 == 0;
+  }
+  if (keys) append_keys(ctx, p, a, keys, index_cache);
+  return launch_append(p, s, launches);
+}
+
+cudaError_t launch_append_kv(const dsa_ctx *ctx, const dsa_plan_t *plan, const dsa_rotary *table, const dsa_append_t &a,
+                             int32_t kv_heads, int32_t head_dim, const void *k, const void *v, void *kv_cache,
+                             const void *keys, void *index_cache, cudaStream_t s, int32_t *launches) {
+  AppendParams p = append_base(ctx, plan, table);
+  p.part[p.parts++] = kPartK;
+  p.part[p.parts++] = kPartV;
+  p.k = static_cast<const char *>(k), p.v = static_cast<const char *>(v), p.kv = static_cast<char *>(kv_cache);
+  p.heads = kv_heads, p.dim = head_dim, p.kv_type = a.kv_type, p.kv_layout = a.layout, p.kv_offset = a.kv_offset;
+  const int size = bytes_of(a.kv_type);
+  p.k_stride = a.k_stride * size, p.k_head = a.k_head * size, p.v_stride = a.v_stride * size, p.v_head = a.v_head * size;
+  const bool whole = rotary_whole(p.rot ? p.kv_offset : 0, p.rot, a.layout);
+  p.k_vec = whole && on16(k, p.k_stride, p.k_head), p.v_vec = on16(v, p.v_stride, p.v_head);
+  p.kv_vec = whole && on16(kv_cache, 2ll * head_dim);
+  if (keys) append_keys(ctx, p, a, keys, index_cache);
+  return launch_append(p, s, launches);
+}
+
+}  // namespace dsa

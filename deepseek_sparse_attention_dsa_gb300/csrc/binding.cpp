@@ -1,5 +1,7 @@
 // binding.cpp -- torch tensors to the C calls of the 8-bit rows and projections
-// (dsa_rmsnorm, dsa_quantize_rows, dsa_quantize_weight, dsa_project_fp8).
+// (dsa_rmsnorm, dsa_quantize_rows, dsa_quantize_weight, dsa_project_fp8), and to
+// those between projections and caches (dsa_rotate, dsa_append_latents,
+// dsa_append_kv, dsa_prefix_attend).
 //
 // A norm of one token takes 3 us on the GPU.  Reading its tensors' shapes,
 // types and strides and making its outputs took 15 us in Python; here they take
@@ -9,6 +11,8 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <algorithm>
 
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -20,12 +24,13 @@ namespace {
 
 PyObject *g_check = nullptr;   // dsa._check(status, what, handle): raises
 
-enum Kind { kValues, kCodes, kScales };
+enum Kind { kValues, kCodes, kScales, kPositions };
 
 // DSA_BF16 / DSA_FP32 for values, 0 for the others; -1: not of this kind.
 int type_of(at::ScalarType t, Kind kind) {
   switch (kind) {
     case kValues: return t == at::kBFloat16 ? DSA_BF16 : t == at::kFloat ? DSA_FP32 : -1;
+    case kPositions: return t == at::kInt ? 0 : -1;
     case kCodes: return t == at::kByte || t == at::kFloat8_e4m3fn ? 0 : -1;
     default: return t == at::kFloat ? 0 : -1;
   }
@@ -92,7 +97,8 @@ bool view(const Call &call, PyObject *o, const char *name, Kind kind, at::IntArr
   v->type = type_of(t.scalar_type(), kind);
   if (v->type < 0) {
     PyErr_Format(PyExc_TypeError, "%s has dtype %s, expected %s", name, c10::toString(t.scalar_type()),
-                 kind == kValues ? "bfloat16 or float32" : kind == kCodes ? "uint8 or float8_e4m3fn" : "float32");
+                 kind == kValues ? "bfloat16 or float32" : kind == kCodes ? "uint8 or float8_e4m3fn"
+                 : kind == kPositions ? "int32" : "float32");
     return false;
   }
   if (call.device < 0 ? !t.is_cpu() : !t.is_cuda() || t.get_device() != call.device) {
@@ -350,6 +356,187 @@ PyObject *project_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+int64_t integer(PyObject *o) { return PyLong_AsLongLong(o); }
+// (out of an int's range: refused by the call)
+int32_t small(PyObject *o) { return static_cast<int32_t>(std::min<int64_t>(std::max<int64_t>(integer(o), -1), INT32_MAX)); }
+template <typename T>
+T *handle(PyObject *o) { return is_none(o) ? nullptr : static_cast<T *>(PyLong_AsVoidPtr(o)); }
+
+// A cache: contiguous, of this type (bf16, or packed bytes) and at least this many bytes.
+bool cache(const Call &call, PyObject *o, const char *name, bool packed, int64_t bytes, void **p) {
+  if (!tensor(o, name)) return false;
+  const at::Tensor &t = THPVariable_Unpack(o);
+  if (t.scalar_type() != (packed ? at::kByte : at::kBFloat16)) {
+    PyErr_Format(PyExc_TypeError, "%s has dtype %s, expected %s", name, c10::toString(t.scalar_type()), packed ? "uint8" : "bfloat16");
+    return false;
+  }
+  if (call.device < 0 ? !t.is_cpu() : !t.is_cuda() || t.get_device() != call.device) {
+    PyErr_Format(PyExc_ValueError, "%s is on %s, expected %s %d", name, t.device().str().c_str(),
+                 call.device < 0 ? "cpu" : "cuda", call.device);
+    return false;
+  }
+  if (!t.is_contiguous() || t.is_neg() || t._is_zerotensor()) {
+    PyErr_Format(PyExc_ValueError, "%s must be contiguous", name);
+    return false;
+  }
+  if (static_cast<int64_t>(t.nbytes()) < bytes) {
+    PyErr_Format(PyExc_ValueError, "%s has %lld bytes, the plan's pages take %lld", name, static_cast<long long>(t.nbytes()),
+                 static_cast<long long>(bytes));
+    return false;
+  }
+  *p = t.data_ptr();
+  return true;
+}
+
+// rotary(handle, device, plan, stream, table, x, positions, offset, layout, inverse, out) -> out
+PyObject *rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Call call;
+  if (!wants(n, 11) || !call.take(a) || !tensor(a[5], "x")) return nullptr;
+  const at::Tensor &x = THPVariable_Unpack(a[5]);
+  if (x.dim() != 2 && x.dim() != 3) {
+    PyErr_SetString(PyExc_ValueError, "x must be (rows, heads, width) or (rows, width)");
+    return nullptr;
+  }
+  const at::IntArrayRef shape = x.sizes();
+  const bool many = shape.size() == 3;
+  View vx, vp, vo;
+  Kept kept;
+  if (!view(call, a[5], "x", kValues, shape, &vx) ||
+      (!is_none(a[6]) && !view(call, a[6], "positions", kPositions, {shape[0]}, &vp)) ||
+      !output(call, a[10], "out", kValues, shape, x.scalar_type(), &vo, &kept.o[0]))
+    return nullptr;
+  if (vo.type != vx.type) {
+    PyErr_SetString(PyExc_TypeError, "out must have x's dtype");
+    return nullptr;
+  }
+  if ((many && shape[1] > INT32_MAX) || shape.back() > INT32_MAX) {
+    PyErr_SetString(PyExc_ValueError, "a dimension has too many elements");
+    return nullptr;
+  }
+  dsa_rotate_t s{};
+  s.rows = shape[0], s.heads = many ? static_cast<int32_t>(shape[1]) : 1, s.width = static_cast<int32_t>(shape.back());
+  s.offset = small(a[7]), s.layout = small(a[8]), s.inverse = PyObject_IsTrue(a[9]) == 1, s.type = vx.type;
+  s.x_stride = vx.stride[0], s.out_stride = vo.stride[0];
+  if (many) s.x_head = vx.stride[1], s.out_head = vo.stride[1];
+  const dsa_rotary_t *table = handle<dsa_rotary_t>(a[4]);
+  if (PyErr_Occurred()) return nullptr;
+  dsa_status st;
+  Py_BEGIN_ALLOW_THREADS
+  st = dsa_rotate(call.ctx, call.plan, table, &s, vx.p, static_cast<const int32_t *>(vp.p), vo.p, call.stream);
+  Py_END_ALLOW_THREADS
+  return call.done(st, "dsa_rotate", result(kept, {0}));
+  END_HANDLE_TH_ERRORS
+}
+
+// The index keys of an append: (keys, index_dim, index_cache, packed, bytes) at a[0 .. 4].
+bool append_keys(const Call &call, PyObject *const *a, int64_t rows, dsa_append_t *s, void **keys, void **index_cache) {
+  *keys = *index_cache = nullptr;
+  if (is_none(a[0]) && is_none(a[2])) return true;
+  View v;
+  if (!view(call, a[0], "keys", kValues, {rows, integer(a[1])}, &v) ||
+      !cache(call, a[2], "index_cache", PyObject_IsTrue(a[3]) == 1, integer(a[4]), index_cache))
+    return false;
+  *keys = v.p, s->key_type = v.type, s->keys_stride = v.stride[0];
+  return true;
+}
+
+// append_latents(handle, device, plan, stream, table, rows, c, kv_lora_rank, k_pe, rope_dim, latent_cache, packed,
+//   bytes, keys, index_dim, index_cache, packed, bytes, layout, key_layout, key_offset)
+PyObject *append_latents(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Call call;
+  if (!wants(n, 21) || !call.take(a)) return nullptr;
+  const int64_t rows = integer(a[5]);
+  dsa_append_t s{};
+  void *keys, *index_cache, *latent_cache = nullptr;
+  View vc, vk;
+  if (!is_none(a[6]) || !is_none(a[8]) || !is_none(a[10])) {
+    const int64_t rope = integer(a[9]);
+    if (!view(call, a[6], "c", kValues, {rows, integer(a[7])}, &vc) ||
+        !((rope == 0 && is_none(a[8])) || view(call, a[8], "k_pe", kValues, {rows, rope}, &vk)) ||
+        !cache(call, a[10], "latent_cache", PyObject_IsTrue(a[11]) == 1, integer(a[12]), &latent_cache))
+      return nullptr;
+    s.c_type = vc.type, s.k_pe_type = vk.type, s.c_stride = vc.stride[0], s.k_pe_stride = vk.stride[0];
+  }
+  if (!append_keys(call, a + 13, rows, &s, &keys, &index_cache)) return nullptr;
+  s.layout = small(a[18]), s.key_layout = small(a[19]), s.key_offset = small(a[20]);
+  const dsa_rotary_t *table = handle<dsa_rotary_t>(a[4]);
+  if (PyErr_Occurred()) return nullptr;
+  dsa_status st;
+  Py_BEGIN_ALLOW_THREADS
+  st = dsa_append_latents(call.ctx, call.plan, table, &s, vc.p, vk.p, latent_cache, keys, index_cache, call.stream);
+  Py_END_ALLOW_THREADS
+  return call.done(st, "dsa_append_latents", Py_NewRef(Py_None));
+  END_HANDLE_TH_ERRORS
+}
+
+// append_kv(handle, device, plan, stream, table, rows, kv_heads, head_dim, k, v, kv_cache, bytes,
+//   keys, index_dim, index_cache, packed, bytes, layout, kv_offset, key_layout, key_offset)
+PyObject *append_kv(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Call call;
+  if (!wants(n, 21) || !call.take(a)) return nullptr;
+  const int64_t rows = integer(a[5]);
+  dsa_append_t s{};
+  dsa_msa_shape_t msa{};
+  msa.kv_heads = small(a[6]), msa.head_dim = small(a[7]);
+  void *keys, *index_cache, *kv_cache;
+  View vk, vv;
+  const int64_t shape[3] = {rows, msa.kv_heads, msa.head_dim};
+  if (!view(call, a[8], "k", kValues, shape, &vk) || !view(call, a[9], "v", kValues, shape, &vv) ||
+      !cache(call, a[10], "kv_cache", false, integer(a[11]), &kv_cache) ||
+      !append_keys(call, a + 12, rows, &s, &keys, &index_cache))
+    return nullptr;
+  if (vk.type != vv.type) {
+    PyErr_SetString(PyExc_TypeError, "k and v must have the same dtype");
+    return nullptr;
+  }
+  s.kv_type = vk.type, s.k_stride = vk.stride[0], s.k_head = vk.stride[1], s.v_stride = vv.stride[0], s.v_head = vv.stride[1];
+  s.layout = small(a[17]), s.kv_offset = small(a[18]), s.key_layout = small(a[19]), s.key_offset = small(a[20]);
+  const dsa_rotary_t *table = handle<dsa_rotary_t>(a[4]);
+  if (PyErr_Occurred()) return nullptr;
+  dsa_status st;
+  Py_BEGIN_ALLOW_THREADS
+  st = dsa_append_kv(call.ctx, call.plan, table, &msa, &s, vk.p, vv.p, kv_cache, keys, index_cache, call.stream);
+  Py_END_ALLOW_THREADS
+  return call.done(st, "dsa_append_kv", Py_NewRef(Py_None));
+  END_HANDLE_TH_ERRORS
+}
+
+// prefix_attend(handle, device, None, stream, prefix plan, rows, q_heads, head_dim, q, kv_cache, bytes, sm_scale, out) -> out
+PyObject *prefix_attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Call call;
+  if (!wants(n, 13) || !call.take(a)) return nullptr;
+  const int64_t shape[3] = {integer(a[5]), integer(a[6]), integer(a[7])};
+  const dsa_prefix_plan_t *pp = handle<dsa_prefix_plan_t>(a[4]);
+  const int64_t bytes = integer(a[10]);
+  const double scale = PyFloat_AsDouble(a[11]);
+  if (PyErr_Occurred()) return nullptr;
+  void *kv_cache;
+  View vq, vo;
+  Kept kept;
+  if (!view(call, a[8], "q", kValues, shape, &vq) || !cache(call, a[9], "kv_cache", false, bytes, &kv_cache) ||
+      !output(call, a[12], "out", kValues, shape, at::kBFloat16, &vo, &kept.o[0]))
+    return nullptr;
+  if (vq.type != DSA_BF16 || vo.type != DSA_BF16) {
+    PyErr_SetString(PyExc_TypeError, "q and out must be bfloat16");
+    return nullptr;
+  }
+  const bool dense = THPVariable_Unpack(a[8]).is_contiguous() && (is_none(a[12]) || THPVariable_Unpack(a[12]).is_contiguous());
+  if (!dense) {
+    PyErr_SetString(PyExc_ValueError, "q and out must be contiguous");
+    return nullptr;
+  }
+  dsa_status st;
+  Py_BEGIN_ALLOW_THREADS
+  st = dsa_prefix_attend(call.ctx, pp, vq.p, kv_cache, static_cast<float>(scale), vo.p, call.stream);
+  Py_END_ALLOW_THREADS
+  return call.done(st, "dsa_prefix_attend", result(kept, {0}));
+  END_HANDLE_TH_ERRORS
+}
+
 PyObject *set_check(PyObject *, PyObject *f) {
   Py_INCREF(f);
   Py_XSETREF(g_check, f);
@@ -361,6 +548,10 @@ PyMethodDef methods[] = {
     {"quantize_rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(quantize_rows)), METH_FASTCALL, nullptr},
     {"quantize_weight", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(quantize_weight)), METH_FASTCALL, nullptr},
     {"project_fp8", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(project_fp8)), METH_FASTCALL, nullptr},
+    {"rotary", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(rotary)), METH_FASTCALL, nullptr},
+    {"append_latents", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(append_latents)), METH_FASTCALL, nullptr},
+    {"append_kv", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(append_kv)), METH_FASTCALL, nullptr},
+    {"prefix_attend", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(prefix_attend)), METH_FASTCALL, nullptr},
     {"set_check", set_check, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -242,6 +242,13 @@ inline dsa_status cuda_status(dsa_ctx *ctx, cudaError_t e) {
 
 }  // namespace dsa
 
+namespace dsa {
+// A span of a host plan; its pages are host_pages[page_off .. page_off + num_pages) of the plan.
+struct PlanSpan {
+  int32_t q_start, q_len, ctx_start, page_start, page_off, num_pages;
+};
+}  // namespace dsa
+
 struct dsa_plan {
   dsa_ctx *ctx = nullptr;
   cudaStream_t stream = nullptr;
@@ -249,6 +256,8 @@ struct dsa_plan {
   int32_t box_rows = 1;           // TMA box height of the indexer's key tiles (index_box_rows of the page size)
   int64_t num_scores = 0;
   std::vector<char> host;         // staging copy of the device metadata
+  std::vector<dsa::PlanSpan> spans;     // host plans
+  const int32_t *host_pages = nullptr;  // in `host`
   char *dev = nullptr;
   // device views
   int32_t *row_pos = nullptr, *row_page_off = nullptr, *row_npages = nullptr, *row_page_start = nullptr;
@@ -273,6 +282,14 @@ struct dsa_plan {
   int64_t page_ids = 0;                 // length of the page array of the last update
   float *own_scores = nullptr, *own_opart = nullptr, *own_mlpart = nullptr;
   int32_t *counts = nullptr;            // device [8], see dsa_plan_read_counts
+};
+
+// A rotation's table: turns[i] = round(2^64 frequency[i] / 2 pi) on the device (rotary.cuh).
+struct dsa_rotary {
+  int device = -1;
+  int32_t rot = 0;
+  float amplitude = 1.f;
+  uint64_t *turns = nullptr;
 };
 
 namespace dsa {
@@ -332,6 +349,18 @@ cudaError_t launch_project_fp8(const dsa_ctx *ctx, const dsa_project_t &g, const
                                const void *w, const float *w_scale, void *out, const int32_t *count, int32_t per_row,
                                cudaStream_t s, int32_t *launches);
 bool project_tc_supported(const dsa_project_t &g, const void *a, const void *w);
+
+// Rotations and appends.  positions: the call's, or the plan's (plan_rows: those below 0 are padding).
+cudaError_t launch_rotary(const dsa_rotary *table, const dsa_rotate_t &g, const void *x, const int32_t *positions,
+                          bool plan_rows, void *out, cudaStream_t s, int32_t *launches);
+int64_t rotary_ctas(const dsa_rotary *table, const dsa_rotate_t &g, bool in_place);   // the launch's grid
+// table, and either source of the first, may be NULL.
+cudaError_t launch_append_latents(const dsa_ctx *ctx, const dsa_plan_t *plan, const dsa_rotary *table, const dsa_append_t &a,
+                                  const void *c, const void *k_pe, void *latent_cache, const void *keys, void *index_cache,
+                                  cudaStream_t s, int32_t *launches);
+cudaError_t launch_append_kv(const dsa_ctx *ctx, const dsa_plan_t *plan, const dsa_rotary *table, const dsa_append_t &a,
+                             int32_t kv_heads, int32_t head_dim, const void *k, const void *v, void *kv_cache,
+                             const void *keys, void *index_cache, cudaStream_t s, int32_t *launches);
 
 // Device address of the fixed score array behind dsa_index_topk_static on the
 // current device (loads the module that holds it, so the array is taken when

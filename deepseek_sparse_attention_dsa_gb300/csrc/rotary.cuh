@@ -1,0 +1,96 @@
+// rotary.cuh -- rotation of pairs of columns by position x frequency, as the
+// rotary kernel (rotary.cu) and the appends (append.cu) apply it.
+//
+// A pair (a, b) at angle t becomes (a cos t - b sin t, a sin t + b cos t), in
+// fp32.  Angles are exact to the last bit that matters at any position: a table
+// holds each pair's frequency in turns a position as a 64-bit fraction of a turn,
+// f = round(2^64 frequency / 2 pi), so position * f modulo 2^64 (what a 64-bit
+// product keeps by itself) is the fraction of a turn with an error of at most
+// |position| * 2^-65 turns, and its signed value times 2^-63 is the angle in units
+// of pi, in -1 .. 1, where sincospif needs no reduction.  (position * frequency
+// in fp32 is off by 2^-24 of the angle: 0.008 rad at position 131,072.)
+#pragma once
+#include <stdint.h>
+
+#include "dsa.h"
+#include "fp8.cuh"
+
+namespace dsa {
+
+// (cos, sin) of a position's angle for one pair, times the table's amplitude.
+__device__ __forceinline__ float2 rotary_angle(int32_t position, uint64_t turns, float amplitude) {
+  const int64_t part = static_cast<int64_t>(static_cast<uint64_t>(static_cast<int64_t>(position)) * turns);
+  float s, c;
+  sincospif(__ll2float_rn(part) * 0x1p-63f, &s, &c);
+  return make_float2(c * amplitude, s * amplitude);
+}
+
+// Four neighbouring pairs in eight columns ("interleaved"); cs: their angles.
+__device__ __forceinline__ void rotate_interleaved(float (&v)[8], const float2 *cs) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 w = cs[i];
+    const float a = v[2 * i], b = v[2 * i + 1];
+    v[2 * i] = fmaf(a, w.x, -b * w.y);
+    v[2 * i + 1] = fmaf(a, w.y, b * w.x);
+  }
+}
+// Eight pairs, the first columns in a, the second in b ("half").
+__device__ __forceinline__ void rotate_half(float (&a)[8], float (&b)[8], const float2 *cs) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 w = cs[i];
+    const float x = a[i], y = b[i];
+    a[i] = fmaf(x, w.x, -y * w.y);
+    b[i] = fmaf(x, w.y, y * w.x);
+  }
+}
+
+// Units of a row of `width` columns whose columns offset .. offset + rot rotate:
+// first the rotated ones (eight columns, or twice eight where the layout is half),
+// then pieces of up to eight of the columns before and behind them.
+__host__ __device__ inline int rotary_units(int rot, int layout) {
+  return layout == DSA_ROTARY_HALF ? (rot / 2 + 7) / 8 : (rot + 7) / 8;
+}
+__host__ __device__ inline int rotary_copies(int width, int offset, int rot) {
+  return (offset + 7) / 8 + (width - offset - rot + 7) / 8;
+}
+// Angles held for a row: whole units of them, so that a cut unit reads inside its row.
+__host__ __device__ inline int rotary_pairs(int rot) { return (rot / 2 + 7) / 8 * 8; }
+
+// Unit u of a row of `src` into `dst` (types and alignment each its own); cs: the
+// row's angles, null where nothing rotates (rot 0).
+__device__ __forceinline__ void rotary_unit(int u, int rot, int layout, int offset, int width, const float2 *cs,
+                                            const void *src, int src_type, bool src_vec, void *dst, int dst_type,
+                                            bool dst_vec) {
+  const int n = rotary_units(rot, layout);
+  float a[8];
+  if (u < n) {
+    if (layout == DSA_ROTARY_HALF) {
+      float b[8];
+      const int half = rot / 2, i = u * 8;
+      load8(a, src, src_type, offset + i, offset + half, src_vec);
+      load8(b, src, src_type, offset + half + i, offset + rot, src_vec);
+      rotate_half(a, b, cs + i);
+      store8(dst, dst_type, offset + i, offset + half, dst_vec, a);
+      store8(dst, dst_type, offset + half + i, offset + rot, dst_vec, b);
+    } else {
+      load8(a, src, src_type, offset + u * 8, offset + rot, src_vec);
+      rotate_interleaved(a, cs + u * 4);
+      store8(dst, dst_type, offset + u * 8, offset + rot, dst_vec, a);
+    }
+    return;
+  }
+  u -= n;
+  const int before = (offset + 7) / 8;
+  const int col = u < before ? u * 8 : offset + rot + (u - before) * 8, end = u < before ? offset : width;
+  load8(a, src, src_type, col, end, src_vec);
+  store8(dst, dst_type, col, end, dst_vec, a);
+}
+
+// Whether every unit's pieces start on 16 bytes when the rows do.
+__host__ __device__ inline bool rotary_whole(int offset, int rot, int layout) {
+  return offset % 8 == 0 && rot % (layout == DSA_ROTARY_HALF ? 16 : 8) == 0;
+}
+
+}  // namespace dsa

@@ -62,7 +62,9 @@ EXPORTED = ["dsa_create", "dsa_destroy", "dsa_plan", "dsa_plan_destroy", "dsa_pl
             "dsa_plan_update", "dsa_plan_read_counts", "dsa_quantize_q", "dsa_index_scores_fp8q",
             "dsa_index_topk_fp8q", "dsa_selftest_wait_timeout", "dsa_selftest_warp_wait_timeout", "dsa_msa_select_blocks", "dsa_msa_index_select",
             "dsa_msa_attend", "dsa_msa_attend_on_tensor_cores", "dsa_rmsnorm", "dsa_quantize_rows",
-            "dsa_quantize_weight", "dsa_project_fp8", "dsa_project_on_tensor_cores"]
+            "dsa_quantize_weight", "dsa_project_fp8", "dsa_project_on_tensor_cores", "dsa_rotary_create", "dsa_rotary_destroy",
+            "dsa_rotate", "dsa_append_latents", "dsa_append_kv", "dsa_prefix_plan", "dsa_prefix_plan_destroy",
+            "dsa_prefix_plan_get_info", "dsa_prefix_attend"]
 
 # dsa_device_span_t: q_len, ctx_start, page_start, page_off, num_pages, reserved (int32 each)
 DEVICE_SPAN_FIELDS = 6
@@ -117,6 +119,45 @@ class _Project(ctypes.Structure):
                 ("a_scale_stride", ctypes.c_int64), ("a_scale_batch", ctypes.c_int64), ("w_stride", ctypes.c_int64),
                 ("w_batch", ctypes.c_int64), ("w_scale_stride", ctypes.c_int64), ("w_scale_batch", ctypes.c_int64),
                 ("out_stride", ctypes.c_int64), ("out_batch", ctypes.c_int64)]
+
+
+class _RotaryConfig(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("form", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_context", ctypes.c_double), ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("amplitude", ctypes.c_double), ("frequencies", ctypes.POINTER(ctypes.c_double))]
+
+
+class _Rotate(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("heads", ctypes.c_int32), ("width", ctypes.c_int32), ("offset", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("inverse", ctypes.c_int32), ("type", ctypes.c_int32), ("x_stride", ctypes.c_int64),
+                ("x_head", ctypes.c_int64), ("out_stride", ctypes.c_int64), ("out_head", ctypes.c_int64)]
+
+
+class _Append(ctypes.Structure):
+    _fields_ = [("c_stride", ctypes.c_int64), ("k_pe_stride", ctypes.c_int64), ("keys_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("k_head", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("v_head", ctypes.c_int64), ("c_type", ctypes.c_int32), ("k_pe_type", ctypes.c_int32),
+                ("key_type", ctypes.c_int32), ("kv_type", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("key_layout", ctypes.c_int32), ("kv_offset", ctypes.c_int32), ("key_offset", ctypes.c_int32)]
+
+
+class _Prefix(ctypes.Structure):
+    _fields_ = [("first_span", ctypes.c_int32), ("num_spans", ctypes.c_int32), ("tokens", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class PrefixInfo(ctypes.Structure):
+    _fields_ = [("num_prefixes", ctypes.c_int32), ("on_tensor_cores", ctypes.c_int32), ("tokens_read", ctypes.c_int64)]
+
+
+ROTARY_LAYOUTS = {"interleaved": 0, "half": 1}
+ROTARY_FORMS = {None: 0, "linear": 1, "yarn": 2}
+
+
+def _layout(name) -> int:
+    if name not in ROTARY_LAYOUTS:
+        raise ValueError("layout must be one of %s, not %r" % (sorted(ROTARY_LAYOUTS), name))
+    return ROTARY_LAYOUTS[name]
 
 
 def _msa_shape(ms) -> _MsaShape:
@@ -186,6 +227,17 @@ def load() -> ctypes.CDLL:
     L.dsa_msa_attend.argtypes = [vp, vp, msp, vp, vp, vp, ctypes.c_float, vp, vp]
     L.dsa_msa_attend_on_tensor_cores.argtypes = [vp, vp, msp]
     L.dsa_msa_attend_on_tensor_cores.restype = ctypes.c_int
+    L.dsa_rotary_create.argtypes = [vp, ctypes.POINTER(_RotaryConfig), ctypes.POINTER(vp)]
+    L.dsa_rotary_destroy.argtypes = [vp]
+    L.dsa_rotary_destroy.restype = None
+    L.dsa_rotate.argtypes = [vp, vp, vp, ctypes.POINTER(_Rotate), vp, vp, vp, vp]
+    L.dsa_append_latents.argtypes = [vp, vp, vp, ctypes.POINTER(_Append), vp, vp, vp, vp, vp, vp]
+    L.dsa_append_kv.argtypes = [vp, vp, vp, msp, ctypes.POINTER(_Append), vp, vp, vp, vp, vp, vp]
+    L.dsa_prefix_plan.argtypes = [vp, vp, msp, ctypes.POINTER(_Prefix), i32, vp, ctypes.POINTER(vp)]
+    L.dsa_prefix_plan_destroy.argtypes = [vp]
+    L.dsa_prefix_plan_destroy.restype = None
+    L.dsa_prefix_plan_get_info.argtypes = [vp, ctypes.POINTER(PrefixInfo)]
+    L.dsa_prefix_attend.argtypes = [vp, vp, vp, vp, ctypes.c_float, vp, vp]
     L.dsa_last_launch_count.argtypes = [vp]
     L.dsa_last_launch_count.restype = i32
     L.dsa_last_cuda_error.argtypes = [vp]
@@ -197,14 +249,16 @@ def load() -> ctypes.CDLL:
                  "dsa_quantize_store_latents", "dsa_attend_shared", "dsa_plan_capturable", "dsa_plan_update",
                  "dsa_plan_read_counts", "dsa_quantize_q", "dsa_index_scores_fp8q", "dsa_index_topk_fp8q",
                  "dsa_selftest_wait_timeout", "dsa_selftest_warp_wait_timeout", "dsa_msa_select_blocks", "dsa_msa_index_select", "dsa_msa_attend",
-                 "dsa_rmsnorm", "dsa_quantize_rows", "dsa_quantize_weight", "dsa_project_fp8"):
+                 "dsa_rmsnorm", "dsa_quantize_rows", "dsa_quantize_weight", "dsa_project_fp8", "dsa_rotary_create", "dsa_rotate",
+                 "dsa_append_latents", "dsa_append_kv", "dsa_prefix_plan", "dsa_prefix_plan_get_info", "dsa_prefix_attend"):
         getattr(L, name).restype = i32
     _lib = L
     return L
 
 
 def load_binding():
-    """The extension module that passes tensors to the 8-bit calls (csrc/binding.cpp); raises if it has not been built."""
+    """The extension module that passes tensors to the 8-bit calls, rotations, appends and the prefix attention
+    (csrc/binding.cpp); raises if it has not been built."""
     global _binding
     with _binding_lock:
         if _binding is None:
@@ -265,9 +319,10 @@ def _stream(stream) -> ctypes.c_void_p:
 class Plan:
     """A step's rows (dsa_plan_t).  Keeps the spans' page arrays alive."""
 
-    def __init__(self, ctx: "Context", handle: ctypes.c_void_p, keepalive, capturable: bool = False):
+    def __init__(self, ctx: "Context", handle: ctypes.c_void_p, keepalive, cache_pages: int, capturable: bool = False):
         self.ctx = ctx
         self.handle = handle
+        self.cache_pages = cache_pages
         self._keep = keepalive
         self.capturable = capturable
         info = PlanInfo()
@@ -301,6 +356,54 @@ class Plan:
     def close(self):
         if self.handle:
             load().dsa_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class RotaryTable:
+    """A model's rotation frequencies on one device (dsa_rotary_t), made by Context.rotary_table."""
+
+    def __init__(self, handle: ctypes.c_void_p, rot_dim: int):
+        self.handle = handle
+        self.rot_dim = rot_dim
+
+    def close(self):
+        if self.handle:
+            load().dsa_rotary_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class PrefixPlan:
+    """Which of a plan's spans share a prefix, and the attention's work (dsa_prefix_plan_t).  Keeps the plan alive."""
+
+    def __init__(self, plan: Plan, msa, handle: ctypes.c_void_p):
+        self.plan = plan
+        self.msa = msa
+        self.handle = handle
+        info = PrefixInfo()
+        _check(load().dsa_prefix_plan_get_info(handle, ctypes.byref(info)), "dsa_prefix_plan_get_info")
+        self.info = info
+        self._call = (plan.num_rows, int(msa.q_heads), int(msa.head_dim))
+        self._bytes = plan.cache_pages * plan.ctx.shape.page_size * 4 * int(msa.kv_heads) * int(msa.head_dim)
+
+    @property
+    def on_tensor_cores(self) -> bool:
+        return bool(self.info.on_tensor_cores)
+
+    def close(self):
+        if self.handle:
+            load().dsa_prefix_plan_destroy(self.handle)
             self.handle = None
 
     def __del__(self):
@@ -348,7 +451,7 @@ class Context:
         h = ctypes.c_void_p()
         st = None if self.device_index < 0 else _stream(stream)
         _check(load().dsa_plan(self.handle, arr, len(spans), int(cache_pages), st, ctypes.byref(h)), "dsa_plan")
-        return Plan(self, h, (arr, keep))
+        return Plan(self, h, (arr, keep), int(cache_pages))
 
     def plan_capturable(self, max_rows: int, max_spans: int, max_scores: int, cache_pages: int,
                         page_start_align: int = 1, stream=None) -> Plan:
@@ -359,7 +462,7 @@ class Context:
         _check(load().dsa_plan_capturable(self.handle, int(max_rows), int(max_spans), int(max_scores),
                                           int(page_start_align), int(cache_pages), st, ctypes.byref(h)),
                "dsa_plan_capturable", self.handle)
-        return Plan(self, h, None, capturable=True)
+        return Plan(self, h, None, int(cache_pages), capturable=True)
 
     def plan_update(self, plan: Plan, num_spans: torch.Tensor, spans: torch.Tensor, pages: torch.Tensor, stream=None):
         """dsa_plan_update: num_spans (1,) int32, spans (max_spans, 6) int32
@@ -566,6 +669,99 @@ class Context:
     def project_on_tensor_cores(self, a, a_scale, w, w_scale, out) -> bool:
         """Whether project_fp8 runs this call on the tensor cores."""
         return self._rows.project_fp8(self._address(), self.device_index, None, 0, a, a_scale, w, w_scale, out, None, True)
+
+    # ------------------------------------------- rotary positions and appends
+    def rotary_table(self, rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                     original_context: float = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, amplitude: float = 1.0,
+                     frequencies: Optional[Sequence[float]] = None) -> RotaryTable:
+        """dsa_rotary_create: the frequencies of rot_dim rotated columns, base **
+        (-2 i / rot_dim), divided by `factor` (scaling "linear") or stretched for
+        long contexts (scaling "yarn"); or `frequencies`, rot_dim / 2 of them in
+        radians a position.  Synchronises; made once for a model."""
+        given = None
+        if frequencies is not None:
+            if scaling is not None:
+                raise ValueError("frequencies are given as they are: scaling must be None")
+            if len(frequencies) * 2 != rot_dim:
+                raise ValueError("frequencies must be rot_dim / 2 = %s values" % (rot_dim / 2))
+            given = (ctypes.c_double * max(1, len(frequencies)))(*[float(f) for f in frequencies])
+        elif scaling not in ROTARY_FORMS:
+            raise ValueError("scaling must be None, 'linear' or 'yarn', not %r" % (scaling,))
+        cfg = _RotaryConfig(int(rot_dim), 3 if given is not None else ROTARY_FORMS[scaling], float(base), float(factor),
+                            float(original_context), float(beta_fast), float(beta_slow), float(amplitude), given)
+        h = ctypes.c_void_p()
+        _check(load().dsa_rotary_create(self.handle, ctypes.byref(cfg), ctypes.byref(h)), "dsa_rotary_create", self.handle)
+        return RotaryTable(h, int(rot_dim))
+
+    @staticmethod
+    def _table_of(table, needed=False):
+        if table is None and not needed:
+            return None
+        if not isinstance(table, RotaryTable):
+            raise TypeError("table must be a RotaryTable")
+        if not table.handle:
+            raise DSAError(1, "rotary table")
+        return table.handle.value
+
+    def rotary(self, table: RotaryTable, x, positions, offset: int = 0, layout: str = "interleaved", inverse: bool = False,
+               out=None, stream=None) -> torch.Tensor:
+        """dsa_rotate: x (rows, heads, width) or (rows, width), bf16 or fp32, with
+        columns offset .. offset + table.rot_dim of each head rotated by the row's
+        position: `positions` is a plan of that many rows, or an int32 tensor (rows,).
+        inverse turns back (the rotation's gradient).  out may be x."""
+        plan = isinstance(positions, Plan)
+        return self._rows.rotary(self._address(), self.device_index, self._plan_of(positions) if plan else None,
+                                 stream and self._stream_of(stream), self._table_of(table, True), x,
+                                 None if plan else positions, offset, _layout(layout), inverse, out)
+
+    def _index_bytes(self, plan):
+        return plan.cache_pages * self.shape.page_size * self.shape.index_row_bytes
+
+    def append_latents(self, plan: Plan, table: Optional[RotaryTable], c=None, k_pe=None, latent_cache=None, keys=None,
+                       index_cache=None, layout: str = "interleaved", key_layout: str = "half", key_offset: int = 0, stream=None):
+        """dsa_append_latents: latents c (T, kv_lora_rank) and k_pe (T, rope_dim),
+        rotated, and/or index keys (T, index_dim), rotated from key_offset on, to
+        each row's slot in the context's cache formats.  table None: not rotated."""
+        sh = self.shape
+        self._rows.append_latents(self._address(), self.device_index, self._plan_of(plan), stream and self._stream_of(stream),
+                                  self._table_of(table), plan.num_rows, c, sh.kv_lora_rank, k_pe, sh.rope_dim, latent_cache,
+                                  bool(sh.latent_fmt), plan.cache_pages * sh.page_size * sh.latent_row_bytes, keys, sh.index_dim,
+                                  index_cache, bool(sh.index_fmt), self._index_bytes(plan), _layout(layout),
+                                  _layout(key_layout), key_offset)
+
+    def append_kv(self, plan: Plan, msa, table: Optional[RotaryTable], k, v, kv_cache, keys=None, index_cache=None,
+                  layout: str = "half", offset: int = 0, key_layout: str = "half", key_offset: int = 0, stream=None):
+        """dsa_append_kv: k (T, kv_heads, head_dim), rotated from `offset` on, and v
+        to each row's slot of the GQA cache that msa_attend and prefix_attend read;
+        and index keys as in append_latents.  table None: not rotated."""
+        sh = self.shape
+        self._rows.append_kv(self._address(), self.device_index, self._plan_of(plan), stream and self._stream_of(stream),
+                             self._table_of(table), plan.num_rows, msa.kv_heads, msa.head_dim, k, v, kv_cache,
+                             plan.cache_pages * sh.page_size * 4 * msa.kv_heads * msa.head_dim, keys, sh.index_dim, index_cache,
+                             bool(sh.index_fmt), self._index_bytes(plan), _layout(layout), offset, _layout(key_layout), key_offset)
+
+    # --------------------------------------- attention over a shared prefix
+    def plan_prefix(self, plan: Plan, msa, prefixes: Optional[Sequence] = None, stream=None) -> PrefixPlan:
+        """dsa_prefix_plan: `prefixes` are (first span, spans, tokens) of the plan's
+        spans that hold their first tokens in the same pages; None finds them."""
+        if not plan.handle:
+            raise DSAError(1, "plan")
+        ms = _msa_shape(msa)
+        arr = None if prefixes is None else (_Prefix * max(1, len(prefixes)))(*[_Prefix(int(f), int(n), int(t), 0) for f, n, t in prefixes])
+        h = ctypes.c_void_p()
+        st = None if self.device_index < 0 else _stream(stream)
+        _check(load().dsa_prefix_plan(self.handle, plan.handle, ctypes.byref(ms), arr, -1 if prefixes is None else len(prefixes),
+                                      st, ctypes.byref(h)), "dsa_prefix_plan", self.handle)
+        return PrefixPlan(plan, msa, h)
+
+    def prefix_attend(self, prefixes: PrefixPlan, q, kv_cache, sm_scale: Optional[float] = None, out=None, stream=None):
+        """dsa_prefix_attend: dense causal GQA, the shared positions read once:
+        q (T, q_heads, head_dim) bf16 -> (T, q_heads, head_dim) bf16."""
+        if not prefixes.handle or not prefixes.plan.handle:
+            raise DSAError(1, "prefix plan")
+        return self._rows.prefix_attend(self._address(), self.device_index, None, stream and self._stream_of(stream),
+                                        prefixes.handle.value, *prefixes._call, q, kv_cache, prefixes._bytes,
+                                        prefixes.msa.sm_scale if sm_scale is None else sm_scale, out)
 
     def index_scores(self, plan: Plan, q, w, index_cache, scores=None, stream=None) -> torch.Tensor:
         d = self.device

@@ -497,6 +497,168 @@ dsa_status dsa_project_fp8(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_pro
 /* 1 when dsa_project_fp8 runs this call on the tensor cores, else 0 (host-side query). */
 int dsa_project_on_tensor_cores(const dsa_project_t *shape, const void *a, const void *w);
 
+/* ---- Rotary positions and appends ------------------------------------------
+ * Between a layer's projections and the calls above: the rotation of queries and
+ * keys by their positions, and the append of a step's rows to the caches with the
+ * rotation applied on the way.
+ *
+ * A rotation takes pairs (a, b) of a row's columns to
+ *   (a cos t - b sin t, a sin t + b cos t) * amplitude,  t = position * frequency[pair],
+ * in fp32 with t exact for any int32 position (to 2^-43 of a turn at position
+ * 2^20), rounded once to the output's type.  Column pairs of the rot_dim rotated
+ * columns: (2i, 2i + 1) for DSA_ROTARY_INTERLEAVED, (i, i + rot_dim / 2) for
+ * DSA_ROTARY_HALF.  `inverse` turns by -t: with the same amplitude that is also the
+ * gradient of the rotation.  Values that are not finite reach their own pair only.
+ *
+ * A table holds the frequencies of a model, in radians a position, for
+ * pair i = 0 .. rot_dim / 2 - 1:
+ *   DSA_ROTARY_PLAIN   base^(-2i / rot_dim)
+ *   DSA_ROTARY_LINEAR  that, divided by factor (a context `factor` times as long)
+ *   DSA_ROTARY_YARN    f_i * (1 - r_i) + f_i / factor * r_i, f_i the plain one and
+ *                      r_i = clamp((i - low) / (high - low), 0, 1) (high - low at
+ *                      least 0.001), where low = max(floor(d(beta_fast)), 0), high =
+ *                      min(ceil(d(beta_slow)), rot_dim - 1), and d(n) = rot_dim
+ *                      ln(original_context / (2 pi n)) / (2 ln base) is the pair that
+ *                      turns n times over the original context
+ *   DSA_ROTARY_GIVEN   `frequencies` (host, rot_dim / 2 doubles, read during the call)
+ * Fields that a form does not read are ignored.  dsa_rotary_create copies the
+ * table to the context's device and synchronises; a table is constant after that
+ * and may be used by any context of that device, on any stream or thread, and in
+ * captured graphs as long as it lives.  On a host-only context it is made without a device copy.
+ * DSA_ERR_INVALID_ARG: rot_dim odd, below 2 or above 1024, an unknown form, a base
+ * not above 1, a factor, original_context or beta not above 0, beta_fast below
+ * beta_slow, values that are not finite. */
+enum { DSA_ROTARY_INTERLEAVED = 0, DSA_ROTARY_HALF = 1 };
+enum { DSA_ROTARY_PLAIN = 0, DSA_ROTARY_LINEAR = 1, DSA_ROTARY_YARN = 2, DSA_ROTARY_GIVEN = 3 };
+typedef struct dsa_rotary_config {
+  int32_t rot_dim;
+  int32_t form;
+  double base, factor, original_context, beta_fast, beta_slow;
+  double amplitude;            /* 1 for a pure rotation */
+  const double *frequencies;
+} dsa_rotary_config_t;
+typedef struct dsa_rotary dsa_rotary_t;
+dsa_status dsa_rotary_create(dsa_ctx_t *ctx, const dsa_rotary_config_t *cfg, dsa_rotary_t **out);
+void dsa_rotary_destroy(dsa_rotary_t *table);
+
+/* Rotates columns offset .. offset + rot_dim of every head of x (rows, heads,
+ * width); the other columns are copied.  bf16 or fp32 (type; out's too).  A row's
+ * position is that of the plan's row (then rows must be the plan's num_rows; rows
+ * that a capturable plan holds as padding are neither read nor written), or
+ * positions[row] (DEVICE int32, any value) where plan is NULL; exactly one of
+ * the two is given.  Strides in elements, from a row to the next and from a head
+ * to the next; a head's values are adjacent.  Any stride and alignment of the
+ * type's own size is accepted; 16-byte aligned heads, with offset a multiple of 8
+ * and rot_dim of 8 (DSA_ROTARY_HALF: of 16), run faster.  out may be x, with the
+ * same strides: then the other columns are left as they are.  Otherwise it must
+ * not overlap x, and its heads must not overlap each other.  The kernels of this
+ * call and of the appends are launched as those of the 8-bit rows (programmatic
+ * stream serialization).  DSA_ERR_INVALID_ARG: null pointers or pointers off
+ * their type, sizes below 1 (rows may be 0: nothing is launched), offset + rot_dim
+ * above width, an unknown type or layout, negative strides, written heads that
+ * would overlap, a table of another device, a plan of another context, rows that do
+ * not match the plan; DSA_ERR_UNSUPPORTED: more than 2^31 - 1 blocks of work. */
+typedef struct dsa_rotate {
+  int64_t rows;
+  int32_t heads, width, offset;
+  int32_t layout, inverse;     /* DSA_ROTARY_*; 0 or 1 */
+  int32_t type;                /* DSA_BF16 or DSA_FP32 */
+  int64_t x_stride, x_head, out_stride, out_head;
+} dsa_rotate_t;
+dsa_status dsa_rotate(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_rotary_t *table, const dsa_rotate_t *shape,
+                      const void *x, const int32_t *positions, void *out, dsa_stream_t stream);
+
+/* Appends: row r of the plan goes to the slot of its own position, as in
+ * dsa_store_keys, rotated by that position where a table is given (table NULL:
+ * stored as it is).  Host and capturable plans; padding rows are neither read nor
+ * written, and nothing but the rows' own slots is written.  Rows whose slots are
+ * the same slot leave it undefined.  Sources are bf16 or fp32, strided by rows (and
+ * heads), adjacent within a row (head); each value is rounded once, to bf16 or to
+ * the e4m3 code of the cache's format.
+ *
+ * dsa_append_latents: c (T, kv_lora_rank) and k_pe (T, rope_dim), of which k_pe is
+ *   rotated in `layout` (a table's rot_dim must be rope_dim), into latent_cache in
+ *   the context's latent format; and/or keys (T, index_dim), of which columns
+ *   key_offset .. key_offset + rot_dim are rotated in `key_layout`, into index_cache
+ *   in the context's index format, in the same launch.  c, k_pe and latent_cache
+ *   are all NULL where only keys are appended, keys and index_cache where only latents
+ *   are.  (k_pe may be NULL where rope_dim is 0.)  8-bit rows follow the rule of the
+ *   8-bit rows above (a NaN or an infinity reaches its group's scale).
+ * dsa_append_kv: k and v (T, kv_heads, head_dim), of whose k columns kv_offset ..
+ *   kv_offset + rot_dim of every head are rotated in `layout`, into kv_cache as
+ *   dsa_msa_attend and dsa_prefix_attend read it; and keys as above, or NULL.  Of
+ *   `msa` kv_heads and head_dim are read.
+ * DSA_ERR_INVALID_ARG: null pointers other than those, pointers off their type
+ * (caches: 4 bytes; bf16 caches 2), unknown types or layouts, negative strides or
+ * offsets, rotated columns past a row's end, a table of another device or a plan of
+ * another context.
+ * A page id outside the cache sets DSA_ERR_BOUNDS, and the row is skipped. */
+typedef struct dsa_append {
+  int64_t c_stride, k_pe_stride, keys_stride;
+  int64_t k_stride, k_head, v_stride, v_head;
+  int32_t c_type, k_pe_type, key_type, kv_type;   /* DSA_BF16 or DSA_FP32 */
+  int32_t layout, key_layout;                     /* DSA_ROTARY_* */
+  int32_t kv_offset, key_offset;
+} dsa_append_t;
+dsa_status dsa_append_latents(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_rotary_t *table, const dsa_append_t *shape,
+                              const void *c, const void *k_pe, void *latent_cache, const void *keys, void *index_cache,
+                              dsa_stream_t stream);
+dsa_status dsa_append_kv(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_rotary_t *table, const dsa_msa_shape_t *msa,
+                         const dsa_append_t *shape, const void *k, const void *v, void *kv_cache, const void *keys,
+                         void *index_cache, dsa_stream_t stream);
+
+/* ---- Attention over a shared prefix ----------------------------------------
+ * Dense causal GQA over the cache that dsa_msa_attend reads, for a batch whose
+ * requests start with the same pages (a system prompt, a document): the shared
+ * positions' keys and values are read once for all rows of a run of spans, each
+ * request's own after them, and the two softmaxes are joined:
+ *   out[r, h] = softmax_j((q[r, h] . k_j) * sm_scale) . v_j,  j = 0 .. pos(r),
+ * query head h reading kv head h / (q_heads / kv_heads).  Spans without a shared
+ * prefix are attended by themselves, so any host plan can be used.
+ *
+ * dsa_prefix_plan: prefixes[i] says that spans first_span .. first_span +
+ * num_spans - 1 of the plan hold their positions 0 .. tokens - 1 in the same slots
+ * of the same pages, none of them this step's new rows (tokens <= ctx_start); in
+ * order, without overlap.  num_prefixes = -1 finds them: runs of neighbouring
+ * spans with the same page_start and the same first pages (at least 128 tokens),
+ * a run growing while that lowers the tokens read.  0: nothing is shared.
+ * Host work, then one host-to-device copy on `stream`, as dsa_plan; made once a
+ * step and used for every layer of it.  It keeps pointing at `plan`, which must
+ * outlive it, and owns the scratch of its calls: calls with one prefix plan are
+ * ordered one after another (also two captured graphs of them).  Of `shape` the
+ * fields q_heads, kv_heads and head_dim are read.  A context of device -1 makes the
+ * plan without a device copy.
+ * DSA_ERR_INVALID_ARG: null pointers, a plan of another context, q_heads not a
+ * multiple of kv_heads, a nonzero reserved field, prefixes out of order, or whose
+ * spans do not share those positions; DSA_ERR_UNSUPPORTED: a capturable plan,
+ * head_dim above 512, q_heads above 1024, 2^31 or more rows x q_heads.
+ *
+ * dsa_prefix_attend: q (T, q_heads, head_dim) bf16, kv_cache as dsa_msa_attend's
+ * with this step's rows in place (dsa_append_kv), out (T, q_heads, head_dim) bf16;
+ * sums, maxima and logits in fp32, probabilities rounded to bf16 on the tensor
+ * cores.  Each on 16 bytes.  Cache rows that no row of the call sees may
+ * hold anything; keys and values that some row sees must be finite for all rows
+ * of that span.  Equal calls with one plan give equal bits.  A page id outside the
+ * cache cannot occur (dsa_plan checks them). */
+typedef struct dsa_prefix {
+  int32_t first_span;
+  int32_t num_spans;
+  int32_t tokens;
+  int32_t reserved;      /* set to 0 */
+} dsa_prefix_t;
+typedef struct dsa_prefix_plan dsa_prefix_plan_t;
+typedef struct dsa_prefix_info {
+  int32_t num_prefixes;      /* runs of spans that share a prefix */
+  int32_t on_tensor_cores;   /* 1 when the plan's calls run on the tensor cores */
+  int64_t tokens_read;       /* tokens whose keys and values one call reads (per kv head) */
+} dsa_prefix_info_t;
+dsa_status dsa_prefix_plan(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_msa_shape_t *shape, const dsa_prefix_t *prefixes,
+                           int32_t num_prefixes, dsa_stream_t stream, dsa_prefix_plan_t **out);
+void dsa_prefix_plan_destroy(dsa_prefix_plan_t *pp);
+dsa_status dsa_prefix_plan_get_info(const dsa_prefix_plan_t *pp, dsa_prefix_info_t *info);
+dsa_status dsa_prefix_attend(dsa_ctx_t *ctx, const dsa_prefix_plan_t *pp, const void *q, const void *kv_cache, float sm_scale,
+                             void *out, dsa_stream_t stream);
+
 /* Drive the pipeline's bounded wait to its limit, for testing the failure
  * path (mstar IndexKeyStore.history: a failure is reported to the caller, not
  * fatal).  One CTA takes tensor memory, waits on an mbarrier that nothing
