@@ -30,7 +30,7 @@ BINDING = os.path.join(OUT_DIR, "_dsa_binding.so")
 BINDING_SOURCE = "binding.cpp"
 SOURCES = ["api.cu", "plan_device.cu", "store_keys.cu", "quantize.cu", "indexer.cu", "indexer_f8q.cu", "topk.cu",
            "attend.cu", "msa.cu", "rmsnorm.cu", "quantize_rows.cu", "project.cu",
-           "rotary.cu", "append.cu", "prefix.cu", "static_scratch.cu", "selftest.cu"]
+           "rotary.cu", "append.cu", "prefix.cu", "prefix_tc.cu", "static_scratch.cu", "selftest.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -13,22 +13,15 @@
 #include <new>
 #include <vector>
 
-#include "dsa_internal.h"
 #include "fp8.cuh"
+#include "prefix.h"
 #include "ptx.cuh"
-
-struct dsa_prefix_plan {
-  const dsa_plan_t *plan = nullptr;
-  dsa_msa_shape_t shape{};
-  std::vector<dsa_prefix_t> prefixes;
-  int64_t tokens_read = 0;
-};
 
 namespace dsa {
 namespace {
 
 constexpr float kPrefixLog2e = 1.4426950408889634f;
-constexpr float kNoMax = -1.0e30f;   // the reference maximum of a row that has seen no key
+constexpr float kNoMax = -3.0e38f;   // the reference maximum of a row that has seen no key
 
 __device__ __forceinline__ float exp2_approx(float x) {   // (relative error 2^-22; 0 for -inf)
   float y;
@@ -137,12 +130,263 @@ void find_prefixes(const dsa_plan_t &plan, int32_t page_size, std::vector<dsa_pr
   }
 }
 
+// ---- the tensor cores' work
+struct Chain {
+  int32_t tile[2];              // tiles of queries (-1: one only)
+  int32_t span, causal;
+  int32_t g, slot0, ntiles, lo, hi;
+};
+struct QueryTile {
+  int32_t row, rows;
+};
+// Tiles [t0, t1) of a chain.
+struct Piece {
+  int32_t chain, t0, t1;
+};
+
+// A segment costs kStart key tiles beside its own: its queries' load, the first product's latency, its output.
+constexpr double kStart = 2.0;
+
+// Cuts a line of pieces into at most n runs of about the same cost, at least `least` each.  A cut that would
+// leave less than a sliver on either side of it goes to the piece's end there.
+std::vector<std::vector<Piece>> cut_line(const std::vector<Piece> &line, int n, double least) {
+  double total = 0.0;
+  for (const Piece &x : line) total += x.t1 - x.t0 + kStart;
+  std::vector<std::vector<Piece>> out;
+  if (line.empty()) return out;
+  n = std::max(1, std::min(n, static_cast<int>(total / least)));
+  const double each = total / n, sliver = std::max(1.0, 0.08 * each);
+  out.resize(n);
+  double at = 0.0;      // cost laid out so far
+  int b = 0;
+  for (Piece x : line) {
+    for (;;) {
+      const double cost = x.t1 - x.t0 + kStart, room = (b + 1) * each - at;
+      if (b == n - 1 || cost <= room + sliver) {
+        out[b].push_back(x);
+        at += cost;
+        if (b < n - 1 && at >= (b + 1) * each - 0.5) ++b;
+        break;
+      }
+      const int32_t here = static_cast<int32_t>(room - kStart + 0.5);
+      if (here < sliver) {      // (nothing of it here)
+        at = std::max(at, (b + 1) * each);
+        ++b;
+        continue;
+      }
+      out[b].push_back(Piece{x.chain, x.t0, x.t0 + here});
+      at = std::max(at + here + kStart, (b + 1) * each);
+      x.t0 += here;
+      ++b;
+    }
+  }
+  return out;
+}
+
+struct Work {
+  std::vector<QueryTile> tiles;
+  std::vector<Chain> chains;
+  std::vector<PrefixSeg> segs;
+  std::vector<PrefixCta> ctas;
+  std::vector<PrefixParts> parts;
+  std::vector<PrefixRow> rows;
+};
+
+void lay_out(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, Work &w) {
+  const dsa_plan_t &plan = *pp->plan;
+  const int32_t Hkv = pp->shape.kv_heads, group = pp->shape.q_heads / Hkv, per = kPrefixTile / group, BH = plan.box_rows;
+  pp->rows_a_tile = per;
+  w.rows.assign(plan.T, PrefixRow{-1, 0, -1, 0});
+  // Rows [r0, r1) against slots lo .. hi - 1 (causal: row r sees those below limit0 + r - r0 + 1 - ...).
+  auto add = [&](int32_t r0, int32_t r1, int32_t span, int64_t lo, int64_t hi, bool causal, bool shared) {
+    const PlanSpan &sp = plan.spans[span];
+    const int32_t first = static_cast<int32_t>(w.tiles.size());
+    for (int32_t r = r0; r < r1; r += per) {
+      const int32_t n = std::min(per, r1 - r), id = static_cast<int32_t>(w.tiles.size());
+      w.tiles.push_back(QueryTile{r, n});
+      for (int32_t k = 0; k < n; ++k) {
+        PrefixRow &x = w.rows[r + k];
+        (shared ? x.shared : x.own) = id;
+        (shared ? x.shared_lane : x.own_lane) = k * group;
+      }
+    }
+    const int32_t count = static_cast<int32_t>(w.tiles.size()) - first;
+    const int32_t slot0 = static_cast<int32_t>(lo / BH * BH);
+    for (int32_t g = 0; g < Hkv; ++g)
+      for (int32_t t = 0; t < count; t += 2) {
+        const bool pair = t + 1 < count;
+        const QueryTile &last = w.tiles[first + t + pair];
+        // a causal chain ends behind its last row's own key
+        const int64_t end = causal ? static_cast<int64_t>(sp.page_start) + sp.ctx_start + (last.row + last.rows - sp.q_start) : hi;
+        w.chains.push_back(Chain{{first + t, pair ? first + t + 1 : -1}, span, causal, g, slot0,
+                                 static_cast<int32_t>((end - slot0 + kPrefixTile - 1) / kPrefixTile), static_cast<int32_t>(lo),
+                                 static_cast<int32_t>(end)});
+      }
+  };
+  size_t next = 0;
+  const int32_t spans = static_cast<int32_t>(plan.spans.size());
+  for (int32_t i = 0; i < spans;) {
+    const dsa_prefix_t *x = next < pp->prefixes.size() && pp->prefixes[next].first_span == i ? &pp->prefixes[next++] : nullptr;
+    const int32_t end = x ? x->first_span + x->num_spans : i + 1;
+    for (int32_t j = i; j < end;) {
+      // A span that fills tiles by itself takes the shared keys with its own in one chain: its rows need no joining, and
+      // the pages are in L2 for the next span.  The others' rows are put together, in runs of neighbours.
+      auto fills = [&](int32_t k) { return !x || plan.spans[k].q_len >= 4 * per; };
+      const PlanSpan &s = plan.spans[j];
+      const int64_t start = s.page_start;
+      int32_t k = j;
+      while (k < end && !fills(k)) ++k;
+      if (k > j) {
+        const PlanSpan &l = plan.spans[k - 1];
+        add(s.q_start, l.q_start + l.q_len, j, start, start + x->tokens, false, true);
+        for (int32_t m = j; m < k; ++m) {
+          const PlanSpan &o = plan.spans[m];
+          add(o.q_start, o.q_start + o.q_len, m, start + x->tokens, 0, true, false);
+        }
+      }
+      if (k < end) {
+        const PlanSpan &o = plan.spans[k];
+        add(o.q_start, o.q_start + o.q_len, k, o.page_start, 0, true, false);
+        ++k;
+      }
+      j = k;
+    }
+    i = end;
+  }
+  // The pairs' line, then the lone tiles'; each cut evenly over the CTAs.  Chains of pairs over the same keys
+  // that are longer than a CTA's share go in blocks of it, all pairs' first block first, so that CTAs that
+  // run together read the same keys.
+  std::vector<Piece> pairs, lone;
+  const int n = std::max(1, ctx->num_sms);
+  double cost = 0.0;
+  for (const Chain &c : w.chains)
+    if (c.tile[1] >= 0) cost += c.ntiles + kStart;
+  const int32_t block = std::max<int32_t>(4, static_cast<int32_t>(cost / n - kStart + 0.5));
+  for (size_t c = 0; c < w.chains.size();) {
+    const Chain &x = w.chains[c];
+    size_t e = c + 1;
+    while (e < w.chains.size() && w.chains[e].span == x.span && w.chains[e].g == x.g && w.chains[e].slot0 == x.slot0 &&
+           w.chains[e].causal == x.causal)
+      ++e;
+    int32_t most = 0;
+    for (size_t k = c; k < e; ++k) most = std::max(most, w.chains[k].ntiles);
+    for (int32_t t = 0; t < most; t += block)
+      for (size_t k = c; k < e; ++k)
+        if (w.chains[k].tile[1] >= 0 && t < w.chains[k].ntiles)
+          pairs.push_back(Piece{static_cast<int32_t>(k), t, std::min(t + block, w.chains[k].ntiles)});
+    for (size_t k = c; k < e; ++k)
+      if (w.chains[k].tile[1] < 0) lone.push_back(Piece{static_cast<int32_t>(k), 0, w.chains[k].ntiles});
+    c = e;
+  }
+  const auto a = cut_line(pairs, n, 4.0 + kStart), b = cut_line(lone, n, 2.0);
+  w.ctas.assign(std::max(a.size(), b.size()), PrefixCta{});
+  std::vector<int32_t> pieces_of(w.tiles.size() * Hkv, 0);
+  auto put = [&](const Piece &x) {
+    const Chain &c = w.chains[x.chain];
+    PrefixSeg s{};
+    for (int m = 0; m < 2; ++m) {
+      if (c.tile[m] < 0) continue;
+      const QueryTile &t = w.tiles[c.tile[m]];
+      const PlanSpan &sp = plan.spans[c.span];
+      s.row[m] = t.row, s.lanes[m] = t.rows * group;
+      s.limit[m] = c.causal ? sp.page_start + sp.ctx_start + (t.row - sp.q_start) + 1 : c.hi;
+      s.part[m] = pieces_of[static_cast<size_t>(c.tile[m]) * Hkv + c.g]++;   // (its number, for now)
+    }
+    s.causal = c.causal, s.g = c.g;
+    s.page_off = plan.spans[c.span].page_off, s.npages = plan.spans[c.span].num_pages;
+    s.slot0 = c.slot0 + x.t0 * kPrefixTile, s.ntiles = x.t1 - x.t0;
+    s.lo = c.lo, s.hi = c.hi;
+    w.segs.push_back(s);
+    return static_cast<size_t>(x.chain);
+  };
+  std::vector<size_t> chain_of;
+  for (size_t i = 0; i < w.ctas.size(); ++i) {
+    PrefixCta &cta = w.ctas[i];
+    cta.a0 = static_cast<int32_t>(w.segs.size());
+    if (i < a.size())
+      for (const Piece &x : a[i]) {
+        chain_of.push_back(put(x));
+        cta.tiles_a += x.t1 - x.t0;
+      }
+    cta.a1 = static_cast<int32_t>(w.segs.size());
+    if (i < b.size())
+      for (const Piece &x : b[i]) cta.tiles_b += x.t1 - x.t0;
+    int32_t left = (cta.tiles_b + 1) / 2;   // the first stream's tiles
+    size_t at = 0;
+    int32_t from = 0;                       // tiles of piece `at` that are laid out
+    for (int m = 0; m < 2; ++m) {
+      cta.b0[m] = static_cast<int32_t>(w.segs.size());
+      if (m == 1) left = cta.tiles_b / 2;
+      while (left > 0) {
+        const Piece &x = b[i][at];
+        const int32_t k = std::min(left, x.t1 - x.t0 - from);
+        chain_of.push_back(put(Piece{x.chain, x.t0 + from, x.t0 + from + k}));
+        left -= k, from += k;
+        if (from == x.t1 - x.t0) ++at, from = 0;
+      }
+      cta.b1[m] = static_cast<int32_t>(w.segs.size());
+    }
+  }
+  // partial results: none where a tile's only result is its own keys' only segment
+  std::vector<char> has_shared(w.tiles.size(), 0);
+  for (const PrefixRow &r : w.rows)
+    if (r.shared >= 0) has_shared[r.own] = has_shared[r.shared] = 1;
+  w.parts.resize(w.tiles.size() * Hkv);
+  int64_t lanes = 0;
+  for (size_t t = 0; t < w.tiles.size(); ++t)
+    for (int32_t g = 0; g < Hkv; ++g) {
+      PrefixParts &x = w.parts[t * Hkv + g];
+      const int32_t count = pieces_of[t * Hkv + g];
+      x.lanes = w.tiles[t].rows * group;
+      if (count == 1 && !has_shared[t]) continue;   // (count stays 0)
+      x.first = static_cast<int32_t>(lanes), x.count = count;
+      lanes += static_cast<int64_t>(count) * x.lanes;
+      pp->joins = true;
+    }
+  pp->part_lanes = lanes;
+  for (size_t i = 0; i < w.segs.size(); ++i)
+    for (int m = 0; m < 2; ++m) {
+      const int32_t t = w.chains[chain_of[i]].tile[m];
+      if (t < 0) continue;
+      const PrefixParts &x = w.parts[static_cast<size_t>(t) * Hkv + w.segs[i].g];
+      w.segs[i].part[m] = x.count ? x.first + w.segs[i].part[m] * x.lanes : -1;
+    }
+  pp->n_ctas = static_cast<int32_t>(w.ctas.size());
+}
+
+// The tables and the partial results' space on the device, in order on `stream`.
+dsa_status upload(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, const Work &w) {
+  auto round = [](size_t n) { return (n + 255) / 256 * 256; };
+  const size_t o_seg = 0, o_cta = o_seg + round(w.segs.size() * sizeof(PrefixSeg)),
+               o_part = o_cta + round(w.ctas.size() * sizeof(PrefixCta)),
+               o_row = o_part + round(w.parts.size() * sizeof(PrefixParts)), tables = o_row + round(w.rows.size() * sizeof(PrefixRow)),
+               o_ml = tables + round(static_cast<size_t>(pp->part_lanes) * pp->shape.head_dim * sizeof(float)),
+               bytes = o_ml + round(static_cast<size_t>(pp->part_lanes) * sizeof(float2)) + 256;
+  pp->host.assign(tables, 0);
+  std::memcpy(pp->host.data() + o_seg, w.segs.data(), w.segs.size() * sizeof(PrefixSeg));
+  std::memcpy(pp->host.data() + o_cta, w.ctas.data(), w.ctas.size() * sizeof(PrefixCta));
+  std::memcpy(pp->host.data() + o_part, w.parts.data(), w.parts.size() * sizeof(PrefixParts));
+  std::memcpy(pp->host.data() + o_row, w.rows.data(), w.rows.size() * sizeof(PrefixRow));
+  if (ctx->device < 0) return DSA_OK;
+  if (cudaSetDevice(ctx->device) != cudaSuccess) return DSA_ERR_CUDA;
+  if (cudaMallocAsync(reinterpret_cast<void **>(&pp->dev), bytes, pp->stream) != cudaSuccess) {
+    cudaGetLastError();
+    pp->dev = nullptr;
+    return DSA_ERR_OOM;
+  }
+  if (cudaMemcpyAsync(pp->dev, pp->host.data(), tables, cudaMemcpyHostToDevice, pp->stream) != cudaSuccess) return DSA_ERR_CUDA;
+  pp->segs = reinterpret_cast<PrefixSeg *>(pp->dev + o_seg), pp->ctas = reinterpret_cast<PrefixCta *>(pp->dev + o_cta);
+  pp->parts = reinterpret_cast<PrefixParts *>(pp->dev + o_part), pp->rows = reinterpret_cast<PrefixRow *>(pp->dev + o_row);
+  pp->part_o = reinterpret_cast<float *>(pp->dev + tables), pp->part_ml = reinterpret_cast<float2 *>(pp->dev + o_ml);
+  return DSA_OK;
+}
+
 }  // namespace
 
 dsa_status make_prefix_plan(const dsa_ctx *ctx, const dsa_plan_t *plan, const dsa_msa_shape_t &shape, const dsa_prefix_t *prefixes,
-                            int32_t n, cudaStream_t, dsa_prefix_plan_t *pp) {
+                            int32_t n, cudaStream_t stream, dsa_prefix_plan_t *pp) {
   const int32_t spans = static_cast<int32_t>(plan->spans.size()), P = ctx->cfg.page_size;
-  pp->plan = plan, pp->shape = shape;
+  pp->plan = plan, pp->shape = shape, pp->stream = stream, pp->device = ctx->device;
   if (n < 0) {
     find_prefixes(*plan, P, pp->prefixes);
   } else {
@@ -160,11 +404,20 @@ dsa_status make_prefix_plan(const dsa_ctx *ctx, const dsa_plan_t *plan, const ds
   }
   for (const PlanSpan &s : plan->spans) pp->tokens_read += s.ctx_start + s.q_len;
   for (const dsa_prefix_t &x : pp->prefixes) pp->tokens_read -= static_cast<int64_t>(x.tokens) * (x.num_spans - 1);
-  return DSA_OK;
+  // (TMA takes 32-bit cache rows, the tables 32-bit slots)
+  int64_t end = static_cast<int64_t>(plan->cache_pages) * P;
+  for (const PlanSpan &s : plan->spans) end = std::max(end, static_cast<int64_t>(s.page_start) + s.ctx_start + s.q_len + 2 * kPrefixTile);
+  pp->tc = prefix_tc_supported(ctx->cfg, shape) && end <= INT32_MAX;
+  if (!pp->tc || plan->T == 0) return DSA_OK;
+  Work w;
+  lay_out(ctx, pp, w);
+  if (pp->part_lanes > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  return upload(ctx, pp, w);
 }
 
 cudaError_t launch_prefix_attend(const dsa_ctx *ctx, const dsa_prefix_plan_t *pp, const void *q, const void *kv, float sm_scale,
                                  void *out, cudaStream_t s, int32_t *launches) {
+  if (pp->tc) return launch_prefix_tc(ctx, pp, q, kv, sm_scale, out, s, launches);
   const dsa_plan_t &plan = *pp->plan;
   PrefixSimpleParams p{};
   p.q = static_cast<const __nv_bfloat16 *>(q), p.kv = static_cast<const __nv_bfloat16 *>(kv);
@@ -211,6 +464,10 @@ dsa_status dsa_prefix_plan(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_msa
 
 void dsa_prefix_plan_destroy(dsa_prefix_plan_t *pp) {
   if (!pp) return;
+  if (pp->dev) {
+    cudaSetDevice(pp->device);
+    cudaFreeAsync(pp->dev, pp->stream);
+  }
   delete pp;
 }
 
@@ -218,13 +475,14 @@ dsa_status dsa_prefix_plan_get_info(const dsa_prefix_plan_t *pp, dsa_prefix_info
   if (!pp || !info) return DSA_ERR_INVALID_ARG;
   *info = dsa_prefix_info_t{};
   info->num_prefixes = static_cast<int32_t>(pp->prefixes.size());
+  info->on_tensor_cores = pp->tc ? 1 : 0;
   info->tokens_read = pp->tokens_read;
   return DSA_OK;
 }
 
 dsa_status dsa_prefix_attend(dsa_ctx_t *ctx, const dsa_prefix_plan_t *pp, const void *q, const void *kv_cache, float sm_scale,
                              void *out, dsa_stream_t stream) {
-  if (!ctx || !pp || pp->plan->ctx != ctx || ctx->device < 0 || !(sm_scale >= 0.f) || !std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
+  if (!ctx || !pp || pp->plan->ctx != ctx || ctx->device < 0 || !(sm_scale > 0.f) || !std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
   if (cudaSetDevice(ctx->device) != cudaSuccess) return DSA_ERR_CUDA;
   LaunchCount launched(ctx);
   if (pp->plan->T == 0) return DSA_OK;

@@ -1,0 +1,559 @@
+// prefix_tc.cu -- the attention over a shared prefix on the tensor cores.
+//
+// For a tile of 128 lanes (rows x heads of one kv head, so that the rows of many
+// requests meet the same keys in one product) and tiles of 128 keys:
+//     S = Q . K^T      (M = lanes, N = keys; both from shared memory)
+//     P = 2^(S * sm_scale * log2 e - m)  in bf16, over S in tensor memory
+//     O += P . V       (M = lanes, N = dims; A = P from tensor memory)
+// with a reference maximum m per lane that moves only when a logit is more than
+// 2^8 above it (O is rescaled then, in tensor memory).  A thread is a lane: its
+// maximum and sum need no exchange.
+//
+// A CTA has two streams of steps, each with its S and O (all 512 columns): while one
+// is in its softmax the tensor core works for the other.  Two tiles of queries over
+// the same keys are the two streams of a pair (each key tile is loaded once for
+// both); a lone tile's keys are given to the streams of many CTAs instead, each
+// with keys of its own.  Warps 0-3 and 4-7: a stream's softmax; warp 8 loads, by TMA
+// into a ring of half-tiles (K or V of 128 keys); warp 9 issues the products.  A
+// chain that more than one stream worked on leaves partial results, which
+// prefix_join_kernel adds up in a fixed order.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "fp8.cuh"
+#include "prefix.h"
+#include "ptx.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescale = 8.0f;        // log2 units that a logit may be above the reference maximum
+constexpr float kNoMax = -3.0e38f;      // the reference maximum of a lane that has seen no key (finite: less -inf it is no NaN)
+constexpr int kThreads = 320;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+
+__device__ __forceinline__ float exp2_approx(float x) {   // (relative error 2^-22; 0 for -inf)
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void st_global8(float *p, const float *v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+               "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+struct PrefixParams {
+  CUtensorMap tm_kv;   // cache as [pages * P, 2 * Hkv * D], box {64, BH}
+  CUtensorMap tm_q;    // q as [T, Hq, D], box {64, group, rows_a_tile}
+  const PrefixSeg *segs;
+  const PrefixCta *ctas;
+  const int32_t *pages;
+  __nv_bfloat16 *out;
+  float *part_o;
+  float2 *part_ml;
+  int *err;
+  int32_t Hq, Hkv, group, P, BH, num_pages, q_bytes;
+  float scale_log2;
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int CH = D / 64;                     // 64-column chunks of a row
+  static constexpr int CHUNK = kPrefixTile * 128;       // bytes: 128 rows of 64 columns
+  static constexpr int HALF = CH * CHUNK;               // K or V of a tile
+  static constexpr int NS = D == 128 ? 5 : 8;           // half-tiles in the ring
+  static constexpr int OFF_Q = NS * HALF;
+  static constexpr int OFF_BAR = OFF_Q + 2 * HALF;
+  static constexpr int BARS = 2 * NS + 10;
+  static constexpr int OFF_MISC = OFF_BAR + BARS * 8;
+  static constexpr int BYTES = OFF_MISC + 16 + 1024;    // + alignment slack
+  static constexpr uint32_t S_COL = 0, O_COL = 256;     // stream w's S at S_COL + 128 w, O at O_COL + 128 w
+  static constexpr uint32_t IDESC_QK = mma_idesc(128, kPrefixTile, 1u, false, false);
+  static constexpr uint32_t IDESC_PV = mma_idesc(128, D, 1u, false, true);
+};
+
+// Order of the ring's half-tiles.  A pair's key tile i: K, V at 2 i, 2 i + 1 of the phase.  The lone streams'
+// steps t (stream t & 1): K(0), K(1), V(0), K(2), V(1), ... K(n - 1), V(n - 2), V(n - 1), the order of their use.
+__device__ __forceinline__ int lone_k(int t) { return t == 0 ? 0 : 2 * t - 1; }
+__device__ __forceinline__ int lone_v(int t, int n) { return t < n - 1 ? 2 * t + 2 : 2 * n - 1; }
+
+// A walk over the tiles of a list of segments.
+struct Walk {
+  const PrefixSeg *seg;
+  int j, n;   // tile of the segment, its tiles
+  __device__ __forceinline__ void start(const PrefixSeg *s) { seg = s, j = 0, n = s->ntiles; }
+  // (past the list's end nothing is read: `left` tiles of the list are still to come)
+  __device__ __forceinline__ void next(int left) {
+    if (++j == n && left > 0) start(seg + 1);
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_constant__ PrefixParams p) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem), bar0 = sbase + C::OFF_BAR;
+  auto full = [&](int r) { return bar0 + 8u * (r % C::NS); };
+  auto empty = [&](int r) { return bar0 + 8u * (C::NS + r % C::NS); };
+  auto phase = [&](int r) { return static_cast<uint32_t>(r / C::NS) & 1u; };
+  auto qfull = [&](int w) { return bar0 + 8u * (2 * C::NS + w); };
+  auto qempty = [&](int w) { return bar0 + 8u * (2 * C::NS + 2 + w); };
+  auto sfull = [&](int w) { return bar0 + 8u * (2 * C::NS + 4 + w); };
+  auto pfull = [&](int w) { return bar0 + 8u * (2 * C::NS + 6 + w); };
+  auto ofull = [&](int w) { return bar0 + 8u * (2 * C::NS + 8 + w); };
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+  const uint32_t abort_addr = sbase + C::OFF_MISC + 4;
+  const int warp = threadIdx.x / 32, lane = lane_id();
+
+  if (threadIdx.x == 0) {
+    for (int r = 0; r < C::NS; ++r) {
+      mbar_init(full(r), 1);
+      mbar_init(empty(r), 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(qfull(w), 1);
+      mbar_init(qempty(w), 1);
+      mbar_init(sfull(w), 1);
+      mbar_init(pfull(w), 4);   // one arrival a warp
+      mbar_init(ofull(w), 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_kv);
+    tma_prefetch_desc(&p.tm_q);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency();
+  const PrefixCta cta = p.ctas[blockIdx.x];
+  const int na = cta.tiles_a, nb = cta.tiles_b;
+
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------ loads
+    // A lane's box: box lane / CH of the tile, chunk lane % CH; its cache row, or -1
+    const int box = lane / C::CH, chunk = lane % C::CH, boxes = kPrefixTile / p.BH;
+    auto lookup = [&](const Walk &k) {
+      if (box >= boxes) return -1;
+      const PrefixSeg &s = *k.seg;
+      const int q0 = s.slot0 + k.j * kPrefixTile + box * p.BH;
+      if (q0 + p.BH <= s.lo || q0 >= s.hi) return -1;
+      const uint32_t pi = static_cast<uint32_t>(q0) / static_cast<uint32_t>(p.P);
+      const int page = pi < static_cast<uint32_t>(s.npages) ? p.pages[s.page_off + pi] : -1;
+      if (page < 0 || page >= p.num_pages) {
+        atomicOr(p.err, kErrBounds);
+        return -1;
+      }
+      return page * p.P + (q0 - static_cast<int>(pi) * p.P);
+    };
+    int r = 0, q_loads[2] = {0, 0};
+    bool ok = true;
+    auto load = [&](int x0, int row) {   // the next half-tile of the ring, columns x0 ..
+      ok = ok && mbar_wait_warp(empty(r), phase(r) ^ 1u, abort_addr, p.err);
+      if (!ok) return;
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, row >= 0)) * p.BH * 128;
+      if (lane == 0) {
+        if (bytes) mbar_arrive_expect_tx(full(r), bytes);
+        else mbar_arrive(full(r));
+      }
+      __syncwarp();
+      if (row >= 0) tma_load_2d(sbase + (r % C::NS) * C::HALF + chunk * C::CHUNK + box * p.BH * 128, &p.tm_kv, x0 + chunk * 64, row, full(r));
+      ++r;
+    };
+    auto load_q = [&](int w, const PrefixSeg *s, int tile) {
+      if (q_loads[w] > 0) ok = ok && mbar_wait_warp(qempty(w), (q_loads[w] - 1) & 1, abort_addr, p.err);
+      if (!ok) return;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(qfull(w), p.q_bytes);
+        for (int c = 0; c < C::CH; ++c)
+          tma_load_3d(sbase + C::OFF_Q + w * C::HALF + c * C::CHUNK, &p.tm_q, c * 64, s->g * p.group, s->row[tile], qfull(w));
+      }
+      __syncwarp();
+      ++q_loads[w];
+    };
+    // (a tile's pages are looked up one tile ahead)
+    if (na > 0) {
+      Walk k;
+      k.start(p.segs + cta.a0);
+      int row = lookup(k);
+      for (int i = 0; i < na && ok; ++i) {
+        const PrefixSeg *s = k.seg;
+        const bool first = k.j == 0;
+        k.next(na - 1 - i);
+        const int row_next = i + 1 < na ? lookup(k) : -1;
+        if (first) {
+          load_q(0, s, 0);
+          load_q(1, s, 1);
+        }
+        load(s->g * D, row);
+        load((p.Hkv + s->g) * D, row);
+        row = row_next;
+      }
+    }
+    if (nb > 0 && ok) {
+      Walk k[2];
+      int left[2] = {(nb + 1) / 2, nb / 2}, rows[2] = {-1, -1}, rows_before = -1, g_before = 0;
+      for (int w = 0; w < 2; ++w)
+        if (left[w] > 0) {
+          k[w].start(p.segs + cta.b0[w]);
+          rows[w] = lookup(k[w]);
+        }
+#pragma unroll 1
+      for (int t = 0; t <= nb && ok; ++t) {
+        int row = -1, g = 0;
+        if (t < nb) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (w != (t & 1)) continue;
+            const PrefixSeg *s = k[w].seg;
+            const bool first = k[w].j == 0;
+            row = rows[w], g = s->g;
+            --left[w];
+            k[w].next(left[w]);
+            rows[w] = left[w] > 0 ? lookup(k[w]) : -1;
+            if (first) load_q(w, s, 0);
+          }
+          load(g * D, row);
+        }
+        if (t > 0) load((p.Hkv + g_before) * D, rows_before);
+        rows_before = row, g_before = g;
+      }
+    }
+    // nothing of ours may still be landing when the CTA leaves (an abort apart, all of it has been used)
+    if (lane == 0 && !ok) {
+      volatile int no_abort = 0;
+      for (int i = max(0, r - C::NS); i < r; ++i) mbar_wait(full(i), phase(i), &no_abort, p.err);
+      for (int w = 0; w < 2; ++w)
+        if (q_loads[w] > 0) mbar_wait(qfull(w), (q_loads[w] - 1) & 1, &no_abort, p.err);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      int q_waits[2] = {0, 0}, p_waits[2] = {0, 0};
+      bool ok = true;
+      auto qk = [&](int w, int r, bool first, bool last, bool release) {
+        if (first) {
+          ok = ok && mbar_wait(qfull(w), q_waits[w] & 1, abort_flag, p.err);
+          ++q_waits[w];
+        }
+        ok = ok && mbar_wait(full(r), phase(r), abort_flag, p.err);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t k = sbase + (r % C::NS) * C::HALF, q = sbase + C::OFF_Q + w * C::HALF;
+#pragma unroll
+        for (int c = 0; c < C::CH; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mma_f16_ss(tmem + C::S_COL + w * 128, smem_desc(q + c * C::CHUNK + i * 32, 16, 1024, kSwizzle128),
+                       smem_desc(k + c * C::CHUNK + i * 32, 16, 1024, kSwizzle128), C::IDESC_QK, (c | i) ? 1u : 0u);
+        mma_commit(sfull(w));
+        if (release) mma_commit(empty(r));
+        if (last) mma_commit(qempty(w));
+      };
+      auto pv = [&](int w, int r, bool first, bool last, bool release) {
+        ok = ok && mbar_wait(pfull(w), p_waits[w] & 1, abort_flag, p.err);
+        ++p_waits[w];
+        ok = ok && mbar_wait(full(r), phase(r), abort_flag, p.err);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t v = sbase + (r % C::NS) * C::HALF;
+#pragma unroll
+        for (int i = 0; i < kPrefixTile / 16; ++i)   // A: 16 keys are 8 columns; B read MN-major: 64-dim chunks CHUNK apart
+          mma_f16_ts(tmem + C::O_COL + w * 128, tmem + C::S_COL + w * 128 + i * 8,
+                     smem_desc(v + i * 16 * 128, C::CHUNK, 1024, kSwizzle128), C::IDESC_PV, (!first || i > 0) ? 1u : 0u);
+        if (release) mma_commit(empty(r));
+        if (last) mma_commit(ofull(w));
+      };
+      if (na > 0) {
+        Walk kq, kp;
+        kq.start(p.segs + cta.a0);
+        kp.start(p.segs + cta.a0);
+        qk(0, 0, true, kq.n == 1, false);
+        qk(1, 0, true, kq.n == 1, true);
+        for (int i = 0; i < na && ok; ++i) {
+          const bool more = i + 1 < na;
+          kq.next(na - 1 - i);
+          pv(0, 2 * i + 1, kp.j == 0, kp.j + 1 == kp.n, false);
+          if (more) qk(0, 2 * i + 2, kq.j == 0, kq.j + 1 == kq.n, false);
+          pv(1, 2 * i + 1, kp.j == 0, kp.j + 1 == kp.n, true);
+          if (more) qk(1, 2 * i + 2, kq.j == 0, kq.j + 1 == kq.n, true);
+          kp.next(na - 1 - i);
+        }
+      }
+      if (nb > 0 && ok) {
+        Walk kq[2], kp[2];
+        const int rb = 2 * na;
+        int left_q[2] = {(nb + 1) / 2, nb / 2}, left_p[2] = {(nb + 1) / 2, nb / 2};
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          if (left_q[w] > 0) {
+            kq[w].start(p.segs + cta.b0[w]);
+            kp[w].start(p.segs + cta.b0[w]);
+            qk(w, rb + lone_k(w), true, kq[w].n == 1, true);
+            kq[w].next(--left_q[w]);
+          }
+#pragma unroll 1
+        for (int t = 0; t < nb && ok; t += 2) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const int u = t + w;
+            if (u >= nb) continue;
+            pv(w, rb + lone_v(u, nb), kp[w].j == 0, kp[w].j + 1 == kp[w].n, true);
+            kp[w].next(--left_p[w]);
+            if (u + 2 < nb) {
+              qk(w, rb + lone_k(u + 2), kq[w].j == 0, kq[w].j + 1 == kq[w].n, true);
+              kq[w].next(--left_q[w]);
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int w = warp >> 2;
+    const int i = (warp & 3) * 32 + lane;   // lane of the tile
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t t_s = t_lane + C::S_COL + w * 128, t_o = t_lane + C::O_COL + w * 128;
+    const int own_row = i / p.group, own_head = i - own_row * p.group;
+    int s_waits = 0, o_waits = 0;
+    bool ok = true;
+    // a segment whose tile j's values are half-tile v_of(j) of the ring; zero: this stream clears values that no lane sees
+    auto run = [&](const PrefixSeg &s, int tile, bool zero, auto v_of) {
+      const int limit = s.causal ? s.limit[tile] + own_row : s.hi;
+      const int least = s.causal ? s.limit[tile] : s.hi;   // every lane sees the slots below
+      const int n = s.ntiles, lo = s.lo, hi = s.hi;
+      float m = kNoMax, l = 0.f;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        const int t0 = s.slot0 + j * kPrefixTile;
+        ok = mbar_wait_warp(sfull(w), s_waits & 1, abort_addr, p.err);
+        ++s_waits;
+        if (!ok) return;
+        tc_fence_after();
+        float x[kPrefixTile];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, *reinterpret_cast<float(*)[32]>(x + c * 32));
+        tmem_ld_wait();
+        if (t0 < lo || t0 + kPrefixTile > least) {
+#pragma unroll
+          for (int c = 0; c < kPrefixTile; ++c)
+            if (t0 + c < lo || t0 + c >= limit) x[c] = -INFINITY;
+        }
+        float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int c = 4; c < kPrefixTile; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        const bool move = top > m + kRescale;
+        if (__any_sync(0xffffffffu, move)) {
+          const float keep = move ? exp2_approx(m - top) : 1.f;
+          m = move ? top : m;
+          l *= keep;
+          // (every earlier product into O is complete: this S was issued after it)
+          if (j > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              float o[16];
+              tmem_ld16(t_o + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] *= keep;
+              tmem_st16(t_o + c, o);
+            }
+          }
+        }
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t packed[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const float a = exp2_approx(fmaf(x[h * 64 + 2 * c], p.scale_log2, -m));
+            const float b = exp2_approx(fmaf(x[h * 64 + 2 * c + 1], p.scale_log2, -m));
+            sum[c & 3] += a + b;
+            packed[c] = pack_bf16(a, b);
+          }
+          tmem_st32(t_s + h * 32, packed);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_st_wait();
+        // values of slots that no lane sees are cleared once they are there (a zero weight must not meet what
+        // they hold, or what an unloaded box left)
+        if (zero && (t0 < lo || t0 + kPrefixTile > hi)) {
+          const int r = v_of(j);
+          ok = mbar_wait_warp(full(r), phase(r), abort_addr, p.err);
+          if (!ok) return;
+          if (t0 + i < lo || t0 + i >= hi) {
+#pragma unroll
+            for (int c = 0; c < C::CH; ++c)
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                st_shared_v4(sbase + (r % C::NS) * C::HALF + c * C::CHUNK + i * 128 + k * 16, make_uint4(0u, 0u, 0u, 0u));
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pfull(w));
+      }
+      ok = mbar_wait_warp(ofull(w), o_waits & 1, abort_addr, p.err);
+      ++o_waits;
+      if (!ok) return;
+      tc_fence_after();
+      const int part = s.part[tile];
+      const bool live = i < s.lanes[tile];
+      const float scale = part < 0 ? 1.f / l : 1.f;
+      float *to = p.part_o + (static_cast<int64_t>(part) + i) * D;
+      __nv_bfloat16 *out = p.out + ((static_cast<int64_t>(s.row[tile]) + own_row) * p.Hq + s.g * p.group + own_head) * D;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        tmem_ld32(t_o + c, o);
+        tmem_ld_wait();
+        if (!live) continue;
+        if (part < 0) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8)
+            *reinterpret_cast<uint4 *>(out + c + k) =
+                make_uint4(pack_bf16(o[k] * scale, o[k + 1] * scale), pack_bf16(o[k + 2] * scale, o[k + 3] * scale),
+                           pack_bf16(o[k + 4] * scale, o[k + 5] * scale), pack_bf16(o[k + 6] * scale, o[k + 7] * scale));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) st_global8(to + c + k, o + k);
+        }
+      }
+      if (live && part >= 0) p.part_ml[part + i] = make_float2(m, l);
+      tc_fence_before();   // (O is read: the stream's next products into it follow its next arrival)
+    };
+    int done = 0;
+    for (int a = cta.a0; a < cta.a1 && ok; ++a) {
+      const PrefixSeg &s = p.segs[a];
+      run(s, w, w == 0, [&](int j) { return 2 * (done + j) + 1; });
+      done += s.ntiles;
+    }
+    done = 0;
+    for (int b = cta.b0[w]; b < cta.b1[w] && ok; ++b) {
+      const PrefixSeg &s = p.segs[b];
+      run(s, 0, true, [&](int j) { return 2 * na + lone_v(2 * (done + j) + w, nb); });
+      done += s.ntiles;
+    }
+  }
+  __syncthreads();
+  linger_if_aborted(abort_addr, 1000 * 1000);   // (products in flight end in microseconds)
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+struct JoinParams {
+  const PrefixRow *rows;
+  const PrefixParts *parts;
+  const float *part_o;
+  const float2 *part_ml;
+  __nv_bfloat16 *out;
+  int64_t items;
+  int32_t Hq, Hkv, group;
+};
+
+// A warp a (row, query head): its partial results, the own keys' first, in their order.
+template <int D>
+__global__ void __launch_bounds__(256) prefix_join_kernel(const JoinParams p) {
+  constexpr int N = D / 32;
+  grid_dependency();
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
+  if (item >= p.items) return;
+  const int lane = lane_id();
+  const int64_t row = item / p.Hq;
+  const int h = static_cast<int>(item - row * p.Hq), g = h / p.group, hl = h - g * p.group;
+  const PrefixRow at = p.rows[row];
+  const PrefixParts own = p.parts[static_cast<int64_t>(at.own) * p.Hkv + g];
+  if (own.count == 0) return;   // written already
+  PrefixParts shared{0, 0, 0};
+  if (at.shared >= 0) shared = p.parts[static_cast<int64_t>(at.shared) * p.Hkv + g];
+  const int n = own.count + shared.count;
+  auto lane_of = [&](int k) {
+    return k < own.count ? static_cast<int64_t>(own.first) + static_cast<int64_t>(k) * own.lanes + at.own_lane + hl
+                         : static_cast<int64_t>(shared.first) + static_cast<int64_t>(k - own.count) * shared.lanes + at.shared_lane + hl;
+  };
+  float top = kNoMax;
+  for (int k = lane; k < n; k += 32) top = fmaxf(top, p.part_ml[lane_of(k)].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float sum = 0.f, o[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) o[i] = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) {
+    const int64_t l = lane_of(k);
+    const float2 ml = p.part_ml[l];
+    const float weight = exp2_approx(ml.x - top);
+    sum = fmaf(weight, ml.y, sum);
+    const float *src = p.part_o + l * D + lane * N;
+    float v[N];
+    if constexpr (N == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(src);
+    else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(src);
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = fmaf(weight, v[i], o[i]);
+  }
+  const float scale = 1.f / sum;
+  __nv_bfloat16 *out = p.out + item * D + lane * N;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) *reinterpret_cast<uint32_t *>(out + i) = pack_bf16(o[i] * scale, o[i + 1] * scale);
+}
+
+template <int D>
+cudaError_t run(const dsa_ctx *ctx, const dsa_prefix_plan_t *pp, const void *q, const void *kv, float sm_scale, void *out,
+                cudaStream_t s, int32_t *launches) {
+  const dsa_plan_t &plan = *pp->plan;
+  const dsa_msa_shape_t &ms = pp->shape;
+  PrefixParams p{};
+  p.P = ctx->cfg.page_size, p.BH = plan.box_rows, p.num_pages = plan.cache_pages;
+  p.Hq = ms.q_heads, p.Hkv = ms.kv_heads, p.group = ms.q_heads / ms.kv_heads;
+  const uint64_t cols = 2ull * ms.kv_heads * D;
+  const uint64_t dims[3] = {D, static_cast<uint64_t>(ms.q_heads), static_cast<uint64_t>(plan.T)};
+  const uint64_t strides[2] = {D * 2, static_cast<uint64_t>(ms.q_heads) * D * 2};
+  const uint32_t box[3] = {64, static_cast<uint32_t>(p.group), static_cast<uint32_t>(pp->rows_a_tile)};
+  if (!encode_tiled_2d(&p.tm_kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, const_cast<void *>(kv), cols,
+                       static_cast<uint64_t>(plan.cache_pages) * p.P, cols * 2, 64, p.BH, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tiled_3d(&p.tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, const_cast<void *>(q), dims, strides, box,
+                       CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  p.segs = pp->segs, p.ctas = pp->ctas, p.pages = plan.pages;
+  p.out = static_cast<__nv_bfloat16 *>(out);
+  p.part_o = pp->part_o, p.part_ml = pp->part_ml, p.err = ctx->err;
+  p.q_bytes = pp->rows_a_tile * p.group * D * 2;
+  p.scale_log2 = sm_scale * kLog2e;
+  static std::atomic<uint64_t> smem_limit_set{0};
+  cudaError_t e = ensure_smem_limit(prefix_tc_kernel<D>, Cfg<D>::BYTES, ctx->device, smem_limit_set);
+  if (e != cudaSuccess) return e;
+  *launches += 1;
+  e = launch_overlapped(prefix_tc_kernel<D>, dim3(pp->n_ctas), kThreads, Cfg<D>::BYTES, 1, s, p);
+  if (e != cudaSuccess || !pp->joins) return e;
+  JoinParams j{pp->rows, pp->parts, pp->part_o, pp->part_ml, p.out, static_cast<int64_t>(plan.T) * ms.q_heads, p.Hq, p.Hkv, p.group};
+  *launches += 1;
+  return launch_overlapped(prefix_join_kernel<D>, dim3(static_cast<unsigned>((j.items + 7) / 8)), 256, 0, 1, s, j);
+}
+
+}  // namespace
+
+bool prefix_tc_supported(const dsa_config_t &c, const dsa_msa_shape_t &s) {
+  return (s.head_dim == 128 || s.head_dim == 64) && s.q_heads / s.kv_heads <= kPrefixTile && c.page_size % 8 == 0;
+}
+
+cudaError_t launch_prefix_tc(const dsa_ctx *ctx, const dsa_prefix_plan_t *pp, const void *q, const void *kv, float sm_scale,
+                             void *out, cudaStream_t s, int32_t *launches) {
+  return pp->shape.head_dim == 128 ? run<128>(ctx, pp, q, kv, sm_scale, out, s, launches)
+                                   : run<64>(ctx, pp, q, kv, sm_scale, out, s, launches);
+}
+
+}  // namespace dsa

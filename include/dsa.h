@@ -633,7 +633,7 @@ dsa_status dsa_append_kv(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_rotar
  * spans do not share those positions; DSA_ERR_UNSUPPORTED: a capturable plan,
  * head_dim above 512, q_heads above 1024, 2^31 or more rows x q_heads.
  *
- * dsa_prefix_attend: q (T, q_heads, head_dim) bf16, kv_cache as dsa_msa_attend's
+ * dsa_prefix_attend (sm_scale above 0): q (T, q_heads, head_dim) bf16, kv_cache as dsa_msa_attend's
  * with this step's rows in place (dsa_append_kv), out (T, q_heads, head_dim) bf16;
  * sums, maxima and logits in fp32, probabilities rounded to bf16 on the tensor
  * cores.  Each on 16 bytes.  Cache rows that no row of the call sees may
