@@ -147,37 +147,40 @@ struct Piece {
 // A segment costs kStart key tiles beside its own: its queries' load, the first product's latency, its output.
 constexpr double kStart = 2.0;
 
-// Cuts a line of pieces into at most n runs of about the same cost, at least `least` each.  A cut that would
-// leave less than a sliver on either side of it goes to the piece's end there.
+// Cuts a line of pieces into at most n runs of about the same cost, at least `least` each.  A cut costs a start;
+// one that would leave less than a sliver behind it is not made, nor one before a piece's first key tile.
 std::vector<std::vector<Piece>> cut_line(const std::vector<Piece> &line, int n, double least) {
-  double total = 0.0;
-  for (const Piece &x : line) total += x.t1 - x.t0 + kStart;
+  double left = 0.0;      // cost still to lay out
+  for (const Piece &x : line) left += x.t1 - x.t0 + kStart;
   std::vector<std::vector<Piece>> out;
   if (line.empty()) return out;
-  n = std::max(1, std::min(n, static_cast<int>(total / least)));
-  const double each = total / n, sliver = std::max(1.0, 0.08 * each);
-  out.resize(n);
-  double at = 0.0;      // cost laid out so far
-  int b = 0;
-  for (Piece x : line) {
-    for (;;) {
-      const double cost = x.t1 - x.t0 + kStart, room = (b + 1) * each - at;
-      if (b == n - 1 || cost <= room + sliver) {
-        out[b].push_back(x);
-        at += cost;
-        if (b < n - 1 && at >= (b + 1) * each - 0.5) ++b;
-        break;
-      }
-      const int32_t here = static_cast<int32_t>(room - kStart + 0.5);
-      if (here < sliver) {      // (nothing of it here)
-        at = std::max(at, (b + 1) * each);
-        ++b;
+  n = std::max(1, std::min(n, static_cast<int>(left / least)));
+  size_t i = 0;
+  Piece x = line[0];
+  for (; n > 0 && i < line.size(); --n) {
+    out.emplace_back();
+    const double share = left / n, sliver = std::max(0.5, 0.05 * share);
+    double room = share;
+    while (i < line.size()) {
+      const double cost = x.t1 - x.t0 + kStart;
+      if (n == 1 || cost <= room + sliver) {
+        out.back().push_back(x);
+        room -= cost, left -= cost;
+        if (++i < line.size()) x = line[i];
         continue;
       }
-      out[b].push_back(Piece{x.chain, x.t0, x.t0 + here});
-      at = std::max(at + here + kStart, (b + 1) * each);
-      x.t0 += here;
-      ++b;
+      int32_t here = static_cast<int32_t>(room - kStart + 0.5);
+      if (out.back().empty()) here = std::max(here, 1);
+      here = std::min(here, x.t1 - x.t0 - 1);
+      if (here < 1 || (here < sliver && !out.back().empty())) break;
+      out.back().push_back(Piece{x.chain, x.t0, x.t0 + here});
+      x.t0 += here, left -= here;
+      break;
+    }
+    if (out.back().empty()) {      // (a piece of one tile that is above the share)
+      out.back().push_back(x);
+      left -= x.t1 - x.t0 + kStart;
+      if (++i < line.size()) x = line[i];
     }
   }
   return out;
@@ -278,7 +281,7 @@ void lay_out(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, Work &w) {
       if (w.chains[k].tile[1] < 0) lone.push_back(Piece{static_cast<int32_t>(k), 0, w.chains[k].ntiles});
     c = e;
   }
-  const auto a = cut_line(pairs, n, 4.0 + kStart), b = cut_line(lone, n, 2.0);
+  const auto a = cut_line(pairs, n, 4.0 + kStart), b = cut_line(lone, n, 4.0);
   w.ctas.assign(std::max(a.size(), b.size()), PrefixCta{});
   std::vector<int32_t> pieces_of(w.tiles.size() * Hkv, 0);
   auto put = [&](const Piece &x) {

@@ -68,7 +68,7 @@ struct Cfg {
   static constexpr int NS = D == 128 ? 5 : 8;           // half-tiles in the ring
   static constexpr int OFF_Q = NS * HALF;
   static constexpr int OFF_BAR = OFF_Q + 2 * HALF;
-  static constexpr int BARS = 2 * NS + 10;
+  static constexpr int BARS = 2 * NS + 12;
   static constexpr int OFF_MISC = OFF_BAR + BARS * 8;
   static constexpr int BYTES = OFF_MISC + 16 + 1024;    // + alignment slack
   static constexpr uint32_t S_COL = 0, O_COL = 256;     // stream w's S at S_COL + 128 w, O at O_COL + 128 w
@@ -78,8 +78,19 @@ struct Cfg {
 
 // Order of the ring's half-tiles.  A pair's key tile i: K, V at 2 i, 2 i + 1 of the phase.  The lone streams'
 // steps t (stream t & 1): K(0), K(1), V(0), K(2), V(1), ... K(n - 1), V(n - 2), V(n - 1), the order of their use.
-__device__ __forceinline__ int lone_k(int t) { return t == 0 ? 0 : 2 * t - 1; }
 __device__ __forceinline__ int lone_v(int t, int n) { return t < n - 1 ? 2 * t + 2 : 2 * n - 1; }
+
+// A place in the ring: its slot, and the parity of that slot's use.
+template <int NS>
+struct Ring {
+  int st;
+  uint32_t phase;
+  __device__ __forceinline__ explicit Ring(int i) : st(i % NS), phase(static_cast<uint32_t>(i / NS) & 1u) {}
+  __device__ __forceinline__ void skip(int n) {
+    st += n;
+    if (st >= NS) st -= NS, phase ^= 1u;
+  }
+};
 
 // A walk over the tiles of a list of segments.
 struct Walk {
@@ -104,8 +115,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
   auto qfull = [&](int w) { return bar0 + 8u * (2 * C::NS + w); };
   auto qempty = [&](int w) { return bar0 + 8u * (2 * C::NS + 2 + w); };
   auto sfull = [&](int w) { return bar0 + 8u * (2 * C::NS + 4 + w); };
-  auto pfull = [&](int w) { return bar0 + 8u * (2 * C::NS + 6 + w); };
-  auto ofull = [&](int w) { return bar0 + 8u * (2 * C::NS + 8 + w); };
+  auto pfull = [&](int w, int h) { return bar0 + 8u * (2 * C::NS + 6 + 2 * w + h); };   // h: the first 64 keys, the others
+  auto ofull = [&](int w) { return bar0 + 8u * (2 * C::NS + 10 + w); };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
   const uint32_t abort_addr = sbase + C::OFF_MISC + 4;
@@ -120,7 +131,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
       mbar_init(qfull(w), 1);
       mbar_init(qempty(w), 1);
       mbar_init(sfull(w), 1);
-      mbar_init(pfull(w), 4);   // one arrival a warp
+      mbar_init(pfull(w, 0), 4);   // one arrival a warp
+      mbar_init(pfull(w, 1), 4);
       mbar_init(ofull(w), 1);
     }
     *abort_flag = 0;
@@ -240,87 +252,106 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      int q_waits[2] = {0, 0}, p_waits[2] = {0, 0};
-      bool ok = true;
-      auto qk = [&](int w, int r, bool first, bool last, bool release) {
-        if (first) {
-          ok = ok && mbar_wait(qfull(w), q_waits[w] & 1, abort_flag, p.err);
-          ++q_waits[w];
-        }
-        ok = ok && mbar_wait(full(r), phase(r), abort_flag, p.err);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t k = sbase + (r % C::NS) * C::HALF, q = sbase + C::OFF_Q + w * C::HALF;
+    // (the whole warp walks and waits, one elected thread issues: its operands stay in uniform registers.  Issued by a
+    // lane that a branch picked, each of the 16 instructions of a step took some 80 cycles.)
+    const uint64_t desc0 = smem_desc(sbase, 16, 1024, kSwizzle128), desc_v0 = smem_desc(sbase, C::CHUNK, 1024, kSwizzle128);
+    uint32_t q_phase = 0, p_phase = 0;      // bit w: stream w's
+    bool ok = true;
+    auto qk = [&](int w, const Ring<C::NS> &r, bool first, bool last, bool release) {
+      ok = ok && mbar_wait_warp(full(r.st), r.phase, abort_addr, p.err);
+      if (first) {
+        ok = ok && mbar_wait_warp(qfull(w), (q_phase >> w) & 1, abort_addr, p.err);
+        q_phase ^= 1u << w;
+      }
+      if (!ok) return;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t q = desc0 + ((C::OFF_Q + w * C::HALF) >> 4), k = desc0 + r.st * (C::HALF >> 4);
 #pragma unroll
         for (int c = 0; c < C::CH; ++c)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            mma_f16_ss(tmem + C::S_COL + w * 128, smem_desc(q + c * C::CHUNK + i * 32, 16, 1024, kSwizzle128),
-                       smem_desc(k + c * C::CHUNK + i * 32, 16, 1024, kSwizzle128), C::IDESC_QK, (c | i) ? 1u : 0u);
+            mma_f16_ss(tmem + C::S_COL + w * 128, q + c * (C::CHUNK >> 4) + 2 * i, k + c * (C::CHUNK >> 4) + 2 * i, C::IDESC_QK,
+                       (c | i) ? 1u : 0u);
         mma_commit(sfull(w));
-        if (release) mma_commit(empty(r));
+        if (release) mma_commit(empty(r.st));
         if (last) mma_commit(qempty(w));
-      };
-      auto pv = [&](int w, int r, bool first, bool last, bool release) {
-        ok = ok && mbar_wait(pfull(w), p_waits[w] & 1, abort_flag, p.err);
-        ++p_waits[w];
-        ok = ok && mbar_wait(full(r), phase(r), abort_flag, p.err);
+      }
+      __syncwarp();
+    };
+    auto pv = [&](int w, const Ring<C::NS> &r, bool first, bool last, bool release) {
+      const uint32_t ph = (p_phase >> w) & 1;
+      p_phase ^= 1u << w;
+      ok = ok && mbar_wait_warp_both(full(r.st), r.phase, pfull(w, 0), ph, abort_addr, p.err);
+      const uint64_t v = desc_v0 + r.st * (C::HALF >> 4);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h) ok = ok && mbar_wait_warp(pfull(w, 1), ph, abort_addr, p.err);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t v = sbase + (r % C::NS) * C::HALF;
+        if (elect_one()) {
 #pragma unroll
-        for (int i = 0; i < kPrefixTile / 16; ++i)   // A: 16 keys are 8 columns; B read MN-major: 64-dim chunks CHUNK apart
-          mma_f16_ts(tmem + C::O_COL + w * 128, tmem + C::S_COL + w * 128 + i * 8,
-                     smem_desc(v + i * 16 * 128, C::CHUNK, 1024, kSwizzle128), C::IDESC_PV, (!first || i > 0) ? 1u : 0u);
-        if (release) mma_commit(empty(r));
-        if (last) mma_commit(ofull(w));
-      };
-      if (na > 0) {
-        Walk kq, kp;
-        kq.start(p.segs + cta.a0);
-        kp.start(p.segs + cta.a0);
-        qk(0, 0, true, kq.n == 1, false);
-        qk(1, 0, true, kq.n == 1, true);
-        for (int i = 0; i < na && ok; ++i) {
-          const bool more = i + 1 < na;
-          kq.next(na - 1 - i);
-          pv(0, 2 * i + 1, kp.j == 0, kp.j + 1 == kp.n, false);
-          if (more) qk(0, 2 * i + 2, kq.j == 0, kq.j + 1 == kq.n, false);
-          pv(1, 2 * i + 1, kp.j == 0, kp.j + 1 == kp.n, true);
-          if (more) qk(1, 2 * i + 2, kq.j == 0, kq.j + 1 == kq.n, true);
-          kp.next(na - 1 - i);
+          for (int i = 4 * h; i < 4 * h + 4; ++i)   // A: 16 keys are 8 columns; B read MN-major: 64-dim chunks CHUNK apart
+            mma_f16_ts(tmem + C::O_COL + w * 128, tmem + C::S_COL + w * 128 + i * 8, v + i * (16 * 128 >> 4), C::IDESC_PV,
+                       (!first || i > 0) ? 1u : 0u);
+          if (h && release) mma_commit(empty(r.st));
+          if (h && last) mma_commit(ofull(w));
         }
+        __syncwarp();
       }
-      if (nb > 0 && ok) {
-        Walk kq[2], kp[2];
-        const int rb = 2 * na;
-        int left_q[2] = {(nb + 1) / 2, nb / 2}, left_p[2] = {(nb + 1) / 2, nb / 2};
-#pragma unroll
-        for (int w = 0; w < 2; ++w)
-          if (left_q[w] > 0) {
-            kq[w].start(p.segs + cta.b0[w]);
-            kp[w].start(p.segs + cta.b0[w]);
-            qk(w, rb + lone_k(w), true, kq[w].n == 1, true);
-            kq[w].next(--left_q[w]);
-          }
+    };
+    if (na > 0) {
+      Walk kq, kp;
+      kq.start(p.segs + cta.a0);
+      kp.start(p.segs + cta.a0);
+      Ring<C::NS> rk(0), rv(1);
+      qk(0, rk, true, kq.n == 1, false);
+      qk(1, rk, true, kq.n == 1, true);
 #pragma unroll 1
-        for (int t = 0; t < nb && ok; t += 2) {
+      for (int i = 0; i < na && ok; ++i) {
+        const bool more = i + 1 < na;
+        kq.next(na - 1 - i);
+        rk.skip(2);
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const int u = t + w;
-            if (u >= nb) continue;
-            pv(w, rb + lone_v(u, nb), kp[w].j == 0, kp[w].j + 1 == kp[w].n, true);
+        for (int w = 0; w < 2; ++w) {
+          pv(w, rv, kp.j == 0, kp.j + 1 == kp.n, w == 1);
+          if (more) qk(w, rk, kq.j == 0, kq.j + 1 == kq.n, w == 1);
+        }
+        rv.skip(2);
+        kp.next(na - 1 - i);
+      }
+    }
+    if (nb > 0 && ok) {
+      Walk kq[2], kp[2];
+      int left_q[2] = {(nb + 1) / 2, nb / 2}, left_p[2] = {(nb + 1) / 2, nb / 2};
+      Ring<C::NS> rk(2 * na), rv(2 * na + lone_v(0, nb));
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        if (left_q[w] > 0) {
+          kq[w].start(p.segs + cta.b0[w]);
+          kp[w] = kq[w];
+          qk(w, rk, true, kq[w].n == 1, true);
+          kq[w].next(--left_q[w]);
+          rk.skip(w + 1);      // K(0), K(1), then every other half-tile
+        }
+#pragma unroll 1
+      for (int t = 0; t < nb && ok; t += 2) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const int u = t + w;
+          if (u < nb) {
+            pv(w, rv, kp[w].j == 0, kp[w].j + 1 == kp[w].n, true);
             kp[w].next(--left_p[w]);
+            rv.skip(u + 2 < nb ? 2 : 1);
             if (u + 2 < nb) {
-              qk(w, rb + lone_k(u + 2), kq[w].j == 0, kq[w].j + 1 == kq[w].n, true);
+              qk(w, rk, kq[w].j == 0, kq[w].j + 1 == kq[w].n, true);
               kq[w].next(--left_q[w]);
+              rk.skip(2);
             }
           }
         }
       }
     }
-    __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
     const int w = warp >> 2;
@@ -330,8 +361,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
     const int own_row = i / p.group, own_head = i - own_row * p.group;
     int s_waits = 0, o_waits = 0;
     bool ok = true;
-    // a segment whose tile j's values are half-tile v_of(j) of the ring; zero: this stream clears values that no lane sees
-    auto run = [&](const PrefixSeg &s, int tile, bool zero, auto v_of) {
+    // The pairs' segments, then this stream's own (one loop: the code is large enough to miss the instruction cache).
+    const int own_pairs = cta.a1 - cta.a0, segs = own_pairs + cta.b1[w] - cta.b0[w];
+    int done = 0;      // key tiles of the phase before this segment
+#pragma unroll 1
+    for (int n_seg = 0; n_seg < segs; ++n_seg) {
+      const bool lone = n_seg >= own_pairs;
+      if (n_seg == own_pairs) done = 0;
+      const PrefixSeg &s = p.segs[lone ? cta.b0[w] + n_seg - own_pairs : cta.a0 + n_seg];
+      const int tile = lone ? 0 : w;
+      const bool zero = lone || w == 0;      // whether this stream clears values that no lane sees
       const int limit = s.causal ? s.limit[tile] + own_row : s.hi;
       const int least = s.causal ? s.limit[tile] : s.hi;   // every lane sees the slots below
       const int n = s.ntiles, lo = s.lo, hi = s.hi;
@@ -341,20 +380,33 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
         const int t0 = s.slot0 + j * kPrefixTile;
         ok = mbar_wait_warp(sfull(w), s_waits & 1, abort_addr, p.err);
         ++s_waits;
-        if (!ok) return;
+        if (!ok) break;
         tc_fence_after();
+        if (t0 < lo || t0 + kPrefixTile > least) {
+          // slots that the lane does not see, in tensor memory: kept out of the unrolled code below
+#pragma unroll 1
+          for (int c0 = 0; c0 < kPrefixTile; c0 += 16) {
+            float v[16];
+            tmem_ld16(t_s + c0, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              if (t0 + c0 + c < lo || t0 + c0 + c >= limit) v[c] = -INFINITY;
+            tmem_st16(t_s + c0, v);
+          }
+          tmem_st_wait();
+        }
         float x[kPrefixTile];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, *reinterpret_cast<float(*)[32]>(x + c * 32));
         tmem_ld_wait();
-        if (t0 < lo || t0 + kPrefixTile > least) {
-#pragma unroll
-          for (int c = 0; c < kPrefixTile; ++c)
-            if (t0 + c < lo || t0 + c >= limit) x[c] = -INFINITY;
-        }
         float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int c = 4; c < kPrefixTile; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
+        for (int c = 4; c + 8 <= kPrefixTile; c += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], x[c + k]), x[c + 4 + k]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[kPrefixTile - 4 + k]);
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
         const bool move = top > m + kRescale;
         if (__any_sync(0xffffffffu, move)) {
@@ -374,27 +426,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
             }
           }
         }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t packed[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float a = exp2_approx(fmaf(x[h * 64 + 2 * c], p.scale_log2, -m));
-            const float b = exp2_approx(fmaf(x[h * 64 + 2 * c + 1], p.scale_log2, -m));
-            sum[c & 3] += a + b;
-            packed[c] = pack_bf16(a, b);
-          }
-          tmem_st32(t_s + h * 32, packed);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_st_wait();
         // values of slots that no lane sees are cleared once they are there (a zero weight must not meet what
         // they hold, or what an unloaded box left)
         if (zero && (t0 < lo || t0 + kPrefixTile > hi)) {
-          const int r = v_of(j);
+          const int r = lone ? 2 * na + lone_v(2 * (done + j) + w, nb) : 2 * (done + j) + 1;
           ok = mbar_wait_warp(full(r), phase(r), abort_addr, p.err);
-          if (!ok) return;
+          if (!ok) break;
           if (t0 + i < lo || t0 + i >= hi) {
 #pragma unroll
             for (int c = 0; c < C::CH; ++c)
@@ -404,13 +441,36 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
           }
           fence_proxy_async_smem();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(pfull(w));
+        // the weights, 64 keys at a time: the product starts on the first of them
+        const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2), minus2 = f2_pack(-m, -m);
+        uint64_t sum[2] = {f2_pack(l, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t packed[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float a, b;
+            f2_unpack(f2_fma(f2_pack(x[q * 32 + 2 * c], x[q * 32 + 2 * c + 1]), scale2, minus2), a, b);
+            a = exp2_approx(a), b = exp2_approx(b);
+            sum[c & 1] = f2_add(sum[c & 1], f2_pack(a, b));
+            packed[c] = pack_bf16(a, b);
+          }
+          tmem_st16(t_s + q * 16, packed);
+          if (q & 1) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pfull(w, q >> 1));
+          }
+        }
+        float a, b;
+        f2_unpack(f2_add(sum[0], sum[1]), a, b);
+        l = a + b;
       }
-      ok = mbar_wait_warp(ofull(w), o_waits & 1, abort_addr, p.err);
+      ok = ok && mbar_wait_warp(ofull(w), o_waits & 1, abort_addr, p.err);
       ++o_waits;
-      if (!ok) return;
+      if (!ok) break;
+      done += n;
       tc_fence_after();
       const int part = s.part[tile];
       const bool live = i < s.lanes[tile];
@@ -422,32 +482,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
         float o[32];
         tmem_ld32(t_o + c, o);
         tmem_ld_wait();
-        if (!live) continue;
-        if (part < 0) {
+        if (live && part < 0) {
 #pragma unroll
           for (int k = 0; k < 32; k += 8)
             *reinterpret_cast<uint4 *>(out + c + k) =
                 make_uint4(pack_bf16(o[k] * scale, o[k + 1] * scale), pack_bf16(o[k + 2] * scale, o[k + 3] * scale),
                            pack_bf16(o[k + 4] * scale, o[k + 5] * scale), pack_bf16(o[k + 6] * scale, o[k + 7] * scale));
-        } else {
+        } else if (live) {
 #pragma unroll
           for (int k = 0; k < 32; k += 8) st_global8(to + c + k, o + k);
         }
+        __syncwarp();
       }
       if (live && part >= 0) p.part_ml[part + i] = make_float2(m, l);
       tc_fence_before();   // (O is read: the stream's next products into it follow its next arrival)
-    };
-    int done = 0;
-    for (int a = cta.a0; a < cta.a1 && ok; ++a) {
-      const PrefixSeg &s = p.segs[a];
-      run(s, w, w == 0, [&](int j) { return 2 * (done + j) + 1; });
-      done += s.ntiles;
-    }
-    done = 0;
-    for (int b = cta.b0[w]; b < cta.b1[w] && ok; ++b) {
-      const PrefixSeg &s = p.segs[b];
-      run(s, 0, true, [&](int j) { return 2 * na + lone_v(2 * (done + j) + w, nb); });
-      done += s.ntiles;
     }
   }
   __syncthreads();
