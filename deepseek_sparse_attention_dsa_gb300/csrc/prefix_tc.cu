@@ -252,19 +252,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
-    // (the whole warp walks and waits, one elected thread issues: its operands stay in uniform registers.  Issued by a
-    // lane that a branch picked, each of the 16 instructions of a step took some 80 cycles.)
+    // One warp for both streams, so that half-tiles are awaited in the order in which they were asked for (a parity
+    // says nothing of a fill two uses away).  The whole warp walks and waits, one elected thread issues: its operands
+    // stay in uniform registers.  (Issued by a lane that a branch picked, each of the 16 instructions of a step took
+    // some 80 cycles.)  A wait costs some 200 cycles, met or not: the three that a step begins with are tried
+    // together, and the one between its products has the first half of the first behind it.
     const uint64_t desc0 = smem_desc(sbase, 16, 1024, kSwizzle128), desc_v0 = smem_desc(sbase, C::CHUNK, 1024, kSwizzle128);
     uint32_t q_phase = 0, p_phase = 0;      // bit w: stream w's
     bool ok = true;
     auto qk = [&](int w, const Ring<C::NS> &r, bool first, bool last, bool release) {
-      ok = ok && mbar_wait_warp(full(r.st), r.phase, abort_addr, p.err);
       if (first) {
         ok = ok && mbar_wait_warp(qfull(w), (q_phase >> w) & 1, abort_addr, p.err);
         q_phase ^= 1u << w;
+        tc_fence_after();
       }
       if (!ok) return;
-      tc_fence_after();
       if (elect_one()) {
         const uint64_t q = desc0 + ((C::OFF_Q + w * C::HALF) >> 4), k = desc0 + r.st * (C::HALF >> 4);
 #pragma unroll
@@ -279,32 +281,43 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
       }
       __syncwarp();
     };
-    auto pv = [&](int w, const Ring<C::NS> &r, bool first, bool last, bool release) {
+    // Stream w's step: O += P V, and behind it (they run in order, and S's columns hold P) the next S of the stream.
+    auto step = [&](int w, const Ring<C::NS> &v, const Walk &kp, const Ring<C::NS> &k, const Walk &kq, bool more, bool release) {
       const uint32_t ph = (p_phase >> w) & 1;
       p_phase ^= 1u << w;
-      ok = ok && mbar_wait_warp_both(full(r.st), r.phase, pfull(w, 0), ph, abort_addr, p.err);
-      const uint64_t v = desc_v0 + r.st * (C::HALF >> 4);
+      if (more) ok = ok && mbar_wait_warp_three(full(v.st), v.phase, full(k.st), k.phase, pfull(w, 0), ph, abort_addr, p.err);
+      else ok = ok && mbar_wait_warp_both(full(v.st), v.phase, pfull(w, 0), ph, abort_addr, p.err);
+      if (!ok) return;
+      tc_fence_after();
+      const uint64_t vd = desc_v0 + v.st * (C::HALF >> 4);
+      const bool last = kp.j + 1 == kp.n, first = kp.j == 0;
+      if (elect_one()) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (h) ok = ok && mbar_wait_warp(pfull(w, 1), ph, abort_addr, p.err);
-        if (!ok) return;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int i = 4 * h; i < 4 * h + 4; ++i)   // A: 16 keys are 8 columns; B read MN-major: 64-dim chunks CHUNK apart
-            mma_f16_ts(tmem + C::O_COL + w * 128, tmem + C::S_COL + w * 128 + i * 8, v + i * (16 * 128 >> 4), C::IDESC_PV,
-                       (!first || i > 0) ? 1u : 0u);
-          if (h && release) mma_commit(empty(r.st));
-          if (h && last) mma_commit(ofull(w));
-        }
-        __syncwarp();
+        for (int i = 0; i < 4; ++i)   // A: 16 keys are 8 columns; B read MN-major: 64-dim chunks CHUNK apart
+          mma_f16_ts(tmem + C::O_COL + w * 128, tmem + C::S_COL + w * 128 + i * 8, vd + i * (16 * 128 >> 4), C::IDESC_PV,
+                     (!first || i > 0) ? 1u : 0u);
       }
+      __syncwarp();
+      ok = mbar_wait_warp(pfull(w, 1), ph, abort_addr, p.err);
+      if (!ok) return;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int i = 4; i < 8; ++i)
+          mma_f16_ts(tmem + C::O_COL + w * 128, tmem + C::S_COL + w * 128 + i * 8, vd + i * (16 * 128 >> 4), C::IDESC_PV, 1u);
+        if (release) mma_commit(empty(v.st));
+        if (last) mma_commit(ofull(w));
+      }
+      __syncwarp();
+      if (more) qk(w, k, kq.j == 0, kq.j + 1 == kq.n, release);
     };
     if (na > 0) {
       Walk kq, kp;
       kq.start(p.segs + cta.a0);
-      kp.start(p.segs + cta.a0);
+      kp = kq;
       Ring<C::NS> rk(0), rv(1);
+      ok = mbar_wait_warp(full(0), 0, abort_addr, p.err);
+      tc_fence_after();
       qk(0, rk, true, kq.n == 1, false);
       qk(1, rk, true, kq.n == 1, true);
 #pragma unroll 1
@@ -312,11 +325,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
         const bool more = i + 1 < na;
         kq.next(na - 1 - i);
         rk.skip(2);
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          pv(w, rv, kp.j == 0, kp.j + 1 == kp.n, w == 1);
-          if (more) qk(w, rk, kq.j == 0, kq.j + 1 == kq.n, w == 1);
-        }
+        step(0, rv, kp, rk, kq, more, false);
+        step(1, rv, kp, rk, kq, more, true);
         rv.skip(2);
         kp.next(na - 1 - i);
       }
@@ -330,6 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
         if (left_q[w] > 0) {
           kq[w].start(p.segs + cta.b0[w]);
           kp[w] = kq[w];
+          ok = ok && mbar_wait_warp(full(rk.st), rk.phase, abort_addr, p.err);
+          tc_fence_after();
           qk(w, rk, true, kq[w].n == 1, true);
           kq[w].next(--left_q[w]);
           rk.skip(w + 1);      // K(0), K(1), then every other half-tile
@@ -340,11 +352,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
         for (int w = 0; w < 2; ++w) {
           const int u = t + w;
           if (u < nb) {
-            pv(w, rv, kp[w].j == 0, kp[w].j + 1 == kp[w].n, true);
+            const bool more = u + 2 < nb;
+            step(w, rv, kp[w], rk, kq[w], more, true);
             kp[w].next(--left_p[w]);
-            rv.skip(u + 2 < nb ? 2 : 1);
-            if (u + 2 < nb) {
-              qk(w, rk, kq[w].j == 0, kq[w].j + 1 == kq[w].n, true);
+            rv.skip(more ? 2 : 1);
+            if (more) {
               kq[w].next(--left_q[w]);
               rk.skip(2);
             }
