@@ -305,6 +305,9 @@ void lay_out(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, Work &w) {
   std::vector<size_t> chain_of;
   for (size_t i = 0; i < w.ctas.size(); ++i) {
     PrefixCta &cta = w.ctas[i];
+    // pairs are bound by their products, lone tiles by their loads: half of the CTAs take them the other way round
+    // (halves, not every other one: those over the same keys stay together)
+    cta.lone_first = 2 * i >= w.ctas.size();
     cta.a0 = static_cast<int32_t>(w.segs.size());
     if (i < a.size())
       for (const Piece &x : a[i]) {
@@ -329,6 +332,9 @@ void lay_out(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, Work &w) {
       }
       cta.b1[m] = static_cast<int32_t>(w.segs.size());
     }
+    cta.small = 1;
+    for (int32_t k = cta.a1; k < static_cast<int32_t>(w.segs.size()); ++k)
+      if (w.segs[k].lanes[0] > kPrefixTile / 2) cta.small = 0;
   }
   // partial results: none where a tile's only result is its own keys' only segment
   std::vector<char> has_shared(w.tiles.size(), 0);
@@ -354,6 +360,7 @@ void lay_out(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, Work &w) {
       const PrefixParts &x = w.parts[static_cast<size_t>(t) * Hkv + w.segs[i].g];
       w.segs[i].part[m] = x.count ? x.first + w.segs[i].part[m] * x.lanes : -1;
     }
+  w.segs.push_back(PrefixSeg{});   // (what lies behind the last is looked at, not used)
   pp->n_ctas = static_cast<int32_t>(w.ctas.size());
 }
 

@@ -30,6 +30,8 @@ struct PrefixSeg {
 struct PrefixCta {
   int32_t a0, a1, tiles_a;
   int32_t b0[2], b1[2], tiles_b;
+  int32_t lone_first;      // the streams' own lists before the pairs
+  int32_t small;           // no tile of the streams' own lists has more than 64 lanes
 };
 
 // Partial results of a tile of queries and a kv head: `count` of them, `lanes` apart, from `first` on
@@ -58,7 +60,7 @@ struct dsa_prefix_plan {
   int64_t part_lanes = 0;
   std::vector<char> host;                // staging copy of the tables
   char *dev = nullptr;
-  dsa::PrefixSeg *segs = nullptr;        // device
+  dsa::PrefixSeg *segs = nullptr;        // device, and one more behind the last
   dsa::PrefixCta *ctas = nullptr;
   dsa::PrefixParts *parts = nullptr;     // [tile][kv head]
   dsa::PrefixRow *rows = nullptr;

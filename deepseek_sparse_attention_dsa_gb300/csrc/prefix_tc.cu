@@ -49,6 +49,7 @@ __device__ __forceinline__ void st_global8(float *p, const float *v) {
 struct PrefixParams {
   CUtensorMap tm_kv;   // cache as [pages * P, 2 * Hkv * D], box {64, BH}
   CUtensorMap tm_q;    // q as [T, Hq, D], box {64, group, rows_a_tile}
+  CUtensorMap tm_q_small;   // the same, box {64, group, 64 / group}
   const PrefixSeg *segs;
   const PrefixCta *ctas;
   const int32_t *pages;
@@ -56,7 +57,7 @@ struct PrefixParams {
   float *part_o;
   float2 *part_ml;
   int *err;
-  int32_t Hq, Hkv, group, P, BH, num_pages, q_bytes;
+  int32_t Hq, Hkv, group, P, BH, num_pages, q_bytes, q_small_bytes;
   float scale_log2;
 };
 
@@ -66,9 +67,11 @@ struct Cfg {
   static constexpr int CHUNK = kPrefixTile * 128;       // bytes: 128 rows of 64 columns
   static constexpr int HALF = CH * CHUNK;               // K or V of a tile
   static constexpr int NS = D == 128 ? 5 : 8;           // half-tiles in the ring
-  static constexpr int OFF_Q = NS * HALF;
-  static constexpr int OFF_BAR = OFF_Q + 2 * HALF;
-  static constexpr int BARS = 2 * NS + 12;
+  static constexpr int SMALL = kPrefixTile / 2 * 128;   // second of two buffers of 64 lanes: into each chunk of a stream's Q
+  // (queries first: a product over the second buffer reads 64 lanes past it, which are dead)
+  static constexpr int OFF_RING = 2 * HALF;
+  static constexpr int OFF_BAR = OFF_RING + NS * HALF;
+  static constexpr int BARS = 2 * NS + 16;
   static constexpr int OFF_MISC = OFF_BAR + BARS * 8;
   static constexpr int BYTES = OFF_MISC + 16 + 1024;    // + alignment slack
   static constexpr uint32_t S_COL = 0, O_COL = 256;     // stream w's S at S_COL + 128 w, O at O_COL + 128 w
@@ -92,16 +95,20 @@ struct Ring {
   }
 };
 
-// A walk over the tiles of a list of segments.
+// A walk over the tiles of a list of segments.  The next one's length is loaded a segment ahead (one more segment
+// lies behind the last of all lists).
 struct Walk {
   const PrefixSeg *seg;
-  int j, n;   // tile of the segment, its tiles
-  __device__ __forceinline__ void start(const PrefixSeg *s) { seg = s, j = 0, n = s->ntiles; }
-  // (past the list's end nothing is read: `left` tiles of the list are still to come)
-  __device__ __forceinline__ void next(int left) {
-    if (++j == n && left > 0) start(seg + 1);
+  int j, n, n_next;   // tile of the segment, its tiles, the next one's
+  __device__ __forceinline__ void start(const PrefixSeg *s) { seg = s, j = 0, n = s->ntiles, n_next = s[1].ntiles; }
+  __device__ __forceinline__ void next() {
+    if (++j == n) seg += 1, j = 0, n = n_next, n_next = seg[1].ntiles;
   }
 };
+__device__ __forceinline__ void prefetch_seg(const PrefixSeg *s) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(s));
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(reinterpret_cast<const char *>(s) + sizeof(PrefixSeg) - 4));
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_constant__ PrefixParams p) {
@@ -112,11 +119,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
   auto full = [&](int r) { return bar0 + 8u * (r % C::NS); };
   auto empty = [&](int r) { return bar0 + 8u * (C::NS + r % C::NS); };
   auto phase = [&](int r) { return static_cast<uint32_t>(r / C::NS) & 1u; };
-  auto qfull = [&](int w) { return bar0 + 8u * (2 * C::NS + w); };
-  auto qempty = [&](int w) { return bar0 + 8u * (2 * C::NS + 2 + w); };
-  auto sfull = [&](int w) { return bar0 + 8u * (2 * C::NS + 4 + w); };
-  auto pfull = [&](int w, int h) { return bar0 + 8u * (2 * C::NS + 6 + 2 * w + h); };   // h: the first 64 keys, the others
-  auto ofull = [&](int w) { return bar0 + 8u * (2 * C::NS + 10 + w); };
+  auto qfull = [&](int w, int b) { return bar0 + 8u * (2 * C::NS + 2 * w + b); };
+  auto qempty = [&](int w, int b) { return bar0 + 8u * (2 * C::NS + 4 + 2 * w + b); };
+  auto sfull = [&](int w) { return bar0 + 8u * (2 * C::NS + 8 + w); };
+  auto pfull = [&](int w, int h) { return bar0 + 8u * (2 * C::NS + 10 + 2 * w + h); };   // h: the first 64 keys, the others
+  auto ofull = [&](int w) { return bar0 + 8u * (2 * C::NS + 14 + w); };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
   const uint32_t abort_addr = sbase + C::OFF_MISC + 4;
@@ -128,8 +135,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
       mbar_init(empty(r), 1);
     }
     for (int w = 0; w < 2; ++w) {
-      mbar_init(qfull(w), 1);
-      mbar_init(qempty(w), 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(qfull(w, b), 1);
+        mbar_init(qempty(w, b), 1);
+      }
       mbar_init(sfull(w), 1);
       mbar_init(pfull(w, 0), 4);   // one arrival a warp
       mbar_init(pfull(w, 1), 4);
@@ -139,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
     fence_mbar_init();
     tma_prefetch_desc(&p.tm_kv);
     tma_prefetch_desc(&p.tm_q);
+    tma_prefetch_desc(&p.tm_q_small);
   }
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -151,6 +161,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
   grid_dependency();
   const PrefixCta cta = p.ctas[blockIdx.x];
   const int na = cta.tiles_a, nb = cta.tiles_b;
+  const bool small = cta.small != 0;
+  // the two parts' places in the ring
+  const int base_a = cta.lone_first ? 2 * nb : 0, base_b = cta.lone_first ? 0 : 2 * na;
 
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------ loads
@@ -169,7 +182,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
       }
       return page * p.P + (q0 - static_cast<int>(pi) * p.P);
     };
-    int r = 0, q_loads[2] = {0, 0};
+    int r = 0;
+    uint32_t q_loaded = 0, q_odd = 0;      // bit 2 w + b: stream w's buffer b has been loaded; an odd number of times
     bool ok = true;
     auto load = [&](int x0, int row) {   // the next half-tile of the ring, columns x0 ..
       ok = ok && mbar_wait_warp(empty(r), phase(r) ^ 1u, abort_addr, p.err);
@@ -180,66 +194,80 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
         else mbar_arrive(full(r));
       }
       __syncwarp();
-      if (row >= 0) tma_load_2d(sbase + (r % C::NS) * C::HALF + chunk * C::CHUNK + box * p.BH * 128, &p.tm_kv, x0 + chunk * 64, row, full(r));
+      if (row >= 0) tma_load_2d(sbase + C::OFF_RING + (r % C::NS) * C::HALF + chunk * C::CHUNK + box * p.BH * 128, &p.tm_kv, x0 + chunk * 64, row, full(r));
       ++r;
     };
-    auto load_q = [&](int w, const PrefixSeg *s, int tile) {
-      if (q_loads[w] > 0) ok = ok && mbar_wait_warp(qempty(w), (q_loads[w] - 1) & 1, abort_addr, p.err);
+    // Stream w's queries: of a pair or a large tile into the whole of its buffer, of tiles of up to 64 lanes (`small`)
+    // into one half and the other by turns, so that the next ones are there when the last ones are done with.
+    auto load_q = [&](int w, const PrefixSeg *s, int tile, bool small, int b) {
+      const uint32_t bit = 1u << (2 * w + b), busy = q_loaded & (small ? bit : 3u << (2 * w));
+      for (int o = 0; o < 2; ++o)
+        if (busy >> (2 * w + o) & 1) ok = ok && mbar_wait_warp(qempty(w, o), (q_odd >> (2 * w + o) & 1) ^ 1, abort_addr, p.err);
       if (!ok) return;
       if (lane == 0) {
-        mbar_arrive_expect_tx(qfull(w), p.q_bytes);
+        mbar_arrive_expect_tx(qfull(w, b), small ? p.q_small_bytes : p.q_bytes);
         for (int c = 0; c < C::CH; ++c)
-          tma_load_3d(sbase + C::OFF_Q + w * C::HALF + c * C::CHUNK, &p.tm_q, c * 64, s->g * p.group, s->row[tile], qfull(w));
+          tma_load_3d(sbase + w * C::HALF + c * C::CHUNK + b * C::SMALL, small ? &p.tm_q_small : &p.tm_q, c * 64, s->g * p.group,
+                      s->row[tile], qfull(w, b));
       }
       __syncwarp();
-      ++q_loads[w];
+      q_loaded |= bit, q_odd ^= bit;
     };
     // (a tile's pages are looked up one tile ahead)
-    if (na > 0) {
-      Walk k;
-      k.start(p.segs + cta.a0);
-      int row = lookup(k);
-      for (int i = 0; i < na && ok; ++i) {
-        const PrefixSeg *s = k.seg;
-        const bool first = k.j == 0;
-        k.next(na - 1 - i);
-        const int row_next = i + 1 < na ? lookup(k) : -1;
-        if (first) {
-          load_q(0, s, 0);
-          load_q(1, s, 1);
-        }
-        load(s->g * D, row);
-        load((p.Hkv + s->g) * D, row);
-        row = row_next;
-      }
-    }
-    if (nb > 0 && ok) {
-      Walk k[2];
-      int left[2] = {(nb + 1) / 2, nb / 2}, rows[2] = {-1, -1}, rows_before = -1, g_before = 0;
-      for (int w = 0; w < 2; ++w)
-        if (left[w] > 0) {
-          k[w].start(p.segs + cta.b0[w]);
-          rows[w] = lookup(k[w]);
-        }
 #pragma unroll 1
-      for (int t = 0; t <= nb && ok; ++t) {
-        int row = -1, g = 0;
-        if (t < nb) {
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (w != (t & 1)) continue;
-            const PrefixSeg *s = k[w].seg;
-            const bool first = k[w].j == 0;
-            row = rows[w], g = s->g;
-            --left[w];
-            k[w].next(left[w]);
-            rows[w] = left[w] > 0 ? lookup(k[w]) : -1;
-            if (first) load_q(w, s, 0);
+    for (int part = 0; part < 2 && ok; ++part) {
+      const bool lone = (part == 0) == (cta.lone_first != 0);
+      if (!lone && na > 0) {
+        Walk k;
+        k.start(p.segs + cta.a0);
+        int row = lookup(k);
+        for (int i = 0; i < na && ok; ++i) {
+          const PrefixSeg *s = k.seg;
+          const bool first = k.j == 0;
+          k.next();
+          const int row_next = i + 1 < na ? lookup(k) : -1;
+          load(s->g * D, row);
+          if (first) {
+            load_q(0, s, 0, false, 0);
+            load_q(1, s, 1, false, 0);
           }
-          load(g * D, row);
+          load((p.Hkv + s->g) * D, row);
+          row = row_next;
         }
-        if (t > 0) load((p.Hkv + g_before) * D, rows_before);
-        rows_before = row, g_before = g;
+      }
+      if (lone && nb > 0) {
+        Walk k[2];
+        int left[2] = {(nb + 1) / 2, nb / 2}, rows[2] = {-1, -1}, rows_before = -1, g_before = 0;
+        uint32_t turn = 0;      // bit w: the buffer of stream w's next queries
+        for (int w = 0; w < 2; ++w)
+          if (left[w] > 0) {
+            k[w].start(p.segs + cta.b0[w]);
+            rows[w] = lookup(k[w]);
+          }
+#pragma unroll 1
+        for (int t = 0; t <= nb && ok; ++t) {
+          int row = -1, g = 0;
+          if (t < nb) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              if (w != (t & 1)) continue;
+              const PrefixSeg *s = k[w].seg;
+              const bool first = k[w].j == 0;
+              row = rows[w], g = s->g;
+              --left[w];
+              k[w].next();
+              rows[w] = left[w] > 0 ? lookup(k[w]) : -1;
+              load(g * D, row);
+              if (first) {
+                prefetch_seg(s + 1);
+                load_q(w, s, 0, small, turn >> w & 1);
+                if (small) turn ^= 1u << w;
+              }
+            }
+          }
+          if (t > 0) load((p.Hkv + g_before) * D, rows_before);
+          rows_before = row, g_before = g;
+        }
       }
     }
     // nothing of ours may still be landing when the CTA leaves (an abort apart, all of it has been used)
@@ -247,7 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
       volatile int no_abort = 0;
       for (int i = max(0, r - C::NS); i < r; ++i) mbar_wait(full(i), phase(i), &no_abort, p.err);
       for (int w = 0; w < 2; ++w)
-        if (q_loads[w] > 0) mbar_wait(qfull(w), (q_loads[w] - 1) & 1, &no_abort, p.err);
+        for (int b = 0; b < 2; ++b)
+          if (q_loaded >> (2 * w + b) & 1) mbar_wait(qfull(w, b), (q_odd >> (2 * w + b) & 1) ^ 1, &no_abort, p.err);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
@@ -257,18 +286,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
     // stay in uniform registers.  (Issued by a lane that a branch picked, each of the 16 instructions of a step took
     // some 80 cycles.)  A wait costs some 200 cycles, met or not: the three that a step begins with are tried
     // together, and the one between its products has the first half of the first behind it.
-    const uint64_t desc0 = smem_desc(sbase, 16, 1024, kSwizzle128), desc_v0 = smem_desc(sbase, C::CHUNK, 1024, kSwizzle128);
-    uint32_t q_phase = 0, p_phase = 0;      // bit w: stream w's
+    const uint64_t desc_q0 = smem_desc(sbase, 16, 1024, kSwizzle128), desc_k0 = smem_desc(sbase + C::OFF_RING, 16, 1024, kSwizzle128),
+                   desc_v0 = smem_desc(sbase + C::OFF_RING, C::CHUNK, 1024, kSwizzle128);
+    uint32_t q_phase = 0, p_phase = 0;      // bit 2 w + b: stream w's buffer b; bit w: stream w's
+    uint32_t turn = 0;                      // bit w: the buffer of stream w's queries
     bool ok = true;
-    auto qk = [&](int w, const Ring<C::NS> &r, bool first, bool last, bool release) {
+    auto qk = [&](int w, const Ring<C::NS> &r, bool first, bool last, bool release, bool halves) {
+      const uint32_t b = (turn >> w) & 1;
       if (first) {
-        ok = ok && mbar_wait_warp(qfull(w), (q_phase >> w) & 1, abort_addr, p.err);
-        q_phase ^= 1u << w;
+        ok = ok && mbar_wait_warp(qfull(w, b), (q_phase >> (2 * w + b)) & 1, abort_addr, p.err);
+        q_phase ^= 1u << (2 * w + b);
         tc_fence_after();
       }
+      if (last && halves) turn ^= 1u << w;
       if (!ok) return;
       if (elect_one()) {
-        const uint64_t q = desc0 + ((C::OFF_Q + w * C::HALF) >> 4), k = desc0 + r.st * (C::HALF >> 4);
+        const uint64_t q = desc_q0 + (w * C::HALF >> 4) + b * (C::SMALL >> 4), k = desc_k0 + r.st * (C::HALF >> 4);
 #pragma unroll
         for (int c = 0; c < C::CH; ++c)
 #pragma unroll
@@ -277,12 +310,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
                        (c | i) ? 1u : 0u);
         mma_commit(sfull(w));
         if (release) mma_commit(empty(r.st));
-        if (last) mma_commit(qempty(w));
+        if (last) mma_commit(qempty(w, b));
       }
       __syncwarp();
     };
     // Stream w's step: O += P V, and behind it (they run in order, and S's columns hold P) the next S of the stream.
-    auto step = [&](int w, const Ring<C::NS> &v, const Walk &kp, const Ring<C::NS> &k, const Walk &kq, bool more, bool release) {
+    auto step = [&](int w, const Ring<C::NS> &v, const Walk &kp, const Ring<C::NS> &k, const Walk &kq, bool more, bool release,
+                    bool halves) {
       const uint32_t ph = (p_phase >> w) & 1;
       p_phase ^= 1u << w;
       if (more) ok = ok && mbar_wait_warp_three(full(v.st), v.phase, full(k.st), k.phase, pfull(w, 0), ph, abort_addr, p.err);
@@ -309,56 +343,60 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
         if (last) mma_commit(ofull(w));
       }
       __syncwarp();
-      if (more) qk(w, k, kq.j == 0, kq.j + 1 == kq.n, release);
+      if (more) qk(w, k, kq.j == 0, kq.j + 1 == kq.n, release, halves);
     };
-    if (na > 0) {
-      Walk kq, kp;
-      kq.start(p.segs + cta.a0);
-      kp = kq;
-      Ring<C::NS> rk(0), rv(1);
-      ok = mbar_wait_warp(full(0), 0, abort_addr, p.err);
-      tc_fence_after();
-      qk(0, rk, true, kq.n == 1, false);
-      qk(1, rk, true, kq.n == 1, true);
 #pragma unroll 1
-      for (int i = 0; i < na && ok; ++i) {
-        const bool more = i + 1 < na;
-        kq.next(na - 1 - i);
-        rk.skip(2);
-        step(0, rv, kp, rk, kq, more, false);
-        step(1, rv, kp, rk, kq, more, true);
-        rv.skip(2);
-        kp.next(na - 1 - i);
-      }
-    }
-    if (nb > 0 && ok) {
-      Walk kq[2], kp[2];
-      int left_q[2] = {(nb + 1) / 2, nb / 2}, left_p[2] = {(nb + 1) / 2, nb / 2};
-      Ring<C::NS> rk(2 * na), rv(2 * na + lone_v(0, nb));
-#pragma unroll
-      for (int w = 0; w < 2; ++w)
-        if (left_q[w] > 0) {
-          kq[w].start(p.segs + cta.b0[w]);
-          kp[w] = kq[w];
-          ok = ok && mbar_wait_warp(full(rk.st), rk.phase, abort_addr, p.err);
-          tc_fence_after();
-          qk(w, rk, true, kq[w].n == 1, true);
-          kq[w].next(--left_q[w]);
-          rk.skip(w + 1);      // K(0), K(1), then every other half-tile
+    for (int part = 0; part < 2 && ok; ++part) {
+      const bool lone = (part == 0) == (cta.lone_first != 0);
+      turn = 0;
+      if (!lone && na > 0) {
+        Walk kq, kp;
+        kq.start(p.segs + cta.a0);
+        kp = kq;
+        Ring<C::NS> rk(base_a), rv(base_a + 1);
+        ok = mbar_wait_warp(full(rk.st), rk.phase, abort_addr, p.err);
+        tc_fence_after();
+        qk(0, rk, true, kq.n == 1, false, false);
+        qk(1, rk, true, kq.n == 1, true, false);
+#pragma unroll 1
+        for (int i = 0; i < na && ok; ++i) {
+          const bool more = i + 1 < na;
+          kq.next();
+          rk.skip(2);
+          step(0, rv, kp, rk, kq, more, false, false);
+          step(1, rv, kp, rk, kq, more, true, false);
+          rv.skip(2);
+          kp.next();
         }
-#pragma unroll 1
-      for (int t = 0; t < nb && ok; t += 2) {
+      }
+      if (lone && nb > 0) {
+        Walk kq[2], kp[2];
+        Ring<C::NS> rk(base_b), rv(base_b + lone_v(0, nb));
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const int u = t + w;
-          if (u < nb) {
-            const bool more = u + 2 < nb;
-            step(w, rv, kp[w], rk, kq[w], more, true);
-            kp[w].next(--left_p[w]);
-            rv.skip(more ? 2 : 1);
-            if (more) {
-              kq[w].next(--left_q[w]);
-              rk.skip(2);
+        for (int w = 0; w < 2; ++w)
+          if (w < nb) {
+            kq[w].start(p.segs + cta.b0[w]);
+            kp[w] = kq[w];
+            ok = ok && mbar_wait_warp(full(rk.st), rk.phase, abort_addr, p.err);
+            tc_fence_after();
+            qk(w, rk, true, kq[w].n == 1, true, small);
+            kq[w].next();
+            rk.skip(w + 1);      // K(0), K(1), then every other half-tile
+          }
+#pragma unroll 1
+        for (int t = 0; t < nb && ok; t += 2) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const int u = t + w;
+            if (u < nb) {
+              const bool more = u + 2 < nb;
+              step(w, rv, kp[w], rk, kq[w], more, true, small);
+              kp[w].next();
+              rv.skip(more ? 2 : 1);
+              if (more) {
+                kq[w].next();
+                rk.skip(2);
+              }
             }
           }
         }
@@ -373,52 +411,90 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
     const int own_row = i / p.group, own_head = i - own_row * p.group;
     int s_waits = 0, o_waits = 0;
     bool ok = true;
-    // The pairs' segments, then this stream's own (one loop: the code is large enough to miss the instruction cache).
-    const int own_pairs = cta.a1 - cta.a0, segs = own_pairs + cta.b1[w] - cta.b0[w];
-    int done = 0;      // key tiles of the phase before this segment
+    // The pairs' segments and this stream's own, in the CTA's order (in one loop: the code is large enough to miss the
+    // instruction cache).
+    const int n_a = cta.a1 - cta.a0, n_b = cta.b1[w] - cta.b0[w], n_first = cta.lone_first ? n_b : n_a;
+    auto is_lone = [&](int k) { return (k < n_first) == (cta.lone_first != 0); };
+    auto seg_at = [&](int k) { return p.segs + (is_lone(k) ? cta.b0[w] : cta.a0) + k - (k < n_first ? 0 : n_first); };
+    int done = 0;      // key tiles of the part before this segment
 #pragma unroll 1
-    for (int n_seg = 0; n_seg < segs; ++n_seg) {
-      const bool lone = n_seg >= own_pairs;
-      if (n_seg == own_pairs) done = 0;
-      const PrefixSeg &s = p.segs[lone ? cta.b0[w] + n_seg - own_pairs : cta.a0 + n_seg];
+    for (int n_seg = 0; n_seg < n_a + n_b; ++n_seg) {
+      const bool lone = is_lone(n_seg);
+      if (n_seg == n_first) done = 0;
+      const PrefixSeg &s = *seg_at(n_seg);
       const int tile = lone ? 0 : w;
       const bool zero = lone || w == 0;      // whether this stream clears values that no lane sees
       const int limit = s.causal ? s.limit[tile] + own_row : s.hi;
       const int least = s.causal ? s.limit[tile] : s.hi;   // every lane sees the slots below
-      const int n = s.ntiles, lo = s.lo, hi = s.hi;
+      const int n = s.ntiles, lo = s.lo, hi = s.hi, slot0 = s.slot0, part = s.part[tile], lanes = s.lanes[tile];
+      const int64_t out_row = (static_cast<int64_t>(s.row[tile]) + own_row) * p.Hq + s.g * p.group + own_head;
+      if (n_seg + 1 < n_a + n_b) prefetch_seg(seg_at(n_seg + 1));
+      // a warp without live lanes leaves P as it is (what comes of it stays in dead lanes of O) and only keeps step
+      const bool dead = (warp & 3) * 32 >= lanes;
       float m = kNoMax, l = 0.f;
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
-        const int t0 = s.slot0 + j * kPrefixTile;
+        const int t0 = slot0 + j * kPrefixTile;
         ok = mbar_wait_warp(sfull(w), s_waits & 1, abort_addr, p.err);
         ++s_waits;
         if (!ok) break;
         tc_fence_after();
+        // values of slots that no lane sees are cleared once they are there (a zero weight must not meet what
+        // they hold, or what an unloaded box left)
+        if (zero && (t0 < lo || t0 + kPrefixTile > hi)) {
+          const int r = lone ? base_b + lone_v(2 * (done + j) + w, nb) : base_a + 2 * (done + j) + 1;
+          ok = mbar_wait_warp(full(r), phase(r), abort_addr, p.err);
+          if (!ok) break;
+          const int before = max(lo - t0, 0), from = min(hi - t0, kPrefixTile);   // rows [0, before) and [from, 128)
+          const uint32_t v = sbase + C::OFF_RING + (r % C::NS) * C::HALF;
+#pragma unroll 1
+          for (int k = i; k < (before + kPrefixTile - from) * 8; k += 128) {
+            const uint32_t at = v + (k + (k >> 3 >= before ? (from - before) * 8 : 0)) * 16;
+#pragma unroll
+            for (int c = 0; c < C::CH; ++c) st_shared_v4(at + c * C::CHUNK, make_uint4(0u, 0u, 0u, 0u));
+          }
+          fence_proxy_async_smem();
+        }
+        if (dead) {
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(pfull(w, 0));
+            mbar_arrive(pfull(w, 1));
+          }
+          continue;
+        }
         if (t0 < lo || t0 + kPrefixTile > least) {
           // slots that the lane does not see, in tensor memory: kept out of the unrolled code below
 #pragma unroll 1
           for (int c0 = 0; c0 < kPrefixTile; c0 += 16) {
+            const int s0 = t0 + c0;
+            if (s0 >= lo && s0 + 16 <= least) continue;
             float v[16];
-            tmem_ld16(t_s + c0, v);
-            tmem_ld_wait();
+            if (s0 + 16 > lo && s0 < hi) {
+              tmem_ld16(t_s + c0, v);
+              tmem_ld_wait();
+            }
 #pragma unroll
             for (int c = 0; c < 16; ++c)
-              if (t0 + c0 + c < lo || t0 + c0 + c >= limit) v[c] = -INFINITY;
+              if (s0 + c < lo || s0 + c >= min(limit, hi)) v[c] = -INFINITY;
             tmem_st16(t_s + c0, v);
           }
           tmem_st_wait();
         }
-        float x[kPrefixTile];
+        // Half of S at a time in registers (all of it, 128, leaves too few for the rest and spills): the maximum of the
+        // upper half, then of the lower one, whose weights are made from the same registers while the upper half
+        // comes again.
+        float x[64], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, *reinterpret_cast<float(*)[32]>(x + c * 32));
-        tmem_ld_wait();
-        float mx[4] = {x[0], x[1], x[2], x[3]};
+        for (int h = 1; h >= 0; --h) {
+          tmem_ld32(t_s + h * 64, *reinterpret_cast<float(*)[32]>(x));
+          tmem_ld32(t_s + h * 64 + 32, *reinterpret_cast<float(*)[32]>(x + 32));
+          tmem_ld_wait();
 #pragma unroll
-        for (int c = 4; c + 8 <= kPrefixTile; c += 8)
+          for (int c = 0; c < 64; c += 8)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], x[c + k]), x[c + 4 + k]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[kPrefixTile - 4 + k]);
+            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], x[c + k]), x[c + 4 + k]);
+        }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
         const bool move = top > m + kRescale;
         if (__any_sync(0xffffffffu, move)) {
@@ -438,43 +514,38 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
             }
           }
         }
-        // values of slots that no lane sees are cleared once they are there (a zero weight must not meet what
-        // they hold, or what an unloaded box left)
-        if (zero && (t0 < lo || t0 + kPrefixTile > hi)) {
-          const int r = lone ? 2 * na + lone_v(2 * (done + j) + w, nb) : 2 * (done + j) + 1;
-          ok = mbar_wait_warp(full(r), phase(r), abort_addr, p.err);
-          if (!ok) break;
-          if (t0 + i < lo || t0 + i >= hi) {
-#pragma unroll
-            for (int c = 0; c < C::CH; ++c)
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                st_shared_v4(sbase + (r % C::NS) * C::HALF + c * C::CHUNK + i * 128 + k * 16, make_uint4(0u, 0u, 0u, 0u));
-          }
-          fence_proxy_async_smem();
-        }
         // the weights, 64 keys at a time: the product starts on the first of them
         const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2), minus2 = f2_pack(-m, -m);
         uint64_t sum[2] = {f2_pack(l, 0.f), f2_pack(0.f, 0.f)};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        auto weights = [&](int q, const float *v) {      // of 32 keys; they lie over columns of S that have been read
           uint32_t packed[16];
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
             float a, b;
-            f2_unpack(f2_fma(f2_pack(x[q * 32 + 2 * c], x[q * 32 + 2 * c + 1]), scale2, minus2), a, b);
+            f2_unpack(f2_fma(f2_pack(v[2 * c], v[2 * c + 1]), scale2, minus2), a, b);
             a = exp2_approx(a), b = exp2_approx(b);
             sum[c & 1] = f2_add(sum[c & 1], f2_pack(a, b));
             packed[c] = pack_bf16(a, b);
           }
           tmem_st16(t_s + q * 16, packed);
-          if (q & 1) {
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(pfull(w, q >> 1));
-          }
-        }
+        };
+        auto hand_over = [&](int h) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pfull(w, h));
+        };
+        float y[32];
+        tmem_ld32(t_s + 64, y);
+        weights(0, x);
+        weights(1, x + 32);
+        hand_over(0);
+        tmem_ld_wait();
+        tmem_ld32(t_s + 96, *reinterpret_cast<float(*)[32]>(x));
+        weights(2, y);
+        tmem_ld_wait();
+        weights(3, x);
+        hand_over(1);
         float a, b;
         f2_unpack(f2_add(sum[0], sum[1]), a, b);
         l = a + b;
@@ -484,29 +555,31 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
       if (!ok) break;
       done += n;
       tc_fence_after();
-      const int part = s.part[tile];
-      const bool live = i < s.lanes[tile];
-      const float scale = part < 0 ? 1.f / l : 1.f;
-      float *to = p.part_o + (static_cast<int64_t>(part) + i) * D;
-      __nv_bfloat16 *out = p.out + ((static_cast<int64_t>(s.row[tile]) + own_row) * p.Hq + s.g * p.group + own_head) * D;
+      if (!dead) {
+        const bool live = i < lanes;
+        const float scale = part < 0 ? 1.f / l : 1.f;
+        float *to = p.part_o + (static_cast<int64_t>(part) + i) * D;
+        __nv_bfloat16 *out = p.out + out_row * D;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        float o[32];
-        tmem_ld32(t_o + c, o);
-        tmem_ld_wait();
-        if (live && part < 0) {
+        for (int c = 0; c < D; c += 64) {
+          float o[64];
+          tmem_ld32(t_o + c, *reinterpret_cast<float(*)[32]>(o));
+          tmem_ld32(t_o + c + 32, *reinterpret_cast<float(*)[32]>(o + 32));
+          tmem_ld_wait();
+          if (live && part < 0) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8)
-            *reinterpret_cast<uint4 *>(out + c + k) =
-                make_uint4(pack_bf16(o[k] * scale, o[k + 1] * scale), pack_bf16(o[k + 2] * scale, o[k + 3] * scale),
-                           pack_bf16(o[k + 4] * scale, o[k + 5] * scale), pack_bf16(o[k + 6] * scale, o[k + 7] * scale));
-        } else if (live) {
+            for (int k = 0; k < 64; k += 8)
+              *reinterpret_cast<uint4 *>(out + c + k) =
+                  make_uint4(pack_bf16(o[k] * scale, o[k + 1] * scale), pack_bf16(o[k + 2] * scale, o[k + 3] * scale),
+                             pack_bf16(o[k + 4] * scale, o[k + 5] * scale), pack_bf16(o[k + 6] * scale, o[k + 7] * scale));
+          } else if (live) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) st_global8(to + c + k, o + k);
+            for (int k = 0; k < 64; k += 8) st_global8(to + c + k, o + k);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (live && part >= 0) p.part_ml[part + i] = make_float2(m, l);
       }
-      if (live && part >= 0) p.part_ml[part + i] = make_float2(m, l);
       tc_fence_before();   // (O is read: the stream's next products into it follow its next arrival)
     }
   }
@@ -583,15 +656,20 @@ cudaError_t run(const dsa_ctx *ctx, const dsa_prefix_plan_t *pp, const void *q, 
   const uint64_t dims[3] = {D, static_cast<uint64_t>(ms.q_heads), static_cast<uint64_t>(plan.T)};
   const uint64_t strides[2] = {D * 2, static_cast<uint64_t>(ms.q_heads) * D * 2};
   const uint32_t box[3] = {64, static_cast<uint32_t>(p.group), static_cast<uint32_t>(pp->rows_a_tile)};
+  const uint32_t small_rows = std::max(1, kPrefixTile / 2 / p.group);   // (a group above 64: no tile is small)
+  const uint32_t small_box[3] = {64, static_cast<uint32_t>(p.group), small_rows};
   if (!encode_tiled_2d(&p.tm_kv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, const_cast<void *>(kv), cols,
                        static_cast<uint64_t>(plan.cache_pages) * p.P, cols * 2, 64, p.BH, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_tiled_3d(&p.tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, const_cast<void *>(q), dims, strides, box,
+                       CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tiled_3d(&p.tm_q_small, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, const_cast<void *>(q), dims, strides, small_box,
                        CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   p.segs = pp->segs, p.ctas = pp->ctas, p.pages = plan.pages;
   p.out = static_cast<__nv_bfloat16 *>(out);
   p.part_o = pp->part_o, p.part_ml = pp->part_ml, p.err = ctx->err;
   p.q_bytes = pp->rows_a_tile * p.group * D * 2;
+  p.q_small_bytes = static_cast<int32_t>(small_rows) * p.group * D * 2;
   p.scale_log2 = sm_scale * kLog2e;
   static std::atomic<uint64_t> smem_limit_set{0};
   cudaError_t e = ensure_smem_limit(prefix_tc_kernel<D>, Cfg<D>::BYTES, ctx->device, smem_limit_set);
