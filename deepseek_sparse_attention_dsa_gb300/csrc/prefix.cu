@@ -305,9 +305,6 @@ void lay_out(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, Work &w) {
   std::vector<size_t> chain_of;
   for (size_t i = 0; i < w.ctas.size(); ++i) {
     PrefixCta &cta = w.ctas[i];
-    // pairs are bound by their products, lone tiles by their loads: half of the CTAs take them the other way round
-    // (halves, not every other one: those over the same keys stay together)
-    cta.lone_first = 2 * i >= w.ctas.size();
     cta.a0 = static_cast<int32_t>(w.segs.size());
     if (i < a.size())
       for (const Piece &x : a[i]) {

@@ -30,7 +30,6 @@ struct PrefixSeg {
 struct PrefixCta {
   int32_t a0, a1, tiles_a;
   int32_t b0[2], b1[2], tiles_b;
-  int32_t lone_first;      // the streams' own lists before the pairs
   int32_t small;           // no tile of the streams' own lists has more than 64 lanes
 };
 

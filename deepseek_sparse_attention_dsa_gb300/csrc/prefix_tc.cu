@@ -162,25 +162,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
   const PrefixCta cta = p.ctas[blockIdx.x];
   const int na = cta.tiles_a, nb = cta.tiles_b;
   const bool small = cta.small != 0;
-  // the two parts' places in the ring
-  const int base_a = cta.lone_first ? 2 * nb : 0, base_b = cta.lone_first ? 0 : 2 * na;
 
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------ loads
     // A lane's box: box lane / CH of the tile, chunk lane % CH; its cache row, or -1
     const int box = lane / C::CH, chunk = lane % C::CH, boxes = kPrefixTile / p.BH;
+    // (The page is looked at when the tile is loaded, a step later: the table's latency would hold up every load.  It is
+    // one of the plan's, which were checked against the cache's size when it was made.)
+    struct Box {
+      int page, slot;
+      __device__ __forceinline__ int row(int P) const { return page < 0 ? -1 : page * P + slot; }
+    };
     auto lookup = [&](const Walk &k) {
-      if (box >= boxes) return -1;
       const PrefixSeg &s = *k.seg;
       const int q0 = s.slot0 + k.j * kPrefixTile + box * p.BH;
-      if (q0 + p.BH <= s.lo || q0 >= s.hi) return -1;
-      const uint32_t pi = static_cast<uint32_t>(q0) / static_cast<uint32_t>(p.P);
-      const int page = pi < static_cast<uint32_t>(s.npages) ? p.pages[s.page_off + pi] : -1;
-      if (page < 0 || page >= p.num_pages) {
-        atomicOr(p.err, kErrBounds);
-        return -1;
+      Box x{-1, 0};
+      if (box < boxes && q0 + p.BH > s.lo && q0 < s.hi) {
+        const uint32_t pi = static_cast<uint32_t>(q0) / static_cast<uint32_t>(p.P);
+        x.slot = q0 - static_cast<int>(pi) * p.P;
+        x.page = p.pages[s.page_off + pi];
       }
-      return page * p.P + (q0 - static_cast<int>(pi) * p.P);
+      return x;
     };
     int r = 0;
     uint32_t q_loaded = 0, q_odd = 0;      // bit 2 w + b: stream w's buffer b has been loaded; an odd number of times
@@ -214,60 +216,57 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
       q_loaded |= bit, q_odd ^= bit;
     };
     // (a tile's pages are looked up one tile ahead)
-#pragma unroll 1
-    for (int part = 0; part < 2 && ok; ++part) {
-      const bool lone = (part == 0) == (cta.lone_first != 0);
-      if (!lone && na > 0) {
-        Walk k;
-        k.start(p.segs + cta.a0);
-        int row = lookup(k);
-        for (int i = 0; i < na && ok; ++i) {
-          const PrefixSeg *s = k.seg;
-          const bool first = k.j == 0;
-          k.next();
-          const int row_next = i + 1 < na ? lookup(k) : -1;
-          load(s->g * D, row);
-          if (first) {
-            load_q(0, s, 0, false, 0);
-            load_q(1, s, 1, false, 0);
-          }
-          load((p.Hkv + s->g) * D, row);
-          row = row_next;
+    if (na > 0) {
+      Walk k;
+      k.start(p.segs + cta.a0);
+      Box ahead = lookup(k);
+      for (int i = 0; i < na && ok; ++i) {
+        const int row = ahead.row(p.P);
+        const PrefixSeg *s = k.seg;
+        const bool first = k.j == 0;
+        k.next();
+        if (i + 1 < na) ahead = lookup(k);
+        load(s->g * D, row);
+        if (first) {
+          load_q(0, s, 0, false, 0);
+          load_q(1, s, 1, false, 0);
         }
+        load((p.Hkv + s->g) * D, row);
       }
-      if (lone && nb > 0) {
-        Walk k[2];
-        int left[2] = {(nb + 1) / 2, nb / 2}, rows[2] = {-1, -1}, rows_before = -1, g_before = 0;
-        uint32_t turn = 0;      // bit w: the buffer of stream w's next queries
-        for (int w = 0; w < 2; ++w)
-          if (left[w] > 0) {
-            k[w].start(p.segs + cta.b0[w]);
-            rows[w] = lookup(k[w]);
-          }
+    }
+    if (nb > 0 && ok) {
+      Walk k[2];
+      int left[2] = {(nb + 1) / 2, nb / 2}, row_before = -1, g_before = 0;
+      Box ahead[2];
+      uint32_t turn = 0;      // bit w: the buffer of stream w's next queries
+      for (int w = 0; w < 2; ++w)
+        if (left[w] > 0) {
+          k[w].start(p.segs + cta.b0[w]);
+          ahead[w] = lookup(k[w]);
+        }
 #pragma unroll 1
-        for (int t = 0; t <= nb && ok; ++t) {
-          int row = -1, g = 0;
-          if (t < nb) {
+      for (int t = 0; t <= nb && ok; ++t) {
+        int row = -1, g = 0;
+        if (t < nb) {
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              if (w != (t & 1)) continue;
-              const PrefixSeg *s = k[w].seg;
-              const bool first = k[w].j == 0;
-              row = rows[w], g = s->g;
-              --left[w];
-              k[w].next();
-              rows[w] = left[w] > 0 ? lookup(k[w]) : -1;
-              load(g * D, row);
-              if (first) {
-                prefetch_seg(s + 1);
-                load_q(w, s, 0, small, turn >> w & 1);
-                if (small) turn ^= 1u << w;
-              }
+          for (int w = 0; w < 2; ++w) {
+            if (w != (t & 1)) continue;
+            const PrefixSeg *s = k[w].seg;
+            const bool first = k[w].j == 0;
+            row = ahead[w].row(p.P), g = s->g;
+            --left[w];
+            k[w].next();
+            if (left[w] > 0) ahead[w] = lookup(k[w]);
+            load(g * D, row);
+            if (first) {
+              prefetch_seg(s + 1);
+              load_q(w, s, 0, small, turn >> w & 1);
+              if (small) turn ^= 1u << w;
             }
           }
-          if (t > 0) load((p.Hkv + g_before) * D, rows_before);
-          rows_before = row, g_before = g;
         }
+        if (t > 0) load((p.Hkv + g_before) * D, row_before);
+        row_before = row, g_before = g;
       }
     }
     // nothing of ours may still be landing when the CTA leaves (an abort apart, all of it has been used)
@@ -345,58 +344,53 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
       __syncwarp();
       if (more) qk(w, k, kq.j == 0, kq.j + 1 == kq.n, release, halves);
     };
+    if (na > 0) {
+      Walk kq, kp;
+      kq.start(p.segs + cta.a0);
+      kp = kq;
+      Ring<C::NS> rk(0), rv(1);
+      ok = mbar_wait_warp(full(rk.st), rk.phase, abort_addr, p.err);
+      tc_fence_after();
+      qk(0, rk, true, kq.n == 1, false, false);
+      qk(1, rk, true, kq.n == 1, true, false);
 #pragma unroll 1
-    for (int part = 0; part < 2 && ok; ++part) {
-      const bool lone = (part == 0) == (cta.lone_first != 0);
-      turn = 0;
-      if (!lone && na > 0) {
-        Walk kq, kp;
-        kq.start(p.segs + cta.a0);
-        kp = kq;
-        Ring<C::NS> rk(base_a), rv(base_a + 1);
-        ok = mbar_wait_warp(full(rk.st), rk.phase, abort_addr, p.err);
-        tc_fence_after();
-        qk(0, rk, true, kq.n == 1, false, false);
-        qk(1, rk, true, kq.n == 1, true, false);
-#pragma unroll 1
-        for (int i = 0; i < na && ok; ++i) {
-          const bool more = i + 1 < na;
-          kq.next();
-          rk.skip(2);
-          step(0, rv, kp, rk, kq, more, false, false);
-          step(1, rv, kp, rk, kq, more, true, false);
-          rv.skip(2);
-          kp.next();
-        }
+      for (int i = 0; i < na && ok; ++i) {
+        const bool more = i + 1 < na;
+        kq.next();
+        rk.skip(2);
+        step(0, rv, kp, rk, kq, more, false, false);
+        step(1, rv, kp, rk, kq, more, true, false);
+        rv.skip(2);
+        kp.next();
       }
-      if (lone && nb > 0) {
-        Walk kq[2], kp[2];
-        Ring<C::NS> rk(base_b), rv(base_b + lone_v(0, nb));
+    }
+    if (nb > 0 && ok) {
+      Walk kq[2], kp[2];
+      Ring<C::NS> rk(2 * na), rv(2 * na + lone_v(0, nb));
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
-          if (w < nb) {
-            kq[w].start(p.segs + cta.b0[w]);
-            kp[w] = kq[w];
-            ok = ok && mbar_wait_warp(full(rk.st), rk.phase, abort_addr, p.err);
-            tc_fence_after();
-            qk(w, rk, true, kq[w].n == 1, true, small);
-            kq[w].next();
-            rk.skip(w + 1);      // K(0), K(1), then every other half-tile
-          }
+      for (int w = 0; w < 2; ++w)
+        if (w < nb) {
+          kq[w].start(p.segs + cta.b0[w]);
+          kp[w] = kq[w];
+          ok = ok && mbar_wait_warp(full(rk.st), rk.phase, abort_addr, p.err);
+          tc_fence_after();
+          qk(w, rk, true, kq[w].n == 1, true, small);
+          kq[w].next();
+          rk.skip(w + 1);      // K(0), K(1), then every other half-tile
+        }
 #pragma unroll 1
-        for (int t = 0; t < nb && ok; t += 2) {
+      for (int t = 0; t < nb && ok; t += 2) {
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const int u = t + w;
-            if (u < nb) {
-              const bool more = u + 2 < nb;
-              step(w, rv, kp[w], rk, kq[w], more, true, small);
-              kp[w].next();
-              rv.skip(more ? 2 : 1);
-              if (more) {
-                kq[w].next();
-                rk.skip(2);
-              }
+        for (int w = 0; w < 2; ++w) {
+          const int u = t + w;
+          if (u < nb) {
+            const bool more = u + 2 < nb;
+            step(w, rv, kp[w], rk, kq[w], more, true, small);
+            kp[w].next();
+            rv.skip(more ? 2 : 1);
+            if (more) {
+              kq[w].next();
+              rk.skip(2);
             }
           }
         }
@@ -411,16 +405,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
     const int own_row = i / p.group, own_head = i - own_row * p.group;
     int s_waits = 0, o_waits = 0;
     bool ok = true;
-    // The pairs' segments and this stream's own, in the CTA's order (in one loop: the code is large enough to miss the
-    // instruction cache).
-    const int n_a = cta.a1 - cta.a0, n_b = cta.b1[w] - cta.b0[w], n_first = cta.lone_first ? n_b : n_a;
-    auto is_lone = [&](int k) { return (k < n_first) == (cta.lone_first != 0); };
-    auto seg_at = [&](int k) { return p.segs + (is_lone(k) ? cta.b0[w] : cta.a0) + k - (k < n_first ? 0 : n_first); };
+    // The pairs' segments, then this stream's own (in one loop: the code is large enough to miss the instruction
+    // cache).
+    const int n_a = cta.a1 - cta.a0, n_b = cta.b1[w] - cta.b0[w];
+    auto seg_at = [&](int k) { return p.segs + (k < n_a ? cta.a0 + k : cta.b0[w] + k - n_a); };
     int done = 0;      // key tiles of the part before this segment
 #pragma unroll 1
     for (int n_seg = 0; n_seg < n_a + n_b; ++n_seg) {
-      const bool lone = is_lone(n_seg);
-      if (n_seg == n_first) done = 0;
+      const bool lone = n_seg >= n_a;
+      if (n_seg == n_a) done = 0;
       const PrefixSeg &s = *seg_at(n_seg);
       const int tile = lone ? 0 : w;
       const bool zero = lone || w == 0;      // whether this stream clears values that no lane sees
@@ -442,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
         // values of slots that no lane sees are cleared once they are there (a zero weight must not meet what
         // they hold, or what an unloaded box left)
         if (zero && (t0 < lo || t0 + kPrefixTile > hi)) {
-          const int r = lone ? base_b + lone_v(2 * (done + j) + w, nb) : base_a + 2 * (done + j) + 1;
+          const int r = lone ? 2 * na + lone_v(2 * (done + j) + w, nb) : 2 * (done + j) + 1;
           ok = mbar_wait_warp(full(r), phase(r), abort_addr, p.err);
           if (!ok) break;
           const int before = max(lo - t0, 0), from = min(hi - t0, kPrefixTile);   // rows [0, before) and [from, 128)
