@@ -186,20 +186,29 @@ std::vector<std::vector<Piece>> cut_line(const std::vector<Piece> &line, int n, 
   return out;
 }
 
+// Partial results of a tile of queries and a kv head: `count` of them from `first` on (0: its only segment writes
+// the output).
+struct Parts {
+  int32_t first, count;
+};
+// A row's tile over its own keys and its tile over the shared ones (-1: none), and its first lane in each.
+struct RowTiles {
+  int32_t own, own_lane, shared, shared_lane;
+};
+
 struct Work {
   std::vector<QueryTile> tiles;
   std::vector<Chain> chains;
   std::vector<PrefixSeg> segs;
   std::vector<PrefixCta> ctas;
-  std::vector<PrefixParts> parts;
-  std::vector<PrefixRow> rows;
+  std::vector<PrefixJoin> join;
 };
 
 void lay_out(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, Work &w) {
   const dsa_plan_t &plan = *pp->plan;
   const int32_t Hkv = pp->shape.kv_heads, group = pp->shape.q_heads / Hkv, per = kPrefixTile / group, BH = plan.box_rows;
   pp->rows_a_tile = per;
-  w.rows.assign(plan.T, PrefixRow{-1, 0, -1, 0});
+  std::vector<RowTiles> rows(plan.T, RowTiles{-1, 0, -1, 0});
   // Rows [r0, r1) against slots lo .. hi - 1 (causal: row r sees those below limit0 + r - r0 + 1 - ...).
   auto add = [&](int32_t r0, int32_t r1, int32_t span, int64_t lo, int64_t hi, bool causal, bool shared) {
     const PlanSpan &sp = plan.spans[span];
@@ -208,7 +217,7 @@ void lay_out(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, Work &w) {
       const int32_t n = std::min(per, r1 - r), id = static_cast<int32_t>(w.tiles.size());
       w.tiles.push_back(QueryTile{r, n});
       for (int32_t k = 0; k < n; ++k) {
-        PrefixRow &x = w.rows[r + k];
+        RowTiles &x = rows[r + k];
         (shared ? x.shared : x.own) = id;
         (shared ? x.shared_lane : x.own_lane) = k * group;
       }
@@ -335,27 +344,37 @@ void lay_out(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, Work &w) {
   }
   // partial results: none where a tile's only result is its own keys' only segment
   std::vector<char> has_shared(w.tiles.size(), 0);
-  for (const PrefixRow &r : w.rows)
+  for (const RowTiles &r : rows)
     if (r.shared >= 0) has_shared[r.own] = has_shared[r.shared] = 1;
-  w.parts.resize(w.tiles.size() * Hkv);
+  std::vector<Parts> parts(w.tiles.size() * Hkv);
   int64_t lanes = 0;
   for (size_t t = 0; t < w.tiles.size(); ++t)
     for (int32_t g = 0; g < Hkv; ++g) {
-      PrefixParts &x = w.parts[t * Hkv + g];
+      Parts &x = parts[t * Hkv + g];
       const int32_t count = pieces_of[t * Hkv + g];
-      x.lanes = w.tiles[t].rows * group;
       if (count == 1 && !has_shared[t]) continue;   // (count stays 0)
-      x.first = static_cast<int32_t>(lanes), x.count = count;
-      lanes += static_cast<int64_t>(count) * x.lanes;
+      x = Parts{static_cast<int32_t>(lanes), count};
+      lanes += static_cast<int64_t>(count) * w.tiles[t].rows * group;
       pp->joins = true;
+    }
+  w.join.resize(static_cast<size_t>(plan.T) * Hkv);
+  for (int32_t r = 0; r < plan.T; ++r)
+    for (int32_t g = 0; g < Hkv; ++g) {
+      PrefixJoin &x = w.join[static_cast<size_t>(r) * Hkv + g];
+      const int32_t tile[2] = {rows[r].own, rows[r].shared}, lane[2] = {rows[r].own_lane, rows[r].shared_lane};
+      for (int k = 0; k < 2; ++k) {
+        if (tile[k] < 0) continue;
+        const Parts &y = parts[static_cast<size_t>(tile[k]) * Hkv + g];
+        x.first[k] = y.first + lane[k], x.count[k] = y.count, x.stride[k] = w.tiles[tile[k]].rows * group;
+      }
     }
   pp->part_lanes = lanes;
   for (size_t i = 0; i < w.segs.size(); ++i)
     for (int m = 0; m < 2; ++m) {
       const int32_t t = w.chains[chain_of[i]].tile[m];
       if (t < 0) continue;
-      const PrefixParts &x = w.parts[static_cast<size_t>(t) * Hkv + w.segs[i].g];
-      w.segs[i].part[m] = x.count ? x.first + w.segs[i].part[m] * x.lanes : -1;
+      const Parts &x = parts[static_cast<size_t>(t) * Hkv + w.segs[i].g];
+      w.segs[i].part[m] = x.count ? x.first + w.segs[i].part[m] * w.segs[i].lanes[m] : -1;
     }
   w.segs.push_back(PrefixSeg{});   // (what lies behind the last is looked at, not used)
   pp->n_ctas = static_cast<int32_t>(w.ctas.size());
@@ -365,15 +384,13 @@ void lay_out(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, Work &w) {
 dsa_status upload(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, const Work &w) {
   auto round = [](size_t n) { return (n + 255) / 256 * 256; };
   const size_t o_seg = 0, o_cta = o_seg + round(w.segs.size() * sizeof(PrefixSeg)),
-               o_part = o_cta + round(w.ctas.size() * sizeof(PrefixCta)),
-               o_row = o_part + round(w.parts.size() * sizeof(PrefixParts)), tables = o_row + round(w.rows.size() * sizeof(PrefixRow)),
+               o_join = o_cta + round(w.ctas.size() * sizeof(PrefixCta)), tables = o_join + round(w.join.size() * sizeof(PrefixJoin)),
                o_ml = tables + round(static_cast<size_t>(pp->part_lanes) * pp->shape.head_dim * sizeof(float)),
                bytes = o_ml + round(static_cast<size_t>(pp->part_lanes) * sizeof(float2)) + 256;
   pp->host.assign(tables, 0);
   std::memcpy(pp->host.data() + o_seg, w.segs.data(), w.segs.size() * sizeof(PrefixSeg));
   std::memcpy(pp->host.data() + o_cta, w.ctas.data(), w.ctas.size() * sizeof(PrefixCta));
-  std::memcpy(pp->host.data() + o_part, w.parts.data(), w.parts.size() * sizeof(PrefixParts));
-  std::memcpy(pp->host.data() + o_row, w.rows.data(), w.rows.size() * sizeof(PrefixRow));
+  std::memcpy(pp->host.data() + o_join, w.join.data(), w.join.size() * sizeof(PrefixJoin));
   if (ctx->device < 0) return DSA_OK;
   if (cudaSetDevice(ctx->device) != cudaSuccess) return DSA_ERR_CUDA;
   if (cudaMallocAsync(reinterpret_cast<void **>(&pp->dev), bytes, pp->stream) != cudaSuccess) {
@@ -383,7 +400,7 @@ dsa_status upload(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, const Work &w) {
   }
   if (cudaMemcpyAsync(pp->dev, pp->host.data(), tables, cudaMemcpyHostToDevice, pp->stream) != cudaSuccess) return DSA_ERR_CUDA;
   pp->segs = reinterpret_cast<PrefixSeg *>(pp->dev + o_seg), pp->ctas = reinterpret_cast<PrefixCta *>(pp->dev + o_cta);
-  pp->parts = reinterpret_cast<PrefixParts *>(pp->dev + o_part), pp->rows = reinterpret_cast<PrefixRow *>(pp->dev + o_row);
+  pp->join = reinterpret_cast<PrefixJoin *>(pp->dev + o_join);
   pp->part_o = reinterpret_cast<float *>(pp->dev + tables), pp->part_ml = reinterpret_cast<float2 *>(pp->dev + o_ml);
   return DSA_OK;
 }

@@ -33,15 +33,11 @@ struct PrefixCta {
   int32_t small;           // no tile of the streams' own lists has more than 64 lanes
 };
 
-// Partial results of a tile of queries and a kv head: `count` of them, `lanes` apart, from `first` on
-// (count 0: written by its only segment).
-struct PrefixParts {
-  int32_t first, count, lanes;
-};
-// Where a row's results are: its tile over its own keys and its tile over the shared ones (-1: none),
-// and its first lane in each.
-struct PrefixRow {
-  int32_t own, own_lane, shared, shared_lane;
+// A row's partial results for the heads of one kv head: over its own keys, then over the shared ones; part k of
+// each lies `stride` lanes behind the one before, from `first` (the group's first head) on.  Both counts 0: the
+// row's only segment has written the output.
+struct PrefixJoin {
+  int32_t first[2], count[2], stride[2];
 };
 
 }  // namespace dsa
@@ -61,8 +57,7 @@ struct dsa_prefix_plan {
   char *dev = nullptr;
   dsa::PrefixSeg *segs = nullptr;        // device, and one more behind the last
   dsa::PrefixCta *ctas = nullptr;
-  dsa::PrefixParts *parts = nullptr;     // [tile][kv head]
-  dsa::PrefixRow *rows = nullptr;
+  dsa::PrefixJoin *join = nullptr;       // [row][kv head]
   float *part_o = nullptr;               // [lane][head_dim]
   float2 *part_ml = nullptr;             // [lane]: reference maximum (log2 units), sum
 };

@@ -158,8 +158,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  grid_dependency();
-  const PrefixCta cta = p.ctas[blockIdx.x];
+  launch_dependents();
+  const PrefixCta cta = p.ctas[blockIdx.x];   // (the plan's: nothing of this launch's stream writes it)
+  grid_dependency_wait();
   const int na = cta.tiles_a, nb = cta.tiles_b;
   const bool small = cta.small != 0;
 
@@ -582,8 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
 }
 
 struct JoinParams {
-  const PrefixRow *rows;
-  const PrefixParts *parts;
+  const PrefixJoin *join;
   const float *part_o;
   const float2 *part_ml;
   __nv_bfloat16 *out;
@@ -591,45 +591,61 @@ struct JoinParams {
   int32_t Hq, Hkv, group;
 };
 
-// A warp a (row, query head): its partial results, the own keys' first, in their order.
+// A warp a (row, query head): its partial results, the own keys' first, in their order.  A lane holds D / 32 dims, and
+// of 32 parts at a time the weight of one.
 template <int D>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const JoinParams p) {
-  constexpr int N = D / 32;
-  grid_dependency();
+  constexpr int N = D / 32, kAtOnce = 8;
+  launch_dependents();
   const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
-  if (item >= p.items) return;
   const int lane = lane_id();
-  const int64_t row = item / p.Hq;
-  const int h = static_cast<int>(item - row * p.Hq), g = h / p.group, hl = h - g * p.group;
-  const PrefixRow at = p.rows[row];
-  const PrefixParts own = p.parts[static_cast<int64_t>(at.own) * p.Hkv + g];
-  if (own.count == 0) return;   // written already
-  PrefixParts shared{0, 0, 0};
-  if (at.shared >= 0) shared = p.parts[static_cast<int64_t>(at.shared) * p.Hkv + g];
-  const int n = own.count + shared.count;
+  PrefixJoin at{};
+  int hl = 0;
+  if (item < p.items) {   // (the table is the plan's: nothing of this launch's stream writes it)
+    const int64_t row = item / p.Hq;
+    const int h = static_cast<int>(item - row * p.Hq), g = h / p.group;
+    hl = h - g * p.group;
+    at = p.join[row * p.Hkv + g];
+  }
+  grid_dependency_wait();
+  const int n = at.count[0] + at.count[1];
+  if (n == 0) return;   // past the end, or written already
   auto lane_of = [&](int k) {
-    return k < own.count ? static_cast<int64_t>(own.first) + static_cast<int64_t>(k) * own.lanes + at.own_lane + hl
-                         : static_cast<int64_t>(shared.first) + static_cast<int64_t>(k - own.count) * shared.lanes + at.shared_lane + hl;
+    const int s = k < at.count[0] ? 0 : 1, i = k - (s ? at.count[0] : 0);
+    return static_cast<int64_t>(at.first[s]) + static_cast<int64_t>(i) * at.stride[s] + hl;
   };
-  float top = kNoMax;
-  for (int k = lane; k < n; k += 32) top = fmaxf(top, p.part_ml[lane_of(k)].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float sum = 0.f, o[N];
+  float top = kNoMax, sum = 0.f, o[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) o[i] = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < n; ++k) {
-    const int64_t l = lane_of(k);
-    const float2 ml = p.part_ml[l];
-    const float weight = exp2_approx(ml.x - top);
-    sum = fmaf(weight, ml.y, sum);
-    const float *src = p.part_o + l * D + lane * N;
-    float v[N];
-    if constexpr (N == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(src);
-    else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(src);
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    float2 ml = make_float2(kNoMax, 0.f);
+    if (k0 + lane < n) ml = p.part_ml[lane_of(k0 + lane)];
+    float most = fmaxf(top, ml.x);
 #pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = fmaf(weight, v[i], o[i]);
+    for (int w = 16; w; w >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, w));
+    const float keep = exp2_approx(top - most), weight = exp2_approx(ml.x - most);
+    top = most;
+    sum *= keep;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] *= keep;
+    const int parts = min(n - k0, 32);
+    for (int k = 0; k < parts; k += kAtOnce) {
+      float v[kAtOnce][N];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const float *src = p.part_o + lane_of(min(k0 + k + u, n - 1)) * D + lane * N;   // (past the last: weight 0)
+        if constexpr (N == 4) *reinterpret_cast<float4 *>(v[u]) = *reinterpret_cast<const float4 *>(src);
+        else *reinterpret_cast<float2 *>(v[u]) = *reinterpret_cast<const float2 *>(src);
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const float x = __shfl_sync(0xffffffffu, weight, k + u), y = __shfl_sync(0xffffffffu, ml.y, k + u);
+        if (k + u >= parts) break;
+        sum = fmaf(x, y, sum);
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = fmaf(x, v[u][i], o[i]);
+      }
+    }
   }
   const float scale = 1.f / sum;
   __nv_bfloat16 *out = p.out + item * D + lane * N;
@@ -670,7 +686,7 @@ cudaError_t run(const dsa_ctx *ctx, const dsa_prefix_plan_t *pp, const void *q, 
   *launches += 1;
   e = launch_overlapped(prefix_tc_kernel<D>, dim3(pp->n_ctas), kThreads, Cfg<D>::BYTES, 1, s, p);
   if (e != cudaSuccess || !pp->joins) return e;
-  JoinParams j{pp->rows, pp->parts, pp->part_o, pp->part_ml, p.out, static_cast<int64_t>(plan.T) * ms.q_heads, p.Hq, p.Hkv, p.group};
+  JoinParams j{pp->join, pp->part_o, pp->part_ml, p.out, static_cast<int64_t>(plan.T) * ms.q_heads, p.Hq, p.Hkv, p.group};
   *launches += 1;
   return launch_overlapped(prefix_join_kernel<D>, dim3(static_cast<unsigned>((j.items + 7) / 8)), 256, 0, 1, s, j);
 }
