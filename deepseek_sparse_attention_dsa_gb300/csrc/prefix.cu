@@ -144,45 +144,38 @@ struct Piece {
   int32_t chain, t0, t1;
 };
 
-// A segment costs kStart key tiles beside its own: its queries' load, the first product's latency, its output.
-constexpr double kStart = 2.0;
+// What a CTA spends on a piece, in us: a key tile, and beside its tiles the queries' load, the first product's latency
+// and the output.  Measured on 152 SMs: a pair's tile 1.55 (its products), its partial results 2.5 to 3; lone tiles
+// two streams at a time.
+struct Cost {
+  double tile, start;
+};
+constexpr Cost kPairCost{1.55, 3.0}, kLoneCost{1.2, 1.3};
+constexpr double kLeast = 2.5;      // fewer CTAs rather than less than this for each
 
-// Cuts a line of pieces into at most n runs of about the same cost, at least `least` each.  A cut costs a start;
-// one that would leave less than a sliver behind it is not made, nor one before a piece's first key tile.
-std::vector<std::vector<Piece>> cut_line(const std::vector<Piece> &line, int n, double least) {
-  double left = 0.0;      // cost still to lay out
-  for (const Piece &x : line) left += x.t1 - x.t0 + kStart;
-  std::vector<std::vector<Piece>> out;
-  if (line.empty()) return out;
-  n = std::max(1, std::min(n, static_cast<int>(left / least)));
-  size_t i = 0;
-  Piece x = line[0];
-  for (; n > 0 && i < line.size(); --n) {
-    out.emplace_back();
-    const double share = left / n, sliver = std::max(0.5, 0.05 * share);
-    double room = share;
-    while (i < line.size()) {
-      const double cost = x.t1 - x.t0 + kStart;
-      if (n == 1 || cost <= room + sliver) {
+// A line of pieces in runs of at most `most` each: a piece that does not fit is cut, unless that would leave a sliver
+// of it in a run that has something already (a cut costs a start).
+template <typename CostOf>
+std::vector<std::vector<Piece>> cut_line(const std::vector<Piece> &line, double most, CostOf cost_of) {
+  std::vector<std::vector<Piece>> out(1);
+  double room = most;
+  for (Piece x : line)
+    for (;;) {
+      const Cost c = cost_of(x);
+      const int32_t n = x.t1 - x.t0;
+      const bool empty = out.back().empty();
+      if (n * c.tile + c.start <= room || (empty && n == 1)) {
         out.back().push_back(x);
-        room -= cost, left -= cost;
-        if (++i < line.size()) x = line[i];
-        continue;
+        room -= n * c.tile + c.start;
+        break;
       }
-      int32_t here = static_cast<int32_t>(room - kStart + 0.5);
-      if (out.back().empty()) here = std::max(here, 1);
-      here = std::min(here, x.t1 - x.t0 - 1);
-      if (here < 1 || (here < sliver && !out.back().empty())) break;
-      out.back().push_back(Piece{x.chain, x.t0, x.t0 + here});
-      x.t0 += here, left -= here;
-      break;
+      int32_t here = static_cast<int32_t>(std::max(0.0, (room - c.start) / c.tile));
+      here = std::min(empty ? std::max(here, 1) : here * c.tile < 0.1 * most ? 0 : here, n - 1);
+      if (here > 0) out.back().push_back(Piece{x.chain, x.t0, x.t0 + here});
+      x.t0 += here;
+      out.emplace_back();
+      room = most;
     }
-    if (out.back().empty()) {      // (a piece of one tile that is above the share)
-      out.back().push_back(x);
-      left -= x.t1 - x.t0 + kStart;
-      if (++i < line.size()) x = line[i];
-    }
-  }
   return out;
 }
 
@@ -265,15 +258,17 @@ void lay_out(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, Work &w) {
     }
     i = end;
   }
-  // The pairs' line, then the lone tiles'; each cut evenly over the CTAs.  Chains of pairs over the same keys
+  // One line, the pairs' chains, then the lone tiles', cut evenly over the CTAs.  Chains of pairs over the same keys
   // that are longer than a CTA's share go in blocks of it, all pairs' first block first, so that CTAs that
   // run together read the same keys.
-  std::vector<Piece> pairs, lone;
-  const int n = std::max(1, ctx->num_sms);
+  std::vector<Piece> line, lone;
+  const int n = std::max(2, ctx->num_sms / 2 * 2);
   double cost = 0.0;
-  for (const Chain &c : w.chains)
-    if (c.tile[1] >= 0) cost += c.ntiles + kStart;
-  const int32_t block = std::max<int32_t>(4, static_cast<int32_t>(cost / n - kStart + 0.5));
+  for (const Chain &c : w.chains) {
+    const Cost x = c.tile[1] >= 0 ? kPairCost : kLoneCost;
+    cost += c.ntiles * x.tile + x.start;
+  }
+  const int32_t block = std::max<int32_t>(4, static_cast<int32_t>((cost / n - kPairCost.start) / kPairCost.tile + 0.5));
   for (size_t c = 0; c < w.chains.size();) {
     const Chain &x = w.chains[c];
     size_t e = c + 1;
@@ -285,13 +280,30 @@ void lay_out(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, Work &w) {
     for (int32_t t = 0; t < most; t += block)
       for (size_t k = c; k < e; ++k)
         if (w.chains[k].tile[1] >= 0 && t < w.chains[k].ntiles)
-          pairs.push_back(Piece{static_cast<int32_t>(k), t, std::min(t + block, w.chains[k].ntiles)});
+          line.push_back(Piece{static_cast<int32_t>(k), t, std::min(t + block, w.chains[k].ntiles)});
     for (size_t k = c; k < e; ++k)
       if (w.chains[k].tile[1] < 0) lone.push_back(Piece{static_cast<int32_t>(k), 0, w.chains[k].ntiles});
     c = e;
   }
-  const auto a = cut_line(pairs, n, 4.0 + kStart), b = cut_line(lone, n, 4.0);
-  w.ctas.assign(std::max(a.size(), b.size()), PrefixCta{});
+  line.insert(line.end(), lone.begin(), lone.end());
+  // the least that a CTA can be given so that n of them do
+  auto cost_of = [&](const Piece &x) { return w.chains[x.chain].tile[1] >= 0 ? kPairCost : kLoneCost; };
+  double low = std::max(cost / n, kLeast), high = 2.0 * low + kPairCost.start + kPairCost.tile;
+  auto runs = cut_line(line, low, cost_of);
+  if (static_cast<int>(runs.size()) > n) {
+    while (static_cast<int>((runs = cut_line(line, high, cost_of)).size()) > n) high *= 1.5;
+    for (int i = 0; i < 10; ++i) {
+      const double mid = 0.5 * (low + high);
+      auto r = cut_line(line, mid, cost_of);
+      if (static_cast<int>(r.size()) <= n) high = mid, runs = std::move(r);
+      else low = mid;
+    }
+  }
+  // neighbours share a TPC where there are more of them than TPCs (launched as clusters of two): lone tiles beside
+  // pairs, both wait longer for their loads
+  pp->paired = static_cast<int>(runs.size()) > n / 2;
+  if (pp->paired && runs.size() % 2) runs.emplace_back();
+  w.ctas.assign(runs.size(), PrefixCta{});
   std::vector<int32_t> pieces_of(w.tiles.size() * Hkv, 0);
   auto put = [&](const Piece &x) {
     const Chain &c = w.chains[x.chain];
@@ -315,22 +327,20 @@ void lay_out(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, Work &w) {
   for (size_t i = 0; i < w.ctas.size(); ++i) {
     PrefixCta &cta = w.ctas[i];
     cta.a0 = static_cast<int32_t>(w.segs.size());
-    if (i < a.size())
-      for (const Piece &x : a[i]) {
-        chain_of.push_back(put(x));
-        cta.tiles_a += x.t1 - x.t0;
-      }
+    size_t at = 0;                          // (the pairs come first)
+    for (; at < runs[i].size() && w.chains[runs[i][at].chain].tile[1] >= 0; ++at) {
+      chain_of.push_back(put(runs[i][at]));
+      cta.tiles_a += runs[i][at].t1 - runs[i][at].t0;
+    }
     cta.a1 = static_cast<int32_t>(w.segs.size());
-    if (i < b.size())
-      for (const Piece &x : b[i]) cta.tiles_b += x.t1 - x.t0;
+    for (size_t k = at; k < runs[i].size(); ++k) cta.tiles_b += runs[i][k].t1 - runs[i][k].t0;
     int32_t left = (cta.tiles_b + 1) / 2;   // the first stream's tiles
-    size_t at = 0;
     int32_t from = 0;                       // tiles of piece `at` that are laid out
     for (int m = 0; m < 2; ++m) {
       cta.b0[m] = static_cast<int32_t>(w.segs.size());
       if (m == 1) left = cta.tiles_b / 2;
       while (left > 0) {
-        const Piece &x = b[i][at];
+        const Piece &x = runs[i][at];
         const int32_t k = std::min(left, x.t1 - x.t0 - from);
         chain_of.push_back(put(Piece{x.chain, x.t0 + from, x.t0 + from + k}));
         left -= k, from += k;

@@ -49,6 +49,7 @@ struct dsa_prefix_plan {
   int64_t tokens_read = 0;
   // tensor cores
   bool tc = false, joins = false;        // joins: some row has partial results
+  bool paired = false;                   // neighbouring CTAs on one TPC
   cudaStream_t stream = nullptr;
   int device = -1;
   int32_t rows_a_tile = 0, n_ctas = 0;

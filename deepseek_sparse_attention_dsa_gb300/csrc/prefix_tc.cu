@@ -160,7 +160,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
   const uint32_t tmem = *tmem_slot;
   launch_dependents();
   const PrefixCta cta = p.ctas[blockIdx.x];   // (the plan's: nothing of this launch's stream writes it)
-  grid_dependency_wait();
   const int na = cta.tiles_a, nb = cta.tiles_b;
   const bool small = cta.small != 0;
 
@@ -185,10 +184,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
       }
       return x;
     };
+    bool waited = false;      // for the kernels before: the plan's tables are read ahead of that, nothing else
     int r = 0;
     uint32_t q_loaded = 0, q_odd = 0;      // bit 2 w + b: stream w's buffer b has been loaded; an odd number of times
     bool ok = true;
     auto load = [&](int x0, int row) {   // the next half-tile of the ring, columns x0 ..
+      if (!waited) grid_dependency_wait();
+      waited = true;
       ok = ok && mbar_wait_warp(empty(r), phase(r) ^ 1u, abort_addr, p.err);
       if (!ok) return;
       const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, row >= 0)) * p.BH * 128;
@@ -280,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
+    // (reads the plan's tables and shared memory only: it does not wait for the kernels before)
     // ------------------------------------------------------------ products
     // One warp for both streams, so that half-tiles are awaited in the order in which they were asked for (a parity
     // says nothing of a fill two uses away).  The whole warp walks and waits, one elected thread issues: its operands
@@ -406,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
     const int own_row = i / p.group, own_head = i - own_row * p.group;
     int s_waits = 0, o_waits = 0;
     bool ok = true;
+    grid_dependency_wait();      // (before the first store)
     // The pairs' segments, then this stream's own (in one loop: the code is large enough to miss the instruction
     // cache).
     const int n_a = cta.a1 - cta.a0, n_b = cta.b1[w] - cta.b0[w];
@@ -684,7 +688,7 @@ cudaError_t run(const dsa_ctx *ctx, const dsa_prefix_plan_t *pp, const void *q, 
   cudaError_t e = ensure_smem_limit(prefix_tc_kernel<D>, Cfg<D>::BYTES, ctx->device, smem_limit_set);
   if (e != cudaSuccess) return e;
   *launches += 1;
-  e = launch_overlapped(prefix_tc_kernel<D>, dim3(pp->n_ctas), kThreads, Cfg<D>::BYTES, 1, s, p);
+  e = launch_overlapped(prefix_tc_kernel<D>, dim3(pp->n_ctas), kThreads, Cfg<D>::BYTES, pp->paired ? 2 : 1, s, p);
   if (e != cudaSuccess || !pp->joins) return e;
   JoinParams j{pp->join, pp->part_o, pp->part_ml, p.out, static_cast<int64_t>(plan.T) * ms.q_heads, p.Hq, p.Hkv, p.group};
   *launches += 1;
