@@ -365,19 +365,19 @@ void lay_out(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, Work &w) {
       if (count == 1 && !has_shared[t]) continue;   // (count stays 0)
       x = Parts{static_cast<int32_t>(lanes), count};
       lanes += static_cast<int64_t>(count) * w.tiles[t].rows * group;
-      pp->joins = true;
     }
-  w.join.resize(static_cast<size_t>(plan.T) * Hkv);
   for (int32_t r = 0; r < plan.T; ++r)
     for (int32_t g = 0; g < Hkv; ++g) {
-      PrefixJoin &x = w.join[static_cast<size_t>(r) * Hkv + g];
+      PrefixJoin x{r, g, {0, 0}, {0, 0}, {0, 0}};
       const int32_t tile[2] = {rows[r].own, rows[r].shared}, lane[2] = {rows[r].own_lane, rows[r].shared_lane};
       for (int k = 0; k < 2; ++k) {
         if (tile[k] < 0) continue;
         const Parts &y = parts[static_cast<size_t>(tile[k]) * Hkv + g];
         x.first[k] = y.first + lane[k], x.count[k] = y.count, x.stride[k] = w.tiles[tile[k]].rows * group;
       }
+      if (x.count[0] > 0) w.join.push_back(x);
     }
+  pp->n_join = static_cast<int32_t>(w.join.size());
   pp->part_lanes = lanes;
   for (size_t i = 0; i < w.segs.size(); ++i)
     for (int m = 0; m < 2; ++m) {

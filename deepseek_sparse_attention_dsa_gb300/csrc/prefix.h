@@ -33,10 +33,10 @@ struct PrefixCta {
   int32_t small;           // no tile of the streams' own lists has more than 64 lanes
 };
 
-// A row's partial results for the heads of one kv head: over its own keys, then over the shared ones; part k of
-// each lies `stride` lanes behind the one before, from `first` (the group's first head) on.  Both counts 0: the
-// row's only segment has written the output.
+// A row's partial results for the heads of kv head g: over its own keys, then over the shared ones; part k of each
+// lies `stride` lanes behind the one before, from `first` (the group's first head) on.  Only rows that have such.
 struct PrefixJoin {
+  int32_t row, g;
   int32_t first[2], count[2], stride[2];
 };
 
@@ -48,17 +48,17 @@ struct dsa_prefix_plan {
   std::vector<dsa_prefix_t> prefixes;
   int64_t tokens_read = 0;
   // tensor cores
-  bool tc = false, joins = false;        // joins: some row has partial results
+  bool tc = false;
   bool paired = false;                   // neighbouring CTAs on one TPC
   cudaStream_t stream = nullptr;
   int device = -1;
-  int32_t rows_a_tile = 0, n_ctas = 0;
+  int32_t rows_a_tile = 0, n_ctas = 0, n_join = 0;
   int64_t part_lanes = 0;
   std::vector<char> host;                // staging copy of the tables
   char *dev = nullptr;
   dsa::PrefixSeg *segs = nullptr;        // device, and one more behind the last
   dsa::PrefixCta *ctas = nullptr;
-  dsa::PrefixJoin *join = nullptr;       // [row][kv head]
+  dsa::PrefixJoin *join = nullptr;       // [n_join]
   float *part_o = nullptr;               // [lane][head_dim]
   float2 *part_ml = nullptr;             // [lane]: reference maximum (log2 units), sum
 };

@@ -592,31 +592,33 @@ struct JoinParams {
   const float2 *part_ml;
   __nv_bfloat16 *out;
   int64_t items;
-  int32_t Hq, Hkv, group;
+  int32_t Hq, group;
 };
 
 // A warp a (row, query head): its partial results, the own keys' first, in their order.  A lane holds D / 32 dims, and
-// of 32 parts at a time the weight of one.
+// of 32 parts at a time the weight of one; a dozen parts are loaded at once, ahead of their weights.  Four warps and
+// few registers, so that a CTA is set up beside the CTA of the attention that it waits for.
+constexpr int kJoinWarps = 4;
 template <int D>
-__global__ void __launch_bounds__(256) prefix_join_kernel(const JoinParams p) {
-  constexpr int N = D / 32, kAtOnce = 8;
+__global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(const JoinParams p) {
+  constexpr int N = D / 32, kAtOnce = 12;
   launch_dependents();
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kJoinWarps + threadIdx.x / 32;
   const int lane = lane_id();
   PrefixJoin at{};
   int hl = 0;
   if (item < p.items) {   // (the table is the plan's: nothing of this launch's stream writes it)
-    const int64_t row = item / p.Hq;
-    const int h = static_cast<int>(item - row * p.Hq), g = h / p.group;
-    hl = h - g * p.group;
-    at = p.join[row * p.Hkv + g];
+    const int64_t entry = item / p.group;
+    hl = static_cast<int>(item - entry * p.group);
+    at = p.join[entry];
   }
   grid_dependency_wait();
   const int n = at.count[0] + at.count[1];
-  if (n == 0) return;   // past the end, or written already
+  if (n == 0) return;   // past the end
   auto lane_of = [&](int k) {
-    const int s = k < at.count[0] ? 0 : 1, i = k - (s ? at.count[0] : 0);
-    return static_cast<int64_t>(at.first[s]) + static_cast<int64_t>(i) * at.stride[s] + hl;
+    const bool own = k < at.count[0];
+    const int i = own ? k : k - at.count[0];
+    return static_cast<int64_t>(own ? at.first[0] : at.first[1]) + static_cast<int64_t>(i) * (own ? at.stride[0] : at.stride[1]) + hl;
   };
   float top = kNoMax, sum = 0.f, o[N];
 #pragma unroll
@@ -624,27 +626,32 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const JoinParams p) {
   for (int k0 = 0; k0 < n; k0 += 32) {
     float2 ml = make_float2(kNoMax, 0.f);
     if (k0 + lane < n) ml = p.part_ml[lane_of(k0 + lane)];
-    float most = fmaxf(top, ml.x);
-#pragma unroll
-    for (int w = 16; w; w >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, w));
-    const float keep = exp2_approx(top - most), weight = exp2_approx(ml.x - most);
-    top = most;
-    sum *= keep;
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] *= keep;
+    float weight = 0.f;
     const int parts = min(n - k0, 32);
     for (int k = 0; k < parts; k += kAtOnce) {
       float v[kAtOnce][N];
 #pragma unroll
       for (int u = 0; u < kAtOnce; ++u) {
-        const float *src = p.part_o + lane_of(min(k0 + k + u, n - 1)) * D + lane * N;   // (past the last: weight 0)
+        if (k + u >= parts) break;
+        const float *src = p.part_o + lane_of(k0 + k + u) * D + lane * N;
         if constexpr (N == 4) *reinterpret_cast<float4 *>(v[u]) = *reinterpret_cast<const float4 *>(src);
         else *reinterpret_cast<float2 *>(v[u]) = *reinterpret_cast<const float2 *>(src);
       }
+      if (k == 0) {
+        float most = fmaxf(top, ml.x);
+#pragma unroll
+        for (int w = 16; w; w >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, w));
+        const float keep = exp2_approx(top - most);
+        weight = exp2_approx(ml.x - most);
+        top = most;
+        sum *= keep;
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] *= keep;
+      }
 #pragma unroll
       for (int u = 0; u < kAtOnce; ++u) {
-        const float x = __shfl_sync(0xffffffffu, weight, k + u), y = __shfl_sync(0xffffffffu, ml.y, k + u);
         if (k + u >= parts) break;
+        const float x = __shfl_sync(0xffffffffu, weight, k + u), y = __shfl_sync(0xffffffffu, ml.y, k + u);
         sum = fmaf(x, y, sum);
 #pragma unroll
         for (int i = 0; i < N; ++i) o[i] = fmaf(x, v[u][i], o[i]);
@@ -652,7 +659,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const JoinParams p) {
     }
   }
   const float scale = 1.f / sum;
-  __nv_bfloat16 *out = p.out + item * D + lane * N;
+  __nv_bfloat16 *out = p.out + (static_cast<int64_t>(at.row) * p.Hq + at.g * p.group + hl) * D + lane * N;
 #pragma unroll
   for (int i = 0; i < N; i += 2) *reinterpret_cast<uint32_t *>(out + i) = pack_bf16(o[i] * scale, o[i + 1] * scale);
 }
@@ -689,10 +696,11 @@ cudaError_t run(const dsa_ctx *ctx, const dsa_prefix_plan_t *pp, const void *q, 
   if (e != cudaSuccess) return e;
   *launches += 1;
   e = launch_overlapped(prefix_tc_kernel<D>, dim3(pp->n_ctas), kThreads, Cfg<D>::BYTES, pp->paired ? 2 : 1, s, p);
-  if (e != cudaSuccess || !pp->joins) return e;
-  JoinParams j{pp->join, pp->part_o, pp->part_ml, p.out, static_cast<int64_t>(plan.T) * ms.q_heads, p.Hq, p.Hkv, p.group};
+  if (e != cudaSuccess || pp->n_join == 0) return e;
+  JoinParams j{pp->join, pp->part_o, pp->part_ml, p.out, static_cast<int64_t>(pp->n_join) * p.group, p.Hq, p.group};
   *launches += 1;
-  return launch_overlapped(prefix_join_kernel<D>, dim3(static_cast<unsigned>((j.items + 7) / 8)), 256, 0, 1, s, j);
+  return launch_overlapped(prefix_join_kernel<D>, dim3(static_cast<unsigned>((j.items + kJoinWarps - 1) / kJoinWarps)),
+                           kJoinWarps * 32, 0, 1, s, j);
 }
 
 }  // namespace
