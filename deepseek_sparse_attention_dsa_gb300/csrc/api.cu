@@ -1004,7 +1004,7 @@ dsa_status dsa_rotate(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_rotary_t
       !apart(g.width, g.rows, g.out_stride, g.heads, g.out_head) ||
       (x == out && (g.x_stride != g.out_stride || g.x_head != g.out_head)))
     return DSA_ERR_INVALID_ARG;
-  if (rotary_ctas(table, g, x == out) > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  if (rotary_ctas(table, g, x, out) > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   return cuda_status(ctx, launch_rotary(table, g, x, plan ? plan->row_pos : positions, plan != nullptr, out,
                                         reinterpret_cast<cudaStream_t>(stream), &launched.n));
 }

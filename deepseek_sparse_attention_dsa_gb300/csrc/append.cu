@@ -26,6 +26,8 @@ struct AppendParams {
   const uint64_t *turns;
   int *err;
   int32_t T, P, num_pages, rot, parts, part[3];
+  int32_t groups, side, deep;   // append_pieces_kernel
+  bool padded, halves;          // a capturable plan's rows; some part rotates halves
   float amplitude;
   // latents
   const char *c, *k_pe;
@@ -142,6 +144,155 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
   }
 }
 
+// The same where every row consists of whole pieces of eight columns on 16 bytes (8 for codes), in groups of 16 lanes:
+// 128 columns of a latent, its rope, an index key, a head of K or V.  A thread has one piece of each of several rows:
+// they are on their way, packed, while positions and pages are looked up and angles made, once for all of a row's
+// groups.  The other column of a pair comes from a neighbouring lane, a group's maximum from its 16.
+// p.groups a row, p.side rows beside one another in a CTA and p.deep of them in a thread.  kWide: some source is fp32.
+constexpr int kAppendThreads = 256;
+template <bool kWide>
+constexpr int kAppendDeep = kWide ? 2 : 4;
+constexpr int kAppendRows = kAppendThreads / 16 * 4;   // the most that a CTA has (one group a row)
+
+template <bool kWide>
+__global__ void __launch_bounds__(kAppendThreads) append_pieces_kernel(const AppendParams p) {
+  constexpr int W = kWide ? 2 : 1, DEEP = kAppendDeep<kWide>;
+  extern __shared__ float2 angles[];   // [rows of the CTA][rot / 2]
+  __shared__ int2 where[kAppendRows];  // of the CTA's rows: page (-1: nothing to write), slot in it
+  grid_dependency();
+  const int group = threadIdx.x / 16, lane = threadIdx.x % 16, local = group / p.groups, rows = p.side * p.deep;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows;
+  int gi = group - local * p.groups, part = kPartLatent, base = 0;
+  // the group's part of the row: latents (kv_lora_rank / 128 groups and the rope's), key, heads of K, heads of V
+  int width = 0, type = DSA_BF16, rot = 0, layout = 0, offset = 0;
+  int64_t stride = 0;
+  const char *src = nullptr;
+  bool rope = false;
+  const int latent_groups = p.c ? (p.L + 127) / 128 + (p.R > 0 ? 1 : 0) : 0, key_groups = p.keys ? 1 : 0;
+  if (gi < latent_groups) {
+    rope = p.R > 0 && gi == latent_groups - 1;
+    if (rope) src = p.k_pe, stride = p.k_pe_stride, width = p.R, type = p.k_pe_type, rot = p.rot, layout = p.layout;
+    else src = p.c, stride = p.c_stride, width = p.L, type = p.c_type, base = gi * 128;
+  } else if ((gi -= latent_groups) < key_groups) {
+    part = kPartKey;
+    src = p.keys, stride = p.keys_stride, width = p.D, type = p.key_type, rot = p.rot, layout = p.key_layout, offset = p.key_offset;
+  } else {
+    gi -= key_groups;
+    part = gi < p.heads ? kPartK : kPartV;
+    if (part == kPartV) gi -= p.heads;
+    src = part == kPartK ? p.k + gi * p.k_head : p.v + gi * p.v_head;
+    stride = part == kPartK ? p.k_stride : p.v_stride, width = p.dim, type = p.kv_type;
+    if (part == kPartK) rot = p.rot, layout = p.kv_layout, offset = p.kv_offset;
+  }
+  const int col = base + lane * 8;
+  src += col * (type == DSA_BF16 ? 2 : 4);
+  uint4 x[DEEP][W];
+#pragma unroll
+  for (int i = 0; i < DEEP; ++i) {
+    const int64_t row = row0 + i * p.side + local;
+    if (i < p.deep && local < p.side && row < p.T && col < width && !(p.padded && p.row_pos[row] < 0)) {   // (padding is not read)
+      const uint4 *from = reinterpret_cast<const uint4 *>(src + row * stride);
+      x[i][0] = from[0];
+      if constexpr (kWide)
+        if (type != DSA_BF16) x[i][1] = from[1];
+    }
+  }
+  for (int r = threadIdx.x; r < rows; r += blockDim.x) {
+    const int64_t row = row0 + r;
+    int2 at = make_int2(-1, 0);
+    if (row < p.T && p.row_pos[row] >= 0) {
+      // (both are below 2^31)
+      const uint32_t slot = static_cast<uint32_t>(p.row_page_start[row]) + static_cast<uint32_t>(p.row_pos[row]);
+      const uint32_t pi = slot / static_cast<uint32_t>(p.P);
+      if (pi < static_cast<uint32_t>(p.row_npages[row])) at = make_int2(p.pages[p.row_page_off[row] + pi], static_cast<int>(slot - pi * p.P));
+      if (at.x < 0 || at.x >= p.num_pages) {
+        atomicOr(p.err, kErrBounds);
+        at.x = -1;
+      }
+    }
+    where[r] = at;
+  }
+  if (p.rot) {
+    const int half = p.rot / 2;
+    // (from the last thread on: the first ones look the pages up)
+    for (int k = blockDim.x - 1 - threadIdx.x; k < rows * half; k += blockDim.x) {
+      const int r = k / half;
+      if (row0 + r < p.T) angles[k] = rotary_angle(p.row_pos[row0 + r], p.turns[k - r * half], p.amplitude);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < DEEP; ++i) {
+    if (i >= p.deep) break;      // uniform
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = 0.f;
+    const int r = i * p.side + local;
+    const int2 place = local < p.side ? where[r] : make_int2(-1, 0);
+    const bool in = col < width && place.x >= 0;
+    if (in) {
+      if (type == DSA_BF16) {
+        unpack8(v, x[i][0]);
+      } else if constexpr (kWide) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          v[4 * w] = __uint_as_float(x[i][w].x), v[4 * w + 1] = __uint_as_float(x[i][w].y);
+          v[4 * w + 2] = __uint_as_float(x[i][w].z), v[4 * w + 3] = __uint_as_float(x[i][w].w);
+        }
+      }
+    }
+    if (p.rot) {
+      const int half = p.rot / 2;
+      const bool turns = rot > 0 && in && col >= offset && col < offset + rot;
+      const float2 *cs = angles + r * half;
+      if (turns && layout == DSA_ROTARY_INTERLEAVED) rotate_interleaved(v, cs + (col - offset) / 2);
+      if (p.halves) {      // (all lanes take part in the exchange)
+        const bool mine = turns && layout == DSA_ROTARY_HALF, second = col - offset >= half;
+        const int from = mine ? lane + (second ? -half / 8 : half / 8) : lane;
+        float other[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) other[k] = __shfl_sync(0xffffffffu, v[k], from, 16);
+        if (mine) {
+          const float2 *w = cs + (col - offset) - (second ? half : 0);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            v[k] = second ? fmaf(other[k], w[k].y, v[k] * w[k].x) : fmaf(v[k], w[k].x, -other[k] * w[k].y);
+        }
+      }
+    }
+    uint32_t m = 0;
+    if (p.latent_fp8 || p.index_fp8) {
+      m = amax_bits8(v);
+#pragma unroll
+      for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));   // the group's 16 lanes
+    }
+    if (!in) continue;
+    const int64_t at = static_cast<int64_t>(place.x) * p.P + place.y;
+    if ((part == kPartLatent && !rope && p.latent_fp8) || (part == kPartKey && p.index_fp8)) {
+      const GroupScale g(m);
+      uint8_t *codes;
+      float *scale;
+      if (part == kPartLatent) {
+        char *out = p.latent + at * p.latent_row;
+        codes = reinterpret_cast<uint8_t *>(out) + col;
+        scale = reinterpret_cast<float *>(out + p.L) + base / 128;
+      } else {
+        char *out = p.index + static_cast<int64_t>(place.x) * p.P * (128 + 4);
+        codes = reinterpret_cast<uint8_t *>(out) + place.y * 128 + col;
+        scale = reinterpret_cast<float *>(out + static_cast<int64_t>(p.P) * 128) + place.y;
+      }
+      *reinterpret_cast<uint2 *>(codes) = codes8(v, g);
+      if (lane == 0) *scale = g.scale;
+      continue;
+    }
+    char *out;
+    if (part == kPartLatent) out = p.latent + at * p.latent_row + (rope ? p.rope_at : 0);
+    else if (part == kPartKey) out = p.index + at * p.D * 2;
+    else out = p.kv + (at * 2 * p.heads + (part == kPartV ? p.heads : 0) + gi) * p.dim * 2;
+    store8(out, DSA_BF16, col, width, true, v);
+  }
+}
+
 int bytes_of(int type) { return type == DSA_BF16 ? 2 : 4; }
 
 bool on16(const void *p, int64_t stride_bytes, int64_t head_bytes = 0) {
@@ -153,6 +304,7 @@ AppendParams append_base(const dsa_ctx *ctx, const dsa_plan_t *plan, const dsa_r
   p.row_pos = plan->row_pos, p.row_page_off = plan->row_page_off, p.row_npages = plan->row_npages;
   p.row_page_start = plan->row_page_start, p.pages = plan->pages, p.err = ctx->err;
   p.T = plan->T, p.P = ctx->cfg.page_size, p.num_pages = plan->cache_pages;
+  p.padded = plan->capturable;
   if (table) p.turns = table->turns, p.rot = table->rot, p.amplitude = table->amplitude;
   return p;
 }
@@ -169,11 +321,38 @@ void append_keys(const dsa_ctx *ctx, AppendParams &p, const dsa_append_t &a, con
   p.index_vec = whole && on16(index_cache, p.D * 2);
 }
 
-cudaError_t launch_append(const AppendParams &p, cudaStream_t s, int32_t *launches) {
+// Whether append_pieces_kernel takes the call: whole pieces, and pairs of them within a group of 16 lanes.
+bool whole_pieces(const AppendParams &p) {
+  if (p.c && (!p.c_vec || p.L % 8 || !p.latent_vec || p.R > 128 || p.R % 8 || (p.R > 0 && (!p.k_pe_vec || !p.rope_vec))))
+    return false;
+  if (p.keys && (!p.keys_vec || p.D > 128 || p.D % 8 || (p.index_fp8 ? reinterpret_cast<uintptr_t>(p.index) % 8 || p.P % 2 : !p.index_vec)))
+    return false;
+  if (p.k && (!p.k_vec || !p.v_vec || !p.kv_vec || p.dim > 128 || p.dim % 8)) return false;
+  return true;
+}
+
+cudaError_t launch_append(const dsa_ctx *ctx, AppendParams &p, cudaStream_t s, int32_t *launches) {
+  *launches += 1;
+  p.halves = p.rot && ((p.c && p.layout == DSA_ROTARY_HALF) || (p.keys && p.key_layout == DSA_ROTARY_HALF) ||
+                       (p.k && p.kv_layout == DSA_ROTARY_HALF));
+  p.groups = (p.c ? (p.L + 127) / 128 + (p.R > 0 ? 1 : 0) : 0) + (p.keys ? 1 : 0) + (p.k ? 2 * p.heads : 0);
+  if (whole_pieces(p) && p.groups <= kAppendThreads / 16) {
+    const bool wide = (p.c && (p.c_type != DSA_BF16 || (p.R > 0 && p.k_pe_type != DSA_BF16))) || (p.keys && p.key_type != DSA_BF16) ||
+                      (p.k && p.kv_type != DSA_BF16);
+    // as many rows side by side as the threads hold, and a thread as deep as leaves two CTAs an SM (and the angles in
+    // 48 KB): one row a CTA for a decode step, eight for a prefill chunk
+    const int sms = std::max(1, ctx->num_sms);
+    p.side = std::max(1, std::min(kAppendThreads / 16 / p.groups, p.T / sms));
+    p.deep = std::max(1, std::min(wide ? kAppendDeep<true> : kAppendDeep<false>, p.T / (2 * sms * p.side)));
+    while (p.deep > 1 && p.side * p.deep * (p.rot / 2) * sizeof(float2) > 48 * 1024) --p.deep;
+    const int rows = p.side * p.deep, threads = (p.side * p.groups + 1) / 2 * 32;
+    return launch_overlapped(wide ? append_pieces_kernel<true> : append_pieces_kernel<false>,
+                             dim3(static_cast<unsigned>((p.T + rows - 1) / rows)), threads,
+                             rows * (p.rot / 2) * static_cast<int>(sizeof(float2)), 1, s, p);
+  }
   int floats = p.rot ? rotary_pairs(p.rot) * 2 : 0;
   if (p.keys && p.index_fp8) floats += p.D;
   const int64_t tasks = static_cast<int64_t>(p.T) * p.parts;
-  *launches += 1;
   return launch_overlapped(append_kernel, dim3(static_cast<unsigned>((tasks + kAppendWarps - 1) / kAppendWarps)),
                            kAppendWarps * 32, floats * kAppendWarps * 4, 1, s, p);
 }
@@ -199,7 +378,7 @@ cudaError_t launch_append_latents(const dsa_ctx *ctx, const dsa_plan_t *plan, co
     p.rope_vec = whole && p.latent_vec && p.rope_at % 16 == 0;
   }
   if (keys) append_keys(ctx, p, a, keys, index_cache);
-  return launch_append(p, s, launches);
+  return launch_append(ctx, p, s, launches);
 }
 
 cudaError_t launch_append_kv(const dsa_ctx *ctx, const dsa_plan_t *plan, const dsa_rotary *table, const dsa_append_t &a,
@@ -216,7 +395,7 @@ cudaError_t launch_append_kv(const dsa_ctx *ctx, const dsa_plan_t *plan, const d
   p.k_vec = whole && on16(k, p.k_stride, p.k_head), p.v_vec = on16(v, p.v_stride, p.v_head);
   p.kv_vec = whole && on16(kv_cache, 2ll * head_dim);
   if (keys) append_keys(ctx, p, a, keys, index_cache);
-  return launch_append(p, s, launches);
+  return launch_append(ctx, p, s, launches);
 }
 
 }  // namespace dsa

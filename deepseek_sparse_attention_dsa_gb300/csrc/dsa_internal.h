@@ -353,7 +353,7 @@ bool project_tc_supported(const dsa_project_t &g, const void *a, const void *w);
 // Rotations and appends.  positions: the call's, or the plan's (plan_rows: those below 0 are padding).
 cudaError_t launch_rotary(const dsa_rotary *table, const dsa_rotate_t &g, const void *x, const int32_t *positions,
                           bool plan_rows, void *out, cudaStream_t s, int32_t *launches);
-int64_t rotary_ctas(const dsa_rotary *table, const dsa_rotate_t &g, bool in_place);   // the launch's grid
+int64_t rotary_ctas(const dsa_rotary *table, const dsa_rotate_t &g, const void *x, const void *out);   // the launch's grid
 // table, and either source of the first, may be NULL.
 cudaError_t launch_append_latents(const dsa_ctx *ctx, const dsa_plan_t *plan, const dsa_rotary *table, const dsa_append_t &a,
                                   const void *c, const void *k_pe, void *latent_cache, const void *keys, void *index_cache,

@@ -25,20 +25,22 @@ __device__ __forceinline__ float2 rotary_angle(int32_t position, uint64_t turns,
   return make_float2(c * amplitude, s * amplitude);
 }
 
-// Four neighbouring pairs in eight columns ("interleaved"); cs: their angles.
-__device__ __forceinline__ void rotate_interleaved(float (&v)[8], const float2 *cs) {
+// Neighbouring pairs in N columns ("interleaved"); cs: their angles.
+template <int N>
+__device__ __forceinline__ void rotate_interleaved(float (&v)[N], const float2 *cs) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < N / 2; ++i) {
     const float2 w = cs[i];
     const float a = v[2 * i], b = v[2 * i + 1];
     v[2 * i] = fmaf(a, w.x, -b * w.y);
     v[2 * i + 1] = fmaf(a, w.y, b * w.x);
   }
 }
-// Eight pairs, the first columns in a, the second in b ("half").
-__device__ __forceinline__ void rotate_half(float (&a)[8], float (&b)[8], const float2 *cs) {
+// N pairs, the first columns in a, the second in b ("half").
+template <int N>
+__device__ __forceinline__ void rotate_half(float (&a)[N], float (&b)[N], const float2 *cs) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < N; ++i) {
     const float2 w = cs[i];
     const float x = a[i], y = b[i];
     a[i] = fmaf(x, w.x, -y * w.y);
