@@ -26,8 +26,8 @@ struct AppendParams {
   const uint64_t *turns;
   int *err;
   int32_t T, P, num_pages, rot, parts, part[3];
-  int32_t groups, side, deep;   // append_pieces_kernel
-  bool padded, halves;          // a capturable plan's rows; some part rotates halves
+  int32_t groups, side, deep;   // append_runs_kernel
+  bool padded;                  // a capturable plan's rows
   float amplitude;
   // latents
   const char *c, *k_pe;
@@ -144,23 +144,27 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
   }
 }
 
-// The same where every row consists of whole pieces of eight columns on 16 bytes (8 for codes), in groups of 16 lanes:
-// 128 columns of a latent, its rope, an index key, a head of K or V.  A thread has one piece of each of several rows:
-// they are on their way, packed, while positions and pages are looked up and angles made, once for all of a row's
-// groups.  The other column of a pair comes from a neighbouring lane, a group's maximum from its 16.
-// p.groups a row, p.side rows beside one another in a CTA and p.deep of them in a thread.  kWide: some source is fp32.
+// The same where every row consists of whole runs of 16 columns on 16 bytes, in groups of eight lanes: 128 columns of a
+// latent, its rope, an index key, a head of K or V.  A thread has one run of each of several rows: they are on their
+// way, packed, while positions and pages are looked up and angles made, once for all of a row's groups.  The other
+// column of a pair comes from a neighbouring lane, a group's maximum from its eight.  p.groups a row, p.side rows beside one
+// another in a CTA and p.deep of them in a thread.  kWide: some source is fp32.  (Bound by its instructions and by the way
+// from one look-up to the next: with 8 columns a lane, twice the threads, 8192 rows took 11.8 us in 8 bits.)
 constexpr int kAppendThreads = 256;
+constexpr int kLaneCols = 16, kGroupLanes = 128 / kLaneCols;
 template <bool kWide>
 constexpr int kAppendDeep = kWide ? 2 : 4;
-constexpr int kAppendRows = kAppendThreads / 16 * 4;   // the most that a CTA has (one group a row)
+// Place of a row's angle q: lanes that read 8 or 16 of them from their own on meet no common bank.
+__host__ __device__ constexpr int padded(int q) { return q + q / 16; }
+constexpr int kAppendRows = kAppendThreads / kGroupLanes * 4;   // the most that a CTA has (one group a row)
 
 template <bool kWide>
-__global__ void __launch_bounds__(kAppendThreads) append_pieces_kernel(const AppendParams p) {
-  constexpr int W = kWide ? 2 : 1, DEEP = kAppendDeep<kWide>;
-  extern __shared__ float2 angles[];   // [rows of the CTA][rot / 2]
+__global__ void __launch_bounds__(kAppendThreads) append_runs_kernel(const AppendParams p) {
+  constexpr int N = kLaneCols, W = kWide ? 4 : 2, DEEP = kAppendDeep<kWide>;
+  extern __shared__ float2 angles[];   // [rows of the CTA][padded(rot / 2)]
   __shared__ int2 where[kAppendRows];  // of the CTA's rows: page (-1: nothing to write), slot in it
   grid_dependency();
-  const int group = threadIdx.x / 16, lane = threadIdx.x % 16, local = group / p.groups, rows = p.side * p.deep;
+  const int group = threadIdx.x / kGroupLanes, lane = threadIdx.x % kGroupLanes, local = group / p.groups, rows = p.side * p.deep;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows;
   int gi = group - local * p.groups, part = kPartLatent, base = 0;
   // the group's part of the row: latents (kv_lora_rank / 128 groups and the rope's), key, heads of K, heads of V
@@ -184,17 +188,29 @@ __global__ void __launch_bounds__(kAppendThreads) append_pieces_kernel(const App
     stride = part == kPartK ? p.k_stride : p.v_stride, width = p.dim, type = p.kv_type;
     if (part == kPartK) rot = p.rot, layout = p.kv_layout, offset = p.kv_offset;
   }
-  const int col = base + lane * 8;
-  src += col * (type == DSA_BF16 ? 2 : 4);
+  const int col = base + lane * N;
+  const bool mine = local < p.side && col < width, is_bf16 = !kWide || type == DSA_BF16;
+  const bool codes = (part == kPartLatent && !rope && p.latent_fp8) || (part == kPartKey && p.index_fp8);
+  const bool turns = rot > 0 && mine && col >= offset && col < offset + rot, second = turns && col - offset >= rot / 2;
+  const bool halves = __any_sync(0xffffffffu, rot > 0 && layout == DSA_ROTARY_HALF);     // (of the warp's groups)
+  const bool any_codes = __any_sync(0xffffffffu, codes);
+  // where this lane's run goes in a row of the cache, in bytes: row * row_bytes + at, or for index codes page by page
+  int64_t row_bytes = 0, at_byte = 0;
+  char *to = p.latent;
+  if (part == kPartLatent) row_bytes = p.latent_row, at_byte = rope ? p.rope_at + 2 * col : p.latent_fp8 ? col : 2 * col;
+  else if (part == kPartKey) to = p.index, row_bytes = p.index_fp8 ? 128 : 2 * p.D, at_byte = p.index_fp8 ? col : 2 * col;
+  else to = p.kv, row_bytes = 4ll * p.heads * p.dim, at_byte = 2ll * ((part == kPartV ? p.heads : 0) + gi) * p.dim + 2 * col;
+  to += at_byte;
+  src += col * (is_bf16 ? 2 : 4);
   uint4 x[DEEP][W];
 #pragma unroll
   for (int i = 0; i < DEEP; ++i) {
     const int64_t row = row0 + i * p.side + local;
-    if (i < p.deep && local < p.side && row < p.T && col < width && !(p.padded && p.row_pos[row] < 0)) {   // (padding is not read)
+    if (i < p.deep && mine && row < p.T && !(p.padded && p.row_pos[row] < 0)) {   // (padding is not read)
       const uint4 *from = reinterpret_cast<const uint4 *>(src + row * stride);
-      x[i][0] = from[0];
+      x[i][0] = from[0], x[i][1] = from[1];
       if constexpr (kWide)
-        if (type != DSA_BF16) x[i][1] = from[1];
+        if (!is_bf16) x[i][2] = from[2], x[i][3] = from[3];
     }
   }
   for (int r = threadIdx.x; r < rows; r += blockDim.x) {
@@ -217,79 +233,76 @@ __global__ void __launch_bounds__(kAppendThreads) append_pieces_kernel(const App
     // (from the last thread on: the first ones look the pages up)
     for (int k = blockDim.x - 1 - threadIdx.x; k < rows * half; k += blockDim.x) {
       const int r = k / half;
-      if (row0 + r < p.T) angles[k] = rotary_angle(p.row_pos[row0 + r], p.turns[k - r * half], p.amplitude);
+      if (row0 + r < p.T) angles[r * padded(half) + padded(k - r * half)] = rotary_angle(p.row_pos[row0 + r], p.turns[k - r * half], p.amplitude);
     }
   }
   __syncthreads();
+  auto row_of = [&](const int2 place) {
+    return part == kPartKey && p.index_fp8 ? to + static_cast<int64_t>(place.x) * p.P * (128 + 4) + place.y * 128
+                                           : to + (static_cast<int64_t>(place.x) * p.P + place.y) * row_bytes;
+  };
 #pragma unroll
   for (int i = 0; i < DEEP; ++i) {
     if (i >= p.deep) break;      // uniform
-    float v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = 0.f;
     const int r = i * p.side + local;
-    const int2 place = local < p.side ? where[r] : make_int2(-1, 0);
-    const bool in = col < width && place.x >= 0;
-    if (in) {
-      if (type == DSA_BF16) {
-        unpack8(v, x[i][0]);
-      } else if constexpr (kWide) {
+    const int2 place = mine ? where[r] : make_int2(-1, 0);
+    const bool in = place.x >= 0;
+    if (!__any_sync(0xffffffffu, in && (turns || codes || !is_bf16))) {      // copied as it is
+      if (in) {
+        uint4 *out = reinterpret_cast<uint4 *>(row_of(place));
+        out[0] = x[i][0], out[1] = x[i][1];
+      }
+      continue;
+    }
+    float v[N];
+    if (!in) {
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          v[4 * w] = __uint_as_float(x[i][w].x), v[4 * w + 1] = __uint_as_float(x[i][w].y);
-          v[4 * w + 2] = __uint_as_float(x[i][w].z), v[4 * w + 3] = __uint_as_float(x[i][w].w);
-        }
+      for (int k = 0; k < N; ++k) v[k] = 0.f;
+    } else if (is_bf16) {
+      unpack8(*reinterpret_cast<float(*)[8]>(v), x[i][0]);
+      unpack8(*reinterpret_cast<float(*)[8]>(v + 8), x[i][1]);
+    } else if constexpr (kWide) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        v[4 * w] = __uint_as_float(x[i][w].x), v[4 * w + 1] = __uint_as_float(x[i][w].y);
+        v[4 * w + 2] = __uint_as_float(x[i][w].z), v[4 * w + 3] = __uint_as_float(x[i][w].w);
       }
     }
     if (p.rot) {
-      const int half = p.rot / 2;
-      const bool turns = rot > 0 && in && col >= offset && col < offset + rot;
-      const float2 *cs = angles + r * half;
-      if (turns && layout == DSA_ROTARY_INTERLEAVED) rotate_interleaved(v, cs + (col - offset) / 2);
-      if (p.halves) {      // (all lanes take part in the exchange)
-        const bool mine = turns && layout == DSA_ROTARY_HALF, second = col - offset >= half;
-        const int from = mine ? lane + (second ? -half / 8 : half / 8) : lane;
-        float other[8];
+      const int half = p.rot / 2, q = layout == DSA_ROTARY_HALF ? col - offset - (second ? half : 0) : (col - offset) / 2;
+      const float2 *cs = angles + r * padded(half) + padded(q);
+      if (turns && layout == DSA_ROTARY_INTERLEAVED) rotate_interleaved(v, cs);
+      if (halves) {      // (all lanes of the warp take part in the exchange)
+        const bool exchange = turns && layout == DSA_ROTARY_HALF;
+        const int from = exchange ? lane + (second ? -1 : 1) * (half / N) : lane;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) other[k] = __shfl_sync(0xffffffffu, v[k], from, 16);
-        if (mine) {
-          const float2 *w = cs + (col - offset) - (second ? half : 0);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            v[k] = second ? fmaf(other[k], w[k].y, v[k] * w[k].x) : fmaf(v[k], w[k].x, -other[k] * w[k].y);
+        for (int k = 0; k < N; ++k) {
+          const float other = __shfl_sync(0xffffffffu, v[k], from, kGroupLanes);
+          if (exchange) v[k] = fmaf(v[k], cs[k].x, second ? other * cs[k].y : -other * cs[k].y);
         }
       }
     }
     uint32_t m = 0;
-    if (p.latent_fp8 || p.index_fp8) {
-      m = amax_bits8(v);
+    if (any_codes) {
+      m = max(amax_bits8(*reinterpret_cast<float(*)[8]>(v)), amax_bits8(*reinterpret_cast<float(*)[8]>(v + 8)));
 #pragma unroll
-      for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));   // the group's 16 lanes
+      for (int o = kGroupLanes / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));   // the group's lanes
     }
     if (!in) continue;
-    const int64_t at = static_cast<int64_t>(place.x) * p.P + place.y;
-    if ((part == kPartLatent && !rope && p.latent_fp8) || (part == kPartKey && p.index_fp8)) {
+    char *out = row_of(place);
+    if (codes) {
       const GroupScale g(m);
-      uint8_t *codes;
-      float *scale;
-      if (part == kPartLatent) {
-        char *out = p.latent + at * p.latent_row;
-        codes = reinterpret_cast<uint8_t *>(out) + col;
-        scale = reinterpret_cast<float *>(out + p.L) + base / 128;
-      } else {
-        char *out = p.index + static_cast<int64_t>(place.x) * p.P * (128 + 4);
-        codes = reinterpret_cast<uint8_t *>(out) + place.y * 128 + col;
-        scale = reinterpret_cast<float *>(out + static_cast<int64_t>(p.P) * 128) + place.y;
-      }
-      *reinterpret_cast<uint2 *>(codes) = codes8(v, g);
-      if (lane == 0) *scale = g.scale;
-      continue;
+      const uint2 a = codes8(*reinterpret_cast<float(*)[8]>(v), g), b = codes8(*reinterpret_cast<float(*)[8]>(v + 8), g);
+      *reinterpret_cast<uint2 *>(out) = a;
+      *reinterpret_cast<uint2 *>(out + 8) = b;
+      if (lane == 0)
+        *(part == kPartLatent ? reinterpret_cast<float *>(out - col + p.L) + base / 128
+                              : reinterpret_cast<float *>(p.index + static_cast<int64_t>(place.x) * p.P * (128 + 4) +
+                                                          static_cast<int64_t>(p.P) * 128) + place.y) = g.scale;
+    } else {
+      store8(out, DSA_BF16, 0, 8, true, *reinterpret_cast<float(*)[8]>(v));
+      store8(out, DSA_BF16, 8, 16, true, *reinterpret_cast<float(*)[8]>(v + 8));
     }
-    char *out;
-    if (part == kPartLatent) out = p.latent + at * p.latent_row + (rope ? p.rope_at : 0);
-    else if (part == kPartKey) out = p.index + at * p.D * 2;
-    else out = p.kv + (at * 2 * p.heads + (part == kPartV ? p.heads : 0) + gi) * p.dim * 2;
-    store8(out, DSA_BF16, col, width, true, v);
   }
 }
 
@@ -321,34 +334,46 @@ void append_keys(const dsa_ctx *ctx, AppendParams &p, const dsa_append_t &a, con
   p.index_vec = whole && on16(index_cache, p.D * 2);
 }
 
-// Whether append_pieces_kernel takes the call: whole pieces, and pairs of them within a group of 16 lanes.
-bool whole_pieces(const AppendParams &p) {
-  if (p.c && (!p.c_vec || p.L % 8 || !p.latent_vec || p.R > 128 || p.R % 8 || (p.R > 0 && (!p.k_pe_vec || !p.rope_vec))))
+// Whether append_runs_kernel takes the call: whole runs of 16 columns, and pairs of them within a group of lanes.
+bool whole_runs(const AppendParams &p) {
+  auto turned = [&](int offset, int layout) {
+    return offset % kLaneCols == 0 && p.rot % (layout == DSA_ROTARY_HALF ? 2 * kLaneCols : kLaneCols) == 0;
+  };
+  if (p.c && (!p.c_vec || p.L % kLaneCols || !p.latent_vec || p.R > 128 || p.R % kLaneCols ||
+              (p.R > 0 && (!p.k_pe_vec || !p.rope_vec || !turned(0, p.layout)))))
     return false;
-  if (p.keys && (!p.keys_vec || p.D > 128 || p.D % 8 || (p.index_fp8 ? reinterpret_cast<uintptr_t>(p.index) % 8 || p.P % 2 : !p.index_vec)))
+  if (p.keys && (!p.keys_vec || p.D > 128 || p.D % kLaneCols || !turned(p.key_offset, p.key_layout) ||
+                 (p.index_fp8 ? reinterpret_cast<uintptr_t>(p.index) % 8 || p.P % 2 : !p.index_vec)))
     return false;
-  if (p.k && (!p.k_vec || !p.v_vec || !p.kv_vec || p.dim > 128 || p.dim % 8)) return false;
+  if (p.k && (!p.k_vec || !p.v_vec || !p.kv_vec || p.dim > 128 || p.dim % kLaneCols || !turned(p.rot ? p.kv_offset : 0, p.kv_layout)))
+    return false;
   return true;
 }
 
 cudaError_t launch_append(const dsa_ctx *ctx, AppendParams &p, cudaStream_t s, int32_t *launches) {
   *launches += 1;
-  p.halves = p.rot && ((p.c && p.layout == DSA_ROTARY_HALF) || (p.keys && p.key_layout == DSA_ROTARY_HALF) ||
-                       (p.k && p.kv_layout == DSA_ROTARY_HALF));
   p.groups = (p.c ? (p.L + 127) / 128 + (p.R > 0 ? 1 : 0) : 0) + (p.keys ? 1 : 0) + (p.k ? 2 * p.heads : 0);
-  if (whole_pieces(p) && p.groups <= kAppendThreads / 16) {
+  if (whole_runs(p) && p.groups <= kAppendThreads / kGroupLanes) {
     const bool wide = (p.c && (p.c_type != DSA_BF16 || (p.R > 0 && p.k_pe_type != DSA_BF16))) || (p.keys && p.key_type != DSA_BF16) ||
                       (p.k && p.kv_type != DSA_BF16);
-    // as many rows side by side as the threads hold, and a thread as deep as leaves two CTAs an SM (and the angles in
-    // 48 KB): one row a CTA for a decode step, eight for a prefill chunk
+    // As many rows side by side as the threads hold, fewer where that leaves SMs without any; and a thread as deep as
+    // takes least by waves of CTAs (80 registers a thread) of some 2.5 us and 0.6 for each of its rows: one row for a
+    // decode step; for 8197 rows of K and V three, 9.2 us (four: 11.1, a second wave of few); for 8192 in 8 bits four,
+    // 9.4 us (three: 10.4).
     const int sms = std::max(1, ctx->num_sms);
-    p.side = std::max(1, std::min(kAppendThreads / 16 / p.groups, p.T / sms));
-    p.deep = std::max(1, std::min(wide ? kAppendDeep<true> : kAppendDeep<false>, p.T / (2 * sms * p.side)));
-    while (p.deep > 1 && p.side * p.deep * (p.rot / 2) * sizeof(float2) > 48 * 1024) --p.deep;
-    const int rows = p.side * p.deep, threads = (p.side * p.groups + 1) / 2 * 32;
-    return launch_overlapped(wide ? append_pieces_kernel<true> : append_pieces_kernel<false>,
+    p.side = std::max(1, std::min(kAppendThreads / kGroupLanes / p.groups, p.T / sms));
+    const int threads = (p.side * p.groups * kGroupLanes + 31) / 32 * 32, at_once = sms * (65536 / (80 * threads));
+    double least = 0.0;
+    for (int deep = 1; deep <= (wide ? kAppendDeep<true> : kAppendDeep<false>); ++deep) {
+      if (p.side * deep * padded(p.rot / 2) * sizeof(float2) > 46 * 1024) break;
+      const int ctas = (p.T + p.side * deep - 1) / (p.side * deep);
+      const double cost = ((ctas + at_once - 1) / at_once) * (2.5 + 0.6 * deep);
+      if (deep == 1 || cost < least) least = cost, p.deep = deep;
+    }
+    const int rows = p.side * p.deep;
+    return launch_overlapped(wide ? append_runs_kernel<true> : append_runs_kernel<false>,
                              dim3(static_cast<unsigned>((p.T + rows - 1) / rows)), threads,
-                             rows * (p.rot / 2) * static_cast<int>(sizeof(float2)), 1, s, p);
+                             rows * padded(p.rot / 2) * static_cast<int>(sizeof(float2)), 1, s, p);
   }
   int floats = p.rot ? rotary_pairs(p.rot) * 2 : 0;
   if (p.keys && p.index_fp8) floats += p.D;
