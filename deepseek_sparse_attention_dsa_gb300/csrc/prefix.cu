@@ -154,29 +154,35 @@ constexpr Cost kPairCost{1.55, 3.0}, kLoneCost{1.2, 1.3};
 constexpr double kLeast = 2.5;      // fewer CTAs rather than less than this for each
 
 // A line of pieces in runs of at most `most` each: a piece that does not fit is cut, unless that would leave a sliver
-// of it in a run that has something already (a cut costs a start).
+// of it in a run that has something already (a cut costs a start).  Returns how many; `out`, where given, gets them.
 template <typename CostOf>
-std::vector<std::vector<Piece>> cut_line(const std::vector<Piece> &line, double most, CostOf cost_of) {
-  std::vector<std::vector<Piece>> out(1);
+int cut_line(const std::vector<Piece> &line, double most, CostOf cost_of, std::vector<std::vector<Piece>> *out = nullptr) {
+  int runs = 1;
   double room = most;
+  bool empty = true;
+  if (out) out->assign(1, {});
+  auto put = [&](const Piece &x) {
+    empty = false;
+    if (out) out->back().push_back(x);
+  };
   for (Piece x : line)
     for (;;) {
       const Cost c = cost_of(x);
       const int32_t n = x.t1 - x.t0;
-      const bool empty = out.back().empty();
       if (n * c.tile + c.start <= room || (empty && n == 1)) {
-        out.back().push_back(x);
+        put(x);
         room -= n * c.tile + c.start;
         break;
       }
       int32_t here = static_cast<int32_t>(std::max(0.0, (room - c.start) / c.tile));
       here = std::min(empty ? std::max(here, 1) : here * c.tile < 0.1 * most ? 0 : here, n - 1);
-      if (here > 0) out.back().push_back(Piece{x.chain, x.t0, x.t0 + here});
+      if (here > 0) put(Piece{x.chain, x.t0, x.t0 + here});
       x.t0 += here;
-      out.emplace_back();
-      room = most;
+      ++runs;
+      room = most, empty = true;
+      if (out) out->emplace_back();
     }
-  return out;
+  return runs;
 }
 
 // Partial results of a tile of queries and a kv head: `count` of them from `first` on (0: its only segment writes
@@ -288,17 +294,16 @@ void lay_out(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, Work &w) {
   line.insert(line.end(), lone.begin(), lone.end());
   // the least that a CTA can be given so that n of them do
   auto cost_of = [&](const Piece &x) { return w.chains[x.chain].tile[1] >= 0 ? kPairCost : kLoneCost; };
-  double low = std::max(cost / n, kLeast), high = 2.0 * low + kPairCost.start + kPairCost.tile;
-  auto runs = cut_line(line, low, cost_of);
-  if (static_cast<int>(runs.size()) > n) {
-    while (static_cast<int>((runs = cut_line(line, high, cost_of)).size()) > n) high *= 1.5;
-    for (int i = 0; i < 10; ++i) {
+  double low = std::max(cost / n, kLeast), high = low;
+  if (cut_line(line, low, cost_of) > n) {
+    while (cut_line(line, high, cost_of) > n) high *= 1.25;
+    for (int i = 0; i < 8; ++i) {
       const double mid = 0.5 * (low + high);
-      auto r = cut_line(line, mid, cost_of);
-      if (static_cast<int>(r.size()) <= n) high = mid, runs = std::move(r);
-      else low = mid;
+      (cut_line(line, mid, cost_of) <= n ? high : low) = mid;
     }
   }
+  std::vector<std::vector<Piece>> runs;
+  cut_line(line, high, cost_of, &runs);
   // neighbours share a TPC where there are more of them than TPCs (launched as clusters of two): lone tiles beside
   // pairs, both wait longer for their loads
   pp->paired = static_cast<int>(runs.size()) > n / 2;
@@ -522,6 +527,9 @@ dsa_status dsa_prefix_attend(dsa_ctx_t *ctx, const dsa_prefix_plan_t *pp, const 
   if (pp->plan->T == 0) return DSA_OK;
   auto on16 = [](const void *p) { return p && reinterpret_cast<uintptr_t>(p) % 16 == 0; };
   if (!on16(q) || !on16(kv_cache) || !on16(out)) return DSA_ERR_INVALID_ARG;
+  const uintptr_t from = reinterpret_cast<uintptr_t>(q), to = reinterpret_cast<uintptr_t>(out),
+                  bytes = static_cast<uintptr_t>(pp->plan->T) * pp->shape.q_heads * pp->shape.head_dim * 2;
+  if (from < to + bytes && to < from + bytes) return DSA_ERR_INVALID_ARG;   // a row's queries may be read after another's output
   return cuda_status(ctx, launch_prefix_attend(ctx, pp, q, kv_cache, sm_scale, out, reinterpret_cast<cudaStream_t>(stream),
                                                &launched.n));
 }

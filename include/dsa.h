@@ -624,8 +624,11 @@ dsa_status dsa_append_kv(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_rotar
  * a run growing while that lowers the tokens read.  0: nothing is shared.
  * Host work, then one host-to-device copy on `stream`, as dsa_plan; made once a
  * step and used for every layer of it.  It keeps pointing at `plan`, which must
- * outlive it, and owns the scratch of its calls: calls with one prefix plan are
- * ordered one after another (also two captured graphs of them).  Of `shape` the
+ * outlive it, and owns the scratch of its calls (partial results in fp32: up to some
+ * rows x q_heads x (head_dim + 2) x 4 bytes for each part that a row's keys are cut
+ * into, two and more behind a shared prefix): calls with one prefix plan must come
+ * one after another (also two captured graphs of them); two plans of the same spans
+ * may run at once.  Of `shape` the
  * fields q_heads, kv_heads and head_dim are read.  A context of device -1 makes the
  * plan without a device copy.
  * DSA_ERR_INVALID_ARG: null pointers, a plan of another context, q_heads not a
@@ -636,7 +639,8 @@ dsa_status dsa_append_kv(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_rotar
  * dsa_prefix_attend (sm_scale above 0): q (T, q_heads, head_dim) bf16, kv_cache as dsa_msa_attend's
  * with this step's rows in place (dsa_append_kv), out (T, q_heads, head_dim) bf16;
  * sums, maxima and logits in fp32, probabilities rounded to bf16 on the tensor
- * cores.  Each on 16 bytes.  Cache rows that no row of the call sees may
+ * cores.  Each on 16 bytes; out must not overlap q (DSA_ERR_INVALID_ARG).  Logits have
+ * fp32's range.  Cache rows that no row of the call sees may
  * hold anything; keys and values that some row sees must be finite for all rows
  * of that span.  Equal calls with one plan give equal bits.  A page id outside the
  * cache cannot occur (dsa_plan checks them). */

@@ -125,6 +125,99 @@ def test_groups_of_rows(contexts, rows, new, shared, own):
     check(ctx, spans, pages, shape(8, 1), q, kv, found=None if rows > 1 else 0)
 
 
+@pytest.mark.parametrize("q_heads,kv_heads,dim", [(16, 1, 64), (40, 1, 128), (128, 1, 64), (12, 4, 128)])
+def test_groups_of_rows_of_other_heads(contexts, q_heads, kv_heads, dim):
+    """Tiles of 8, 3, 1 and 42 rows: pairs, lone ones of more and of fewer than 64 lanes, in one plan."""
+    ctx = contexts()
+    requests = [(256 + i, 1) for i in range(21)] + [(300, 2), (310, 3), (256, 9), (700, 70)]
+    spans, pages = batch(30, 64, requests, 4)
+    q, kv = inputs(31, spans, pages, 64, q_heads, kv_heads, dim)
+    check(ctx, spans, pages, shape(q_heads, kv_heads, dim), q, kv, found=1)
+
+
+def test_a_row_of_many_parts(contexts):
+    """One row's keys over every SM: more partial results than the join takes at once."""
+    ctx = contexts()
+    spans, pages = batch(32, 64, [(60011, 1)])
+    q, kv = inputs(33, spans, pages, 64, 4, 1, 128)
+    check(ctx, spans, pages, shape(4, 1), q, kv, found=0)
+
+
+def test_a_row_that_is_not_finite_stays_alone(contexts):
+    """NaN and infinities in one row's queries, and in one request's own keys, reach no other row."""
+    ctx = contexts()
+    spans, pages = batch(34, 64, [(320 + i, 1) for i in range(12)], 5)
+    q, kv = inputs(35, spans, pages, 64, 16, 2, 128)
+    want, _ = attend(ctx, spans, pages, shape(16, 2), q, kv)
+    q[3] = float("nan")
+    q[7, 5, 100] = float("inf")
+    own = spans[9].pages[5]                                   # the first page behind the shared ones
+    kv[own, 0] = float("nan")
+    got, _ = attend(ctx, spans, pages, shape(16, 2), q, kv)
+    touched = torch.zeros(12, 16, dtype=torch.bool)
+    touched[3] = touched[9] = touched[7, 5] = True
+    assert torch.equal(got[~touched.cuda()], want[~touched.cuda()])
+    assert torch.isnan(got[touched.cuda()]).all()
+
+
+def test_long_caches(contexts):
+    """Pages whose rows lie past 2^31 elements (and 2^32 bytes) of the cache."""
+    ctx = contexts()
+    pages = 2 ** 31 // (64 * 1024) + 40
+    kv = torch.zeros(pages, 64, 1024, dtype=BF16, device="cuda")
+    used = np.arange(pages - 12, pages, dtype=np.int32)
+    spans = [W.Span(0, 0, 1, 200, used[[3, 1, 7, 5]]), W.Span(1, 1, 2, 210, used[[3, 1, 7, 0]])]
+    q, small = inputs(36, [W.Span(0, s.q_start, s.q_len, s.ctx_start, s.pages - (pages - 12)) for s in spans], 12, 64, 16, 4, 128)
+    kv[pages - 12:] = small.cuda()
+    msa = shape(16, 4)
+    plan = ctx.plan(spans, pages)
+    pp = ctx.plan_prefix(plan, msa)
+    out = ctx.prefix_attend(pp, q.cuda(), kv)
+    ctx.get_error()
+    near = [W.Span(0, s.q_start, s.q_len, s.ctx_start, s.pages - (pages - 12)) for s in spans]
+    ref.check_attend(out, ref.prefix_attend(near, 64, q, small, 4, msa.sm_scale), 128, 212, pp.on_tensor_cores)
+
+
+def test_two_plans_at_once(contexts):
+    """Two plans of the same spans have scratch of their own: calls on two streams, also captured as a fork and a join."""
+    ctx = contexts()
+    spans, pages = batch(37, 64, [(1280 + i, 1) for i in range(16)], 20)
+    q, kv = inputs(38, spans, pages, 64, 64, 4, 128)
+    msa = shape(64, 4)
+    plan = ctx.plan(spans, pages)
+    plans = [ctx.plan_prefix(plan, msa) for _ in range(2)]
+    kv = kv.cuda()
+    qs = [q.cuda(), torch.randn(q.shape, generator=torch.Generator().manual_seed(39)).to(BF16).cuda()]
+    want = [ctx.prefix_attend(p, x, kv) for p, x in zip(plans, qs)]
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = [torch.zeros_like(w) for w in want]
+
+    def both():
+        fork, join = torch.cuda.Event(), torch.cuda.Event()
+        fork.record(main)
+        side.wait_event(fork)
+        for _ in range(3):
+            ctx.prefix_attend(plans[0], qs[0], kv, out=outs[0], stream=main)
+            ctx.prefix_attend(plans[1], qs[1], kv, out=outs[1], stream=side)
+        join.record(side)
+        main.wait_event(join)
+    with torch.cuda.stream(main):
+        both()
+        main.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+            o.zero_()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=main):
+            both()
+    graph.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+    ctx.get_error()
+
+
 def test_several_prefixes(contexts):
     """Three runs of requests and two lone ones in one step, of unlike lengths."""
     ctx = contexts()
@@ -213,7 +306,7 @@ def test_no_rows_and_refusals(contexts):
     q = torch.zeros(1, 8, 128, dtype=BF16, device="cuda")
     off = torch.zeros(8 * 128 + 1, dtype=BF16, device="cuda")[1:].view(1, 8, 128)
     for bad in (lambda: ctx.prefix_attend(pp, off, kv), lambda: ctx.prefix_attend(pp, q, kv, out=off), lambda: ctx.prefix_attend(pp, q, kv, sm_scale=float("nan")),
-                lambda: ctx.prefix_attend(pp, q, kv, sm_scale=-1.0),
+                lambda: ctx.prefix_attend(pp, q, kv, out=q), lambda: ctx.prefix_attend(pp, q, kv, sm_scale=-1.0),
                 lambda: ctx.prefix_attend(pp, q, kv, sm_scale=0.0)):
         with pytest.raises(dsa.DSAError) as e:
             bad()
@@ -281,3 +374,42 @@ def test_a_layer_of_appends_and_attention(contexts):
         known[i] = known["prompt"]
     assert step([(i, 192, 5 + i, np.concatenate((prompt, own[i]))) for i in range(3)]) == 1
     assert step([(i, 197 + i, 1, np.concatenate((prompt, own[i]))) for i in range(3)]) == 1
+
+
+def test_a_captured_layer(contexts):
+    """Rotation, append and attention in one graph, replayed over new rows in the same buffers."""
+    ctx = contexts()
+    msa, table = shape(64, 4), ctx.rotary_table(128)
+    spans, pages = batch(40, 64, [(640 + 3 * i, 1) for i in range(9)], 10)
+    plan = ctx.plan(spans, pages)
+    pp = ctx.plan_prefix(plan, msa)
+    _, kv0 = inputs(41, spans, pages, 64, 64, 4, 128)
+    kv = kv0.cuda()
+    q, k, v = (torch.zeros(9, h, 128, dtype=BF16, device="cuda") for h in (64, 4, 4))
+    rq, out = torch.zeros_like(q), torch.zeros_like(q)
+
+    def layer():
+        ctx.rotary(table, q, plan, layout="half", out=rq)
+        ctx.append_kv(plan, msa, table, k, v, kv, layout="half")
+        ctx.prefix_attend(pp, rq, kv, out=out)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            layer()
+            layer()
+    torch.cuda.synchronize()
+    for seed in (1, 2):
+        g = torch.Generator().manual_seed(seed)
+        for t in (q, k, v):
+            t.copy_(torch.randn(t.shape, generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        kv2 = kv0.cuda()
+        rq2 = ctx.rotary(table, q, plan, layout="half")
+        ctx.append_kv(plan, msa, table, k, v, kv2, layout="half")
+        assert torch.equal(got, ctx.prefix_attend(pp, rq2, kv2)) and torch.equal(torch.nan_to_num(kv), torch.nan_to_num(kv2))
+    ctx.get_error()
