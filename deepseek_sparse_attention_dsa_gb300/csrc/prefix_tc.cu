@@ -40,10 +40,28 @@ __device__ __forceinline__ float exp2_approx(float x) {   // (relative error 2^-
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void st_global8(float *p, const float *v) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
-               "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+__device__ __forceinline__ void st_global8(void *p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
+}
+// Four lanes' 128 bytes each, from a row a lane to the same quarter of four rows: b[i] is then this lane's 32 bytes
+// of the i-th lane's row, so that a store of them fills whole lines.  (A lane a row, each store of a warp touched 32
+// lines, and a pair's 128 KB of partial results took some 3 us.)
+__device__ __forceinline__ void across_quad(uint32_t (&b)[4][8]) {
+#pragma unroll
+  for (int d = 1; d <= 2; d <<= 1) {
+    const bool upper = lane_id() & d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & d) continue;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? b[i][k] : b[i | d][k], d);
+        (upper ? b[i][k] : b[i | d][k]) = got;
+      }
+    }
+  }
 }
 
 struct PrefixParams {
@@ -425,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
       const int limit = s.causal ? s.limit[tile] + own_row : s.hi;
       const int least = s.causal ? s.limit[tile] : s.hi;   // every lane sees the slots below
       const int n = s.ntiles, lo = s.lo, hi = s.hi, slot0 = s.slot0, part = s.part[tile], lanes = s.lanes[tile];
-      const int64_t out_row = (static_cast<int64_t>(s.row[tile]) + own_row) * p.Hq + s.g * p.group + own_head;
+      const int out_row = (s.row[tile] + own_row) * p.Hq + s.g * p.group + own_head;   // (rows x heads are below 2^31)
       if (n_seg + 1 < n_a + n_b) prefetch_seg(seg_at(n_seg + 1));
       // a warp without live lanes leaves P as it is (what comes of it stays in dead lanes of O) and only keeps step
       const bool dead = (warp & 3) * 32 >= lanes;
@@ -553,31 +571,71 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
       if (!ok) break;
       done += n;
       tc_fence_after();
-      if (!dead) {
-        const bool live = i < lanes;
-        const float scale = part < 0 ? 1.f / l : 1.f;
-        float *to = p.part_o + (static_cast<int64_t>(part) + i) * D;
-        __nv_bfloat16 *out = p.out + out_row * D;
+      // Many rows: whole lines, for some 300 shuffles; few: a row a lane, which is over sooner (4 rows behind 1024 tokens
+      // 7.3 us against 8.0).
+      if (lanes > kPrefixTile / 2) {
+        if (!dead) {
+          const float scale = part < 0 ? 1.f / l : 1.f;
+          const int quad = i & ~3, quarter = lane & 3;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 64) {
-          float o[64];
-          tmem_ld32(t_o + c, *reinterpret_cast<float(*)[32]>(o));
-          tmem_ld32(t_o + c + 32, *reinterpret_cast<float(*)[32]>(o + 32));
-          tmem_ld_wait();
-          if (live && part < 0) {
+          for (int c = 0; c < D; c += 64) {
+            float o[64];
+            tmem_ld32(t_o + c, *reinterpret_cast<float(*)[32]>(o));
+            tmem_ld32(t_o + c + 32, *reinterpret_cast<float(*)[32]>(o + 32));
+            tmem_ld_wait();
+            uint32_t b[4][8];
+            if (part < 0) {
 #pragma unroll
-            for (int k = 0; k < 64; k += 8)
-              *reinterpret_cast<uint4 *>(out + c + k) =
+              for (int k = 0; k < 32; ++k) b[k / 8][k % 8] = pack_bf16(o[2 * k] * scale, o[2 * k + 1] * scale);
+              across_quad(b);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const int to = __shfl_sync(0xffffffffu, out_row, (lane & ~3) + r);
+                if (quad + r < lanes) {      // (the output is on 16 bytes)
+                  uint4 *at = reinterpret_cast<uint4 *>(p.out + static_cast<int64_t>(to) * D + c + quarter * 16);
+                  at[0] = make_uint4(b[r][0], b[r][1], b[r][2], b[r][3]);
+                  at[1] = make_uint4(b[r][4], b[r][5], b[r][6], b[r][7]);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) b[k / 8][k % 8] = __float_as_uint(o[h * 32 + k]);
+                across_quad(b);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  if (quad + r < lanes) st_global8(p.part_o + (static_cast<int64_t>(part) + quad + r) * D + c + h * 32 + quarter * 8, b[r]);
+              }
+            }
+          }
+        }
+      } else if (!dead) {
+        const float scale = part < 0 ? 1.f / l : 1.f;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(t_o + c, o);
+          tmem_ld_wait();
+          if (i < lanes && part < 0) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8)
+              *reinterpret_cast<uint4 *>(p.out + static_cast<int64_t>(out_row) * D + c + k) =
                   make_uint4(pack_bf16(o[k] * scale, o[k + 1] * scale), pack_bf16(o[k + 2] * scale, o[k + 3] * scale),
                              pack_bf16(o[k + 4] * scale, o[k + 5] * scale), pack_bf16(o[k + 6] * scale, o[k + 7] * scale));
-          } else if (live) {
+          } else if (i < lanes) {
 #pragma unroll
-            for (int k = 0; k < 64; k += 8) st_global8(to + c + k, o + k);
+            for (int k = 0; k < 32; k += 8) {
+              uint32_t b[8];
+#pragma unroll
+              for (int u = 0; u < 8; ++u) b[u] = __float_as_uint(o[k + u]);
+              st_global8(p.part_o + (static_cast<int64_t>(part) + i) * D + c + k, b);
+            }
           }
           __syncwarp();
         }
-        if (live && part >= 0) p.part_ml[part + i] = make_float2(m, l);
       }
+      if (!dead && part >= 0 && i < lanes) p.part_ml[part + i] = make_float2(m, l);
       tc_fence_before();   // (O is read: the stream's next products into it follow its next arrival)
     }
   }
