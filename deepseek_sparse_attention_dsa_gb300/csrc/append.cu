@@ -102,7 +102,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
       for (int col = lane * 8; col < p.L; col += 256) copy8(c, p.c_type, p.c_vec, out, p.latent_vec, col, p.L);
     }
     char *rope = out + p.rope_at;
-    const int n = p.rot ? rotary_units(p.rot, p.layout) : (p.R + 7) / 8;   // (rot is R, or 0: all copies)
+    // (a table's rot is R, or R is 0 and it is the key's; without one the columns are copied)
+    const int n = p.R == 0 ? 0 : p.rot ? rotary_units(p.rot, p.layout) : (p.R + 7) / 8;
     for (int u = lane; u < n; u += 32)
       rotary_unit(u, p.rot, p.layout, 0, p.R, cs, k_pe, p.k_pe_type, p.k_pe_vec, rope, DSA_BF16, p.rope_vec);
   } else if (part == kPartKey) {

@@ -168,6 +168,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
     tma_prefetch_desc(&p.tm_q);
     tma_prefetch_desc(&p.tm_q_small);
   }
+  // (No kernel before, launched early as this one is, can still have to take its own tensor memory on this SM: those
+  // that use it leave too little shared memory for this CTA.)
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();

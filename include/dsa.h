@@ -658,6 +658,7 @@ typedef struct dsa_prefix_info {
 } dsa_prefix_info_t;
 dsa_status dsa_prefix_plan(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_msa_shape_t *shape, const dsa_prefix_t *prefixes,
                            int32_t num_prefixes, dsa_stream_t stream, dsa_prefix_plan_t **out);
+/* Frees the plan's tables and scratch in order on its stream. */
 void dsa_prefix_plan_destroy(dsa_prefix_plan_t *pp);
 dsa_status dsa_prefix_plan_get_info(const dsa_prefix_plan_t *pp, dsa_prefix_info_t *info);
 dsa_status dsa_prefix_attend(dsa_ctx_t *ctx, const dsa_prefix_plan_t *pp, const void *q, const void *kv_cache, float sm_scale,

@@ -290,6 +290,38 @@ def test_append_latents(contexts, page, start, fp8, dtype, layout, key_layout, a
     assert ((got - ky).abs() <= bound).all()
 
 
+@pytest.mark.parametrize("lora,rope,dim,rot", [(512, 0, 128, 64), (256, 16, 64, 16), (136, 8, 128, 8), (64, 32, 64, 32), (512, 64, 128, 64)])
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("turned", [True, False])
+def test_append_widths(contexts, lora, rope, dim, rot, aligned, turned):
+    """Other widths of the caches' rows, down to no rope at all (the table is the key's alone then)."""
+    c = contexts(kv_lora_rank=lora, rope_dim=rope, index_dim=dim)
+    spans, pages = spans_for(64, 3)
+    plan = c.plan(spans, pages)
+    T = plan.num_rows
+    table = c.rotary_table(rot) if turned else None
+    stride = (lambda n: None) if aligned else (lambda n: n + 3)
+    lat, keys = rand(1, T, lora, stride=stride(lora)), rand(3, T, dim, stride=stride(dim))
+    k_pe = rand(2, T, rope, stride=stride(rope)) if rope else None
+    where, pos = ref.slots(spans, 64)
+    lc = torch.full((pages, 64, lora + rope), 9.0, dtype=BF16, device="cuda")
+    ic = torch.full((pages, 64, dim), 9.0, dtype=BF16, device="cuda")
+    c.append_latents(plan, table, lat, k_pe, lc, keys, ic, layout="half", key_layout="interleaved", key_offset=dim - rot)
+    c.get_error()
+    l, i = lc.view(-1, lora + rope).cpu(), ic.view(-1, dim).cpu()
+    others = np.setdiff1d(np.arange(pages * 64), where)
+    assert torch.equal(l[where][:, :lora], lat.cpu()) and bool((l[others] == 9.0).all()) and bool((i[others] == 9.0).all())
+    pt, freqs = torch.from_numpy(pos).to(torch.int32), ref.frequencies(rot)
+    for x, got, offset, layout in ((k_pe, l[where][:, lora:], 0, "half"), (keys, i[where], dim - rot, "interleaved")):
+        if x is None:
+            continue
+        if not turned:
+            assert torch.equal(got, x.cpu())
+            continue
+        y, mag = ref.rotate(x[:, None], pt, freqs, offset, layout)
+        ref.close(got, y[:, 0], ref.rotate_bound(x[:, None], y, mag, offset, rot, layout)[:, 0], BF16)
+
+
 @pytest.mark.parametrize("page", [64, 16])
 def test_append_without_a_table_is_the_store(contexts, page):
     """Unrotated bf16 rows: byte for byte what the stores write."""
