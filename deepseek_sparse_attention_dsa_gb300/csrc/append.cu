@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_runs_kernel(const Appen
 #pragma unroll
         for (int k = 0; k < N; ++k) {
           const float other = __shfl_sync(0xffffffffu, v[k], from, kGroupLanes);
-          if (exchange) v[k] = second ? fmaf(other, cs[k].y, v[k] * cs[k].x) : fmaf(v[k], cs[k].x, -other * cs[k].y);   // (as rotate_half)
+          if (exchange) v[k] = fmaf(v[k], cs[k].x, second ? other * cs[k].y : -other * cs[k].y);   // (as rotate_half, bit for bit)
         }
       }
     }

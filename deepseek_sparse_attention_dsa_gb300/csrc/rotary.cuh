@@ -59,7 +59,7 @@ __device__ __forceinline__ void rotate_half(float (&a)[N], float (&b)[N], const 
     const float2 w = cs[i];
     const float x = a[i], y = b[i];
     a[i] = fmaf(x, w.x, -y * w.y);
-    b[i] = fmaf(x, w.y, y * w.x);
+    b[i] = fmaf(y, w.x, x * w.y);
   }
 }
 
