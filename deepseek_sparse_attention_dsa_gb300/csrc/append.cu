@@ -149,8 +149,12 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
 // latent, its rope, an index key, a head of K or V.  A thread has one run of each of several rows: they are on their
 // way, packed, while positions and pages are looked up and angles made, once for all of a row's groups.  The other
 // column of a pair comes from a neighbouring lane, a group's maximum from its eight.  p.groups a row, p.side rows beside one
-// another in a CTA and p.deep of them in a thread.  kWide: some source is fp32.  (Bound by its instructions and by the way
-// from one look-up to the next: with 8 columns a lane, twice the threads, 8192 rows took 11.8 us in 8 bits.)
+// another in a CTA and p.deep of them in a thread; neighbouring groups are the same part of neighbouring rows, so that a
+// warp copies, turns or quantises and seldom does several of these (by rows: 9.3 us in place of 8.5).  kWide: some source
+// is fp32.
+// Bound by its instructions and by the way from one look-up to the next (launch, position, page, row: 2.6 us for 128 rows):
+// 8192 rows into 8 bits take 8.5 us, 2.1 TB/s, with the sources in L2; 8197 rows of keys and values, 4 heads of 128 each,
+// 9.3 us, 3.6 TB/s, and 11.4 from memory.  (With 8 columns a lane, twice the threads, 8192 rows took 2.4 us more.)
 constexpr int kAppendThreads = 256;
 constexpr int kLaneCols = 16, kGroupLanes = 128 / kLaneCols;
 template <bool kWide>
@@ -165,9 +169,9 @@ __global__ void __launch_bounds__(kAppendThreads) append_runs_kernel(const Appen
   extern __shared__ float2 angles[];   // [rows of the CTA][padded(rot / 2)]
   __shared__ int2 where[kAppendRows];  // of the CTA's rows: page (-1: nothing to write), slot in it
   grid_dependency();
-  const int group = threadIdx.x / kGroupLanes, lane = threadIdx.x % kGroupLanes, local = group / p.groups, rows = p.side * p.deep;
+  const int group = threadIdx.x / kGroupLanes, lane = threadIdx.x % kGroupLanes, local = group % p.side, rows = p.side * p.deep;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * rows;
-  int gi = group - local * p.groups, part = kPartLatent, base = 0;
+  int gi = group / p.side, part = kPartLatent, base = 0;
   // the group's part of the row: latents (kv_lora_rank / 128 groups and the rope's), key, heads of K, heads of V
   int width = 0, type = DSA_BF16, rot = 0, layout = 0, offset = 0;
   int64_t stride = 0;
@@ -190,7 +194,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_runs_kernel(const Appen
     if (part == kPartK) rot = p.rot, layout = p.kv_layout, offset = p.kv_offset;
   }
   const int col = base + lane * N;
-  const bool mine = local < p.side && col < width, is_bf16 = !kWide || type == DSA_BF16;
+  const bool mine = group < p.side * p.groups && col < width, is_bf16 = !kWide || type == DSA_BF16;
   const bool codes = (part == kPartLatent && !rope && p.latent_fp8) || (part == kPartKey && p.index_fp8);
   const bool turns = rot > 0 && mine && col >= offset && col < offset + rot, second = turns && col - offset >= rot / 2;
   const bool halves = __any_sync(0xffffffffu, rot > 0 && layout == DSA_ROTARY_HALF);     // (of the warp's groups)
@@ -359,8 +363,8 @@ cudaError_t launch_append(const dsa_ctx *ctx, AppendParams &p, cudaStream_t s, i
                       (p.k && p.kv_type != DSA_BF16);
     // As many rows side by side as the threads hold, fewer where that leaves SMs without any; and a thread as deep as
     // takes least by waves of CTAs (80 registers a thread) of some 2.5 us and 0.6 for each of its rows: one row for a
-    // decode step; for 8197 rows of K and V three, 9.2 us (four: 11.1, a second wave of few); for 8192 in 8 bits four,
-    // 9.4 us (three: 10.4).
+    // decode step; for 8197 rows of K and V three, 9.3 us (four: 11.0, a second wave of few); for 8192 in 8 bits four,
+    // 8.4 us (three: 10.9).
     const int sms = std::max(1, ctx->num_sms);
     p.side = std::max(1, std::min(kAppendThreads / kGroupLanes / p.groups, p.T / sms));
     const int threads = (p.side * p.groups * kGroupLanes + 31) / 32 * 32, at_once = sms * (65536 / (80 * threads));
