@@ -13,8 +13,8 @@
 // is in its softmax the tensor core works for the other.  Two tiles of queries over
 // the same keys are the two streams of a pair (each key tile is loaded once for
 // both); a lone tile's keys are given to the streams of many CTAs instead, each
-// with keys of its own.  Warps 0-3 and 4-7: a stream's softmax; warp 8 loads, by TMA
-// into a ring of half-tiles (K or V of 128 keys); warp 9 issues the products.  A
+// with keys of its own.  Warps 0-3 and 4-7: a stream's softmax; warps 8 and 10 load, by
+// TMA into a ring of half-tiles (K or V of 128 keys); warp 9 issues the products.  A
 // chain that more than one stream worked on leaves partial results, which
 // prefix_join_kernel adds up in a fixed order.
 #include <cuda_bf16.h>
@@ -32,8 +32,8 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 8.0f;        // log2 units that a logit may be above the reference maximum
 constexpr float kNoMax = -3.0e38f;      // the reference maximum of a lane that has seen no key (finite: less -inf it is no NaN)
-constexpr int kThreads = 320;
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 352;
+constexpr int kKeyWarp = 8, kMmaWarp = 9, kValueWarp = 10;
 
 __device__ __forceinline__ float exp2_approx(float x) {   // (relative error 2^-22; 0 for -inf)
   float y;
@@ -99,6 +99,7 @@ struct Cfg {
 
 // Order of the ring's half-tiles.  A pair's key tile i: K, V at 2 i, 2 i + 1 of the phase.  The lone streams'
 // steps t (stream t & 1): K(0), K(1), V(0), K(2), V(1), ... K(n - 1), V(n - 2), V(n - 1), the order of their use.
+__device__ __forceinline__ int lone_k(int t) { return t > 0 ? 2 * t - 1 : 0; }
 __device__ __forceinline__ int lone_v(int t, int n) { return t < n - 1 ? 2 * t + 2 : 2 * n - 1; }
 
 // A place in the ring: its slot, and the parity of that slot's use.
@@ -183,8 +184,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
   const int na = cta.tiles_a, nb = cta.tiles_b;
   const bool small = cta.small != 0;
 
-  if (warp == kLoadWarp) {
+  if (warp == kKeyWarp || warp == kValueWarp) {
     // ------------------------------------------------------------ loads
+    // A warp for the keys (and the queries) and one for the values, each with the ring's places of its own: a half-tile
+    // takes some 1000 cycles of waits, look-ups and issue, and the products of lone tiles are done with two in less.
+    // (Each waits for its slots in the ring's order and less than a round of it apart, which a parity tells.)
+    const bool values = warp == kValueWarp;
     // A lane's box: box lane / CH of the tile, chunk lane % CH; its cache row, or -1
     const int box = lane / C::CH, chunk = lane % C::CH, boxes = kPrefixTile / p.BH;
     // (The page is looked at when the tile is loaded, a step later: the table's latency would hold up every load.  It is
@@ -205,10 +210,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
       return x;
     };
     bool waited = false;      // for the kernels before: the plan's tables are read ahead of that, nothing else
-    int r = 0;
+    int last = -1;            // this warp's last place in the ring
     uint32_t q_loaded = 0, q_odd = 0;      // bit 2 w + b: stream w's buffer b has been loaded; an odd number of times
     bool ok = true;
-    auto load = [&](int x0, int row) {   // the next half-tile of the ring, columns x0 ..
+    auto load = [&](int r, int x0, int row) {   // the ring's half-tile r, columns x0 ..
       if (!waited) grid_dependency_wait();
       waited = true;
       ok = ok && mbar_wait_warp(empty(r), phase(r) ^ 1u, abort_addr, p.err);
@@ -220,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
       }
       __syncwarp();
       if (row >= 0) tma_load_2d(sbase + C::OFF_RING + (r % C::NS) * C::HALF + chunk * C::CHUNK + box * p.BH * 128, &p.tm_kv, x0 + chunk * 64, row, full(r));
-      ++r;
+      last = r;
     };
     // Stream w's queries: of a pair or a large tile into the whole of its buffer, of tiles of up to 64 lanes (`small`)
     // into one half and the other by turns, so that the next ones are there when the last ones are done with.
@@ -249,17 +254,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
         const bool first = k.j == 0;
         k.next();
         if (i + 1 < na) ahead = lookup(k);
-        load(s->g * D, row);
-        if (first) {
+        load(2 * i + values, (values ? p.Hkv + s->g : s->g) * D, row);
+        if (first && !values) {
           load_q(0, s, 0, false, 0);
           load_q(1, s, 1, false, 0);
         }
-        load((p.Hkv + s->g) * D, row);
       }
     }
     if (nb > 0 && ok) {
       Walk k[2];
-      int left[2] = {(nb + 1) / 2, nb / 2}, row_before = -1, g_before = 0;
+      int left[2] = {(nb + 1) / 2, nb / 2};
       Box ahead[2];
       uint32_t turn = 0;      // bit w: the buffer of stream w's next queries
       for (int w = 0; w < 2; ++w)
@@ -268,34 +272,34 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
           ahead[w] = lookup(k[w]);
         }
 #pragma unroll 1
-      for (int t = 0; t <= nb && ok; ++t) {
-        int row = -1, g = 0;
-        if (t < nb) {
+      for (int t0 = 0; t0 < nb && ok; t0 += 2) {
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (w != (t & 1)) continue;
-            const PrefixSeg *s = k[w].seg;
-            const bool first = k[w].j == 0;
-            row = ahead[w].row(p.P), g = s->g;
-            --left[w];
-            k[w].next();
-            if (left[w] > 0) ahead[w] = lookup(k[w]);
-            load(g * D, row);
-            if (first) {
-              prefetch_seg(s + 1);
-              load_q(w, s, 0, small, turn >> w & 1);
-              if (small) turn ^= 1u << w;
-            }
+        for (int w = 0; w < 2; ++w) {
+          const int t = t0 + w;
+          if (t >= nb) break;
+          const PrefixSeg *s = k[w].seg;
+          const bool first = k[w].j == 0;
+          const int row = ahead[w].row(p.P);
+          --left[w];
+          k[w].next();
+          if (left[w] > 0) ahead[w] = lookup(k[w]);
+          load(2 * na + (values ? lone_v(t, nb) : lone_k(t)), (values ? p.Hkv + s->g : s->g) * D, row);
+          if (first && !values) {
+            prefetch_seg(s + 1);
+            load_q(w, s, 0, small, turn >> w & 1);
+            if (small) turn ^= 1u << w;
           }
         }
-        if (t > 0) load((p.Hkv + g_before) * D, row_before);
-        row_before = row, g_before = g;
       }
     }
     // nothing of ours may still be landing when the CTA leaves (an abort apart, all of it has been used)
     if (lane == 0 && !ok) {
       volatile int no_abort = 0;
-      for (int i = max(0, r - C::NS); i < r; ++i) mbar_wait(full(i), phase(i), &no_abort, p.err);
+      for (int r = max(0, last - C::NS + 1); r <= last; ++r) {
+        const int i = r - 2 * na;
+        const bool value = i < 0 ? (r & 1) != 0 : i == 2 * nb - 1 || (i > 0 && i % 2 == 0);   // (of pairs, of lone_v)
+        if (value == values) mbar_wait(full(r), phase(r), &no_abort, p.err);
+      }
       for (int w = 0; w < 2; ++w)
         for (int b = 0; b < 2; ++b)
           if (q_loaded >> (2 * w + b) & 1) mbar_wait(qfull(w, b), (q_odd >> (2 * w + b) & 1) ^ 1, &no_abort, p.err);
