@@ -311,14 +311,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
     // One warp for both streams, so that half-tiles are awaited in the order in which they were asked for (a parity
     // says nothing of a fill two uses away).  The whole warp walks and waits, one elected thread issues: its operands
     // stay in uniform registers.  (Issued by a lane that a branch picked, each of the 16 instructions of a step took
-    // some 80 cycles.)  A wait costs some 200 cycles, met or not: the three that a step begins with are tried
-    // together, and the one between its products has the first half of the first behind it.
+    // some 80 cycles.)  The tensor core holds no more than a few products, so that the issue keeps its pace, and whatever
+    // the warp does between two of them idles it: what the next step needs is looked at, and the walk goes on, ahead of a
+    // step's last products (`peek`); what a step begins with is tried together.
     const uint64_t desc_q0 = smem_desc(sbase, 16, 1024, kSwizzle128), desc_k0 = smem_desc(sbase + C::OFF_RING, 16, 1024, kSwizzle128),
                    desc_v0 = smem_desc(sbase + C::OFF_RING, C::CHUNK, 1024, kSwizzle128);
+    auto slot_full = [&](const Ring<C::NS> &r) { return bar0 + 8u * r.st; };
+    auto slot_empty = [&](const Ring<C::NS> &r) { return bar0 + 8u * (C::NS + r.st); };
     uint32_t q_phase = 0, p_phase = 0;      // bit 2 w + b: stream w's buffer b; bit w: stream w's
     uint32_t turn = 0;                      // bit w: the buffer of stream w's queries
-    bool ok = true;
-    auto qk = [&](int w, const Ring<C::NS> &r, bool first, bool last, bool release, bool halves) {
+    bool ok = true, met = false;            // met: what the next step begins with is there
+    auto nothing = [] {};
+    auto qk = [&](int w, const Ring<C::NS> r, bool first, bool last, bool release, bool halves, auto peek) {
       const uint32_t b = (turn >> w) & 1;
       if (first) {
         ok = ok && mbar_wait_warp(qfull(w, b), (q_phase >> (2 * w + b)) & 1, abort_addr, p.err);
@@ -327,31 +331,48 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
       }
       if (last && halves) turn ^= 1u << w;
       if (!ok) return;
+      const uint64_t q = desc_q0 + (w * C::HALF >> 4) + b * (C::SMALL >> 4), k = desc_k0 + r.st * (C::HALF >> 4);
+      auto product = [&](int n) {
+        const int at = (n >> 2) * (C::CHUNK >> 4) + 2 * (n & 3);
+        mma_f16_ss(tmem + C::S_COL + w * 128, q + at, k + at, C::IDESC_QK, n > 0 ? 1u : 0u);
+      };
+      constexpr int N = 4 * C::CH, BEHIND = 2;   // products, and those behind the peek
       if (elect_one()) {
-        const uint64_t q = desc_q0 + (w * C::HALF >> 4) + b * (C::SMALL >> 4), k = desc_k0 + r.st * (C::HALF >> 4);
 #pragma unroll
-        for (int c = 0; c < C::CH; ++c)
+        for (int n = 0; n < N - BEHIND; ++n) product(n);
+      }
+      __syncwarp();
+      peek();
+      if (elect_one()) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma_f16_ss(tmem + C::S_COL + w * 128, q + c * (C::CHUNK >> 4) + 2 * i, k + c * (C::CHUNK >> 4) + 2 * i, C::IDESC_QK,
-                       (c | i) ? 1u : 0u);
+        for (int n = N - BEHIND; n < N; ++n) product(n);
         mma_commit(sfull(w));
-        if (release) mma_commit(empty(r.st));
+        if (release) mma_commit(slot_empty(r));
         if (last) mma_commit(qempty(w, b));
       }
       __syncwarp();
     };
-    // Stream w's step: O += P V, and behind it (they run in order, and S's columns hold P) the next S of the stream.
-    auto step = [&](int w, const Ring<C::NS> &v, const Walk &kp, const Ring<C::NS> &k, const Walk &kq, bool more, bool release,
-                    bool halves) {
+    // Whether the values, weights and (more) keys that stream w's step begins with are there.
+    auto there = [&](int w, const Ring<C::NS> &v, const Ring<C::NS> &k, bool more) {
       const uint32_t ph = (p_phase >> w) & 1;
+      return more ? mbar_try_warp_three(slot_full(v), v.phase, slot_full(k), k.phase, pfull(w, 0), ph)
+                  : mbar_try_warp_both(slot_full(v), v.phase, pfull(w, 0), ph);
+    };
+    // Stream w's step: O += P V, and behind it (they run in order, and S's columns hold P) the next S of the stream.
+    // peek: walks on and looks at the next step.
+    auto step = [&](int w, const Ring<C::NS> v, const Walk &kp, const Ring<C::NS> k, const Walk &kq, bool more, bool release,
+                    bool halves, auto peek) {
+      const uint32_t ph = (p_phase >> w) & 1;
+      if (!met) {
+        if (more) ok = ok && mbar_wait_warp_three(slot_full(v), v.phase, slot_full(k), k.phase, pfull(w, 0), ph, abort_addr, p.err);
+        else ok = ok && mbar_wait_warp_both(slot_full(v), v.phase, pfull(w, 0), ph, abort_addr, p.err);
+      }
       p_phase ^= 1u << w;
-      if (more) ok = ok && mbar_wait_warp_three(full(v.st), v.phase, full(k.st), k.phase, pfull(w, 0), ph, abort_addr, p.err);
-      else ok = ok && mbar_wait_warp_both(full(v.st), v.phase, pfull(w, 0), ph, abort_addr, p.err);
+      met = false;
       if (!ok) return;
       tc_fence_after();
       const uint64_t vd = desc_v0 + v.st * (C::HALF >> 4);
-      const bool last = kp.j + 1 == kp.n, first = kp.j == 0;
+      const bool last = kp.j + 1 == kp.n, first = kp.j == 0, q_first = kq.j == 0, q_last = kq.j + 1 == kq.n;
       if (elect_one()) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)   // A: 16 keys are 8 columns; B read MN-major: 64-dim chunks CHUNK apart
@@ -366,31 +387,38 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
 #pragma unroll
         for (int i = 4; i < 8; ++i)
           mma_f16_ts(tmem + C::O_COL + w * 128, tmem + C::S_COL + w * 128 + i * 8, vd + i * (16 * 128 >> 4), C::IDESC_PV, 1u);
-        if (release) mma_commit(empty(v.st));
+        if (release) mma_commit(slot_empty(v));
         if (last) mma_commit(ofull(w));
       }
       __syncwarp();
-      if (more) qk(w, k, kq.j == 0, kq.j + 1 == kq.n, release, halves);
+      if (more) qk(w, k, q_first, q_last, release, halves, peek);
+      else peek();
     };
     if (na > 0) {
       Walk kq, kp;
       kq.start(p.segs + cta.a0);
       kp = kq;
       Ring<C::NS> rk(0), rv(1);
-      ok = mbar_wait_warp(full(rk.st), rk.phase, abort_addr, p.err);
+      ok = mbar_wait_warp(slot_full(rk), rk.phase, abort_addr, p.err);
       tc_fence_after();
-      qk(0, rk, true, kq.n == 1, false, false);
-      qk(1, rk, true, kq.n == 1, true, false);
+      qk(0, rk, true, kq.n == 1, false, false, nothing);
+      qk(1, rk, true, kq.n == 1, true, false, nothing);
+      kq.next();
+      rk.skip(2);
 #pragma unroll 1
       for (int i = 0; i < na && ok; ++i) {
         const bool more = i + 1 < na;
-        kq.next();
-        rk.skip(2);
-        step(0, rv, kp, rk, kq, more, false, false);
-        step(1, rv, kp, rk, kq, more, true, false);
-        rv.skip(2);
-        kp.next();
+        step(0, rv, kp, rk, kq, more, false, false, [&] { met = there(1, rv, rk, more); });
+        step(1, rv, kp, rk, kq, more, true, false, [&] {
+          rv.skip(2);
+          kp.next();
+          if (!more) return;
+          kq.next();
+          rk.skip(2);
+          met = there(0, rv, rk, i + 2 < na);
+        });
       }
+      met = false;
     }
     if (nb > 0 && ok) {
       Walk kq[2], kp[2];
@@ -400,9 +428,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
         if (w < nb) {
           kq[w].start(p.segs + cta.b0[w]);
           kp[w] = kq[w];
-          ok = ok && mbar_wait_warp(full(rk.st), rk.phase, abort_addr, p.err);
+          ok = ok && mbar_wait_warp(slot_full(rk), rk.phase, abort_addr, p.err);
           tc_fence_after();
-          qk(w, rk, true, kq[w].n == 1, true, small);
+          qk(w, rk, true, kq[w].n == 1, true, small, nothing);
           kq[w].next();
           rk.skip(w + 1);      // K(0), K(1), then every other half-tile
         }
@@ -413,13 +441,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
           const int u = t + w;
           if (u < nb) {
             const bool more = u + 2 < nb;
-            step(w, rv, kp[w], rk, kq[w], more, true, small);
-            kp[w].next();
-            rv.skip(more ? 2 : 1);
-            if (more) {
-              kq[w].next();
-              rk.skip(2);
-            }
+            step(w, rv, kp[w], rk, kq[w], more, true, small, [&] {
+              kp[w].next();
+              rv.skip(more ? 2 : 1);
+              if (more) {
+                kq[w].next();
+                rk.skip(2);
+              }
+              if (u + 1 < nb) met = there(w ^ 1, rv, rk, u + 3 < nb);
+            });
           }
         }
       }
