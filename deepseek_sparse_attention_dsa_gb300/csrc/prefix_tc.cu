@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
     uint32_t turn = 0;                      // bit w: the buffer of stream w's queries
     bool ok = true, met = false;            // met: what the next step begins with is there
     auto nothing = [] {};
-    auto qk = [&](int w, const Ring<C::NS> r, bool first, bool last, bool release, bool halves, auto peek) {
+    auto qk = [&](int w, const Ring<C::NS> r, bool first, bool last, bool release, bool halves, auto walk, auto peek) {
       const uint32_t b = (turn >> w) & 1;
       if (first) {
         ok = ok && mbar_wait_warp(qfull(w, b), (q_phase >> (2 * w + b)) & 1, abort_addr, p.err);
@@ -336,16 +336,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
         const int at = (n >> 2) * (C::CHUNK >> 4) + 2 * (n & 3);
         mma_f16_ss(tmem + C::S_COL + w * 128, q + at, k + at, C::IDESC_QK, n > 0 ? 1u : 0u);
       };
-      constexpr int N = 4 * C::CH, BEHIND = 2;   // products, and those behind the peek
+      constexpr int N = 4 * C::CH, WALK = N / 2 - 1, PEEK = N - 2;
       if (elect_one()) {
 #pragma unroll
-        for (int n = 0; n < N - BEHIND; ++n) product(n);
+        for (int n = 0; n < WALK; ++n) product(n);
+      }
+      __syncwarp();
+      walk();
+      if (elect_one()) {
+#pragma unroll
+        for (int n = WALK; n < PEEK; ++n) product(n);
       }
       __syncwarp();
       peek();
       if (elect_one()) {
 #pragma unroll
-        for (int n = N - BEHIND; n < N; ++n) product(n);
+        for (int n = PEEK; n < N; ++n) product(n);
         mma_commit(sfull(w));
         if (release) mma_commit(slot_empty(r));
         if (last) mma_commit(qempty(w, b));
@@ -355,13 +361,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
     // Whether the values, weights and (more) keys that stream w's step begins with are there.
     auto there = [&](int w, const Ring<C::NS> &v, const Ring<C::NS> &k, bool more) {
       const uint32_t ph = (p_phase >> w) & 1;
-      return more ? mbar_try_warp_three(slot_full(v), v.phase, slot_full(k), k.phase, pfull(w, 0), ph)
-                  : mbar_try_warp_both(slot_full(v), v.phase, pfull(w, 0), ph);
+      return more ? mbar_test_warp_three(slot_full(v), v.phase, slot_full(k), k.phase, pfull(w, 0), ph)
+                  : mbar_test_warp_both(slot_full(v), v.phase, pfull(w, 0), ph);
     };
     // Stream w's step: O += P V, and behind it (they run in order, and S's columns hold P) the next S of the stream.
-    // peek: walks on and looks at the next step.
+    // walk: goes on to the next step; peek: looks at what it begins with.
     auto step = [&](int w, const Ring<C::NS> v, const Walk &kp, const Ring<C::NS> k, const Walk &kq, bool more, bool release,
-                    bool halves, auto peek) {
+                    bool halves, auto walk, auto peek) {
       const uint32_t ph = (p_phase >> w) & 1;
       if (!met) {
         if (more) ok = ok && mbar_wait_warp_three(slot_full(v), v.phase, slot_full(k), k.phase, pfull(w, 0), ph, abort_addr, p.err);
@@ -391,8 +397,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
         if (last) mma_commit(ofull(w));
       }
       __syncwarp();
-      if (more) qk(w, k, q_first, q_last, release, halves, peek);
-      else peek();
+      if (more) {
+        qk(w, k, q_first, q_last, release, halves, walk, peek);
+      } else {
+        walk();
+        peek();
+      }
     };
     if (na > 0) {
       Walk kq, kp;
@@ -401,22 +411,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
       Ring<C::NS> rk(0), rv(1);
       ok = mbar_wait_warp(slot_full(rk), rk.phase, abort_addr, p.err);
       tc_fence_after();
-      qk(0, rk, true, kq.n == 1, false, false, nothing);
-      qk(1, rk, true, kq.n == 1, true, false, nothing);
+      qk(0, rk, true, kq.n == 1, false, false, nothing, nothing);
+      qk(1, rk, true, kq.n == 1, true, false, nothing, nothing);
       kq.next();
       rk.skip(2);
 #pragma unroll 1
       for (int i = 0; i < na && ok; ++i) {
         const bool more = i + 1 < na;
-        step(0, rv, kp, rk, kq, more, false, false, [&] { met = there(1, rv, rk, more); });
-        step(1, rv, kp, rk, kq, more, true, false, [&] {
-          rv.skip(2);
-          kp.next();
-          if (!more) return;
-          kq.next();
-          rk.skip(2);
-          met = there(0, rv, rk, i + 2 < na);
-        });
+        step(0, rv, kp, rk, kq, more, false, false, nothing, [&] { met = there(1, rv, rk, more); });
+        step(
+            1, rv, kp, rk, kq, more, true, false,
+            [&] {
+              rv.skip(2);
+              kp.next();
+              if (more) {
+                kq.next();
+                rk.skip(2);
+              }
+            },
+            [&] { met = more && there(0, rv, rk, i + 2 < na); });
       }
       met = false;
     }
@@ -430,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
           kp[w] = kq[w];
           ok = ok && mbar_wait_warp(slot_full(rk), rk.phase, abort_addr, p.err);
           tc_fence_after();
-          qk(w, rk, true, kq[w].n == 1, true, small, nothing);
+          qk(w, rk, true, kq[w].n == 1, true, small, nothing, nothing);
           kq[w].next();
           rk.skip(w + 1);      // K(0), K(1), then every other half-tile
         }
@@ -441,15 +454,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
           const int u = t + w;
           if (u < nb) {
             const bool more = u + 2 < nb;
-            step(w, rv, kp[w], rk, kq[w], more, true, small, [&] {
-              kp[w].next();
-              rv.skip(more ? 2 : 1);
-              if (more) {
-                kq[w].next();
-                rk.skip(2);
-              }
-              if (u + 1 < nb) met = there(w ^ 1, rv, rk, u + 3 < nb);
-            });
+            step(
+                w, rv, kp[w], rk, kq[w], more, true, small,
+                [&] {
+                  kp[w].next();
+                  rv.skip(more ? 2 : 1);
+                  if (more) {
+                    kq[w].next();
+                    rk.skip(2);
+                  }
+                },
+                [&] { met = u + 1 < nb && there(w ^ 1, rv, rk, u + 3 < nb); });
           }
         }
       }

@@ -148,8 +148,10 @@ __device__ __forceinline__ void linger_if_aborted(uint32_t abort_flag, uint64_t 
   while (globaltimer() - t0 < stay_ns) __nanosleep(1000);
 }
 
-// Both of two phases, tried together so that one try's latency covers the other's.
-__device__ __forceinline__ bool mbar_try_warp_both(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1) {
+// Both of two phases, tried together first so that one try's latency covers the other's.
+__device__ __forceinline__ bool mbar_wait_warp_both(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1,
+                                                    uint32_t abort_flag, int *err,
+                                                    uint32_t limit_ns = static_cast<uint32_t>(kWaitLimitNs)) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
@@ -160,18 +162,14 @@ __device__ __forceinline__ bool mbar_try_warp_both(uint32_t bar0, uint32_t parit
       : "=r"(ok)
       : "r"(bar0), "r"(parity0), "r"(bar1), "r"(parity1)
       : "memory");
-  return __all_sync(0xffffffffu, ok);
-}
-__device__ __forceinline__ bool mbar_wait_warp_both(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1,
-                                                    uint32_t abort_flag, int *err,
-                                                    uint32_t limit_ns = static_cast<uint32_t>(kWaitLimitNs)) {
-  return mbar_try_warp_both(bar0, parity0, bar1, parity1) ||
-         (mbar_wait_slow(bar0, parity0, abort_flag, err, limit_ns) && mbar_wait_slow(bar1, parity1, abort_flag, err, limit_ns));
+  if (__all_sync(0xffffffffu, ok)) return true;
+  return mbar_wait_slow(bar0, parity0, abort_flag, err, limit_ns) && mbar_wait_slow(bar1, parity1, abort_flag, err, limit_ns);
 }
 
 // All of three phases, tried together.
-__device__ __forceinline__ bool mbar_try_warp_three(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1,
-                                                    uint32_t bar2, uint32_t parity2) {
+__device__ __forceinline__ bool mbar_wait_warp_three(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1,
+                                                     uint32_t bar2, uint32_t parity2, uint32_t abort_flag, int *err,
+                                                     uint32_t limit_ns = static_cast<uint32_t>(kWaitLimitNs)) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p, q, r;\n\t"
@@ -184,14 +182,40 @@ __device__ __forceinline__ bool mbar_try_warp_three(uint32_t bar0, uint32_t pari
       : "=r"(ok)
       : "r"(bar0), "r"(parity0), "r"(bar1), "r"(parity1), "r"(bar2), "r"(parity2)
       : "memory");
+  if (__all_sync(0xffffffffu, ok)) return true;
+  return mbar_wait_slow(bar0, parity0, abort_flag, err, limit_ns) && mbar_wait_slow(bar1, parity1, abort_flag, err, limit_ns) &&
+         mbar_wait_slow(bar2, parity2, abort_flag, err, limit_ns);
+}
+
+// Whether two, or three, phases are over: no waiting.
+__device__ __forceinline__ bool mbar_test_warp_both(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "and.pred p, p, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar0), "r"(parity0), "r"(bar1), "r"(parity1)
+      : "memory");
   return __all_sync(0xffffffffu, ok);
 }
-__device__ __forceinline__ bool mbar_wait_warp_three(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1,
-                                                     uint32_t bar2, uint32_t parity2, uint32_t abort_flag, int *err,
-                                                     uint32_t limit_ns = static_cast<uint32_t>(kWaitLimitNs)) {
-  return mbar_try_warp_three(bar0, parity0, bar1, parity1, bar2, parity2) ||
-         (mbar_wait_slow(bar0, parity0, abort_flag, err, limit_ns) && mbar_wait_slow(bar1, parity1, abort_flag, err, limit_ns) &&
-          mbar_wait_slow(bar2, parity2, abort_flag, err, limit_ns));
+__device__ __forceinline__ bool mbar_test_warp_three(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1,
+                                                     uint32_t bar2, uint32_t parity2) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q, r;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 r, [%5], %6;\n\t"
+      "and.pred p, p, q;\n\t"
+      "and.pred p, p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar0), "r"(parity0), "r"(bar1), "r"(parity1), "r"(bar2), "r"(parity2)
+      : "memory");
+  return __all_sync(0xffffffffu, ok);
 }
 
 // ----------------------------------------------------------------- fences
