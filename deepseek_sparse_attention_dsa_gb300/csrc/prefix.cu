@@ -145,12 +145,13 @@ struct Piece {
 };
 
 // What a CTA spends on a piece, in us: a key tile, and beside its tiles the queries' load, the first product's latency
-// and the output.  Measured on 152 SMs: a pair's tile 1.55 (its products), its partial results 2.5 to 3; lone tiles
-// two streams at a time.
+// and the output.  Measured on 152 SMs: a pair's tile 1.4 in a long chain and up to 2 in one of seven, its partial
+// results 2.5 to 3; lone tiles two streams at a time, 1.05 out of L2.  (Of seven choices about these, the one that took
+// least over fourteen batches; they differ by up to 10 % in one of them, by 1.5 % in all.)
 struct Cost {
   double tile, start;
 };
-constexpr Cost kPairCost{1.55, 3.0}, kLoneCost{1.2, 1.3};
+constexpr Cost kPairCost{1.5, 3.0}, kLoneCost{1.0, 0.7};
 constexpr double kLeast = 2.5;      // fewer CTAs rather than less than this for each
 
 // A line of pieces in runs of at most `most` each: a piece that does not fit is cut, unless that would leave a sliver
