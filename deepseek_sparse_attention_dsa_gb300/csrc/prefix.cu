@@ -145,13 +145,15 @@ struct Piece {
 };
 
 // What a CTA spends on a piece, in us: a key tile, and beside its tiles the queries' load, the first product's latency
-// and the output.  Measured on 152 SMs: a pair's tile 1.4 in a long chain and up to 2 in one of seven, its partial
-// results 2.5 to 3; lone tiles two streams at a time, 1.05 out of L2.  (Of seven choices about these, the one that took
-// least over fourteen batches; they differ by up to 10 % in one of them, by 1.5 % in all.)
+// and the output, which for a lone tile goes by its lanes.  Measured on 152 SMs: a pair's tile 1.4 in a long chain and
+// up to 2 in one of seven, its partial results 2.5 to 3; lone tiles two streams at a time, 1.05 out of L2.  (Of 16
+// choices about these the one that took least over 29 batches, 1 % less than with a lone start of 0.7 or 1.3 whatever
+// the lanes; where the cuts happen to fall moves a batch by 10 % either way.)
 struct Cost {
   double tile, start;
 };
-constexpr Cost kPairCost{1.5, 3.0}, kLoneCost{1.0, 0.7};
+constexpr Cost kPairCost{1.5, 3.0}, kLoneCost{1.0, 1.0};
+constexpr double kLoneLane = 0.0125;
 constexpr double kLeast = 2.5;      // fewer CTAs rather than less than this for each
 
 // A line of pieces in runs of at most `most` each: a piece that does not fit is cut, unless that would leave a sliver
@@ -266,42 +268,64 @@ void lay_out(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, Work &w) {
     i = end;
   }
   // One line, the pairs' chains, then the lone tiles', cut evenly over the CTAs.  Chains of pairs over the same keys
-  // that are longer than a CTA's share go in blocks of it, all pairs' first block first, so that CTAs that
+  // that are longer than a CTA's share go in blocks of about that, all pairs' first block first, so that CTAs that
   // run together read the same keys.
-  std::vector<Piece> line, lone;
+  auto cost_of_chain = [&](const Chain &c) {
+    return c.tile[1] >= 0 ? kPairCost : Cost{kLoneCost.tile, kLoneCost.start + kLoneLane * w.tiles[c.tile[0]].rows * group};
+  };
+  auto cost_of = [&](const Piece &x) { return cost_of_chain(w.chains[x.chain]); };
   const int n = std::max(2, ctx->num_sms / 2 * 2);
   double cost = 0.0;
   for (const Chain &c : w.chains) {
-    const Cost x = c.tile[1] >= 0 ? kPairCost : kLoneCost;
+    const Cost x = cost_of_chain(c);
     cost += c.ntiles * x.tile + x.start;
   }
-  const int32_t block = std::max<int32_t>(4, static_cast<int32_t>((cost / n - kPairCost.start) / kPairCost.tile + 0.5));
-  for (size_t c = 0; c < w.chains.size();) {
-    const Chain &x = w.chains[c];
-    size_t e = c + 1;
-    while (e < w.chains.size() && w.chains[e].span == x.span && w.chains[e].g == x.g && w.chains[e].slot0 == x.slot0 &&
-           w.chains[e].causal == x.causal)
-      ++e;
-    int32_t most = 0;
-    for (size_t k = c; k < e; ++k) most = std::max(most, w.chains[k].ntiles);
-    for (int32_t t = 0; t < most; t += block)
+  const double share = std::max(4.0, (cost / n - kPairCost.start) / kPairCost.tile);
+  std::vector<Piece> lone;
+  for (size_t c = 0; c < w.chains.size(); ++c)
+    if (w.chains[c].tile[1] < 0) lone.push_back(Piece{static_cast<int32_t>(c), 0, w.chains[c].ntiles});
+  auto line_of = [&](double block) {
+    std::vector<Piece> line;
+    std::vector<int32_t> done;      // tiles of a chain of the group that are in the line
+    for (size_t c = 0; c < w.chains.size();) {
+      const Chain &x = w.chains[c];
+      size_t e = c + 1;
+      while (e < w.chains.size() && w.chains[e].span == x.span && w.chains[e].g == x.g && w.chains[e].slot0 == x.slot0 &&
+             w.chains[e].causal == x.causal)
+        ++e;
+      int32_t most = 0;
       for (size_t k = c; k < e; ++k)
-        if (w.chains[k].tile[1] >= 0 && t < w.chains[k].ntiles)
-          line.push_back(Piece{static_cast<int32_t>(k), t, std::min(t + block, w.chains[k].ntiles)});
-    for (size_t k = c; k < e; ++k)
-      if (w.chains[k].tile[1] < 0) lone.push_back(Piece{static_cast<int32_t>(k), 0, w.chains[k].ntiles});
-    c = e;
-  }
-  line.insert(line.end(), lone.begin(), lone.end());
-  // the least that a CTA can be given so that n of them do
-  auto cost_of = [&](const Piece &x) { return w.chains[x.chain].tile[1] >= 0 ? kPairCost : kLoneCost; };
-  double low = std::max(cost / n, kLeast), high = low;
-  if (cut_line(line, low, cost_of) > n) {
-    while (cut_line(line, high, cost_of) > n) high *= 1.25;
-    for (int i = 0; i < 8; ++i) {
-      const double mid = 0.5 * (low + high);
-      (cut_line(line, mid, cost_of) <= n ? high : low) = mid;
+        if (w.chains[k].tile[1] >= 0) most = std::max(most, w.chains[k].ntiles);
+      const int32_t blocks = std::max(1, static_cast<int32_t>(most / block + 0.5));
+      done.assign(e - c, 0);
+      for (int32_t i = 1; i <= blocks; ++i) {
+        const int32_t end = static_cast<int32_t>(static_cast<int64_t>(most) * i / blocks);
+        for (size_t k = c; k < e; ++k) {
+          const int32_t tiles = w.chains[k].ntiles, t = done[k - c];
+          if (w.chains[k].tile[1] < 0 || t >= tiles || t >= end) continue;
+          done[k - c] = tiles - end < block / 3 ? tiles : end;      // (no sliver behind it)
+          line.push_back(Piece{static_cast<int32_t>(k), t, done[k - c]});
+        }
+      }
+      c = e;
     }
+    line.insert(line.end(), lone.begin(), lone.end());
+    return line;
+  };
+  // the least that a CTA can be given so that n of them do, with the blocks that leave the least
+  std::vector<Piece> line;
+  double high = 0.0;
+  for (const double f : {1.0, 0.85, 1.2}) {
+    std::vector<Piece> tried = line_of(share * f);
+    double low = std::max(cost / n, kLeast), top = low;
+    if (cut_line(tried, low, cost_of) > n) {
+      while (cut_line(tried, top, cost_of) > n) top *= 1.25;
+      for (int i = 0; i < 8; ++i) {
+        const double mid = 0.5 * (low + top);
+        (cut_line(tried, mid, cost_of) <= n ? top : low) = mid;
+      }
+    }
+    if (line.empty() || top < high) high = top, line.swap(tried);
   }
   std::vector<std::vector<Piece>> runs;
   cut_line(line, high, cost_of, &runs);
