@@ -146,9 +146,8 @@ struct Piece {
 
 // What a CTA spends on a piece, in us: a key tile, and beside its tiles the queries' load, the first product's latency
 // and the output, which for a lone tile goes by its lanes.  Measured on 152 SMs: a pair's tile 1.4 in a long chain and
-// up to 2 in one of seven, its partial results 2.5 to 3; lone tiles two streams at a time, 1.05 out of L2.  (Of 16
-// choices about these the one that took least over 29 batches, 1 % less than with a lone start of 0.7 or 1.3 whatever
-// the lanes; where the cuts happen to fall moves a batch by 10 % either way.)
+// up to 2 in one of seven, its partial results 2.5 to 3; lone tiles two streams at a time, 1.05 out of L2.  (Over 29
+// batches, values half as large again or a third less for any one of them took 0 to 3 % more.)
 struct Cost {
   double tile, start;
 };
@@ -312,10 +311,13 @@ void lay_out(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, Work &w) {
     line.insert(line.end(), lone.begin(), lone.end());
     return line;
   };
-  // the least that a CTA can be given so that n of them do, with the blocks that leave the least
+  // The least that a CTA can be given so that n of them do, with the blocks that leave the least: a block that does not
+  // fit a whole number of times ends in a rest, which costs a start of its own (32 rows behind 8192 tokens took 26 us
+  // with blocks of the share alone and 20.5 with these; over 29 batches one size took 5 % longer than the best of five,
+  // three 1.6 %).
   std::vector<Piece> line;
   double high = 0.0;
-  for (const double f : {1.0, 0.85, 1.2}) {
+  for (const double f : {1.0, 0.85, 1.2, 0.7, 1.45}) {
     std::vector<Piece> tried = line_of(share * f);
     double low = std::max(cost / n, kLeast), top = low;
     if (cut_line(tried, low, cost_of) > n) {
