@@ -2,10 +2,12 @@
 // on the way: latent rows [c | rotated k_pe] and index keys (bf16, or quantised
 // to the 656- and 132-byte rows), or the keys and values of a GQA cache.
 //
-// Each value is read and written once.  A warp takes one part of one row (its
-// latent, its index key, its keys, its values), since a row is one to four
-// kilobytes and a decode step has few of them.  Values to be quantised stay in
-// fp32 between rotation and code, so that they are rounded once.
+// Each value is read and written once.  Values to be quantised stay in fp32
+// between rotation and code, so that they are rounded once.  append_runs_kernel takes
+// sources and caches on 16 bytes in whole runs of 16 columns; append_kernel, a warp
+// for each part of a row (its latent, its index key, its keys, its values), any
+// others: 128 rows 4.1 us in place of 2.9, 8192 rows into 8 bits 16.0 in place of
+// 8.9, 8197 rows of keys and values 14.7 in place of 9.5 (fp32: 14.9 and 13.0).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -146,8 +146,9 @@ struct Piece {
 
 // What a CTA spends on a piece, in us: a key tile, and beside its tiles the queries' load, the first product's latency
 // and the output, which for a lone tile goes by its lanes.  Measured on 152 SMs: a pair's tile 1.4 in a long chain and
-// up to 2 in one of seven, its partial results 2.5 to 3; lone tiles two streams at a time, 1.05 out of L2.  (Over 29
-// batches, values half as large again or a third less for any one of them took 0 to 3 % more.)
+// up to 2 in one of seven, its partial results 2 to 3; lone tiles two streams at a time, 1.05 out of L2.  (Over 29
+// batches 1.7 for a pair's tile, 2.5 to 4 for its start, 0.9 to 1.1 and 0.7 to 1.4 for a lone tile took up to 1 % more,
+// two of them at once up to 3 %.)
 struct Cost {
   double tile, start;
 };

@@ -4,7 +4,14 @@
 //
 // (rotary.cuh: the arithmetic, and why the angles hold at any position.)  Each
 // value is read and written once; the angles of a row, the expensive part (some
-// 60 instructions each), are made once for all of its heads, in shared memory.
+// 30 instructions each), are made once for all of its heads, in shared memory.
+//
+// Bound by HBM: 8192 rows x 128 heads of 64 columns out of rows of 192, bf16, 44.2 us
+// (6.07 TB/s, 0.91 of a plain copy); 4096 x 64 x 128, 23.5 us (0.86); 1031 x 64 x 128 in
+// fp32, 11.0 us (0.92).  One token of 128 heads: 2.3 us, a launch and one way to
+// memory and back.  rotary_pieces_kernel takes what lies on 16 bytes; the
+// general kernel, which asks every unit for its edges, is 3 to 4 times as long where a
+// row's stride is odd (131, 88 and 31 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -64,7 +71,8 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
 }
 
 // The same where every piece of 16 bytes is whole and on 16 bytes: a unit is two pieces (a rotated pair of them where
-// the layout is half), a thread's pieces are on their way while the angles are made, and stay packed.
+// the layout is half), a thread's pieces are on their way while the angles are made, and stay packed.  (The general
+// kernel took 70, 50 and 12.7 us for the three sizes above; eight items a thread were slower than four.)
 template <int kType>
 __global__ void __launch_bounds__(kRotThreads) rotary_pieces_kernel(const RotaryParams p) {
   constexpr int N = kType == DSA_BF16 ? 8 : 4;   // columns a piece

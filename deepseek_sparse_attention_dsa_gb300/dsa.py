@@ -31,6 +31,16 @@ row or per 128 x 128 block of a weight):
 These four take rows at any stride and need no plan (plan= marks the padding
 rows of a capturable plan).
 
+Between projections and caches, and dense attention over a cache whose requests
+start with the same pages:
+
+    table = ctx.rotary_table(rot_dim, base, scaling="yarn", factor=40.0)  # dsa_rotary_create, once
+    q = ctx.rotary(table, q, plan)                                        # dsa_rotate, by the rows' positions
+    ctx.append_latents(plan, table, c, k_pe, latent_cache, keys, index_cache)   # dsa_append_latents
+    ctx.append_kv(plan, msa, table, k, v, kv_cache)                       # dsa_append_kv
+    prefixes = ctx.plan_prefix(plan, msa)                                 # dsa_prefix_plan, once a step
+    out = ctx.prefix_attend(prefixes, q, kv_cache)                        # dsa_prefix_attend
+
 Tensors are torch tensors on the context's device, contiguous, in the dtypes
 the header states; the calls run on torch's current CUDA stream unless a
 stream is given.

@@ -47,12 +47,15 @@ def rotate(x, positions, freqs, offset=0, layout="interleaved", inverse=False, a
 
 def rotated_error() -> float:
     """Error of a rotated value in fp32 before its last rounding, relative to its
-    terms' magnitudes: sine and cosine of the rounded angle are off by 2 half
-    steps, and the angle, off by half a step of at most pi, moves them by pi half
-    steps of 1, which is not relative to a small sine or cosine (see rotate_bound);
-    the amplitude (itself rounded), its product, the term's product and the sum
-    add half a step each."""
-    return (2 + 1 + 1 + 1 + 1) * EPS32
+    terms' magnitudes, in half steps.  Sine and cosine of the rounded angle by
+    their sums: the sine's last coefficient is off by 0.5, its last addition and
+    the product with x by 1 each, the sum before them (0.1 of the value, 2.5)
+    by 0.3: 2.8 in all; the cosine's last addition by 1, and x x and the sum before it
+    (at most 0.44 of the value) by 1 and 1.5: 2.1 in all.  The angle, off by half a
+    step of at most pi, moves them by pi half steps of 1, which is not relative
+    to a small sine or cosine (see rotate_bound).  The amplitude (itself
+    rounded), its product, the term's product and the sum add half a step each."""
+    return (3 + 1 + 1 + 1 + 1) * EPS32
 
 
 def rotate_bound(x, y, mag, offset, rot, layout, amplitude=1.0):
