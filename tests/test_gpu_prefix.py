@@ -90,6 +90,17 @@ def test_head_layouts(contexts, q_heads, kv_heads, dim):
     check(ctx, spans, pages, shape(q_heads, kv_heads, dim), q, kv, found=1)
 
 
+@pytest.mark.parametrize("rows,q_heads,kv_heads,dim", [(170, 40, 2, 96), (90, 33, 3, 33), (60, 5, 5, 7), (33, 260, 2, 128), (3, 7, 1, 512), (40, 18, 1, 511)])
+def test_shapes_of_the_general_kernel(contexts, rows, q_heads, kv_heads, dim):
+    """Few and many rows: heads over one warp and over all of a CTA's, odd head sizes."""
+    ctx = contexts()
+    spans, pages = batch(11, 64, [(128 + (37 * i) % 300, 1 + (i == 2) * 2) for i in range(rows)], shared=2)
+    q, kv = inputs(12, spans, pages, 64, q_heads, kv_heads, dim)
+    _, pp = attend(ctx, spans, pages, shape(q_heads, kv_heads, dim), q, kv)
+    assert not pp.on_tensor_cores
+    check(ctx, spans, pages, shape(q_heads, kv_heads, dim), q, kv, found=1)
+
+
 @pytest.mark.parametrize("page,start,shared", [(64, 0, 2), (64, 37, 3), (64, 63, 4), (16, 5, 20), (8, 3, 40), (128, 0, 1), (128, 100, 2),
                                                (7, 0, 30), (24, 11, 9), (256, 130, 2)])
 def test_pages(contexts, page, start, shared):
