@@ -154,10 +154,13 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
 // another in a CTA and p.deep of them in a thread; neighbouring groups are the same part of neighbouring rows, so that a
 // warp copies, turns or quantises and seldom does several of these (by rows: 9.3 us in place of 8.5).  kWide: some source
 // is fp32.
-// Bound by its instructions and by the way from one look-up to the next (launch, position, page, row: 2.6 us for 128 rows):
+// Bound by its instructions and by the way from one look-up to the next (launch, position, page, row: 2.5 us for 128 rows):
 // 8192 rows into 8 bits take 8.5 us, 2.1 TB/s, with the sources in L2; 8197 rows of keys and values, 4 heads of 128 each,
-// 9.3 us, 3.6 TB/s, and 11.4 from memory.  (With 8 columns a lane, twice the threads, 8192 rows took 2.4 us more.)
+// 8.6 us, 3.9 TB/s, and 10.0 from memory.  (With 8 columns a lane, twice the threads, 8192 rows took 2.4 us more; with 80
+// registers and without the few spills that 64 cost, 8197 rows 0.7 to 1.4 us more.  A step of few rows has a kernel of
+// its own, DEEP 1: 2.5 us for 128 rows in place of 2.9.)
 constexpr int kAppendThreads = 256;
+constexpr int kAppendRegisters = 64;   // a thread's, by the launch bounds
 constexpr int kLaneCols = 16, kGroupLanes = 128 / kLaneCols;
 template <bool kWide>
 constexpr int kAppendDeep = kWide ? 2 : 4;
@@ -165,9 +168,9 @@ constexpr int kAppendDeep = kWide ? 2 : 4;
 __host__ __device__ constexpr int padded(int q) { return q + q / 16; }
 constexpr int kAppendRows = kAppendThreads / kGroupLanes * 4;   // the most that a CTA has (one group a row)
 
-template <bool kWide>
-__global__ void __launch_bounds__(kAppendThreads) append_runs_kernel(const AppendParams p) {
-  constexpr int N = kLaneCols, W = kWide ? 4 : 2, DEEP = kAppendDeep<kWide>;
+template <bool kWide, int DEEP>
+__global__ void __launch_bounds__(kAppendThreads, 4) append_runs_kernel(const AppendParams p) {
+  constexpr int N = kLaneCols, W = kWide ? 4 : 2;
   extern __shared__ float2 angles[];   // [rows of the CTA][padded(rot / 2)]
   __shared__ int2 where[kAppendRows];  // of the CTA's rows: page (-1: nothing to write), slot in it
   grid_dependency();
@@ -364,12 +367,11 @@ cudaError_t launch_append(const dsa_ctx *ctx, AppendParams &p, cudaStream_t s, i
     const bool wide = (p.c && (p.c_type != DSA_BF16 || (p.R > 0 && p.k_pe_type != DSA_BF16))) || (p.keys && p.key_type != DSA_BF16) ||
                       (p.k && p.kv_type != DSA_BF16);
     // As many rows side by side as the threads hold, fewer where that leaves SMs without any; and a thread as deep as
-    // takes least by waves of CTAs (80 registers a thread) of some 2.5 us and 0.6 for each of its rows: one row for a
-    // decode step; for 8197 rows of K and V three, 9.3 us (four: 11.0, a second wave of few); for 8192 in 8 bits four,
-    // 8.4 us (three: 10.9).
+    // takes least by waves of CTAs of some 2.5 us and 0.6 for each of its rows: one row for a decode step; for 8197
+    // rows of K and V four, 8.6 us (three: 10.4, a second wave of few); for 8192 in 8 bits three, 8.5 us (four: 10.1).
     const int sms = std::max(1, ctx->num_sms);
     p.side = std::max(1, std::min(kAppendThreads / kGroupLanes / p.groups, p.T / sms));
-    const int threads = (p.side * p.groups * kGroupLanes + 31) / 32 * 32, at_once = sms * (65536 / (80 * threads));
+    const int threads = (p.side * p.groups * kGroupLanes + 31) / 32 * 32, at_once = sms * (65536 / (kAppendRegisters * threads));
     double least = 0.0;
     for (int deep = 1; deep <= (wide ? kAppendDeep<true> : kAppendDeep<false>); ++deep) {
       if (p.side * deep * padded(p.rot / 2) * sizeof(float2) > 46 * 1024) break;
@@ -378,8 +380,9 @@ cudaError_t launch_append(const dsa_ctx *ctx, AppendParams &p, cudaStream_t s, i
       if (deep == 1 || cost < least) least = cost, p.deep = deep;
     }
     const int rows = p.side * p.deep;
-    return launch_overlapped(wide ? append_runs_kernel<true> : append_runs_kernel<false>,
-                             dim3(static_cast<unsigned>((p.T + rows - 1) / rows)), threads,
+    auto kernel = wide ? p.deep == 1 ? append_runs_kernel<true, 1> : append_runs_kernel<true, kAppendDeep<true>>
+                       : p.deep == 1 ? append_runs_kernel<false, 1> : append_runs_kernel<false, kAppendDeep<false>>;
+    return launch_overlapped(kernel, dim3(static_cast<unsigned>((p.T + rows - 1) / rows)), threads,
                              rows * padded(p.rot / 2) * static_cast<int>(sizeof(float2)), 1, s, p);
   }
   int floats = p.rot ? rotary_pairs(p.rot) * 2 : 0;
