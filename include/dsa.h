@@ -654,7 +654,7 @@ typedef struct dsa_prefix_plan dsa_prefix_plan_t;
 typedef struct dsa_prefix_info {
   int32_t num_prefixes;      /* runs of spans that share a prefix */
   int32_t on_tensor_cores;   /* 1 when the plan's calls run on the tensor cores */
-  int64_t tokens_read;       /* tokens whose keys and values one call reads (per kv head) */
+  int64_t tokens_read;       /* tokens whose keys and values one call needs (per kv head), shared ones once */
 } dsa_prefix_info_t;
 dsa_status dsa_prefix_plan(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_msa_shape_t *shape, const dsa_prefix_t *prefixes,
                            int32_t num_prefixes, dsa_stream_t stream, dsa_prefix_plan_t **out);
