@@ -6,12 +6,12 @@
 // value is read and written once; the angles of a row, the expensive part (some
 // 30 instructions each), are made once for all of its heads, in shared memory.
 //
-// Bound by HBM: 8192 rows x 128 heads of 64 columns out of rows of 192, bf16, 44.2 us
-// (6.07 TB/s, 0.91 of a plain copy); 4096 x 64 x 128, 23.5 us (0.86); 1031 x 64 x 128 in
-// fp32, 11.0 us (0.92).  One token of 128 heads: 2.3 us, a launch and one way to
+// Bound by HBM: 8192 rows x 128 heads of 64 columns out of rows of 192, bf16, 41.1 us
+// (6.5 TB/s, 0.98 of a plain copy); 4096 x 64 x 128, 21.4 us (0.94); 1031 x 64 x 128 in
+// fp32, 10.0 us (1.01).  One token of 128 heads: 1.9 us, a launch and one way to
 // memory and back.  rotary_pieces_kernel takes what lies on 16 bytes; the
 // general kernel, which asks every unit for its edges, is 3 to 4 times as long where a
-// row's stride is odd (131, 88 and 31 us).
+// row's stride is odd (131, 82 and 30 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -22,8 +22,8 @@
 namespace dsa {
 namespace {
 
-constexpr int kRotThreads = 256;
-constexpr int kRotItems = 4;   // (row, head) items a thread of rotary_pieces_kernel
+constexpr int kRotThreads = 128;
+constexpr int kRotItems = 2;   // (row, head) items a thread of rotary_pieces_kernel
 
 struct RotaryParams {
   const char *x;
@@ -72,7 +72,9 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
 
 // The same where every piece of 16 bytes is whole and on 16 bytes: a unit is two pieces (a rotated pair of them where
 // the layout is half), a thread's pieces are on their way while the angles are made, and stay packed.  (The general
-// kernel took 70, 50 and 12.7 us for the three sizes above; eight items a thread were slower than four.)
+// kernel took 70, 50 and 12.7 us for the three sizes above.  Small CTAs of short threads: 256 threads with four items
+// each took 44.2, 23.5, 11.0 and, for one token, 2.3 us, 512 with four 63, 33, 16 and 2.8; one item a thread 48, 24, 11.5
+// and 1.7.)
 template <int kType>
 __global__ void __launch_bounds__(kRotThreads) rotary_pieces_kernel(const RotaryParams p) {
   constexpr int N = kType == DSA_BF16 ? 8 : 4;   // columns a piece
@@ -178,7 +180,7 @@ struct Cut {
     if (!pieces) units = rotary_units(rot, g.layout) + (in_place ? 0 : rotary_copies(g.width, g.offset, rot));
     threads = std::min(units, kRotThreads);
     pitch = pieces ? rot / 2 : rotary_pairs(rot);
-    // four items a thread (two where units of twice eight columns are taken one by one), while the rows' angles fit 48 KB
+    // kRotItems items a thread, in the general kernel four (two of twice eight columns), while the rows' angles fit 48 KB
     const int64_t most = 48 * 1024 / (pitch * sizeof(float2));
     items = (pieces ? kRotItems : half ? 2 : 4) * (kRotThreads / threads);
     items = static_cast<int>(std::min<int64_t>(items, g.heads == 1 ? most : (most - 2) * g.heads + 1));
