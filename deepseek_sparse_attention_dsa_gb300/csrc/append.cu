@@ -372,6 +372,7 @@ cudaError_t launch_append(const dsa_ctx *ctx, AppendParams &p, cudaStream_t s, i
     const int sms = std::max(1, ctx->num_sms);
     p.side = std::max(1, std::min(kAppendThreads / kGroupLanes / p.groups, p.T / sms));
     const int threads = (p.side * p.groups * kGroupLanes + 31) / 32 * 32, at_once = sms * (65536 / (kAppendRegisters * threads));
+    // (whole_runs bounds rot by the 128 columns of what turns, so that one row a thread always fits)
     double least = 0.0;
     for (int deep = 1; deep <= (wide ? kAppendDeep<true> : kAppendDeep<false>); ++deep) {
       if (p.side * deep * padded(p.rot / 2) * sizeof(float2) > 46 * 1024) break;
@@ -397,7 +398,8 @@ cudaError_t launch_append(const dsa_ctx *ctx, AppendParams &p, cudaStream_t s, i
 cudaError_t launch_append_latents(const dsa_ctx *ctx, const dsa_plan_t *plan, const dsa_rotary *table, const dsa_append_t &a,
                                   const void *c, const void *k_pe, void *latent_cache, const void *keys, void *index_cache,
                                   cudaStream_t s, int32_t *launches) {
-  AppendParams p = append_base(ctx, plan, table);
+  // (a rope of no columns: a table is the keys' alone, and without keys nothing turns, whatever its width)
+  AppendParams p = append_base(ctx, plan, ctx->cfg.rope_dim > 0 || keys ? table : nullptr);
   if (c) {
     const dsa_config_t &g = ctx->cfg;
     p.part[p.parts++] = kPartLatent;

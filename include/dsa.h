@@ -577,8 +577,8 @@ dsa_status dsa_rotate(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_rotary_t
  * the e4m3 code of the cache's format.
  *
  * dsa_append_latents: c (T, kv_lora_rank) and k_pe (T, rope_dim), of which k_pe is
- *   rotated in `layout` (a table's rot_dim must be rope_dim), into latent_cache in
- *   the context's latent format; and/or keys (T, index_dim), of which columns
+ *   rotated in `layout` (a table's rot_dim must be rope_dim; where that is 0 the table is
+ *   the keys' alone), into latent_cache in the context's latent format; and/or keys (T, index_dim), of which columns
  *   key_offset .. key_offset + rot_dim are rotated in `key_layout`, into index_cache
  *   in the context's index format, in the same launch.  c, k_pe and latent_cache
  *   are all NULL where only keys are appended, keys and index_cache where only latents

@@ -322,6 +322,24 @@ def test_append_widths(contexts, lora, rope, dim, rot, aligned, turned):
         ref.close(got, y[:, 0], ref.rotate_bound(x[:, None], y, mag, offset, rot, layout)[:, 0], BF16)
 
 
+@pytest.mark.parametrize("lora,rot,rows", [(128, 1024, 1672), (256, 1024, 4999), (128, 512, 3344), (128, 1024, 70), (136, 1024, 4999)])
+def test_append_without_a_rope_ignores_a_wide_table(contexts, lora, rot, rows):
+    """Nothing of such a latent turns: a table of any width leaves it as it is, however many rows there are."""
+    c = contexts(kv_lora_rank=lora, rope_dim=0)
+    pages = rows // 64 + 2
+    order = np.random.default_rng(rows).permutation(pages).astype(np.int32)
+    plan = c.plan([W.Span(0, 0, rows, 5, order)], pages)
+    lat = rand(1, rows, lora)
+    lc = torch.full((pages, 64, lora), 9.0, dtype=BF16, device="cuda")
+    c.append_latents(plan, c.rotary_table(rot), lat, None, lc)
+    c.get_error()
+    slot = np.arange(5, 5 + rows)
+    where = order[slot // 64].astype(np.int64) * 64 + slot % 64
+    want = torch.full((pages * 64, lora), 9.0, dtype=BF16)
+    want[where] = lat.cpu()
+    assert torch.equal(lc.view(-1, lora).cpu(), want)
+
+
 @pytest.mark.parametrize("page", [64, 16])
 def test_append_without_a_table_is_the_store(contexts, page):
     """Unrotated bf16 rows: byte for byte what the stores write."""
