@@ -321,7 +321,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
-    // (reads the plan's tables and shared memory only: it does not wait for the kernels before)
     // ------------------------------------------------------------ products
     // One warp for both streams, so that half-tiles are awaited in the order in which they were asked for (a parity
     // says nothing of a fill two uses away).  The whole warp walks and waits, one elected thread issues: its operands
@@ -333,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
                    desc_v0 = smem_desc(sbase + C::OFF_RING, C::CHUNK, 1024, kSwizzle128);
     auto slot_full = [&](const Ring<C::NS> &r) { return bar0 + 8u * r.st; };
     auto slot_empty = [&](const Ring<C::NS> &r) { return bar0 + 8u * (C::NS + r.st); };
+    grid_dependency_wait();      // (a barrier's time limit is for this kernel's own work, not for that of the kernels before)
     uint32_t q_phase = 0, p_phase = 0;      // bit 2 w + b: stream w's buffer b; bit w: stream w's
     uint32_t turn = 0;                      // bit w: the buffer of stream w's queries
     bool ok = true, met = false;            // met: what the next step begins with is there

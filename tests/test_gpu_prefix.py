@@ -298,6 +298,29 @@ def test_large_logits(contexts):
         check(ctx, spans, pages, shape(8, 2), q, k.to(BF16).view(kv.shape), found=1)
 
 
+def test_behind_a_kernel_that_takes_longer_than_a_wait_may(contexts):
+    """A row of four million tokens, which the general kernel takes some 1.6 s for, with the attention set up beside it: a
+    wait's limit of 1 s is for the attention's own work."""
+    ctx = contexts()
+    tokens, page = 1 << 22, torch.randn(1, 64, 2 * 511, generator=torch.Generator().manual_seed(50)).to(BF16).cuda()
+    long = ctx.plan_prefix(ctx.plan([W.Span(0, 0, 1, tokens - 1, np.zeros(tokens // 64, np.int32))], 1), shape(1, 1, 511))
+    assert not long.on_tensor_cores
+    spans, pages = batch(51, 64, [(130, 1), (200, 1), (128, 3)], shared=2)
+    q, kv = inputs(52, spans, pages, 64, 16, 2, 128)
+    pp = ctx.plan_prefix(ctx.plan(spans, pages), shape(16, 2))
+    q, kv, one = q.cuda(), kv.cuda(), torch.randn(1, 1, 511, generator=torch.Generator().manual_seed(53)).to(BF16).cuda()
+    want, out, far = ctx.prefix_attend(pp, q, kv), torch.zeros_like(q), torch.zeros_like(one)
+    torch.cuda.synchronize()
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    begin.record()
+    ctx.prefix_attend(long, one, page, out=far)
+    ctx.prefix_attend(pp, q, kv, out=out)
+    end.record()
+    ctx.get_error()
+    assert begin.elapsed_time(end) > 1000.0      # (as long as the limit: a faster kernel wants a longer row here)
+    assert torch.equal(out, want)
+
+
 def test_uniform_logits_are_the_mean(contexts):
     ctx = contexts()
     spans, pages = batch(16, 64, [(512, 1), (600, 1)], 8)
