@@ -937,6 +937,20 @@ static bool rotary_frequencies(const dsa_rotary_config_t &c, double *f) {
   return true;
 }
 
+// frequency / 2 pi modulo whole turns, which change nothing, in units of 2^-64 of a turn: off by half a unit, and by
+// some 2^-106 of the turns (nothing below 2^40 of them).  1 / 2 pi and the product in two doubles each.
+static uint64_t turns_of(double frequency) {
+  constexpr double kHigh = 0x1.45f306dc9c883p-3, kLow = -0x1.6b01ec5417056p-57;
+  const double f = std::fabs(frequency), whole = f * kHigh;
+  double rest = std::fma(f, kLow, std::fma(f, kHigh, -whole));
+  rest -= std::nearbyint(rest);
+  const double units = std::ldexp(whole - std::floor(whole), 64), down = std::floor(units);
+  const double more = std::nearbyint((units - down) + std::ldexp(rest, 64));   // (at most 2^63 either way)
+  uint64_t turns = static_cast<uint64_t>(down);
+  turns = more < 0.0 ? turns - static_cast<uint64_t>(-more) : turns + static_cast<uint64_t>(more);
+  return frequency < 0.0 ? 0 - turns : turns;
+}
+
 dsa_status dsa_rotary_create(dsa_ctx_t *ctx, const dsa_rotary_config_t *cfg, dsa_rotary_t **out) {
   if (!out) return DSA_ERR_INVALID_ARG;
   *out = nullptr;
@@ -947,12 +961,7 @@ dsa_status dsa_rotary_create(dsa_ctx_t *ctx, const dsa_rotary_config_t *cfg, dsa
   if (!rotary_frequencies(*cfg, f)) return DSA_ERR_INVALID_ARG;
   uint64_t turns[512];
   const int n = cfg->rot_dim / 2;
-  for (int i = 0; i < n; ++i) {
-    // whole turns a position change nothing: the fraction alone, 2^64 of them a turn
-    double t = f[i] / 6.283185307179586476925286766559;
-    t -= std::floor(t);
-    turns[i] = t < 1.0 ? static_cast<uint64_t>(std::ldexp(t, 64)) : 0;
-  }
+  for (int i = 0; i < n; ++i) turns[i] = turns_of(f[i]);
   dsa_rotary_t *table = new (std::nothrow) dsa_rotary_t();
   if (!table) return DSA_ERR_OOM;
   table->device = ctx->device, table->rot = cfg->rot_dim, table->amplitude = static_cast<float>(cfg->amplitude);

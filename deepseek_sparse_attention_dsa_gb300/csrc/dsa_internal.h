@@ -284,7 +284,7 @@ struct dsa_plan {
   int32_t *counts = nullptr;            // device [8], see dsa_plan_read_counts
 };
 
-// A rotation's table: turns[i] = round(2^64 frequency[i] / 2 pi) on the device (rotary.cuh).
+// A rotation's table: turns[i] = round(2^64 frequency[i] / 2 pi) modulo 2^64, on the device (rotary.cuh).
 struct dsa_rotary {
   int device = -1;
   int32_t rot = 0;

@@ -3,10 +3,10 @@
 //
 // A pair (a, b) at angle t becomes (a cos t - b sin t, a sin t + b cos t), in
 // fp32.  Angles are exact to the last bit that matters at any position: a table
-// holds each pair's frequency in turns a position as a 64-bit fraction of a turn,
-// f = round(2^64 frequency / 2 pi), so position * f modulo 2^64 (what a 64-bit
-// product keeps by itself) is the fraction of a turn with an error of at most
-// |position| * 2^-65 turns.  Its nearest quarter goes to the signs and the order of
+// holds each pair's frequency (a double) in turns a position as a 64-bit fraction of
+// a turn, f = round(2^64 frequency / 2 pi) modulo 2^64, so position * f modulo 2^64
+// (what a 64-bit product keeps by itself) is the fraction of a turn with an error of
+// at most |position| * 2^-65 turns.  Its nearest quarter goes to the signs and the order of
 // sine and cosine, and what is left, at most an eighth of a turn, is converted to
 // fp32 with all of its digits.  (position * frequency in fp32 is off by 2^-24 of the
 // angle: 0.008 rad at position 131,072.)

@@ -504,13 +504,14 @@ int dsa_project_on_tensor_cores(const dsa_project_t *shape, const void *a, const
  *
  * A rotation takes pairs (a, b) of a row's columns to
  *   (a cos t - b sin t, a sin t + b cos t) * amplitude,  t = position * frequency[pair],
- * in fp32 with t exact for any int32 position (to 2^-43 of a turn at position
- * 2^20), rounded once to the output's type.  Column pairs of the rot_dim rotated
+ * in fp32 with t exact for any int32 position (to |position| * 2^-64 of a turn, for
+ * frequencies below 2^40, each the double that the table is made from), rounded
+ * once to the output's type.  Column pairs of the rot_dim rotated
  * columns: (2i, 2i + 1) for DSA_ROTARY_INTERLEAVED, (i, i + rot_dim / 2) for
  * DSA_ROTARY_HALF.  `inverse` turns by -t: with the same amplitude that is also the
  * gradient of the rotation.  Values that are not finite reach their own pair only.
  *
- * A table holds the frequencies of a model, in radians a position, for
+ * A table holds the frequencies of a model, computed in 64 bits, in radians a position, for
  * pair i = 0 .. rot_dim / 2 - 1:
  *   DSA_ROTARY_PLAIN   base^(-2i / rot_dim)
  *   DSA_ROTARY_LINEAR  that, divided by factor (a context `factor` times as long)

@@ -1,4 +1,7 @@
 """GPU: rotations and appends against their definitions in 64 bits."""
+import math
+from decimal import Decimal, localcontext
+
 import numpy as np
 import pytest
 import torch
@@ -123,6 +126,30 @@ def test_frequencies_beyond_a_turn(ctx):
     got = ctx.rotary(ctx.rotary_table(8, frequencies=freqs), x, pos)
     want, mag = ref.rotate(x, pos, freqs)
     ref.close(got, want, ref.rotate_bound(x, want, mag, 0, 8, "interleaved") + 2.0 ** -52 * 1001 * 100 * 4, F32)
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+def test_angles_hold_at_any_position(ctx, layout):
+    """The fraction of a turn of position x frequency, the frequency as the double it is, in 60 digits."""
+    freqs = [100.0, 0.9, 730000.5, -12345.678, 1.0, 1e9 + 0.1, 2.5e-7, -0.1, 3.3e11, 6.283185307179586, 1e-19, 0.75, 5e-324, -1e-300, 41.5, 0.3]
+    far = FAR + (2147483646, 1073741789, -1999999973)
+    x = rand(15, len(far), 3, 32, dtype=F32)
+    got = ctx.rotary(ctx.rotary_table(32, frequencies=freqs), x, positions(*far), layout=layout)
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+    want, mag = x.cpu().double().clone(), torch.zeros(x.shape, dtype=torch.float64)
+    with localcontext() as digits:
+        digits.prec = 80
+        for r, p in enumerate(far):
+            for i, f in enumerate(freqs):
+                turns = p * Decimal(f) / two_pi
+                t = 2 * math.pi * float(turns - turns.to_integral_value())
+                a, b = (2 * i, 2 * i + 1) if layout == "interleaved" else (i, i + 16)
+                u, v, c, s = x[r, :, a].cpu().double(), x[r, :, b].cpu().double(), math.cos(t), math.sin(t)
+                want[r, :, a], want[r, :, b] = u * c - v * s, u * s + v * c
+                mag[r, :, a], mag[r, :, b] = (u * c).abs() + (v * s).abs(), (u * s).abs() + (v * c).abs()
+    # a table is off by 2^-65 of a turn a position, half a unit (and 2^-106 of the turns, here below 2^36)
+    bound = ref.rotate_bound(x, want, mag, 0, 32, layout) + 2 * math.pi * 2.0 ** -34 * 2 * x.cpu().double().abs().amax()
+    ref.close(got, want, bound, F32)
 
 
 def test_small_angles_keep_their_sine(ctx):
