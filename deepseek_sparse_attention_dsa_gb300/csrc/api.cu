@@ -11,6 +11,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
@@ -955,7 +956,7 @@ dsa_status dsa_rotary_create(dsa_ctx_t *ctx, const dsa_rotary_config_t *cfg, dsa
   if (!out) return DSA_ERR_INVALID_ARG;
   *out = nullptr;
   if (!ctx || !cfg || cfg->rot_dim < 2 || cfg->rot_dim > 1024 || cfg->rot_dim % 2 || cfg->form < DSA_ROTARY_PLAIN ||
-      cfg->form > DSA_ROTARY_GIVEN || !std::isfinite(cfg->amplitude) || (cfg->form == DSA_ROTARY_GIVEN && !cfg->frequencies))
+      cfg->form > DSA_ROTARY_GIVEN || !(std::fabs(cfg->amplitude) <= FLT_MAX) || (cfg->form == DSA_ROTARY_GIVEN && !cfg->frequencies))
     return DSA_ERR_INVALID_ARG;
   double f[512];
   if (!rotary_frequencies(*cfg, f)) return DSA_ERR_INVALID_ARG;

@@ -528,7 +528,7 @@ int dsa_project_on_tensor_cores(const dsa_project_t *shape, const void *a, const
  * captured graphs as long as it lives.  On a host-only context it is made without a device copy.
  * DSA_ERR_INVALID_ARG: rot_dim odd, below 2 or above 1024, an unknown form, a base
  * not above 1, a factor, original_context or beta not above 0, beta_fast below
- * beta_slow, values that are not finite. */
+ * beta_slow, values that are not finite, an amplitude beyond fp32's range. */
 enum { DSA_ROTARY_INTERLEAVED = 0, DSA_ROTARY_HALF = 1 };
 enum { DSA_ROTARY_PLAIN = 0, DSA_ROTARY_LINEAR = 1, DSA_ROTARY_YARN = 2, DSA_ROTARY_GIVEN = 3 };
 typedef struct dsa_rotary_config {

@@ -44,6 +44,14 @@ def test_tables_refuse(ctx, bad):
     assert status(lambda: ctx.rotary_table(**args)) == 1
 
 
+def test_tables_refuse_amplitudes_beyond_fp32(ctx):
+    """They are applied in fp32: one that is infinite there would make every value so."""
+    for bad in (3.5e38, -1e39, 1.7e308):
+        assert status(lambda: ctx.rotary_table(64, amplitude=bad)) == 1
+    for good in (3.4e38, -3.4e38, 0.0, 1e-60):
+        ctx.rotary_table(64, amplitude=good).close()
+
+
 def test_tables_check_their_arguments(ctx):
     with pytest.raises(ValueError):
         ctx.rotary_table(64, scaling="cubic")
