@@ -64,6 +64,10 @@ struct Layout {
   }
 };
 
+// Waits for what a creating call has put on the default stream: copies from pageable memory and memsets may be on their
+// way when they return, and streams that do not block on the default one would not wait for them.
+cudaError_t settle() { return cudaStreamSynchronize(nullptr); }
+
 bool is_host_only(const dsa_ctx *ctx) { return ctx == nullptr || ctx->device < 0; }
 
 dsa_status ensure_scratch(dsa_ctx *ctx, size_t scores, size_t slots) {
@@ -194,7 +198,7 @@ dsa_status dsa_create(const dsa_config_t *cfg, int device, dsa_ctx_t **out) {
       return DSA_ERR_CUDA;
     }
     if (cudaMalloc(&ctx->err, sizeof(int)) != cudaSuccess) { delete ctx; return DSA_ERR_OOM; }
-    if (cudaMemset(ctx->err, 0, sizeof(int)) != cudaSuccess) { cudaFree(ctx->err); delete ctx; return DSA_ERR_CUDA; }
+    if (cudaMemset(ctx->err, 0, sizeof(int)) != cudaSuccess || settle() != cudaSuccess) { cudaFree(ctx->err); delete ctx; return DSA_ERR_CUDA; }
     // the fixed score array of dsa_index_topk_static: looking up its address
     // loads the module that holds it, so the array is on the device from here
     // on and the static entry point never makes the driver allocate
@@ -572,7 +576,8 @@ dsa_status dsa_plan_capturable(dsa_ctx_t *ctx, int32_t max_rows, int32_t max_spa
   for (int64_t i = 0; i < units_cap; ++i) reinterpret_cast<AttUnit *>(h.data() + o_u)[i] = AttUnit{-1, 0, 0, -1};
   for (int32_t i = 0; i < combine_cap; ++i) reinterpret_cast<AttCombine *>(h.data() + o_cb)[i] = AttCombine{-1, 0, 0, 0};
   // (clusters start idle: zero-filled, u0 == u1)
-  if (cudaMemcpy(plan->dev, h.data(), lay.bytes, cudaMemcpyHostToDevice) != cudaSuccess) return fail(DSA_ERR_CUDA);
+  if (cudaMemcpy(plan->dev, h.data(), lay.bytes, cudaMemcpyHostToDevice) != cudaSuccess || settle() != cudaSuccess)
+    return fail(DSA_ERR_CUDA);
   *out = plan;
   return DSA_OK;
 }
@@ -974,6 +979,7 @@ dsa_status dsa_rotary_create(dsa_ctx_t *ctx, const dsa_rotary_config_t *cfg, dsa
       return DSA_ERR_OOM;
     }
     if (e == cudaSuccess) e = cudaMemcpy(table->turns, turns, n * sizeof(uint64_t), cudaMemcpyHostToDevice);
+    if (e == cudaSuccess) e = settle();
     if (e != cudaSuccess) {
       cudaFree(table->turns);
       delete table;

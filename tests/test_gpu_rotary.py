@@ -208,6 +208,21 @@ def test_rotary_rows_of_a_plan(ctx):
     ctx.get_error()
 
 
+def test_a_table_is_there_when_its_call_returns(ctx):
+    """Used at once on a stream that waits for nothing, table after table in the memory of the last one."""
+    x, pos, side = rand(16, 1, 1, 1024, dtype=F32), positions(1), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for i in range(50):
+        table = ctx.rotary_table(1024, frequencies=[0.01 * (i + 1)] * 512)
+        got.append(ctx.rotary(table, x, pos, stream=side))
+        side.synchronize()
+        table.close()
+    for i, y in enumerate(got):
+        want, mag = ref.rotate(x, pos, [0.01 * (i + 1)] * 512)
+        ref.close(y, want, ref.rotate_bound(x, want, mag, 0, 1024, "interleaved"), F32)
+
+
 def test_rotary_refuses(ctx):
     table = ctx.rotary_table(64)
     x = rand(1, 4, 2, 64)
