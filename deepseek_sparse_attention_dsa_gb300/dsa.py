@@ -164,6 +164,11 @@ ROTARY_LAYOUTS = {"interleaved": 0, "half": 1}
 ROTARY_FORMS = {None: 0, "linear": 1, "yarn": 2}
 
 
+def _small(value) -> int:
+    """An int32 of a C structure; one that does not fit (ctypes would take its low bits) becomes -1, which the calls refuse."""
+    return int(value) if -2 ** 31 <= int(value) < 2 ** 31 else -1
+
+
 def _layout(name) -> int:
     if name not in ROTARY_LAYOUTS:
         raise ValueError("layout must be one of %s, not %r" % (sorted(ROTARY_LAYOUTS), name))
@@ -171,7 +176,7 @@ def _layout(name) -> int:
 
 
 def _msa_shape(ms) -> _MsaShape:
-    return _MsaShape(int(ms.block_size), int(ms.topk_blocks), int(ms.q_heads), int(ms.kv_heads), int(ms.head_dim), 0)
+    return _MsaShape(_small(ms.block_size), _small(ms.topk_blocks), _small(ms.q_heads), _small(ms.kv_heads), _small(ms.head_dim), 0)
 
 
 class PlanInfo(ctypes.Structure):
@@ -697,7 +702,7 @@ class Context:
             given = (ctypes.c_double * max(1, len(frequencies)))(*[float(f) for f in frequencies])
         elif scaling not in ROTARY_FORMS:
             raise ValueError("scaling must be None, 'linear' or 'yarn', not %r" % (scaling,))
-        cfg = _RotaryConfig(int(rot_dim), 3 if given is not None else ROTARY_FORMS[scaling], float(base), float(factor),
+        cfg = _RotaryConfig(_small(rot_dim), 3 if given is not None else ROTARY_FORMS[scaling], float(base), float(factor),
                             float(original_context), float(beta_fast), float(beta_slow), float(amplitude), given)
         h = ctypes.c_void_p()
         _check(load().dsa_rotary_create(self.handle, ctypes.byref(cfg), ctypes.byref(h)), "dsa_rotary_create", self.handle)
@@ -757,7 +762,7 @@ class Context:
         if not plan.handle:
             raise DSAError(1, "plan")
         ms = _msa_shape(msa)
-        arr = None if prefixes is None else (_Prefix * max(1, len(prefixes)))(*[_Prefix(int(f), int(n), int(t), 0) for f, n, t in prefixes])
+        arr = None if prefixes is None else (_Prefix * max(1, len(prefixes)))(*[_Prefix(_small(f), _small(n), _small(t), 0) for f, n, t in prefixes])
         h = ctypes.c_void_p()
         st = None if self.device_index < 0 else _stream(stream)
         _check(load().dsa_prefix_plan(self.handle, plan.handle, ctypes.byref(ms), arr, -1 if prefixes is None else len(prefixes),

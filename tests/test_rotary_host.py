@@ -196,6 +196,18 @@ def test_prefixes_that_do_not_hold_are_refused(ctx):
     assert lib.dsa_prefix_plan(ctx.handle, plan.handle, ctypes.byref(ms), x, 1, None, ctypes.byref(h)) == 1
 
 
+def test_numbers_that_do_not_fit_are_refused(ctx):
+    """Not taken modulo 2^32."""
+    spans, pages = shared_spans([10, 70, 1, 64], 4)
+    plan = ctx.plan(spans, pages)
+    for bad in (2 ** 32 + 64, 2 ** 63 + 64, -2 ** 32 + 64):
+        assert status(lambda: ctx.rotary_table(bad)) == 1, bad
+        for prefix in ((bad, 2, 64), (0, bad, 64), (0, 2, bad)):
+            assert status(lambda: ctx.plan_prefix(plan, W.MSAShape(), [prefix])) == 1, prefix
+        for field in ("q_heads", "kv_heads", "head_dim"):
+            assert status(lambda: ctx.plan_prefix(plan, W.MSAShape(**{field: bad}))) in (1, 7), field
+
+
 def test_prefix_attend_checks_its_tensors(ctx):
     spans, pages = shared_spans([10, 70], 4)
     plan = ctx.plan(spans, pages)
