@@ -70,7 +70,8 @@ __host__ __device__ inline int rotary_units(int rot, int layout) {
   return layout == DSA_ROTARY_HALF ? (rot / 2 + 7) / 8 : (rot + 7) / 8;
 }
 __host__ __device__ inline int rotary_copies(int width, int offset, int rot) {
-  return (offset + 7) / 8 + (width - offset - rot + 7) / 8;
+  auto pieces = [](int n) { return n / 8 + (n % 8 > 0); };      // (a width may be 2^31 - 1)
+  return pieces(offset) + pieces(width - offset - rot);
 }
 // Angles held for a row: whole units of them, so that a cut unit reads inside its row.
 __host__ __device__ inline int rotary_pairs(int rot) { return (rot / 2 + 7) / 8 * 8; }
@@ -99,7 +100,7 @@ __device__ __forceinline__ void rotary_unit(int u, int rot, int layout, int offs
     return;
   }
   u -= n;
-  const int before = (offset + 7) / 8;
+  const int before = offset / 8 + (offset % 8 > 0);
   const int col = u < before ? u * 8 : offset + rot + (u - before) * 8, end = u < before ? offset : width;
   load8(a, src, src_type, col, end, src_vec);
   store8(dst, dst_type, col, end, dst_vec, a);

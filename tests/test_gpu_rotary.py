@@ -223,6 +223,18 @@ def test_a_table_is_there_when_its_call_returns(ctx):
         ref.close(y, want, ref.rotate_bound(x, want, mag, 0, 1024, "interleaved"), F32)
 
 
+@pytest.mark.parametrize("width,offset,rot", [(2 ** 31 - 1, 0, 2), (2 ** 31 - 1, 2 ** 31 - 3, 2), (2 ** 31 - 1, 2 ** 31 - 1 - 64, 64), (2 ** 31 - 8, 0, 64)])
+def test_the_widest_row(ctx, width, offset, rot):
+    """Counts of its pieces stay below 2^31."""
+    table, pos = ctx.rotary_table(rot), positions(1000)
+    x = torch.empty(1, width, dtype=BF16, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(17))
+    got = ctx.rotary(table, x, pos, offset=offset)
+    ctx.get_error()
+    end = offset + rot
+    assert torch.equal(got[:, :offset], x[:, :offset]) and torch.equal(got[:, end:], x[:, end:])
+    assert torch.equal(got[:, offset:end], ctx.rotary(table, x[:, offset:end].clone(), pos))
+
+
 def test_rotary_refuses(ctx):
     table = ctx.rotary_table(64)
     x = rand(1, 4, 2, 64)
