@@ -471,7 +471,7 @@ void lay_out(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, Work &w) {
       s.part[m] = pieces_of[static_cast<size_t>(c.tile[m]) * Hkv + c.g]++;   // (its number, for now)
     }
     s.causal = c.causal, s.g = c.g;
-    s.page_off = plan.spans[c.span].page_off, s.npages = plan.spans[c.span].num_pages;
+    s.page_off = plan.spans[c.span].page_off;
     s.slot0 = c.slot0 + x.t0 * kPrefixTile, s.ntiles = x.t1 - x.t0;
     s.lo = c.lo, s.hi = c.hi;
     w.segs.push_back(s);
@@ -540,7 +540,7 @@ void lay_out(const dsa_ctx *ctx, dsa_prefix_plan_t *pp, Work &w) {
       const Parts &x = parts[static_cast<size_t>(t) * Hkv + w.segs[i].g];
       w.segs[i].part[m] = x.count ? x.first + w.segs[i].part[m] * w.segs[i].lanes[m] : -1;
     }
-  w.segs.push_back(PrefixSeg{});   // (what lies behind the last is looked at, not used)
+  w.segs.resize(w.segs.size() + 2);   // (a walk that ends looks at two behind its last, and uses neither)
   pp->n_ctas = static_cast<int32_t>(w.ctas.size());
 }
 

@@ -14,13 +14,13 @@ namespace dsa {
 
 constexpr int kPrefixTile = 128;   // keys a tile, and lanes a tile of queries
 
-struct PrefixSeg {
+struct alignas(16) PrefixSeg {   // (64 bytes)
   int32_t row[2], lanes[2];     // first row and live lanes of each tile of queries (one: lanes[1] = 0)
   int32_t part[2];              // where lane 0's partial result goes, in lanes; -1: lanes are written to the output
   int32_t limit[2];             // causal: lane l sees slots below limit + l / group
   int32_t causal;
   int32_t g;                    // kv head
-  int32_t page_off, npages;
+  int32_t page_off;
   int32_t slot0, ntiles;        // first tile's first slot (a multiple of the box height), key tiles
   int32_t lo, hi;               // slots that some lane sees: lo .. hi - 1; not causal: every lane
 };
@@ -56,7 +56,7 @@ struct dsa_prefix_plan {
   int64_t part_lanes = 0;
   std::vector<char> host;                // staging copy of the tables
   char *dev = nullptr;
-  dsa::PrefixSeg *segs = nullptr;        // device, and one more behind the last
+  dsa::PrefixSeg *segs = nullptr;        // device, and two more behind the last
   dsa::PrefixCta *ctas = nullptr;
   dsa::PrefixJoin *join = nullptr;       // [n_join]
   float *part_o = nullptr;               // [lane][head_dim]

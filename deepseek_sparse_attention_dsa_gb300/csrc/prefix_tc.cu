@@ -90,7 +90,7 @@ struct PrefixParams {
   float *part_o;
   float2 *part_ml;
   int *err;
-  int32_t Hq, Hkv, group, P, BH, num_pages, q_bytes, q_small_bytes;
+  int32_t Hq, Hkv, group, P, BH, q_bytes, q_small_bytes;
   float scale_log2;
 };
 
@@ -129,8 +129,8 @@ struct Ring {
   }
 };
 
-// A walk over the tiles of a list of segments.  The next one's length is loaded a segment ahead (one more segment
-// lies behind the last of all lists).
+// A walk over the tiles of a list of segments.  The next one's length is loaded a segment ahead: at its end it has
+// looked at the two behind its list (two more lie behind the last of all lists).
 struct Walk {
   const PrefixSeg *seg;
   int j, n, n_next;   // tile of the segment, its tiles, the next one's
@@ -794,7 +794,7 @@ cudaError_t run(const dsa_ctx *ctx, const dsa_prefix_plan_t *pp, const void *q, 
   const dsa_plan_t &plan = *pp->plan;
   const dsa_msa_shape_t &ms = pp->shape;
   PrefixParams p{};
-  p.P = ctx->cfg.page_size, p.BH = plan.box_rows, p.num_pages = plan.cache_pages;
+  p.P = ctx->cfg.page_size, p.BH = plan.box_rows;
   p.Hq = ms.q_heads, p.Hkv = ms.kv_heads, p.group = ms.q_heads / ms.kv_heads;
   const uint64_t cols = 2ull * ms.kv_heads * D;
   const uint64_t dims[3] = {D, static_cast<uint64_t>(ms.q_heads), static_cast<uint64_t>(plan.T)};
