@@ -24,9 +24,9 @@
 //                                              sustained rate
 //   8192 rows of one sequence                  683 us, 1,609 TFLOP/s
 //   256 rows on two documents of 32768         247 us (148 at the burst rate, 107 at a copy's)
-//   32 rows behind 8192                        20.9 us (8.1 at a copy's rate)
+//   32 rows behind 8192                        20.2 us (8.1 at a copy's rate; 22.1 with three sets of inputs in turn)
 //   8 rows of 100000 tokens each alone         233 us, 7.0 TB/s
-//   4 rows behind 1024                         7.4 us
+//   4 rows behind 1024                         7.2 us
 // A pair's tile takes some 2,700 cycles, 2,048 of them the tensor core's; the others go
 // between a step's last product and the next one's first, and to the softmax, whose
 // way from S to the first weights (800 cycles) is about as long as the other

@@ -10,8 +10,8 @@
 // (6.5 TB/s, 0.98 of a plain copy); 4096 x 64 x 128, 21.4 us (0.94); 1031 x 64 x 128 in
 // fp32, 10.0 us (1.01).  One token of 128 heads: 1.9 us, a launch and one way to
 // memory and back.  rotary_pieces_kernel takes what lies on 16 bytes; the
-// general kernel, which asks every unit for its edges, is 3 to 4 times as long where a
-// row's stride is odd (131, 82 and 30 us).
+// general kernel, which asks every unit for its edges, is about twice as long where the
+// source's row stride is odd (82, 54 and 18 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>

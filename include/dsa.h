@@ -552,9 +552,10 @@ void dsa_rotary_destroy(dsa_rotary_t *table);
  * type's own size is accepted; 16-byte aligned heads, with offset a multiple of 8
  * and rot_dim of 8 (DSA_ROTARY_HALF: of 16), run faster.  out may be x, with the
  * same strides: then the other columns are left as they are.  Otherwise it must
- * not overlap x, and its heads must not overlap each other.  The kernels of this
- * call and of the appends are launched as those of the 8-bit rows (programmatic
- * stream serialization).  DSA_ERR_INVALID_ARG: null pointers or pointers off
+ * not overlap x, and its heads must not overlap each other.  This call and the
+ * appends need no workspace and share nothing between streams or threads but what the
+ * 8-bit rows' do; their kernels are launched as those (programmatic stream
+ * serialization).  DSA_ERR_INVALID_ARG: null pointers or pointers off
  * their type, sizes below 1 (rows may be 0: nothing is launched), offset + rot_dim
  * above width, an unknown type or layout, negative strides, written heads that
  * would overlap, a table of another device, a plan of another context, rows that do
@@ -615,14 +616,22 @@ dsa_status dsa_append_kv(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_rotar
  * request's own after them, and the two softmaxes are joined:
  *   out[r, h] = softmax_j((q[r, h] . k_j) * sm_scale) . v_j,  j = 0 .. pos(r),
  * query head h reading kv head h / (q_heads / kv_heads).  Spans without a shared
- * prefix are attended by themselves, so any host plan can be used.
+ * prefix are attended by themselves, so any host plan can be used.  (A load of shared
+ * rows serves one or two tiles of up to 128 (row, head) pairs of a kv head; more tiles
+ * load them again, mostly out of L2.  Spans of many rows go through shared and own keys
+ * by themselves.  The shapes that do not run on the tensor cores, head_dim
+ * other than 64 and 128, more than 128 query heads a kv head or pages of no multiple of
+ * 8 tokens, read every row's whole history: there a prefix changes nothing.)
  *
  * dsa_prefix_plan: prefixes[i] says that spans first_span .. first_span +
  * num_spans - 1 of the plan hold their positions 0 .. tokens - 1 in the same slots
  * of the same pages, none of them this step's new rows (tokens <= ctx_start); in
  * order, without overlap.  num_prefixes = -1 finds them: runs of neighbouring
  * spans with the same page_start and the same first pages (at least 128 tokens),
- * a run growing while that lowers the tokens read.  0: nothing is shared.
+ * a run growing while that lowers the tokens read.  Requests of one prefix have to
+ * follow one another, and a prefix within a prefix is not looked for.  0: nothing is
+ * shared.  The plan, its tables and its grid are those of one step: a graph that holds
+ * its calls serves that step's layers, and a capturable plan has none.
  * Host work, then one host-to-device copy on `stream`, as dsa_plan; made once a
  * step and used for every layer of it.  It keeps pointing at `plan`, which must
  * outlive it, and owns the scratch of its calls (partial results in fp32: up to some
@@ -655,7 +664,8 @@ typedef struct dsa_prefix_plan dsa_prefix_plan_t;
 typedef struct dsa_prefix_info {
   int32_t num_prefixes;      /* runs of spans that share a prefix */
   int32_t on_tensor_cores;   /* 1 when the plan's calls run on the tensor cores */
-  int64_t tokens_read;       /* tokens whose keys and values one call needs (per kv head), shared ones once */
+  int64_t tokens_read;       /* tokens whose keys and values one call needs (per kv head), shared ones once; for
+                                any shape, also one whose kernel reads them more often */
 } dsa_prefix_info_t;
 dsa_status dsa_prefix_plan(dsa_ctx_t *ctx, const dsa_plan_t *plan, const dsa_msa_shape_t *shape, const dsa_prefix_t *prefixes,
                            int32_t num_prefixes, dsa_stream_t stream, dsa_prefix_plan_t **out);
