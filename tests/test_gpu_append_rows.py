@@ -177,3 +177,38 @@ def test_padding_among_the_rows_of_a_thread(contexts, live, fp8):
     c.get_error()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows", [12, 4999])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_codes_of_any_values(contexts, rows, dtype, shift):
+    """NaN, infinities, zeros of both signs, values at both ends of the type's range: the codes and scales of the 8-bit rows,
+    to the byte, on 16 bytes and off them."""
+    c = contexts(latent_fmt=W.LATENT_FP8_656, index_fmt=W.INDEX_FP8_132)
+    spans, pages = spans_of(rows, 64)
+    plan = c.plan(spans, pages)
+    x = torch.randn(rows, 512 + 128, generator=torch.Generator().manual_seed(6))
+    special = [float("nan"), float("inf"), -float("inf"), -0.0, 0.0, 1e-38, -3e-41, 3e38, 1e-45, 448.0]
+    for i, v in enumerate(special):
+        x[i::12, 17 + 50 * i] = v                  # one such value in a group
+    x[10::12] = torch.where(x[10::12] > 0, 1e-30, -0.0)
+    x[11::12, :300] *= 1e-39
+    x[9::12, 128:256], x[9::12, 512:] = -0.0, 0.0
+    x = x.to(dtype)
+    lat, keys = (torch.empty(rows * n + shift, dtype=dtype, device="cuda")[shift:].view(rows, n) for n in (512, 128))
+    lat.copy_(x[:, :512])
+    keys.copy_(x[:, 512:])
+    k_pe = torch.zeros(rows, 64, dtype=dtype, device="cuda")
+    lc = torch.full((pages, 64, 656), 77, dtype=U8, device="cuda")
+    ic = torch.full((pages, 64 * 132), 77, dtype=U8, device="cuda")
+    c.append_latents(plan, None, lat, k_pe, lc, keys, ic)
+    c.get_error()
+    where = torch.from_numpy(ref.slots(spans, 64)[0]).cuda()
+    l = lc.view(-1, 656)[where]
+    codes, scales = c.quantize_rows(lat.clone())
+    assert torch.equal(l[:, :512], codes) and bool((l[:, 528:] == 0).all())
+    torch.testing.assert_close(l[:, 512:528].contiguous().view(F32), scales, rtol=0, atol=0, equal_nan=True)
+    codes, scales = c.quantize_rows(keys.clone())
+    assert torch.equal(ic[:, :64 * 128].reshape(-1, 128)[where], codes)
+    torch.testing.assert_close(ic[:, 64 * 128:].contiguous().view(F32).view(-1)[where], scales[:, 0], rtol=0, atol=0, equal_nan=True)
